@@ -55,7 +55,12 @@ extern "C" {
 #define SWA_DERR_TIMEOUT  2u /* a bounded wait on a copy into shared memory
                                 expired; the kernel stopped without output */
 #define SWA_DERR_SEGMENT  4u /* swa_flash: a segment reaches past row T or is
-                                longer than max_len (its rows are not written) */
+                                longer than max_len (its rows are not written);
+                                paged calls: a sequence's rows run backwards,
+                                reach past row T or are more than max_rows */
+#define SWA_DERR_PAGE     8u /* paged calls: a page table entry names no page of
+                                the pool (its keys are read as zeros, its slots
+                                are not written) */
 
 /* Per-sequence ring state, as the per-group meta of o1c_msl.metal:
  *   win_len  — keys held in the ring (<= window)
@@ -476,6 +481,258 @@ typedef struct swa_flash_args {
  * first use. */
 size_t swa_flash_workspace_size(const swa_flash_args* args);
 int swa_flash(const swa_flash_args* args, cudaStream_t stream);
+
+/*
+ * ---------------------------------------------------------------------------
+ * Paged cache: the layers of a model that keep every key beside the sealed
+ * sliding-window ones. K and V lie in 16 bits in a pool of pages that the
+ * caller hands out; the calls rotate and append a chunk, attend over the
+ * pages, add up the weight each cached key received and evict keys by it.
+ * The pages of the reference have no counterpart.
+ * ---------------------------------------------------------------------------
+ */
+
+/* Element types of the paged and rotary calls. */
+#define SWA_F32   0
+#define SWA_BF16  1
+#define SWA_F16   2
+
+/*
+ * A paged cache and the ragged batch that uses it, shared by the paged calls.
+ *   k, v       [num_pages][nk][page][hd], dtype SWA_BF16 or SWA_F16, 16-byte
+ *              aligned. hd 64, 128 or 256; page a power of two, 16 .. 256;
+ *              num_pages * nk * page < 2^31.
+ *   table      [B][max_pages] i32: page of each sequence's slots
+ *              [i * page, (i + 1) * page); entries past the sequence's length
+ *              are not read. max_pages * page (the capacity of a sequence,
+ *              `cap` below) <= 2^30.
+ *   row_start  [B + 1] i32, ascending: the chunk's rows of sequence b are the
+ *              packed rows [row_start[b], row_start[b+1]) of T. t_b = 0 is
+ *              allowed; rows behind row_start[B] belong to no sequence: no
+ *              output is written for them. Not read by swa_paged_evict.
+ *   lens       [B] i32: keys each sequence holds, the chunk's own rows among
+ *              them. Row i of a chunk of t_b rows has slot lens[b] - t_b + i.
+ *   B          1 .. 65535; nk 1 .. 65535.
+ * On the device, a length outside 0 .. cap is clamped (SWA_DERR_META), a
+ * sequence with rows out of range is skipped (SWA_DERR_SEGMENT), and pages out
+ * of range are reported (SWA_DERR_PAGE); every access stays in bounds.
+ */
+typedef struct swa_paged_cache {
+  int B, nk, hd, page, num_pages, max_pages, dtype;
+  void* k;
+  void* v;
+  const int32_t* table;
+  const int32_t* row_start;
+  const int32_t* lens;
+} swa_paged_cache;
+
+/*
+ * swa_rotary_turns — the frequencies of rotary positions, on the HOST.
+ *   freqs [rot/2] f64 (output, may be NULL): f_e in radians per position
+ *   turns [rot/2] u64 (output, may be NULL): f_e / 2 pi in turns, as 64-bit
+ *     fixed point: floor(frac(f_e / 2 pi) * 2^64). The kernels take
+ *     pos * turns modulo 2^64: positions are whole, so whole turns drop out
+ *     and the angle is exact to 2^-33 turns at every position (the fraction is
+ *     good to 2^-53 turns a position and pos < 2^31).
+ * Copy `turns` to the device once and keep it; a table of one's own may be
+ * built the same way.
+ * Schedules (rot even, >= 2; theta > 0; factor >= 1 where read):
+ *   SWA_ROTARY_PLAIN   f_e = theta^(-2e/rot)
+ *   SWA_ROTARY_LINEAR  f_e / factor
+ *   SWA_ROTARY_BASE    theta replaced by theta * factor^(rot / (rot - 2)), so
+ *                      that the slowest pair turns `factor` times slower and
+ *                      the fastest as before (rot > 2)
+ *   SWA_ROTARY_PARTS   with r = orig_len * f_e / 2 pi turns over the trained
+ *                      length: f_e where r >= high, f_e / factor where
+ *                      r <= low, in between mixed linearly in r (low < high)
+ * Errors: SWA_E_NULL (s NULL), SWA_E_SHAPE.
+ */
+#define SWA_ROTARY_PLAIN   0
+#define SWA_ROTARY_LINEAR  1
+#define SWA_ROTARY_BASE    2
+#define SWA_ROTARY_PARTS   3
+typedef struct swa_rotary_schedule {
+  int kind, rot;
+  double theta, factor, orig_len, low, high;
+} swa_rotary_schedule;
+int swa_rotary_turns(const swa_rotary_schedule* s, double* freqs, uint64_t* turns);
+
+/*
+ * swa_rotary — rotary positions of packed rows: for row r, head h, pair e
+ * with the angle a = pos[r] * f_e:
+ *   u' = mag * (u cos a - v sin a),  v' = mag * (v cos a + u sin a)
+ * (u, v) = features (e, rot/2 + e), or (2e, 2e + 1) when interleaved; the
+ * features from rot on are copied. inverse = 1 turns the other way: the
+ * gradient of the forward call with the same mag (the rotation's transpose).
+ * Computed in f32, rounded once.
+ *   x    [T] rows of H heads of hd features: row r, head h at
+ *        x + r * x_row + h * x_head (elements)
+ *   out  the same with out_row, out_head; out may be x itself with the same
+ *        strides, or must not overlap it (SWA_E_SHAPE).
+ *   pos  [T] i32, any value;  turns [rot/2] u64 device (swa_rotary_turns)
+ *   dtype SWA_F32, SWA_BF16 or SWA_F16; hd a multiple of 8, <= 1024; rot even,
+ *   2 <= rot <= hd; strides positive multiples of 16 bytes, heads (hd) and
+ *   rows (H heads) not overlapping: x_head >= hd and x_row >= H * x_head, or
+ *   x_row >= hd and x_head >= T * x_row. mag finite. T >= 0 (0: no work).
+ * Errors: SWA_E_NULL, SWA_E_SHAPE (also T * H * hd >= 2^40), SWA_E_ALIGN,
+ * SWA_E_CUDA. One launch.
+ */
+typedef struct swa_rotary_args {
+  int T, H, hd, rot, dtype, interleaved, inverse;
+  float mag;
+  const void* x;
+  long long x_row, x_head;
+  void* out;
+  long long out_row, out_head;
+  const int32_t* pos;
+  const uint64_t* turns;
+} swa_rotary_args;
+int swa_rotary(const swa_rotary_args* args, cudaStream_t stream);
+
+/*
+ * swa_paged_append — the chunk's rows enter the cache: k is rotated (as by
+ * swa_rotary, when rot > 0) and rounded into cache.k, v rounded into cache.v,
+ * at each row's slot; q, when given, is rotated and rounded to the cache's
+ * type into q_out. One launch, before swa_paged_attend on the same lens.
+ *   k, v  [T][nk][hd], q [T][nh][hd] with row strides k_row, v_row, q_row in
+ *         elements (heads dense), of type src (SWA_F32, SWA_BF16, SWA_F16;
+ *         SWA_F32 or the cache's type); rows at multiples of 16 bytes
+ *   q_out [T][nh][hd] dense, of the cache's type (required with q); must not
+ *         overlap q unless it is q itself, of the same type and dense
+ *   pos   [T] i32 (required with rot > 0 or slot_pos)
+ *   turns [rot/2] u64 (required with rot > 0); rot 0 or even, <= hd
+ *   slot_pos [B][nk][cap] i32, weight [B][nk][cap] f32 (each optional): the
+ *         new slots get the row's position and weight 0 (swa_paged_evict)
+ * Rows whose slot is below 0 (a chunk longer than lens[b]) set SWA_DERR_META
+ * and are not stored (their q is). Slots must not be given twice, and pages
+ * that are written must belong to one sequence: this is not checked.
+ * Errors: SWA_E_NULL, SWA_E_SHAPE, SWA_E_ALIGN, SWA_E_CUDA.
+ */
+typedef struct swa_paged_append_args {
+  swa_paged_cache cache;
+  int T, nh, rot, src, interleaved;
+  float mag;
+  const void* q;
+  const void* k;
+  const void* v;
+  long long q_row, k_row, v_row;
+  void* q_out;
+  const int32_t* pos;
+  const uint64_t* turns;
+  int32_t* slot_pos;
+  float* weight;
+  uint32_t* err;
+} swa_paged_append_args;
+int swa_paged_append(const swa_paged_append_args* args, cudaStream_t stream);
+
+/*
+ * swa_paged_attend — causal attention of a chunk's rows over the paged cache
+ * (their own keys already appended). Row i of sequence b sees the slots
+ * [0, lens[b] - t_b + i + 1); query head h reads KV head h / (nh / nk):
+ *   s = scale * <q, k>, p = exp(s - max s), out = sum p v / sum p,
+ *   lse = log(sum exp(s)).
+ * Scores, maxima and sums are f32; the weights p are rounded to the cache's
+ * type for the value product (one rounding of each weight, relative 2^-8 or
+ * 2^-11 at most); out is rounded once. A row that sees no key gets out = 0,
+ * lse = -inf. What lies behind a sequence's last key in its pages is not used,
+ * NaN and infinities included; keys that some row of the chunk sees must be
+ * finite in V for the rows before them.
+ *   q    [T][nh][hd] of the cache's type, rows q_row elements apart (heads
+ *        dense, rows at multiples of 16 bytes); nh / nk <= 32
+ *   out  [T][nh][hd] dense, of the cache's type, or f32 with out_f32 = 1
+ *   lse  [T][nh] f32, optional
+ *   scale  finite, >= 0
+ *   max_rows  upper bound of t_b: it chooses the kernel and sizes the grid.
+ *   workspace  device scratch of swa_paged_attend_workspace_size(args) bytes,
+ *        256-byte aligned, no initial contents needed, not shared by calls
+ *        that overlap on the GPU
+ *   ev_start, ev_stop  optional, recorded around the attention kernels
+ * The result does not depend on timing: the same call gives the same bits.
+ * Errors: SWA_E_NULL, SWA_E_SHAPE (also T * nh >= 2^31), SWA_E_ALIGN,
+ * SWA_E_WORKSPACE, SWA_E_CUDA. T = 0: nothing is launched.
+ */
+typedef struct swa_paged_attend_args {
+  swa_paged_cache cache;
+  int T, nh, max_rows, out_f32;
+  float scale;
+  const void* q;
+  long long q_row;
+  void* out;
+  float* lse;
+  void* workspace;
+  size_t workspace_bytes;
+  uint32_t* err;
+  cudaEvent_t ev_start, ev_stop;
+} swa_paged_attend_args;
+/* Bytes of workspace for these sizes (0: invalid sizes). Queries the current
+ * device's SM count on first use. */
+size_t swa_paged_attend_workspace_size(const swa_paged_attend_args* args);
+int swa_paged_attend(const swa_paged_attend_args* args, cudaStream_t stream);
+
+/*
+ * swa_paged_weigh — the attention weight each cached key received from the
+ * chunk's rows, added to what it has:
+ *   out[b][g][j] = weight[b][g][j] + sum over rows i that see slot j and query
+ *                  heads h of KV head g of exp(scale * <q, k_j> - lse[i][h])
+ * for every slot j < lens[b]; other entries of out are left as they were.
+ *   q, q_row, scale, max_rows  as swa_paged_attend (any rows: q may hold only
+ *         the last rows of a chunk, with a row_start of their own)
+ *   lse   [T][nh] f32 of the same rows (swa_paged_attend)
+ *   weight [B][nk][cap] f32 or NULL (zeros); out [B][nk][cap] f32, may be
+ *         weight itself, else must not overlap it
+ * The sums run in f32 in a fixed order. cache.v is not read.
+ * Errors: SWA_E_NULL, SWA_E_SHAPE, SWA_E_ALIGN, SWA_E_CUDA.
+ */
+typedef struct swa_paged_weigh_args {
+  swa_paged_cache cache;
+  int T, nh, max_rows;
+  float scale;
+  const void* q;
+  long long q_row;
+  const float* lse;
+  const float* weight;
+  float* out;
+  uint32_t* err;
+} swa_paged_weigh_args;
+int swa_paged_weigh(const swa_paged_weigh_args* args, cudaStream_t stream);
+
+/*
+ * swa_paged_evict — cut every sequence's cache to at most `keep` keys per KV
+ * head by the keys' weights. Of the lens[b] slots of (b, g) the
+ * n' = min(lens[b], keep) first in this order stay: protected slots (position
+ * < sinks, or >= recent_from[b]), then by descending weight (NaN before all
+ * numbers, -0 as 0), equal ones by ascending slot. Kept slots below n' stay
+ * where they are; the i-th kept slot from n' on moves into the i-th freed slot
+ * below n' (both ascending): K and V rows within the pages, and its weight and
+ * position. A softmax does not ask for the order of its keys, positions are
+ * already in the rotated keys, and new rows are appended behind n'.
+ *   weight, slot_pos         [B][nk][cap] before, read only
+ *   weight_out, slot_pos_out [B][nk][cap] after: entries below n' are written
+ *   lens_out                 [B] = n'
+ *       (the three outputs must not overlap the inputs: SWA_E_SHAPE. The call
+ *       may be repeated on the same inputs: rows that move are only read and
+ *       freed ones only written.)
+ *   recent_from              [B] i32 or NULL (no recent positions protected)
+ *   keep >= 1, sinks >= 0
+ *   workspace  swa_paged_evict_workspace_size(args) bytes, 256-byte aligned
+ * Pages must belong to one sequence (not checked). cache.row_start is not read.
+ * Errors: SWA_E_NULL, SWA_E_SHAPE, SWA_E_ALIGN, SWA_E_WORKSPACE, SWA_E_CUDA.
+ */
+typedef struct swa_paged_evict_args {
+  swa_paged_cache cache;
+  int keep, sinks;
+  const float* weight;
+  const int32_t* slot_pos;
+  const int32_t* recent_from;
+  float* weight_out;
+  int32_t* slot_pos_out;
+  int32_t* lens_out;
+  void* workspace;
+  size_t workspace_bytes;
+  uint32_t* err;
+} swa_paged_evict_args;
+size_t swa_paged_evict_workspace_size(const swa_paged_evict_args* args);
+int swa_paged_evict(const swa_paged_evict_args* args, cudaStream_t stream);
 
 #ifdef __cplusplus
 }

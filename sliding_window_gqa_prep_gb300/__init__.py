@@ -14,6 +14,8 @@ Public calls (same names as the C ABI):
   decode_step(yq, yk, yv, q_scale, pos0, meta, ring_k, ring_v, sink_k, sink_v,
               gate, gate_scale, scale, ...)      -> out [B][nh][hd] (t = 1, one call)
   TokenPath: holds a batch's ring state and runs whole steps
+  rotary_turns, rotary, paged_append, paged_attend, paged_weigh, paged_evict: rotary
+  positions and the paged cache of the layers that keep every key (paged.py)
 Meta tensors are int32 [B][4] = (win_len, win_head, far_len, window), read by
 the kernels as uint32; pos0 tensors are int32 [B].
 """
@@ -25,11 +27,14 @@ from typing import Optional
 import torch
 
 from . import _abi
-from ._abi import SwaError, SWA_DERR_META, SWA_DERR_TIMEOUT  # noqa: F401
+from ._abi import (SwaError, SWA_DERR_META, SWA_DERR_PAGE, SWA_DERR_SEGMENT,  # noqa: F401
+                   SWA_DERR_TIMEOUT)
+from . import paged as _paged
+from .paged import *  # noqa: F401,F403
 
 __all__ = ["rope_table", "prep", "attend", "attend_workspace_size", "decode_step",
            "decode_workspace_size", "decode_launches", "rollback", "launch_count",
-           "TokenPath", "SwaError", "library"]
+           "TokenPath", "SwaError", "library"] + _paged.__all__
 
 
 def library() -> ctypes.CDLL:

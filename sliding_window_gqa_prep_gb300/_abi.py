@@ -18,6 +18,12 @@ SWA_E_CUDA = -6
 
 SWA_DERR_META = 1
 SWA_DERR_TIMEOUT = 2
+SWA_DERR_SEGMENT = 4
+SWA_DERR_PAGE = 8
+
+SWA_F32 = 0
+SWA_BF16 = 1
+SWA_F16 = 2
 
 
 class PrepArgs(ctypes.Structure):
@@ -84,6 +90,74 @@ class FlashArgs(ctypes.Structure):
     ]
 
 
+class PagedCache(ctypes.Structure):
+    _fields_ = [
+        ("B", ctypes.c_int), ("nk", ctypes.c_int), ("hd", ctypes.c_int), ("page", ctypes.c_int),
+        ("num_pages", ctypes.c_int), ("max_pages", ctypes.c_int), ("dtype", ctypes.c_int),
+        ("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("table", ctypes.c_void_p),
+        ("row_start", ctypes.c_void_p), ("lens", ctypes.c_void_p),
+    ]
+
+
+class RotarySchedule(ctypes.Structure):
+    _fields_ = [
+        ("kind", ctypes.c_int), ("rot", ctypes.c_int), ("theta", ctypes.c_double), ("factor", ctypes.c_double),
+        ("orig_len", ctypes.c_double), ("low", ctypes.c_double), ("high", ctypes.c_double),
+    ]
+
+
+class RotaryArgs(ctypes.Structure):
+    _fields_ = [
+        ("T", ctypes.c_int), ("H", ctypes.c_int), ("hd", ctypes.c_int), ("rot", ctypes.c_int),
+        ("dtype", ctypes.c_int), ("interleaved", ctypes.c_int), ("inverse", ctypes.c_int), ("mag", ctypes.c_float),
+        ("x", ctypes.c_void_p), ("x_row", ctypes.c_longlong), ("x_head", ctypes.c_longlong),
+        ("out", ctypes.c_void_p), ("out_row", ctypes.c_longlong), ("out_head", ctypes.c_longlong),
+        ("pos", ctypes.c_void_p), ("turns", ctypes.c_void_p),
+    ]
+
+
+class PagedAppendArgs(ctypes.Structure):
+    _fields_ = [
+        ("cache", PagedCache),
+        ("T", ctypes.c_int), ("nh", ctypes.c_int), ("rot", ctypes.c_int), ("src", ctypes.c_int),
+        ("interleaved", ctypes.c_int), ("mag", ctypes.c_float),
+        ("q", ctypes.c_void_p), ("k", ctypes.c_void_p), ("v", ctypes.c_void_p),
+        ("q_row", ctypes.c_longlong), ("k_row", ctypes.c_longlong), ("v_row", ctypes.c_longlong),
+        ("q_out", ctypes.c_void_p), ("pos", ctypes.c_void_p), ("turns", ctypes.c_void_p),
+        ("slot_pos", ctypes.c_void_p), ("weight", ctypes.c_void_p), ("err", ctypes.c_void_p),
+    ]
+
+
+class PagedAttendArgs(ctypes.Structure):
+    _fields_ = [
+        ("cache", PagedCache),
+        ("T", ctypes.c_int), ("nh", ctypes.c_int), ("max_rows", ctypes.c_int), ("out_f32", ctypes.c_int),
+        ("scale", ctypes.c_float),
+        ("q", ctypes.c_void_p), ("q_row", ctypes.c_longlong), ("out", ctypes.c_void_p), ("lse", ctypes.c_void_p),
+        ("workspace", ctypes.c_void_p), ("workspace_bytes", ctypes.c_size_t), ("err", ctypes.c_void_p),
+        ("ev_start", ctypes.c_void_p), ("ev_stop", ctypes.c_void_p),
+    ]
+
+
+class PagedWeighArgs(ctypes.Structure):
+    _fields_ = [
+        ("cache", PagedCache),
+        ("T", ctypes.c_int), ("nh", ctypes.c_int), ("max_rows", ctypes.c_int), ("scale", ctypes.c_float),
+        ("q", ctypes.c_void_p), ("q_row", ctypes.c_longlong), ("lse", ctypes.c_void_p),
+        ("weight", ctypes.c_void_p), ("out", ctypes.c_void_p), ("err", ctypes.c_void_p),
+    ]
+
+
+class PagedEvictArgs(ctypes.Structure):
+    _fields_ = [
+        ("cache", PagedCache),
+        ("keep", ctypes.c_int), ("sinks", ctypes.c_int),
+        ("weight", ctypes.c_void_p), ("slot_pos", ctypes.c_void_p), ("recent_from", ctypes.c_void_p),
+        ("weight_out", ctypes.c_void_p), ("slot_pos_out", ctypes.c_void_p), ("lens_out", ctypes.c_void_p),
+        ("workspace", ctypes.c_void_p), ("workspace_bytes", ctypes.c_size_t), ("err", ctypes.c_void_p),
+    ]
+
+
 _lib = None
 
 
@@ -138,6 +212,19 @@ def load(build_if_missing: bool = True) -> ctypes.CDLL:
     lib.swa_flash.argtypes = [ctypes.POINTER(FlashArgs), ctypes.c_void_p]
     lib.swa_flash_workspace_size.restype = ctypes.c_size_t
     lib.swa_flash_workspace_size.argtypes = [ctypes.POINTER(FlashArgs)]
+    lib.swa_rotary_turns.restype = ctypes.c_int
+    lib.swa_rotary_turns.argtypes = [ctypes.POINTER(RotarySchedule), ctypes.c_void_p, ctypes.c_void_p]
+    for name, args in (("swa_rotary", RotaryArgs), ("swa_paged_append", PagedAppendArgs),
+                       ("swa_paged_attend", PagedAttendArgs), ("swa_paged_weigh", PagedWeighArgs),
+                       ("swa_paged_evict", PagedEvictArgs)):
+        fn = getattr(lib, name)
+        fn.restype = ctypes.c_int
+        fn.argtypes = [ctypes.POINTER(args), ctypes.c_void_p]
+    for name, args in (("swa_paged_attend_workspace_size", PagedAttendArgs),
+                       ("swa_paged_evict_workspace_size", PagedEvictArgs)):
+        fn = getattr(lib, name)
+        fn.restype = ctypes.c_size_t
+        fn.argtypes = [ctypes.POINTER(args)]
     _lib = lib
     return lib
 

@@ -1,0 +1,568 @@
+// Attention of a ragged chunk over the paged cache: the kernel for few query
+// vectors per KV head (decode tokens, verify chunks), the merge of its partial
+// records, and the host side of swa_paged_attend.
+//
+// A block of up to 64 query vectors (rows x heads of one KV head) needs 4 * 64 * hd
+// operations for the 4 * hd bytes of a key: 64 a byte, far below the 280 a byte where
+// the matrix peak meets the memory's. The kernel is bound by reading K and V once.
+// So: every CTA gets the same number of 64-key tiles of the whole call (work of all
+// sequences, KV heads and row blocks laid end to end and cut evenly, wherever the cuts
+// fall), streams them through a ring of cp.async stages, and computes with warp-level
+// mma.sync.m16n8k16: S = Q K^T with Q in registers, the online softmax on S's
+// registers, and these registers again as the A operand of P V. A (sequence, KV head,
+// row block) that lies whole in one CTA is finished there; one that is cut leaves a
+// record (m, l, sum p v) per CTA, joined by paged_merge_kernel.
+#include <cmath>
+
+#include "swa_mma16.cuh"
+#include "swa_paged_attend.cuh"
+
+namespace swa {
+
+// ---------------------------------------------------------------------------
+// Host checks shared by the paged calls
+// ---------------------------------------------------------------------------
+bool bytes_overlap(const void* a, size_t an, const void* b, size_t bn) {
+  const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
+  return x < y + bn && y < x + an;
+}
+
+int paged_cache_status(const swa_paged_cache* c, bool rows) {
+  if (!c->k || !c->v || !c->table || !c->lens || (rows && !c->row_start)) return SWA_E_NULL;
+  if (c->B < 1 || c->B > 65535 || c->nk < 1 || c->nk > 65535) return SWA_E_SHAPE;
+  if (c->hd != 64 && c->hd != 128 && c->hd != 256) return SWA_E_SHAPE;
+  if (c->page < 16 || c->page > 256 || (c->page & (c->page - 1))) return SWA_E_SHAPE;
+  if (c->num_pages < 1 || (long long)c->num_pages * c->nk >= (1LL << 31) / c->page) return SWA_E_SHAPE;
+  if (c->max_pages < 1 || c->max_pages > (1 << 30) / c->page) return SWA_E_SHAPE;
+  if (c->dtype != SWA_BF16 && c->dtype != SWA_F16) return SWA_E_SHAPE;
+  if (!aligned16p(c->k) || !aligned16p(c->v) || (reinterpret_cast<uintptr_t>(c->table) & 3u) ||
+      (reinterpret_cast<uintptr_t>(c->row_start) & 3u) || (reinterpret_cast<uintptr_t>(c->lens) & 3u))
+    return SWA_E_ALIGN;
+  return SWA_OK;
+}
+
+PagedMap paged_map(const swa_paged_cache* c) {
+  PagedMap m{};
+  m.B = c->B; m.nk = c->nk; m.num_pages = c->num_pages; m.max_pages = c->max_pages;
+  while ((1 << m.page_shift) < c->page) ++m.page_shift;
+  m.cap = c->max_pages << m.page_shift;
+  m.table = c->table; m.row_start = c->row_start; m.lens = c->lens;
+  return m;
+}
+
+// ---------------------------------------------------------------------------
+// The split kernel
+// ---------------------------------------------------------------------------
+constexpr int kThreads = 128;        // four warps
+constexpr int kKeys = 64;            // keys per tile
+constexpr int kMinTiles = 2;         // a CTA takes at least this many tiles
+
+template <int D>
+struct SplitCfg {
+  // stages of one K and one V tile; about 96 KB (two CTAs an SM) at hd 128
+  static constexpr int ST = D == 64 ? 4 : 3;
+  static constexpr int TILE = kKeys * D * 2;
+  static constexpr int SMEM = ST * 2 * TILE;
+};
+
+// Sequences this kernel works on have query vectors in blocks of `rows_tok` rows.
+__device__ __forceinline__ long long split_units(const PagedSeq& s, const PagedAttendParams& p, int& n_rb, int& n_tiles) {
+  n_rb = (s.t + p.rows_tok - 1) / p.rows_tok;
+  n_tiles = s.len > 0 ? (s.len + kKeys - 1) / kKeys : 1;   // a row without keys is still written
+  return (long long)p.map.nk * n_rb * n_tiles;
+}
+
+// ROWS: query vectors of a CTA's block (16, 32 or 64): ROWS / 16 groups of 16 rows,
+// the other warps take the tile's keys in turn.
+template <typename T, int D, int ROWS>
+__global__ void __launch_bounds__(kThreads) paged_split_kernel(const PagedAttendParams p) {
+  using C = SplitCfg<D>;
+  constexpr int RG = ROWS / 16, KG = 4 / RG, KW = kKeys / KG;   // row groups, key groups, keys of a warp
+  extern __shared__ __align__(128) unsigned char sm[];
+  __shared__ long long s_scan[4];
+  __shared__ long long s_off, s_total;
+  __shared__ int s_b;
+  __shared__ int s_pages[2][kKeys / 16];
+  __shared__ float2 s_ml[4][16];
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  pdl_wait();
+  pdl_trigger();
+
+  // --- this CTA's share of all tiles: a scan over the sequences
+  uint32_t bits = 0;
+  {
+    const int E = (p.map.B + kThreads - 1) / kThreads;
+    long long mine = 0;
+    for (int e = 0; e < E; ++e) {
+      const int b = tid * E + e;
+      if (b < p.map.B) {
+        const PagedSeq s = paged_seq(p.map, b, p.T, p.max_rows, bits);
+        int a1, a2;
+        mine += split_units(s, p, a1, a2);
+      }
+    }
+    if (bits && blockIdx.x == 0) set_err(p.err, bits);
+    long long incl = mine;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const long long v = __shfl_up_sync(0xffffffffu, incl, o);
+      if (lane >= o) incl += v;
+    }
+    if (lane == 31) s_scan[warp] = incl;
+    if (tid == 0) s_b = -1;
+    __syncthreads();
+    long long before = incl - mine, total = 0;
+    for (int w = 0; w < 4; ++w) {
+      if (w < warp) before += s_scan[w];
+      total += s_scan[w];
+    }
+    long long per = (total + gridDim.x - 1) / gridDim.x;
+    if (per < kMinTiles) per = kMinTiles;
+    const long long u0 = per * blockIdx.x;
+    if (u0 >= before && u0 < before + mine) {
+      long long off = u0 - before;
+      for (int e = 0; e < E; ++e) {
+        const int b = tid * E + e;
+        uint32_t ignore = 0;
+        int a1, a2;
+        const long long n = split_units(paged_seq(p.map, b, p.T, p.max_rows, ignore), p, a1, a2);
+        if (off < n) {
+          s_b = b;
+          s_off = off;
+          break;
+        }
+        off -= n;
+      }
+    }
+    if (tid == 0) s_total = total;
+    __syncthreads();
+  }
+  const long long total = s_total;
+  long long per = (total + gridDim.x - 1) / gridDim.x;
+  if (per < kMinTiles) per = kMinTiles;
+  const long long u0 = per * blockIdx.x;
+  if (s_b < 0) {
+    if (tid == 0) p.ws_desc[blockIdx.x] = make_int4(-1, 0, 0, 0);
+    return;
+  }
+  long long left = min(per, total - u0);
+  int b = s_b;
+  uint32_t ignore = 0;
+  PagedSeq s = paged_seq(p.map, b, p.T, p.max_rows, ignore);
+  int n_rb, n_tiles;
+  split_units(s, p, n_rb, n_tiles);
+  int tile0 = (int)(s_off % n_tiles), rb, g;
+  {
+    const int item = (int)(s_off / n_tiles);
+    g = item / n_rb;
+    rb = item % n_rb;
+  }
+  if (tid == 0) p.ws_desc[blockIdx.x] = make_int4(-1, 0, 0, 0);
+
+  const int rg = warp / KG, kg = warp % KG;
+  const int hpg = p.hpg, page_mask = (1 << p.map.page_shift) - 1;
+  const T* const qp = static_cast<const T*>(p.q);
+  const uint32_t smb = smem_u32(sm);
+
+  while (left > 0) {
+    const int tile1 = (int)min((long long)n_tiles, tile0 + left);
+    const int tok0 = rb * p.rows_tok;                       // first row of the block
+    const int ntok = min(p.rows_tok, s.t - tok0), nvec = ntok * hpg;
+    const int* table = p.map.table + (size_t)b * p.map.max_pages;
+    const T* const kp = static_cast<const T*>(p.ck);
+    const T* const vp = static_cast<const T*>(p.cv);
+
+    // --- page ids of a tile: thread i < 4 holds the page of keys [16 i, 16 i + 16)
+    auto fetch_page = [&](int tile) -> int {
+      const int key = tile * kKeys + tid * 16;
+      if (tid >= kKeys / 16 || tile >= tile1 || key >= s.len) return -1;
+      const int id = table[key >> p.map.page_shift];
+      if (!page_ok(p.map, id)) {
+        set_err(p.err, SWA_DERR_PAGE);
+        return -1;
+      }
+      return id;
+    };
+    auto load_tile = [&](int tile, const int* ids) {
+      const int st = tile % C::ST;
+      constexpr int CH = D / 8;                             // 16-byte chunks of a row
+#pragma unroll
+      for (int i = 0; i < kKeys * CH / kThreads; ++i) {
+        const int x = tid + i * kThreads, r = x / CH, c = x % CH;
+        const int key = tile * kKeys + r, id = ids[r >> 4];
+        const bool ok = key < s.len && id >= 0;
+        const size_t off = ok ? (((size_t)id * p.map.nk + g << p.map.page_shift) + (key & page_mask)) * D + c * 8 : 0;
+        const uint32_t dst = smb + (uint32_t)(st * 2 * C::TILE) + tile_off<D>(r, c);
+        cp16_or_zero(dst, kp + off, ok);
+        cp16_or_zero(dst + C::TILE, vp + off, ok);
+      }
+    };
+
+    // prologue: the first ST - 1 tiles, with their page ids read directly
+    __syncthreads();
+#pragma unroll 1
+    for (int i = 0; i < C::ST - 1; ++i) {
+      if (tile0 + i < tile1) {
+        int ids[kKeys / 16];
+#pragma unroll
+        for (int j = 0; j < kKeys / 16; ++j) {
+          const int key = (tile0 + i) * kKeys + j * 16;
+          ids[j] = -1;
+          if (key < s.len) {
+            const int id = table[key >> p.map.page_shift];
+            if (page_ok(p.map, id)) ids[j] = id;
+            else set_err(p.err, SWA_DERR_PAGE);
+          }
+        }
+        load_tile(tile0 + i, ids);
+      }
+      cp_commit();
+    }
+    int next_id = fetch_page(tile0 + C::ST - 1);
+
+    // --- Q of this warp's 16 rows as A operands; the rows' limits
+    uint32_t qf[D / 16][4];
+    int lim[2];
+#pragma unroll
+    for (int hrow = 0; hrow < 2; ++hrow) {
+      const int r = rg * 16 + hrow * 8 + (lane >> 2);
+      const bool ok = r < nvec;
+      const int i = ok ? r / hpg : 0, h = ok ? r % hpg : 0;
+      lim[hrow] = ok ? min(s.len, s.len - s.t + tok0 + i + 1) : 0;
+      const T* src = qp + (size_t)(s.r0 + tok0 + i) * p.q_row + (size_t)(g * hpg + h) * D + (lane & 3) * 2;
+#pragma unroll
+      for (int k = 0; k < D / 16; ++k) {
+        qf[k][hrow] = ok ? *reinterpret_cast<const uint32_t*>(src + k * 16) : 0u;
+        qf[k][hrow + 2] = ok ? *reinterpret_cast<const uint32_t*>(src + k * 16 + 8) : 0u;
+      }
+    }
+    const int lim_min = s.len - s.t + tok0 + 1;            // keys below it are seen by every row
+
+    float o[D / 8][4];
+#pragma unroll
+    for (int i = 0; i < D / 8; ++i)
+#pragma unroll
+      for (int j = 0; j < 4; ++j) o[i][j] = 0.f;
+    float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
+
+    for (int tile = tile0; tile < tile1; ++tile) {
+      if (tid < kKeys / 16) s_pages[tile & 1][tid] = next_id;
+      cp_wait<C::ST - 2>();
+      __syncthreads();                                     // tile landed; its predecessor's stage is free
+      if (tile + C::ST - 1 < tile1) load_tile(tile + C::ST - 1, s_pages[tile & 1]);
+      cp_commit();
+      next_id = fetch_page(tile + C::ST);
+      const uint32_t kb = smb + (uint32_t)((tile % C::ST) * 2 * C::TILE), vb = kb + C::TILE;
+      const int k0 = tile * kKeys + kg * KW;
+
+      float sc[KW / 8][4];
+#pragma unroll
+      for (int i = 0; i < KW / 8; ++i)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) sc[i][j] = 0.f;
+#pragma unroll
+      for (int k = 0; k < D / 16; ++k) {
+#pragma unroll
+        for (int n = 0; n < KW / 16; ++n) {
+          uint32_t f[4];
+          ldsm4(f, kb + tile_off<D>(kg * KW + n * 16 + ((lane >> 4) << 3) + (lane & 7), k * 2 + ((lane >> 3) & 1)));
+          mma16816<T>(sc[2 * n], qf[k], f[0], f[1]);
+          mma16816<T>(sc[2 * n + 1], qf[k], f[2], f[3]);
+        }
+      }
+      // scores in log2 units, masked
+      const bool mask = tile * kKeys + kKeys > lim_min;
+      float mx[2] = {-INFINITY, -INFINITY};
+#pragma unroll
+      for (int n = 0; n < KW / 8; ++n)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          float x = sc[n][j] * p.qmul;
+          if (mask && k0 + n * 8 + (lane & 3) * 2 + (j & 1) >= lim[j >> 1]) x = -INFINITY;
+          sc[n][j] = x;
+          mx[j >> 1] = fmaxf(mx[j >> 1], x);
+        }
+#pragma unroll
+      for (int r = 0; r < 2; ++r) {
+        mx[r] = fmaxf(mx[r], __shfl_xor_sync(0xffffffffu, mx[r], 1));
+        mx[r] = fmaxf(mx[r], __shfl_xor_sync(0xffffffffu, mx[r], 2));
+        const float mn = fmaxf(m[r], mx[r]);
+        const float a = mn == -INFINITY ? 1.f : ex2(m[r] - mn);   // m = -inf: 0
+        m[r] = mn;
+        l[r] *= a;
+#pragma unroll
+        for (int i = 0; i < D / 8; ++i) {
+          o[i][2 * r] *= a;
+          o[i][2 * r + 1] *= a;
+        }
+        mx[r] = (mn == -INFINITY ? 0.f : mn) - PScale<T>::kLog2;
+      }
+#pragma unroll
+      for (int n = 0; n < KW / 8; ++n)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          sc[n][j] = ex2(sc[n][j] - mx[j >> 1]);
+          l[j >> 1] += sc[n][j];
+        }
+#pragma unroll
+      for (int n = 0; n < KW / 16; ++n) {
+        const uint32_t pa[4] = {pack2(sc[2 * n][0], sc[2 * n][1], (const T*)nullptr),
+                                pack2(sc[2 * n][2], sc[2 * n][3], (const T*)nullptr),
+                                pack2(sc[2 * n + 1][0], sc[2 * n + 1][1], (const T*)nullptr),
+                                pack2(sc[2 * n + 1][2], sc[2 * n + 1][3], (const T*)nullptr)};
+#pragma unroll
+        for (int dd = 0; dd < D / 16; ++dd) {
+          uint32_t f[4];
+          ldsm4t(f, vb + tile_off<D>(kg * KW + n * 16 + (((lane >> 3) & 1) << 3) + (lane & 7), dd * 2 + (lane >> 4)));
+          mma16816<T>(o[2 * dd], pa, f[0], f[1]);
+          mma16816<T>(o[2 * dd + 1], pa, f[2], f[3]);
+        }
+      }
+    }
+
+    // --- join the key groups through shared memory (the stages are done with)
+    cp_wait<0>();
+    __syncthreads();
+    float* const ob = reinterpret_cast<float*>(sm);          // [4 warps][16][D]
+#pragma unroll
+    for (int r = 0; r < 2; ++r) {
+      l[r] += __shfl_xor_sync(0xffffffffu, l[r], 1);
+      l[r] += __shfl_xor_sync(0xffffffffu, l[r], 2);
+      const int row = r * 8 + (lane >> 2);
+      if ((lane & 3) == 0) s_ml[warp][row] = make_float2(m[r], l[r]);
+#pragma unroll
+      for (int i = 0; i < D / 8; ++i)
+        *reinterpret_cast<float2*>(ob + (warp * 16 + row) * D + i * 8 + (lane & 3) * 2) =
+            make_float2(o[i][2 * r], o[i][2 * r + 1]);
+    }
+    __syncthreads();
+    const bool whole = tile0 == 0 && tile1 == n_tiles;
+    // record of the item this CTA continues: slot 2c, of the one it starts: 2c + 1
+    const size_t rec = ((size_t)blockIdx.x * 2 + (tile0 == 0 ? 1 : 0)) * ROWS;
+    for (int x = tid; x < nvec * (D / 8); x += kThreads) {
+      const int row = x / (D / 8), c = x % (D / 8);
+      const int w0 = (row >> 4) * KG, rr = row & 15;
+      float mt = -INFINITY;
+#pragma unroll
+      for (int w = 0; w < KG; ++w) mt = fmaxf(mt, s_ml[w0 + w][rr].x);
+      float lt = 0.f, acc[8] = {};
+#pragma unroll
+      for (int w = 0; w < KG; ++w) {
+        const float2 ml = s_ml[w0 + w][rr];
+        const float a = ml.x == -INFINITY ? 0.f : ex2(ml.x - mt);
+        float y[8];
+        load8(ob + ((w0 + w) * 16 + rr) * D + c * 8, y);
+        lt += a * ml.y;
+#pragma unroll
+        for (int j = 0; j < 8; ++j) acc[j] += a * y[j];
+      }
+      if (whole) {
+        paged_store_row<T>(p, s.r0 + tok0 + row / hpg, g * hpg + row % hpg, D, c * 8, mt, lt, acc, c == 0);
+      } else {
+        store8(p.ws_acc + (rec + row) * D + c * 8, acc);
+        if (c == 0) p.ws_ml[rec + row] = make_float2(mt, lt);
+      }
+    }
+    if (!whole && tile0 == 0 && tid == 0) {
+      // units of this item from here on / per CTA: the CTA that ends it
+      const long long end = u0 + (min(per, total - u0) - left) + n_tiles - 1;
+      p.ws_desc[blockIdx.x] = make_int4(b, g, rb, (int)(end / per));
+    }
+
+    // --- the next item
+    left -= tile1 - tile0;
+    tile0 = 0;
+    if (left <= 0) break;
+    if (++rb == n_rb) {
+      rb = 0;
+      if (++g == p.map.nk) {
+        g = 0;
+        do {
+          ++b;
+          s = paged_seq(p.map, b, p.T, p.max_rows, ignore);
+        } while (s.t == 0);
+        split_units(s, p, n_rb, n_tiles);
+      }
+    }
+  }
+}
+
+// ---------------------------------------------------------------------------
+// Merge: block (c, row) joins the records of the item that CTA c left unfinished at
+// its end: slot 2c + 1, then slot 2c' of the following CTAs up to the one that ended
+// it. 8 features a lane; the thread groups take the records in turn.
+// ---------------------------------------------------------------------------
+constexpr int kMergeThreads = 128;
+template <typename T, int D>
+__global__ void __launch_bounds__(kMergeThreads) paged_merge_kernel(const PagedAttendParams p, int rows) {
+  constexpr int L = D / 8, NG = kMergeThreads / L;
+  __shared__ float s_acc[NG][D];
+  __shared__ float s_l[NG];
+  pdl_wait();
+  pdl_trigger();
+  const int4 dsc = p.ws_desc[blockIdx.x];
+  if (dsc.x < 0) return;
+  uint32_t ignore = 0;
+  const PagedSeq s = paged_seq(p.map, dsc.x, p.T, p.max_rows, ignore);
+  const int tok0 = dsc.z * p.rows_tok, row = blockIdx.y;
+  const int nvec = min(p.rows_tok, s.t - tok0) * p.hpg;
+  if (row >= nvec) return;
+  const int c0 = blockIdx.x, n = dsc.w - c0 + 1;
+  const int tid = threadIdx.x, grp = tid / L, c = tid % L;
+  auto rec = [&](int i) { return ((size_t)(c0 + i) * 2 + (i == 0 ? 1 : 0)) * rows + row; };
+  float mt = -INFINITY;
+  for (int i = tid; i < n; i += kMergeThreads) mt = fmaxf(mt, p.ws_ml[rec(i)].x);
+#pragma unroll
+  for (int o = 16; o; o >>= 1) mt = fmaxf(mt, __shfl_xor_sync(0xffffffffu, mt, o));
+  if ((tid & 31) == 0) s_l[tid >> 5] = mt;
+  __syncthreads();
+  mt = fmaxf(fmaxf(s_l[0], s_l[1]), fmaxf(s_l[2], s_l[3]));
+  __syncthreads();
+  float lt = 0.f, acc[8] = {};
+#pragma unroll 4
+  for (int i = grp; i < n; i += NG) {
+    const float2 ml = p.ws_ml[rec(i)];
+    const float a = ml.x == -INFINITY ? 0.f : ex2(ml.x - mt);
+    float y[8];
+    load8(p.ws_acc + rec(i) * D + c * 8, y);
+    lt += a * ml.y;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) acc[j] += a * y[j];
+  }
+  store8(&s_acc[grp][c * 8], acc);
+  if (c == 0) s_l[grp] = lt;
+  __syncthreads();
+  if (grp == 0) {
+#pragma unroll
+    for (int w = 1; w < NG; ++w) {
+      float y[8];
+      load8(&s_acc[w][c * 8], y);
+      lt += s_l[w];
+#pragma unroll
+      for (int j = 0; j < 8; ++j) acc[j] += y[j];
+    }
+    paged_store_row<T>(p, s.r0 + tok0 + row / p.hpg, dsc.y * p.hpg + row % p.hpg, D, c * 8, mt, lt, acc, c == 0);
+  }
+}
+
+// ---------------------------------------------------------------------------
+// Launches
+// ---------------------------------------------------------------------------
+struct SplitPlan {
+  int rows, rows_tok, grid;       // query vectors of a block, chunk rows of it, CTAs
+  size_t off_ml, off_desc, bytes;
+};
+
+template <typename T, int D, int ROWS>
+static int split_occupancy() {
+  static int cache[64] = {};
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return 1;
+  if (!cache[dev]) {
+    auto k = paged_split_kernel<T, D, ROWS>;
+    int n = 0;
+    if (cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, SplitCfg<D>::SMEM) != cudaSuccess ||
+        cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, k, kThreads, SplitCfg<D>::SMEM) != cudaSuccess || n < 1) {
+      (void)cudaGetLastError();
+      n = 1;
+    }
+    cache[dev] = n;
+  }
+  return cache[dev];
+}
+
+template <typename T, int D, int ROWS>
+static int launch_split(const PagedAttendParams& p, const SplitPlan& sp, cudaStream_t s, cudaEvent_t e0, cudaEvent_t e1) {
+  cudaError_t e = cudaFuncSetAttribute(paged_split_kernel<T, D, ROWS>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                       SplitCfg<D>::SMEM);
+  if (e != cudaSuccess) return cuda_status(e);
+  if (e0 && (e = cudaEventRecord(e0, s)) != cudaSuccess) return cuda_status(e);
+  int rc = finish_launch(launch_pdl(paged_split_kernel<T, D, ROWS>, dim3(sp.grid), dim3(kThreads), SplitCfg<D>::SMEM, s, p));
+  if (rc != SWA_OK) return rc;
+  if (e1 && (e = cudaEventRecord(e1, s)) != cudaSuccess) return cuda_status(e);
+  const int most = p.max_rows < p.rows_tok ? p.max_rows : p.rows_tok;
+  return finish_launch(launch_pdl(paged_merge_kernel<T, D>, dim3(sp.grid, most * p.hpg), dim3(kMergeThreads), 0, s, p, ROWS));
+}
+
+template <typename F>
+static int by_type(int dtype, int hd, int rows, F f) {
+#define SWA_ROWS(T, D) (rows == 16 ? f((T*)nullptr, Int<D>{}, Int<16>{}) : rows == 32 ? f((T*)nullptr, Int<D>{}, Int<32>{}) \
+                                                                                    : f((T*)nullptr, Int<D>{}, Int<64>{}))
+#define SWA_HD(T) (hd == 64 ? SWA_ROWS(T, 64) : hd == 128 ? SWA_ROWS(T, 128) : SWA_ROWS(T, 256))
+  return dtype == SWA_BF16 ? SWA_HD(__nv_bfloat16) : SWA_HD(__half);
+#undef SWA_HD
+#undef SWA_ROWS
+}
+
+static void split_plan(const swa_paged_attend_args* a, SplitPlan* sp) {
+  const int hpg = a->nh / a->cache.nk;
+  const long long vecs = (long long)a->max_rows * hpg;
+  sp->rows = vecs <= 16 ? 16 : vecs <= 32 ? 32 : 64;
+  sp->rows_tok = sp->rows / hpg;
+  const int occ = by_type(a->cache.dtype, a->cache.hd, sp->rows, [](auto* t, auto d, auto r) {
+    return split_occupancy<std::remove_pointer_t<decltype(t)>, decltype(d)::value, decltype(r)::value>();
+  });
+  const int sms = num_sms() > 0 ? num_sms() : 148;
+  sp->grid = sms * occ;
+  const size_t recs = (size_t)sp->grid * 2 * sp->rows;
+  sp->off_ml = up256s(recs * a->cache.hd * sizeof(float));
+  sp->off_desc = sp->off_ml + up256s(recs * sizeof(float2));
+  sp->bytes = sp->off_desc + up256s((size_t)sp->grid * sizeof(int4));
+}
+
+// Sizes alone (the workspace query); pointers are checked by the call.
+static bool attend_sizes_ok(const swa_paged_attend_args* a) {
+  const swa_paged_cache& c = a->cache;
+  if (c.B < 1 || c.B > 65535 || c.nk < 1 || c.nk > 65535 || (c.hd != 64 && c.hd != 128 && c.hd != 256)) return false;
+  if (c.dtype != SWA_BF16 && c.dtype != SWA_F16) return false;
+  if (a->T < 0 || a->max_rows < 1 || a->nh < 1 || a->nh % c.nk || a->nh / c.nk > 32) return false;
+  return (long long)a->T * a->nh < (1LL << 31);
+}
+
+}  // namespace swa
+
+using namespace swa;
+
+extern "C" {
+
+size_t swa_paged_attend_workspace_size(const swa_paged_attend_args* a) {
+  if (!a || !attend_sizes_ok(a)) return 0;
+  SplitPlan sp;
+  split_plan(a, &sp);
+  return sp.bytes;
+}
+
+int swa_paged_attend(const swa_paged_attend_args* a, cudaStream_t stream) {
+  if (!a) return SWA_E_NULL;
+  const swa_paged_cache& c = a->cache;
+  const int rc = paged_cache_status(&c, true);
+  if (rc != SWA_OK) return rc;
+  if (!attend_sizes_ok(a) || !(a->scale >= 0.f) || std::isinf(a->scale)) return SWA_E_SHAPE;
+  if (a->T == 0) return SWA_OK;
+  if (!a->q || !a->out) return SWA_E_NULL;
+  if (a->q_row < (long long)a->nh * c.hd || a->q_row > (1LL << 40)) return SWA_E_SHAPE;
+  if (!aligned16p(a->q) || !aligned16p(a->out) || (a->q_row & 7) || (reinterpret_cast<uintptr_t>(a->lse) & 3u))
+    return SWA_E_ALIGN;
+  SplitPlan sp;
+  split_plan(a, &sp);
+  if (!a->workspace || a->workspace_bytes < sp.bytes) return SWA_E_WORKSPACE;
+  if (reinterpret_cast<uintptr_t>(a->workspace) & 255u) return SWA_E_ALIGN;
+  PagedAttendParams p{};
+  p.map = paged_map(&c);
+  p.T = a->T; p.nh = a->nh; p.hpg = a->nh / c.nk; p.max_rows = a->max_rows;
+  p.rows_tok = sp.rows_tok;
+  p.qmul = a->scale * 1.4426950408889634f;
+  p.q = a->q; p.q_row = a->q_row; p.ck = c.k; p.cv = c.v;
+  p.out = a->out; p.out_f32 = a->out_f32 != 0; p.lse = a->lse;
+  char* ws = static_cast<char*>(a->workspace);
+  p.ws_acc = reinterpret_cast<float*>(ws);
+  p.ws_ml = reinterpret_cast<float2*>(ws + sp.off_ml);
+  p.ws_desc = reinterpret_cast<int4*>(ws + sp.off_desc);
+  p.err = a->err;
+  return by_type(c.dtype, c.hd, sp.rows, [&](auto* t, auto d, auto r) {
+    return launch_split<std::remove_pointer_t<decltype(t)>, decltype(d)::value, decltype(r)::value>(
+        p, sp, stream, a->ev_start, a->ev_stop);
+  });
+}
+
+}  // extern "C"

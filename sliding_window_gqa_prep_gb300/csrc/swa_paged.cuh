@@ -1,0 +1,114 @@
+// Shared by the paged-cache and rotary kernels: element types, the page map and
+// a sequence's rows and length as the kernels read them (all bounds applied).
+#pragma once
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+
+#include "swa_internal.cuh"
+
+namespace swa {
+
+// The page map of a swa_paged_cache as the kernels take it (by value).
+struct PagedMap {
+  int B, nk, page_shift, num_pages, max_pages, cap;   // cap = max_pages << page_shift
+  const int32_t* table;
+  const int32_t* row_start;
+  const int32_t* lens;
+};
+
+// Host checks shared by the paged calls (swa_paged.cu). rows: row_start is read.
+int paged_cache_status(const swa_paged_cache* c, bool rows);
+PagedMap paged_map(const swa_paged_cache* c);
+// [a, a + an) and [b, b + bn) share a byte
+bool bytes_overlap(const void* a, size_t an, const void* b, size_t bn);
+inline bool aligned16p(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
+inline size_t up256s(size_t x) { return (x + 255) & ~(size_t)255; }
+
+#ifdef __CUDACC__
+
+// Rows and keys of sequence b. Rows out of range leave t = 0, a length out of
+// range is clamped; `bits` collects the SWA_DERR_* of what was found.
+struct PagedSeq {
+  int r0, t, len;
+};
+__device__ __forceinline__ PagedSeq paged_seq(const PagedMap& m, int b, int T, int max_rows, uint32_t& bits) {
+  PagedSeq s;
+  const int r0 = m.row_start[b], r1 = m.row_start[b + 1];
+  int len = m.lens[b];
+  s.r0 = r0;
+  s.t = r1 - r0;
+  if (r0 < 0 || r1 < r0 || r1 > T || s.t > max_rows) {
+    bits |= SWA_DERR_SEGMENT;
+    s.r0 = 0;
+    s.t = 0;
+  }
+  if (len < 0 || len > m.cap) {
+    bits |= SWA_DERR_META;
+    len = len < 0 ? 0 : m.cap;
+  }
+  s.len = len;
+  return s;
+}
+
+__device__ __forceinline__ bool page_ok(const PagedMap& m, int page) {
+  return (unsigned)page < (unsigned)m.num_pages;
+}
+
+// Eight elements of a 16-bit or f32 row, 16-byte aligned, to and from f32.
+__device__ __forceinline__ void load8(const float* p, float (&x)[8]) {
+  const float4 a = *reinterpret_cast<const float4*>(p), b = *reinterpret_cast<const float4*>(p + 4);
+  x[0] = a.x; x[1] = a.y; x[2] = a.z; x[3] = a.w;
+  x[4] = b.x; x[5] = b.y; x[6] = b.z; x[7] = b.w;
+}
+__device__ __forceinline__ void load8(const __nv_bfloat16* p, float (&x)[8]) {
+  const uint4 r = *reinterpret_cast<const uint4*>(p);
+  const uint32_t w[4] = {r.x, r.y, r.z, r.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {   // a bf16 is the upper half of its f32
+    x[2 * i] = __uint_as_float(w[i] << 16);
+    x[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+  }
+}
+__device__ __forceinline__ void load8(const __half* p, float (&x)[8]) {
+  const uint4 r = *reinterpret_cast<const uint4*>(p);
+  const uint32_t w[4] = {r.x, r.y, r.z, r.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&w[i]));
+    x[2 * i] = f.x;
+    x[2 * i + 1] = f.y;
+  }
+}
+__device__ __forceinline__ uint32_t pack2(float a, float b, const __nv_bfloat16*) {
+  const __nv_bfloat162 v = __floats2bfloat162_rn(a, b);
+  return *reinterpret_cast<const uint32_t*>(&v);
+}
+__device__ __forceinline__ uint32_t pack2(float a, float b, const __half*) {
+  const __half2 v = __floats2half2_rn(a, b);
+  return *reinterpret_cast<const uint32_t*>(&v);
+}
+__device__ __forceinline__ void store8(float* p, const float (&x)[8]) {
+  *reinterpret_cast<float4*>(p) = make_float4(x[0], x[1], x[2], x[3]);
+  *reinterpret_cast<float4*>(p + 4) = make_float4(x[4], x[5], x[6], x[7]);
+}
+template <typename T>
+__device__ __forceinline__ void store8(T* p, const float (&x)[8]) {
+  *reinterpret_cast<uint4*>(p) = make_uint4(pack2(x[0], x[1], p), pack2(x[2], x[3], p), pack2(x[4], x[5], p),
+                                            pack2(x[6], x[7], p));
+}
+__device__ __forceinline__ float load1(const float* p) { return *p; }
+__device__ __forceinline__ float load1(const __nv_bfloat16* p) { return __bfloat162float(*p); }
+__device__ __forceinline__ float load1(const __half* p) { return __half2float(*p); }
+__device__ __forceinline__ void store1(float* p, float x) { *p = x; }
+__device__ __forceinline__ void store1(__nv_bfloat16* p, float x) { *p = __float2bfloat16_rn(x); }
+__device__ __forceinline__ void store1(__half* p, float x) { *p = __float2half_rn(x); }
+
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+#endif  // __CUDACC__
+
+}  // namespace swa

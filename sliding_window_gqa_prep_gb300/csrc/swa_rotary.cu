@@ -1,0 +1,366 @@
+// Rotary positions of packed rows (swa_rotary) and of a chunk that enters the
+// paged cache (swa_paged_append).
+//
+// u' = u cos a - v sin a, v' = v cos a + u sin a with a = pos * f. The angle is
+// taken modulo one turn in integers: turns = f / 2 pi as a 64-bit fraction, and
+// pos * turns modulo 2^64 is the angle's fraction of a turn, exact but for the
+// fraction's own last bit. Its upper 32 bits, signed, times 2^-31 are half turns in
+// [-1, 1), what sincospif takes: no f64 arithmetic (two lanes an SM here) and no
+// range reduction, at any position.
+//
+// Memory bound: each element is read and written once. A thread owns one unit (8
+// pairs, or 8 features when interleaved: 16-byte accesses for 16-bit types) of one
+// row and walks `HB` heads with it, so that an angle's sine and cosine are computed
+// once for those heads; HB shrinks while the launch would not fill the device.
+// Units whose halves do not start at multiples of 8 features take the same kernel
+// with one pair (two features) a unit.
+#include <cmath>
+
+#include "swa_paged.cuh"
+
+namespace swa {
+
+struct RotaryParams {
+  int T, H, hd, rot, HB, nHB, units, inverse;
+  float mag;
+  const void* x;               // rows of heads [0, H) (swa_rotary) or of q (append)
+  long long x_row, x_head;
+  void* out;
+  long long out_row, out_head;
+  const int32_t* pos;
+  const uint64_t* turns;
+  // append: heads [0, nh) are q, [nh, nh + nk) k, [nh + nk, nh + 2 nk) v
+  int nh, nk, hd_page;         // hd_page = page * hd
+  const void* k;
+  const void* v;
+  long long k_row, v_row;
+  void* cache_k;
+  void* cache_v;
+  PagedMap map;
+  int32_t* slot_pos;
+  float* weight;
+  uint32_t* err;
+};
+
+constexpr int kRotThreads = 256;
+constexpr int kRotStarts = 2048;   // row starts searched in shared memory
+
+// V: pairs (half layout) or features (interleaved) of a unit
+template <typename TI, typename TO, bool INTER, int V, bool APPEND>
+__global__ void __launch_bounds__(kRotThreads) rotary_kernel(const RotaryParams p) {
+  __shared__ int starts[APPEND ? kRotStarts : 1];
+  pdl_wait();
+  pdl_trigger();
+  if constexpr (APPEND) {
+    if (p.map.B < kRotStarts) {
+      for (int i = threadIdx.x; i <= p.map.B; i += kRotThreads) starts[i] = p.map.row_start[i];
+      __syncthreads();
+    }
+  }
+  const unsigned idx = blockIdx.x * (unsigned)kRotThreads + threadIdx.x;
+  const unsigned u = idx % (unsigned)p.units, rest = idx / (unsigned)p.units;
+  const int h0 = (int)(rest % (unsigned)p.nHB) * p.HB;
+  const unsigned row = rest / (unsigned)p.nHB;
+  if (row >= (unsigned)p.T) return;
+
+  // the row's sequence and slot
+  long long slot_off = -1;           // cache element of (page, head 0, slot), < 0: not stored
+  long long aux_off = -1;            // slot_pos / weight entry of head 0
+  if constexpr (APPEND) {
+    const bool in_smem = p.map.B < kRotStarts;
+    int lo = 0, hi = p.map.B;        // the last b with row_start[b] <= row
+    while (hi - lo > 1) {
+      const int mid = (lo + hi) >> 1;
+      if ((in_smem ? starts[mid] : p.map.row_start[mid]) <= (int)row) lo = mid; else hi = mid;
+    }
+    uint32_t bits = 0;
+    const int r0 = p.map.row_start[lo], r1 = p.map.row_start[lo + 1];
+    if (((int)row >= r1 && lo == p.map.B - 1 && r1 >= r0 && r1 >= 0) || ((int)row < r0 && lo == 0))
+      return;                        // behind the last sequence or before the first
+    if (r0 < 0 || r1 > p.T || (int)row < r0 || (int)row >= r1) {
+      if (u == 0 && h0 == 0) set_err(p.err, SWA_DERR_SEGMENT);
+      return;
+    }
+    const int len = p.map.lens[lo];
+    const long long slot = (long long)len - r1 + (int)row;
+    if (len < 0 || len > p.map.cap || slot < 0) {
+      bits |= SWA_DERR_META;
+    } else {
+      const int page = p.map.table[(size_t)lo * p.map.max_pages + (size_t)(slot >> p.map.page_shift)];
+      if (!page_ok(p.map, page)) {
+        bits |= SWA_DERR_PAGE;
+      } else {
+        slot_off = (long long)page * p.nk * p.hd_page + (slot & ((1 << p.map.page_shift) - 1)) * p.hd;
+        aux_off = (long long)lo * p.nk * p.map.cap + slot;
+      }
+    }
+    if (bits && u == 0 && h0 == 0) set_err(p.err, bits);
+  }
+
+  // the unit's features and angles
+  constexpr int NP = INTER ? (V > 1 ? V / 2 : 1) : V;   // pairs of a unit
+  const int half = p.rot >> 1;
+  const int rot_units = INTER ? p.rot / V : half / V;
+  const bool turn = (int)u < rot_units;
+  const int e0 = (int)u * (INTER ? V / 2 : V);           // first pair
+  const int f0 = turn ? (INTER ? 2 * e0 : e0)            // first feature
+                      : (INTER ? (int)u * V : p.rot + ((int)u - rot_units) * V);
+  float c[NP], s[NP];
+  if (turn) {
+    const uint64_t pos = (uint64_t)(int64_t)p.pos[row];
+#pragma unroll
+    for (int i = 0; i < NP; ++i) {
+      const uint64_t frac = pos * p.turns[e0 + i];       // modulo 2^64: the fraction of a turn
+      sincospif((float)(int32_t)(uint32_t)(frac >> 32) * 0x1p-31f, &s[i], &c[i]);
+      c[i] *= p.mag;
+      s[i] *= p.inverse ? -p.mag : p.mag;
+    }
+  }
+
+  const int h1 = min(h0 + p.HB, p.H);
+#pragma unroll 4
+  for (int h = h0; h < h1; ++h) {
+    const TI* src;
+    TO* dst;
+    bool rotate = turn;
+    if constexpr (APPEND) {
+      if (h < p.nh) {
+        src = static_cast<const TI*>(p.x) + (long long)row * p.x_row + (long long)h * p.hd;
+        dst = static_cast<TO*>(p.out) + (long long)row * p.out_row + (long long)h * p.hd;
+      } else {
+        const bool is_k = h < p.nh + p.nk;
+        const int g = h - p.nh - (is_k ? 0 : p.nk);
+        if (slot_off < 0) continue;
+        src = (is_k ? static_cast<const TI*>(p.k) + (long long)row * p.k_row
+                    : static_cast<const TI*>(p.v) + (long long)row * p.v_row) + (long long)g * p.hd;
+        dst = static_cast<TO*>(is_k ? p.cache_k : p.cache_v) + slot_off + (long long)g * p.hd_page;
+        rotate = turn && is_k;
+        if (is_k && u == 0) {
+          if (p.slot_pos) p.slot_pos[aux_off + (long long)g * p.map.cap] = p.pos[row];
+          if (p.weight) p.weight[aux_off + (long long)g * p.map.cap] = 0.f;
+        }
+      }
+    } else {
+      src = static_cast<const TI*>(p.x) + (long long)row * p.x_row + (long long)h * p.x_head;
+      dst = static_cast<TO*>(p.out) + (long long)row * p.out_row + (long long)h * p.out_head;
+    }
+    if constexpr (V == 8) {
+      float a[8];
+      load8(src + f0, a);
+      if constexpr (INTER) {
+        if (rotate) {
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const float x = a[2 * i], y = a[2 * i + 1];
+            a[2 * i] = x * c[i] - y * s[i];
+            a[2 * i + 1] = y * c[i] + x * s[i];
+          }
+        }
+        store8(dst + f0, a);
+      } else if (turn) {
+        float b[8];
+        load8(src + half + f0, b);
+        if (rotate) {
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            const float x = a[i], y = b[i];
+            a[i] = x * c[i] - y * s[i];
+            b[i] = y * c[i] + x * s[i];
+          }
+        }
+        store8(dst + f0, a);
+        store8(dst + half + f0, b);
+      } else {
+        store8(dst + f0, a);
+      }
+    } else {
+      const int f1 = INTER ? f0 + 1 : f0 + half;
+      if (turn) {
+        const float x = load1(src + f0), y = load1(src + f1);
+        store1(dst + f0, rotate ? x * c[0] - y * s[0] : x);
+        store1(dst + f1, rotate ? y * c[0] + x * s[0] : y);
+      } else {
+        store1(dst + f0, load1(src + f0));
+        if constexpr (INTER) store1(dst + f1, load1(src + f1));
+      }
+    }
+  }
+}
+
+// Units of a row: pairs of the rotated part, then the copied part.
+static bool rotary_units(RotaryParams& p, bool inter, bool* wide) {
+  const int half = p.rot / 2, rest = p.hd - p.rot;
+  *wide = inter ? p.rot % 8 == 0 : half % 8 == 0;      // hd is a multiple of 8, so the rest is too
+  if (inter)
+    p.units = p.hd / (*wide ? 8 : 2);
+  else
+    p.units = *wide ? half / 8 + rest / 8 : half + rest;
+  // heads per thread: enough threads to fill the device four times over first
+  const long long all = (long long)p.T * p.units * p.H, fill = 4LL * 2048 * (num_sms() > 0 ? num_sms() : 148);
+  long long hb = all / fill;
+  p.HB = (int)(hb < 1 ? 1 : (hb > 8 ? 8 : hb));
+  if (p.HB > p.H) p.HB = p.H;
+  p.nHB = (p.H + p.HB - 1) / p.HB;
+  return (long long)p.T * p.units * p.nHB < (1LL << 31);
+}
+
+template <typename TI, typename TO, bool APPEND>
+static int launch_rotary(const RotaryParams& p, bool inter, bool wide, cudaStream_t s) {
+  const long long threads = (long long)p.T * p.units * p.nHB;
+  const dim3 grid((unsigned)((threads + kRotThreads - 1) / kRotThreads)), block(kRotThreads);
+  cudaError_t e;
+  if (inter)
+    e = wide ? launch_pdl(rotary_kernel<TI, TO, true, 8, APPEND>, grid, block, 0, s, p)
+             : launch_pdl(rotary_kernel<TI, TO, true, 2, APPEND>, grid, block, 0, s, p);
+  else
+    e = wide ? launch_pdl(rotary_kernel<TI, TO, false, 8, APPEND>, grid, block, 0, s, p)
+             : launch_pdl(rotary_kernel<TI, TO, false, 1, APPEND>, grid, block, 0, s, p);
+  return finish_launch(e);
+}
+
+static int type_bytes(int t) { return t == SWA_F32 ? 4 : 2; }
+
+// Frequencies of a schedule in f64 (declared and explained in swa.h).
+static int rotary_freqs(const swa_rotary_schedule* s, int e, double* f) {
+  double theta = s->theta;
+  if (s->kind == SWA_ROTARY_BASE) theta *= std::pow(s->factor, (double)s->rot / (s->rot - 2));
+  double v = std::pow(theta, -2.0 * e / s->rot);
+  if (s->kind == SWA_ROTARY_LINEAR) v /= s->factor;
+  if (s->kind == SWA_ROTARY_PARTS) {
+    const double r = s->orig_len * v / 6.283185307179586476925;
+    double keep = (r - s->low) / (s->high - s->low);
+    keep = keep < 0 ? 0 : (keep > 1 ? 1 : keep);
+    v = keep * v + (1 - keep) * v / s->factor;
+  }
+  *f = v;
+  return std::isfinite(v) && v >= 0;
+}
+
+}  // namespace swa
+
+using namespace swa;
+
+extern "C" {
+
+int swa_rotary_turns(const swa_rotary_schedule* s, double* freqs, uint64_t* turns) {
+  if (!s) return SWA_E_NULL;
+  if (s->kind < SWA_ROTARY_PLAIN || s->kind > SWA_ROTARY_PARTS) return SWA_E_SHAPE;
+  if (s->rot < 2 || s->rot > 1024 || (s->rot & 1) || !(s->theta > 0.0) || !std::isfinite(s->theta))
+    return SWA_E_SHAPE;
+  if (s->kind != SWA_ROTARY_PLAIN && !(s->factor >= 1.0 && std::isfinite(s->factor))) return SWA_E_SHAPE;
+  if (s->kind == SWA_ROTARY_BASE && s->rot <= 2) return SWA_E_SHAPE;
+  if (s->kind == SWA_ROTARY_PARTS &&
+      !(s->orig_len > 0.0 && std::isfinite(s->orig_len) && s->high > s->low && std::isfinite(s->high) &&
+        std::isfinite(s->low)))
+    return SWA_E_SHAPE;
+  for (int e = 0; e < s->rot / 2; ++e) {   // nothing is written unless every frequency is finite
+    double f;
+    if (!rotary_freqs(s, e, &f)) return SWA_E_SHAPE;
+  }
+  for (int e = 0; e < s->rot / 2; ++e) {
+    double f;
+    rotary_freqs(s, e, &f);
+    if (freqs) freqs[e] = f;
+    if (turns) {
+      const double t = f / 6.283185307179586476925;
+      // the fraction is below 1 and has at most 53 significant bits: exact in 64
+      turns[e] = (uint64_t)std::ldexp(t - std::floor(t), 64);
+    }
+  }
+  return SWA_OK;
+}
+
+// Extent in elements of T rows of H heads, or -1 when rows and heads overlap.
+static long long extent(long long T, long long H, long long hd, long long row, long long head) {
+  const long long lim = 1LL << 40;
+  if (row < 1 || head < hd || row < hd || row > lim || head > lim) return -1;
+  const long long heads = (H - 1) * head + hd, rows = (T - 1) * row + hd;   // < 2^63: H, T < 2^21, 2^31
+  if (!(row >= heads || head >= rows)) return -1;
+  return (T - 1) * row + heads;
+}
+
+int swa_rotary(const swa_rotary_args* a, cudaStream_t stream) {
+  if (!a) return SWA_E_NULL;
+  if (a->T < 0 || a->H < 1 || a->hd < 8 || a->hd > 1024 || a->hd % 8 || a->rot < 2 || (a->rot & 1) || a->rot > a->hd)
+    return SWA_E_SHAPE;
+  if (a->dtype != SWA_F32 && a->dtype != SWA_BF16 && a->dtype != SWA_F16) return SWA_E_SHAPE;
+  if (!std::isfinite(a->mag)) return SWA_E_SHAPE;
+  if (a->H >= (1 << 21) || (long long)a->T * a->H >= (1LL << 40) / a->hd) return SWA_E_SHAPE;
+  if (a->T == 0) return SWA_OK;
+  if (!a->x || !a->out || !a->pos || !a->turns) return SWA_E_NULL;
+  const long long nx = extent(a->T, a->H, a->hd, a->x_row, a->x_head);
+  const long long no = extent(a->T, a->H, a->hd, a->out_row, a->out_head);
+  if (nx < 0 || no < 0) return SWA_E_SHAPE;
+  const int w = type_bytes(a->dtype);
+  if (!aligned16p(a->x) || !aligned16p(a->out) || ((a->x_row | a->x_head | a->out_row | a->out_head) * w & 15) ||
+      (reinterpret_cast<uintptr_t>(a->pos) & 3u) || (reinterpret_cast<uintptr_t>(a->turns) & 7u))
+    return SWA_E_ALIGN;
+  const bool same = a->x == a->out && a->x_row == a->out_row && a->x_head == a->out_head;
+  if (!same && bytes_overlap(a->x, (size_t)nx * w, a->out, (size_t)no * w)) return SWA_E_SHAPE;
+  RotaryParams p{};
+  p.T = a->T; p.H = a->H; p.hd = a->hd; p.rot = a->rot; p.inverse = a->inverse != 0; p.mag = a->mag;
+  p.x = a->x; p.x_row = a->x_row; p.x_head = a->x_head;
+  p.out = a->out; p.out_row = a->out_row; p.out_head = a->out_head;
+  p.pos = a->pos; p.turns = a->turns;
+  const bool inter = a->interleaved != 0;
+  bool wide;
+  if (!rotary_units(p, inter, &wide)) return SWA_E_SHAPE;
+  switch (a->dtype) {
+    case SWA_F32: return launch_rotary<float, float, false>(p, inter, wide, stream);
+    case SWA_BF16: return launch_rotary<__nv_bfloat16, __nv_bfloat16, false>(p, inter, wide, stream);
+    default: return launch_rotary<__half, __half, false>(p, inter, wide, stream);
+  }
+}
+
+int swa_paged_append(const swa_paged_append_args* a, cudaStream_t stream) {
+  if (!a) return SWA_E_NULL;
+  const swa_paged_cache& c = a->cache;
+  const int rc = paged_cache_status(&c, true);
+  if (rc != SWA_OK) return rc;
+  const int nh = a->q || a->q_out ? a->nh : 0;
+  if (a->T < 0 || a->nh < 0 || a->nh >= (1 << 20) || a->rot < 0 || (a->rot & 1) || a->rot > c.hd) return SWA_E_SHAPE;
+  if (a->src != SWA_F32 && a->src != c.dtype) return SWA_E_SHAPE;
+  if (!std::isfinite(a->mag)) return SWA_E_SHAPE;
+  const long long H = (long long)nh + 2LL * c.nk;
+  if (H >= (1 << 21) || (long long)a->T * H >= (1LL << 40) / c.hd) return SWA_E_SHAPE;
+  if (a->T == 0) return SWA_OK;
+  if (!a->k || !a->v || (a->q != nullptr) != (a->q_out != nullptr)) return SWA_E_NULL;
+  if (a->rot > 0 && (!a->pos || !a->turns)) return SWA_E_NULL;
+  if (a->slot_pos && !a->pos) return SWA_E_NULL;
+  if (a->q && a->nh < 1) return SWA_E_SHAPE;
+  const int w = type_bytes(a->src);
+  const long long kd = (long long)c.nk * c.hd, qd = (long long)nh * c.hd, lim = 1LL << 40;
+  if (a->k_row < kd || a->v_row < kd || a->k_row > lim || a->v_row > lim ||
+      (a->q && (a->q_row < qd || a->q_row > lim)))
+    return SWA_E_SHAPE;
+  if (!aligned16p(a->k) || !aligned16p(a->v) || !aligned16p(a->q) || !aligned16p(a->q_out) ||
+      ((a->k_row | a->v_row | (a->q ? a->q_row : 0)) * w & 15) || (reinterpret_cast<uintptr_t>(a->pos) & 3u) ||
+      (reinterpret_cast<uintptr_t>(a->turns) & 7u) || (reinterpret_cast<uintptr_t>(a->slot_pos) & 3u) ||
+      (reinterpret_cast<uintptr_t>(a->weight) & 3u))
+    return SWA_E_ALIGN;
+  if (a->q) {
+    const bool same = a->q == a->q_out && a->src == c.dtype && a->q_row == qd;
+    if (!same && bytes_overlap(a->q, (size_t)((a->T - 1) * a->q_row + qd) * w, a->q_out, (size_t)a->T * qd * 2))
+      return SWA_E_SHAPE;
+  }
+  RotaryParams p{};
+  p.T = a->T; p.H = (int)H; p.hd = c.hd; p.rot = a->rot; p.mag = a->mag;
+  p.x = a->q; p.x_row = a->q_row;
+  p.out = a->q_out; p.out_row = qd;
+  p.pos = a->pos; p.turns = a->turns;
+  p.nh = nh; p.nk = c.nk; p.hd_page = c.page * c.hd;
+  p.k = a->k; p.v = a->v; p.k_row = a->k_row; p.v_row = a->v_row;
+  p.cache_k = c.k; p.cache_v = c.v;
+  p.map = paged_map(&c);
+  p.slot_pos = a->slot_pos; p.weight = a->weight; p.err = a->err;
+  const bool inter = a->interleaved != 0;
+  bool wide;
+  if (!rotary_units(p, inter, &wide)) return SWA_E_SHAPE;
+  if (a->src == SWA_F32)
+    return c.dtype == SWA_BF16 ? launch_rotary<float, __nv_bfloat16, true>(p, inter, wide, stream)
+                               : launch_rotary<float, __half, true>(p, inter, wide, stream);
+  return c.dtype == SWA_BF16 ? launch_rotary<__nv_bfloat16, __nv_bfloat16, true>(p, inter, wide, stream)
+                             : launch_rotary<__half, __half, true>(p, inter, wide, stream);
+}
+
+}  // extern "C"
