@@ -512,7 +512,7 @@ int swa_flash(const swa_flash_args* args, cudaStream_t stream);
  *              output is written for them. Not read by swa_paged_evict.
  *   lens       [B] i32: keys each sequence holds, the chunk's own rows among
  *              them. Row i of a chunk of t_b rows has slot lens[b] - t_b + i.
- *   B          1 .. 65535; nk 1 .. 65535.
+ *   B          1 .. 65535; nk 1 .. 65535; B * nk <= 2^24.
  * On the device, a length outside 0 .. cap is clamped (SWA_DERR_META), a
  * sequence with rows out of range is skipped (SWA_DERR_SEGMENT), and pages out
  * of range are reported (SWA_DERR_PAGE); every access stays in bounds.

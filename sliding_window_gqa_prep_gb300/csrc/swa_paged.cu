@@ -6,11 +6,11 @@
 // operations for the 4 * hd bytes of a key: 64 a byte, far below the 280 a byte where
 // the matrix peak meets the memory's. The kernel is bound by reading K and V once.
 // So: every CTA gets the same number of 64-key tiles of the whole call (work of all
-// sequences, KV heads and row blocks laid end to end and cut evenly, wherever the cuts
+// sequences and KV heads laid end to end and cut evenly, wherever the cuts
 // fall), streams them through a ring of cp.async stages, and computes with warp-level
 // mma.sync.m16n8k16: S = Q K^T with Q in registers, the online softmax on S's
-// registers, and these registers again as the A operand of P V. A (sequence, KV head,
-// row block) that lies whole in one CTA is finished there; one that is cut leaves a
+// registers, and these registers again as the A operand of P V. A (sequence, KV head)
+// that lies whole in one CTA is finished there; one that is cut leaves a
 // record (m, l, sum p v) per CTA, joined by paged_merge_kernel.
 #include <cmath>
 
@@ -29,7 +29,7 @@ bool bytes_overlap(const void* a, size_t an, const void* b, size_t bn) {
 
 int paged_cache_status(const swa_paged_cache* c, bool rows) {
   if (!c->k || !c->v || !c->table || !c->lens || (rows && !c->row_start)) return SWA_E_NULL;
-  if (c->B < 1 || c->B > 65535 || c->nk < 1 || c->nk > 65535) return SWA_E_SHAPE;
+  if (c->B < 1 || c->B > 65535 || c->nk < 1 || c->nk > 65535 || (long long)c->B * c->nk > (1 << 24)) return SWA_E_SHAPE;
   if (c->hd != 64 && c->hd != 128 && c->hd != 256) return SWA_E_SHAPE;
   if (c->page < 16 || c->page > 256 || (c->page & (c->page - 1))) return SWA_E_SHAPE;
   if (c->num_pages < 1 || (long long)c->num_pages * c->nk >= (1LL << 31) / c->page) return SWA_E_SHAPE;
@@ -65,11 +65,11 @@ struct SplitCfg {
   static constexpr int SMEM = ST * 2 * TILE;
 };
 
-// Sequences this kernel works on have query vectors in blocks of `rows_tok` rows.
-__device__ __forceinline__ long long split_units(const PagedSeq& s, const PagedAttendParams& p, int& n_rb, int& n_tiles) {
-  n_rb = (s.t + p.rows_tok - 1) / p.rows_tok;
-  n_tiles = s.len > 0 ? (s.len + kKeys - 1) / kKeys : 1;   // a row without keys is still written
-  return (long long)p.map.nk * n_rb * n_tiles;
+// Tiles of one (sequence, KV head): none where the sequence has no rows or more query
+// vectors than this kernel takes.
+__device__ __forceinline__ int split_tiles(const PagedSeq& s, const PagedAttendParams& p) {
+  if (s.t == 0 || (long long)s.t * p.hpg > p.most) return 0;
+  return s.len > 0 ? (s.len + kKeys - 1) / kKeys : 1;      // a row without keys is still written
 }
 
 // ROWS: query vectors of a CTA's block (16, 32 or 64): ROWS / 16 groups of 16 rows,
@@ -96,9 +96,7 @@ __global__ void __launch_bounds__(kThreads) paged_split_kernel(const PagedAttend
     for (int e = 0; e < E; ++e) {
       const int b = tid * E + e;
       if (b < p.map.B) {
-        const PagedSeq s = paged_seq(p.map, b, p.T, p.max_rows, bits);
-        int a1, a2;
-        mine += split_units(s, p, a1, a2);
+        mine += (long long)p.map.nk * split_tiles(paged_seq(p.map, b, p.T, p.max_rows, bits), p);
       }
     }
     if (bits && blockIdx.x == 0) set_err(p.err, bits);
@@ -124,8 +122,7 @@ __global__ void __launch_bounds__(kThreads) paged_split_kernel(const PagedAttend
       for (int e = 0; e < E; ++e) {
         const int b = tid * E + e;
         uint32_t ignore = 0;
-        int a1, a2;
-        const long long n = split_units(paged_seq(p.map, b, p.T, p.max_rows, ignore), p, a1, a2);
+        const long long n = (long long)p.map.nk * split_tiles(paged_seq(p.map, b, p.T, p.max_rows, ignore), p);
         if (off < n) {
           s_b = b;
           s_off = off;
@@ -149,14 +146,8 @@ __global__ void __launch_bounds__(kThreads) paged_split_kernel(const PagedAttend
   int b = s_b;
   uint32_t ignore = 0;
   PagedSeq s = paged_seq(p.map, b, p.T, p.max_rows, ignore);
-  int n_rb, n_tiles;
-  split_units(s, p, n_rb, n_tiles);
-  int tile0 = (int)(s_off % n_tiles), rb, g;
-  {
-    const int item = (int)(s_off / n_tiles);
-    g = item / n_rb;
-    rb = item % n_rb;
-  }
+  int n_tiles = split_tiles(s, p);
+  int tile0 = (int)(s_off % n_tiles), g = (int)(s_off / n_tiles);
   if (tid == 0) p.ws_desc[blockIdx.x] = make_int4(-1, 0, 0, 0);
 
   const int rg = warp / KG, kg = warp % KG;
@@ -166,8 +157,7 @@ __global__ void __launch_bounds__(kThreads) paged_split_kernel(const PagedAttend
 
   while (left > 0) {
     const int tile1 = (int)min((long long)n_tiles, tile0 + left);
-    const int tok0 = rb * p.rows_tok;                       // first row of the block
-    const int ntok = min(p.rows_tok, s.t - tok0), nvec = ntok * hpg;
+    const int nvec = s.t * hpg;
     const int* table = p.map.table + (size_t)b * p.map.max_pages;
     const T* const kp = static_cast<const T*>(p.ck);
     const T* const vp = static_cast<const T*>(p.cv);
@@ -228,15 +218,15 @@ __global__ void __launch_bounds__(kThreads) paged_split_kernel(const PagedAttend
       const int r = rg * 16 + hrow * 8 + (lane >> 2);
       const bool ok = r < nvec;
       const int i = ok ? r / hpg : 0, h = ok ? r % hpg : 0;
-      lim[hrow] = ok ? min(s.len, s.len - s.t + tok0 + i + 1) : 0;
-      const T* src = qp + (size_t)(s.r0 + tok0 + i) * p.q_row + (size_t)(g * hpg + h) * D + (lane & 3) * 2;
+      lim[hrow] = ok ? min(s.len, s.len - s.t + i + 1) : 0;
+      const T* src = qp + (size_t)(s.r0 + i) * p.q_row + (size_t)(g * hpg + h) * D + (lane & 3) * 2;
 #pragma unroll
       for (int k = 0; k < D / 16; ++k) {
         qf[k][hrow] = ok ? *reinterpret_cast<const uint32_t*>(src + k * 16) : 0u;
         qf[k][hrow + 2] = ok ? *reinterpret_cast<const uint32_t*>(src + k * 16 + 8) : 0u;
       }
     }
-    const int lim_min = s.len - s.t + tok0 + 1;            // keys below it are seen by every row
+    const int lim_min = s.len - s.t + 1;                   // keys below it are seen by every row
 
     float o[D / 8][4];
 #pragma unroll
@@ -357,7 +347,7 @@ __global__ void __launch_bounds__(kThreads) paged_split_kernel(const PagedAttend
         for (int j = 0; j < 8; ++j) acc[j] += a * y[j];
       }
       if (whole) {
-        paged_store_row<T>(p, s.r0 + tok0 + row / hpg, g * hpg + row % hpg, D, c * 8, mt, lt, acc, c == 0);
+        paged_store_row<T>(p, s.r0 + row / hpg, g * hpg + row % hpg, D, c * 8, mt, lt, PScale<T>::kLog2, acc, c == 0);
       } else {
         store8(p.ws_acc + (rec + row) * D + c * 8, acc);
         if (c == 0) p.ws_ml[rec + row] = make_float2(mt, lt);
@@ -366,23 +356,19 @@ __global__ void __launch_bounds__(kThreads) paged_split_kernel(const PagedAttend
     if (!whole && tile0 == 0 && tid == 0) {
       // units of this item from here on / per CTA: the CTA that ends it
       const long long end = u0 + (min(per, total - u0) - left) + n_tiles - 1;
-      p.ws_desc[blockIdx.x] = make_int4(b, g, rb, (int)(end / per));
+      p.ws_desc[blockIdx.x] = make_int4(b, g, (int)(end / per), 0);
     }
 
     // --- the next item
     left -= tile1 - tile0;
     tile0 = 0;
     if (left <= 0) break;
-    if (++rb == n_rb) {
-      rb = 0;
-      if (++g == p.map.nk) {
-        g = 0;
-        do {
-          ++b;
-          s = paged_seq(p.map, b, p.T, p.max_rows, ignore);
-        } while (s.t == 0);
-        split_units(s, p, n_rb, n_tiles);
-      }
+    if (++g == p.map.nk) {
+      g = 0;
+      do {
+        s = paged_seq(p.map, ++b, p.T, p.max_rows, ignore);
+        n_tiles = split_tiles(s, p);
+      } while (n_tiles == 0);
     }
   }
 }
@@ -404,10 +390,9 @@ __global__ void __launch_bounds__(kMergeThreads) paged_merge_kernel(const PagedA
   if (dsc.x < 0) return;
   uint32_t ignore = 0;
   const PagedSeq s = paged_seq(p.map, dsc.x, p.T, p.max_rows, ignore);
-  const int tok0 = dsc.z * p.rows_tok, row = blockIdx.y;
-  const int nvec = min(p.rows_tok, s.t - tok0) * p.hpg;
-  if (row >= nvec) return;
-  const int c0 = blockIdx.x, n = dsc.w - c0 + 1;
+  const int row = blockIdx.y;
+  if (row >= s.t * p.hpg) return;
+  const int c0 = blockIdx.x, n = dsc.z - c0 + 1;
   const int tid = threadIdx.x, grp = tid / L, c = tid % L;
   auto rec = [&](int i) { return ((size_t)(c0 + i) * 2 + (i == 0 ? 1 : 0)) * rows + row; };
   float mt = -INFINITY;
@@ -441,15 +426,19 @@ __global__ void __launch_bounds__(kMergeThreads) paged_merge_kernel(const PagedA
 #pragma unroll
       for (int j = 0; j < 8; ++j) acc[j] += y[j];
     }
-    paged_store_row<T>(p, s.r0 + tok0 + row / p.hpg, dsc.y * p.hpg + row % p.hpg, D, c * 8, mt, lt, acc, c == 0);
+    paged_store_row<T>(p, s.r0 + row / p.hpg, dsc.y * p.hpg + row % p.hpg, D, c * 8, mt, lt, PScale<T>::kLog2, acc, c == 0);
   }
 }
 
 // ---------------------------------------------------------------------------
 // Launches
 // ---------------------------------------------------------------------------
+// Query vectors of a (sequence, KV head) up to which the split kernel takes it; more go
+// to the tensor-core kernel (swa_paged_chunk.cu).
+constexpr int kSplitVecs = 64;
+
 struct SplitPlan {
-  int rows, rows_tok, grid;       // query vectors of a block, chunk rows of it, CTAs
+  int rows, grid;                 // query vectors of a block (16, 32 or 64; 0: no sequence for this kernel), CTAs
   size_t off_ml, off_desc, bytes;
 };
 
@@ -472,16 +461,15 @@ static int split_occupancy() {
 }
 
 template <typename T, int D, int ROWS>
-static int launch_split(const PagedAttendParams& p, const SplitPlan& sp, cudaStream_t s, cudaEvent_t e0, cudaEvent_t e1) {
-  cudaError_t e = cudaFuncSetAttribute(paged_split_kernel<T, D, ROWS>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                       SplitCfg<D>::SMEM);
+static int launch_split(const PagedAttendParams& p, const SplitPlan& sp, cudaStream_t s) {
+  const cudaError_t e = cudaFuncSetAttribute(paged_split_kernel<T, D, ROWS>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                             SplitCfg<D>::SMEM);
   if (e != cudaSuccess) return cuda_status(e);
-  if (e0 && (e = cudaEventRecord(e0, s)) != cudaSuccess) return cuda_status(e);
-  int rc = finish_launch(launch_pdl(paged_split_kernel<T, D, ROWS>, dim3(sp.grid), dim3(kThreads), SplitCfg<D>::SMEM, s, p));
+  const int rc = finish_launch(launch_pdl(paged_split_kernel<T, D, ROWS>, dim3(sp.grid), dim3(kThreads), SplitCfg<D>::SMEM, s, p));
   if (rc != SWA_OK) return rc;
-  if (e1 && (e = cudaEventRecord(e1, s)) != cudaSuccess) return cuda_status(e);
-  const int most = p.max_rows < p.rows_tok ? p.max_rows : p.rows_tok;
-  return finish_launch(launch_pdl(paged_merge_kernel<T, D>, dim3(sp.grid, most * p.hpg), dim3(kMergeThreads), 0, s, p, ROWS));
+  const long long vecs = (long long)p.max_rows * p.hpg;
+  return finish_launch(launch_pdl(paged_merge_kernel<T, D>, dim3(sp.grid, (unsigned)(vecs < p.most ? vecs : p.most)),
+                                  dim3(kMergeThreads), 0, s, p, ROWS));
 }
 
 template <typename F>
@@ -494,27 +482,48 @@ static int by_type(int dtype, int hd, int rows, F f) {
 #undef SWA_ROWS
 }
 
-static void split_plan(const swa_paged_attend_args* a, SplitPlan* sp) {
+// Which kernels a call runs. All sequences have at most max_rows rows: when these fit
+// the split kernel it runs alone. Otherwise the tensor-core kernel runs, and before it
+// the split kernel if some sequence may be shorter (B * max_rows > T); if not, the
+// tensor-core kernel takes every sequence.
+struct PagedPlan {
+  SplitPlan split;
+  ChunkPlan chunk;
+  bool has_chunk;
+  size_t off_chunk, bytes;
+};
+
+static void attend_plan(const swa_paged_attend_args* a, PagedPlan* pl) {
   const int hpg = a->nh / a->cache.nk;
   const long long vecs = (long long)a->max_rows * hpg;
-  sp->rows = vecs <= 16 ? 16 : vecs <= 32 ? 32 : 64;
-  sp->rows_tok = sp->rows / hpg;
-  const int occ = by_type(a->cache.dtype, a->cache.hd, sp->rows, [](auto* t, auto d, auto r) {
-    return split_occupancy<std::remove_pointer_t<decltype(t)>, decltype(d)::value, decltype(r)::value>();
-  });
-  const int sms = num_sms() > 0 ? num_sms() : 148;
-  sp->grid = sms * occ;
-  const size_t recs = (size_t)sp->grid * 2 * sp->rows;
-  sp->off_ml = up256s(recs * a->cache.hd * sizeof(float));
-  sp->off_desc = sp->off_ml + up256s(recs * sizeof(float2));
-  sp->bytes = sp->off_desc + up256s((size_t)sp->grid * sizeof(int4));
+  SplitPlan& sp = pl->split;
+  sp = SplitPlan{};
+  pl->has_chunk = vecs > kSplitVecs;
+  if (!pl->has_chunk || (long long)a->cache.B * a->max_rows > a->T) {
+    sp.rows = vecs <= 16 ? 16 : vecs <= 32 ? 32 : 64;
+    const int occ = by_type(a->cache.dtype, a->cache.hd, sp.rows, [](auto* t, auto d, auto r) {
+      return split_occupancy<std::remove_pointer_t<decltype(t)>, decltype(d)::value, decltype(r)::value>();
+    });
+    sp.grid = (num_sms() > 0 ? num_sms() : 148) * occ;
+    const size_t recs = (size_t)sp.grid * 2 * sp.rows;
+    sp.off_ml = up256s(recs * a->cache.hd * sizeof(float));
+    sp.off_desc = sp.off_ml + up256s(recs * sizeof(float2));
+    sp.bytes = sp.off_desc + up256s((size_t)sp.grid * sizeof(int4));
+  }
+  pl->off_chunk = sp.bytes;
+  pl->bytes = sp.bytes;
+  if (pl->has_chunk) {
+    pl->chunk = chunk_plan(a);
+    pl->bytes += pl->chunk.bytes;
+  }
 }
 
 // Sizes alone (the workspace query); pointers are checked by the call.
 static bool attend_sizes_ok(const swa_paged_attend_args* a) {
   const swa_paged_cache& c = a->cache;
-  if (c.B < 1 || c.B > 65535 || c.nk < 1 || c.nk > 65535 || (c.hd != 64 && c.hd != 128 && c.hd != 256)) return false;
-  if (c.dtype != SWA_BF16 && c.dtype != SWA_F16) return false;
+  if (c.B < 1 || c.B > 65535 || c.nk < 1 || c.nk > 65535 || (long long)c.B * c.nk > (1 << 24)) return false;
+  if ((c.hd != 64 && c.hd != 128 && c.hd != 256) || (c.dtype != SWA_BF16 && c.dtype != SWA_F16)) return false;
+  if (c.page < 16 || c.page > 256 || c.max_pages < 1 || c.max_pages > (1 << 30) / c.page) return false;
   if (a->T < 0 || a->max_rows < 1 || a->nh < 1 || a->nh % c.nk || a->nh / c.nk > 32) return false;
   return (long long)a->T * a->nh < (1LL << 31);
 }
@@ -527,15 +536,15 @@ extern "C" {
 
 size_t swa_paged_attend_workspace_size(const swa_paged_attend_args* a) {
   if (!a || !attend_sizes_ok(a)) return 0;
-  SplitPlan sp;
-  split_plan(a, &sp);
-  return sp.bytes;
+  PagedPlan pl;
+  attend_plan(a, &pl);
+  return pl.bytes ? pl.bytes : 256;
 }
 
 int swa_paged_attend(const swa_paged_attend_args* a, cudaStream_t stream) {
   if (!a) return SWA_E_NULL;
   const swa_paged_cache& c = a->cache;
-  const int rc = paged_cache_status(&c, true);
+  int rc = paged_cache_status(&c, true);
   if (rc != SWA_OK) return rc;
   if (!attend_sizes_ok(a) || !(a->scale >= 0.f) || std::isinf(a->scale)) return SWA_E_SHAPE;
   if (a->T == 0) return SWA_OK;
@@ -543,26 +552,36 @@ int swa_paged_attend(const swa_paged_attend_args* a, cudaStream_t stream) {
   if (a->q_row < (long long)a->nh * c.hd || a->q_row > (1LL << 40)) return SWA_E_SHAPE;
   if (!aligned16p(a->q) || !aligned16p(a->out) || (a->q_row & 7) || (reinterpret_cast<uintptr_t>(a->lse) & 3u))
     return SWA_E_ALIGN;
-  SplitPlan sp;
-  split_plan(a, &sp);
-  if (!a->workspace || a->workspace_bytes < sp.bytes) return SWA_E_WORKSPACE;
+  PagedPlan pl;
+  attend_plan(a, &pl);
+  if (!a->workspace || a->workspace_bytes < (pl.bytes ? pl.bytes : 256)) return SWA_E_WORKSPACE;
   if (reinterpret_cast<uintptr_t>(a->workspace) & 255u) return SWA_E_ALIGN;
   PagedAttendParams p{};
   p.map = paged_map(&c);
   p.T = a->T; p.nh = a->nh; p.hpg = a->nh / c.nk; p.max_rows = a->max_rows;
-  p.rows_tok = sp.rows_tok;
+  p.most = kSplitVecs;
   p.qmul = a->scale * 1.4426950408889634f;
   p.q = a->q; p.q_row = a->q_row; p.ck = c.k; p.cv = c.v;
   p.out = a->out; p.out_f32 = a->out_f32 != 0; p.lse = a->lse;
-  char* ws = static_cast<char*>(a->workspace);
-  p.ws_acc = reinterpret_cast<float*>(ws);
-  p.ws_ml = reinterpret_cast<float2*>(ws + sp.off_ml);
-  p.ws_desc = reinterpret_cast<int4*>(ws + sp.off_desc);
   p.err = a->err;
-  return by_type(c.dtype, c.hd, sp.rows, [&](auto* t, auto d, auto r) {
-    return launch_split<std::remove_pointer_t<decltype(t)>, decltype(d)::value, decltype(r)::value>(
-        p, sp, stream, a->ev_start, a->ev_stop);
-  });
+  char* ws = static_cast<char*>(a->workspace);
+  cudaError_t e;
+  if (a->ev_start && (e = cudaEventRecord(a->ev_start, stream)) != cudaSuccess) return cuda_status(e);
+  if (pl.split.rows) {
+    p.ws_acc = reinterpret_cast<float*>(ws);
+    p.ws_ml = reinterpret_cast<float2*>(ws + pl.split.off_ml);
+    p.ws_desc = reinterpret_cast<int4*>(ws + pl.split.off_desc);
+    rc = by_type(c.dtype, c.hd, pl.split.rows, [&](auto* t, auto d, auto r) {
+      return launch_split<std::remove_pointer_t<decltype(t)>, decltype(d)::value, decltype(r)::value>(p, pl.split, stream);
+    });
+    if (rc != SWA_OK) return rc;
+  }
+  if (pl.has_chunk) {
+    rc = launch_paged_chunk(a, p, pl.chunk, pl.split.rows ? kSplitVecs : 0, ws + pl.off_chunk, stream);
+    if (rc != SWA_OK) return rc;
+  }
+  if (a->ev_stop && (e = cudaEventRecord(a->ev_stop, stream)) != cudaSuccess) return cuda_status(e);
+  return SWA_OK;
 }
 
 }  // extern "C"

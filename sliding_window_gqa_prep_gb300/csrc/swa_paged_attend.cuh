@@ -13,7 +13,7 @@ using Int = std::integral_constant<int, N>;
 struct PagedAttendParams {
   PagedMap map;
   int T, nh, hpg, max_rows;
-  int rows_tok;                // chunk rows of a block of query vectors
+  int most;                    // split kernel: sequences with more query vectors are not its
   float qmul;                  // scale * log2(e): scores in log2 units
   const void* q;
   long long q_row;
@@ -22,9 +22,9 @@ struct PagedAttendParams {
   void* out;
   int out_f32;
   float* lse;
-  float* ws_acc;               // [records][rows][hd]
+  float* ws_acc;               // [records][rows][hd] (split kernel)
   float2* ws_ml;               // [records][rows] (m in log2 units, l)
-  int4* ws_desc;               // per CTA: the item it left unfinished (b, g, row block, last CTA), b < 0: none
+  int4* ws_desc;               // per CTA: the item it left unfinished (b, g, last CTA, 0), b < 0: none
   uint32_t* err;
 };
 
@@ -41,11 +41,22 @@ struct PScale<__half> {
   static constexpr float kLog2 = 15.f;
 };
 
+// The tensor-core kernel for chunks of many query vectors (swa_paged_chunk.cu)
+struct ChunkPlan {
+  int tile_tok, splits;        // chunk rows of a query tile, shares of an item's keys
+  long long items;             // upper bound of its items (grid)
+  size_t off_ml, off_desc, bytes;
+};
+ChunkPlan chunk_plan(const swa_paged_attend_args* a);
+int launch_paged_chunk(const swa_paged_attend_args* a, const PagedAttendParams& p, const ChunkPlan& plan, int small,
+                       char* ws, cudaStream_t s);
+
 #ifdef __CUDACC__
-// Features [f, f + 8) of a finished row: out = acc / l, and its lse.
+// Features [f, f + 8) of a finished row: out = acc / l, and its lse (the weights in l
+// carry 2^log2_scale).
 template <typename T>
 __device__ __forceinline__ void paged_store_row(const PagedAttendParams& p, int row, int head, int hd, int f, float m,
-                                                float l, float (&acc)[8], bool first) {
+                                                float l, float log2_scale, float (&acc)[8], bool first) {
   const float inv = l > 0.f ? 1.f / l : (l == 0.f ? 0.f : l);   // no key: zeros; NaN stays
 #pragma unroll
   for (int j = 0; j < 8; ++j) acc[j] = l == 0.f ? 0.f : acc[j] * inv;
@@ -55,7 +66,7 @@ __device__ __forceinline__ void paged_store_row(const PagedAttendParams& p, int 
   else
     store8(static_cast<T*>(p.out) + at, acc);
   if (first && p.lse)
-    p.lse[(size_t)row * p.nh + head] = l == 0.f ? -INFINITY : (m - PScale<T>::kLog2 + log2f(l)) * 0.6931471805599453f;
+    p.lse[(size_t)row * p.nh + head] = l == 0.f ? -INFINITY : (m - log2_scale + log2f(l)) * 0.6931471805599453f;
 }
 #endif
 

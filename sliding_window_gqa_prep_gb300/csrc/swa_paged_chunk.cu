@@ -1,0 +1,600 @@
+// Attention of chunks with many query vectors per KV head over the paged cache, on the
+// tensor cores (tcgen05, accumulators in TMEM, pages copied by TMA).
+//
+// Work item: NT tiles of 128 query vectors (rows x heads of one KV head) of one
+// sequence. S = Q K^T and O += P V per tile of KT keys are both matrix products with
+// 128 rows; between them stand 128 x KT exponentials, which at hd 128 take the 16 / clk
+// of an SM's special-function units as long as the two products take its tensor core
+// (4 * 128 * 128 * 128 / 8192 = 1024 clk each). So both must run all the time:
+//   - hd 64 and 128: two tiles (NT = 2), each with its own softmax warpgroup and its
+//     own issuing warp, share every K and V tile; while one tile is in its softmax the
+//     tensor core works for the other. TMEM: S 2 x 128 and O 2 x hd columns.
+//   - hd 256: O of two tiles would fill TMEM, so there is one tile, and S has two
+//     buffers: the product of the next keys runs during this softmax (KT = 64, so that
+//     Q and five slots of K / V fit in shared memory).
+// P overwrites its S columns as 16-bit pairs and is read from TMEM as the A operand.
+// One thread owns one row of S: maxima and sums need no exchange. The running maximum
+// is raised only when a row's scores pass it by 2^kLazy (weights then stay below
+// 2^kLazy times the scale), so that O is seldom rescaled.
+// V of keys behind the sequence's last one is zeroed in shared memory (0 * NaN).
+// Few items are split over the keys: grid.y shares of an item's tiles leave records
+// that chunk_merge_kernel joins.
+#include <cmath>
+#include <cuda.h>
+
+#include "swa_paged_attend.cuh"
+#include "swa_tcgen05.cuh"
+
+namespace swa {
+
+template <int D>
+struct ChunkCfg {
+  static constexpr int NT = D == 256 ? 1 : 2;          // query tiles of an item
+  static constexpr int SB = D == 256 ? 2 : 1;          // S buffers of a tile
+  static constexpr int KT = D == 256 ? 64 : 128;       // keys of a tile
+  static constexpr int NS = D == 64 ? 8 : 5;           // K / V slots
+  static constexpr int SLOT = KT * D * 2;
+  static constexpr int QB = 128 * D * 2;               // bytes of a query tile
+  static constexpr int THREADS = NT * 128 + 32 + NT * 32;   // softmax, loader, issuers
+  static constexpr int SMEM = NT * QB + NS * SLOT + 1024;   // + alignment
+  static constexpr int C_O = NT * SB * KT;             // first O column
+};
+template <typename T>
+struct LazyMax {                                       // log2 of what a weight may exceed its scale by
+  static constexpr float kLazy = 8.f, kLog2 = 0.f;
+};
+template <>
+struct LazyMax<__half> {                               // 2^(4 + 11) = 2^15 < 65504; see PScale
+  static constexpr float kLazy = 4.f, kLog2 = 11.f;
+};
+
+struct ChunkParams {
+  PagedAttendParams a;
+  int small;                   // sequences with at most this many query vectors are not ours
+  int tile_tok;                // chunk rows of a query tile (128 / hpg)
+  int splits;
+  float* rec_acc;              // [item][split][NT * 128][D]
+  float2* rec_ml;              // [item][split][NT * 128]
+  int4* rec_desc;              // [item]: (b, g, first row of the item, 0), b < 0: no such item
+};
+
+// kind::f16 with D in f32, A and B both f16 or both bf16, A K-major, B K-major or not
+__host__ __device__ constexpr uint32_t chunk_idesc(bool bf16, bool b_mn_major, int n) {
+  return (1u << 4) | ((bf16 ? 1u : 0u) << 7) | ((bf16 ? 1u : 0u) << 10) | ((b_mn_major ? 1u : 0u) << 16) |
+         ((uint32_t)(n >> 3) << 17) | ((uint32_t)(128 >> 4) << 24);
+}
+// Shared-memory matrix descriptor, 128-byte swizzle (rows of 128 bytes, groups of 8
+// rows every 1024 bytes). K-major: sbo = 1024. MN-major: sbo = 1024 between groups of
+// 8 K rows, lbo between columns of 64 MN elements.
+__device__ __forceinline__ uint64_t sw128_desc(uint32_t addr, uint32_t lbo) {
+  return (uint64_t)((addr >> 4) & 0x3FFF) | ((uint64_t)((lbo >> 4) & 0x3FFF) << 16) |
+         ((uint64_t)(1024 >> 4) << 32) | (1ull << 46) | (2ull << 61);
+}
+__device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, bool acc) {
+  asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+               "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}"
+               :: "r"(d), "l"(a), "l"(b), "r"(idesc), "r"(acc ? 1 : 0) : "memory");
+}
+// Waits for this thread's TMEM loads; the registers are operands, so that nothing that
+// reads them moves ahead of the wait.
+#define SWA_RW32(r) "+r"(r[0]),"+r"(r[1]),"+r"(r[2]),"+r"(r[3]),"+r"(r[4]),"+r"(r[5]),"+r"(r[6]),"+r"(r[7]), \
+  "+r"(r[8]),"+r"(r[9]),"+r"(r[10]),"+r"(r[11]),"+r"(r[12]),"+r"(r[13]),"+r"(r[14]),"+r"(r[15]), \
+  "+r"(r[16]),"+r"(r[17]),"+r"(r[18]),"+r"(r[19]),"+r"(r[20]),"+r"(r[21]),"+r"(r[22]),"+r"(r[23]), \
+  "+r"(r[24]),"+r"(r[25]),"+r"(r[26]),"+r"(r[27]),"+r"(r[28]),"+r"(r[29]),"+r"(r[30]),"+r"(r[31])
+template <int N>
+__device__ __forceinline__ void wait_ld(uint32_t (&x)[N][32]) {
+  asm volatile("tcgen05.wait::ld.sync.aligned;" : SWA_RW32(x[0]) :: "memory");
+#pragma unroll
+  for (int i = 1; i < N; ++i) asm volatile("" : SWA_RW32(x[i]) :: "memory");
+}
+__device__ __forceinline__ void wait_ld(uint32_t (&x)[32]) {
+  asm volatile("tcgen05.wait::ld.sync.aligned;" : SWA_RW32(x) :: "memory");
+}
+__device__ __forceinline__ void tma_2d(uint32_t dst, const CUtensorMap* map, int x, int y, uint64_t* bar) {
+  asm volatile("cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%3, %4}], [%2];"
+               :: "r"(dst), "l"(map), "r"(smem_u32(bar)), "r"(x), "r"(y) : "memory");
+}
+
+// First K / V slot position of tile j's K and V in the order they are consumed.
+template <int SB>
+__device__ __forceinline__ int pos_k(int j) { return SB == 1 ? 2 * j : (j == 0 ? 0 : 2 * j - 1); }
+template <int SB>
+__device__ __forceinline__ int pos_v(int j, int n) { return SB == 1 ? 2 * j + 1 : (j < n - 1 ? 2 * j + 2 : 2 * n - 1); }
+
+__device__ __forceinline__ int chunk_items(const PagedSeq& s, const ChunkParams& p, int item_tok) {
+  return (long long)s.t * p.a.hpg > p.small ? (s.t + item_tok - 1) / item_tok * p.a.map.nk : 0;
+}
+
+template <typename T, int D>
+__global__ void __launch_bounds__(ChunkCfg<D>::THREADS, 1)
+    paged_chunk_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constant__ CUtensorMap map_v, const ChunkParams p) {
+  using C = ChunkCfg<D>;
+  constexpr int NT = C::NT, SB = C::SB, KT = C::KT, NS = C::NS;
+  constexpr bool BF = std::is_same<T, __nv_bfloat16>::value;
+  extern __shared__ unsigned char sm_raw[];
+  __shared__ __align__(8) uint64_t b_full[NS], b_empty[NS], b_q[NT], b_s[NT * SB], b_p[NT * SB], b_pv[NT], b_fin[NT], b_tail;
+  __shared__ uint32_t s_tmem;
+  __shared__ int s_abort, s_b, s_idx;
+  __shared__ int s_scan[32];
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  constexpr int NW = C::THREADS / 32, W_LOAD = NT * 4, W_MMA = NT * 4 + 1;
+  unsigned char* const sm = reinterpret_cast<unsigned char*>((reinterpret_cast<uintptr_t>(sm_raw) + 1023) & ~(uintptr_t)1023);
+  unsigned char* const sm_kv = sm + NT * C::QB;
+  const PagedAttendParams& a = p.a;
+  pdl_wait();
+  pdl_trigger();
+
+  // --- which item: a scan over the sequences' item counts
+  const int item_tok = NT * p.tile_tok;
+  {
+    uint32_t bits = 0;
+    const int E = (a.map.B + C::THREADS - 1) / C::THREADS;
+    int mine = 0;
+    for (int e = 0; e < E; ++e) {
+      const int b = tid * E + e;
+      if (b < a.map.B) mine += chunk_items(paged_seq(a.map, b, a.T, a.max_rows, bits), p, item_tok);
+    }
+    if (bits && blockIdx.x == 0 && blockIdx.y == 0) set_err(a.err, bits);
+    int incl = mine;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int v = __shfl_up_sync(0xffffffffu, incl, o);
+      if (lane >= o) incl += v;
+    }
+    if (lane == 31) s_scan[warp] = incl;
+    if (tid == 0) {
+      s_b = -1;
+      s_abort = 0;
+    }
+    __syncthreads();
+    int before = incl - mine;
+    for (int w = 0; w < warp; ++w) before += s_scan[w];
+    const int want = blockIdx.x;
+    if (want >= before && want < before + mine) {
+      int off = want - before;
+      for (int e = 0; e < E; ++e) {
+        uint32_t ignore = 0;
+        const int n = chunk_items(paged_seq(a.map, tid * E + e, a.T, a.max_rows, ignore), p, item_tok);
+        if (off < n) {
+          s_b = tid * E + e;
+          s_idx = off;
+          break;
+        }
+        off -= n;
+      }
+    }
+    __syncthreads();
+  }
+  if (s_b < 0) {
+    if (p.splits > 1 && blockIdx.y == 0 && tid == 0) p.rec_desc[blockIdx.x] = make_int4(-1, 0, 0, 0);
+    return;
+  }
+  uint32_t ignore = 0;
+  const int b = s_b, g = s_idx % a.map.nk;
+  const PagedSeq s = paged_seq(a.map, b, a.T, a.max_rows, ignore);
+  // the item with the most keys first
+  const int n_qt = (s.t + item_tok - 1) / item_tok;
+  const int tok0 = (n_qt - 1 - s_idx / a.map.nk) * item_tok;
+  if (p.splits > 1 && blockIdx.y == 0 && tid == 0) p.rec_desc[blockIdx.x] = make_int4(b, g, tok0, 0);
+
+  // key tiles of each query tile, and this CTA's share [j0, j1) of the item's
+  int n_tile[NT], n_all = 0;
+#pragma unroll
+  for (int t = 0; t < NT; ++t) {
+    const int first = tok0 + t * p.tile_tok, last = min(first + p.tile_tok, s.t) - 1;
+    const int lim = last >= first ? min(s.len, s.len - s.t + last + 1) : 0;
+    n_tile[t] = lim > 0 ? (lim + KT - 1) / KT : 0;
+    n_all = max(n_all, n_tile[t]);
+  }
+  const int j0 = (int)((long long)n_all * blockIdx.y / p.splits), j1 = (int)((long long)n_all * (blockIdx.y + 1) / p.splits);
+  const int n = j1 - j0;                                   // tiles of this CTA
+
+  if (warp == W_LOAD) {
+    if (lane == 0) {
+      for (int i = 0; i < NS; ++i) {
+        mbar_init(&b_full[i], 1);
+        mbar_init(&b_empty[i], NT);
+      }
+      for (int t = 0; t < NT; ++t) {
+        mbar_init(&b_q[t], 128);
+        mbar_init(&b_pv[t], 1);
+        mbar_init(&b_fin[t], 1);
+      }
+      for (int i = 0; i < NT * SB; ++i) {
+        mbar_init(&b_s[i], 1);
+        mbar_init(&b_p[i], 128);
+      }
+      mbar_init(&b_tail, 1);
+      mbar_fence_init();
+    }
+  } else if (warp == W_MMA) {
+    tc_alloc(&s_tmem, 512);
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = s_tmem;
+  auto give_up = [&]() {
+    s_abort = 1;
+    __threadfence_block();
+    set_err(a.err, SWA_DERR_TIMEOUT);
+  };
+  auto wait = [&](uint64_t* bar, int phase) -> bool {
+    return mbar_wait_bounded(bar, (uint32_t)(phase & 1), kWaitLimitNs) && !*(volatile int*)&s_abort;
+  };
+
+  if (warp == W_LOAD) {
+    // ------------------------------------------------------------ loader
+    // lane i copies box i of a slot: `rows` keys x 64 features
+    const int page = 1 << a.map.page_shift, rows = min(page, KT), per_half = KT / rows;
+    constexpr int HALVES = D / 64;
+    const int32_t* table = a.map.table + (size_t)b * a.map.max_pages;
+    const int oob = a.map.num_pages * a.map.nk << a.map.page_shift;       // rows of the pool: reads zeros
+    bool ok = true;
+    int issued = 0;
+    auto load = [&](int j, bool is_v, int pos) {
+      const int slot = pos % NS, use = pos / NS;
+      if (!__all_sync(0xffffffffu, use == 0 || wait(&b_empty[slot], use - 1))) return false;
+      const int key0 = (j0 + j) * KT;
+      const bool tail = is_v && key0 + KT > s.len;
+      uint64_t* bar = tail ? &b_tail : &b_full[slot];
+      if (lane == 0) mbar_arrive_expect_tx(bar, C::SLOT);
+      __syncwarp();
+      unsigned char* dst = sm_kv + slot * C::SLOT;
+      for (int i = lane; i < per_half * HALVES; i += 32) {
+        const int half = i / per_half, bx = i % per_half, key = key0 + bx * rows;
+        int y = oob;
+        if (key < s.len) {
+          const int id = table[key >> a.map.page_shift];
+          if (page_ok(a.map, id))
+            y = ((id * a.map.nk + g) << a.map.page_shift) + (key & (page - 1));
+          else
+            set_err(a.err, SWA_DERR_PAGE);
+        }
+        tma_2d(smem_u32(dst + half * (KT * 128) + bx * rows * 128), is_v ? &map_v : &map_k, half * 64, y, bar);
+      }
+      issued = pos + 1;
+      if (tail) {
+        // at most one tile of a sequence: its V rows from the last key on become zeros
+        if (!__all_sync(0xffffffffu, mbar_wait_bounded(&b_tail, 0, kWaitLimitNs))) return false;
+        const int first = s.len - key0;
+        for (int i = lane; i < (KT - first) * 8 * HALVES; i += 32) {
+          const int c = i & 7, r = first + (i >> 3) % (KT - first), half = (i >> 3) / (KT - first);
+          *reinterpret_cast<uint4*>(dst + half * (KT * 128) + r * 128 + c * 16) = make_uint4(0, 0, 0, 0);
+        }
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&b_full[slot]);
+      }
+      return true;
+    };
+    for (int x = 0; ok && x < n; ++x) {
+      if (SB == 1) {
+        ok = load(x, false, pos_k<SB>(x)) && load(x, true, pos_v<SB>(x, n));
+      } else {
+        if (x == 0) ok = load(0, false, 0);
+        if (ok && x + 1 < n) ok = load(x + 1, false, pos_k<SB>(x + 1));
+        if (ok) ok = load(x, true, pos_v<SB>(x, n));
+      }
+    }
+    if (!ok) {
+      give_up();
+      // copies in flight land before the CTA exits (bounded)
+      for (int q = max(0, issued - NS); q < issued; ++q) mbar_wait_bounded(&b_full[q % NS], (uint32_t)((q / NS) & 1), kWaitLimitNs);
+    }
+  } else if (warp >= W_MMA) {
+    // ------------------------------------------------------------ issuers, one per query tile
+    const int t = warp - W_MMA;
+    if (lane == 0 && n > 0) {
+      constexpr uint32_t ID_S = chunk_idesc(BF, false, KT), ID_O = chunk_idesc(BF, true, D);
+      const uint32_t q_addr = smem_u32(sm + t * C::QB), kv_addr = smem_u32(sm_kv);
+      const uint32_t c_o = tmem + C::C_O + t * D;
+      const int mine = max(0, min(n_tile[t] - j0, n));     // tiles that this query tile sees
+      bool ok = mine == 0 || wait(&b_q[t], 0);
+      auto s_mma = [&](int j) {                             // S of tile j
+        const int slot = pos_k<SB>(j) % NS;
+        if (!wait(&b_full[slot], pos_k<SB>(j) / NS)) return false;
+        tc_fence_after();
+        const uint32_t d = tmem + (t * SB + j % SB) * KT;
+#pragma unroll
+        for (int k = 0; k < D / 16; ++k)
+          mma_ss(d, sw128_desc(q_addr + (k >> 2) * (128 * 128) + (k & 3) * 32, 16),
+                 sw128_desc(kv_addr + slot * C::SLOT + (k >> 2) * (KT * 128) + (k & 3) * 32, 16), ID_S, k > 0);
+        tc_commit(&b_empty[slot]);
+        tc_commit(&b_s[t * SB + j % SB]);
+        return true;
+      };
+      auto pv_mma = [&](int j) {                            // O += P V of tile j
+        const int pos = pos_v<SB>(j, n), slot = pos % NS;
+        if (!wait(&b_full[slot], pos / NS) || !wait(&b_p[t * SB + j % SB], j / SB)) return false;
+        tc_fence_after();
+        const uint32_t pa = tmem + (t * SB + j % SB) * KT;
+#pragma unroll
+        for (int k = 0; k < KT / 16; ++k)
+          tc_mma_f16(c_o, pa + k * 8, sw128_desc(kv_addr + slot * C::SLOT + k * 2048, KT * 128), ID_O, j > 0 || k > 0);
+        tc_commit(&b_empty[slot]);
+        tc_commit(&b_pv[t]);
+        return true;
+      };
+      if (ok && mine > 0) ok = s_mma(0);
+      for (int j = 0; ok && j < mine; ++j) {
+        if (SB == 2 && j + 1 < mine) {
+          // the other S buffer holds P of tile j - 1
+          ok = (j == 0 || wait(&b_pv[t], j - 1)) && s_mma(j + 1);
+        }
+        if (ok) ok = pv_mma(j);
+        if (SB == 1 && ok && j + 1 < mine) ok = wait(&b_pv[t], j) && s_mma(j + 1);   // S overwrites P
+      }
+      for (int j = mine; ok && j < n; ++j) {                // the other tile's keys: hand the slots on
+        const int pk = pos_k<SB>(j), pv = pos_v<SB>(j, n);
+        ok = wait(&b_full[pk % NS], pk / NS);
+        if (ok) mbar_arrive(&b_empty[pk % NS]);
+        ok = ok && wait(&b_full[pv % NS], pv / NS);
+        if (ok) mbar_arrive(&b_empty[pv % NS]);
+      }
+      if (!ok) {
+        give_up();
+        // what this thread issued finishes before TMEM goes (bounded)
+        tc_commit(&b_fin[t]);
+        mbar_wait_bounded(&b_fin[t], 0, kWaitLimitNs);
+      }
+    }
+  } else {
+    // ------------------------------------------------------------ softmax: thread = row
+    const int t = warp >> 2, r = tid & 127, hpg = a.hpg;
+    const int first = tok0 + t * p.tile_tok;
+    const int ntok = max(0, min(p.tile_tok, s.t - first)), nvec = ntok * hpg;
+    const int mine = max(0, min(n_tile[t] - j0, n));
+    const bool valid = r < nvec;
+    const int tok = valid ? first + r / hpg : 0, head = g * hpg + (valid ? r % hpg : 0);
+    // rows of no query vector (Q = 0) stay unmasked: nothing of them is written
+    const int lim = valid ? min(s.len, s.len - s.t + tok + 1) : 0x7fffffff;
+    const int lim_min = s.len - s.t + first + 1;           // keys below it need no mask
+    float m = -INFINITY, l = 0.f;
+    bool ok = true;
+    if (mine > 0) {
+      // Q into shared memory: 16-byte chunks, rows of 128 bytes, swizzled
+      unsigned char* qs = sm + t * C::QB;
+      const T* qp = static_cast<const T*>(a.q);
+      constexpr int CH = D / 8;
+      for (int i = r; i < 128 * CH; i += 128) {
+        const int row = i / CH, c = i % CH;
+        uint4 v = make_uint4(0, 0, 0, 0);
+        if (row < nvec)
+          v = *reinterpret_cast<const uint4*>(qp + (size_t)(s.r0 + first + row / hpg) * a.q_row +
+                                              (size_t)(g * hpg + row % hpg) * D + c * 8);
+        *reinterpret_cast<uint4*>(qs + (c >> 3) * (128 * 128) + row * 128 + (((c & 7) ^ (row & 7)) << 4)) = v;
+      }
+      fence_proxy_async_smem();
+      mbar_arrive(&b_q[t]);
+    }
+    const uint32_t lanes = tmem + ((uint32_t)((warp & 3) * 32) << 16);
+    const uint32_t c_o = lanes + C::C_O + t * D;
+    for (int j = 0; j < mine; ++j) {
+      const uint32_t c_s = lanes + (t * SB + j % SB) * KT;
+      if (!wait(&b_s[t * SB + j % SB], j / SB)) {
+        ok = false;
+        break;
+      }
+      tc_fence_after();
+      uint32_t x[KT / 32][32];
+#pragma unroll
+      for (int i = 0; i < KT / 32; ++i) tc_ld32(c_s + i * 32, x[i]);
+      wait_ld(x);
+      const int key0 = (j0 + j) * KT;
+      if (key0 + KT > lim_min) {
+#pragma unroll
+        for (int i = 0; i < KT / 32; ++i)
+#pragma unroll
+          for (int k = 0; k < 32; ++k)
+            if (key0 + i * 32 + k >= lim) x[i][k] = 0xff800000u;
+      }
+      float mx4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+      for (int i = 0; i < KT / 32; ++i)
+#pragma unroll
+        for (int k = 0; k < 32; ++k) mx4[k & 3] = fmaxf(mx4[k & 3], __uint_as_float(x[i][k]));
+      const float mx = fmaxf(fmaxf(mx4[0], mx4[1]), fmaxf(mx4[2], mx4[3])) * a.qmul;
+      const bool raise = mx > m + LazyMax<T>::kLazy;        // m starts at -inf
+      if (__any_sync(0xffffffffu, raise) && j > 0) {
+        const float f = raise ? ex2(m - mx) : 1.f;
+        // with one S buffer S of this tile came after P V of the last one
+        if (SB == 2 && !wait(&b_pv[t], j - 1)) {
+          ok = false;
+          break;
+        }
+        if (SB == 2) tc_fence_after();
+#pragma unroll
+        for (int i = 0; i < D / 32; ++i) {
+          uint32_t o[32];
+          tc_ld32(c_o + i * 32, o);
+          wait_ld(o);
+#pragma unroll
+          for (int k = 0; k < 32; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * f);
+          tc_st32(c_o + i * 32, o);
+        }
+        l *= f;
+      }
+      if (raise) m = mx;
+      const float off = LazyMax<T>::kLog2 - (m == -INFINITY ? 0.f : m);
+      float sum[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+      for (int i = 0; i < KT / 64; ++i) {
+        uint32_t w[32];
+#pragma unroll
+        for (int k = 0; k < 32; ++k) {
+          const float e0 = ex2(fmaf(__uint_as_float(x[2 * i + (k >> 4)][(2 * k) & 31]), a.qmul, off));
+          const float e1 = ex2(fmaf(__uint_as_float(x[2 * i + (k >> 4)][(2 * k + 1) & 31]), a.qmul, off));
+          sum[(2 * k) & 3] += e0;
+          sum[(2 * k + 1) & 3] += e1;
+          w[k] = pack2(e0, e1, (const T*)nullptr);
+        }
+        tc_st32(c_s + i * 32, w);
+      }
+      l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+      tc_wait_st();
+      tc_fence_before();
+      mbar_arrive(&b_p[t * SB + j % SB]);
+    }
+    // a wait sees only the parity of a phase, so the one before must be known complete:
+    // with one S buffer the last S came after it, with two only after the one before that
+    if (SB == 2 && ok && mine > 1) ok = wait(&b_pv[t], mine - 2);
+    if (ok && mine > 0) ok = wait(&b_pv[t], mine - 1);
+    if (ok) {
+      tc_fence_after();
+      const size_t rec = (((size_t)blockIdx.x * p.splits + blockIdx.y) * NT + t) * 128 + r;
+#pragma unroll 1
+      for (int i = 0; i < D / 32; ++i) {
+        uint32_t o[32];
+        if (mine > 0) {
+          tc_ld32(c_o + i * 32, o);
+          wait_ld(o);
+        }
+        if (!valid) continue;
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          float y[8];
+#pragma unroll
+          for (int e = 0; e < 8; ++e) y[e] = mine > 0 ? __uint_as_float(o[k * 8 + e]) : 0.f;
+          if (p.splits > 1)
+            store8(p.rec_acc + rec * D + i * 32 + k * 8, y);
+          else
+            paged_store_row<T>(a, s.r0 + tok, head, D, i * 32 + k * 8, m, l, LazyMax<T>::kLog2, y, i == 0 && k == 0);
+        }
+      }
+      if (p.splits > 1 && valid) p.rec_ml[rec] = make_float2(m, l);
+    } else {
+      give_up();
+    }
+  }
+  __syncwarp();
+  tc_fence_before();
+  __syncthreads();
+  if (warp == W_MMA) {
+    tc_fence_after();
+    tc_dealloc(tmem, 512);
+  }
+}
+
+// Joins the records of split items: a block per (item, row of the item), threads over
+// groups of 8 features.
+template <typename T, int D>
+__global__ void __launch_bounds__(128) chunk_merge_kernel(const ChunkParams p) {
+  constexpr int L = D / 8, RW = 128 / L;                   // threads a row, rows a block
+  constexpr int NT = ChunkCfg<D>::NT;
+  pdl_wait();
+  pdl_trigger();
+  const int4 d = p.rec_desc[blockIdx.x];
+  if (d.x < 0) return;
+  uint32_t ignore = 0;
+  const PagedAttendParams& a = p.a;
+  const PagedSeq s = paged_seq(a.map, d.x, a.T, a.max_rows, ignore);
+  const int row = blockIdx.y * RW + threadIdx.x / L, c = threadIdx.x % L;
+  const int t = row >> 7, r = row & 127;
+  const int tok = d.z + t * p.tile_tok + r / a.hpg;
+  if (r >= p.tile_tok * a.hpg || tok >= s.t) return;
+  const size_t rec0 = ((size_t)blockIdx.x * p.splits * NT + t) * 128 + r;
+  float m = -INFINITY, l = 0.f, acc[8] = {};
+  for (int i = 0; i < p.splits; ++i) m = fmaxf(m, p.rec_ml[rec0 + (size_t)i * NT * 128].x);
+  for (int i = 0; i < p.splits; ++i) {
+    const size_t rec = rec0 + (size_t)i * NT * 128;
+    const float2 ml = p.rec_ml[rec];
+    if (ml.x == -INFINITY) continue;
+    const float f = ex2(ml.x - m);
+    float y[8];
+    load8(p.rec_acc + rec * D + c * 8, y);
+    l += f * ml.y;
+#pragma unroll
+    for (int k = 0; k < 8; ++k) acc[k] += f * y[k];
+  }
+  paged_store_row<T>(a, s.r0 + tok, d.y * a.hpg + r % a.hpg, D, c * 8, m, l, LazyMax<T>::kLog2, acc, c == 0);
+}
+
+// ---------------------------------------------------------------------------
+// Host side
+// ---------------------------------------------------------------------------
+typedef CUresult (*EncodeTiled)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*, const cuuint64_t*,
+                                const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle,
+                                CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+
+// Tensor map of a pool: rows of hd elements, boxes of 64 features x min(page, KT) rows.
+static int pool_map(const swa_paged_cache& c, void* base, int kt, CUtensorMap* m) {
+  static EncodeTiled encode = nullptr;
+  if (!encode) {
+    void* f = nullptr;
+    cudaDriverEntryPointQueryResult st;
+    const cudaError_t e = cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &f, 12000, cudaEnableDefault, &st);
+    if (e != cudaSuccess) return cuda_status(e);
+    if (st != cudaDriverEntryPointSuccess || !f) return cuda_status(cudaErrorNotSupported);
+    encode = reinterpret_cast<EncodeTiled>(f);
+  }
+  const cuuint64_t dims[2] = {(cuuint64_t)c.hd, (cuuint64_t)c.num_pages * c.nk * c.page};
+  const cuuint64_t strides[1] = {(cuuint64_t)c.hd * 2};
+  const cuuint32_t box[2] = {64, (cuuint32_t)(c.page < kt ? c.page : kt)}, es[2] = {1, 1};
+  const CUresult r = encode(m, c.dtype == SWA_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 2,
+                            base, dims, strides, box, es, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                            CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  return r == CUDA_SUCCESS ? SWA_OK : cuda_status(cudaErrorInvalidValue);
+}
+
+ChunkPlan chunk_plan(const swa_paged_attend_args* a) {
+  const swa_paged_cache& c = a->cache;
+  const int hpg = a->nh / c.nk, nt = c.hd == 256 ? 1 : 2, kt = c.hd == 256 ? 64 : 128;
+  ChunkPlan pl{};
+  pl.tile_tok = 128 / hpg;
+  const long long item_tok = (long long)nt * pl.tile_tok;
+  pl.items = ((long long)a->T / item_tok + c.B) * c.nk;
+  // one sequence of max_rows rows has no more items than its rows need
+  const long long most = (a->max_rows + item_tok - 1) / item_tok * c.B * c.nk;
+  if (most < pl.items) pl.items = most;
+  // fewer items than SMs: cut the keys, at least four tiles a share
+  const long long sms = num_sms() > 0 ? num_sms() : 148;
+  const long long tiles = ((long long)c.max_pages * c.page + kt - 1) / kt;
+  long long sp = sms / pl.items;
+  if (sp > (tiles + 3) / 4) sp = (tiles + 3) / 4;
+  pl.splits = (int)(sp < 1 ? 1 : sp);
+  if (pl.splits > 1) {
+    const size_t recs = (size_t)pl.items * pl.splits * nt * 128;
+    pl.off_ml = up256s(recs * c.hd * sizeof(float));
+    pl.off_desc = pl.off_ml + up256s(recs * sizeof(float2));
+    pl.bytes = pl.off_desc + up256s((size_t)pl.items * sizeof(int4));
+  }
+  return pl;
+}
+
+template <typename T, int D>
+static int launch(const swa_paged_attend_args* a, const PagedAttendParams& ap, const ChunkPlan& pl, int small, char* ws,
+                  cudaStream_t s) {
+  CUtensorMap mk, mv;
+  int rc = pool_map(a->cache, a->cache.k, ChunkCfg<D>::KT, &mk);
+  if (rc == SWA_OK) rc = pool_map(a->cache, a->cache.v, ChunkCfg<D>::KT, &mv);
+  if (rc != SWA_OK) return rc;
+  ChunkParams p{};
+  p.a = ap;
+  p.a.qmul = fmaxf(ap.qmul, 0x1p-100f);                    // masked scores stay -inf when scale is 0
+  p.small = small;
+  p.tile_tok = pl.tile_tok;
+  p.splits = pl.splits;
+  p.rec_acc = reinterpret_cast<float*>(ws);
+  p.rec_ml = reinterpret_cast<float2*>(ws + pl.off_ml);
+  p.rec_desc = reinterpret_cast<int4*>(ws + pl.off_desc);
+  const cudaError_t e = cudaFuncSetAttribute(paged_chunk_kernel<T, D>, cudaFuncAttributeMaxDynamicSharedMemorySize, ChunkCfg<D>::SMEM);
+  if (e != cudaSuccess) return cuda_status(e);
+  rc = finish_launch(launch_pdl(paged_chunk_kernel<T, D>, dim3((unsigned)pl.items, pl.splits), dim3(ChunkCfg<D>::THREADS),
+                                ChunkCfg<D>::SMEM, s, mk, mv, p));
+  if (rc != SWA_OK || pl.splits == 1) return rc;
+  constexpr int RW = 128 / (D / 8);
+  return finish_launch(launch_pdl(chunk_merge_kernel<T, D>, dim3((unsigned)pl.items, ChunkCfg<D>::NT * 128 / RW), dim3(128), 0, s, p));
+}
+
+int launch_paged_chunk(const swa_paged_attend_args* a, const PagedAttendParams& p, const ChunkPlan& pl, int small, char* ws,
+                       cudaStream_t s) {
+  const int d = a->cache.hd;
+  if (a->cache.dtype == SWA_BF16)
+    return d == 64 ? launch<__nv_bfloat16, 64>(a, p, pl, small, ws, s)
+                   : d == 128 ? launch<__nv_bfloat16, 128>(a, p, pl, small, ws, s) : launch<__nv_bfloat16, 256>(a, p, pl, small, ws, s);
+  return d == 64 ? launch<__half, 64>(a, p, pl, small, ws, s)
+                 : d == 128 ? launch<__half, 128>(a, p, pl, small, ws, s) : launch<__half, 256>(a, p, pl, small, ws, s);
+}
+
+}  // namespace swa
