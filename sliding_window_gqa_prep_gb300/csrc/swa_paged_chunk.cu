@@ -35,7 +35,7 @@ struct ChunkCfg {
   static constexpr int NS = D == 64 ? 8 : 5;           // K / V slots
   static constexpr int SLOT = KT * D * 2;
   static constexpr int QB = 128 * D * 2;               // bytes of a query tile
-  static constexpr int THREADS = NT * 128 + 32 + NT * 32;   // softmax, loader, issuers
+  static constexpr int THREADS = NT * 128 + 128;       // softmax warpgroups; loader, issuers, idle warps
   static constexpr int SMEM = NT * QB + NS * SLOT + 1024;   // + alignment
   static constexpr int C_O = NT * SB * KT;             // first O column
 };
@@ -75,6 +75,36 @@ __device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint3
                "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}"
                :: "r"(d), "l"(a), "l"(b), "r"(idesc), "r"(acc ? 1 : 0) : "memory");
 }
+// one lane of a converged warp
+__device__ __forceinline__ bool elect_one() {
+  uint32_t p;
+  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(p));
+  return p != 0;
+}
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float d;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+  return d;
+}
+// packed pairs of f32
+__device__ __forceinline__ uint64_t pack64(uint32_t lo, uint32_t hi) {
+  uint64_t d;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(d) : "r"(lo), "r"(hi));
+  return d;
+}
+__device__ __forceinline__ void unpack64(uint64_t v, float& lo, float& hi) {
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(v));
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t d;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
+  return d;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+  uint64_t d;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+  return d;
+}
 // Waits for this thread's TMEM loads; the registers are operands, so that nothing that
 // reads them moves ahead of the wait.
 #define SWA_RW32(r) "+r"(r[0]),"+r"(r[1]),"+r"(r[2]),"+r"(r[3]),"+r"(r[4]),"+r"(r[5]),"+r"(r[6]),"+r"(r[7]), \
@@ -95,6 +125,21 @@ __device__ __forceinline__ void tma_2d(uint32_t dst, const CUtensorMap* map, int
                :: "r"(dst), "l"(map), "r"(smem_u32(bar)), "r"(x), "r"(y) : "memory");
 }
 
+// A wait that gives up after kWaitLimitNs; the clock is read every 64th try only (the
+// read takes longer than a try).
+__device__ __forceinline__ bool chunk_wait(uint64_t* bar, uint32_t parity, const int* abort_flag) {
+  if (mbar_try_wait(bar, parity)) return true;
+  uint64_t t0 = 0;
+  for (uint32_t i = 1;; ++i) {
+    if (mbar_try_wait(bar, parity)) return true;
+    if ((i & 63) == 0) {
+      const uint64_t now = global_ns();
+      if (t0 == 0) t0 = now;
+      if (now - t0 > kWaitLimitNs || *(const volatile int*)abort_flag) return false;
+    }
+  }
+}
+
 // First K / V slot position of tile j's K and V in the order they are consumed.
 template <int SB>
 __device__ __forceinline__ int pos_k(int j) { return SB == 1 ? 2 * j : (j == 0 ? 0 : 2 * j - 1); }
@@ -112,12 +157,12 @@ __global__ void __launch_bounds__(ChunkCfg<D>::THREADS, 1)
   constexpr int NT = C::NT, SB = C::SB, KT = C::KT, NS = C::NS;
   constexpr bool BF = std::is_same<T, __nv_bfloat16>::value;
   extern __shared__ unsigned char sm_raw[];
-  __shared__ __align__(8) uint64_t b_full[NS], b_empty[NS], b_q[NT], b_s[NT * SB], b_p[NT * SB], b_pv[NT], b_fin[NT], b_tail;
+  __shared__ __align__(8) uint64_t b_full[NS], b_empty[NS], b_q[NT], b_s[NT * SB], b_p[NT * SB], b_pv[NT], b_fin, b_tail;
   __shared__ uint32_t s_tmem;
   __shared__ int s_abort, s_b, s_idx;
   __shared__ int s_scan[32];
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  constexpr int NW = C::THREADS / 32, W_LOAD = NT * 4, W_MMA = NT * 4 + 1;
+  const int tid = threadIdx.x, lane = tid & 31, warp = __shfl_sync(0xffffffffu, tid >> 5, 0);
+  constexpr int W_LOAD = NT * 4, W_MMA = NT * 4 + 1;
   unsigned char* const sm = reinterpret_cast<unsigned char*>((reinterpret_cast<uintptr_t>(sm_raw) + 1023) & ~(uintptr_t)1023);
   unsigned char* const sm_kv = sm + NT * C::QB;
   const PagedAttendParams& a = p.a;
@@ -193,17 +238,17 @@ __global__ void __launch_bounds__(ChunkCfg<D>::THREADS, 1)
     if (lane == 0) {
       for (int i = 0; i < NS; ++i) {
         mbar_init(&b_full[i], 1);
-        mbar_init(&b_empty[i], NT);
+        mbar_init(&b_empty[i], 1);
       }
       for (int t = 0; t < NT; ++t) {
         mbar_init(&b_q[t], 128);
         mbar_init(&b_pv[t], 1);
-        mbar_init(&b_fin[t], 1);
       }
       for (int i = 0; i < NT * SB; ++i) {
         mbar_init(&b_s[i], 1);
         mbar_init(&b_p[i], 128);
       }
+      mbar_init(&b_fin, 1);
       mbar_init(&b_tail, 1);
       mbar_fence_init();
     }
@@ -213,16 +258,20 @@ __global__ void __launch_bounds__(ChunkCfg<D>::THREADS, 1)
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  const uint32_t tmem = s_tmem;
+  const uint32_t tmem = __shfl_sync(0xffffffffu, s_tmem, 0);
   auto give_up = [&]() {
     s_abort = 1;
     __threadfence_block();
     set_err(a.err, SWA_DERR_TIMEOUT);
   };
   auto wait = [&](uint64_t* bar, int phase) -> bool {
-    return mbar_wait_bounded(bar, (uint32_t)(phase & 1), kWaitLimitNs) && !*(volatile int*)&s_abort;
+    return chunk_wait(bar, (uint32_t)(phase & 1), &s_abort);
   };
 
+  // The softmax threads hold a row of S: registers move over to them (384 threads are
+  // launched with 168 each: 2 * 128 * 216 + 128 * 72 = 384 * 168).
+  if (warp >= W_LOAD) {
+  if constexpr (NT == 2) asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
   if (warp == W_LOAD) {
     // ------------------------------------------------------------ loader
     // lane i copies box i of a slot: `rows` keys x 64 features
@@ -282,65 +331,76 @@ __global__ void __launch_bounds__(ChunkCfg<D>::THREADS, 1)
       // copies in flight land before the CTA exits (bounded)
       for (int q = max(0, issued - NS); q < issued; ++q) mbar_wait_bounded(&b_full[q % NS], (uint32_t)((q / NS) & 1), kWaitLimitNs);
     }
-  } else if (warp >= W_MMA) {
-    // ------------------------------------------------------------ issuers, one per query tile
-    const int t = warp - W_MMA;
-    if (lane == 0 && n > 0) {
-      constexpr uint32_t ID_S = chunk_idesc(BF, false, KT), ID_O = chunk_idesc(BF, true, D);
-      const uint32_t q_addr = smem_u32(sm + t * C::QB), kv_addr = smem_u32(sm_kv);
-      const uint32_t c_o = tmem + C::C_O + t * D;
-      const int mine = max(0, min(n_tile[t] - j0, n));     // tiles that this query tile sees
-      bool ok = mine == 0 || wait(&b_q[t], 0);
-      auto s_mma = [&](int j) {                             // S of tile j
-        const int slot = pos_k<SB>(j) % NS;
-        if (!wait(&b_full[slot], pos_k<SB>(j) / NS)) return false;
-        tc_fence_after();
-        const uint32_t d = tmem + (t * SB + j % SB) * KT;
+  } else if (warp == W_MMA && n > 0) {
+    // ------------------------------------------------------------ issuer
+    // One warp issues every product, the two tiles strictly in turn (P V of a tile, then
+    // its next S): were their products mixed, both tiles would wait for S, compute, and
+    // wait for P V at the same time. The warp stays converged and one elected lane issues.
+    constexpr uint32_t ID_S = chunk_idesc(BF, false, KT), ID_O = chunk_idesc(BF, true, D);
+    const bool leader = elect_one();
+    // descriptors are a base plus (byte offset >> 4): the addresses stay below 2^18, so the
+    // address field never carries
+    const uint64_t q_desc = sw128_desc(smem_u32(sm), 16), k_desc = sw128_desc(smem_u32(sm_kv), 16);
+    const uint64_t v_desc = sw128_desc(smem_u32(sm_kv), KT * 128);
+    int mine[NT];                                           // tiles that each query tile sees: the last one most
+#pragma unroll
+    for (int t = 0; t < NT; ++t) mine[t] = max(0, min(n_tile[t] - j0, n));
+    auto last_user = [&](int t, int j) { return t == NT - 1 || mine[NT - 1] <= j; };
+    auto s_mma = [&](int t, int j) {                        // S of tile j
+      const int slot = pos_k<SB>(j) % NS, buf = t * SB + j % SB;
+      if (!wait(&b_full[slot], pos_k<SB>(j) / NS)) return false;
+      tc_fence_after();
+      if (leader) {
+        const uint64_t qd = q_desc + (uint64_t)((t * C::QB) >> 4), kd = k_desc + (uint64_t)((slot * C::SLOT) >> 4);
 #pragma unroll
         for (int k = 0; k < D / 16; ++k)
-          mma_ss(d, sw128_desc(q_addr + (k >> 2) * (128 * 128) + (k & 3) * 32, 16),
-                 sw128_desc(kv_addr + slot * C::SLOT + (k >> 2) * (KT * 128) + (k & 3) * 32, 16), ID_S, k > 0);
-        tc_commit(&b_empty[slot]);
-        tc_commit(&b_s[t * SB + j % SB]);
-        return true;
-      };
-      auto pv_mma = [&](int j) {                            // O += P V of tile j
-        const int pos = pos_v<SB>(j, n), slot = pos % NS;
-        if (!wait(&b_full[slot], pos / NS) || !wait(&b_p[t * SB + j % SB], j / SB)) return false;
-        tc_fence_after();
-        const uint32_t pa = tmem + (t * SB + j % SB) * KT;
+          mma_ss(tmem + buf * KT, qd + (((k >> 2) * (128 * 128) + (k & 3) * 32) >> 4),
+                 kd + (((k >> 2) * (KT * 128) + (k & 3) * 32) >> 4), ID_S, k > 0);
+        tc_commit(&b_s[buf]);
+        if (last_user(t, j)) tc_commit(&b_empty[slot]);
+      }
+      __syncwarp();
+      return true;
+    };
+    auto pv_mma = [&](int t, int j) {                       // O += P V of tile j
+      const int pos = pos_v<SB>(j, n), slot = pos % NS, buf = t * SB + j % SB;
+      if (!wait(&b_full[slot], pos / NS) || !wait(&b_p[buf], j / SB)) return false;
+      tc_fence_after();
+      if (leader) {
+        const uint64_t vd = v_desc + (uint64_t)((slot * C::SLOT) >> 4);
 #pragma unroll
         for (int k = 0; k < KT / 16; ++k)
-          tc_mma_f16(c_o, pa + k * 8, sw128_desc(kv_addr + slot * C::SLOT + k * 2048, KT * 128), ID_O, j > 0 || k > 0);
-        tc_commit(&b_empty[slot]);
+          tc_mma_f16(tmem + C::C_O + t * D, tmem + buf * KT + k * 8, vd + (uint64_t)((k * 2048) >> 4), ID_O, j > 0 || k > 0);
         tc_commit(&b_pv[t]);
-        return true;
-      };
-      if (ok && mine > 0) ok = s_mma(0);
-      for (int j = 0; ok && j < mine; ++j) {
-        if (SB == 2 && j + 1 < mine) {
-          // the other S buffer holds P of tile j - 1
-          ok = (j == 0 || wait(&b_pv[t], j - 1)) && s_mma(j + 1);
-        }
-        if (ok) ok = pv_mma(j);
-        if (SB == 1 && ok && j + 1 < mine) ok = wait(&b_pv[t], j) && s_mma(j + 1);   // S overwrites P
+        if (last_user(t, j)) tc_commit(&b_empty[slot]);
       }
-      for (int j = mine; ok && j < n; ++j) {                // the other tile's keys: hand the slots on
-        const int pk = pos_k<SB>(j), pv = pos_v<SB>(j, n);
-        ok = wait(&b_full[pk % NS], pk / NS);
-        if (ok) mbar_arrive(&b_empty[pk % NS]);
-        ok = ok && wait(&b_full[pv % NS], pv / NS);
-        if (ok) mbar_arrive(&b_empty[pv % NS]);
-      }
-      if (!ok) {
-        give_up();
-        // what this thread issued finishes before TMEM goes (bounded)
-        tc_commit(&b_fin[t]);
-        mbar_wait_bounded(&b_fin[t], 0, kWaitLimitNs);
+      __syncwarp();
+      return true;
+    };
+    bool ok = true;
+#pragma unroll
+    for (int t = 0; t < NT; ++t)
+      if (ok && mine[t] > 0) ok = wait(&b_q[t], 0) && s_mma(t, 0);
+    for (int j = 0; ok && j < n; ++j) {
+#pragma unroll
+      for (int t = 0; t < NT; ++t) {
+        if (!ok || j >= mine[t]) continue;
+        // with two S buffers the other one holds P of tile j - 1, with one S overwrites P of tile j
+        if (SB == 2 && j + 1 < mine[t]) ok = (j == 0 || wait(&b_pv[t], j - 1)) && s_mma(t, j + 1);
+        if (ok) ok = pv_mma(t, j);
+        if (SB == 1 && ok && j + 1 < mine[t]) ok = wait(&b_pv[t], j) && s_mma(t, j + 1);
       }
     }
+    if (!ok) {
+      give_up();
+      // what was issued finishes before TMEM goes (bounded)
+      if (leader) tc_commit(&b_fin);
+      mbar_wait_bounded(&b_fin, 0, kWaitLimitNs);
+    }
+  }
   } else {
     // ------------------------------------------------------------ softmax: thread = row
+    if constexpr (NT == 2) asm volatile("setmaxnreg.inc.sync.aligned.u32 216;");
     const int t = warp >> 2, r = tid & 127, hpg = a.hpg;
     const int first = tok0 + t * p.tile_tok;
     const int ntok = max(0, min(p.tile_tok, s.t - first)), nvec = ntok * hpg;
@@ -393,7 +453,8 @@ __global__ void __launch_bounds__(ChunkCfg<D>::THREADS, 1)
 #pragma unroll
       for (int i = 0; i < KT / 32; ++i)
 #pragma unroll
-        for (int k = 0; k < 32; ++k) mx4[k & 3] = fmaxf(mx4[k & 3], __uint_as_float(x[i][k]));
+        for (int k = 0; k < 32; k += 2)
+          mx4[(k >> 1) & 3] = max3(mx4[(k >> 1) & 3], __uint_as_float(x[i][k]), __uint_as_float(x[i][k + 1]));
       const float mx = fmaxf(fmaxf(mx4[0], mx4[1]), fmaxf(mx4[2], mx4[3])) * a.qmul;
       const bool raise = mx > m + LazyMax<T>::kLazy;        // m starts at -inf
       if (__any_sync(0xffffffffu, raise) && j > 0) {
@@ -417,21 +478,27 @@ __global__ void __launch_bounds__(ChunkCfg<D>::THREADS, 1)
       }
       if (raise) m = mx;
       const float off = LazyMax<T>::kLog2 - (m == -INFINITY ? 0.f : m);
-      float sum[4] = {0.f, 0.f, 0.f, 0.f};
+      const uint64_t mul2 = pack64(__float_as_uint(a.qmul), __float_as_uint(a.qmul)),
+                     off2 = pack64(__float_as_uint(off), __float_as_uint(off));
+      uint64_t sum[2] = {0, 0};
 #pragma unroll
       for (int i = 0; i < KT / 64; ++i) {
         uint32_t w[32];
 #pragma unroll
         for (int k = 0; k < 32; ++k) {
-          const float e0 = ex2(fmaf(__uint_as_float(x[2 * i + (k >> 4)][(2 * k) & 31]), a.qmul, off));
-          const float e1 = ex2(fmaf(__uint_as_float(x[2 * i + (k >> 4)][(2 * k + 1) & 31]), a.qmul, off));
-          sum[(2 * k) & 3] += e0;
-          sum[(2 * k + 1) & 3] += e1;
+          const uint32_t* y = &x[2 * i + (k >> 4)][(2 * k) & 31];
+          float e0, e1;
+          unpack64(fma2(pack64(y[0], y[1]), mul2, off2), e0, e1);
+          e0 = ex2(e0);
+          e1 = ex2(e1);
+          sum[k & 1] = add2(sum[k & 1], pack64(__float_as_uint(e0), __float_as_uint(e1)));
           w[k] = pack2(e0, e1, (const T*)nullptr);
         }
         tc_st32(c_s + i * 32, w);
       }
-      l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+      float l0, l1;
+      unpack64(add2(sum[0], sum[1]), l0, l1);
+      l += l0 + l1;
       tc_wait_st();
       tc_fence_before();
       mbar_arrive(&b_p[t * SB + j % SB]);
