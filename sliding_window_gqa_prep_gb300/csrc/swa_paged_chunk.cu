@@ -157,7 +157,7 @@ __global__ void __launch_bounds__(ChunkCfg<D>::THREADS, 1)
   constexpr int NT = C::NT, SB = C::SB, KT = C::KT, NS = C::NS;
   constexpr bool BF = std::is_same<T, __nv_bfloat16>::value;
   extern __shared__ unsigned char sm_raw[];
-  __shared__ __align__(8) uint64_t b_full[NS], b_empty[NS], b_q[NT], b_s[NT * SB], b_p[NT * SB], b_pv[NT], b_fin, b_tail;
+  __shared__ __align__(8) uint64_t b_full[NS], b_empty[NS], b_q[NT], b_s[NT * SB], b_p[NT * SB][2], b_pv[NT], b_fin, b_tail;
   __shared__ uint32_t s_tmem;
   __shared__ int s_abort, s_b, s_idx;
   __shared__ int s_scan[32];
@@ -246,7 +246,8 @@ __global__ void __launch_bounds__(ChunkCfg<D>::THREADS, 1)
       }
       for (int i = 0; i < NT * SB; ++i) {
         mbar_init(&b_s[i], 1);
-        mbar_init(&b_p[i], 128);
+        mbar_init(&b_p[i][0], 128);
+        mbar_init(&b_p[i][1], 128);
       }
       mbar_init(&b_fin, 1);
       mbar_init(&b_tail, 1);
@@ -357,23 +358,34 @@ __global__ void __launch_bounds__(ChunkCfg<D>::THREADS, 1)
           mma_ss(tmem + buf * KT, qd + (((k >> 2) * (128 * 128) + (k & 3) * 32) >> 4),
                  kd + (((k >> 2) * (KT * 128) + (k & 3) * 32) >> 4), ID_S, k > 0);
         tc_commit(&b_s[buf]);
-        if (last_user(t, j)) tc_commit(&b_empty[slot]);
       }
       __syncwarp();
       return true;
     };
     auto pv_mma = [&](int t, int j) {                       // O += P V of tile j
       const int pos = pos_v<SB>(j, n), slot = pos % NS, buf = t * SB + j % SB;
-      if (!wait(&b_full[slot], pos / NS) || !wait(&b_p[buf], j / SB)) return false;
-      tc_fence_after();
-      if (leader) {
-        const uint64_t vd = v_desc + (uint64_t)((slot * C::SLOT) >> 4);
+      const uint64_t vd = v_desc + (uint64_t)((slot * C::SLOT) >> 4);
+      if (!wait(&b_full[slot], pos / NS)) return false;
 #pragma unroll
-        for (int k = 0; k < KT / 16; ++k)
-          tc_mma_f16(tmem + C::C_O + t * D, tmem + buf * KT + k * 8, vd + (uint64_t)((k * 2048) >> 4), ID_O, j > 0 || k > 0);
-        tc_commit(&b_pv[t]);
-        if (last_user(t, j)) tc_commit(&b_empty[slot]);
+      for (int h = 0; h < 2; ++h) {                         // P arrives in halves
+        if (!wait(&b_p[buf][h], j / SB)) return false;
+        tc_fence_after();
+        if (leader) {
+#pragma unroll
+          for (int k = h * (KT / 32); k < (h + 1) * (KT / 32); ++k)
+            tc_mma_f16(tmem + C::C_O + t * D, tmem + buf * KT + k * 8, vd + (uint64_t)((k * 2048) >> 4), ID_O, j > 0 || k > 0);
+          if (h == 1) tc_commit(&b_pv[t]);
+          // P came out of S, so K of this tile is done with
+          if (h == 0 && last_user(t, j)) mbar_arrive(&b_empty[pos_k<SB>(j) % NS]);
+        }
+        __syncwarp();
       }
+      return true;
+    };
+    // O of tile j is there: its V is done with
+    auto pv_done = [&](int t, int j) {
+      if (!wait(&b_pv[t], j)) return false;
+      if (leader && last_user(t, j)) mbar_arrive(&b_empty[pos_v<SB>(j, n) % NS]);
       __syncwarp();
       return true;
     };
@@ -386,9 +398,9 @@ __global__ void __launch_bounds__(ChunkCfg<D>::THREADS, 1)
       for (int t = 0; t < NT; ++t) {
         if (!ok || j >= mine[t]) continue;
         // with two S buffers the other one holds P of tile j - 1, with one S overwrites P of tile j
-        if (SB == 2 && j + 1 < mine[t]) ok = (j == 0 || wait(&b_pv[t], j - 1)) && s_mma(t, j + 1);
+        if (SB == 2 && j + 1 < mine[t]) ok = (j == 0 || pv_done(t, j - 1)) && s_mma(t, j + 1);
         if (ok) ok = pv_mma(t, j);
-        if (SB == 1 && ok && j + 1 < mine[t]) ok = wait(&b_pv[t], j) && s_mma(t, j + 1);
+        if (SB == 1 && ok && j + 1 < mine[t]) ok = pv_done(t, j) && s_mma(t, j + 1);
       }
     }
     if (!ok) {
@@ -482,26 +494,27 @@ __global__ void __launch_bounds__(ChunkCfg<D>::THREADS, 1)
                      off2 = pack64(__float_as_uint(off), __float_as_uint(off));
       uint64_t sum[2] = {0, 0};
 #pragma unroll
-      for (int i = 0; i < KT / 64; ++i) {
-        uint32_t w[32];
+      for (int h = 0; h < 2; ++h) {                         // each half of P goes to P V on its own
+        uint32_t w[KT / 4];
 #pragma unroll
-        for (int k = 0; k < 32; ++k) {
-          const uint32_t* y = &x[2 * i + (k >> 4)][(2 * k) & 31];
+        for (int k = 0; k < KT / 4; ++k) {
+          const int e = h * (KT / 2) + 2 * k;
           float e0, e1;
-          unpack64(fma2(pack64(y[0], y[1]), mul2, off2), e0, e1);
+          unpack64(fma2(pack64(x[e >> 5][e & 31], x[e >> 5][(e & 31) + 1]), mul2, off2), e0, e1);
           e0 = ex2(e0);
           e1 = ex2(e1);
           sum[k & 1] = add2(sum[k & 1], pack64(__float_as_uint(e0), __float_as_uint(e1)));
           w[k] = pack2(e0, e1, (const T*)nullptr);
         }
-        tc_st32(c_s + i * 32, w);
+        if constexpr (KT == 128) tc_st32(c_s + h * (KT / 4), w);
+        else tc_st16(c_s + h * (KT / 4), w);
+        tc_wait_st();
+        tc_fence_before();
+        mbar_arrive(&b_p[t * SB + j % SB][h]);
       }
       float l0, l1;
       unpack64(add2(sum[0], sum[1]), l0, l1);
       l += l0 + l1;
-      tc_wait_st();
-      tc_fence_before();
-      mbar_arrive(&b_p[t * SB + j % SB]);
     }
     // a wait sees only the parity of a phase, so the one before must be known complete:
     // with one S buffer the last S came after it, with two only after the one before that
