@@ -157,7 +157,7 @@ __global__ void __launch_bounds__(ChunkCfg<D>::THREADS, 1)
   constexpr int NT = C::NT, SB = C::SB, KT = C::KT, NS = C::NS;
   constexpr bool BF = std::is_same<T, __nv_bfloat16>::value;
   extern __shared__ unsigned char sm_raw[];
-  __shared__ __align__(8) uint64_t b_full[NS], b_empty[NS], b_q[NT], b_s[NT * SB], b_p[NT * SB][2], b_pv[NT], b_fin, b_tail;
+  __shared__ __align__(8) uint64_t b_full[NS], b_empty[NS], b_q[NT], b_s[NT * SB], b_p[NT * SB][2], b_pv[NT], b_fin[NT], b_turn[NT], b_tail;
   __shared__ uint32_t s_tmem;
   __shared__ int s_abort, s_b, s_idx;
   __shared__ int s_scan[32];
@@ -238,18 +238,19 @@ __global__ void __launch_bounds__(ChunkCfg<D>::THREADS, 1)
     if (lane == 0) {
       for (int i = 0; i < NS; ++i) {
         mbar_init(&b_full[i], 1);
-        mbar_init(&b_empty[i], 1);
+        mbar_init(&b_empty[i], NT);
       }
       for (int t = 0; t < NT; ++t) {
         mbar_init(&b_q[t], 128);
         mbar_init(&b_pv[t], 1);
+        mbar_init(&b_fin[t], 1);
+        mbar_init(&b_turn[t], 1);
       }
       for (int i = 0; i < NT * SB; ++i) {
         mbar_init(&b_s[i], 1);
         mbar_init(&b_p[i][0], 128);
         mbar_init(&b_p[i][1], 128);
       }
-      mbar_init(&b_fin, 1);
       mbar_init(&b_tail, 1);
       mbar_fence_init();
     }
@@ -332,82 +333,105 @@ __global__ void __launch_bounds__(ChunkCfg<D>::THREADS, 1)
       // copies in flight land before the CTA exits (bounded)
       for (int q = max(0, issued - NS); q < issued; ++q) mbar_wait_bounded(&b_full[q % NS], (uint32_t)((q / NS) & 1), kWaitLimitNs);
     }
-  } else if (warp == W_MMA && n > 0) {
-    // ------------------------------------------------------------ issuer
-    // One warp issues every product, the two tiles strictly in turn (P V of a tile, then
-    // its next S): were their products mixed, both tiles would wait for S, compute, and
-    // wait for P V at the same time. The warp stays converged and one elected lane issues.
+  } else if (warp < W_MMA + NT && n > 0) {
+    // ------------------------------------------------------------ issuers, one per query tile
+    // Products run in the order P V of tile 0, its next S, P V of tile 1, its next S: each
+    // tile's softmax lies under the other's products. (Left alone, the two tiles fall into
+    // step, wait together for the tensor core and leave it idle together: 888 instead of
+    // 696 us at hd 128, 8192 rows over 8192 keys.) A warp waits, issues and commits for its
+    // tile alone and passes the turn on through b_turn, so that these latencies (about 100
+    // clk a wait, 250 a commit) overlap with the other tile's. The warp stays converged and
+    // one elected lane issues.
     constexpr uint32_t ID_S = chunk_idesc(BF, false, KT), ID_O = chunk_idesc(BF, true, D);
+    const int t = warp - W_MMA;
     const bool leader = elect_one();
+    const int mine = max(0, min(n_tile[NT == 2 ? t : 0] - j0, n));   // tiles that this query tile sees
+    const uint32_t c_s = tmem + t * SB * KT, c_o = tmem + C::C_O + t * D;
     // descriptors are a base plus (byte offset >> 4): the addresses stay below 2^18, so the
     // address field never carries
-    const uint64_t q_desc = sw128_desc(smem_u32(sm), 16), k_desc = sw128_desc(smem_u32(sm_kv), 16);
+    const uint64_t q_desc = sw128_desc(smem_u32(sm + t * C::QB), 16), k_desc = sw128_desc(smem_u32(sm_kv), 16);
     const uint64_t v_desc = sw128_desc(smem_u32(sm_kv), KT * 128);
-    int mine[NT];                                           // tiles that each query tile sees: the last one most
-#pragma unroll
-    for (int t = 0; t < NT; ++t) mine[t] = max(0, min(n_tile[t] - j0, n));
-    auto last_user = [&](int t, int j) { return t == NT - 1 || mine[NT - 1] <= j; };
-    auto s_mma = [&](int t, int j) {                        // S of tile j
-      const int slot = pos_k<SB>(j) % NS, buf = t * SB + j % SB;
+    const int other = NT == 2 ? max(0, min(n_tile[NT - 1 - t] - j0, n)) : 0;
+    auto pass_turn = [&]() {
+      if (NT == 2) mbar_arrive(&b_turn[1 - t]);
+    };
+    // before this tile's j-th P V: after tile 0's j-th (tile 1), after tile 1's j-1st (tile 0)
+    auto my_turn = [&](int j) {
+      if (NT == 1) return true;
+      return t == 0 ? j == 0 || other == 0 || wait(&b_turn[0], j - 1) : j >= other || wait(&b_turn[1], j);
+    };
+    auto s_mma = [&](int j) {                               // S of tile j
+      const int slot = pos_k<SB>(j) % NS;
       if (!wait(&b_full[slot], pos_k<SB>(j) / NS)) return false;
       tc_fence_after();
       if (leader) {
-        const uint64_t qd = q_desc + (uint64_t)((t * C::QB) >> 4), kd = k_desc + (uint64_t)((slot * C::SLOT) >> 4);
+        const uint64_t kd = k_desc + (uint64_t)((slot * C::SLOT) >> 4);
 #pragma unroll
         for (int k = 0; k < D / 16; ++k)
-          mma_ss(tmem + buf * KT, qd + (((k >> 2) * (128 * 128) + (k & 3) * 32) >> 4),
+          mma_ss(c_s + (j % SB) * KT, q_desc + (((k >> 2) * (128 * 128) + (k & 3) * 32) >> 4),
                  kd + (((k >> 2) * (KT * 128) + (k & 3) * 32) >> 4), ID_S, k > 0);
-        tc_commit(&b_s[buf]);
+        if (j > 0) pass_turn();
+        tc_commit(&b_s[t * SB + j % SB]);
       }
       __syncwarp();
       return true;
     };
-    auto pv_mma = [&](int t, int j) {                       // O += P V of tile j
-      const int pos = pos_v<SB>(j, n), slot = pos % NS, buf = t * SB + j % SB;
+    auto pv_mma = [&](int j) {                              // O += P V of tile j
+      const int pos = pos_v<SB>(j, n), slot = pos % NS;
       const uint64_t vd = v_desc + (uint64_t)((slot * C::SLOT) >> 4);
-      if (!wait(&b_full[slot], pos / NS)) return false;
+      if (!wait(&b_full[slot], pos / NS) || !my_turn(j)) return false;
 #pragma unroll
       for (int h = 0; h < 2; ++h) {                         // P arrives in halves
-        if (!wait(&b_p[buf][h], j / SB)) return false;
+        if (!wait(&b_p[t * SB + j % SB][h], j / SB)) return false;
         tc_fence_after();
         if (leader) {
 #pragma unroll
           for (int k = h * (KT / 32); k < (h + 1) * (KT / 32); ++k)
-            tc_mma_f16(tmem + C::C_O + t * D, tmem + buf * KT + k * 8, vd + (uint64_t)((k * 2048) >> 4), ID_O, j > 0 || k > 0);
+            tc_mma_f16(c_o, c_s + (j % SB) * KT + k * 8, vd + (uint64_t)((k * 2048) >> 4), ID_O, j > 0 || k > 0);
+          if (h == 1 && j + 1 == mine) pass_turn();
           if (h == 1) tc_commit(&b_pv[t]);
           // P came out of S, so K of this tile is done with
-          if (h == 0 && last_user(t, j)) mbar_arrive(&b_empty[pos_k<SB>(j) % NS]);
+          if (h == 0) mbar_arrive(&b_empty[pos_k<SB>(j) % NS]);
         }
         __syncwarp();
       }
       return true;
     };
     // O of tile j is there: its V is done with
-    auto pv_done = [&](int t, int j) {
+    auto pv_done = [&](int j) {
       if (!wait(&b_pv[t], j)) return false;
-      if (leader && last_user(t, j)) mbar_arrive(&b_empty[pos_v<SB>(j, n) % NS]);
+      if (leader) mbar_arrive(&b_empty[pos_v<SB>(j, n) % NS]);
       __syncwarp();
       return true;
     };
     bool ok = true;
-#pragma unroll
-    for (int t = 0; t < NT; ++t)
-      if (ok && mine[t] > 0) ok = wait(&b_q[t], 0) && s_mma(t, 0);
-    for (int j = 0; ok && j < n; ++j) {
-#pragma unroll
-      for (int t = 0; t < NT; ++t) {
-        if (!ok || j >= mine[t]) continue;
-        // with two S buffers the other one holds P of tile j - 1, with one S overwrites P of tile j
-        if (SB == 2 && j + 1 < mine[t]) ok = (j == 0 || pv_done(t, j - 1)) && s_mma(t, j + 1);
-        if (ok) ok = pv_mma(t, j);
-        if (SB == 1 && ok && j + 1 < mine[t]) ok = pv_done(t, j) && s_mma(t, j + 1);
-      }
+    if (mine > 0) {
+      ok = wait(&b_q[t], 0);
+      if (ok && t == 1 && n_tile[0] > j0) ok = wait(&b_s[0], 0);
+      if (ok) ok = s_mma(0);
+    }
+    for (int j = 0; ok && j < mine; ++j) {
+      // with two S buffers the other one holds P of tile j - 1, with one S overwrites P of tile j
+      if (SB == 2 && j > 0) ok = pv_done(j - 1);
+      if (SB == 2 && ok && j + 1 < mine) ok = s_mma(j + 1);
+      if (ok) ok = pv_mma(j);
+      if (SB == 1 && ok) ok = pv_done(j);
+      if (SB == 1 && ok && j + 1 < mine) ok = s_mma(j + 1);
+    }
+    for (int j = mine; ok && j < n; ++j) {                  // the other tile's keys: hand the slots on
+      const int pk = pos_k<SB>(j), pv = pos_v<SB>(j, n);
+      ok = wait(&b_full[pk % NS], pk / NS);
+      if (ok && leader) mbar_arrive(&b_empty[pk % NS]);
+      __syncwarp();
+      if (ok) ok = wait(&b_full[pv % NS], pv / NS);
+      if (ok && leader) mbar_arrive(&b_empty[pv % NS]);
+      __syncwarp();
     }
     if (!ok) {
       give_up();
       // what was issued finishes before TMEM goes (bounded)
-      if (leader) tc_commit(&b_fin);
-      mbar_wait_bounded(&b_fin, 0, kWaitLimitNs);
+      if (leader) tc_commit(&b_fin[t]);
+      mbar_wait_bounded(&b_fin[t], 0, kWaitLimitNs);
     }
   }
   } else {
