@@ -214,17 +214,14 @@ def load(build_if_missing: bool = True) -> ctypes.CDLL:
     lib.swa_flash_workspace_size.argtypes = [ctypes.POINTER(FlashArgs)]
     lib.swa_rotary_turns.restype = ctypes.c_int
     lib.swa_rotary_turns.argtypes = [ctypes.POINTER(RotarySchedule), ctypes.c_void_p, ctypes.c_void_p]
-    for name, args in (("swa_rotary", RotaryArgs), ("swa_paged_append", PagedAppendArgs),
-                       ("swa_paged_attend", PagedAttendArgs), ("swa_paged_weigh", PagedWeighArgs),
-                       ("swa_paged_evict", PagedEvictArgs)):
+    for name in ("swa_rotary", "swa_paged_append", "swa_paged_attend", "swa_paged_weigh", "swa_paged_evict"):
         fn = getattr(lib, name)
         fn.restype = ctypes.c_int
-        fn.argtypes = [ctypes.POINTER(args), ctypes.c_void_p]
-    for name, args in (("swa_paged_attend_workspace_size", PagedAttendArgs),
-                       ("swa_paged_evict_workspace_size", PagedEvictArgs)):
+        fn.argtypes = [ctypes.c_void_p, ctypes.c_void_p]   # a packed struct (bytes) or byref of one
+    for name in ("swa_paged_attend_workspace_size", "swa_paged_evict_workspace_size"):
         fn = getattr(lib, name)
         fn.restype = ctypes.c_size_t
-        fn.argtypes = [ctypes.POINTER(args)]
+        fn.argtypes = [ctypes.c_void_p]
     _lib = lib
     return lib
 

@@ -146,7 +146,7 @@ __global__ void __launch_bounds__(kWThreads) paged_weigh_kernel(const PagedWeigh
 template <typename T, int D>
 static int launch_weigh(const PagedWeighParams& p, cudaStream_t s) {
   constexpr int smem = (kWKeys + 2 * kWVecs) * D * 2;
-  cudaError_t e = cudaFuncSetAttribute(paged_weigh_kernel<T, D>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  cudaError_t e = allow_smem<paged_weigh_kernel<T, D>>(smem);
   if (e != cudaSuccess) return cuda_status(e);
   const dim3 grid((unsigned)((p.map.cap + kWKeys - 1) / kWKeys), (unsigned)p.map.nk, (unsigned)p.map.B);
   return finish_launch(launch_pdl(paged_weigh_kernel<T, D>, grid, dim3(kWThreads), smem, s, p));

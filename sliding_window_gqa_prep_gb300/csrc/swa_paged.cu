@@ -90,7 +90,17 @@ __global__ void __launch_bounds__(kThreads) paged_split_kernel(const PagedAttend
 
   // --- this CTA's share of all tiles: a scan over the sequences
   uint32_t bits = 0;
-  {
+  if (p.whole) {
+    if (tid == 0) {
+      const int b = blockIdx.x / p.map.nk;
+      const int n = split_tiles(paged_seq(p.map, b, p.T, p.max_rows, bits), p);
+      if (bits) set_err(p.err, bits);
+      s_b = n > 0 ? b : -1;
+      s_off = (long long)(blockIdx.x % p.map.nk) * n;
+      s_total = n;
+    }
+    __syncthreads();
+  } else {
     const int E = (p.map.B + kThreads - 1) / kThreads;
     long long mine = 0;
     for (int e = 0; e < E; ++e) {
@@ -137,18 +147,16 @@ __global__ void __launch_bounds__(kThreads) paged_split_kernel(const PagedAttend
   const long long total = s_total;
   long long per = (total + gridDim.x - 1) / gridDim.x;
   if (per < kMinTiles) per = kMinTiles;
-  const long long u0 = per * blockIdx.x;
-  if (s_b < 0) {
-    if (tid == 0) p.ws_desc[blockIdx.x] = make_int4(-1, 0, 0, 0);
-    return;
-  }
+  if (p.whole) per = total;
+  const long long u0 = p.whole ? 0 : per * blockIdx.x;
+  if (tid == 0 && !p.whole) p.ws_desc[blockIdx.x] = make_int4(-1, 0, 0, 0);
+  if (s_b < 0) return;
   long long left = min(per, total - u0);
   int b = s_b;
   uint32_t ignore = 0;
   PagedSeq s = paged_seq(p.map, b, p.T, p.max_rows, ignore);
   int n_tiles = split_tiles(s, p);
   int tile0 = (int)(s_off % n_tiles), g = (int)(s_off / n_tiles);
-  if (tid == 0) p.ws_desc[blockIdx.x] = make_int4(-1, 0, 0, 0);
 
   const int rg = warp / KG, kg = warp % KG;
   const int hpg = p.hpg, page_mask = (1 << p.map.page_shift) - 1;
@@ -437,8 +445,12 @@ __global__ void __launch_bounds__(kMergeThreads) paged_merge_kernel(const PagedA
 // to the tensor-core kernel (swa_paged_chunk.cu).
 constexpr int kSplitVecs = 64;
 
+// Keys of a sequence up to which a CTA takes a (sequence, KV head) whole: no scan over the
+// sequences and no second kernel.
+constexpr int kWholeKeys = 512;
+
 struct SplitPlan {
-  int rows, grid;                 // query vectors of a block (16, 32 or 64; 0: no sequence for this kernel), CTAs
+  int rows, whole, grid;                 // query vectors of a block (16, 32 or 64; 0: no sequence for this kernel), CTAs
   size_t off_ml, off_desc, bytes;
 };
 
@@ -450,7 +462,7 @@ static int split_occupancy() {
   if (!cache[dev]) {
     auto k = paged_split_kernel<T, D, ROWS>;
     int n = 0;
-    if (cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, SplitCfg<D>::SMEM) != cudaSuccess ||
+    if (allow_smem<paged_split_kernel<T, D, ROWS>>(SplitCfg<D>::SMEM) != cudaSuccess ||
         cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, k, kThreads, SplitCfg<D>::SMEM) != cudaSuccess || n < 1) {
       (void)cudaGetLastError();
       n = 1;
@@ -462,11 +474,10 @@ static int split_occupancy() {
 
 template <typename T, int D, int ROWS>
 static int launch_split(const PagedAttendParams& p, const SplitPlan& sp, cudaStream_t s) {
-  const cudaError_t e = cudaFuncSetAttribute(paged_split_kernel<T, D, ROWS>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                             SplitCfg<D>::SMEM);
+  const cudaError_t e = allow_smem<paged_split_kernel<T, D, ROWS>>(SplitCfg<D>::SMEM);
   if (e != cudaSuccess) return cuda_status(e);
   const int rc = finish_launch(launch_pdl(paged_split_kernel<T, D, ROWS>, dim3(sp.grid), dim3(kThreads), SplitCfg<D>::SMEM, s, p));
-  if (rc != SWA_OK) return rc;
+  if (rc != SWA_OK || p.whole) return rc;
   const long long vecs = (long long)p.max_rows * p.hpg;
   return finish_launch(launch_pdl(paged_merge_kernel<T, D>, dim3(sp.grid, (unsigned)(vecs < p.most ? vecs : p.most)),
                                   dim3(kMergeThreads), 0, s, p, ROWS));
@@ -501,14 +512,17 @@ static void attend_plan(const swa_paged_attend_args* a, PagedPlan* pl) {
   pl->has_chunk = vecs > kSplitVecs;
   if (!pl->has_chunk || (long long)a->cache.B * a->max_rows > a->T) {
     sp.rows = vecs <= 16 ? 16 : vecs <= 32 ? 32 : 64;
-    const int occ = by_type(a->cache.dtype, a->cache.hd, sp.rows, [](auto* t, auto d, auto r) {
+    sp.whole = (long long)a->cache.max_pages * a->cache.page <= kWholeKeys;
+    const int occ = sp.whole ? 0 : by_type(a->cache.dtype, a->cache.hd, sp.rows, [](auto* t, auto d, auto r) {
       return split_occupancy<std::remove_pointer_t<decltype(t)>, decltype(d)::value, decltype(r)::value>();
     });
-    sp.grid = (num_sms() > 0 ? num_sms() : 148) * occ;
-    const size_t recs = (size_t)sp.grid * 2 * sp.rows;
-    sp.off_ml = up256s(recs * a->cache.hd * sizeof(float));
-    sp.off_desc = sp.off_ml + up256s(recs * sizeof(float2));
-    sp.bytes = sp.off_desc + up256s((size_t)sp.grid * sizeof(int4));
+    sp.grid = sp.whole ? a->cache.B * a->cache.nk : (num_sms() > 0 ? num_sms() : 148) * occ;
+    if (!sp.whole) {
+      const size_t recs = (size_t)sp.grid * 2 * sp.rows;
+      sp.off_ml = up256s(recs * a->cache.hd * sizeof(float));
+      sp.off_desc = sp.off_ml + up256s(recs * sizeof(float2));
+      sp.bytes = sp.off_desc + up256s((size_t)sp.grid * sizeof(int4));
+    }
   }
   pl->off_chunk = sp.bytes;
   pl->bytes = sp.bytes;
@@ -568,6 +582,7 @@ int swa_paged_attend(const swa_paged_attend_args* a, cudaStream_t stream) {
   cudaError_t e;
   if (a->ev_start && (e = cudaEventRecord(a->ev_start, stream)) != cudaSuccess) return cuda_status(e);
   if (pl.split.rows) {
+    p.whole = pl.split.whole;
     p.ws_acc = reinterpret_cast<float*>(ws);
     p.ws_ml = reinterpret_cast<float2*>(ws + pl.split.off_ml);
     p.ws_desc = reinterpret_cast<int4*>(ws + pl.split.off_desc);

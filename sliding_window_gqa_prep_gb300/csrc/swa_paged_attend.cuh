@@ -13,6 +13,7 @@ using Int = std::integral_constant<int, N>;
 struct PagedAttendParams {
   PagedMap map;
   int T, nh, hpg, max_rows;
+  int whole;                   // split kernel: a CTA per (sequence, KV head), nothing to merge
   int most;                    // split kernel: sequences with more query vectors are not its
   float qmul;                  // scale * log2(e): scores in log2 units
   const void* q;
@@ -50,6 +51,20 @@ struct ChunkPlan {
 ChunkPlan chunk_plan(const swa_paged_attend_args* a);
 int launch_paged_chunk(const swa_paged_attend_args* a, const PagedAttendParams& p, const ChunkPlan& plan, int small,
                        char* ws, cudaStream_t s);
+
+// Dynamic shared memory of a kernel, allowed once per device (an attribute call costs as
+// much host time as the rest of a launch's preparation).
+template <auto Kernel>
+cudaError_t allow_smem(int bytes) {
+  static bool done[64] = {};
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  if (dev >= 0 && dev < 64 && done[dev]) return cudaSuccess;
+  e = cudaFuncSetAttribute(Kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+  if (e == cudaSuccess && dev >= 0 && dev < 64) done[dev] = true;
+  return e;
+}
 
 #ifdef __CUDACC__
 // Features [f, f + 8) of a finished row: out = acc / l, and its lse (the weights in l

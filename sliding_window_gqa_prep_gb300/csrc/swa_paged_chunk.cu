@@ -682,7 +682,7 @@ static int launch(const swa_paged_attend_args* a, const PagedAttendParams& ap, c
   p.rec_acc = reinterpret_cast<float*>(ws);
   p.rec_ml = reinterpret_cast<float2*>(ws + pl.off_ml);
   p.rec_desc = reinterpret_cast<int4*>(ws + pl.off_desc);
-  const cudaError_t e = cudaFuncSetAttribute(paged_chunk_kernel<T, D>, cudaFuncAttributeMaxDynamicSharedMemorySize, ChunkCfg<D>::SMEM);
+  const cudaError_t e = allow_smem<paged_chunk_kernel<T, D>>(ChunkCfg<D>::SMEM);
   if (e != cudaSuccess) return cuda_status(e);
   rc = finish_launch(launch_pdl(paged_chunk_kernel<T, D>, dim3((unsigned)pl.items, pl.splits), dim3(ChunkCfg<D>::THREADS),
                                 ChunkCfg<D>::SMEM, s, mk, mv, p));

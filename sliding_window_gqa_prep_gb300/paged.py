@@ -14,9 +14,10 @@ and workspaces that the caller does not pass are allocated too.
 """
 from __future__ import annotations
 
-import contextlib
 import ctypes
-from typing import Optional, Tuple
+import functools
+import struct
+from typing import Tuple
 
 import torch
 
@@ -27,48 +28,71 @@ __all__ = ["rotary_freqs", "rotary_turns", "rotary", "paged_append", "paged_atte
 
 _TYPES = {torch.float32: _abi.SWA_F32, torch.bfloat16: _abi.SWA_BF16, torch.float16: _abi.SWA_F16}
 _KINDS = {"plain": 0, "linear": 1, "base": 2, "parts": 3}
-_I32, _F32 = torch.int32, torch.float32
+_I32, _I64, _F32, _U8 = torch.int32, torch.int64, torch.float32, torch.uint8
+
+# The argument structs of include/swa.h as struct formats (native alignment): one pack
+# call costs a decode step less host time than setting a ctypes field at a time.
+_CACHE = "7i5P"                                        # swa_paged_cache
+_ROTARY = struct.Struct("@7ifP2qP2q2P")                # swa_rotary_args
+_APPEND = struct.Struct("@" + _CACHE + "5if3P3q6P")    # swa_paged_append_args
+_ATTEND = struct.Struct("@" + _CACHE + "4ifPq3PN3P")   # swa_paged_attend_args
+_WEIGH = struct.Struct("@" + _CACHE + "3ifPq4P")       # swa_paged_weigh_args
+_EVICT = struct.Struct("@" + _CACHE + "2i7PNP")        # swa_paged_evict_args
 
 
-def _arg(x, name, dev, shape=None, dtype=None, dense=True) -> int:
-    """Device address of a checked tensor."""
+def _complain(x, name, dev, dtype, shape):
     if not isinstance(x, torch.Tensor) or not x.is_cuda:
         raise ValueError(f"{name} must be a CUDA tensor")
-    if x.device != dev:
-        raise ValueError(f"{name} is on {x.device}, expected {dev}")
-    if dtype is not None and x.dtype != dtype:
+    if x.get_device() != dev:
+        raise ValueError(f"{name} is on {x.device}, expected cuda:{dev}")
+    if x.dtype != dtype:
         raise ValueError(f"{name} must be {dtype}, got {x.dtype}")
-    if shape is not None and tuple(x.shape) != shape:
-        raise ValueError(f"{name} has shape {tuple(x.shape)}, expected {shape}")
-    if dense and not x.is_contiguous():
-        raise ValueError(f"{name} must be contiguous")
+    if shape is not None and tuple(x.shape) != tuple(shape):
+        raise ValueError(f"{name} has shape {tuple(x.shape)}, expected {tuple(shape)}")
+    raise ValueError(f"{name} must be contiguous")
+
+
+def _arg(x, name, dev, dtype, shape=None) -> int:
+    """Device address of a checked dense tensor."""
+    if (not isinstance(x, torch.Tensor) or x.get_device() != dev or x.dtype != dtype
+            or (shape is not None and x.shape != shape) or not x.is_contiguous()):
+        _complain(x, name, dev, dtype, shape)
     return x.data_ptr()
 
 
-def _opt(x, name, dev, shape=None, dtype=None) -> int:
-    return 0 if x is None else _arg(x, name, dev, shape, dtype)
+def _opt(x, name, dev, dtype, shape=None) -> int:
+    return 0 if x is None else _arg(x, name, dev, dtype, shape)
 
 
-def _rows(x, name, dev, dtype) -> Tuple[int, int]:
+def _rows(x, name, dev, dtype, shape) -> Tuple[int, int]:
     """Address and row stride of packed rows [T][heads][hd] with dense heads."""
-    ptr = _arg(x, name, dev, dtype=dtype, dense=False)
-    T, H, hd = x.shape
-    if (x.stride(2) != 1 and hd > 1) or (x.stride(1) != hd and H > 1):
+    if not isinstance(x, torch.Tensor) or x.get_device() != dev or x.dtype != dtype or x.shape != shape:
+        _complain(x, name, dev, dtype, shape)
+    T, H, hd = shape
+    row, head, one = x.stride()
+    if one != 1 or (head != hd and H > 1):
         raise ValueError(f"{name}: the heads of a row must be dense")
-    return ptr, (x.stride(0) if T > 1 else H * hd)
+    return x.data_ptr(), (row if T > 1 else H * hd)
 
 
-@contextlib.contextmanager
-def _place(dev, stream):
-    """The call's device and stream as the current ones; yields the stream's handle."""
-    if stream is not None and stream.device != dev:
-        raise ValueError(f"stream is on {stream.device}, the tensors are on {dev}")
-    with torch.cuda.device(dev), torch.cuda.stream(stream):
-        yield torch.cuda.current_stream(dev).cuda_stream
+def _placed(fn):
+    """Runs a call on the device of its first tensor and on `stream`: as it is when that is
+    the current device and its current stream, inside both contexts otherwise."""
+    @functools.wraps(fn)
+    def call(first, *args, stream=None, **kw):
+        if not isinstance(first, torch.Tensor) or not first.is_cuda:
+            raise ValueError("expected CUDA tensors")
+        dev = first.get_device()
+        if stream is None and torch._C._cuda_getDevice() == dev:
+            return fn(first, *args, dev=dev, stream=torch._C._cuda_getCurrentRawStream(dev), **kw)
+        if stream is not None and stream.device.index != dev:
+            raise ValueError(f"stream is on {stream.device}, the tensors are on cuda:{dev}")
+        with torch.cuda.device(dev), torch.cuda.stream(stream):
+            return fn(first, *args, dev=dev, stream=torch._C._cuda_getCurrentRawStream(dev), **kw)
+    return call
 
 
-def _lib():
-    return _abi.load()
+_lib = _abi.load
 
 
 def _schedule(rot, theta, schedule, factor, orig_len, low, high):
@@ -100,8 +124,9 @@ def rotary_turns(rot, theta=10000.0, *, schedule="plain", factor=1.0, orig_len=0
     return torch.tensor([v - (1 << 64) if v >> 63 else v for v in t], dtype=torch.int64).to(device)
 
 
+@_placed
 def rotary(x, pos, turns, *, interleaved: bool = False, inverse: bool = False, mag: float = 1.0, out=None,
-           stream=None):
+           dev=None, stream=None):
     """Rotary positions of packed rows x [T][H][hd] (f32, bf16 or f16; any row and head
     strides at multiples of 16 bytes): the first 2 * len(turns) features of every head turn
     by pos[row], the others are copied. inverse=True is the gradient of the call. out may
@@ -109,202 +134,179 @@ def rotary(x, pos, turns, *, interleaved: bool = False, inverse: bool = False, m
     if x.dim() != 3 or x.dtype not in _TYPES:
         raise ValueError("x must be [T][H][hd] in float32, bfloat16 or float16")
     T, H, hd = x.shape
-    dev = x.device
-    with _place(dev, stream) as handle:
-        if out is None:
-            out = torch.empty(T, H, hd, device=dev, dtype=x.dtype)
-        a = _abi.RotaryArgs()
-        a.x, a.out = _arg(x, "x", dev, dense=False), _arg(out, "out", dev, (T, H, hd), x.dtype, dense=False)
-        for y, name in ((x, "x"), (out, "out")):
-            if hd > 1 and y.stride(2) != 1:
-                raise ValueError(f"{name}: the features of a head must be dense")
-        a.T, a.H, a.hd, a.rot, a.dtype = T, H, hd, 2 * turns.numel(), _TYPES[x.dtype]
-        # a stride along a dimension of one is free: the dense one then
-        a.x_head, a.out_head = (x.stride(1), out.stride(1)) if H > 1 else (hd, hd)
-        a.x_row, a.out_row = (x.stride(0), out.stride(0)) if T > 1 else (H * a.x_head, H * a.out_head)
-        a.interleaved, a.inverse, a.mag = int(interleaved), int(inverse), float(mag)
-        a.pos = _arg(pos, "pos", dev, (T,), _I32)
-        a.turns = _arg(turns, "turns", dev, (turns.numel(),), torch.int64)
-        _abi.check(_lib().swa_rotary(ctypes.byref(a), handle), "swa_rotary")
+    if out is None:
+        out = torch.empty(T, H, hd, device=x.device, dtype=x.dtype)
+    elif out.get_device() != dev or out.dtype != x.dtype or out.shape != x.shape:
+        _complain(out, "out", dev, x.dtype, x.shape)
+    x_row, x_head, x_one = x.stride()
+    o_row, o_head, o_one = out.stride()
+    if (x_one != 1 or o_one != 1) and hd > 1:
+        raise ValueError("x and out: the features of a head must be dense")
+    # a stride along a dimension of one is free: the dense one then
+    if H <= 1:
+        x_head = o_head = hd
+    if T <= 1:
+        x_row, o_row = H * x_head, H * o_head
+    n = turns.numel()
+    a = _ROTARY.pack(T, H, hd, 2 * n, _TYPES[x.dtype], bool(interleaved), bool(inverse), mag,
+                     x.data_ptr(), x_row, x_head, out.data_ptr(), o_row, o_head,
+                     _arg(pos, "pos", dev, _I32, (T,)), _arg(turns, "turns", dev, _I64, (n,)))
+    _abi.check(_lib().swa_rotary(a, stream), "swa_rotary")
     return out
 
 
-def _cache(c, cache_k, cache_v, page_table, row_start, lens, dev) -> None:
+def _cache(cache_k, cache_v, page_table, row_start, lens, dev):
+    """The fields of a swa_paged_cache and the capacity of a sequence."""
     if cache_k.dim() != 4 or cache_k.dtype not in (torch.bfloat16, torch.float16):
         raise ValueError("cache_k must be [num_pages][nk][page][hd] in bfloat16 or float16")
     if page_table.dim() != 2:
         raise ValueError("page_table must be [B][max_pages]")
-    B = page_table.shape[0]
-    c.k = _arg(cache_k, "cache_k", dev)
-    c.v = c.k if cache_v is None else _arg(cache_v, "cache_v", dev, tuple(cache_k.shape), cache_k.dtype)
-    c.num_pages, c.nk, c.page, c.hd = cache_k.shape
-    c.B, c.max_pages, c.dtype = B, page_table.shape[1], _TYPES[cache_k.dtype]
-    c.table = _arg(page_table, "page_table", dev, dtype=_I32)
-    c.row_start = _opt(row_start, "row_start", dev, (B + 1,), _I32)
-    c.lens = _arg(lens, "lens", dev, (B,), _I32)
+    num_pages, nk, page, hd = cache_k.shape
+    B, max_pages = page_table.shape
+    k = _arg(cache_k, "cache_k", dev, cache_k.dtype)
+    v = k if cache_v is None else _arg(cache_v, "cache_v", dev, cache_k.dtype, cache_k.shape)
+    return (B, nk, hd, page, num_pages, max_pages, _TYPES[cache_k.dtype], k, v,
+            _arg(page_table, "page_table", dev, _I32), _opt(row_start, "row_start", dev, _I32, (B + 1,)),
+            _arg(lens, "lens", dev, _I32, (B,))), max_pages * page
 
 
+@_placed
 def paged_append(k, v, pos, cache_k, cache_v, page_table, row_start, lens, *, q=None, q_out=None, turns=None,
-                 interleaved: bool = False, mag: float = 1.0, slot_pos=None, weight=None, err=None, stream=None):
+                 interleaved: bool = False, mag: float = 1.0, slot_pos=None, weight=None, err=None, dev=None,
+                 stream=None):
     """A chunk's rows enter the cache: k [T][nk][hd] rotated by pos (when turns is given) and
     v, rounded to the cache's type, go to the slots lens[b] - t_b + i of their sequence;
     lens counts the chunk's rows. q [T][nh][hd] is rotated and rounded into q_out, which is
     returned (None without q). slot_pos and weight [B][nk][cap], when given, get the new
     slots' positions and weight 0."""
-    dev = cache_k.device
-    with _place(dev, stream) as handle:
-        a = _abi.PagedAppendArgs()
-        _cache(a.cache, cache_k, cache_v, page_table, row_start, lens, dev)
-        if row_start is None:
-            raise ValueError("row_start is required")
-        nk, hd, cap = a.cache.nk, a.cache.hd, a.cache.max_pages * a.cache.page
-        if k.dtype not in _TYPES:
-            raise ValueError("k must be float32, bfloat16 or float16")
-        T = k.shape[0]
-        if tuple(k.shape) != (T, nk, hd) or tuple(v.shape) != (T, nk, hd):
-            raise ValueError(f"k and v must be [T][{nk}][{hd}]")
-        a.T, a.src, a.interleaved, a.mag = T, _TYPES[k.dtype], int(interleaved), float(mag)
-        a.k, a.k_row = _rows(k, "k", dev, k.dtype)
-        a.v, a.v_row = _rows(v, "v", dev, k.dtype)
-        if q is not None:
-            if q.dim() != 3 or q.shape[0] != T or q.shape[2] != hd:
-                raise ValueError(f"q must be [{T}][nh][{hd}]")
-            a.nh = q.shape[1]
-            a.q, a.q_row = _rows(q, "q", dev, k.dtype)
-            if q_out is None:
-                q_out = torch.empty(T, a.nh, hd, device=dev, dtype=cache_k.dtype)
-            a.q_out = _arg(q_out, "q_out", dev, (T, a.nh, hd), cache_k.dtype)
-        elif q_out is not None:
-            raise ValueError("q_out without q")
-        a.pos = _opt(pos, "pos", dev, (T,), _I32)
-        if turns is not None:
-            a.turns, a.rot = _arg(turns, "turns", dev, (turns.numel(),), torch.int64), 2 * turns.numel()
-        a.slot_pos = _opt(slot_pos, "slot_pos", dev, (a.cache.B, nk, cap), _I32)
-        a.weight = _opt(weight, "weight", dev, (a.cache.B, nk, cap), _F32)
-        a.err = _opt(err, "err", dev, (1,), _I32)
-        _abi.check(_lib().swa_paged_append(ctypes.byref(a), handle), "swa_paged_append")
+    cache, cap = _cache(cache_k, cache_v, page_table, row_start, lens, dev)
+    B, nk, hd = cache[:3]
+    if row_start is None:
+        raise ValueError("row_start is required")
+    if k.dtype not in _TYPES:
+        raise ValueError("k must be float32, bfloat16 or float16")
+    T = k.shape[0]
+    kp, k_row = _rows(k, "k", dev, k.dtype, (T, nk, hd))
+    vp, v_row = _rows(v, "v", dev, k.dtype, (T, nk, hd))
+    nh = qp = q_row = qo = 0
+    if q is not None:
+        if q.dim() != 3:
+            raise ValueError(f"q must be [{T}][nh][{hd}]")
+        nh = q.shape[1]
+        qp, q_row = _rows(q, "q", dev, k.dtype, (T, nh, hd))
+        if q_out is None:
+            q_out = torch.empty(T, nh, hd, device=q.device, dtype=cache_k.dtype)
+        qo = _arg(q_out, "q_out", dev, cache_k.dtype, (T, nh, hd))
+    elif q_out is not None:
+        raise ValueError("q_out without q")
+    n = 0 if turns is None else turns.numel()
+    a = _APPEND.pack(*cache, T, nh, 2 * n, _TYPES[k.dtype], bool(interleaved), mag, qp, kp, vp, q_row, k_row, v_row,
+                     qo, _opt(pos, "pos", dev, _I32, (T,)), _opt(turns, "turns", dev, _I64, (n,)),
+                     _opt(slot_pos, "slot_pos", dev, _I32, (B, nk, cap)), _opt(weight, "weight", dev, _F32, (B, nk, cap)),
+                     _opt(err, "err", dev, _I32, (1,)))
+    _abi.check(_lib().swa_paged_append(a, stream), "swa_paged_append")
     return q_out
-
-
-def _sizes(a, B, T, nh, nk, hd, page, max_pages, max_rows, dtype):
-    c = a.cache
-    c.B, c.nk, c.hd, c.page, c.max_pages, c.dtype = B, nk, hd, page, max_pages, _TYPES[dtype]
-    a.T, a.nh, a.max_rows = T, nh, max_rows
 
 
 def paged_attend_workspace_size(B, T, nh, nk, hd, page, max_pages, max_rows, dtype=torch.bfloat16) -> int:
     """Workspace bytes of paged_attend on the current device."""
-    a = _abi.PagedAttendArgs()
-    _sizes(a, B, T, nh, nk, hd, page, max_pages, max_rows, dtype)
-    n = int(_lib().swa_paged_attend_workspace_size(ctypes.byref(a)))
+    a = _ATTEND.pack(B, nk, hd, page, 0, max_pages, _TYPES[dtype], 0, 0, 0, 0, 0, T, nh, max_rows, 0, 0.0, 0, 0, 0, 0,
+                     0, 0, 0, 0, 0)
+    n = int(_lib().swa_paged_attend_workspace_size(a))
     if n == 0:
         raise _abi.SwaError(_abi.SWA_E_SHAPE, "swa_paged_attend_workspace_size")
     return n
 
 
+@_placed
 def paged_attend(q, cache_k, cache_v, page_table, row_start, lens, scale: float, *, max_rows: int, out=None,
-                 lse=None, workspace=None, err=None, ev_start=None, ev_stop=None, stream=None):
+                 lse=None, workspace=None, err=None, ev_start=None, ev_stop=None, dev=None, stream=None):
     """Causal attention of a chunk's rows q [T][nh][hd] (the cache's type) over the paged
     cache, their own keys already appended: row i of sequence b sees the slots below
     lens[b] - t_b + i + 1. max_rows bounds the rows of a sequence. out [T][nh][hd] in the
     cache's type or float32; lse [T][nh] f32, when given, gets log sum exp of the scores.
     Rows of no sequence are left as they were (zeros in a new out)."""
-    dev = q.device
-    with _place(dev, stream) as handle:
-        a = _abi.PagedAttendArgs()
-        _cache(a.cache, cache_k, cache_v, page_table, row_start, lens, dev)
-        if row_start is None:
-            raise ValueError("row_start is required")
-        if q.dim() != 3 or q.shape[2] != a.cache.hd:
-            raise ValueError(f"q must be [T][nh][{a.cache.hd}]")
-        T, nh, hd = q.shape
-        a.T, a.nh, a.max_rows, a.scale = T, nh, int(max_rows), float(scale)
-        a.q, a.q_row = _rows(q, "q", dev, cache_k.dtype)
-        if out is None:
-            out = torch.zeros(T, nh, hd, device=dev, dtype=q.dtype)
-        if out.dtype not in (q.dtype, _F32):
-            raise ValueError(f"out must be {q.dtype} or float32")
-        a.out, a.out_f32 = _arg(out, "out", dev, (T, nh, hd)), int(out.dtype == _F32)
-        a.lse = _opt(lse, "lse", dev, (T, nh), _F32)
-        if workspace is None:
-            need = int(_lib().swa_paged_attend_workspace_size(ctypes.byref(a)))
-            workspace = torch.empty(max(need, 1), device=dev, dtype=torch.uint8)
-        a.workspace, a.workspace_bytes = _arg(workspace, "workspace", dev, dtype=torch.uint8), workspace.numel()
-        a.err = _opt(err, "err", dev, (1,), _I32)
-        a.ev_start = ev_start.cuda_event if ev_start is not None else None
-        a.ev_stop = ev_stop.cuda_event if ev_stop is not None else None
-        _abi.check(_lib().swa_paged_attend(ctypes.byref(a), handle), "swa_paged_attend")
+    cache, _ = _cache(cache_k, cache_v, page_table, row_start, lens, dev)
+    B, nk, hd, page, _, max_pages = cache[:6]
+    if row_start is None:
+        raise ValueError("row_start is required")
+    if q.dim() != 3:
+        raise ValueError(f"q must be [T][nh][{hd}]")
+    T, nh = q.shape[:2]
+    qp, q_row = _rows(q, "q", dev, cache_k.dtype, (T, nh, hd))
+    if out is None:
+        out = torch.zeros(T, nh, hd, device=q.device, dtype=q.dtype)
+    wide = out.dtype == _F32
+    op = _arg(out, "out", dev, _F32 if wide else q.dtype, (T, nh, hd))
+    if workspace is None:
+        need = _lib().swa_paged_attend_workspace_size(
+            _ATTEND.pack(*cache, T, nh, max_rows, wide, scale, 0, 0, 0, 0, 0, 0, 0, 0, 0))
+        workspace = torch.empty(max(need, 1), device=q.device, dtype=_U8)
+    a = _ATTEND.pack(*cache, T, nh, max_rows, wide, scale, qp, q_row, op, _opt(lse, "lse", dev, _F32, (T, nh)),
+                     _arg(workspace, "workspace", dev, _U8), workspace.numel(), _opt(err, "err", dev, _I32, (1,)),
+                     ev_start.cuda_event if ev_start is not None else 0, ev_stop.cuda_event if ev_stop is not None else 0)
+    _abi.check(_lib().swa_paged_attend(a, stream), "swa_paged_attend")
     return out
 
 
+@_placed
 def paged_weigh(q, lse, cache_k, page_table, row_start, lens, scale: float, *, max_rows: int, weight=None, out=None,
-                err=None, stream=None):
+                err=None, dev=None, stream=None):
     """The attention weight every cached key received from the rows q, added to weight
     [B][nk][cap] (None: zeros): out[b][g][j] = weight[b][g][j] + sum over rows that see slot j
     and heads of g of exp(scale <q, k_j> - lse). lse [T][nh] is paged_attend's for the same
     rows. out may be weight; entries from lens[b] on are left as they were (zeros in a new
     out)."""
-    dev = q.device
-    with _place(dev, stream) as handle:
-        a = _abi.PagedWeighArgs()
-        _cache(a.cache, cache_k, None, page_table, row_start, lens, dev)
-        if row_start is None:
-            raise ValueError("row_start is required")
-        if q.dim() != 3 or q.shape[2] != a.cache.hd:
-            raise ValueError(f"q must be [T][nh][{a.cache.hd}]")
-        T, nh, _ = q.shape
-        shape = (a.cache.B, a.cache.nk, a.cache.max_pages * a.cache.page)
-        a.T, a.nh, a.max_rows, a.scale = T, nh, int(max_rows), float(scale)
-        a.q, a.q_row = _rows(q, "q", dev, cache_k.dtype)
-        a.lse = _arg(lse, "lse", dev, (T, nh), _F32)
-        a.weight = _opt(weight, "weight", dev, shape, _F32)
-        if out is None:
-            out = torch.zeros(shape, device=dev, dtype=_F32)
-        a.out = _arg(out, "out", dev, shape, _F32)
-        a.err = _opt(err, "err", dev, (1,), _I32)
-        _abi.check(_lib().swa_paged_weigh(ctypes.byref(a), handle), "swa_paged_weigh")
+    cache, cap = _cache(cache_k, None, page_table, row_start, lens, dev)
+    B, nk, hd = cache[:3]
+    if row_start is None:
+        raise ValueError("row_start is required")
+    if q.dim() != 3:
+        raise ValueError(f"q must be [T][nh][{hd}]")
+    T, nh = q.shape[:2]
+    qp, q_row = _rows(q, "q", dev, cache_k.dtype, (T, nh, hd))
+    if out is None:
+        out = torch.zeros(B, nk, cap, device=q.device, dtype=_F32)
+    a = _WEIGH.pack(*cache, T, nh, max_rows, scale, qp, q_row, _arg(lse, "lse", dev, _F32, (T, nh)),
+                    _opt(weight, "weight", dev, _F32, (B, nk, cap)), _arg(out, "out", dev, _F32, (B, nk, cap)),
+                    _opt(err, "err", dev, _I32, (1,)))
+    _abi.check(_lib().swa_paged_weigh(a, stream), "swa_paged_weigh")
     return out
 
 
 def paged_evict_workspace_size(B, nk, page, max_pages, keep) -> int:
     """Workspace bytes of paged_evict."""
-    a = _abi.PagedEvictArgs()
-    c = a.cache
-    c.B, c.nk, c.page, c.max_pages, a.keep = B, nk, page, max_pages, int(keep)
-    n = int(_lib().swa_paged_evict_workspace_size(ctypes.byref(a)))
+    a = _EVICT.pack(B, nk, 0, page, 0, max_pages, 0, 0, 0, 0, 0, 0, keep, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0)
+    n = int(_lib().swa_paged_evict_workspace_size(a))
     if n == 0:
         raise _abi.SwaError(_abi.SWA_E_SHAPE, "swa_paged_evict_workspace_size")
     return n
 
 
+@_placed
 def paged_evict(cache_k, cache_v, page_table, lens, weight, slot_pos, keep: int, *, recent_from=None, sinks: int = 0,
-                weight_out=None, slot_pos_out=None, lens_out=None, workspace=None, err=None, stream=None):
+                weight_out=None, slot_pos_out=None, lens_out=None, workspace=None, err=None, dev=None, stream=None):
     """Cut every sequence's cache to at most `keep` keys per KV head: those at positions
     below sinks or from recent_from[b] on first, then by weight. Kept keys behind the new
     length move into the freed slots (within the pages, in place); weight and slot_pos
     [B][nk][cap] are read, their new values and the new lengths written to the outputs.
     Returns (lens_out, weight_out, slot_pos_out)."""
-    dev = cache_k.device
-    with _place(dev, stream) as handle:
-        a = _abi.PagedEvictArgs()
-        _cache(a.cache, cache_k, cache_v, page_table, None, lens, dev)
-        B, shape = a.cache.B, (a.cache.B, a.cache.nk, a.cache.max_pages * a.cache.page)
-        a.keep, a.sinks = int(keep), int(sinks)
-        a.weight, a.slot_pos = _arg(weight, "weight", dev, shape, _F32), _arg(slot_pos, "slot_pos", dev, shape, _I32)
-        a.recent_from = _opt(recent_from, "recent_from", dev, (B,), _I32)
-        if weight_out is None:
-            weight_out = torch.zeros_like(weight)
-        if slot_pos_out is None:
-            slot_pos_out = torch.zeros_like(slot_pos)
-        if lens_out is None:
-            lens_out = torch.empty_like(lens)
-        a.weight_out = _arg(weight_out, "weight_out", dev, shape, _F32)
-        a.slot_pos_out = _arg(slot_pos_out, "slot_pos_out", dev, shape, _I32)
-        a.lens_out = _arg(lens_out, "lens_out", dev, (B,), _I32)
-        if workspace is None:
-            need = int(_lib().swa_paged_evict_workspace_size(ctypes.byref(a)))
-            workspace = torch.empty(max(need, 1), device=dev, dtype=torch.uint8)
-        a.workspace, a.workspace_bytes = _arg(workspace, "workspace", dev, dtype=torch.uint8), workspace.numel()
-        a.err = _opt(err, "err", dev, (1,), _I32)
-        _abi.check(_lib().swa_paged_evict(ctypes.byref(a), handle), "swa_paged_evict")
+    cache, cap = _cache(cache_k, cache_v, page_table, None, lens, dev)
+    B, nk = cache[:2]
+    shape = (B, nk, cap)
+    wp, pp = _arg(weight, "weight", dev, _F32, shape), _arg(slot_pos, "slot_pos", dev, _I32, shape)
+    if weight_out is None:
+        weight_out = torch.zeros_like(weight)
+    if slot_pos_out is None:
+        slot_pos_out = torch.zeros_like(slot_pos)
+    if lens_out is None:
+        lens_out = torch.empty_like(lens)
+    if workspace is None:
+        need = _lib().swa_paged_evict_workspace_size(_EVICT.pack(*cache, keep, sinks, 0, 0, 0, 0, 0, 0, 0, 0, 0))
+        workspace = torch.empty(max(need, 1), device=cache_k.device, dtype=_U8)
+    a = _EVICT.pack(*cache, keep, sinks, wp, pp, _opt(recent_from, "recent_from", dev, _I32, (B,)),
+                    _arg(weight_out, "weight_out", dev, _F32, shape), _arg(slot_pos_out, "slot_pos_out", dev, _I32, shape),
+                    _arg(lens_out, "lens_out", dev, _I32, (B,)), _arg(workspace, "workspace", dev, _U8),
+                    workspace.numel(), _opt(err, "err", dev, _I32, (1,)))
+    _abi.check(_lib().swa_paged_evict(a, stream), "swa_paged_evict")
     return lens_out, weight_out, slot_pos_out

@@ -290,6 +290,28 @@ def test_evict_refusals(lib):
     assert lib.swa_paged_evict_workspace_size(ctypes.byref(_evict(keep=0))) == 0
 
 
+def test_packed_structs_match_the_abi(lib):
+    """The binding packs the argument structs by format strings: the same sizes and field
+    offsets as the ctypes declarations."""
+    from sliding_window_gqa_prep_gb300 import paged
+    for fmt, cls in ((paged._ROTARY, _abi.RotaryArgs), (paged._APPEND, _abi.PagedAppendArgs),
+                     (paged._ATTEND, _abi.PagedAttendArgs), (paged._WEIGH, _abi.PagedWeighArgs),
+                     (paged._EVICT, _abi.PagedEvictArgs)):
+        assert fmt.size == ctypes.sizeof(cls)
+        fields = []
+        for name, kind in cls._fields_:
+            if kind is _abi.PagedCache:
+                fields += [(name, sub) for sub, _ in kind._fields_]
+            else:
+                fields.append((name, None))
+        values = [float(i + 1) if getattr(dict(cls._fields_)[f[0]], "_type_", "") == "f" else i + 1
+                  for i, f in enumerate(fields)]
+        a = cls.from_buffer_copy(fmt.pack(*values))
+        for (name, sub), want in zip(fields, values):
+            x = getattr(a, name)
+            assert (getattr(x, sub) if sub else x) == want, (cls, name, sub)
+
+
 def test_binding_wants_cuda_tensors():
     import torch
     x = torch.zeros(2, 3, 64)
