@@ -1,159 +1,10 @@
-// The weight each cached key received (swa_paged_weigh) and the eviction of keys by it
-// (swa_paged_evict).
-#include <cmath>
-
-#include "swa_mma16.cuh"
-#include "swa_paged_attend.cuh"
+// Eviction of cached keys by their accumulated weight (swa_paged_evict).
+#include "swa_paged.cuh"
 
 namespace swa {
 
 // ---------------------------------------------------------------------------
-// Weigh. w_j += sum over query vectors of 2^(qmul <q, k_j> - lse log2 e): with the
-// row's lse known every weight stands alone, so a CTA takes 64 keys of one KV head,
-// holds them as A operands (16 keys a warp) and streams the query vectors that see
-// them through shared memory as B operands; S has a key a row, and the sum over its
-// columns stays in registers until the end. K is read once; bound by that while a
-// sequence has few rows.
-// ---------------------------------------------------------------------------
-struct PagedWeighParams {
-  PagedMap map;
-  int T, nh, hpg, max_rows;
-  float qmul;
-  const void* q;
-  long long q_row;
-  const void* ck;
-  const float* lse;
-  const float* weight;
-  float* out;
-  uint32_t* err;
-};
-
-constexpr int kWThreads = 128;
-constexpr int kWKeys = 64;     // keys of a CTA
-constexpr int kWVecs = 32;     // query vectors of a tile
-
-template <typename T, int D>
-__global__ void __launch_bounds__(kWThreads) paged_weigh_kernel(const PagedWeighParams p) {
-  constexpr int CH = D / 8;
-  extern __shared__ __align__(128) unsigned char sm[];       // K tile, two Q tiles
-  __shared__ float s_lse[2][kWVecs];
-  __shared__ int s_lim[2][kWVecs];
-  const uint32_t smk = smem_u32(sm), smq = smk + kWKeys * D * 2;
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const int b = blockIdx.z, g = blockIdx.y, k0 = blockIdx.x * kWKeys;
-  pdl_wait();
-  pdl_trigger();
-  uint32_t bits = 0;
-  const PagedSeq s = paged_seq(p.map, b, p.T, p.max_rows, bits);
-  if (bits && tid == 0 && g == 0 && blockIdx.x == 0) set_err(p.err, bits);
-  if (k0 >= s.len) return;
-
-  const int32_t* table = p.map.table + (size_t)b * p.map.max_pages;
-  const T* const kp = static_cast<const T*>(p.ck);
-  const T* const qp = static_cast<const T*>(p.q);
-#pragma unroll
-  for (int i = 0; i < kWKeys * CH / kWThreads; ++i) {
-    const int x = tid + i * kWThreads, r = x / CH, c = x % CH, key = k0 + r;
-    int id = -1;
-    if (key < s.len) {
-      id = table[key >> p.map.page_shift];
-      if (!page_ok(p.map, id)) {
-        set_err(p.err, SWA_DERR_PAGE);
-        id = -1;
-      }
-    }
-    const size_t off =
-        id >= 0 ? ((((size_t)id * p.map.nk + g) << p.map.page_shift) + (key & ((1 << p.map.page_shift) - 1))) * D + c * 8 : 0;
-    cp16_or_zero(smk + tile_off<D>(r, c), kp + off, id >= 0);
-  }
-  // rows that see some key of the block: limit > k0
-  const int i_first = max(0, k0 - (s.len - s.t));
-  const int v0 = i_first * p.hpg, nv = s.t * p.hpg;
-  auto load_q = [&](int buf, int v) {
-    for (int x = tid; x < kWVecs * CH; x += kWThreads) {
-      const int r = x / CH, c = x % CH, vec = v + r;
-      const bool ok = vec < nv;
-      const int i = ok ? vec / p.hpg : 0, h = ok ? vec % p.hpg : 0;
-      cp16_or_zero(smq + (uint32_t)(buf * kWVecs * D * 2) + tile_off<D>(r, c),
-                   qp + (ok ? (size_t)(s.r0 + i) * p.q_row + (size_t)(g * p.hpg + h) * D + c * 8 : 0), ok);
-    }
-    if (tid < kWVecs) {
-      const int vec = v + tid;
-      float lse = 0.f;
-      int lim = 0;
-      if (vec < nv) {
-        const int i = vec / p.hpg;
-        lse = p.lse[(size_t)(s.r0 + i) * p.nh + g * p.hpg + vec % p.hpg] * 1.4426950408889634f;
-        lim = min(s.len, s.len - s.t + i + 1);
-      }
-      s_lse[buf][tid] = lse;
-      s_lim[buf][tid] = lim;
-    }
-  };
-  if (v0 < nv) load_q(0, v0);
-  cp_commit();
-  float w[2] = {0.f, 0.f};
-  uint32_t kf[D / 16][4];
-  int buf = 0;
-  for (int v = v0; v < nv; v += kWVecs, buf ^= 1) {
-    cp_wait<0>();
-    __syncthreads();
-    if (v == v0) {
-#pragma unroll
-      for (int k = 0; k < D / 16; ++k)
-        ldsm4(kf[k], smk + tile_off<D>(warp * 16 + (((lane >> 3) & 1) << 3) + (lane & 7), k * 2 + (lane >> 4)));
-    }
-    if (v + kWVecs < nv) load_q(buf ^ 1, v + kWVecs);
-    cp_commit();
-    const uint32_t qb = smq + (uint32_t)(buf * kWVecs * D * 2);
-    float sc[kWVecs / 8][4];
-#pragma unroll
-    for (int n = 0; n < kWVecs / 8; ++n)
-#pragma unroll
-      for (int j = 0; j < 4; ++j) sc[n][j] = 0.f;
-#pragma unroll
-    for (int k = 0; k < D / 16; ++k)
-#pragma unroll
-      for (int n = 0; n < kWVecs / 16; ++n) {
-        uint32_t f[4];
-        ldsm4(f, qb + tile_off<D>(n * 16 + ((lane >> 4) << 3) + (lane & 7), k * 2 + ((lane >> 3) & 1)));
-        mma16816<T>(sc[2 * n], kf[k], f[0], f[1]);
-        mma16816<T>(sc[2 * n + 1], kf[k], f[2], f[3]);
-      }
-    const int key = k0 + warp * 16 + (lane >> 2);
-#pragma unroll
-    for (int n = 0; n < kWVecs / 8; ++n)
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const int c = n * 8 + (lane & 3) * 2 + (j & 1);
-        const float x = ex2(fmaf(sc[n][j], p.qmul, -s_lse[buf][c]));
-        if (key + (j >> 1) * 8 < s_lim[buf][c]) w[j >> 1] += x;
-      }
-  }
-  cp_wait<0>();
-#pragma unroll
-  for (int r = 0; r < 2; ++r) {
-    w[r] += __shfl_xor_sync(0xffffffffu, w[r], 1);
-    w[r] += __shfl_xor_sync(0xffffffffu, w[r], 2);
-    const int key = k0 + warp * 16 + r * 8 + (lane >> 2);
-    if ((lane & 3) == 0 && key < s.len) {
-      const size_t at = ((size_t)b * p.map.nk + g) * p.map.cap + key;
-      p.out[at] = (p.weight ? p.weight[at] : 0.f) + w[r];
-    }
-  }
-}
-
-template <typename T, int D>
-static int launch_weigh(const PagedWeighParams& p, cudaStream_t s) {
-  constexpr int smem = (kWKeys + 2 * kWVecs) * D * 2;
-  cudaError_t e = allow_smem<paged_weigh_kernel<T, D>>(smem);
-  if (e != cudaSuccess) return cuda_status(e);
-  const dim3 grid((unsigned)((p.map.cap + kWKeys - 1) / kWKeys), (unsigned)p.map.nk, (unsigned)p.map.B);
-  return finish_launch(launch_pdl(paged_weigh_kernel<T, D>, grid, dim3(kWThreads), smem, s, p));
-}
-
-// ---------------------------------------------------------------------------
-// Evict. select: one CTA per (sequence, KV head) finds the threshold key of the n'
+// select: one CTA per (sequence, KV head) finds the threshold key of the n'
 // first slots by a radix select over an order-preserving 32-bit key (four histogram
 // passes of 8 bits), then numbers the freed and the moved slots in slot order with
 // block scans, and writes the kept slots' weights and positions. move: a warp a moved
@@ -348,34 +199,6 @@ static bool evict_sizes_ok(const swa_paged_evict_args* a) {
 using namespace swa;
 
 extern "C" {
-
-int swa_paged_weigh(const swa_paged_weigh_args* a, cudaStream_t stream) {
-  if (!a) return SWA_E_NULL;
-  const swa_paged_cache& c = a->cache;
-  const int rc = paged_cache_status(&c, true);
-  if (rc != SWA_OK) return rc;
-  if (!a->out || (a->T > 0 && (!a->q || !a->lse))) return SWA_E_NULL;
-  if (a->T < 0 || a->max_rows < 1 || a->nh < 1 || a->nh % c.nk || a->nh / c.nk > 32) return SWA_E_SHAPE;
-  if ((long long)a->T * a->nh >= (1LL << 31) || (long long)a->max_rows * (a->nh / c.nk) >= (1LL << 31) - 64) return SWA_E_SHAPE;
-  if (!(a->scale >= 0.f) || std::isinf(a->scale)) return SWA_E_SHAPE;
-  if (a->T > 0 && (a->q_row < (long long)a->nh * c.hd || a->q_row > (1LL << 40))) return SWA_E_SHAPE;
-  if (!aligned16p(a->q) || (a->T > 0 && (a->q_row & 7)) || (reinterpret_cast<uintptr_t>(a->lse) & 3u) ||
-      (reinterpret_cast<uintptr_t>(a->weight) & 3u) || (reinterpret_cast<uintptr_t>(a->out) & 3u))
-    return SWA_E_ALIGN;
-  PagedWeighParams p{};
-  p.map = paged_map(&c);
-  const size_t bytes = (size_t)c.B * c.nk * p.map.cap * 4;
-  if (a->weight && a->weight != a->out && bytes_overlap(a->weight, bytes, a->out, bytes)) return SWA_E_SHAPE;
-  p.T = a->T; p.nh = a->nh; p.hpg = a->nh / c.nk; p.max_rows = a->max_rows;
-  p.qmul = a->scale * 1.4426950408889634f;
-  p.q = a->q; p.q_row = a->q_row; p.ck = c.k;
-  p.lse = a->lse; p.weight = a->weight; p.out = a->out; p.err = a->err;
-  if (c.dtype == SWA_BF16)
-    return c.hd == 64 ? launch_weigh<__nv_bfloat16, 64>(p, stream)
-                      : c.hd == 128 ? launch_weigh<__nv_bfloat16, 128>(p, stream) : launch_weigh<__nv_bfloat16, 256>(p, stream);
-  return c.hd == 64 ? launch_weigh<__half, 64>(p, stream)
-                    : c.hd == 128 ? launch_weigh<__half, 128>(p, stream) : launch_weigh<__half, 256>(p, stream);
-}
 
 size_t swa_paged_evict_workspace_size(const swa_paged_evict_args* a) {
   if (!a || !evict_sizes_ok(a)) return 0;

@@ -15,7 +15,7 @@
 #include <cmath>
 
 #include "swa_mma16.cuh"
-#include "swa_paged_attend.cuh"
+#include "swa_paged_tc.cuh"
 
 namespace swa {
 
@@ -48,6 +48,30 @@ PagedMap paged_map(const swa_paged_cache* c) {
   m.cap = c->max_pages << m.page_shift;
   m.table = c->table; m.row_start = c->row_start; m.lens = c->lens;
   return m;
+}
+
+typedef CUresult (*EncodeTiled)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*, const cuuint64_t*,
+                                const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle,
+                                CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+
+// Tensor map of a pool: rows of hd elements, boxes of 64 features x min(page, KT) rows.
+int pool_map(const swa_paged_cache& c, void* base, int kt, CUtensorMap* m) {
+  static EncodeTiled encode = nullptr;
+  if (!encode) {
+    void* f = nullptr;
+    cudaDriverEntryPointQueryResult st;
+    const cudaError_t e = cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &f, 12000, cudaEnableDefault, &st);
+    if (e != cudaSuccess) return cuda_status(e);
+    if (st != cudaDriverEntryPointSuccess || !f) return cuda_status(cudaErrorNotSupported);
+    encode = reinterpret_cast<EncodeTiled>(f);
+  }
+  const cuuint64_t dims[2] = {(cuuint64_t)c.hd, (cuuint64_t)c.num_pages * c.nk * c.page};
+  const cuuint64_t strides[1] = {(cuuint64_t)c.hd * 2};
+  const cuuint32_t box[2] = {64, (cuuint32_t)(c.page < kt ? c.page : kt)}, es[2] = {1, 1};
+  const CUresult r = encode(m, c.dtype == SWA_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 2,
+                            base, dims, strides, box, es, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                            CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  return r == CUDA_SUCCESS ? SWA_OK : cuda_status(cudaErrorInvalidValue);
 }
 
 // ---------------------------------------------------------------------------

@@ -20,10 +20,8 @@
 // Few items are split over the keys: grid.y shares of an item's tiles leave records
 // that chunk_merge_kernel joins.
 #include <cmath>
-#include <cuda.h>
 
-#include "swa_paged_attend.cuh"
-#include "swa_tcgen05.cuh"
+#include "swa_paged_tc.cuh"
 
 namespace swa {
 
@@ -57,88 +55,6 @@ struct ChunkParams {
   float2* rec_ml;              // [item][split][NT * 128]
   int4* rec_desc;              // [item]: (b, g, first row of the item, 0), b < 0: no such item
 };
-
-// kind::f16 with D in f32, A and B both f16 or both bf16, A K-major, B K-major or not
-__host__ __device__ constexpr uint32_t chunk_idesc(bool bf16, bool b_mn_major, int n) {
-  return (1u << 4) | ((bf16 ? 1u : 0u) << 7) | ((bf16 ? 1u : 0u) << 10) | ((b_mn_major ? 1u : 0u) << 16) |
-         ((uint32_t)(n >> 3) << 17) | ((uint32_t)(128 >> 4) << 24);
-}
-// Shared-memory matrix descriptor, 128-byte swizzle (rows of 128 bytes, groups of 8
-// rows every 1024 bytes). K-major: sbo = 1024. MN-major: sbo = 1024 between groups of
-// 8 K rows, lbo between columns of 64 MN elements.
-__device__ __forceinline__ uint64_t sw128_desc(uint32_t addr, uint32_t lbo) {
-  return (uint64_t)((addr >> 4) & 0x3FFF) | ((uint64_t)((lbo >> 4) & 0x3FFF) << 16) |
-         ((uint64_t)(1024 >> 4) << 32) | (1ull << 46) | (2ull << 61);
-}
-__device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, bool acc) {
-  asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
-               "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}"
-               :: "r"(d), "l"(a), "l"(b), "r"(idesc), "r"(acc ? 1 : 0) : "memory");
-}
-// one lane of a converged warp
-__device__ __forceinline__ bool elect_one() {
-  uint32_t p;
-  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(p));
-  return p != 0;
-}
-__device__ __forceinline__ float max3(float a, float b, float c) {
-  float d;
-  asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
-  return d;
-}
-// packed pairs of f32
-__device__ __forceinline__ uint64_t pack64(uint32_t lo, uint32_t hi) {
-  uint64_t d;
-  asm("mov.b64 %0, {%1, %2};" : "=l"(d) : "r"(lo), "r"(hi));
-  return d;
-}
-__device__ __forceinline__ void unpack64(uint64_t v, float& lo, float& hi) {
-  asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(v));
-}
-__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
-  uint64_t d;
-  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
-  return d;
-}
-__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
-  uint64_t d;
-  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
-  return d;
-}
-// Waits for this thread's TMEM loads; the registers are operands, so that nothing that
-// reads them moves ahead of the wait.
-#define SWA_RW32(r) "+r"(r[0]),"+r"(r[1]),"+r"(r[2]),"+r"(r[3]),"+r"(r[4]),"+r"(r[5]),"+r"(r[6]),"+r"(r[7]), \
-  "+r"(r[8]),"+r"(r[9]),"+r"(r[10]),"+r"(r[11]),"+r"(r[12]),"+r"(r[13]),"+r"(r[14]),"+r"(r[15]), \
-  "+r"(r[16]),"+r"(r[17]),"+r"(r[18]),"+r"(r[19]),"+r"(r[20]),"+r"(r[21]),"+r"(r[22]),"+r"(r[23]), \
-  "+r"(r[24]),"+r"(r[25]),"+r"(r[26]),"+r"(r[27]),"+r"(r[28]),"+r"(r[29]),"+r"(r[30]),"+r"(r[31])
-template <int N>
-__device__ __forceinline__ void wait_ld(uint32_t (&x)[N][32]) {
-  asm volatile("tcgen05.wait::ld.sync.aligned;" : SWA_RW32(x[0]) :: "memory");
-#pragma unroll
-  for (int i = 1; i < N; ++i) asm volatile("" : SWA_RW32(x[i]) :: "memory");
-}
-__device__ __forceinline__ void wait_ld(uint32_t (&x)[32]) {
-  asm volatile("tcgen05.wait::ld.sync.aligned;" : SWA_RW32(x) :: "memory");
-}
-__device__ __forceinline__ void tma_2d(uint32_t dst, const CUtensorMap* map, int x, int y, uint64_t* bar) {
-  asm volatile("cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%3, %4}], [%2];"
-               :: "r"(dst), "l"(map), "r"(smem_u32(bar)), "r"(x), "r"(y) : "memory");
-}
-
-// A wait that gives up after kWaitLimitNs; the clock is read every 64th try only (the
-// read takes longer than a try).
-__device__ __forceinline__ bool chunk_wait(uint64_t* bar, uint32_t parity, const int* abort_flag) {
-  if (mbar_try_wait(bar, parity)) return true;
-  uint64_t t0 = 0;
-  for (uint32_t i = 1;; ++i) {
-    if (mbar_try_wait(bar, parity)) return true;
-    if ((i & 63) == 0) {
-      const uint64_t now = global_ns();
-      if (t0 == 0) t0 = now;
-      if (now - t0 > kWaitLimitNs || *(const volatile int*)abort_flag) return false;
-    }
-  }
-}
 
 // First K / V slot position of tile j's K and V in the order they are consumed.
 template <int SB>
@@ -266,8 +182,9 @@ __global__ void __launch_bounds__(ChunkCfg<D>::THREADS, 1)
     __threadfence_block();
     set_err(a.err, SWA_DERR_TIMEOUT);
   };
+  // a wait made by a whole warp, with one outcome for the warp
   auto wait = [&](uint64_t* bar, int phase) -> bool {
-    return chunk_wait(bar, (uint32_t)(phase & 1), &s_abort);
+    return __all_sync(0xffffffffu, tc_wait(bar, (uint32_t)(phase & 1), &s_abort));
   };
 
   // The softmax threads hold a row of S: registers move over to them (384 threads are
@@ -285,7 +202,7 @@ __global__ void __launch_bounds__(ChunkCfg<D>::THREADS, 1)
     int issued = 0;
     auto load = [&](int j, bool is_v, int pos) {
       const int slot = pos % NS, use = pos / NS;
-      if (!__all_sync(0xffffffffu, use == 0 || wait(&b_empty[slot], use - 1))) return false;
+      if (use > 0 && !wait(&b_empty[slot], use - 1)) return false;
       const int key0 = (j0 + j) * KT;
       const bool tail = is_v && key0 + KT > s.len;
       uint64_t* bar = tail ? &b_tail : &b_full[slot];
@@ -342,7 +259,7 @@ __global__ void __launch_bounds__(ChunkCfg<D>::THREADS, 1)
     // tile alone and passes the turn on through b_turn, so that these latencies (about 100
     // clk a wait, 250 a commit) overlap with the other tile's. The warp stays converged and
     // one elected lane issues.
-    constexpr uint32_t ID_S = chunk_idesc(BF, false, KT), ID_O = chunk_idesc(BF, true, D);
+    constexpr uint32_t ID_S = tc_idesc_16(BF, false, KT), ID_O = tc_idesc_16(BF, true, D);
     const int t = warp - W_MMA;
     const bool leader = elect_one();
     const int mine = max(0, min(n_tile[NT == 2 ? t : 0] - j0, n));   // tiles that this query tile sees
@@ -468,10 +385,8 @@ __global__ void __launch_bounds__(ChunkCfg<D>::THREADS, 1)
     const uint32_t c_o = lanes + C::C_O + t * D;
     for (int j = 0; j < mine; ++j) {
       const uint32_t c_s = lanes + (t * SB + j % SB) * KT;
-      if (!wait(&b_s[t * SB + j % SB], j / SB)) {
-        ok = false;
-        break;
-      }
+      // a thread whose wait gave up goes on (its warp stays together) and writes nothing
+      ok &= tc_wait(&b_s[t * SB + j % SB], (uint32_t)((j / SB) & 1), &s_abort);
       tc_fence_after();
       uint32_t x[KT / 32][32];
 #pragma unroll
@@ -496,10 +411,7 @@ __global__ void __launch_bounds__(ChunkCfg<D>::THREADS, 1)
       if (__any_sync(0xffffffffu, raise) && j > 0) {
         const float f = raise ? ex2(m - mx) : 1.f;
         // with one S buffer S of this tile came after P V of the last one
-        if (SB == 2 && !wait(&b_pv[t], j - 1)) {
-          ok = false;
-          break;
-        }
+        if (SB == 2) ok &= wait(&b_pv[t], j - 1);
         if (SB == 2) tc_fence_after();
 #pragma unroll
         for (int i = 0; i < D / 32; ++i) {
@@ -544,6 +456,7 @@ __global__ void __launch_bounds__(ChunkCfg<D>::THREADS, 1)
     // with one S buffer the last S came after it, with two only after the one before that
     if (SB == 2 && ok && mine > 1) ok = wait(&b_pv[t], mine - 2);
     if (ok && mine > 0) ok = wait(&b_pv[t], mine - 1);
+    ok = __all_sync(0xffffffffu, ok);
     if (ok) {
       tc_fence_after();
       const size_t rec = (((size_t)blockIdx.x * p.splits + blockIdx.y) * NT + t) * 128 + r;
@@ -617,30 +530,6 @@ __global__ void __launch_bounds__(128) chunk_merge_kernel(const ChunkParams p) {
 // ---------------------------------------------------------------------------
 // Host side
 // ---------------------------------------------------------------------------
-typedef CUresult (*EncodeTiled)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*, const cuuint64_t*,
-                                const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle,
-                                CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
-
-// Tensor map of a pool: rows of hd elements, boxes of 64 features x min(page, KT) rows.
-static int pool_map(const swa_paged_cache& c, void* base, int kt, CUtensorMap* m) {
-  static EncodeTiled encode = nullptr;
-  if (!encode) {
-    void* f = nullptr;
-    cudaDriverEntryPointQueryResult st;
-    const cudaError_t e = cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &f, 12000, cudaEnableDefault, &st);
-    if (e != cudaSuccess) return cuda_status(e);
-    if (st != cudaDriverEntryPointSuccess || !f) return cuda_status(cudaErrorNotSupported);
-    encode = reinterpret_cast<EncodeTiled>(f);
-  }
-  const cuuint64_t dims[2] = {(cuuint64_t)c.hd, (cuuint64_t)c.num_pages * c.nk * c.page};
-  const cuuint64_t strides[1] = {(cuuint64_t)c.hd * 2};
-  const cuuint32_t box[2] = {64, (cuuint32_t)(c.page < kt ? c.page : kt)}, es[2] = {1, 1};
-  const CUresult r = encode(m, c.dtype == SWA_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 2,
-                            base, dims, strides, box, es, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
-                            CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
-  return r == CUDA_SUCCESS ? SWA_OK : cuda_status(cudaErrorInvalidValue);
-}
-
 ChunkPlan chunk_plan(const swa_paged_attend_args* a) {
   const swa_paged_cache& c = a->cache;
   const int hpg = a->nh / c.nk, nt = c.hd == 256 ? 1 : 2, kt = c.hd == 256 ? 64 : 128;

@@ -1,0 +1,520 @@
+// The attention weight each cached key received from a chunk's rows (swa_paged_weigh).
+//
+// w_j += sum over query vectors i of 2^(qmul <q_i, k_j> - lse_i log2 e): with lse known
+// every weight stands alone, so this is one matrix product with an exponential and a row
+// sum as its epilogue, S^T = K Q^T: 128 keys (M, A operand) by up to QN query vectors (N, B
+// operand). A thread then owns a key: the sum over its row of S^T needs no exchange.
+// Bytes: K once (few rows: bound by that); operations: 2 hd and one exponential a pair, at
+// hd 128 both 512 clk an SM for 128 x 128 pairs (8192 operations and 32 exponentials a clk).
+//
+// One CTA an SM. The units (sequence, KV head, 128 keys), each as dear as the query tiles
+// that see it, are laid end to end and cut evenly. Roles: warp 8 streams K tiles from the
+// pages by TMA; warps 10 and 11 bring the query tiles (cp.async into the swizzled layout,
+// with each vector's lse and limit); warp 9 issues the products into four S buffers of
+// TMEM; warps 0-7 turn them into sums, each warpgroup every other 32 columns. A sequence of
+// at most two query tiles keeps them in shared memory for all its keys, else they are
+// streamed per unit. The sums run in a fixed order: no atomics.
+#include <cmath>
+
+#include "swa_paged_tc.cuh"
+
+namespace swa {
+
+template <int D>
+struct WeighCfg {
+  static constexpr int QN = D == 256 ? 64 : 128;       // query vectors of a tile
+  static constexpr int NS = D == 64 ? 8 : D == 128 ? 4 : 2;   // K slots
+  static constexpr int KB = 128 * D * 2;               // bytes of a K tile
+  static constexpr int QB = QN * D * 2;
+  static constexpr int SMEM = NS * KB + 2 * QB + 1024;
+};
+constexpr int kWeighThreads = 384;
+constexpr int kSBufs = 4;
+
+struct PagedWeighParams {
+  PagedMap map;
+  int T, nh, hpg, max_rows;
+  float qmul;
+  const void* q;
+  long long q_row;
+  const float* lse;
+  const float* weight;
+  float* out;
+  uint32_t* err;
+};
+
+// A sequence's key tiles and the query tiles that see them.
+struct WeighSeq {
+  PagedSeq s;
+  int nv, nqt, n_tiles, n_full;   // query vectors, query tiles, key tiles, key tiles seen by every query tile
+};
+template <int QN>
+__device__ __forceinline__ WeighSeq weigh_seq(const PagedWeighParams& p, int b, uint32_t& bits) {
+  WeighSeq w;
+  w.s = paged_seq(p.map, b, p.T, p.max_rows, bits);
+  w.nv = w.s.t * p.hpg;
+  w.nqt = (w.nv + QN - 1) / QN;
+  w.n_tiles = (w.s.len + 127) / 128;
+  w.n_full = w.s.len >= w.s.t ? min(w.n_tiles, (w.s.len - w.s.t) / 128 + 1) : 0;
+  return w;
+}
+// First query tile that sees keys of tile `tile`: its last row has a limit above the tile's
+// first key, rows from (first key - (len - t)) on.
+template <int QN>
+__device__ __forceinline__ int first_qt(const PagedWeighParams& p, const WeighSeq& w, int tile) {
+  const long long row = (long long)tile * 128 - (w.s.len - w.s.t);
+  return row <= 0 ? 0 : (int)min((long long)w.nqt, row * p.hpg / QN);
+}
+template <int QN>
+__device__ __forceinline__ int tile_cost(const PagedWeighParams& p, const WeighSeq& w, int tile) {
+  return max(1, w.nqt - first_qt<QN>(p, w, tile));
+}
+template <int QN>
+__device__ __forceinline__ long long head_cost(const PagedWeighParams& p, const WeighSeq& w) {
+  long long c = (long long)w.n_full * max(1, w.nqt);
+  if (w.nqt <= 1) return w.n_tiles;
+  for (int i = w.n_full; i < w.n_tiles; ++i) c += tile_cost<QN>(p, w, i);
+  return c;
+}
+
+// Walks this CTA's units; every role keeps its own.
+template <int QN>
+struct WeighIter {
+  const PagedWeighParams& p;
+  WeighSeq w;
+  int b, g, tile;
+  long long left;              // cost still to take
+  __device__ __forceinline__ bool done() const { return left <= 0; }
+  __device__ __forceinline__ int qt0() const { return first_qt<QN>(p, w, tile); }
+  __device__ __forceinline__ bool resident() const { return w.nqt <= 2; }
+  // the next unit; true when it belongs to another (sequence, KV head) (or there is none)
+  __device__ __forceinline__ bool next() {
+    left -= tile_cost<QN>(p, w, tile);
+    if (++tile < w.n_tiles) return left <= 0;
+    tile = 0;
+    if (left <= 0) return true;
+    if (++g == p.map.nk) {
+      g = 0;
+      uint32_t ignore = 0;
+      do w = weigh_seq<QN>(p, ++b, ignore);
+      while (w.n_tiles == 0);
+    }
+    return true;
+  }
+};
+
+template <typename T, int D>
+__global__ void __launch_bounds__(kWeighThreads, 1)
+    paged_weigh_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constant__ PagedWeighParams p) {
+  using C = WeighCfg<D>;
+  constexpr int QN = C::QN, NS = C::NS, CH = D / 8;
+  constexpr bool BF = std::is_same<T, __nv_bfloat16>::value;
+  extern __shared__ unsigned char sm_raw[];
+  __shared__ __align__(8) uint64_t b_kfull[NS], b_kempty[NS], b_qfull[2], b_qempty[2], b_s[kSBufs], b_sfree[kSBufs], b_part[2], b_pfree[2], b_fin;
+  __shared__ __align__(16) float s_lse[2][QN];
+  __shared__ __align__(16) int s_lim[2][QN];
+  __shared__ float s_part[2][128];
+  __shared__ long long s_scan[kWeighThreads / 32];
+  __shared__ long long s_left;
+  __shared__ uint32_t s_tmem;
+  __shared__ int s_abort, s_b, s_g, s_tile;
+  const int tid = threadIdx.x, lane = tid & 31, warp = __shfl_sync(0xffffffffu, tid >> 5, 0);
+  unsigned char* const sm = reinterpret_cast<unsigned char*>((reinterpret_cast<uintptr_t>(sm_raw) + 1023) & ~(uintptr_t)1023);
+  unsigned char* const sm_q = sm + NS * C::KB;
+  pdl_wait();
+  pdl_trigger();
+
+  // --- this CTA's share: units whose start lies in [u0, u1) of the summed costs
+  {
+    uint32_t bits = 0;
+    const int E = (p.map.B + kWeighThreads - 1) / kWeighThreads;
+    long long mine = 0;
+    for (int e = 0; e < E; ++e) {
+      const int b = tid * E + e;
+      if (b < p.map.B) mine += p.map.nk * head_cost<QN>(p, weigh_seq<QN>(p, b, bits));
+    }
+    if (bits && blockIdx.x == 0) set_err(p.err, bits);
+    long long incl = mine;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const long long v = __shfl_up_sync(0xffffffffu, incl, o);
+      if (lane >= o) incl += v;
+    }
+    if (lane == 31) s_scan[warp] = incl;
+    if (tid == 0) {
+      s_b = -1;
+      s_abort = 0;
+    }
+    __syncthreads();
+    long long before = incl - mine, total = 0;
+    for (int w = 0; w < kWeighThreads / 32; ++w) {
+      if (w < warp) before += s_scan[w];
+      total += s_scan[w];
+    }
+    const long long per = (total + gridDim.x - 1) / gridDim.x;
+    const long long u0 = per * blockIdx.x, u1 = min(total, u0 + per);
+    if (u0 < u1 && u0 >= before && u0 < before + mine) {
+      // the first unit that starts at or after u0
+      long long at = before;
+      uint32_t ignore = 0;
+      int found = 0;
+      for (int e = 0; e < E && !found; ++e) {
+        const int b = tid * E + e;
+        if (b >= p.map.B) break;
+        const WeighSeq w = weigh_seq<QN>(p, b, ignore);
+        const long long hc = head_cost<QN>(p, w);
+        if (hc == 0 || at + hc * p.map.nk <= u0) {
+          at += hc * p.map.nk;
+          continue;
+        }
+        int g = at >= u0 ? 0 : (int)((u0 - at) / hc);
+        at += hc * g;
+        const int full = max(1, w.nqt);
+        int tile = at >= u0 ? 0 : (int)min((long long)w.n_full, (u0 - at + full - 1) / full);
+        if (w.nqt <= 1 && at < u0) tile = (int)(u0 - at);
+        at += (long long)min(tile, w.nqt <= 1 ? tile : w.n_full) * full;
+        while (tile < w.n_tiles && at < u0) at += tile_cost<QN>(p, w, tile++);
+        if (tile == w.n_tiles) {            // the head's units all start before u0: the next head's first
+          tile = 0;
+          if (++g == p.map.nk) continue;    // or the next sequence's (at stands at its start)
+        }
+        found = 1;
+        if (at < u1) {
+          s_b = b;
+          s_g = g;
+          s_tile = tile;
+          s_left = u1 - at;
+        }
+      }
+      if (!found && at < u1) {
+        // the next sequence with keys belongs to a later thread's share
+        for (int b = tid * E + E; b < p.map.B; ++b) {
+          if (weigh_seq<QN>(p, b, ignore).n_tiles > 0) {
+            s_b = b;
+            s_g = 0;
+            s_tile = 0;
+            s_left = u1 - at;
+            break;
+          }
+        }
+      }
+    }
+    __syncthreads();
+  }
+  if (s_b < 0) return;
+
+  if (warp == 8 && lane == 0) {
+    for (int i = 0; i < NS; ++i) {
+      mbar_init(&b_kfull[i], 1);
+      mbar_init(&b_kempty[i], 1);
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&b_qfull[i], 64);
+      mbar_init(&b_qempty[i], 1 + 8);
+      mbar_init(&b_part[i], 128);
+      mbar_init(&b_pfree[i], 128);
+    }
+    for (int i = 0; i < kSBufs; ++i) {
+      mbar_init(&b_s[i], 1);
+      mbar_init(&b_sfree[i], 8);
+    }
+    mbar_init(&b_fin, 1);
+    mbar_fence_init();
+  } else if (warp == 9) {
+    tc_alloc(&s_tmem, 512);
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = __shfl_sync(0xffffffffu, s_tmem, 0);
+  auto give_up = [&]() {
+    s_abort = 1;
+    __threadfence_block();
+    set_err(p.err, SWA_DERR_TIMEOUT);
+  };
+  // every wait is made by whole warps and has one outcome for the warp
+  auto wait = [&](uint64_t* bar, int phase) -> bool {
+    return __all_sync(0xffffffffu, tc_wait(bar, (uint32_t)(phase & 1), &s_abort));
+  };
+  uint32_t ignore = 0;
+  WeighIter<QN> it{p, weigh_seq<QN>(p, s_b, ignore), s_b, s_g, s_tile, s_left};
+  bool ok = true;
+
+  if (warp == 8) {
+    // ------------------------------------------------------------ K tiles
+    const int page = 1 << p.map.page_shift, rows = min(page, 128), per_half = 128 / rows;
+    const int oob = p.map.num_pages * p.map.nk << p.map.page_shift;       // rows of the pool: reads zeros
+    int uc = 0;
+    for (; !it.done(); it.next()) {
+      if (it.qt0() >= it.w.nqt) continue;
+      const int slot = uc % NS, use = uc / NS;
+      ok = use == 0 || wait(&b_kempty[slot], use - 1);
+      if (!ok) break;
+      if (lane == 0) mbar_arrive_expect_tx(&b_kfull[slot], C::KB);
+      __syncwarp();
+      const int32_t* table = p.map.table + (size_t)it.b * p.map.max_pages;
+      for (int i = lane; i < per_half * (D / 64); i += 32) {
+        const int half = i / per_half, bx = i % per_half, key = it.tile * 128 + bx * rows;
+        int y = oob;
+        if (key < it.w.s.len) {
+          const int id = table[key >> p.map.page_shift];
+          if (page_ok(p.map, id))
+            y = ((id * p.map.nk + it.g) << p.map.page_shift) + (key & (page - 1));
+          else
+            set_err(p.err, SWA_DERR_PAGE);
+        }
+        tma_2d(smem_u32(sm + slot * C::KB + half * (128 * 128) + bx * rows * 128), &map_k, half * 64, y, &b_kfull[slot]);
+      }
+      ++uc;
+    }
+    if (!ok) {
+      give_up();
+      // copies in flight land before the CTA exits (bounded)
+      for (int u = max(0, uc - NS); u < uc; ++u) mbar_wait_bounded(&b_kfull[u % NS], (uint32_t)((u / NS) & 1), kWaitLimitNs);
+    }
+  } else if (warp == 9) {
+    // ------------------------------------------------------------ products
+    const bool leader = elect_one();
+    const uint64_t k_desc = sw128_desc(smem_u32(sm), 16), q_desc = sw128_desc(smem_u32(sm_q), 16);
+    int uc = 0, jc = 0, qc = 0;             // units with products, products, query tiles loaded
+    int q_base = it.qt0();                  // first query tile kept of a resident head
+    while (ok && !it.done()) {
+      const int nqt = it.w.nqt, slot = uc % NS;
+      const bool res = it.resident();
+      const int q_first = it.qt0();
+      for (int qt = q_first; ok && qt < nqt; ++qt, ++jc) {
+        const int qi = res ? qc + qt - q_base : qc, buf = jc % kSBufs;
+        ok = (qt > q_first || wait(&b_kfull[slot], uc / NS)) && wait(&b_qfull[qi & 1], qi >> 1) &&
+             (jc < kSBufs || wait(&b_sfree[buf], jc / kSBufs - 1));
+        if (!ok) break;
+        tc_fence_after();
+        if (leader) {
+          const int n = min(QN, (it.w.nv - qt * QN + 31) & ~31);
+          const uint32_t id = tc_idesc_16(BF, false, n);
+          const uint64_t kd = k_desc + (uint64_t)((slot * C::KB) >> 4), qd = q_desc + (uint64_t)(((qi & 1) * C::QB) >> 4);
+#pragma unroll
+          for (int k = 0; k < D / 16; ++k)
+            mma_ss(tmem + buf * QN, kd + (((k >> 2) * (128 * 128) + (k & 3) * 32) >> 4),
+                   qd + (((k >> 2) * (QN * 128) + (k & 3) * 32) >> 4), id, k > 0);
+          tc_commit(&b_s[buf]);
+          if (!res) tc_commit(&b_qempty[qi & 1]);
+          if (qt == nqt - 1) tc_commit(&b_kempty[slot]);
+        }
+        __syncwarp();
+        if (!res) ++qc;
+      }
+      if (q_first < nqt) ++uc;
+      if (!ok) break;
+      const bool moved = it.next();
+      if (moved && res) {
+        if (leader)
+          for (int i = q_base; i < nqt; ++i) tc_commit(&b_qempty[(qc + i - q_base) & 1]);
+        __syncwarp();
+        qc += nqt - q_base;
+      }
+      if (moved && !it.done()) q_base = it.qt0();
+    }
+    if (!ok) {
+      give_up();
+      if (leader) tc_commit(&b_fin);        // what was issued finishes before TMEM goes (bounded)
+      mbar_wait_bounded(&b_fin, 0, kWaitLimitNs);
+    }
+  } else if (warp >= 10) {
+    // ------------------------------------------------------------ query tiles
+    const int th = tid - 320;
+    int qc = 0, pending = -1;               // tiles started, the one whose arrival is still to be told
+    auto tell = [&](bool all) {
+      if (pending < 0) return;
+      if (all) asm volatile("cp.async.wait_group 0;" ::: "memory");
+      else asm volatile("cp.async.wait_group 1;" ::: "memory");
+      fence_proxy_async_smem();
+      mbar_arrive(&b_qfull[pending & 1]);
+      pending = -1;
+    };
+    auto load = [&](int qt) {
+      const int slot = qc & 1, use = qc >> 1;
+      if (use > 0 && !__all_sync(0xffffffffu, mbar_try_wait(&b_qempty[slot], (uint32_t)((use - 1) & 1)))) {
+        tell(true);                         // before a wait that may be long
+        if (!wait(&b_qempty[slot], use - 1)) return false;
+      }
+      const int v0 = qt * QN, n = min(QN, (it.w.nv - v0 + 31) & ~31);
+      const uint32_t dst = smem_u32(sm_q + slot * C::QB);
+      const T* qp = static_cast<const T*>(p.q);
+      for (int x = th; x < n * CH; x += 64) {
+        const int r = x / CH, c = x % CH, vec = v0 + r;
+        const bool in = vec < it.w.nv;
+        const int i = in ? vec / p.hpg : 0, h = in ? vec % p.hpg : 0;
+        const T* src = qp + (in ? (size_t)(it.w.s.r0 + i) * p.q_row + (size_t)(it.g * p.hpg + h) * D + c * 8 : 0);
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;"
+                     :: "r"(dst + (c >> 3) * (QN * 128) + r * 128 + (((c & 7) ^ (r & 7)) << 4)), "l"(src), "r"(in ? 16 : 0)
+                     : "memory");
+      }
+      asm volatile("cp.async.commit_group;" ::: "memory");
+      for (int r = th; r < n; r += 64) {
+        const int vec = v0 + r;
+        float lse = INFINITY;               // no query vector: weight 0
+        int lim = 0;
+        if (vec < it.w.nv) {
+          const int i = vec / p.hpg;
+          lse = p.lse[(size_t)(it.w.s.r0 + i) * p.nh + it.g * p.hpg + vec % p.hpg] * 1.4426950408889634f;
+          lim = min(it.w.s.len, it.w.s.len - it.w.s.t + i + 1);
+        }
+        s_lse[slot][r] = lse;
+        s_lim[slot][r] = lim;
+      }
+      tell(false);
+      pending = qc++;
+      return true;
+    };
+    bool fresh = true;
+    while (ok && !it.done()) {
+      if (it.resident()) {
+        // the head's later key tiles need no query tile that its first one here does not
+        for (int qt = it.qt0(); fresh && ok && qt < it.w.nqt; ++qt) ok = load(qt);
+      } else {
+        for (int qt = it.qt0(); ok && qt < it.w.nqt; ++qt) ok = load(qt);
+      }
+      if (ok) fresh = it.next();
+    }
+    asm volatile("cp.async.wait_group 0;" ::: "memory");
+    if (ok) tell(true);
+    else give_up();
+  } else {
+    // ------------------------------------------------------------ sums: thread = key
+    const int wg = warp >> 2, r = tid & 127;
+    const uint32_t lanes = tmem + ((uint32_t)((warp & 3) * 32) << 16);
+    const uint64_t mul2 = pack64(__float_as_uint(p.qmul), __float_as_uint(p.qmul));
+    int jc = 0, qc = 0, uc = 0, q_base = it.qt0();
+    while (!it.done()) {
+      const int nqt = it.w.nqt, key = it.tile * 128 + r;
+      const bool res = it.resident();
+      const size_t at = ((size_t)it.b * p.map.nk + it.g) * p.map.cap + key;
+      const bool mine = wg == 0 && key < it.w.s.len;
+      const float w0 = mine && p.weight ? p.weight[at] : 0.f;   // under way during the products
+      uint64_t sum[2] = {0, 0};
+      for (int qt = it.qt0(); qt < nqt; ++qt, ++jc) {
+        const int qi = res ? qc + qt - q_base : qc, buf = jc % kSBufs, slot = qi & 1;
+        // lse and limits, then S; a thread whose wait gave up goes on (its warp stays
+        // together) and writes nothing
+        ok &= tc_wait(&b_qfull[slot], (uint32_t)((qi >> 1) & 1), &s_abort) &&
+              tc_wait(&b_s[buf], (uint32_t)((jc / kSBufs) & 1), &s_abort);
+        tc_fence_after();
+        const int n = min(QN, (it.w.nv - qt * QN + 31) & ~31);
+        // some row of the tile does not see the whole key tile
+        const bool mask = it.tile * 128 + 128 > it.w.s.len - it.w.s.t + qt * QN / p.hpg + 1;
+        for (int c = wg * 32; c < n; c += 64) {
+          uint32_t x[32];
+          tc_ld32(lanes + buf * QN + c, x);
+          wait_ld(x);
+#pragma unroll
+          for (int k = 0; k < 32; k += 4) {
+            const float4 ls = *reinterpret_cast<const float4*>(&s_lse[slot][c + k]);
+            const float l4[4] = {-ls.x, -ls.y, -ls.z, -ls.w};
+            float e[4];
+#pragma unroll
+            for (int i = 0; i < 4; i += 2)
+              unpack64(fma2(pack64(x[k + i], x[k + i + 1]), mul2, pack64(__float_as_uint(l4[i]), __float_as_uint(l4[i + 1]))),
+                       e[i], e[i + 1]);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) e[i] = ex2(e[i]);
+            if (mask) {
+              const int4 lm = *reinterpret_cast<const int4*>(&s_lim[slot][c + k]);
+              const int l[4] = {lm.x, lm.y, lm.z, lm.w};
+#pragma unroll
+              for (int i = 0; i < 4; ++i)
+                if (key >= l[i]) e[i] = 0.f;
+            }
+#pragma unroll
+            for (int i = 0; i < 4; i += 2) sum[i >> 1] = add2(sum[i >> 1], pack64(__float_as_uint(e[i]), __float_as_uint(e[i + 1])));
+          }
+        }
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) {
+          mbar_arrive(&b_sfree[buf]);
+          if (!res) mbar_arrive(&b_qempty[slot]);
+        }
+        if (!res) ++qc;
+      }
+      float a0, a1;
+      unpack64(add2(sum[0], sum[1]), a0, a1);
+      float w = a0 + a1;
+      // the second warpgroup's columns reach the first through shared memory, two buffers
+      const int pb = uc & 1, use = uc >> 1;
+      if (wg == 1) {
+        if (use > 0) ok &= tc_wait(&b_pfree[pb], (uint32_t)((use - 1) & 1), &s_abort);
+        s_part[pb][r] = w;
+        mbar_arrive(&b_part[pb]);
+      } else {
+        ok &= tc_wait(&b_part[pb], (uint32_t)(use & 1), &s_abort);
+        w += s_part[pb][r];
+        mbar_arrive(&b_pfree[pb]);
+        if (mine && ok) p.out[at] = w0 + w;
+      }
+      ++uc;
+      const bool moved = it.next();
+      if (moved && res) {
+        __syncwarp();
+        if (lane == 0)
+          for (int i = q_base; i < nqt; ++i) mbar_arrive(&b_qempty[(qc + i - q_base) & 1]);
+        qc += nqt - q_base;
+      }
+      if (moved && !it.done()) q_base = it.qt0();
+    }
+    if (!ok) give_up();
+  }
+  __syncwarp();
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 9) {
+    tc_fence_after();
+    tc_dealloc(tmem, 512);
+  }
+}
+
+template <typename T, int D>
+static int launch_weigh(const swa_paged_weigh_args* a, const PagedWeighParams& p, cudaStream_t s) {
+  CUtensorMap mk;
+  const int rc = pool_map(a->cache, a->cache.k, 128, &mk);
+  if (rc != SWA_OK) return rc;
+  const cudaError_t e = allow_smem<paged_weigh_kernel<T, D>>(WeighCfg<D>::SMEM);
+  if (e != cudaSuccess) return cuda_status(e);
+  return finish_launch(launch_pdl(paged_weigh_kernel<T, D>, dim3(num_sms() > 0 ? num_sms() : 148), dim3(kWeighThreads),
+                                  WeighCfg<D>::SMEM, s, mk, p));
+}
+
+}  // namespace swa
+
+using namespace swa;
+
+extern "C" {
+
+int swa_paged_weigh(const swa_paged_weigh_args* a, cudaStream_t stream) {
+  if (!a) return SWA_E_NULL;
+  const swa_paged_cache& c = a->cache;
+  const int rc = paged_cache_status(&c, true);
+  if (rc != SWA_OK) return rc;
+  if (!a->out || (a->T > 0 && (!a->q || !a->lse))) return SWA_E_NULL;
+  if (a->T < 0 || a->max_rows < 1 || a->nh < 1 || a->nh % c.nk || a->nh / c.nk > 32) return SWA_E_SHAPE;
+  if ((long long)a->T * a->nh >= (1LL << 31) || (long long)a->max_rows * (a->nh / c.nk) >= (1LL << 31) - 64) return SWA_E_SHAPE;
+  if (!(a->scale >= 0.f) || std::isinf(a->scale)) return SWA_E_SHAPE;
+  if (a->T > 0 && (a->q_row < (long long)a->nh * c.hd || a->q_row > (1LL << 40))) return SWA_E_SHAPE;
+  if (!aligned16p(a->q) || (a->T > 0 && (a->q_row & 7)) || (reinterpret_cast<uintptr_t>(a->lse) & 3u) ||
+      (reinterpret_cast<uintptr_t>(a->weight) & 3u) || (reinterpret_cast<uintptr_t>(a->out) & 3u))
+    return SWA_E_ALIGN;
+  PagedWeighParams p{};
+  p.map = paged_map(&c);
+  const size_t bytes = (size_t)c.B * c.nk * p.map.cap * 4;
+  if (a->weight && a->weight != a->out && bytes_overlap(a->weight, bytes, a->out, bytes)) return SWA_E_SHAPE;
+  p.T = a->T; p.nh = a->nh; p.hpg = a->nh / c.nk; p.max_rows = a->max_rows;
+  p.qmul = a->scale * 1.4426950408889634f;
+  p.q = a->q; p.q_row = a->q_row;
+  p.lse = a->lse; p.weight = a->weight; p.out = a->out; p.err = a->err;
+  if (c.dtype == SWA_BF16)
+    return c.hd == 64 ? launch_weigh<__nv_bfloat16, 64>(a, p, stream)
+                      : c.hd == 128 ? launch_weigh<__nv_bfloat16, 128>(a, p, stream) : launch_weigh<__nv_bfloat16, 256>(a, p, stream);
+  return c.hd == 64 ? launch_weigh<__half, 64>(a, p, stream)
+                    : c.hd == 128 ? launch_weigh<__half, 128>(a, p, stream) : launch_weigh<__half, 256>(a, p, stream);
+}
+
+}  // extern "C"
