@@ -7,13 +7,14 @@
 // Bytes: K once (few rows: bound by that); operations: 2 hd and one exponential a pair, at
 // hd 128 both 512 clk an SM for 128 x 128 pairs (8192 operations and 32 exponentials a clk).
 //
-// One CTA an SM. The units (sequence, KV head, 128 keys), each as dear as the query tiles
-// that see it, are laid end to end and cut evenly. Roles: warp 8 streams K tiles from the
-// pages by TMA; warps 10 and 11 bring the query tiles (cp.async into the swizzled layout,
-// with each vector's lse and limit); warp 9 issues the products into four S buffers of
-// TMEM; warps 0-7 turn them into sums, each warpgroup every other 32 columns. A sequence of
-// at most two query tiles keeps them in shared memory for all its keys, else they are
-// streamed per unit. The sums run in a fixed order: no atomics.
+// One CTA an SM. The units (sequence, KV head, 256 keys), each as dear as the query tiles
+// that see it, are laid end to end and cut evenly. Roles: warp 8 streams K tiles of 128
+// keys from the pages by TMA; warps 10 and 11 bring the query tiles (cp.async into the
+// swizzled layout, with each vector's lse and limit); warp 9 issues the products, two S
+// buffers in TMEM for each half of a unit; a warpgroup (warps 0-3, 4-7) sums each half, so
+// that a query tile serves 256 keys and nothing is exchanged. A sequence of at most two
+// query tiles keeps them in shared memory for all its keys, else they are streamed per
+// unit. The sums run in a fixed order: no atomics.
 #include <cmath>
 
 #include "swa_paged_tc.cuh"
@@ -23,17 +24,18 @@ namespace swa {
 template <int D>
 struct WeighCfg {
   static constexpr int QN = D == 256 ? 64 : 128;       // query vectors of a tile
-  static constexpr int NS = D == 64 ? 8 : D == 128 ? 4 : 2;   // K slots
+  static constexpr int NS = D == 64 ? 8 : D == 128 ? 4 : 2;   // K slots of 128 keys
   static constexpr int KB = 128 * D * 2;               // bytes of a K tile
   static constexpr int QB = QN * D * 2;
   static constexpr int SMEM = NS * KB + 2 * QB + 1024;
 };
 constexpr int kWeighThreads = 384;
-constexpr int kSBufs = 4;
+constexpr int kUnit = 256;     // keys of a unit
 
 struct PagedWeighParams {
   PagedMap map;
   int T, nh, hpg, max_rows;
+  uint32_t hpg_mul, hpg_shift; // vec / hpg = vec * hpg_mul >> hpg_shift for 0 <= vec < 2^31 (row_of)
   float qmul;
   const void* q;
   long long q_row;
@@ -43,7 +45,14 @@ struct PagedWeighParams {
   uint32_t* err;
 };
 
-// A sequence's key tiles and the query tiles that see them.
+// The chunk row of a query vector. hpg_shift = 31 + l with 2^l >= hpg and hpg_mul =
+// ceil(2^hpg_shift / hpg) <= 2^32: the product's excess is below vec * 2^l < 2^hpg_shift,
+// so the quotient is exact.
+__device__ __forceinline__ int row_of(const PagedWeighParams& p, int vec) {
+  return (int)((unsigned long long)(unsigned)vec * p.hpg_mul >> p.hpg_shift);
+}
+
+// A sequence's units of a KV head ("tiles" of kUnit keys) and the query tiles that see them.
 struct WeighSeq {
   PagedSeq s;
   int nv, nqt, n_tiles, n_full;   // query vectors, query tiles, key tiles, key tiles seen by every query tile
@@ -54,15 +63,15 @@ __device__ __forceinline__ WeighSeq weigh_seq(const PagedWeighParams& p, int b, 
   w.s = paged_seq(p.map, b, p.T, p.max_rows, bits);
   w.nv = w.s.t * p.hpg;
   w.nqt = (w.nv + QN - 1) / QN;
-  w.n_tiles = (w.s.len + 127) / 128;
-  w.n_full = w.s.len >= w.s.t ? min(w.n_tiles, (w.s.len - w.s.t) / 128 + 1) : 0;
+  w.n_tiles = (w.s.len + kUnit - 1) / kUnit;
+  w.n_full = w.s.len >= w.s.t ? min(w.n_tiles, (w.s.len - w.s.t) / kUnit + 1) : 0;
   return w;
 }
 // First query tile that sees keys of tile `tile`: its last row has a limit above the tile's
 // first key, rows from (first key - (len - t)) on.
 template <int QN>
 __device__ __forceinline__ int first_qt(const PagedWeighParams& p, const WeighSeq& w, int tile) {
-  const long long row = (long long)tile * 128 - (w.s.len - w.s.t);
+  const long long row = (long long)tile * kUnit - (w.s.len - w.s.t);
   return row <= 0 ? 0 : (int)min((long long)w.nqt, row * p.hpg / QN);
 }
 template <int QN>
@@ -87,6 +96,7 @@ struct WeighIter {
   __device__ __forceinline__ bool done() const { return left <= 0; }
   __device__ __forceinline__ int qt0() const { return first_qt<QN>(p, w, tile); }
   __device__ __forceinline__ bool resident() const { return w.nqt <= 2; }
+  __device__ __forceinline__ int halves() const { return tile * kUnit + 128 < w.s.len ? 2 : 1; }
   // the next unit; true when it belongs to another (sequence, KV head) (or there is none)
   __device__ __forceinline__ bool next() {
     left -= tile_cost<QN>(p, w, tile);
@@ -110,10 +120,9 @@ __global__ void __launch_bounds__(kWeighThreads, 1)
   constexpr int QN = C::QN, NS = C::NS, CH = D / 8;
   constexpr bool BF = std::is_same<T, __nv_bfloat16>::value;
   extern __shared__ unsigned char sm_raw[];
-  __shared__ __align__(8) uint64_t b_kfull[NS], b_kempty[NS], b_qfull[2], b_qempty[2], b_s[kSBufs], b_sfree[kSBufs], b_part[2], b_pfree[2], b_fin;
-  __shared__ __align__(16) float s_lse[2][QN];
+  __shared__ __align__(8) uint64_t b_kfull[NS], b_kempty[NS], b_qfull[2], b_qempty[2], b_s[4], b_sfree[4], b_fin;
+  __shared__ __align__(16) float s_nlse[2][QN];             // -lse log2 e
   __shared__ __align__(16) int s_lim[2][QN];
-  __shared__ float s_part[2][128];
   __shared__ long long s_scan[kWeighThreads / 32];
   __shared__ long long s_left;
   __shared__ uint32_t s_tmem;
@@ -211,12 +220,10 @@ __global__ void __launch_bounds__(kWeighThreads, 1)
     for (int i = 0; i < 2; ++i) {
       mbar_init(&b_qfull[i], 64);
       mbar_init(&b_qempty[i], 1 + 8);
-      mbar_init(&b_part[i], 128);
-      mbar_init(&b_pfree[i], 128);
     }
-    for (int i = 0; i < kSBufs; ++i) {
+    for (int i = 0; i < 4; ++i) {
       mbar_init(&b_s[i], 1);
-      mbar_init(&b_sfree[i], 8);
+      mbar_init(&b_sfree[i], 4);
     }
     mbar_init(&b_fin, 1);
     mbar_fence_init();
@@ -244,66 +251,76 @@ __global__ void __launch_bounds__(kWeighThreads, 1)
     // ------------------------------------------------------------ K tiles
     const int page = 1 << p.map.page_shift, rows = min(page, 128), per_half = 128 / rows;
     const int oob = p.map.num_pages * p.map.nk << p.map.page_shift;       // rows of the pool: reads zeros
-    int uc = 0;
-    for (; !it.done(); it.next()) {
+    int kc = 0;                             // tiles started
+    for (; ok && !it.done(); it.next()) {
       if (it.qt0() >= it.w.nqt) continue;
-      const int slot = uc % NS, use = uc / NS;
-      ok = use == 0 || wait(&b_kempty[slot], use - 1);
-      if (!ok) break;
-      if (lane == 0) mbar_arrive_expect_tx(&b_kfull[slot], C::KB);
-      __syncwarp();
       const int32_t* table = p.map.table + (size_t)it.b * p.map.max_pages;
-      for (int i = lane; i < per_half * (D / 64); i += 32) {
-        const int half = i / per_half, bx = i % per_half, key = it.tile * 128 + bx * rows;
-        int y = oob;
-        if (key < it.w.s.len) {
-          const int id = table[key >> p.map.page_shift];
-          if (page_ok(p.map, id))
-            y = ((id * p.map.nk + it.g) << p.map.page_shift) + (key & (page - 1));
-          else
-            set_err(p.err, SWA_DERR_PAGE);
+      for (int h = 0; ok && h < it.halves(); ++h) {
+        const int slot = kc % NS, use = kc / NS;
+        ok = use == 0 || wait(&b_kempty[slot], use - 1);
+        if (!ok) break;
+        if (lane == 0) mbar_arrive_expect_tx(&b_kfull[slot], C::KB);
+        __syncwarp();
+        for (int i = lane; i < per_half * (D / 64); i += 32) {
+          const int half = i / per_half, bx = i % per_half, key = it.tile * kUnit + h * 128 + bx * rows;
+          int y = oob;
+          if (key < it.w.s.len) {
+            const int id = table[key >> p.map.page_shift];
+            if (page_ok(p.map, id))
+              y = ((id * p.map.nk + it.g) << p.map.page_shift) + (key & (page - 1));
+            else
+              set_err(p.err, SWA_DERR_PAGE);
+          }
+          tma_2d(smem_u32(sm + slot * C::KB + half * (128 * 128) + bx * rows * 128), &map_k, half * 64, y, &b_kfull[slot]);
         }
-        tma_2d(smem_u32(sm + slot * C::KB + half * (128 * 128) + bx * rows * 128), &map_k, half * 64, y, &b_kfull[slot]);
+        ++kc;
       }
-      ++uc;
     }
     if (!ok) {
       give_up();
       // copies in flight land before the CTA exits (bounded)
-      for (int u = max(0, uc - NS); u < uc; ++u) mbar_wait_bounded(&b_kfull[u % NS], (uint32_t)((u / NS) & 1), kWaitLimitNs);
+      for (int u = max(0, kc - NS); u < kc; ++u) mbar_wait_bounded(&b_kfull[u % NS], (uint32_t)((u / NS) & 1), kWaitLimitNs);
     }
   } else if (warp == 9) {
     // ------------------------------------------------------------ products
     const bool leader = elect_one();
     const uint64_t k_desc = sw128_desc(smem_u32(sm), 16), q_desc = sw128_desc(smem_u32(sm_q), 16);
-    int uc = 0, jc = 0, qc = 0;             // units with products, products, query tiles loaded
+    int kc = 0, jc[2] = {0, 0}, qc = 0;     // K tiles, products of each half, query tiles loaded
     int q_base = it.qt0();                  // first query tile kept of a resident head
     while (ok && !it.done()) {
-      const int nqt = it.w.nqt, slot = uc % NS;
+      const int nqt = it.w.nqt, nh = it.halves();
       const bool res = it.resident();
       const int q_first = it.qt0();
-      for (int qt = q_first; ok && qt < nqt; ++qt, ++jc) {
-        const int qi = res ? qc + qt - q_base : qc, buf = jc % kSBufs;
-        ok = (qt > q_first || wait(&b_kfull[slot], uc / NS)) && wait(&b_qfull[qi & 1], qi >> 1) &&
-             (jc < kSBufs || wait(&b_sfree[buf], jc / kSBufs - 1));
-        if (!ok) break;
-        tc_fence_after();
-        if (leader) {
-          const int n = min(QN, (it.w.nv - qt * QN + 31) & ~31);
-          const uint32_t id = tc_idesc_16(BF, false, n);
-          const uint64_t kd = k_desc + (uint64_t)((slot * C::KB) >> 4), qd = q_desc + (uint64_t)(((qi & 1) * C::QB) >> 4);
+      for (int qt = q_first; ok && qt < nqt; ++qt) {
+        const int qi = res ? qc + qt - q_base : qc;
+        ok = wait(&b_qfull[qi & 1], qi >> 1);
+        const int n = min(QN, (it.w.nv - qt * QN + 31) & ~31);
+        const uint32_t id = tc_idesc_16(BF, false, n);
+        const uint64_t qd = q_desc + (uint64_t)(((qi & 1) * C::QB) >> 4);
 #pragma unroll
-          for (int k = 0; k < D / 16; ++k)
-            mma_ss(tmem + buf * QN, kd + (((k >> 2) * (128 * 128) + (k & 3) * 32) >> 4),
-                   qd + (((k >> 2) * (QN * 128) + (k & 3) * 32) >> 4), id, k > 0);
-          tc_commit(&b_s[buf]);
-          if (!res) tc_commit(&b_qempty[qi & 1]);
-          if (qt == nqt - 1) tc_commit(&b_kempty[slot]);
+        for (int h = 0; h < 2; ++h) {
+          if (!ok || h >= nh) continue;
+          const int slot = (kc + h) % NS, buf = 2 * h + (jc[h] & 1);
+          ok = (qt > q_first || wait(&b_kfull[slot], (kc + h) / NS)) &&
+               (jc[h] < 2 || wait(&b_sfree[buf], (jc[h] >> 1) - 1));
+          if (!ok) continue;
+          tc_fence_after();
+          if (leader) {
+            const uint64_t kd = k_desc + (uint64_t)((slot * C::KB) >> 4);
+#pragma unroll
+            for (int k = 0; k < D / 16; ++k)
+              mma_ss(tmem + buf * QN, kd + (((k >> 2) * (128 * 128) + (k & 3) * 32) >> 4),
+                     qd + (((k >> 2) * (QN * 128) + (k & 3) * 32) >> 4), id, k > 0);
+            tc_commit(&b_s[buf]);
+            if (qt == nqt - 1) tc_commit(&b_kempty[slot]);
+            if (!res && h == nh - 1) tc_commit(&b_qempty[qi & 1]);
+          }
+          __syncwarp();
+          ++jc[h];
         }
-        __syncwarp();
         if (!res) ++qc;
       }
-      if (q_first < nqt) ++uc;
+      if (q_first < nqt) kc += nh;
       if (!ok) break;
       const bool moved = it.next();
       if (moved && res) {
@@ -340,27 +357,36 @@ __global__ void __launch_bounds__(kWeighThreads, 1)
       const int v0 = qt * QN, n = min(QN, (it.w.nv - v0 + 31) & ~31);
       const uint32_t dst = smem_u32(sm_q + slot * C::QB);
       const T* qp = static_cast<const T*>(p.q);
-      for (int x = th; x < n * CH; x += 64) {
-        const int r = x / CH, c = x % CH, vec = v0 + r;
+      // each thread's lse first: on its way while the copies are issued
+      constexpr int LR = QN / 64;
+      float lse[LR];
+#pragma unroll
+      for (int k = 0; k < LR; ++k) {
+        const int vec = v0 + th + k * 64;
+        lse[k] = INFINITY;                  // no query vector: weight 0
+        if (vec < it.w.nv) {
+          const int i = row_of(p, vec);
+          lse[k] = p.lse[(size_t)(it.w.s.r0 + i) * p.nh + it.g * p.hpg + vec - i * p.hpg];
+        }
+      }
+      // 64 threads: CH chunks of 64 / CH rows at a time
+#pragma unroll 4
+      for (int r = th / CH; r < n; r += 64 / CH) {
+        const int c = th % CH, vec = v0 + r;
         const bool in = vec < it.w.nv;
-        const int i = in ? vec / p.hpg : 0, h = in ? vec % p.hpg : 0;
+        const int i = in ? row_of(p, vec) : 0, h = in ? vec - i * p.hpg : 0;
         const T* src = qp + (in ? (size_t)(it.w.s.r0 + i) * p.q_row + (size_t)(it.g * p.hpg + h) * D + c * 8 : 0);
         asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;"
                      :: "r"(dst + (c >> 3) * (QN * 128) + r * 128 + (((c & 7) ^ (r & 7)) << 4)), "l"(src), "r"(in ? 16 : 0)
                      : "memory");
       }
       asm volatile("cp.async.commit_group;" ::: "memory");
-      for (int r = th; r < n; r += 64) {
-        const int vec = v0 + r;
-        float lse = INFINITY;               // no query vector: weight 0
-        int lim = 0;
-        if (vec < it.w.nv) {
-          const int i = vec / p.hpg;
-          lse = p.lse[(size_t)(it.w.s.r0 + i) * p.nh + it.g * p.hpg + vec % p.hpg] * 1.4426950408889634f;
-          lim = min(it.w.s.len, it.w.s.len - it.w.s.t + i + 1);
-        }
-        s_lse[slot][r] = lse;
-        s_lim[slot][r] = lim;
+#pragma unroll
+      for (int k = 0; k < LR; ++k) {
+        const int vec = v0 + th + k * 64;
+        s_nlse[slot][th + k * 64] = lse[k] * -1.4426950408889634f;
+        s_lim[slot][th + k * 64] =
+            vec < it.w.nv ? min(it.w.s.len, it.w.s.len - it.w.s.t + row_of(p, vec) + 1) : 0;
       }
       tell(false);
       pending = qc++;
@@ -381,77 +407,85 @@ __global__ void __launch_bounds__(kWeighThreads, 1)
     else give_up();
   } else {
     // ------------------------------------------------------------ sums: thread = key
-    const int wg = warp >> 2, r = tid & 127;
-    const uint32_t lanes = tmem + ((uint32_t)((warp & 3) * 32) << 16);
+    const int h = warp >> 2, r = tid & 127;
+    const uint32_t lanes = tmem + ((uint32_t)((warp & 3) * 32) << 16) + h * 2 * QN;
     const uint64_t mul2 = pack64(__float_as_uint(p.qmul), __float_as_uint(p.qmul));
-    int jc = 0, qc = 0, uc = 0, q_base = it.qt0();
+    int jc = 0, qc = 0, q_base = it.qt0(), q_seen = 0;      // q_seen: query tiles known to be there
     while (!it.done()) {
-      const int nqt = it.w.nqt, key = it.tile * 128 + r;
-      const bool res = it.resident();
+      const int nqt = it.w.nqt, key = it.tile * kUnit + h * 128 + r;
+      const bool res = it.resident(), here = h < it.halves();
       const size_t at = ((size_t)it.b * p.map.nk + it.g) * p.map.cap + key;
-      const bool mine = wg == 0 && key < it.w.s.len;
+      const bool mine = key < it.w.s.len;
       const float w0 = mine && p.weight ? p.weight[at] : 0.f;   // under way during the products
-      uint64_t sum[2] = {0, 0};
-      for (int qt = it.qt0(); qt < nqt; ++qt, ++jc) {
-        const int qi = res ? qc + qt - q_base : qc, buf = jc % kSBufs, slot = qi & 1;
-        // lse and limits, then S; a thread whose wait gave up goes on (its warp stays
-        // together) and writes nothing
-        ok &= tc_wait(&b_qfull[slot], (uint32_t)((qi >> 1) & 1), &s_abort) &&
-              tc_wait(&b_s[buf], (uint32_t)((jc / kSBufs) & 1), &s_abort);
-        tc_fence_after();
-        const int n = min(QN, (it.w.nv - qt * QN + 31) & ~31);
-        // some row of the tile does not see the whole key tile
-        const bool mask = it.tile * 128 + 128 > it.w.s.len - it.w.s.t + qt * QN / p.hpg + 1;
-        for (int c = wg * 32; c < n; c += 64) {
-          uint32_t x[32];
-          tc_ld32(lanes + buf * QN + c, x);
-          wait_ld(x);
+      uint64_t sum[4] = {0, 0, 0, 0};
+      for (int qt = it.qt0(); qt < nqt; ++qt) {
+        const int qi = res ? qc + qt - q_base : qc, buf = jc & 1, slot = qi & 1;
+        // lse and limits; a thread whose wait gave up goes on (its warp stays together) and
+        // writes nothing
+        if (qi >= q_seen) {
+          ok &= tc_wait(&b_qfull[slot], (uint32_t)((qi >> 1) & 1), &s_abort);
+          q_seen = qi + 1;
+        }
+        if (here) {
+          ok &= tc_wait(&b_s[2 * h + buf], (uint32_t)((jc >> 1) & 1), &s_abort);
+          tc_fence_after();
+          const int n = min(QN, (it.w.nv - qt * QN + 31) & ~31);
+          // columns [c, c + W): weights into the sums
+          auto columns = [&](int c, auto width, auto masked) {
+            constexpr int W = decltype(width)::value;
+            uint32_t x[W / 32][32];
 #pragma unroll
-          for (int k = 0; k < 32; k += 4) {
-            const float4 ls = *reinterpret_cast<const float4*>(&s_lse[slot][c + k]);
-            const float l4[4] = {-ls.x, -ls.y, -ls.z, -ls.w};
-            float e[4];
-#pragma unroll
-            for (int i = 0; i < 4; i += 2)
-              unpack64(fma2(pack64(x[k + i], x[k + i + 1]), mul2, pack64(__float_as_uint(l4[i]), __float_as_uint(l4[i + 1]))),
-                       e[i], e[i + 1]);
-#pragma unroll
-            for (int i = 0; i < 4; ++i) e[i] = ex2(e[i]);
-            if (mask) {
-              const int4 lm = *reinterpret_cast<const int4*>(&s_lim[slot][c + k]);
-              const int l[4] = {lm.x, lm.y, lm.z, lm.w};
-#pragma unroll
-              for (int i = 0; i < 4; ++i)
-                if (key >= l[i]) e[i] = 0.f;
+            for (int i = 0; i < W / 32; ++i) tc_ld32(lanes + buf * QN + c + i * 32, x[i]);
+            wait_ld(x);
+            if (c + W >= n) {               // S is in registers: the buffer is free
+              tc_fence_before();
+              __syncwarp();
+              if (lane == 0) mbar_arrive(&b_sfree[2 * h + buf]);
             }
 #pragma unroll
-            for (int i = 0; i < 4; i += 2) sum[i >> 1] = add2(sum[i >> 1], pack64(__float_as_uint(e[i]), __float_as_uint(e[i + 1])));
+            for (int k = 0; k < W; k += 4) {
+              const ulonglong2 l2 = *reinterpret_cast<const ulonglong2*>(&s_nlse[slot][c + k]);
+              float e[4];
+              unpack64(fma2(pack64(x[k >> 5][k & 31], x[k >> 5][(k & 31) + 1]), mul2, l2.x), e[0], e[1]);
+              unpack64(fma2(pack64(x[k >> 5][(k & 31) + 2], x[k >> 5][(k & 31) + 3]), mul2, l2.y), e[2], e[3]);
+#pragma unroll
+              for (int i = 0; i < 4; ++i) e[i] = ex2(e[i]);
+              if constexpr (decltype(masked)::value) {
+                const int4 lm = *reinterpret_cast<const int4*>(&s_lim[slot][c + k]);
+                e[0] = key < lm.x ? e[0] : 0.f;
+                e[1] = key < lm.y ? e[1] : 0.f;
+                e[2] = key < lm.z ? e[2] : 0.f;
+                e[3] = key < lm.w ? e[3] : 0.f;
+              }
+              sum[(k >> 1) & 2] = add2(sum[(k >> 1) & 2], pack64(__float_as_uint(e[0]), __float_as_uint(e[1])));
+              sum[((k >> 1) & 2) + 1] = add2(sum[((k >> 1) & 2) + 1], pack64(__float_as_uint(e[2]), __float_as_uint(e[3])));
+            }
+          };
+          // some row of the tile does not see all keys of this half
+          const bool mask =
+              it.tile * kUnit + h * 128 + 128 >
+              it.w.s.len - it.w.s.t + row_of(p, qt * QN) + 1;
+          for (int c = 0; c < n; c += 64) {
+            if (mask) {
+              columns(c, Int<32>{}, std::true_type{});
+              if (c + 32 < n) columns(c + 32, Int<32>{}, std::true_type{});
+            } else if (c + 32 < n) {
+              columns(c, Int<64>{}, std::false_type{});
+            } else {
+              columns(c, Int<32>{}, std::false_type{});
+            }
           }
+          ++jc;
         }
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) {
-          mbar_arrive(&b_sfree[buf]);
-          if (!res) mbar_arrive(&b_qempty[slot]);
+        if (!res) {
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&b_qempty[slot]);
+          ++qc;
         }
-        if (!res) ++qc;
       }
       float a0, a1;
-      unpack64(add2(sum[0], sum[1]), a0, a1);
-      float w = a0 + a1;
-      // the second warpgroup's columns reach the first through shared memory, two buffers
-      const int pb = uc & 1, use = uc >> 1;
-      if (wg == 1) {
-        if (use > 0) ok &= tc_wait(&b_pfree[pb], (uint32_t)((use - 1) & 1), &s_abort);
-        s_part[pb][r] = w;
-        mbar_arrive(&b_part[pb]);
-      } else {
-        ok &= tc_wait(&b_part[pb], (uint32_t)(use & 1), &s_abort);
-        w += s_part[pb][r];
-        mbar_arrive(&b_pfree[pb]);
-        if (mine && ok) p.out[at] = w0 + w;
-      }
-      ++uc;
+      unpack64(add2(add2(sum[0], sum[1]), add2(sum[2], sum[3])), a0, a1);
+      if (mine && ok) p.out[at] = w0 + (a0 + a1);
       const bool moved = it.next();
       if (moved && res) {
         __syncwarp();
@@ -507,6 +541,9 @@ int swa_paged_weigh(const swa_paged_weigh_args* a, cudaStream_t stream) {
   const size_t bytes = (size_t)c.B * c.nk * p.map.cap * 4;
   if (a->weight && a->weight != a->out && bytes_overlap(a->weight, bytes, a->out, bytes)) return SWA_E_SHAPE;
   p.T = a->T; p.nh = a->nh; p.hpg = a->nh / c.nk; p.max_rows = a->max_rows;
+  p.hpg_shift = 31;
+  while ((1 << (p.hpg_shift - 31)) < p.hpg) ++p.hpg_shift;
+  p.hpg_mul = (uint32_t)(((1ull << p.hpg_shift) + p.hpg - 1) / p.hpg);
   p.qmul = a->scale * 1.4426950408889634f;
   p.q = a->q; p.q_row = a->q_row;
   p.lse = a->lse; p.weight = a->weight; p.out = a->out; p.err = a->err;
