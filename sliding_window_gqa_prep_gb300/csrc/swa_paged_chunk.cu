@@ -268,18 +268,27 @@ __global__ void __launch_bounds__(ChunkCfg<D>::THREADS, 1)
     // address field never carries
     const uint64_t q_desc = sw128_desc(smem_u32(sm + t * C::QB), 16), k_desc = sw128_desc(smem_u32(sm_kv), 16);
     const uint64_t v_desc = sw128_desc(smem_u32(sm_kv), KT * 128);
+    bool ok = true;
     const int other = NT == 2 ? max(0, min(n_tile[NT - 1 - t] - j0, n)) : 0;
     auto pass_turn = [&]() {
       if (NT == 2) mbar_arrive(&b_turn[1 - t]);
     };
     // before this tile's j-th P V: after tile 0's j-th (tile 1), after tile 1's j-1st (tile 0)
+    // A wait that gave up leaves ok false and the role goes on to its end (its warp stays
+    // together without votes, which cost 4 % here): what follows only touches this CTA's own
+    // shared memory and TMEM, and nothing of it is written.
+    auto until = [&](uint64_t* bar, int phase) { ok &= tc_wait(bar, (uint32_t)(phase & 1), &s_abort); };
     auto my_turn = [&](int j) {
-      if (NT == 1) return true;
-      return t == 0 ? j == 0 || other == 0 || wait(&b_turn[0], j - 1) : j >= other || wait(&b_turn[1], j);
+      if (NT == 1) return;
+      if (t == 0) {
+        if (j > 0 && other > 0) until(&b_turn[0], j - 1);
+      } else if (j < other) {
+        until(&b_turn[1], j);
+      }
     };
     auto s_mma = [&](int j) {                               // S of tile j
       const int slot = pos_k<SB>(j) % NS;
-      if (!wait(&b_full[slot], pos_k<SB>(j) / NS)) return false;
+      until(&b_full[slot], pos_k<SB>(j) / NS);
       tc_fence_after();
       if (leader) {
         const uint64_t kd = k_desc + (uint64_t)((slot * C::SLOT) >> 4);
@@ -291,15 +300,15 @@ __global__ void __launch_bounds__(ChunkCfg<D>::THREADS, 1)
         tc_commit(&b_s[t * SB + j % SB]);
       }
       __syncwarp();
-      return true;
     };
     auto pv_mma = [&](int j) {                              // O += P V of tile j
       const int pos = pos_v<SB>(j, n), slot = pos % NS;
       const uint64_t vd = v_desc + (uint64_t)((slot * C::SLOT) >> 4);
-      if (!wait(&b_full[slot], pos / NS) || !my_turn(j)) return false;
+      until(&b_full[slot], pos / NS);
+      my_turn(j);
 #pragma unroll
       for (int h = 0; h < 2; ++h) {                         // P arrives in halves
-        if (!wait(&b_p[t * SB + j % SB][h], j / SB)) return false;
+        until(&b_p[t * SB + j % SB][h], j / SB);
         tc_fence_after();
         if (leader) {
 #pragma unroll
@@ -312,38 +321,35 @@ __global__ void __launch_bounds__(ChunkCfg<D>::THREADS, 1)
         }
         __syncwarp();
       }
-      return true;
     };
     // O of tile j is there: its V is done with
     auto pv_done = [&](int j) {
-      if (!wait(&b_pv[t], j)) return false;
+      until(&b_pv[t], j);
       if (leader) mbar_arrive(&b_empty[pos_v<SB>(j, n) % NS]);
       __syncwarp();
-      return true;
     };
-    bool ok = true;
     if (mine > 0) {
-      ok = wait(&b_q[t], 0);
-      if (ok && t == 1 && n_tile[0] > j0) ok = wait(&b_s[0], 0);
-      if (ok) ok = s_mma(0);
+      until(&b_q[t], 0);
+      if (t == 1 && n_tile[0] > j0) until(&b_s[0], 0);
+      s_mma(0);
     }
-    for (int j = 0; ok && j < mine; ++j) {
+    for (int j = 0; j < mine; ++j) {
       // with two S buffers the other one holds P of tile j - 1, with one S overwrites P of tile j
-      if (SB == 2 && j > 0) ok = pv_done(j - 1);
-      if (SB == 2 && ok && j + 1 < mine) ok = s_mma(j + 1);
-      if (ok) ok = pv_mma(j);
-      if (SB == 1 && ok) ok = pv_done(j);
-      if (SB == 1 && ok && j + 1 < mine) ok = s_mma(j + 1);
+      if (SB == 2 && j > 0) pv_done(j - 1);
+      if (SB == 2 && j + 1 < mine) s_mma(j + 1);
+      pv_mma(j);
+      if (SB == 1) pv_done(j);
+      if (SB == 1 && j + 1 < mine) s_mma(j + 1);
     }
-    for (int j = mine; ok && j < n; ++j) {                  // the other tile's keys: hand the slots on
+    for (int j = mine; j < n; ++j) {                        // the other tile's keys: hand the slots on
       const int pk = pos_k<SB>(j), pv = pos_v<SB>(j, n);
-      ok = wait(&b_full[pk % NS], pk / NS);
-      if (ok && leader) mbar_arrive(&b_empty[pk % NS]);
-      __syncwarp();
-      if (ok) ok = wait(&b_full[pv % NS], pv / NS);
-      if (ok && leader) mbar_arrive(&b_empty[pv % NS]);
+      until(&b_full[pk % NS], pk / NS);
+      if (leader) mbar_arrive(&b_empty[pk % NS]);
+      until(&b_full[pv % NS], pv / NS);
+      if (leader) mbar_arrive(&b_empty[pv % NS]);
       __syncwarp();
     }
+    ok = __all_sync(0xffffffffu, ok);
     if (!ok) {
       give_up();
       // what was issued finishes before TMEM goes (bounded)

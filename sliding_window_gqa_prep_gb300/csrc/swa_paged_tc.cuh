@@ -79,9 +79,9 @@ __device__ __forceinline__ void tma_2d(uint32_t dst, const CUtensorMap* map, int
                :: "r"(dst), "l"(map), "r"(smem_u32(bar)), "r"(x), "r"(y) : "memory");
 }
 
-// A wait that gives up after kWaitLimitNs; the clock is read every 64th try only (the
+// A wait that gives up after kWaitLimitNs, for the whole CTA; the clock is read every 64th try only (the
 // read takes longer than a try).
-__device__ __forceinline__ bool tc_wait(uint64_t* bar, uint32_t parity, const int* abort_flag) {
+__device__ __forceinline__ bool tc_wait(uint64_t* bar, uint32_t parity, int* abort_flag) {
   if (mbar_try_wait(bar, parity)) return true;
   uint64_t t0 = 0;
   for (uint32_t i = 1;; ++i) {
@@ -89,7 +89,8 @@ __device__ __forceinline__ bool tc_wait(uint64_t* bar, uint32_t parity, const in
     if ((i & 63) == 0) {
       const uint64_t now = global_ns();
       if (t0 == 0) t0 = now;
-      if (now - t0 > kWaitLimitNs || *(const volatile int*)abort_flag) return false;
+      if (now - t0 > kWaitLimitNs) *(volatile int*)abort_flag = 1;
+      if (*(volatile int*)abort_flag) return false;
     }
   }
 }
