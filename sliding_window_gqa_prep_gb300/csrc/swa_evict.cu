@@ -1,19 +1,28 @@
 // Eviction of cached keys by their accumulated weight (swa_paged_evict).
+//
+// One cluster per (sequence, KV head) does the whole eviction in one launch, each CTA a
+// contiguous share of the slots:
+//   1. keys of its slots into shared memory (an order-preserving 32-bit key);
+//   2. the n'-th largest key by three histogram passes of 11, 11 and 10 bits; the CTAs'
+//      histograms are summed through distributed shared memory;
+//   3. two walks in slot order (a warp a run of slots, ranks by ballots): the first counts
+//      the freed and the moved slots, the second numbers them, writes the kept slots'
+//      weights and positions and the two lists;
+//   4. the rows that move are copied, a half-warp a row of K or V. A source lies at or
+//      behind n', its destination before it: no row is both read and written.
+// Steps 1 to 3 are chains of barriers and short passes, so the CTAs' shares stay small
+// (kSlotsPerCta) while the cluster may grow (8 CTAs at most); copies are bound by memory.
+#include <cooperative_groups.h>
+
 #include "swa_paged.cuh"
 
 namespace swa {
+namespace cg = cooperative_groups;
 
-// ---------------------------------------------------------------------------
-// select: one CTA per (sequence, KV head) finds the threshold key of the n'
-// first slots by a radix select over an order-preserving 32-bit key (four histogram
-// passes of 8 bits), then numbers the freed and the moved slots in slot order with
-// block scans, and writes the kept slots' weights and positions. move: a warp a moved
-// row copies K, V, weight and position; its source lies at or behind n', its
-// destination before it, so no row is both read and written.
-// ---------------------------------------------------------------------------
 struct PagedEvictParams {
   PagedMap map;
   int hd, keep, sinks, list_cap;
+  int key_slots;               // keys of a CTA that fit in its shared memory
   const float* weight;
   const int32_t* slot_pos;
   const int32_t* recent_from;
@@ -22,163 +31,244 @@ struct PagedEvictParams {
   int32_t* lens_out;
   void* ck;
   void* cv;
-  int* ws_count;               // [B][nk]
   int* ws_dst;                 // [B][nk][list_cap]
   int* ws_src;                 // [B][nk][list_cap]
   uint32_t* err;
 };
 
-constexpr int kEThreads = 1024;
+constexpr int kEThreads = 512, kEWarps = kEThreads / 32;
+constexpr int kSlotsPerCta = 4096;          // a cluster of (capacity / this), 1 to 8, CTAs
+constexpr int kMaxKeySlots = 40960;         // keys of a CTA in shared memory; longer shares are read again
+constexpr int kBins = 2048;
 
 // Descending order of slots as descending order of this key: protected slots first,
 // then NaN, then the weights (-0 as 0).
-__device__ __forceinline__ uint32_t evict_key(float w, int pos, int sinks, int recent) {
-  if (pos < sinks || pos >= recent) return 0xffffffffu;
+__device__ __forceinline__ uint32_t evict_key(float w, bool safe) {
+  if (safe) return 0xffffffffu;
   if (w != w) return 0xfffffffeu;
   const uint32_t u = __float_as_uint(w + 0.f);
   return (u & 0x80000000u) ? ~u : u | 0x80000000u;     // +inf: 0xff800000
 }
 
-// Exclusive sum of a small per-thread count over the block, and the block's total.
-__device__ __forceinline__ int block_rank(bool flag, int* warp_sums, int& total) {
-  const unsigned m = __ballot_sync(0xffffffffu, flag);
+// Exclusive sums over the block of a per-thread count; s_sums holds a value a warp.
+__device__ __forceinline__ int block_exclusive(int v, int* s_sums) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  __syncthreads();
-  if (lane == 0) warp_sums[warp] = __popc(m);
-  __syncthreads();
-  int before = 0;
-  total = 0;
+  int incl = v;
 #pragma unroll
-  for (int w = 0; w < kEThreads / 32; ++w) {
-    const int c = warp_sums[w];
-    if (w < warp) before += c;
-    total += c;
+  for (int o = 1; o < 32; o <<= 1) {
+    const int x = __shfl_up_sync(0xffffffffu, incl, o);
+    if (lane >= o) incl += x;
   }
-  return before + __popc(m & ((1u << lane) - 1));
+  __syncthreads();
+  if (lane == 31) s_sums[warp] = incl;
+  __syncthreads();
+  int before = lane < warp && lane < kEWarps ? s_sums[lane] : 0;
+#pragma unroll
+  for (int o = 16; o; o >>= 1) before += __shfl_xor_sync(0xffffffffu, before, o);
+  return before + incl - v;
 }
 
-__global__ void __launch_bounds__(kEThreads) paged_evict_select_kernel(const PagedEvictParams p) {
-  __shared__ int hist[256];
-  __shared__ int warp_sums[kEThreads / 32];
-  __shared__ uint32_t s_prefix;
+__global__ void __launch_bounds__(kEThreads, 2) paged_evict_kernel(const PagedEvictParams p) {
+  extern __shared__ uint32_t s_keys[];
+  __shared__ __align__(16) int hist[3][kBins];
+  __shared__ int s_sums[kEWarps], s_eq[kEWarps], s_freed[kEWarps], s_moved[kEWarps];
+  __shared__ int s_tot[2];                  // this CTA's freed and moved slots
+  __shared__ uint32_t s_digit;
   __shared__ int s_need;
-  const int tid = threadIdx.x, g = blockIdx.x, b = blockIdx.y;
+  cg::cluster_group cluster = cg::this_cluster();
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int CS = (int)cluster.num_blocks(), rank = (int)cluster.block_rank();
+  const int item = blockIdx.x / CS, b = item / p.map.nk, g = item % p.map.nk;
   pdl_wait();
   pdl_trigger();
   int n = p.map.lens[b];
   if (n < 0 || n > p.map.cap) {
-    if (tid == 0 && g == 0) set_err(p.err, SWA_DERR_META);
+    if (tid == 0 && g == 0 && rank == 0) set_err(p.err, SWA_DERR_META);
     n = n < 0 ? 0 : p.map.cap;
   }
   const int keep = min(n, p.keep);
-  const size_t bg = (size_t)b * p.map.nk + g;
-  const float* w = p.weight + bg * p.map.cap;
-  const int32_t* pos = p.slot_pos + bg * p.map.cap;
-  float* wo = p.weight_out + bg * p.map.cap;
-  int32_t* po = p.slot_pos_out + bg * p.map.cap;
-  if (tid == 0 && g == 0) p.lens_out[b] = keep;
-  if (n <= p.keep) {                       // everything stays
-    for (int j = tid; j < n; j += kEThreads) {
+  const size_t base = (size_t)item * p.map.cap;
+  const float* w = p.weight + base;
+  const int32_t* pos = p.slot_pos + base;
+  float* wo = p.weight_out + base;
+  int32_t* po = p.slot_pos_out + base;
+  if (tid == 0 && g == 0 && rank == 0) p.lens_out[b] = keep;
+  // this CTA's slots [lo, hi), a multiple of 32 a CTA
+  const int share = ((n + CS - 1) / CS + 31) & ~31;
+  const int lo = min(n, rank * share), hi = min(n, lo + share);
+  if (n <= p.keep) {                        // everything stays (the same for the whole cluster)
+    for (int j = lo + tid; j < hi; j += kEThreads) {
       wo[j] = w[j];
       po[j] = pos[j];
     }
-    if (tid == 0) p.ws_count[bg] = 0;
     return;
   }
-  const int recent = p.recent_from ? p.recent_from[b] : 0x7fffffff;
   const bool any_recent = p.recent_from != nullptr;
-  auto key_of = [&](int j) {
+  const int recent = any_recent ? p.recent_from[b] : 0;
+  auto make_key = [&](int j) {
     const int ps = pos[j];
-    return evict_key(w[j], any_recent ? ps : min(ps, 0x7ffffffe), p.sinks, recent);
+    return evict_key(w[j], ps < p.sinks || (any_recent && ps >= recent));
   };
-  // the keep-th largest key, eight bits at a time
+  const bool cached = share <= p.key_slots;
+  auto key_of = [&](int j) { return cached ? s_keys[j - lo] : make_key(j); };
+  for (int i = tid; i < 3 * kBins; i += kEThreads) (&hist[0][0])[i] = 0;
+  if (cached) {
+#pragma unroll 4
+    for (int j = lo + tid; j < hi; j += kEThreads) s_keys[j - lo] = make_key(j);
+  }
+  __syncthreads();
+
+  // the keep-th largest key: digits of 11, 11 and 10 bits
   uint32_t prefix = 0;
-  int need = keep;                         // slots still to take among keys with this prefix
-  for (int shift = 24; shift >= 0; shift -= 8) {
-    if (tid < 256) hist[tid] = 0;
-    __syncthreads();
-    for (int j = tid; j < n; j += kEThreads) {
+  int need = keep;                          // slots still to take among keys with this prefix
+#pragma unroll 1
+  for (int pass = 0; pass < 3; ++pass) {
+    const int shift = pass == 0 ? 21 : pass == 1 ? 10 : 0, bits = pass == 2 ? 10 : 11;
+    for (int j = lo + tid; j < hi; j += kEThreads) {
       const uint32_t k = key_of(j);
-      if (shift == 24 || (k >> (shift + 8)) == (prefix >> (shift + 8))) atomicAdd(&hist[(k >> shift) & 255], 1);
+      if (pass == 0 || k >> (shift + bits) == prefix) atomicAdd(&hist[pass][(k >> shift) & ((1u << bits) - 1)], 1);
     }
-    __syncthreads();
-    if (tid == 0) {
-      int c = 0, d = 255;
-      for (; d > 0; --d) {
-        if (c + hist[d] >= need) break;
-        c += hist[d];
+    cluster.sync();
+    // thread t holds the bins 4t .. 4t + 3 counted from the top, summed over the cluster
+    int c[4] = {0, 0, 0, 0};
+    const int top = (1 << bits) - 4 - 4 * tid;
+    if (top >= 0) {
+      for (int r = 0; r < CS; ++r) {
+        const int4 v = *reinterpret_cast<const int4*>(cluster.map_shared_rank(&hist[pass][top], r));
+        c[0] += v.w;
+        c[1] += v.z;
+        c[2] += v.y;
+        c[3] += v.x;
       }
-      s_prefix = prefix | ((uint32_t)d << shift);
-      s_need = need - c;
+    }
+    int before = block_exclusive(c[0] + c[1] + c[2] + c[3], s_sums);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      if (before < need && need <= before + c[i]) {
+        s_digit = (uint32_t)(top + 3 - i);
+        s_need = need - before;
+      }
+      before += c[i];
     }
     __syncthreads();
-    prefix = s_prefix;
+    prefix = prefix << bits | s_digit;
     need = s_need;
   }
-  // keys above `prefix` stay, and the first `need` slots that equal it
-  int* const dst = p.ws_dst + bg * p.list_cap;
-  int* const src = p.ws_src + bg * p.list_cap;
-  int eq_seen = 0, n_dst = 0, n_src = 0;
-  for (int j0 = 0; j0 < n; j0 += kEThreads) {
-    const int j = j0 + tid;
-    const bool in = j < n;
+  // keys above `prefix` stay, and of those that equal it the first `need` in slot order;
+  // the CTAs before this one hold eq_before of them
+  const uint32_t digit = prefix & 1023u;
+  int eq_before = 0;
+  for (int r = 0; r < rank; ++r) eq_before += *cluster.map_shared_rank(&hist[2][digit], r);
+
+  // walks: warp w takes slots [wlo, whi) in order
+  const int run = ((hi - lo + kEWarps - 1) / kEWarps + 31) & ~31;
+  const int wlo = min(hi, lo + warp * run), whi = min(hi, wlo + run);
+  const unsigned below = (1u << lane) - 1;
+  int cnt = 0;
+  for (int j = wlo + lane; j - lane < whi; j += 32) cnt += __popc(__ballot_sync(0xffffffffu, j < whi && key_of(j) == prefix));
+  if (lane == 0) s_eq[warp] = cnt;
+  __syncthreads();
+  int eq = eq_before;
+  for (int i = 0; i < warp; ++i) eq += s_eq[i];
+  const int eq0 = eq;
+  // the slot's fate in the walk; `eq` runs along
+  auto step = [&](int j, bool& freed, bool& moved) {
+    const bool in = j < whi;
     const uint32_t k = in ? key_of(j) : 0u;
-    const bool eq = in && k == prefix;
-    int total;
-    const int rank = block_rank(eq, warp_sums, total);
-    const bool kept = in && (k > prefix || (eq && eq_seen + rank < need));
-    eq_seen += total;
-    const bool freed = in && j < keep && !kept, moved = kept && j >= keep;
+    const bool is_eq = in && k == prefix;
+    const unsigned m = __ballot_sync(0xffffffffu, is_eq);
+    const bool kept = in && (k > prefix || (is_eq && eq + __popc(m & below) < need));
+    eq += __popc(m);
+    freed = in && j < keep && !kept;
+    moved = kept && j >= keep;
+    return kept;
+  };
+  int n_freed = 0, n_moved = 0;
+  for (int j = wlo + lane; j - lane < whi; j += 32) {
+    bool freed, moved;
+    step(j, freed, moved);
+    n_freed += __popc(__ballot_sync(0xffffffffu, freed));
+    n_moved += __popc(__ballot_sync(0xffffffffu, moved));
+  }
+  if (lane == 0) {
+    s_freed[warp] = n_freed;
+    s_moved[warp] = n_moved;
+  }
+  __syncthreads();
+  n_freed = n_moved = 0;
+  for (int i = 0; i < warp; ++i) {
+    n_freed += s_freed[i];
+    n_moved += s_moved[i];
+  }
+  if (warp == kEWarps - 1 && lane == 0) {
+    s_tot[0] = n_freed + s_freed[warp];
+    s_tot[1] = n_moved + s_moved[warp];
+  }
+  cluster.sync();
+  int count = 0;                            // rows that move, in the whole cluster
+  for (int r = 0; r < CS; ++r) {
+    const int f = cluster.map_shared_rank(s_tot, r)[0], v = cluster.map_shared_rank(s_tot, r)[1];
+    if (r < rank) {
+      n_freed += f;
+      n_moved += v;
+    }
+    count += v;
+  }
+  int* const dst = p.ws_dst + (size_t)item * p.list_cap;
+  int* const src = p.ws_src + (size_t)item * p.list_cap;
+  eq = eq0;
+  for (int j = wlo + lane; j - lane < whi; j += 32) {
+    bool freed, moved;
+    const bool kept = step(j, freed, moved);
+    const unsigned mf = __ballot_sync(0xffffffffu, freed), mm = __ballot_sync(0xffffffffu, moved);
+    if (freed) dst[n_freed + __popc(mf & below)] = j;
+    if (moved) src[n_moved + __popc(mm & below)] = j;
+    n_freed += __popc(mf);
+    n_moved += __popc(mm);
     if (kept && j < keep) {
       wo[j] = w[j];
       po[j] = pos[j];
     }
-    if (j0 < keep) {
-      const int r = block_rank(freed, warp_sums, total);
-      if (freed) dst[n_dst + r] = j;
-      n_dst += total;
-    }
-    if (j0 + kEThreads > keep) {
-      const int r = block_rank(moved, warp_sums, total);
-      if (moved) src[n_src + r] = j;
-      n_src += total;
-    }
   }
-  if (tid == 0) p.ws_count[bg] = n_src;    // = n_dst: keep slots stay in all
-}
+  cluster.sync();                           // the lists are complete (and no histogram is read any more)
 
-constexpr int kMoveWarps = 8;
-constexpr int kMoveRows = 4;               // rows of a warp
-
-__global__ void __launch_bounds__(kMoveWarps * 32) paged_evict_move_kernel(const PagedEvictParams p) {
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int g = blockIdx.y, b = blockIdx.z;
-  pdl_wait();
-  pdl_trigger();
-  const size_t bg = (size_t)b * p.map.nk + g;
-  const int count = p.ws_count[bg];
+  // copies: 16 lanes a row of K or V, kRows rows of a half-warp under way at a time
+  constexpr int kRows = 4;
   const int32_t* table = p.map.table + (size_t)b * p.map.max_pages;
-  const int ch = p.hd / 8;                 // 16-byte chunks of a row: 8, 16 or 32
-  for (int r = 0; r < kMoveRows; ++r) {
-    const int i = (blockIdx.x * kMoveWarps + warp) * kMoveRows + r;
-    if (i >= count) return;
-    const int to = p.ws_dst[bg * p.list_cap + i], of = p.ws_src[bg * p.list_cap + i];
-    const int pt = table[to >> p.map.page_shift], pf = table[of >> p.map.page_shift];
-    const int mask = (1 << p.map.page_shift) - 1;
-    if (lane == 0) {
-      p.weight_out[bg * p.map.cap + to] = p.weight[bg * p.map.cap + of];
-      p.slot_pos_out[bg * p.map.cap + to] = p.slot_pos[bg * p.map.cap + of];
+  const int ch = p.hd / 8, mask = (1 << p.map.page_shift) - 1;   // 16-byte chunks of a row: 8, 16 or 32
+  const int hw = tid >> 4, l16 = tid & 15;
+  constexpr int kHalfWarps = kEThreads / 16;
+  // jobs: row i of K (2 i) and of V (2 i + 1), dealt to the cluster's half-warps
+  const int jobs = 2 * count, stride = CS * kHalfWarps;
+  for (int q = rank * kHalfWarps + hw; q < jobs; q += kRows * stride) {
+    uint4* to[kRows];
+    uint4 v[kRows][2];
+#pragma unroll
+    for (int k = 0; k < kRows; ++k) {
+      const int job = q + k * stride;
+      to[k] = nullptr;
+      if (job >= jobs) continue;
+      const int a = dst[job >> 1], z = src[job >> 1];
+      const int pt = table[a >> p.map.page_shift], pf = table[z >> p.map.page_shift];
+      if ((job & 1) == 0 && l16 == 0) {
+        wo[a] = w[z];
+        po[a] = pos[z];
+      }
+      if (!page_ok(p.map, pt) || !page_ok(p.map, pf)) {
+        if (l16 == 0) set_err(p.err, SWA_DERR_PAGE);
+        continue;
+      }
+      uint4* pool = static_cast<uint4*>(job & 1 ? p.cv : p.ck);
+      to[k] = pool + ((((size_t)pt * p.map.nk + g) << p.map.page_shift) + (a & mask)) * ch;
+      const uint4* from = pool + ((((size_t)pf * p.map.nk + g) << p.map.page_shift) + (z & mask)) * ch;
+      if (l16 < ch) v[k][0] = from[l16];
+      if (l16 + 16 < ch) v[k][1] = from[l16 + 16];
     }
-    if (!page_ok(p.map, pt) || !page_ok(p.map, pf)) {
-      if (lane == 0) set_err(p.err, SWA_DERR_PAGE);
-      continue;
-    }
-    const size_t at = ((((size_t)pt * p.map.nk + g) << p.map.page_shift) + (to & mask)) * ch;
-    const size_t from = ((((size_t)pf * p.map.nk + g) << p.map.page_shift) + (of & mask)) * ch;
-    for (int c = lane; c < 2 * ch; c += 32) {
-      uint4* base = static_cast<uint4*>(c < ch ? p.ck : p.cv);
-      const int cc = c < ch ? c : c - ch;
-      base[at + cc] = base[from + cc];
+#pragma unroll
+    for (int k = 0; k < kRows; ++k) {
+      if (!to[k]) continue;
+      if (l16 < ch) to[k][l16] = v[k][0];
+      if (l16 + 16 < ch) to[k][l16 + 16] = v[k][1];
     }
   }
 }
@@ -203,7 +293,7 @@ extern "C" {
 size_t swa_paged_evict_workspace_size(const swa_paged_evict_args* a) {
   if (!a || !evict_sizes_ok(a)) return 0;
   const size_t items = (size_t)a->cache.B * a->cache.nk;
-  return up256s(items * 4) + 2 * up256s(items * evict_list_cap(a) * 4);
+  return 2 * up256s(items * evict_list_cap(a) * 4);
 }
 
 int swa_paged_evict(const swa_paged_evict_args* a, cudaStream_t stream) {
@@ -236,15 +326,30 @@ int swa_paged_evict(const swa_paged_evict_args* a, cudaStream_t stream) {
   p.weight_out = a->weight_out; p.slot_pos_out = a->slot_pos_out; p.lens_out = a->lens_out;
   p.ck = c.k; p.cv = c.v;
   char* ws = static_cast<char*>(a->workspace);
-  p.ws_count = reinterpret_cast<int*>(ws);
-  p.ws_dst = reinterpret_cast<int*>(ws + up256s(items * 4));
-  p.ws_src = reinterpret_cast<int*>(ws + up256s(items * 4) + up256s(items * evict_list_cap(a) * 4));
+  p.ws_dst = reinterpret_cast<int*>(ws);
+  p.ws_src = reinterpret_cast<int*>(ws + need / 2);
   p.err = a->err;
-  const int rc2 = finish_launch(launch_pdl(paged_evict_select_kernel, dim3(c.nk, c.B), dim3(kEThreads), 0, stream, p));
-  if (rc2 != SWA_OK) return rc2;
-  const unsigned per = kMoveWarps * kMoveRows;
-  return finish_launch(launch_pdl(paged_evict_move_kernel, dim3(((unsigned)p.list_cap + per - 1) / per, c.nk, c.B),
-                                  dim3(kMoveWarps * 32), 0, stream, p));
+  // a CTA for every kSlotsPerCta slots of the capacity, 1, 2, 4 or 8 of them a cluster
+  int cs = 1;
+  while (cs < 8 && (long long)cs * kSlotsPerCta < p.map.cap) cs *= 2;
+  const int share = ((p.map.cap + cs - 1) / cs + 31) & ~31;
+  p.key_slots = share < kMaxKeySlots ? share : kMaxKeySlots;
+  const cudaError_t e = allow_smem<paged_evict_kernel>(kMaxKeySlots * 4);
+  if (e != cudaSuccess) return cuda_status(e);
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)(items * cs));
+  cfg.blockDim = dim3(kEThreads);
+  cfg.dynamicSmemBytes = (size_t)p.key_slots * 4;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = (unsigned)cs;
+  attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 2;
+  return finish_launch(cudaLaunchKernelEx(&cfg, paged_evict_kernel, p));
 }
 
 }  // extern "C"

@@ -24,6 +24,20 @@ bool bytes_overlap(const void* a, size_t an, const void* b, size_t bn);
 inline bool aligned16p(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 inline size_t up256s(size_t x) { return (x + 255) & ~(size_t)255; }
 
+// Dynamic shared memory of a kernel, allowed once per device (an attribute call costs as
+// much host time as the rest of a launch's preparation).
+template <auto Kernel>
+cudaError_t allow_smem(int bytes) {
+  static bool done[64] = {};
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  if (dev >= 0 && dev < 64 && done[dev]) return cudaSuccess;
+  e = cudaFuncSetAttribute(Kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+  if (e == cudaSuccess && dev >= 0 && dev < 64) done[dev] = true;
+  return e;
+}
+
 #ifdef __CUDACC__
 
 // Rows and keys of sequence b. Rows out of range leave t = 0, a length out of

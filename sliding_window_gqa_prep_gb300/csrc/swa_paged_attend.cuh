@@ -52,20 +52,6 @@ ChunkPlan chunk_plan(const swa_paged_attend_args* a);
 int launch_paged_chunk(const swa_paged_attend_args* a, const PagedAttendParams& p, const ChunkPlan& plan, int small,
                        char* ws, cudaStream_t s);
 
-// Dynamic shared memory of a kernel, allowed once per device (an attribute call costs as
-// much host time as the rest of a launch's preparation).
-template <auto Kernel>
-cudaError_t allow_smem(int bytes) {
-  static bool done[64] = {};
-  int dev = 0;
-  cudaError_t e = cudaGetDevice(&dev);
-  if (e != cudaSuccess) return e;
-  if (dev >= 0 && dev < 64 && done[dev]) return cudaSuccess;
-  e = cudaFuncSetAttribute(Kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
-  if (e == cudaSuccess && dev >= 0 && dev < 64) done[dev] = true;
-  return e;
-}
-
 #ifdef __CUDACC__
 // Features [f, f + 8) of a finished row: out = acc / l, and its lse (the weights in l
 // carry 2^log2_scale).
