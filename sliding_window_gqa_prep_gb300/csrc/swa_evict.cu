@@ -7,8 +7,8 @@
 //      histograms are summed through distributed shared memory;
 //   3. two walks in slot order (a warp a run of slots, ranks by ballots): the first counts
 //      the freed and the moved slots, the second numbers them, writes the kept slots'
-//      weights and positions and the two lists;
-//   4. the rows that move are copied, a half-warp a row of K or V. A source lies at or
+//      weights and positions and the two lists (slots and rows);
+//   4. the rows that move are copied. A source lies at or
 //      behind n', its destination before it: no row is both read and written.
 // Steps 1 to 3 are chains of barriers and short passes, so the CTAs' shares stay small
 // (kSlotsPerCta) while the cluster may grow (8 CTAs at most); copies are bound by memory.
@@ -31,8 +31,8 @@ struct PagedEvictParams {
   int32_t* lens_out;
   void* ck;
   void* cv;
-  int* ws_dst;                 // [B][nk][list_cap]
-  int* ws_src;                 // [B][nk][list_cap]
+  int2* ws_dst;                // [B][nk][list_cap]: freed slots and their rows in the pool
+  int2* ws_src;                // [B][nk][list_cap]: moved ones
   uint32_t* err;
 };
 
@@ -133,8 +133,8 @@ __global__ void __launch_bounds__(kEThreads, 2) paged_evict_kernel(const PagedEv
     int c[4] = {0, 0, 0, 0};
     const int top = (1 << bits) - 4 - 4 * tid;
     if (top >= 0) {
-      for (int r = 0; r < CS; ++r) {
-        const int4 v = *reinterpret_cast<const int4*>(cluster.map_shared_rank(&hist[pass][top], r));
+      for (int i = 0; i < CS; ++i) {        // each CTA starts at its own
+        const int4 v = *reinterpret_cast<const int4*>(cluster.map_shared_rank(&hist[pass][top], (rank + i) & (CS - 1)));
         c[0] += v.w;
         c[1] += v.z;
         c[2] += v.y;
@@ -214,62 +214,71 @@ __global__ void __launch_bounds__(kEThreads, 2) paged_evict_kernel(const PagedEv
     }
     count += v;
   }
-  int* const dst = p.ws_dst + (size_t)item * p.list_cap;
-  int* const src = p.ws_src + (size_t)item * p.list_cap;
+  int2* const dst = p.ws_dst + (size_t)item * p.list_cap;
+  int2* const src = p.ws_src + (size_t)item * p.list_cap;
+  const int32_t* table = p.map.table + (size_t)b * p.map.max_pages;
+  const int mask = (1 << p.map.page_shift) - 1;
   eq = eq0;
-  for (int j = wlo + lane; j - lane < whi; j += 32) {
-    bool freed, moved;
-    const bool kept = step(j, freed, moved);
-    const unsigned mf = __ballot_sync(0xffffffffu, freed), mm = __ballot_sync(0xffffffffu, moved);
-    if (freed) dst[n_freed + __popc(mf & below)] = j;
-    if (moved) src[n_moved + __popc(mm & below)] = j;
-    n_freed += __popc(mf);
-    n_moved += __popc(mm);
-    if (kept && j < keep) {
-      wo[j] = w[j];
-      po[j] = pos[j];
+  for (int j0 = wlo; j0 < whi; j0 += 128) {
+    float wv[4];
+    int pv[4], pg[4];
+#pragma unroll
+    for (int u = 0; u < 4; ++u) {           // under way together: the ballots below follow one another
+      const int j = min(j0 + u * 32 + lane, n - 1);
+      wv[u] = w[j];
+      pv[u] = pos[j];
+      pg[u] = table[j >> p.map.page_shift];
+    }
+#pragma unroll
+    for (int u = 0; u < 4; ++u) {
+      const int j = j0 + u * 32 + lane;
+      bool freed, moved;
+      const bool kept = step(j, freed, moved);
+      const unsigned mf = __ballot_sync(0xffffffffu, freed), mm = __ballot_sync(0xffffffffu, moved);
+      if (freed || moved) {
+        int row = -1;                       // of head 0 .. nk - 1 of all pages: below 2^31
+        if (page_ok(p.map, pg[u])) row = ((pg[u] * p.map.nk + g) << p.map.page_shift) + (j & mask);
+        else set_err(p.err, SWA_DERR_PAGE);
+        if (freed) dst[n_freed + __popc(mf & below)] = make_int2(j, row);
+        else src[n_moved + __popc(mm & below)] = make_int2(j, row);
+      }
+      n_freed += __popc(mf);
+      n_moved += __popc(mm);
+      if (kept && j < keep) {
+        wo[j] = wv[u];
+        po[j] = pv[u];
+      }
     }
   }
   cluster.sync();                           // the lists are complete (and no histogram is read any more)
 
-  // copies: 16 lanes a row of K or V, kRows rows of a half-warp under way at a time
-  constexpr int kRows = 4;
-  const int32_t* table = p.map.table + (size_t)b * p.map.max_pages;
-  const int ch = p.hd / 8, mask = (1 << p.map.page_shift) - 1;   // 16-byte chunks of a row: 8, 16 or 32
-  const int hw = tid >> 4, l16 = tid & 15;
-  constexpr int kHalfWarps = kEThreads / 16;
-  // jobs: row i of K (2 i) and of V (2 i + 1), dealt to the cluster's half-warps
-  const int jobs = 2 * count, stride = CS * kHalfWarps;
-  for (int q = rank * kHalfWarps + hw; q < jobs; q += kRows * stride) {
-    uint4* to[kRows];
-    uint4 v[kRows][2];
+  // weights and positions of the moved slots
+  for (int i = rank * kEThreads + tid; i < count; i += CS * kEThreads) {
+    const int to = dst[i].x, of = src[i].x;
+    wo[to] = w[of];
+    po[to] = pos[of];
+  }
+  // rows: ch = 8, 16 or 32 lanes a row of K (job 2 i) or V (2 i + 1), kRows of them under way
+  constexpr int kRows = 8;
+  const int ch = p.hd / 8, lc = tid % ch, stride = CS * kEThreads / ch, jobs = 2 * count;
+  for (int q = rank * (kEThreads / ch) + tid / ch; q < jobs; q += kRows * stride) {
+    int to[kRows], of[kRows];
+    uint4 v[kRows];
+#pragma unroll
+    for (int k = 0; k < kRows; ++k) {
+      const int job = min(q + k * stride, jobs - 1);
+      to[k] = dst[job >> 1].y;
+      of[k] = src[job >> 1].y;
+    }
 #pragma unroll
     for (int k = 0; k < kRows; ++k) {
       const int job = q + k * stride;
-      to[k] = nullptr;
-      if (job >= jobs) continue;
-      const int a = dst[job >> 1], z = src[job >> 1];
-      const int pt = table[a >> p.map.page_shift], pf = table[z >> p.map.page_shift];
-      if ((job & 1) == 0 && l16 == 0) {
-        wo[a] = w[z];
-        po[a] = pos[z];
-      }
-      if (!page_ok(p.map, pt) || !page_ok(p.map, pf)) {
-        if (l16 == 0) set_err(p.err, SWA_DERR_PAGE);
-        continue;
-      }
-      uint4* pool = static_cast<uint4*>(job & 1 ? p.cv : p.ck);
-      to[k] = pool + ((((size_t)pt * p.map.nk + g) << p.map.page_shift) + (a & mask)) * ch;
-      const uint4* from = pool + ((((size_t)pf * p.map.nk + g) << p.map.page_shift) + (z & mask)) * ch;
-      if (l16 < ch) v[k][0] = from[l16];
-      if (l16 + 16 < ch) v[k][1] = from[l16 + 16];
+      if (job >= jobs || of[k] < 0) to[k] = -1;
+      if (to[k] >= 0) v[k] = static_cast<const uint4*>(job & 1 ? p.cv : p.ck)[(size_t)of[k] * ch + lc];
     }
 #pragma unroll
-    for (int k = 0; k < kRows; ++k) {
-      if (!to[k]) continue;
-      if (l16 < ch) to[k][l16] = v[k][0];
-      if (l16 + 16 < ch) to[k][l16 + 16] = v[k][1];
-    }
+    for (int k = 0; k < kRows; ++k)
+      if (to[k] >= 0) static_cast<uint4*>((q + k * stride) & 1 ? p.cv : p.ck)[(size_t)to[k] * ch + lc] = v[k];
   }
 }
 
@@ -293,7 +302,7 @@ extern "C" {
 size_t swa_paged_evict_workspace_size(const swa_paged_evict_args* a) {
   if (!a || !evict_sizes_ok(a)) return 0;
   const size_t items = (size_t)a->cache.B * a->cache.nk;
-  return 2 * up256s(items * evict_list_cap(a) * 4);
+  return 2 * up256s(items * evict_list_cap(a) * sizeof(int2));
 }
 
 int swa_paged_evict(const swa_paged_evict_args* a, cudaStream_t stream) {
@@ -326,8 +335,8 @@ int swa_paged_evict(const swa_paged_evict_args* a, cudaStream_t stream) {
   p.weight_out = a->weight_out; p.slot_pos_out = a->slot_pos_out; p.lens_out = a->lens_out;
   p.ck = c.k; p.cv = c.v;
   char* ws = static_cast<char*>(a->workspace);
-  p.ws_dst = reinterpret_cast<int*>(ws);
-  p.ws_src = reinterpret_cast<int*>(ws + need / 2);
+  p.ws_dst = reinterpret_cast<int2*>(ws);
+  p.ws_src = reinterpret_cast<int2*>(ws + need / 2);
   p.err = a->err;
   // a CTA for every kSlotsPerCta slots of the capacity, 1, 2, 4 or 8 of them a cluster
   int cs = 1;
