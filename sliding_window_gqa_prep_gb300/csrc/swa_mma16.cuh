@@ -1,5 +1,5 @@
-// Warp-level 16-bit matrix products and the shared-memory tiles they read, for the
-// paged kernels whose bound is memory (mma.sync.m16n8k16, ldmatrix, cp.async).
+// Warp-level 16-bit matrix products and the loads of their operands, for the paged
+// kernel whose bound is memory (mma.sync.m16n8k16, ldmatrix).
 #pragma once
 #include "swa_paged.cuh"
 
@@ -28,21 +28,5 @@ __device__ __forceinline__ void ldsm4t(uint32_t (&r)[4], uint32_t addr) {
   asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
                : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(addr));
 }
-// 16 bytes global -> shared, zeros instead when !ok (the source is then not read)
-__device__ __forceinline__ void cp16_or_zero(uint32_t dst, const void* src, bool ok) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" :: "r"(dst), "l"(src), "r"(ok ? 16 : 0) : "memory");
-}
-__device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
-template <int N>
-__device__ __forceinline__ void cp_wait() { asm volatile("cp.async.wait_group %0;" :: "n"(N) : "memory"); }
-
-// Byte offset of 16-byte chunk c of row r in a [rows][D] tile: the chunk index is
-// xored with the row's low bits, so that the eight rows of an ldmatrix fall on
-// different banks.
-template <int D>
-__device__ __forceinline__ uint32_t tile_off(int r, int c) {
-  return (uint32_t)(r * (D * 2) + ((c ^ (r & 7)) << 4));
-}
-
 #endif
 }  // namespace swa

@@ -6,10 +6,10 @@
 // operations for the 4 * hd bytes of a key: 64 a byte, far below the 280 a byte where
 // the matrix peak meets the memory's. The kernel is bound by reading K and V once.
 // So: every CTA gets the same number of 64-key tiles of the whole call (work of all
-// sequences and KV heads laid end to end and cut evenly, wherever the cuts
-// fall), streams them through a ring of cp.async stages, and computes with warp-level
-// mma.sync.m16n8k16: S = Q K^T with Q in registers, the online softmax on S's
-// registers, and these registers again as the A operand of P V. A (sequence, KV head)
+// sequences and KV heads laid end to end and cut evenly, wherever the cuts fall). One warp
+// copies them from the pages by TMA, ahead across items; the others compute with warp-level
+// mma.sync.m16n8k16: S = Q K^T with Q in registers, the online softmax on S's registers,
+// and these registers again as the A operand of P V. A (sequence, KV head)
 // that lies whole in one CTA is finished there; one that is cut leaves a
 // record (m, l, sum p v) per CTA, joined by paged_merge_kernel.
 #include <cmath>
@@ -77,16 +77,21 @@ int pool_map(const swa_paged_cache& c, void* base, int kt, CUtensorMap* m) {
 // ---------------------------------------------------------------------------
 // The split kernel
 // ---------------------------------------------------------------------------
-constexpr int kThreads = 128;        // four warps
 constexpr int kKeys = 64;            // keys per tile
 constexpr int kMinTiles = 2;         // a CTA takes at least this many tiles
 
 template <int D>
 struct SplitCfg {
-  // stages of one K and one V tile; about 96 KB (two CTAs an SM) at hd 128
+  // Four warps share a tile's rows and keys. At hd 256 two warps split the value product
+  // of each (and repeat its scores): with one warp a scheduler the chain of dependent
+  // products bounds it (3.2 instead of 4.9 TB/s).
+  static constexpr int DS = D == 256 ? 2 : 1;
+  static constexpr int THREADS = 4 * DS * 32 + 32;          // and the warp that copies
+  // stages of one K and one V tile: 96 KB (two CTAs an SM) at hd 128
   static constexpr int ST = D == 64 ? 4 : 3;
   static constexpr int TILE = kKeys * D * 2;
-  static constexpr int SMEM = ST * 2 * TILE;
+  static constexpr int CW = 32;                             // columns of O a warp joins at a time
+  static constexpr int SMEM = ST * 2 * TILE + 4 * DS * 16 * CW * 4 + 1024;
 };
 
 // Tiles of one (sequence, KV head): none where the sequence has no rows or more query
@@ -99,16 +104,30 @@ __device__ __forceinline__ int split_tiles(const PagedSeq& s, const PagedAttendP
 // ROWS: query vectors of a CTA's block (16, 32 or 64): ROWS / 16 groups of 16 rows,
 // the other warps take the tile's keys in turn.
 template <typename T, int D, int ROWS>
-__global__ void __launch_bounds__(kThreads) paged_split_kernel(const PagedAttendParams p) {
+__global__ void __launch_bounds__(SplitCfg<D>::THREADS)
+    paged_split_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constant__ CUtensorMap map_v,
+                       const __grid_constant__ PagedAttendParams p) {
   using C = SplitCfg<D>;
   constexpr int RG = ROWS / 16, KG = 4 / RG, KW = kKeys / KG;   // row groups, key groups, keys of a warp
-  extern __shared__ __align__(128) unsigned char sm[];
-  __shared__ long long s_scan[4];
+  constexpr int DS = C::DS, DV = D / DS, ST = C::ST, CW = C::CW, NWARPS = C::THREADS / 32;
+  extern __shared__ unsigned char sm_raw[];
+  __shared__ __align__(8) uint64_t b_full[ST], b_empty[ST];
+  __shared__ long long s_scan[NWARPS];
   __shared__ long long s_off, s_total;
-  __shared__ int s_b;
-  __shared__ int s_pages[2][kKeys / 16];
+  __shared__ int s_b, s_abort;
   __shared__ float2 s_ml[4][16];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  unsigned char* const sm = reinterpret_cast<unsigned char*>((reinterpret_cast<uintptr_t>(sm_raw) + 1023) & ~(uintptr_t)1023);
+  float* const ob = reinterpret_cast<float*>(sm + ST * 2 * C::TILE);   // [4 * DS warps][16][CW]
+  if (tid == 0) {
+    for (int i = 0; i < ST; ++i) {
+      mbar_init(&b_full[i], 1);
+      mbar_init(&b_empty[i], 4 * DS);
+    }
+    mbar_fence_init();
+    s_abort = 0;
+    s_b = -1;
+  }
   pdl_wait();
   pdl_trigger();
 
@@ -119,19 +138,17 @@ __global__ void __launch_bounds__(kThreads) paged_split_kernel(const PagedAttend
       const int b = blockIdx.x / p.map.nk;
       const int n = split_tiles(paged_seq(p.map, b, p.T, p.max_rows, bits), p);
       if (bits) set_err(p.err, bits);
-      s_b = n > 0 ? b : -1;
+      if (n > 0) s_b = b;
       s_off = (long long)(blockIdx.x % p.map.nk) * n;
       s_total = n;
     }
     __syncthreads();
   } else {
-    const int E = (p.map.B + kThreads - 1) / kThreads;
+    const int E = (p.map.B + C::THREADS - 1) / C::THREADS;
     long long mine = 0;
     for (int e = 0; e < E; ++e) {
       const int b = tid * E + e;
-      if (b < p.map.B) {
-        mine += (long long)p.map.nk * split_tiles(paged_seq(p.map, b, p.T, p.max_rows, bits), p);
-      }
+      if (b < p.map.B) mine += (long long)p.map.nk * split_tiles(paged_seq(p.map, b, p.T, p.max_rows, bits), p);
     }
     if (bits && blockIdx.x == 0) set_err(p.err, bits);
     long long incl = mine;
@@ -141,10 +158,9 @@ __global__ void __launch_bounds__(kThreads) paged_split_kernel(const PagedAttend
       if (lane >= o) incl += v;
     }
     if (lane == 31) s_scan[warp] = incl;
-    if (tid == 0) s_b = -1;
     __syncthreads();
     long long before = incl - mine, total = 0;
-    for (int w = 0; w < 4; ++w) {
+    for (int w = 0; w < NWARPS; ++w) {
       if (w < warp) before += s_scan[w];
       total += s_scan[w];
     }
@@ -175,107 +191,120 @@ __global__ void __launch_bounds__(kThreads) paged_split_kernel(const PagedAttend
   const long long u0 = p.whole ? 0 : per * blockIdx.x;
   if (tid == 0 && !p.whole) p.ws_desc[blockIdx.x] = make_int4(-1, 0, 0, 0);
   if (s_b < 0) return;
+  // the items of this share, walked by the copying warp and by the others alike
   long long left = min(per, total - u0);
   int b = s_b;
   uint32_t ignore = 0;
   PagedSeq s = paged_seq(p.map, b, p.T, p.max_rows, ignore);
   int n_tiles = split_tiles(s, p);
   int tile0 = (int)(s_off % n_tiles), g = (int)(s_off / n_tiles);
-
-  const int rg = warp / KG, kg = warp % KG;
-  const int hpg = p.hpg, page_mask = (1 << p.map.page_shift) - 1;
-  const T* const qp = static_cast<const T*>(p.q);
+  auto next_item = [&](int tile1) {         // false at the end
+    left -= tile1 - tile0;
+    tile0 = 0;
+    if (left <= 0) return false;
+    if (++g == p.map.nk) {
+      g = 0;
+      do {
+        s = paged_seq(p.map, ++b, p.T, p.max_rows, ignore);
+        n_tiles = split_tiles(s, p);
+      } while (n_tiles == 0);
+    }
+    return true;
+  };
   const uint32_t smb = smem_u32(sm);
+  int it = 0;                               // tiles of this share so far: stage it % ST
 
-  while (left > 0) {
+  if (warp == NWARPS - 1) {
+    // ------------------------------------------------------------ copies: a box a lane
+    constexpr int HALVES = D / 64;
+    const int page = 1 << p.map.page_shift, rows = min(page, kKeys), per_half = kKeys / rows;
+    const int boxes = per_half * HALVES;    // of K, and as many of V: 32 at most together
+    const int oob = p.map.num_pages * p.map.nk << p.map.page_shift;       // rows of the pool: reads zeros
+    const bool mine = lane < 2 * boxes, is_v = lane >= boxes;
+    const int box = is_v ? lane - boxes : lane, half = box / per_half, bx = box % per_half;
+    bool ok = true;
+    do {
+      const int tile1 = (int)min((long long)n_tiles, tile0 + left);
+      const int32_t* table = p.map.table + (size_t)b * p.map.max_pages;
+      for (int tile = tile0; ok && tile < tile1; ++tile, ++it) {
+        const int key = tile * kKeys + bx * rows, st = it % ST;
+        int y = oob;
+        if (mine && key < s.len) {          // looked up before the wait
+          const int id = table[key >> p.map.page_shift];
+          if (page_ok(p.map, id))
+            y = ((id * p.map.nk + g) << p.map.page_shift) + (key & (page - 1));
+          else
+            set_err(p.err, SWA_DERR_PAGE);
+        }
+        if (it >= ST) ok = __all_sync(0xffffffffu, tc_wait(&b_empty[st], (uint32_t)((it / ST - 1) & 1), &s_abort));
+        if (!ok) break;
+        if (lane == 0) mbar_arrive_expect_tx(&b_full[st], 2 * C::TILE);
+        __syncwarp();
+        if (mine)
+          tma_2d(smb + (st * 2 + (is_v ? 1 : 0)) * C::TILE + half * (kKeys * 128) + bx * rows * 128, is_v ? &map_v : &map_k,
+                 half * 64, y, &b_full[st]);
+      }
+      if (!ok || !next_item(tile1)) break;
+    } while (true);
+    if (!ok) {
+      set_err(p.err, SWA_DERR_TIMEOUT);
+      // copies in flight land before the CTA exits (bounded)
+      for (int i = max(0, it - ST); i < it; ++i) mbar_wait_bounded(&b_full[i % ST], (uint32_t)((i / ST) & 1), kWaitLimitNs);
+    }
+    return;
+  }
+
+  // ------------------------------------------------------------ products
+  const int ds = warp >> 2, rg = (warp & 3) / KG, kg = (warp & 3) % KG;
+  const int hpg = p.hpg;
+  const T* const qp = static_cast<const T*>(p.q);
+  bool ok = true;                           // a thread whose wait gave up goes on and writes nothing
+  // 16-byte chunk c of row r of a tile: halves of 64 features, rows of 128 bytes, swizzled
+  auto at = [](int r, int c) { return (uint32_t)((c >> 3) * (kKeys * 128) + r * 128 + (((c & 7) ^ (r & 7)) << 4)); };
+  do {
     const int tile1 = (int)min((long long)n_tiles, tile0 + left);
     const int nvec = s.t * hpg;
-    const int* table = p.map.table + (size_t)b * p.map.max_pages;
-    const T* const kp = static_cast<const T*>(p.ck);
-    const T* const vp = static_cast<const T*>(p.cv);
-
-    // --- page ids of a tile: thread i < 4 holds the page of keys [16 i, 16 i + 16)
-    auto fetch_page = [&](int tile) -> int {
-      const int key = tile * kKeys + tid * 16;
-      if (tid >= kKeys / 16 || tile >= tile1 || key >= s.len) return -1;
-      const int id = table[key >> p.map.page_shift];
-      if (!page_ok(p.map, id)) {
-        set_err(p.err, SWA_DERR_PAGE);
-        return -1;
-      }
-      return id;
-    };
-    auto load_tile = [&](int tile, const int* ids) {
-      const int st = tile % C::ST;
-      constexpr int CH = D / 8;                             // 16-byte chunks of a row
-#pragma unroll
-      for (int i = 0; i < kKeys * CH / kThreads; ++i) {
-        const int x = tid + i * kThreads, r = x / CH, c = x % CH;
-        const int key = tile * kKeys + r, id = ids[r >> 4];
-        const bool ok = key < s.len && id >= 0;
-        const size_t off = ok ? (((size_t)id * p.map.nk + g << p.map.page_shift) + (key & page_mask)) * D + c * 8 : 0;
-        const uint32_t dst = smb + (uint32_t)(st * 2 * C::TILE) + tile_off<D>(r, c);
-        cp16_or_zero(dst, kp + off, ok);
-        cp16_or_zero(dst + C::TILE, vp + off, ok);
-      }
-    };
-
-    // prologue: the first ST - 1 tiles, with their page ids read directly
-    __syncthreads();
-#pragma unroll 1
-    for (int i = 0; i < C::ST - 1; ++i) {
-      if (tile0 + i < tile1) {
-        int ids[kKeys / 16];
-#pragma unroll
-        for (int j = 0; j < kKeys / 16; ++j) {
-          const int key = (tile0 + i) * kKeys + j * 16;
-          ids[j] = -1;
-          if (key < s.len) {
-            const int id = table[key >> p.map.page_shift];
-            if (page_ok(p.map, id)) ids[j] = id;
-            else set_err(p.err, SWA_DERR_PAGE);
-          }
-        }
-        load_tile(tile0 + i, ids);
-      }
-      cp_commit();
-    }
-    int next_id = fetch_page(tile0 + C::ST - 1);
-
     // --- Q of this warp's 16 rows as A operands; the rows' limits
     uint32_t qf[D / 16][4];
     int lim[2];
 #pragma unroll
     for (int hrow = 0; hrow < 2; ++hrow) {
       const int r = rg * 16 + hrow * 8 + (lane >> 2);
-      const bool ok = r < nvec;
-      const int i = ok ? r / hpg : 0, h = ok ? r % hpg : 0;
-      lim[hrow] = ok ? min(s.len, s.len - s.t + i + 1) : 0;
+      const bool in = r < nvec;
+      const int i = in ? r / hpg : 0, h = in ? r % hpg : 0;
+      lim[hrow] = in ? min(s.len, s.len - s.t + i + 1) : 0;
       const T* src = qp + (size_t)(s.r0 + i) * p.q_row + (size_t)(g * hpg + h) * D + (lane & 3) * 2;
 #pragma unroll
       for (int k = 0; k < D / 16; ++k) {
-        qf[k][hrow] = ok ? *reinterpret_cast<const uint32_t*>(src + k * 16) : 0u;
-        qf[k][hrow + 2] = ok ? *reinterpret_cast<const uint32_t*>(src + k * 16 + 8) : 0u;
+        qf[k][hrow] = in ? *reinterpret_cast<const uint32_t*>(src + k * 16) : 0u;
+        qf[k][hrow + 2] = in ? *reinterpret_cast<const uint32_t*>(src + k * 16 + 8) : 0u;
       }
     }
-    const int lim_min = s.len - s.t + 1;                   // keys below it are seen by every row
+    const int lim_min = s.len - s.t + 1;                    // keys below it are seen by every row
 
-    float o[D / 8][4];
+    float o[DV / 8][4];
 #pragma unroll
-    for (int i = 0; i < D / 8; ++i)
+    for (int i = 0; i < DV / 8; ++i)
 #pragma unroll
       for (int j = 0; j < 4; ++j) o[i][j] = 0.f;
     float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
 
-    for (int tile = tile0; tile < tile1; ++tile) {
-      if (tid < kKeys / 16) s_pages[tile & 1][tid] = next_id;
-      cp_wait<C::ST - 2>();
-      __syncthreads();                                     // tile landed; its predecessor's stage is free
-      if (tile + C::ST - 1 < tile1) load_tile(tile + C::ST - 1, s_pages[tile & 1]);
-      cp_commit();
-      next_id = fetch_page(tile + C::ST);
-      const uint32_t kb = smb + (uint32_t)((tile % C::ST) * 2 * C::TILE), vb = kb + C::TILE;
+    for (int tile = tile0; tile < tile1; ++tile, ++it) {
+      const int st = it % ST;
+      ok &= tc_wait(&b_full[st], (uint32_t)((it / ST) & 1), &s_abort);
+      __syncwarp();
+      const uint32_t kb = smb + (uint32_t)(st * 2 * C::TILE), vb = kb + C::TILE;
       const int k0 = tile * kKeys + kg * KW;
+      const bool tail = tile * kKeys + kKeys > s.len;
+      if (tail) {                           // V behind the last key: zeros (0 * NaN)
+        const int first = max(0, s.len - k0);
+        for (int x = lane; x < (KW - first) * (DV / 8); x += 32) {
+          const int r = kg * KW + first + x / (DV / 8), c = ds * (DV / 8) + x % (DV / 8);
+          *reinterpret_cast<uint4*>(sm + (st * 2 + 1) * C::TILE + at(r, c)) = make_uint4(0, 0, 0, 0);
+        }
+        fence_proxy_async_smem();           // before the copy that comes next into this stage
+        __syncwarp();
+      }
 
       float sc[KW / 8][4];
 #pragma unroll
@@ -287,7 +316,7 @@ __global__ void __launch_bounds__(kThreads) paged_split_kernel(const PagedAttend
 #pragma unroll
         for (int n = 0; n < KW / 16; ++n) {
           uint32_t f[4];
-          ldsm4(f, kb + tile_off<D>(kg * KW + n * 16 + ((lane >> 4) << 3) + (lane & 7), k * 2 + ((lane >> 3) & 1)));
+          ldsm4(f, kb + at(kg * KW + n * 16 + ((lane >> 4) << 3) + (lane & 7), k * 2 + ((lane >> 3) & 1)));
           mma16816<T>(sc[2 * n], qf[k], f[0], f[1]);
           mma16816<T>(sc[2 * n + 1], qf[k], f[2], f[3]);
         }
@@ -308,22 +337,29 @@ __global__ void __launch_bounds__(kThreads) paged_split_kernel(const PagedAttend
       for (int r = 0; r < 2; ++r) {
         mx[r] = fmaxf(mx[r], __shfl_xor_sync(0xffffffffu, mx[r], 1));
         mx[r] = fmaxf(mx[r], __shfl_xor_sync(0xffffffffu, mx[r], 2));
-        const float mn = fmaxf(m[r], mx[r]);
-        const float a = mn == -INFINITY ? 1.f : ex2(m[r] - mn);   // m = -inf: 0
-        m[r] = mn;
-        l[r] *= a;
-#pragma unroll
-        for (int i = 0; i < D / 8; ++i) {
-          o[i][2 * r] *= a;
-          o[i][2 * r + 1] *= a;
-        }
-        mx[r] = (mn == -INFINITY ? 0.f : mn) - PScale<T>::kLog2;
       }
+      if (__any_sync(0xffffffffu, mx[0] > m[0] || mx[1] > m[1])) {   // else nothing to rescale
+#pragma unroll
+        for (int r = 0; r < 2; ++r) {
+          const float mn = fmaxf(m[r], mx[r]);
+          const float a = mn == -INFINITY ? 1.f : ex2(m[r] - mn);    // m = -inf: 0
+          m[r] = mn;
+          l[r] *= a;
+#pragma unroll
+          for (int i = 0; i < DV / 8; ++i) {
+            o[i][2 * r] *= a;
+            o[i][2 * r + 1] *= a;
+          }
+        }
+      }
+      float off[2];
+#pragma unroll
+      for (int r = 0; r < 2; ++r) off[r] = PScale<T>::kLog2 - (m[r] == -INFINITY ? 0.f : m[r]);
 #pragma unroll
       for (int n = 0; n < KW / 8; ++n)
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
-          sc[n][j] = ex2(sc[n][j] - mx[j >> 1]);
+          sc[n][j] = ex2(sc[n][j] + off[j >> 1]);
           l[j >> 1] += sc[n][j];
         }
 #pragma unroll
@@ -333,56 +369,61 @@ __global__ void __launch_bounds__(kThreads) paged_split_kernel(const PagedAttend
                                 pack2(sc[2 * n + 1][0], sc[2 * n + 1][1], (const T*)nullptr),
                                 pack2(sc[2 * n + 1][2], sc[2 * n + 1][3], (const T*)nullptr)};
 #pragma unroll
-        for (int dd = 0; dd < D / 16; ++dd) {
+        for (int dd = 0; dd < DV / 16; ++dd) {
           uint32_t f[4];
-          ldsm4t(f, vb + tile_off<D>(kg * KW + n * 16 + (((lane >> 3) & 1) << 3) + (lane & 7), dd * 2 + (lane >> 4)));
+          ldsm4t(f, vb + at(kg * KW + n * 16 + (((lane >> 3) & 1) << 3) + (lane & 7), ds * (DV / 8) + dd * 2 + (lane >> 4)));
           mma16816<T>(o[2 * dd], pa, f[0], f[1]);
           mma16816<T>(o[2 * dd + 1], pa, f[2], f[3]);
         }
       }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&b_empty[st]);
     }
 
-    // --- join the key groups through shared memory (the stages are done with)
-    cp_wait<0>();
-    __syncthreads();
-    float* const ob = reinterpret_cast<float*>(sm);          // [4 warps][16][D]
+    // --- join the key groups, CW columns of each warp's O at a time
 #pragma unroll
     for (int r = 0; r < 2; ++r) {
       l[r] += __shfl_xor_sync(0xffffffffu, l[r], 1);
       l[r] += __shfl_xor_sync(0xffffffffu, l[r], 2);
-      const int row = r * 8 + (lane >> 2);
-      if ((lane & 3) == 0) s_ml[warp][row] = make_float2(m[r], l[r]);
-#pragma unroll
-      for (int i = 0; i < D / 8; ++i)
-        *reinterpret_cast<float2*>(ob + (warp * 16 + row) * D + i * 8 + (lane & 3) * 2) =
-            make_float2(o[i][2 * r], o[i][2 * r + 1]);
+      if (ds == 0 && (lane & 3) == 0) s_ml[warp][r * 8 + (lane >> 2)] = make_float2(m[r], l[r]);
     }
-    __syncthreads();
     const bool whole = tile0 == 0 && tile1 == n_tiles;
     // record of the item this CTA continues: slot 2c, of the one it starts: 2c + 1
     const size_t rec = ((size_t)blockIdx.x * 2 + (tile0 == 0 ? 1 : 0)) * ROWS;
-    for (int x = tid; x < nvec * (D / 8); x += kThreads) {
-      const int row = x / (D / 8), c = x % (D / 8);
-      const int w0 = (row >> 4) * KG, rr = row & 15;
-      float mt = -INFINITY;
 #pragma unroll
-      for (int w = 0; w < KG; ++w) mt = fmaxf(mt, s_ml[w0 + w][rr].x);
-      float lt = 0.f, acc[8] = {};
+    for (int c0 = 0; c0 < DV; c0 += CW) {
+      if (c0 > 0) named_barrier(1, 4 * DS * 32);            // the columns before are read
 #pragma unroll
-      for (int w = 0; w < KG; ++w) {
-        const float2 ml = s_ml[w0 + w][rr];
-        const float a = ml.x == -INFINITY ? 0.f : ex2(ml.x - mt);
-        float y[8];
-        load8(ob + ((w0 + w) * 16 + rr) * D + c * 8, y);
-        lt += a * ml.y;
+      for (int r = 0; r < 2; ++r)
 #pragma unroll
-        for (int j = 0; j < 8; ++j) acc[j] += a * y[j];
-      }
-      if (whole) {
-        paged_store_row<T>(p, s.r0 + row / hpg, g * hpg + row % hpg, D, c * 8, mt, lt, PScale<T>::kLog2, acc, c == 0);
-      } else {
-        store8(p.ws_acc + (rec + row) * D + c * 8, acc);
-        if (c == 0) p.ws_ml[rec + row] = make_float2(mt, lt);
+        for (int i = 0; i < CW / 8; ++i)
+          *reinterpret_cast<float2*>(ob + (warp * 16 + r * 8 + (lane >> 2)) * CW + i * 8 + (lane & 3) * 2) =
+              make_float2(o[c0 / 8 + i][2 * r], o[c0 / 8 + i][2 * r + 1]);
+      named_barrier(1, 4 * DS * 32);
+      if (s_abort) continue;
+      for (int x = tid; x < nvec * DS * (CW / 8); x += 4 * DS * 32) {
+        const int row = x / (DS * (CW / 8)), cc = x % (DS * (CW / 8)), d = cc / (CW / 8), c = cc % (CW / 8);
+        const int w0 = (row >> 4) * KG, rr = row & 15, col = d * DV + c0 + c * 8;
+        float mt = -INFINITY;
+#pragma unroll
+        for (int w = 0; w < KG; ++w) mt = fmaxf(mt, s_ml[w0 + w][rr].x);
+        float lt = 0.f, acc[8] = {};
+#pragma unroll
+        for (int w = 0; w < KG; ++w) {
+          const float2 ml = s_ml[w0 + w][rr];
+          const float a = ml.x == -INFINITY ? 0.f : ex2(ml.x - mt);
+          float y[8];
+          load8(ob + ((d * 4 + w0 + w) * 16 + rr) * CW + c * 8, y);
+          lt += a * ml.y;
+#pragma unroll
+          for (int j = 0; j < 8; ++j) acc[j] += a * y[j];
+        }
+        if (whole) {
+          paged_store_row<T>(p, s.r0 + row / hpg, g * hpg + row % hpg, D, col, mt, lt, PScale<T>::kLog2, acc, col == 0);
+        } else {
+          store8(p.ws_acc + (rec + row) * D + col, acc);
+          if (col == 0) p.ws_ml[rec + row] = make_float2(mt, lt);
+        }
       }
     }
     if (!whole && tile0 == 0 && tid == 0) {
@@ -390,19 +431,10 @@ __global__ void __launch_bounds__(kThreads) paged_split_kernel(const PagedAttend
       const long long end = u0 + (min(per, total - u0) - left) + n_tiles - 1;
       p.ws_desc[blockIdx.x] = make_int4(b, g, (int)(end / per), 0);
     }
-
-    // --- the next item
-    left -= tile1 - tile0;
-    tile0 = 0;
-    if (left <= 0) break;
-    if (++g == p.map.nk) {
-      g = 0;
-      do {
-        s = paged_seq(p.map, ++b, p.T, p.max_rows, ignore);
-        n_tiles = split_tiles(s, p);
-      } while (n_tiles == 0);
-    }
-  }
+    if (!next_item(tile1)) break;
+    named_barrier(1, 4 * DS * 32);          // s_ml and ob are read
+  } while (true);
+  if (!ok) set_err(p.err, SWA_DERR_TIMEOUT);
 }
 
 // ---------------------------------------------------------------------------
@@ -487,7 +519,7 @@ static int split_occupancy() {
     auto k = paged_split_kernel<T, D, ROWS>;
     int n = 0;
     if (allow_smem<paged_split_kernel<T, D, ROWS>>(SplitCfg<D>::SMEM) != cudaSuccess ||
-        cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, k, kThreads, SplitCfg<D>::SMEM) != cudaSuccess || n < 1) {
+        cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, k, SplitCfg<D>::THREADS, SplitCfg<D>::SMEM) != cudaSuccess || n < 1) {
       (void)cudaGetLastError();
       n = 1;
     }
@@ -497,10 +529,15 @@ static int split_occupancy() {
 }
 
 template <typename T, int D, int ROWS>
-static int launch_split(const PagedAttendParams& p, const SplitPlan& sp, cudaStream_t s) {
+static int launch_split(const swa_paged_cache& c, const PagedAttendParams& p, const SplitPlan& sp, cudaStream_t s) {
+  CUtensorMap mk, mv;
+  int rc = pool_map(c, c.k, kKeys, &mk);
+  if (rc == SWA_OK) rc = pool_map(c, c.v, kKeys, &mv);
+  if (rc != SWA_OK) return rc;
   const cudaError_t e = allow_smem<paged_split_kernel<T, D, ROWS>>(SplitCfg<D>::SMEM);
   if (e != cudaSuccess) return cuda_status(e);
-  const int rc = finish_launch(launch_pdl(paged_split_kernel<T, D, ROWS>, dim3(sp.grid), dim3(kThreads), SplitCfg<D>::SMEM, s, p));
+  rc = finish_launch(launch_pdl(paged_split_kernel<T, D, ROWS>, dim3(sp.grid), dim3(SplitCfg<D>::THREADS),
+                                SplitCfg<D>::SMEM, s, mk, mv, p));
   if (rc != SWA_OK || p.whole) return rc;
   const long long vecs = (long long)p.max_rows * p.hpg;
   return finish_launch(launch_pdl(paged_merge_kernel<T, D>, dim3(sp.grid, (unsigned)(vecs < p.most ? vecs : p.most)),
@@ -611,7 +648,7 @@ int swa_paged_attend(const swa_paged_attend_args* a, cudaStream_t stream) {
     p.ws_ml = reinterpret_cast<float2*>(ws + pl.split.off_ml);
     p.ws_desc = reinterpret_cast<int4*>(ws + pl.split.off_desc);
     rc = by_type(c.dtype, c.hd, pl.split.rows, [&](auto* t, auto d, auto r) {
-      return launch_split<std::remove_pointer_t<decltype(t)>, decltype(d)::value, decltype(r)::value>(p, pl.split, stream);
+      return launch_split<std::remove_pointer_t<decltype(t)>, decltype(d)::value, decltype(r)::value>(c, p, pl.split, stream);
     });
     if (rc != SWA_OK) return rc;
   }
