@@ -8,12 +8,14 @@
 // [-1, 1), what sincospif takes: no f64 arithmetic (two lanes an SM here) and no
 // range reduction, at any position.
 //
-// Memory bound: each element is read and written once. A thread owns one unit (8
-// pairs, or 8 features when interleaved: 16-byte accesses for 16-bit types) of one
-// row and walks `HB` heads with it, so that an angle's sine and cosine are computed
-// once for those heads; HB shrinks while the launch would not fill the device.
-// Units whose halves do not start at multiples of 8 features take the same kernel
-// with one pair (two features) a unit.
+// Memory bound: each element is read and written once. A block takes R rows and a group
+// of heads: its threads first compute the rows' sines and cosines into shared memory (one
+// or two a thread, used by all the heads) and, for the cache, the rows' slots; then each
+// thread takes units (8 pairs, or 8 features when interleaved: 16-byte accesses for 16-bit
+// types) of the rows' heads in turn. With the angles in registers instead, recomputed for
+// every few heads, a prompt of 6000 f32 rows of 48 heads entered the cache at 3.6 TB/s.
+// Units whose halves do not start at multiples of 8 features take the same kernel with
+// one pair (two features) a unit.
 #include <cmath>
 
 #include "swa_paged.cuh"
@@ -21,7 +23,7 @@
 namespace swa {
 
 struct RotaryParams {
-  int T, H, hd, rot, HB, nHB, units, inverse;
+  int T, H, hd, rot, R, Hg, units, inverse;   // R rows and Hg heads a block
   float mag;
   const void* x;               // rows of heads [0, H) (swa_rotary) or of q (append)
   long long x_row, x_head;
@@ -43,107 +45,112 @@ struct RotaryParams {
 };
 
 constexpr int kRotThreads = 256;
-constexpr int kRotStarts = 2048;   // row starts searched in shared memory
+constexpr int kRotRows = 4;        // most rows of a block
+constexpr int kRotPairs = 512;     // most pairs of a head
+
+// The last b with row_start[b] <= row (0 if none), by a whole warp: 32 probes a step.
+__device__ __forceinline__ int find_seq(const int32_t* row_start, int B, int row) {
+  int lo = 0, n = B;
+  while (n > 1) {
+    const int step = (n + 31) >> 5, i = lo + (int)(threadIdx.x & 31) * step;
+    const unsigned m = __ballot_sync(0xffffffffu, i < lo + n && row_start[i] <= row);
+    const int k = m ? 31 - __clz(m) : 0;   // ascending: the last probe at or below the row
+    n = min(step, n - k * step);
+    lo += k * step;
+  }
+  return lo;
+}
 
 // V: pairs (half layout) or features (interleaved) of a unit
 template <typename TI, typename TO, bool INTER, int V, bool APPEND>
 __global__ void __launch_bounds__(kRotThreads) rotary_kernel(const RotaryParams p) {
-  __shared__ int starts[APPEND ? kRotStarts : 1];
+  __shared__ __align__(16) float s_cos[kRotRows * kRotPairs], s_sin[kRotRows * kRotPairs];
+  __shared__ long long s_slot[kRotRows], s_aux[kRotRows];   // cache element of (page, head 0, slot); slot_pos entry
+  __shared__ int s_live[kRotRows];
+  const int tid = threadIdx.x;
+  const int row0 = blockIdx.x * p.R, nr = min(p.R, p.T - row0), h0 = blockIdx.y * p.Hg, h1 = min(h0 + p.Hg, p.H);
+  const int half = p.rot >> 1;
   pdl_wait();
   pdl_trigger();
-  if constexpr (APPEND) {
-    if (p.map.B < kRotStarts) {
-      for (int i = threadIdx.x; i <= p.map.B; i += kRotThreads) starts[i] = p.map.row_start[i];
-      __syncthreads();
-    }
-  }
-  const unsigned idx = blockIdx.x * (unsigned)kRotThreads + threadIdx.x;
-  const unsigned u = idx % (unsigned)p.units, rest = idx / (unsigned)p.units;
-  const int h0 = (int)(rest % (unsigned)p.nHB) * p.HB;
-  const unsigned row = rest / (unsigned)p.nHB;
-  if (row >= (unsigned)p.T) return;
 
-  // the row's sequence and slot
-  long long slot_off = -1;           // cache element of (page, head 0, slot), < 0: not stored
-  long long aux_off = -1;            // slot_pos / weight entry of head 0
+  for (int i = tid; i < nr * half; i += kRotThreads) {
+    const int r = i / half, e = i % half;
+    const uint64_t frac = (uint64_t)(int64_t)p.pos[row0 + r] * p.turns[e];   // modulo 2^64: the fraction of a turn
+    float sn, cs;
+    sincospif((float)(int32_t)(uint32_t)(frac >> 32) * 0x1p-31f, &sn, &cs);
+    s_cos[i] = cs * p.mag;
+    s_sin[i] = p.inverse ? -sn * p.mag : sn * p.mag;
+  }
   if constexpr (APPEND) {
-    const bool in_smem = p.map.B < kRotStarts;
-    int lo = 0, hi = p.map.B;        // the last b with row_start[b] <= row
-    while (hi - lo > 1) {
-      const int mid = (lo + hi) >> 1;
-      if ((in_smem ? starts[mid] : p.map.row_start[mid]) <= (int)row) lo = mid; else hi = mid;
-    }
-    uint32_t bits = 0;
-    const int r0 = p.map.row_start[lo], r1 = p.map.row_start[lo + 1];
-    if (((int)row >= r1 && lo == p.map.B - 1 && r1 >= r0 && r1 >= 0) || ((int)row < r0 && lo == 0))
-      return;                        // behind the last sequence or before the first
-    if (r0 < 0 || r1 > p.T || (int)row < r0 || (int)row >= r1) {
-      if (u == 0 && h0 == 0) set_err(p.err, SWA_DERR_SEGMENT);
-      return;
-    }
-    const int len = p.map.lens[lo];
-    const long long slot = (long long)len - r1 + (int)row;
-    if (len < 0 || len > p.map.cap || slot < 0) {
-      bits |= SWA_DERR_META;
-    } else {
-      const int page = p.map.table[(size_t)lo * p.map.max_pages + (size_t)(slot >> p.map.page_shift)];
-      if (!page_ok(p.map, page)) {
-        bits |= SWA_DERR_PAGE;
-      } else {
-        slot_off = (long long)page * p.nk * p.hd_page + (slot & ((1 << p.map.page_shift) - 1)) * p.hd;
-        aux_off = (long long)lo * p.nk * p.map.cap + slot;
+    // the rows' sequences and slots, a warp a row (the last warps: the first ones hold angles)
+    const int r = kRotThreads / 32 - 1 - (tid >> 5);
+    if (r < nr) {
+      const int row = row0 + r, b = find_seq(p.map.row_start, p.map.B, row);
+      const int r0 = p.map.row_start[b], r1 = p.map.row_start[b + 1], len = p.map.lens[b];
+      // a row behind the last sequence or before the first belongs to none
+      const bool none = (row >= r1 && b == p.map.B - 1 && r1 >= r0 && r1 >= 0) || (row < r0 && b == 0);
+      const bool bad = !none && (r0 < 0 || r1 > p.T || row < r0 || row >= r1);
+      uint32_t bits = bad ? SWA_DERR_SEGMENT : 0u;
+      const long long slot = (long long)len - r1 + row;
+      long long at = -1;
+      if (!none && !bad) {
+        if (len < 0 || len > p.map.cap || slot < 0) {
+          bits |= SWA_DERR_META;
+        } else {
+          const int page = p.map.table[(size_t)b * p.map.max_pages + (size_t)(slot >> p.map.page_shift)];
+          if (page_ok(p.map, page))
+            at = (long long)page * p.nk * p.hd_page + (slot & ((1 << p.map.page_shift) - 1)) * p.hd;
+          else
+            bits |= SWA_DERR_PAGE;
+        }
+      }
+      if ((tid & 31) == 0) {
+        s_live[r] = !none && !bad;
+        s_slot[r] = at;
+        s_aux[r] = (long long)b * p.nk * p.map.cap + slot;
+        if (bits && blockIdx.y == 0) set_err(p.err, bits);
       }
     }
-    if (bits && u == 0 && h0 == 0) set_err(p.err, bits);
   }
+  __syncthreads();
 
-  // the unit's features and angles
-  constexpr int NP = INTER ? (V > 1 ? V / 2 : 1) : V;   // pairs of a unit
-  const int half = p.rot >> 1;
+  constexpr int NP = INTER ? V / 2 : V;                 // pairs of a unit
   const int rot_units = INTER ? p.rot / V : half / V;
-  const bool turn = (int)u < rot_units;
-  const int e0 = (int)u * (INTER ? V / 2 : V);           // first pair
-  const int f0 = turn ? (INTER ? 2 * e0 : e0)            // first feature
-                      : (INTER ? (int)u * V : p.rot + ((int)u - rot_units) * V);
-  float c[NP], s[NP];
-  if (turn) {
-    const uint64_t pos = (uint64_t)(int64_t)p.pos[row];
-#pragma unroll
-    for (int i = 0; i < NP; ++i) {
-      const uint64_t frac = pos * p.turns[e0 + i];       // modulo 2^64: the fraction of a turn
-      sincospif((float)(int32_t)(uint32_t)(frac >> 32) * 0x1p-31f, &s[i], &c[i]);
-      c[i] *= p.mag;
-      s[i] *= p.inverse ? -p.mag : p.mag;
-    }
-  }
-
-  const int h1 = min(h0 + p.HB, p.H);
-#pragma unroll 4
-  for (int h = h0; h < h1; ++h) {
+  const int nh = h1 - h0, items = nr * nh * p.units;
+#pragma unroll 2
+  for (int x = tid; x < items; x += kRotThreads) {
+    const int u = x % p.units, y = x / p.units, h = h0 + y % nh, r = y / nh;
+    const long long row = row0 + r;
+    const bool turn = u < rot_units;
+    const int e0 = u * NP;                              // first pair
+    const int f0 = INTER ? u * V : turn ? e0 : p.rot + (u - rot_units) * V;   // first feature
     const TI* src;
     TO* dst;
     bool rotate = turn;
     if constexpr (APPEND) {
+      if (!s_live[r]) continue;
       if (h < p.nh) {
-        src = static_cast<const TI*>(p.x) + (long long)row * p.x_row + (long long)h * p.hd;
-        dst = static_cast<TO*>(p.out) + (long long)row * p.out_row + (long long)h * p.hd;
+        src = static_cast<const TI*>(p.x) + row * p.x_row + (long long)h * p.hd;
+        dst = static_cast<TO*>(p.out) + row * p.out_row + (long long)h * p.hd;
       } else {
         const bool is_k = h < p.nh + p.nk;
         const int g = h - p.nh - (is_k ? 0 : p.nk);
-        if (slot_off < 0) continue;
-        src = (is_k ? static_cast<const TI*>(p.k) + (long long)row * p.k_row
-                    : static_cast<const TI*>(p.v) + (long long)row * p.v_row) + (long long)g * p.hd;
-        dst = static_cast<TO*>(is_k ? p.cache_k : p.cache_v) + slot_off + (long long)g * p.hd_page;
+        if (s_slot[r] < 0) continue;
+        src = (is_k ? static_cast<const TI*>(p.k) + row * p.k_row : static_cast<const TI*>(p.v) + row * p.v_row) +
+              (long long)g * p.hd;
+        dst = static_cast<TO*>(is_k ? p.cache_k : p.cache_v) + s_slot[r] + (long long)g * p.hd_page;
         rotate = turn && is_k;
         if (is_k && u == 0) {
-          if (p.slot_pos) p.slot_pos[aux_off + (long long)g * p.map.cap] = p.pos[row];
-          if (p.weight) p.weight[aux_off + (long long)g * p.map.cap] = 0.f;
+          if (p.slot_pos) p.slot_pos[s_aux[r] + (long long)g * p.map.cap] = p.pos[row];
+          if (p.weight) p.weight[s_aux[r] + (long long)g * p.map.cap] = 0.f;
         }
       }
     } else {
-      src = static_cast<const TI*>(p.x) + (long long)row * p.x_row + (long long)h * p.x_head;
-      dst = static_cast<TO*>(p.out) + (long long)row * p.out_row + (long long)h * p.out_head;
+      src = static_cast<const TI*>(p.x) + row * p.x_row + (long long)h * p.x_head;
+      dst = static_cast<TO*>(p.out) + row * p.out_row + (long long)h * p.out_head;
     }
+    const float* cs = s_cos + r * half + e0;
+    const float* sn = s_sin + r * half + e0;
     if constexpr (V == 8) {
       float a[8];
       load8(src + f0, a);
@@ -151,9 +158,9 @@ __global__ void __launch_bounds__(kRotThreads) rotary_kernel(const RotaryParams 
         if (rotate) {
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
-            const float x = a[2 * i], y = a[2 * i + 1];
-            a[2 * i] = x * c[i] - y * s[i];
-            a[2 * i + 1] = y * c[i] + x * s[i];
+            const float c = cs[i], s = sn[i], u0 = a[2 * i], v0 = a[2 * i + 1];
+            a[2 * i] = u0 * c - v0 * s;
+            a[2 * i + 1] = v0 * c + u0 * s;
           }
         }
         store8(dst + f0, a);
@@ -161,11 +168,14 @@ __global__ void __launch_bounds__(kRotThreads) rotary_kernel(const RotaryParams 
         float b[8];
         load8(src + half + f0, b);
         if (rotate) {
+          float c[8], s[8];
+          load8(cs, c);
+          load8(sn, s);
 #pragma unroll
           for (int i = 0; i < 8; ++i) {
-            const float x = a[i], y = b[i];
-            a[i] = x * c[i] - y * s[i];
-            b[i] = y * c[i] + x * s[i];
+            const float u0 = a[i], v0 = b[i];
+            a[i] = u0 * c[i] - v0 * s[i];
+            b[i] = v0 * c[i] + u0 * s[i];
           }
         }
         store8(dst + f0, a);
@@ -176,9 +186,9 @@ __global__ void __launch_bounds__(kRotThreads) rotary_kernel(const RotaryParams 
     } else {
       const int f1 = INTER ? f0 + 1 : f0 + half;
       if (turn) {
-        const float x = load1(src + f0), y = load1(src + f1);
-        store1(dst + f0, rotate ? x * c[0] - y * s[0] : x);
-        store1(dst + f1, rotate ? y * c[0] + x * s[0] : y);
+        const float u0 = load1(src + f0), v0 = load1(src + f1);
+        store1(dst + f0, rotate ? u0 * cs[0] - v0 * sn[0] : u0);
+        store1(dst + f1, rotate ? v0 * cs[0] + u0 * sn[0] : v0);
       } else {
         store1(dst + f0, load1(src + f0));
         if constexpr (INTER) store1(dst + f1, load1(src + f1));
@@ -187,7 +197,9 @@ __global__ void __launch_bounds__(kRotThreads) rotary_kernel(const RotaryParams 
   }
 }
 
-// Units of a row: pairs of the rotated part, then the copied part.
+// Units of a row (pairs of the rotated part, then the copied part), and the block's rows
+// and heads: all heads of kRotRows rows once that gives every SM four blocks, else one
+// row and as many heads as give each thread a unit.
 static bool rotary_units(RotaryParams& p, bool inter, bool* wide) {
   const int half = p.rot / 2, rest = p.hd - p.rot;
   *wide = inter ? p.rot % 8 == 0 : half % 8 == 0;      // hd is a multiple of 8, so the rest is too
@@ -195,19 +207,18 @@ static bool rotary_units(RotaryParams& p, bool inter, bool* wide) {
     p.units = p.hd / (*wide ? 8 : 2);
   else
     p.units = *wide ? half / 8 + rest / 8 : half + rest;
-  // heads per thread: enough threads to fill the device four times over first
-  const long long all = (long long)p.T * p.units * p.H, fill = 4LL * 2048 * (num_sms() > 0 ? num_sms() : 148);
-  long long hb = all / fill;
-  p.HB = (int)(hb < 1 ? 1 : (hb > 8 ? 8 : hb));
-  if (p.HB > p.H) p.HB = p.H;
-  p.nHB = (p.H + p.HB - 1) / p.HB;
-  return (long long)p.T * p.units * p.nHB < (1LL << 31);
+  const long long sms = num_sms() > 0 ? num_sms() : 148;
+  p.R = p.T >= 4 * sms * kRotRows ? kRotRows : 1;
+  p.Hg = p.R > 1 || p.T >= 4 * sms ? p.H : (kRotThreads + p.units - 1) / p.units;
+  if (p.Hg > p.H) p.Hg = p.H;
+  const long long most = (1 << 20) / p.units;           // items of a block stay well below 2^31
+  if (p.Hg > most) p.Hg = (int)most;
+  return (p.H + p.Hg - 1) / p.Hg <= 65535;
 }
 
 template <typename TI, typename TO, bool APPEND>
 static int launch_rotary(const RotaryParams& p, bool inter, bool wide, cudaStream_t s) {
-  const long long threads = (long long)p.T * p.units * p.nHB;
-  const dim3 grid((unsigned)((threads + kRotThreads - 1) / kRotThreads)), block(kRotThreads);
+  const dim3 grid((unsigned)((p.T + p.R - 1) / p.R), (unsigned)((p.H + p.Hg - 1) / p.Hg)), block(kRotThreads);
   cudaError_t e;
   if (inter)
     e = wide ? launch_pdl(rotary_kernel<TI, TO, true, 8, APPEND>, grid, block, 0, s, p)
