@@ -664,8 +664,8 @@ typedef struct swa_paged_attend_args {
   uint32_t* err;
   cudaEvent_t ev_start, ev_stop;
 } swa_paged_attend_args;
-/* Bytes of workspace for these sizes (0: invalid sizes). Queries the current
- * device's SM count on first use. */
+/* Bytes of workspace for these sizes (0: invalid sizes; 1: none is needed, the
+ * workspace may be NULL). Queries the current device's SM count on first use. */
 size_t swa_paged_attend_workspace_size(const swa_paged_attend_args* args);
 int swa_paged_attend(const swa_paged_attend_args* args, cudaStream_t stream);
 

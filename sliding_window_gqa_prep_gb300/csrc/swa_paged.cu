@@ -613,7 +613,7 @@ size_t swa_paged_attend_workspace_size(const swa_paged_attend_args* a) {
   if (!a || !attend_sizes_ok(a)) return 0;
   PagedPlan pl;
   attend_plan(a, &pl);
-  return pl.bytes ? pl.bytes : 256;
+  return pl.bytes ? pl.bytes : 1;
 }
 
 int swa_paged_attend(const swa_paged_attend_args* a, cudaStream_t stream) {
@@ -629,7 +629,7 @@ int swa_paged_attend(const swa_paged_attend_args* a, cudaStream_t stream) {
     return SWA_E_ALIGN;
   PagedPlan pl;
   attend_plan(a, &pl);
-  if (!a->workspace || a->workspace_bytes < (pl.bytes ? pl.bytes : 256)) return SWA_E_WORKSPACE;
+  if (pl.bytes && (!a->workspace || a->workspace_bytes < pl.bytes)) return SWA_E_WORKSPACE;
   if (reinterpret_cast<uintptr_t>(a->workspace) & 255u) return SWA_E_ALIGN;
   PagedAttendParams p{};
   p.map = paged_map(&c);

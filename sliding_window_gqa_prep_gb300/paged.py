@@ -209,13 +209,21 @@ def paged_append(k, v, pos, cache_k, cache_v, page_table, row_start, lens, *, q=
 
 
 def paged_attend_workspace_size(B, T, nh, nk, hd, page, max_pages, max_rows, dtype=torch.bfloat16) -> int:
-    """Workspace bytes of paged_attend on the current device."""
+    """Workspace bytes of paged_attend on the current device (1: none is needed)."""
     a = _ATTEND.pack(B, nk, hd, page, 0, max_pages, _TYPES[dtype], 0, 0, 0, 0, 0, T, nh, max_rows, 0, 0.0, 0, 0, 0, 0,
                      0, 0, 0, 0, 0)
     n = int(_lib().swa_paged_attend_workspace_size(a))
     if n == 0:
         raise _abi.SwaError(_abi.SWA_E_SHAPE, "swa_paged_attend_workspace_size")
     return n
+
+
+@functools.lru_cache(maxsize=1024)
+def _attend_need(dev, B, T, nh, nk, hd, page, max_pages, max_rows, dtype) -> int:
+    """paged_attend_workspace_size for device dev (the current one); 0 for sizes it refuses."""
+    a = _ATTEND.pack(B, nk, hd, page, 0, max_pages, _TYPES[dtype], 0, 0, 0, 0, 0, T, nh, max_rows, 0, 0.0, 0, 0, 0, 0,
+                     0, 0, 0, 0, 0)
+    return int(_lib().swa_paged_attend_workspace_size(a))
 
 
 @_placed
@@ -238,12 +246,16 @@ def paged_attend(q, cache_k, cache_v, page_table, row_start, lens, scale: float,
         out = torch.zeros(T, nh, hd, device=q.device, dtype=q.dtype)
     wide = out.dtype == _F32
     op = _arg(out, "out", dev, _F32 if wide else q.dtype, (T, nh, hd))
-    if workspace is None:
-        need = _lib().swa_paged_attend_workspace_size(
-            _ATTEND.pack(*cache, T, nh, max_rows, wide, scale, 0, 0, 0, 0, 0, 0, 0, 0, 0))
-        workspace = torch.empty(max(need, 1), device=q.device, dtype=_U8)
+    ws = size = 0
+    if workspace is not None:
+        ws, size = _arg(workspace, "workspace", dev, _U8), workspace.numel()
+    else:
+        size = _attend_need(dev, B, T, nh, nk, hd, page, max_pages, max_rows, cache_k.dtype)
+        if size > 1:
+            workspace = torch.empty(size, device=q.device, dtype=_U8)
+            ws = workspace.data_ptr()
     a = _ATTEND.pack(*cache, T, nh, max_rows, wide, scale, qp, q_row, op, _opt(lse, "lse", dev, _F32, (T, nh)),
-                     _arg(workspace, "workspace", dev, _U8), workspace.numel(), _opt(err, "err", dev, _I32, (1,)),
+                     ws, size, _opt(err, "err", dev, _I32, (1,)),
                      ev_start.cuda_event if ev_start is not None else 0, ev_stop.cuda_event if ev_stop is not None else 0)
     _abi.check(_lib().swa_paged_attend(a, stream), "swa_paged_attend")
     return out
@@ -276,11 +288,16 @@ def paged_weigh(q, lse, cache_k, page_table, row_start, lens, scale: float, *, m
 
 def paged_evict_workspace_size(B, nk, page, max_pages, keep) -> int:
     """Workspace bytes of paged_evict."""
-    a = _EVICT.pack(B, nk, 0, page, 0, max_pages, 0, 0, 0, 0, 0, 0, keep, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0)
-    n = int(_lib().swa_paged_evict_workspace_size(a))
+    n = _evict_need(B, nk, page, max_pages, int(keep))
     if n == 0:
         raise _abi.SwaError(_abi.SWA_E_SHAPE, "swa_paged_evict_workspace_size")
     return n
+
+
+@functools.lru_cache(maxsize=1024)
+def _evict_need(B, nk, page, max_pages, keep) -> int:
+    return int(_lib().swa_paged_evict_workspace_size(
+        _EVICT.pack(B, nk, 0, page, 0, max_pages, 0, 0, 0, 0, 0, 0, keep, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0)))
 
 
 @_placed
@@ -302,8 +319,7 @@ def paged_evict(cache_k, cache_v, page_table, lens, weight, slot_pos, keep: int,
     if lens_out is None:
         lens_out = torch.empty_like(lens)
     if workspace is None:
-        need = _lib().swa_paged_evict_workspace_size(_EVICT.pack(*cache, keep, sinks, 0, 0, 0, 0, 0, 0, 0, 0, 0))
-        workspace = torch.empty(max(need, 1), device=cache_k.device, dtype=_U8)
+        workspace = torch.empty(max(_evict_need(B, nk, cache[3], cache[5], keep), 1), device=cache_k.device, dtype=_U8)
     a = _EVICT.pack(*cache, keep, sinks, wp, pp, _opt(recent_from, "recent_from", dev, _I32, (B,)),
                     _arg(weight_out, "weight_out", dev, _F32, shape), _arg(slot_pos_out, "slot_pos_out", dev, _I32, shape),
                     _arg(lens_out, "lens_out", dev, _I32, (B,)), _arg(workspace, "workspace", dev, _U8),

@@ -227,8 +227,9 @@ def test_attend_refusals(lib):
         assert call(_attend(**kw)) == _abi.SWA_E_SHAPE, kw
     for kw in (dict(q=FAKE + 8), dict(out=FAKE + 4), dict(q_row=516), dict(lse=FAKE + 2), dict(workspace=FAKE + 16)):
         assert call(_attend(**kw)) == _abi.SWA_E_ALIGN, kw
+    # contexts of more than 512 keys are split and need one
     for kw in (dict(workspace=None), dict(workspace_bytes=64)):
-        assert call(_attend(**kw)) == _abi.SWA_E_WORKSPACE, kw
+        assert call(_attend(cache=dict(max_pages=64), **kw)) == _abi.SWA_E_WORKSPACE, kw
     assert call(_attend(T=0)) == _abi.SWA_OK
     assert lib.swa_paged_attend_workspace_size(None) == 0
     assert lib.swa_paged_attend_workspace_size(ctypes.byref(_attend(nh=5))) == 0
