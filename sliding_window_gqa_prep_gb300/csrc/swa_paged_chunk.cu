@@ -82,74 +82,7 @@ __global__ void __launch_bounds__(ChunkCfg<D>::THREADS, 1)
   unsigned char* const sm = reinterpret_cast<unsigned char*>((reinterpret_cast<uintptr_t>(sm_raw) + 1023) & ~(uintptr_t)1023);
   unsigned char* const sm_kv = sm + NT * C::QB;
   const PagedAttendParams& a = p.a;
-  pdl_wait();
-  pdl_trigger();
-
-  // --- which item: a scan over the sequences' item counts
-  const int item_tok = NT * p.tile_tok;
-  {
-    uint32_t bits = 0;
-    const int E = (a.map.B + C::THREADS - 1) / C::THREADS;
-    int mine = 0;
-    for (int e = 0; e < E; ++e) {
-      const int b = tid * E + e;
-      if (b < a.map.B) mine += chunk_items(paged_seq(a.map, b, a.T, a.max_rows, bits), p, item_tok);
-    }
-    if (bits && blockIdx.x == 0 && blockIdx.y == 0) set_err(a.err, bits);
-    int incl = mine;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const int v = __shfl_up_sync(0xffffffffu, incl, o);
-      if (lane >= o) incl += v;
-    }
-    if (lane == 31) s_scan[warp] = incl;
-    if (tid == 0) {
-      s_b = -1;
-      s_abort = 0;
-    }
-    __syncthreads();
-    int before = incl - mine;
-    for (int w = 0; w < warp; ++w) before += s_scan[w];
-    const int want = blockIdx.x;
-    if (want >= before && want < before + mine) {
-      int off = want - before;
-      for (int e = 0; e < E; ++e) {
-        uint32_t ignore = 0;
-        const int n = chunk_items(paged_seq(a.map, tid * E + e, a.T, a.max_rows, ignore), p, item_tok);
-        if (off < n) {
-          s_b = tid * E + e;
-          s_idx = off;
-          break;
-        }
-        off -= n;
-      }
-    }
-    __syncthreads();
-  }
-  if (s_b < 0) {
-    if (p.splits > 1 && blockIdx.y == 0 && tid == 0) p.rec_desc[blockIdx.x] = make_int4(-1, 0, 0, 0);
-    return;
-  }
-  uint32_t ignore = 0;
-  const int b = s_b, g = s_idx % a.map.nk;
-  const PagedSeq s = paged_seq(a.map, b, a.T, a.max_rows, ignore);
-  // the item with the most keys first
-  const int n_qt = (s.t + item_tok - 1) / item_tok;
-  const int tok0 = (n_qt - 1 - s_idx / a.map.nk) * item_tok;
-  if (p.splits > 1 && blockIdx.y == 0 && tid == 0) p.rec_desc[blockIdx.x] = make_int4(b, g, tok0, 0);
-
-  // key tiles of each query tile, and this CTA's share [j0, j1) of the item's
-  int n_tile[NT], n_all = 0;
-#pragma unroll
-  for (int t = 0; t < NT; ++t) {
-    const int first = tok0 + t * p.tile_tok, last = min(first + p.tile_tok, s.t) - 1;
-    const int lim = last >= first ? min(s.len, s.len - s.t + last + 1) : 0;
-    n_tile[t] = lim > 0 ? (lim + KT - 1) / KT : 0;
-    n_all = max(n_all, n_tile[t]);
-  }
-  const int j0 = (int)((long long)n_all * blockIdx.y / p.splits), j1 = (int)((long long)n_all * (blockIdx.y + 1) / p.splits);
-  const int n = j1 - j0;                                   // tiles of this CTA
-
+  // what needs no global memory, before the wait for the kernel in front
   if (warp == W_LOAD) {
     if (lane == 0) {
       for (int i = 0; i < NS; ++i) {
@@ -173,8 +106,79 @@ __global__ void __launch_bounds__(ChunkCfg<D>::THREADS, 1)
   } else if (warp == W_MMA) {
     tc_alloc(&s_tmem, 512);
   }
-  tc_fence_before();
-  __syncthreads();
+  if (tid == 0) {
+    s_b = -1;
+    s_abort = 0;
+  }
+  pdl_wait();
+  pdl_trigger();
+
+  // --- which item: a scan over the sequences' item counts
+  const int item_tok = NT * p.tile_tok;
+  {
+    uint32_t bits = 0;
+    const int E = (a.map.B + C::THREADS - 1) / C::THREADS;
+    int mine = 0;
+    for (int e = 0; e < E; ++e) {
+      const int b = tid * E + e;
+      if (b < a.map.B) mine += chunk_items(paged_seq(a.map, b, a.T, a.max_rows, bits), p, item_tok);
+    }
+    if (bits && blockIdx.x == 0 && blockIdx.y == 0) set_err(a.err, bits);
+    int incl = mine;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int v = __shfl_up_sync(0xffffffffu, incl, o);
+      if (lane >= o) incl += v;
+    }
+    if (lane == 31) s_scan[warp] = incl;
+    __syncthreads();
+    int before = incl - mine;
+    for (int w = 0; w < warp; ++w) before += s_scan[w];
+    const int want = blockIdx.x;
+    if (want >= before && want < before + mine) {
+      int off = want - before;
+      for (int e = 0; e < E; ++e) {
+        uint32_t ignore = 0;
+        const int n = chunk_items(paged_seq(a.map, tid * E + e, a.T, a.max_rows, ignore), p, item_tok);
+        if (off < n) {
+          s_b = tid * E + e;
+          s_idx = off;
+          break;
+        }
+        off -= n;
+      }
+    }
+    tc_fence_before();
+    __syncthreads();
+  }
+  if (s_b < 0) {
+    if (p.splits > 1 && blockIdx.y == 0 && tid == 0) p.rec_desc[blockIdx.x] = make_int4(-1, 0, 0, 0);
+    if (warp == W_MMA) {
+      tc_fence_after();
+      tc_dealloc(s_tmem, 512);
+    }
+    return;
+  }
+  uint32_t ignore = 0;
+  const int b = s_b, g = s_idx % a.map.nk;
+  const PagedSeq s = paged_seq(a.map, b, a.T, a.max_rows, ignore);
+  // the item with the most keys first
+  const int n_qt = (s.t + item_tok - 1) / item_tok;
+  const int tok0 = (n_qt - 1 - s_idx / a.map.nk) * item_tok;
+  if (p.splits > 1 && blockIdx.y == 0 && tid == 0) p.rec_desc[blockIdx.x] = make_int4(b, g, tok0, 0);
+
+  // key tiles of each query tile, and this CTA's share [j0, j1) of the item's
+  int n_tile[NT], n_all = 0;
+#pragma unroll
+  for (int t = 0; t < NT; ++t) {
+    const int first = tok0 + t * p.tile_tok, last = min(first + p.tile_tok, s.t) - 1;
+    const int lim = last >= first ? min(s.len, s.len - s.t + last + 1) : 0;
+    n_tile[t] = lim > 0 ? (lim + KT - 1) / KT : 0;
+    n_all = max(n_all, n_tile[t]);
+  }
+  const int j0 = (int)((long long)n_all * blockIdx.y / p.splits), j1 = (int)((long long)n_all * (blockIdx.y + 1) / p.splits);
+  const int n = j1 - j0;                                   // tiles of this CTA
+
   tc_fence_after();
   const uint32_t tmem = __shfl_sync(0xffffffffu, s_tmem, 0);
   auto give_up = [&]() {
@@ -193,7 +197,7 @@ __global__ void __launch_bounds__(ChunkCfg<D>::THREADS, 1)
   if constexpr (NT == 2) asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
   if (warp == W_LOAD) {
     // ------------------------------------------------------------ loader
-    // lane i copies box i of a slot: `rows` keys x 64 features
+    // a slot is boxes of `rows` keys x 64 features
     const int page = 1 << a.map.page_shift, rows = min(page, KT), per_half = KT / rows;
     constexpr int HALVES = D / 64;
     const int32_t* table = a.map.table + (size_t)b * a.map.max_pages;
@@ -201,26 +205,27 @@ __global__ void __launch_bounds__(ChunkCfg<D>::THREADS, 1)
     bool ok = true;
     int issued = 0;
     auto load = [&](int j, bool is_v, int pos) {
-      const int slot = pos % NS, use = pos / NS;
+      const int slot = pos % NS, use = pos / NS, key0 = (j0 + j) * KT;
+      // lane bx looks up box bx of each half of the features (8 at most), before the wait
+      const int key = key0 + lane * rows;
+      int y = oob;
+      if (lane < per_half && key < s.len) {
+        const int id = table[key >> a.map.page_shift];
+        if (page_ok(a.map, id))
+          y = ((id * a.map.nk + g) << a.map.page_shift) + (key & (page - 1));
+        else
+          set_err(a.err, SWA_DERR_PAGE);
+      }
       if (use > 0 && !wait(&b_empty[slot], use - 1)) return false;
-      const int key0 = (j0 + j) * KT;
       const bool tail = is_v && key0 + KT > s.len;
       uint64_t* bar = tail ? &b_tail : &b_full[slot];
       if (lane == 0) mbar_arrive_expect_tx(bar, C::SLOT);
       __syncwarp();
       unsigned char* dst = sm_kv + slot * C::SLOT;
-      for (int i = lane; i < per_half * HALVES; i += 32) {
-        const int half = i / per_half, bx = i % per_half, key = key0 + bx * rows;
-        int y = oob;
-        if (key < s.len) {
-          const int id = table[key >> a.map.page_shift];
-          if (page_ok(a.map, id))
-            y = ((id * a.map.nk + g) << a.map.page_shift) + (key & (page - 1));
-          else
-            set_err(a.err, SWA_DERR_PAGE);
-        }
-        tma_2d(smem_u32(dst + half * (KT * 128) + bx * rows * 128), is_v ? &map_v : &map_k, half * 64, y, bar);
-      }
+      if (lane < per_half)
+#pragma unroll
+        for (int half = 0; half < HALVES; ++half)
+          tma_2d(smem_u32(dst + half * (KT * 128) + lane * rows * 128), is_v ? &map_v : &map_k, half * 64, y, bar);
       issued = pos + 1;
       if (tail) {
         // at most one tile of a sequence: its V rows from the last key on become zeros

@@ -130,6 +130,27 @@ __global__ void __launch_bounds__(kWeighThreads, 1)
   const int tid = threadIdx.x, lane = tid & 31, warp = __shfl_sync(0xffffffffu, tid >> 5, 0);
   unsigned char* const sm = reinterpret_cast<unsigned char*>((reinterpret_cast<uintptr_t>(sm_raw) + 1023) & ~(uintptr_t)1023);
   unsigned char* const sm_q = sm + NS * C::KB;
+  // what needs no global memory, before the wait for the kernel in front
+  if (warp == 8 && lane == 0) {
+    for (int i = 0; i < NS; ++i) {
+      mbar_init(&b_kfull[i], 1);
+      mbar_init(&b_kempty[i], 1);
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&b_qfull[i], 64);
+      mbar_init(&b_qempty[i], 1 + 8);
+    }
+    for (int i = 0; i < 4; ++i) {
+      mbar_init(&b_s[i], 1);
+      mbar_init(&b_sfree[i], 4);
+    }
+    mbar_init(&b_fin, 1);
+    mbar_fence_init();
+    s_b = -1;
+    s_abort = 0;
+  } else if (warp == 9) {
+    tc_alloc(&s_tmem, 512);
+  }
   pdl_wait();
   pdl_trigger();
 
@@ -150,10 +171,6 @@ __global__ void __launch_bounds__(kWeighThreads, 1)
       if (lane >= o) incl += v;
     }
     if (lane == 31) s_scan[warp] = incl;
-    if (tid == 0) {
-      s_b = -1;
-      s_abort = 0;
-    }
     __syncthreads();
     long long before = incl - mine, total = 0;
     for (int w = 0; w < kWeighThreads / 32; ++w) {
@@ -208,30 +225,16 @@ __global__ void __launch_bounds__(kWeighThreads, 1)
         }
       }
     }
+    tc_fence_before();
     __syncthreads();
   }
-  if (s_b < 0) return;
-
-  if (warp == 8 && lane == 0) {
-    for (int i = 0; i < NS; ++i) {
-      mbar_init(&b_kfull[i], 1);
-      mbar_init(&b_kempty[i], 1);
+  if (s_b < 0) {
+    if (warp == 9) {
+      tc_fence_after();
+      tc_dealloc(s_tmem, 512);
     }
-    for (int i = 0; i < 2; ++i) {
-      mbar_init(&b_qfull[i], 64);
-      mbar_init(&b_qempty[i], 1 + 8);
-    }
-    for (int i = 0; i < 4; ++i) {
-      mbar_init(&b_s[i], 1);
-      mbar_init(&b_sfree[i], 4);
-    }
-    mbar_init(&b_fin, 1);
-    mbar_fence_init();
-  } else if (warp == 9) {
-    tc_alloc(&s_tmem, 512);
+    return;
   }
-  tc_fence_before();
-  __syncthreads();
   tc_fence_after();
   const uint32_t tmem = __shfl_sync(0xffffffffu, s_tmem, 0);
   auto give_up = [&]() {
@@ -257,22 +260,24 @@ __global__ void __launch_bounds__(kWeighThreads, 1)
       const int32_t* table = p.map.table + (size_t)it.b * p.map.max_pages;
       for (int h = 0; ok && h < it.halves(); ++h) {
         const int slot = kc % NS, use = kc / NS;
+        // lane bx looks up box bx of each half of the features (8 at most), before the wait
+        const int key = it.tile * kUnit + h * 128 + lane * rows;
+        int y = oob;
+        if (lane < per_half && key < it.w.s.len) {
+          const int id = table[key >> p.map.page_shift];
+          if (page_ok(p.map, id))
+            y = ((id * p.map.nk + it.g) << p.map.page_shift) + (key & (page - 1));
+          else
+            set_err(p.err, SWA_DERR_PAGE);
+        }
         ok = use == 0 || wait(&b_kempty[slot], use - 1);
         if (!ok) break;
         if (lane == 0) mbar_arrive_expect_tx(&b_kfull[slot], C::KB);
         __syncwarp();
-        for (int i = lane; i < per_half * (D / 64); i += 32) {
-          const int half = i / per_half, bx = i % per_half, key = it.tile * kUnit + h * 128 + bx * rows;
-          int y = oob;
-          if (key < it.w.s.len) {
-            const int id = table[key >> p.map.page_shift];
-            if (page_ok(p.map, id))
-              y = ((id * p.map.nk + it.g) << p.map.page_shift) + (key & (page - 1));
-            else
-              set_err(p.err, SWA_DERR_PAGE);
-          }
-          tma_2d(smem_u32(sm + slot * C::KB + half * (128 * 128) + bx * rows * 128), &map_k, half * 64, y, &b_kfull[slot]);
-        }
+        if (lane < per_half)
+#pragma unroll
+          for (int half = 0; half < D / 64; ++half)
+            tma_2d(smem_u32(sm + slot * C::KB + half * (128 * 128) + lane * rows * 128), &map_k, half * 64, y, &b_kfull[slot]);
         ++kc;
       }
     }
@@ -390,6 +395,7 @@ __global__ void __launch_bounds__(kWeighThreads, 1)
       }
       tell(false);
       pending = qc++;
+      if (it.resident()) tell(true);        // the next load is a head away
       return true;
     };
     bool fresh = true;
