@@ -335,7 +335,6 @@ __global__ void __launch_bounds__(ChunkCfg<D>::THREADS, 1)
     };
     if (mine > 0) {
       until(&b_q[t], 0);
-      if (t == 1 && n_tile[0] > j0) until(&b_s[0], 0);
       s_mma(0);
     }
     for (int j = 0; j < mine; ++j) {
@@ -422,7 +421,7 @@ __global__ void __launch_bounds__(ChunkCfg<D>::THREADS, 1)
       if (__any_sync(0xffffffffu, raise) && j > 0) {
         const float f = raise ? ex2(m - mx) : 1.f;
         // with one S buffer S of this tile came after P V of the last one
-        if (SB == 2) ok &= wait(&b_pv[t], j - 1);
+        if (SB == 2) ok &= tc_wait(&b_pv[t], (uint32_t)((j - 1) & 1), &s_abort);
         if (SB == 2) tc_fence_after();
 #pragma unroll
         for (int i = 0; i < D / 32; ++i) {
@@ -457,16 +456,18 @@ __global__ void __launch_bounds__(ChunkCfg<D>::THREADS, 1)
         else tc_st16(c_s + h * (KT / 4), w);
         tc_wait_st();
         tc_fence_before();
+        // A wait sees only the parity of a phase: when this thread waits for the last P V, the
+        // one before must be known complete, and a wait for that one must not come after the
+        // last. With one S buffer the last S came after it; with two it is waited for here,
+        // while the last P V still lacks this half.
+        if (SB == 2 && h == 1 && j > 0 && j == mine - 1) ok &= tc_wait(&b_pv[t], (uint32_t)((j - 1) & 1), &s_abort);
         mbar_arrive(&b_p[t * SB + j % SB][h]);
       }
       float l0, l1;
       unpack64(add2(sum[0], sum[1]), l0, l1);
       l += l0 + l1;
     }
-    // a wait sees only the parity of a phase, so the one before must be known complete:
-    // with one S buffer the last S came after it, with two only after the one before that
-    if (SB == 2 && ok && mine > 1) ok = wait(&b_pv[t], mine - 2);
-    if (ok && mine > 0) ok = wait(&b_pv[t], mine - 1);
+    if (mine > 0) ok &= tc_wait(&b_pv[t], (uint32_t)((mine - 1) & 1), &s_abort);
     ok = __all_sync(0xffffffffu, ok);
     if (ok) {
       tc_fence_after();

@@ -9,9 +9,9 @@
 //
 // One CTA an SM. The units (sequence, KV head, 256 keys), each as dear as the query tiles
 // that see it, are laid end to end and cut evenly. Roles: warp 8 streams K tiles of 128
-// keys from the pages by TMA; warps 10 and 11 bring the query tiles (cp.async into the
-// swizzled layout, with each vector's lse and limit); warp 9 issues the products, two S
-// buffers in TMEM for each half of a unit; a warpgroup (warps 0-3, 4-7) sums each half, so
+// keys from the pages by TMA; warp 11 brings the query tiles (cp.async into the
+// swizzled layout, with each vector's lse and limit); warps 9 and 10 issue the products, two
+// S buffers in TMEM for each half of a unit; a warpgroup (warps 0-3, 4-7) sums each half, so
 // that a query tile serves 256 keys and nothing is exchanged. A sequence of at most two
 // query tiles keeps them in shared memory for all its keys, else they are streamed per
 // unit. The sums run in a fixed order: no atomics.
@@ -24,7 +24,9 @@ namespace swa {
 template <int D>
 struct WeighCfg {
   static constexpr int QN = D == 256 ? 64 : 128;       // query vectors of a tile
-  static constexpr int NS = D == 64 ? 8 : D == 128 ? 4 : 2;   // K slots of 128 keys
+  // K slots of 128 keys, half of them for each half of a unit: a wait sees only the parity
+  // of a barrier's phase, so whoever waits on a slot has to wait for each of its uses
+  static constexpr int NS = D == 64 ? 8 : D == 128 ? 4 : 2, NSH = NS / 2;
   static constexpr int KB = 128 * D * 2;               // bytes of a K tile
   static constexpr int QB = QN * D * 2;
   static constexpr int SMEM = NS * KB + 2 * QB + 1024;
@@ -117,10 +119,10 @@ template <typename T, int D>
 __global__ void __launch_bounds__(kWeighThreads, 1)
     paged_weigh_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constant__ PagedWeighParams p) {
   using C = WeighCfg<D>;
-  constexpr int QN = C::QN, NS = C::NS, CH = D / 8;
+  constexpr int QN = C::QN, NS = C::NS, NSH = C::NSH, CH = D / 8;
   constexpr bool BF = std::is_same<T, __nv_bfloat16>::value;
   extern __shared__ unsigned char sm_raw[];
-  __shared__ __align__(8) uint64_t b_kfull[NS], b_kempty[NS], b_qfull[2], b_qempty[2], b_s[4], b_sfree[4], b_fin;
+  __shared__ __align__(8) uint64_t b_kfull[NS], b_kempty[NS], b_qfull[2], b_qempty[2], b_s[4], b_sfree[4], b_fin[2];
   __shared__ __align__(16) float s_nlse[2][QN];             // -lse log2 e
   __shared__ __align__(16) int s_lim[2][QN];
   __shared__ long long s_scan[kWeighThreads / 32];
@@ -137,14 +139,14 @@ __global__ void __launch_bounds__(kWeighThreads, 1)
       mbar_init(&b_kempty[i], 1);
     }
     for (int i = 0; i < 2; ++i) {
-      mbar_init(&b_qfull[i], 64);
-      mbar_init(&b_qempty[i], 1 + 8);
+      mbar_init(&b_qfull[i], 32);
+      mbar_init(&b_qempty[i], 2 + 8);
+      mbar_init(&b_fin[i], 1);
     }
     for (int i = 0; i < 4; ++i) {
       mbar_init(&b_s[i], 1);
       mbar_init(&b_sfree[i], 4);
     }
-    mbar_init(&b_fin, 1);
     mbar_fence_init();
     s_b = -1;
     s_abort = 0;
@@ -250,168 +252,7 @@ __global__ void __launch_bounds__(kWeighThreads, 1)
   WeighIter<QN> it{p, weigh_seq<QN>(p, s_b, ignore), s_b, s_g, s_tile, s_left};
   bool ok = true;
 
-  if (warp == 8) {
-    // ------------------------------------------------------------ K tiles
-    const int page = 1 << p.map.page_shift, rows = min(page, 128), per_half = 128 / rows;
-    const int oob = p.map.num_pages * p.map.nk << p.map.page_shift;       // rows of the pool: reads zeros
-    int kc = 0;                             // tiles started
-    for (; ok && !it.done(); it.next()) {
-      if (it.qt0() >= it.w.nqt) continue;
-      const int32_t* table = p.map.table + (size_t)it.b * p.map.max_pages;
-      for (int h = 0; ok && h < it.halves(); ++h) {
-        const int slot = kc % NS, use = kc / NS;
-        // lane bx looks up box bx of each half of the features (8 at most), before the wait
-        const int key = it.tile * kUnit + h * 128 + lane * rows;
-        int y = oob;
-        if (lane < per_half && key < it.w.s.len) {
-          const int id = table[key >> p.map.page_shift];
-          if (page_ok(p.map, id))
-            y = ((id * p.map.nk + it.g) << p.map.page_shift) + (key & (page - 1));
-          else
-            set_err(p.err, SWA_DERR_PAGE);
-        }
-        ok = use == 0 || wait(&b_kempty[slot], use - 1);
-        if (!ok) break;
-        if (lane == 0) mbar_arrive_expect_tx(&b_kfull[slot], C::KB);
-        __syncwarp();
-        if (lane < per_half)
-#pragma unroll
-          for (int half = 0; half < D / 64; ++half)
-            tma_2d(smem_u32(sm + slot * C::KB + half * (128 * 128) + lane * rows * 128), &map_k, half * 64, y, &b_kfull[slot]);
-        ++kc;
-      }
-    }
-    if (!ok) {
-      give_up();
-      // copies in flight land before the CTA exits (bounded)
-      for (int u = max(0, kc - NS); u < kc; ++u) mbar_wait_bounded(&b_kfull[u % NS], (uint32_t)((u / NS) & 1), kWaitLimitNs);
-    }
-  } else if (warp == 9) {
-    // ------------------------------------------------------------ products
-    const bool leader = elect_one();
-    const uint64_t k_desc = sw128_desc(smem_u32(sm), 16), q_desc = sw128_desc(smem_u32(sm_q), 16);
-    int kc = 0, jc[2] = {0, 0}, qc = 0;     // K tiles, products of each half, query tiles loaded
-    int q_base = it.qt0();                  // first query tile kept of a resident head
-    while (ok && !it.done()) {
-      const int nqt = it.w.nqt, nh = it.halves();
-      const bool res = it.resident();
-      const int q_first = it.qt0();
-      for (int qt = q_first; ok && qt < nqt; ++qt) {
-        const int qi = res ? qc + qt - q_base : qc;
-        ok = wait(&b_qfull[qi & 1], qi >> 1);
-        const int n = min(QN, (it.w.nv - qt * QN + 31) & ~31);
-        const uint32_t id = tc_idesc_16(BF, false, n);
-        const uint64_t qd = q_desc + (uint64_t)(((qi & 1) * C::QB) >> 4);
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          if (!ok || h >= nh) continue;
-          const int slot = (kc + h) % NS, buf = 2 * h + (jc[h] & 1);
-          ok = (qt > q_first || wait(&b_kfull[slot], (kc + h) / NS)) &&
-               (jc[h] < 2 || wait(&b_sfree[buf], (jc[h] >> 1) - 1));
-          if (!ok) continue;
-          tc_fence_after();
-          if (leader) {
-            const uint64_t kd = k_desc + (uint64_t)((slot * C::KB) >> 4);
-#pragma unroll
-            for (int k = 0; k < D / 16; ++k)
-              mma_ss(tmem + buf * QN, kd + (((k >> 2) * (128 * 128) + (k & 3) * 32) >> 4),
-                     qd + (((k >> 2) * (QN * 128) + (k & 3) * 32) >> 4), id, k > 0);
-            tc_commit(&b_s[buf]);
-            if (qt == nqt - 1) tc_commit(&b_kempty[slot]);
-            if (!res && h == nh - 1) tc_commit(&b_qempty[qi & 1]);
-          }
-          __syncwarp();
-          ++jc[h];
-        }
-        if (!res) ++qc;
-      }
-      if (q_first < nqt) kc += nh;
-      if (!ok) break;
-      const bool moved = it.next();
-      if (moved && res) {
-        if (leader)
-          for (int i = q_base; i < nqt; ++i) tc_commit(&b_qempty[(qc + i - q_base) & 1]);
-        __syncwarp();
-        qc += nqt - q_base;
-      }
-      if (moved && !it.done()) q_base = it.qt0();
-    }
-    if (!ok) {
-      give_up();
-      if (leader) tc_commit(&b_fin);        // what was issued finishes before TMEM goes (bounded)
-      mbar_wait_bounded(&b_fin, 0, kWaitLimitNs);
-    }
-  } else if (warp >= 10) {
-    // ------------------------------------------------------------ query tiles
-    const int th = tid - 320;
-    int qc = 0, pending = -1;               // tiles started, the one whose arrival is still to be told
-    auto tell = [&](bool all) {
-      if (pending < 0) return;
-      if (all) asm volatile("cp.async.wait_group 0;" ::: "memory");
-      else asm volatile("cp.async.wait_group 1;" ::: "memory");
-      fence_proxy_async_smem();
-      mbar_arrive(&b_qfull[pending & 1]);
-      pending = -1;
-    };
-    auto load = [&](int qt) {
-      const int slot = qc & 1, use = qc >> 1;
-      if (use > 0 && !__all_sync(0xffffffffu, mbar_try_wait(&b_qempty[slot], (uint32_t)((use - 1) & 1)))) {
-        tell(true);                         // before a wait that may be long
-        if (!wait(&b_qempty[slot], use - 1)) return false;
-      }
-      const int v0 = qt * QN, n = min(QN, (it.w.nv - v0 + 31) & ~31);
-      const uint32_t dst = smem_u32(sm_q + slot * C::QB);
-      const T* qp = static_cast<const T*>(p.q);
-      // each thread's lse first: on its way while the copies are issued
-      constexpr int LR = QN / 64;
-      float lse[LR];
-#pragma unroll
-      for (int k = 0; k < LR; ++k) {
-        const int vec = v0 + th + k * 64;
-        lse[k] = INFINITY;                  // no query vector: weight 0
-        if (vec < it.w.nv) {
-          const int i = row_of(p, vec);
-          lse[k] = p.lse[(size_t)(it.w.s.r0 + i) * p.nh + it.g * p.hpg + vec - i * p.hpg];
-        }
-      }
-      // 64 threads: CH chunks of 64 / CH rows at a time
-#pragma unroll 4
-      for (int r = th / CH; r < n; r += 64 / CH) {
-        const int c = th % CH, vec = v0 + r;
-        const bool in = vec < it.w.nv;
-        const int i = in ? row_of(p, vec) : 0, h = in ? vec - i * p.hpg : 0;
-        const T* src = qp + (in ? (size_t)(it.w.s.r0 + i) * p.q_row + (size_t)(it.g * p.hpg + h) * D + c * 8 : 0);
-        asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;"
-                     :: "r"(dst + (c >> 3) * (QN * 128) + r * 128 + (((c & 7) ^ (r & 7)) << 4)), "l"(src), "r"(in ? 16 : 0)
-                     : "memory");
-      }
-      asm volatile("cp.async.commit_group;" ::: "memory");
-#pragma unroll
-      for (int k = 0; k < LR; ++k) {
-        const int vec = v0 + th + k * 64;
-        s_nlse[slot][th + k * 64] = lse[k] * -1.4426950408889634f;
-        s_lim[slot][th + k * 64] =
-            vec < it.w.nv ? min(it.w.s.len, it.w.s.len - it.w.s.t + row_of(p, vec) + 1) : 0;
-      }
-      tell(false);
-      pending = qc++;
-      if (it.resident()) tell(true);        // the next load is a head away
-      return true;
-    };
-    bool fresh = true;
-    while (ok && !it.done()) {
-      if (it.resident()) {
-        // the head's later key tiles need no query tile that its first one here does not
-        for (int qt = it.qt0(); fresh && ok && qt < it.w.nqt; ++qt) ok = load(qt);
-      } else {
-        for (int qt = it.qt0(); ok && qt < it.w.nqt; ++qt) ok = load(qt);
-      }
-      if (ok) fresh = it.next();
-    }
-    asm volatile("cp.async.wait_group 0;" ::: "memory");
-    if (ok) tell(true);
-    else give_up();
-  } else {
+  if (warp < 8) {
     // ------------------------------------------------------------ sums: thread = key
     const int h = warp >> 2, r = tid & 127;
     const uint32_t lanes = tmem + ((uint32_t)((warp & 3) * 32) << 16) + h * 2 * QN;
@@ -501,6 +342,180 @@ __global__ void __launch_bounds__(kWeighThreads, 1)
       }
       if (moved && !it.done()) q_base = it.qt0();
     }
+    if (!ok) give_up();
+  } else if (warp == 8) {
+    // ------------------------------------------------------------ K tiles
+    const int page = 1 << p.map.page_shift, rows = min(page, 128), per_half = 128 / rows;
+    const int oob = p.map.num_pages * p.map.nk << p.map.page_shift;       // rows of the pool: reads zeros
+    int kc[2] = {0, 0};                     // tiles started of each half
+    for (; ok && !it.done(); it.next()) {
+      if (it.qt0() >= it.w.nqt) continue;
+      const int32_t* table = p.map.table + (size_t)it.b * p.map.max_pages;
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        if (!ok || h >= it.halves()) continue;
+        const int slot = h * NSH + kc[h] % NSH, use = kc[h] / NSH;
+        // lane bx looks up box bx of each half of the features (8 at most), before the wait
+        const int key = it.tile * kUnit + h * 128 + lane * rows;
+        int y = oob;
+        if (lane < per_half && key < it.w.s.len) {
+          const int id = table[key >> p.map.page_shift];
+          if (page_ok(p.map, id))
+            y = ((id * p.map.nk + it.g) << p.map.page_shift) + (key & (page - 1));
+          else
+            set_err(p.err, SWA_DERR_PAGE);
+        }
+        ok = use == 0 || wait(&b_kempty[slot], use - 1);
+        if (!ok) continue;
+        if (lane == 0) mbar_arrive_expect_tx(&b_kfull[slot], C::KB);
+        __syncwarp();
+        if (lane < per_half)
+#pragma unroll
+          for (int half = 0; half < D / 64; ++half)
+            tma_2d(smem_u32(sm + slot * C::KB + half * (128 * 128) + lane * rows * 128), &map_k, half * 64, y, &b_kfull[slot]);
+        ++kc[h];
+      }
+    }
+    // commits arrive at their barriers on their own time: the last ones must have done so
+    // before the CTA (and its shared memory) goes
+    for (int h = 0; h < 2; ++h)
+      for (int u = max(0, kc[h] - NSH); ok && u < kc[h]; ++u) ok = wait(&b_kempty[h * NSH + u % NSH], u / NSH);
+    if (!ok) {
+      give_up();
+      // copies in flight land before the CTA exits (bounded)
+      for (int h = 0; h < 2; ++h)
+        for (int u = max(0, kc[h] - NSH); u < kc[h]; ++u)
+          mbar_wait_bounded(&b_kfull[h * NSH + u % NSH], (uint32_t)((u / NSH) & 1), kWaitLimitNs);
+    }
+  } else if (warp <= 10) {
+    // ------------------------------------------------------------ products, a warp a half
+    // Waits, issue and commits take a warp about as long as the sums take a warpgroup.
+    // A wait that gave up leaves ok false and the role goes on to its end (no votes): what
+    // follows only touches this CTA's own shared memory and TMEM, and nothing is written.
+    const int h = warp - 9;
+    const bool leader = elect_one();
+    const uint64_t k_desc = sw128_desc(smem_u32(sm), 16), q_desc = sw128_desc(smem_u32(sm_q), 16);
+    auto until = [&](uint64_t* bar, int phase) { ok &= tc_wait(bar, (uint32_t)(phase & 1), &s_abort); };
+    int kc = 0, jc = 0, qc = 0, q_seen = 0; // this half's K tiles and products, query tiles loaded, known to be there
+    int q_base = it.qt0();                  // first query tile kept of a resident head
+    while (!it.done()) {
+      const int nqt = it.w.nqt, nh = it.halves(), q_first = it.qt0();
+      const bool res = it.resident();
+      for (int qt = q_first; qt < nqt; ++qt) {
+        const int qi = res ? qc + qt - q_base : qc;
+        if (qi >= q_seen) {
+          until(&b_qfull[qi & 1], qi >> 1);
+          q_seen = qi + 1;
+        }
+        if (h < nh) {
+          const int slot = h * NSH + kc % NSH, buf = 2 * h + (jc & 1);
+          if (qt == q_first) until(&b_kfull[slot], kc / NSH);
+          if (jc >= 2) until(&b_sfree[buf], (jc >> 1) - 1);
+          tc_fence_after();
+          if (leader) {
+            const int n = min(QN, (it.w.nv - qt * QN + 31) & ~31);
+            const uint32_t id = tc_idesc_16(BF, false, n);
+            const uint64_t kd = k_desc + (uint64_t)((slot * C::KB) >> 4), qd = q_desc + (uint64_t)(((qi & 1) * C::QB) >> 4);
+#pragma unroll
+            for (int k = 0; k < D / 16; ++k)
+              mma_ss(tmem + buf * QN, kd + (((k >> 2) * (128 * 128) + (k & 3) * 32) >> 4),
+                     qd + (((k >> 2) * (QN * 128) + (k & 3) * 32) >> 4), id, k > 0);
+            tc_commit(&b_s[buf]);
+            if (qt == nqt - 1) tc_commit(&b_kempty[slot]);
+          }
+          __syncwarp();
+          ++jc;
+        }
+        if (!res) {
+          if (leader) tc_commit(&b_qempty[qi & 1]);
+          __syncwarp();
+          ++qc;
+        }
+      }
+      if (q_first < nqt && h < nh) ++kc;
+      const bool moved = it.next();
+      if (moved && res) {
+        if (leader)
+          for (int i = q_base; i < nqt; ++i) tc_commit(&b_qempty[(qc + i - q_base) & 1]);
+        __syncwarp();
+        qc += nqt - q_base;
+      }
+      if (moved && !it.done()) q_base = it.qt0();
+    }
+    // what was issued, commits among it, finishes before TMEM and shared memory go (bounded)
+    if (leader) tc_commit(&b_fin[h]);
+    ok = __all_sync(0xffffffffu, ok && mbar_wait_bounded(&b_fin[h], 0, kWaitLimitNs));
+    if (!ok) give_up();
+  } else if (warp == 11) {
+    // ------------------------------------------------------------ query tiles
+    const int th = lane;
+    int qc = 0, pending = -1;               // tiles started, the one whose arrival is still to be told
+    auto tell = [&](bool all) {
+      if (pending < 0) return;
+      if (all) asm volatile("cp.async.wait_group 0;" ::: "memory");
+      else asm volatile("cp.async.wait_group 1;" ::: "memory");
+      fence_proxy_async_smem();
+      mbar_arrive(&b_qfull[pending & 1]);
+      pending = -1;
+    };
+    auto load = [&](int qt) {
+      const int slot = qc & 1, use = qc >> 1;
+      if (use > 0 && !__all_sync(0xffffffffu, mbar_try_wait(&b_qempty[slot], (uint32_t)((use - 1) & 1)))) {
+        tell(true);                         // before a wait that may be long
+        if (!wait(&b_qempty[slot], use - 1)) return false;
+      }
+      const int v0 = qt * QN, n = min(QN, (it.w.nv - v0 + 31) & ~31);
+      const uint32_t dst = smem_u32(sm_q + slot * C::QB);
+      const T* qp = static_cast<const T*>(p.q);
+      // each thread's lse first: on its way while the copies are issued
+      constexpr int LR = QN / 32;
+      float lse[LR];
+#pragma unroll
+      for (int k = 0; k < LR; ++k) {
+        const int vec = v0 + th + k * 32;
+        lse[k] = INFINITY;                  // no query vector: weight 0
+        if (vec < it.w.nv) {
+          const int i = row_of(p, vec);
+          lse[k] = p.lse[(size_t)(it.w.s.r0 + i) * p.nh + it.g * p.hpg + vec - i * p.hpg];
+        }
+      }
+      // 32 lanes: CH chunks of 32 / CH rows at a time
+#pragma unroll 4
+      for (int r = th / CH; r < n; r += 32 / CH) {
+        const int c = th % CH, vec = v0 + r;
+        const bool in = vec < it.w.nv;
+        const int i = in ? row_of(p, vec) : 0, h = in ? vec - i * p.hpg : 0;
+        const T* src = qp + (in ? (size_t)(it.w.s.r0 + i) * p.q_row + (size_t)(it.g * p.hpg + h) * D + c * 8 : 0);
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;"
+                     :: "r"(dst + (c >> 3) * (QN * 128) + r * 128 + (((c & 7) ^ (r & 7)) << 4)), "l"(src), "r"(in ? 16 : 0)
+                     : "memory");
+      }
+      asm volatile("cp.async.commit_group;" ::: "memory");
+#pragma unroll
+      for (int k = 0; k < LR; ++k) {
+        const int vec = v0 + th + k * 32;
+        s_nlse[slot][th + k * 32] = lse[k] * -1.4426950408889634f;
+        s_lim[slot][th + k * 32] =
+            vec < it.w.nv ? min(it.w.s.len, it.w.s.len - it.w.s.t + row_of(p, vec) + 1) : 0;
+      }
+      tell(false);
+      pending = qc++;
+      if (it.resident()) tell(true);        // the next load is a head away
+      return true;
+    };
+    bool fresh = true;
+    while (ok && !it.done()) {
+      if (it.resident()) {
+        // the head's later key tiles need no query tile that its first one here does not
+        for (int qt = it.qt0(); fresh && ok && qt < it.w.nqt; ++qt) ok = load(qt);
+      } else {
+        for (int qt = it.qt0(); ok && qt < it.w.nqt; ++qt) ok = load(qt);
+      }
+      if (ok) fresh = it.next();
+    }
+    asm volatile("cp.async.wait_group 0;" ::: "memory");
+    tell(true);
+    for (int q = max(0, qc - 2); ok && q < qc; ++q) ok = wait(&b_qempty[q & 1], q >> 1);   // as for K above
     if (!ok) give_up();
   }
   __syncwarp();
