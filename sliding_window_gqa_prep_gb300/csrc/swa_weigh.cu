@@ -7,8 +7,8 @@
 // Bytes: K once (few rows: bound by that); operations: 2 hd and one exponential a pair, at
 // hd 128 both 512 clk an SM for 128 x 128 pairs (8192 operations and 32 exponentials a clk).
 //
-// One CTA an SM. The units (sequence, KV head, 256 keys), each as dear as the query tiles
-// that see it, are laid end to end and cut evenly. Roles: warp 8 streams K tiles of 128
+// One CTA an SM. The units (sequence, KV head, 256 keys), each with its cost (tile_cost), are
+// laid end to end and cut evenly. Roles: warp 8 streams K tiles of 128
 // keys from the pages by TMA; warp 11 brings the query tiles (cp.async into the
 // swizzled layout, with each vector's lse and limit); warps 9 and 10 issue the products, two
 // S buffers in TMEM for each half of a unit; a warpgroup (warps 0-3, 4-7) sums each half, so
@@ -33,6 +33,10 @@ struct WeighCfg {
 };
 constexpr int kWeighThreads = 384;
 constexpr int kUnit = 256;     // keys of a unit
+// Cost of a unit in the time of 32 query columns (about 250 clk): two query tiles' worth of
+// fixed work at least, and a query tile costs its columns and one more. kUnitCost covers the
+// columns that the last query tile may lack, so that every unit costs something.
+constexpr int kUnitCost = 5;
 
 struct PagedWeighParams {
   PagedMap map;
@@ -58,6 +62,7 @@ __device__ __forceinline__ int row_of(const PagedWeighParams& p, int vec) {
 struct WeighSeq {
   PagedSeq s;
   int nv, nqt, n_tiles, n_full;   // query vectors, query tiles, key tiles, key tiles seen by every query tile
+  int base;                       // cost of a unit besides its query tiles
 };
 template <int QN>
 __device__ __forceinline__ WeighSeq weigh_seq(const PagedWeighParams& p, int b, uint32_t& bits) {
@@ -66,7 +71,8 @@ __device__ __forceinline__ WeighSeq weigh_seq(const PagedWeighParams& p, int b, 
   w.nv = w.s.t * p.hpg;
   w.nqt = (w.nv + QN - 1) / QN;
   w.n_tiles = (w.s.len + kUnit - 1) / kUnit;
-  w.n_full = w.s.len >= w.s.t ? min(w.n_tiles, (w.s.len - w.s.t) / kUnit + 1) : 0;
+  w.n_full = w.nqt <= 1 ? w.n_tiles : w.s.len >= w.s.t ? min(w.n_tiles, (w.s.len - w.s.t) / kUnit + 1) : 0;
+  w.base = kUnitCost - (w.nqt > 0 ? (w.nqt * QN - w.nv) / 32 : 0);   // the last query tile's missing columns
   return w;
 }
 // First query tile that sees keys of tile `tile`: its last row has a limit above the tile's
@@ -78,12 +84,11 @@ __device__ __forceinline__ int first_qt(const PagedWeighParams& p, const WeighSe
 }
 template <int QN>
 __device__ __forceinline__ int tile_cost(const PagedWeighParams& p, const WeighSeq& w, int tile) {
-  return max(1, w.nqt - first_qt<QN>(p, w, tile));
+  return w.base + (w.nqt - first_qt<QN>(p, w, tile)) * (QN / 32 + 1);
 }
 template <int QN>
 __device__ __forceinline__ long long head_cost(const PagedWeighParams& p, const WeighSeq& w) {
-  long long c = (long long)w.n_full * max(1, w.nqt);
-  if (w.nqt <= 1) return w.n_tiles;
+  long long c = (long long)w.n_full * (w.base + w.nqt * (QN / 32 + 1));
   for (int i = w.n_full; i < w.n_tiles; ++i) c += tile_cost<QN>(p, w, i);
   return c;
 }
@@ -197,10 +202,9 @@ __global__ void __launch_bounds__(kWeighThreads, 1)
         }
         int g = at >= u0 ? 0 : (int)((u0 - at) / hc);
         at += hc * g;
-        const int full = max(1, w.nqt);
+        const int full = w.base + w.nqt * (QN / 32 + 1);
         int tile = at >= u0 ? 0 : (int)min((long long)w.n_full, (u0 - at + full - 1) / full);
-        if (w.nqt <= 1 && at < u0) tile = (int)(u0 - at);
-        at += (long long)min(tile, w.nqt <= 1 ? tile : w.n_full) * full;
+        at += (long long)tile * full;
         while (tile < w.n_tiles && at < u0) at += tile_cost<QN>(p, w, tile++);
         if (tile == w.n_tiles) {            // the head's units all start before u0: the next head's first
           tile = 0;
@@ -289,23 +293,32 @@ __global__ void __launch_bounds__(kWeighThreads, 1)
               __syncwarp();
               if (lane == 0) mbar_arrive(&b_sfree[2 * h + buf]);
             }
+            // 16 columns at a time: first their scaled scores, then their exponentials
 #pragma unroll
-            for (int k = 0; k < W; k += 4) {
-              const ulonglong2 l2 = *reinterpret_cast<const ulonglong2*>(&s_nlse[slot][c + k]);
-              float e[4];
-              unpack64(fma2(pack64(x[k >> 5][k & 31], x[k >> 5][(k & 31) + 1]), mul2, l2.x), e[0], e[1]);
-              unpack64(fma2(pack64(x[k >> 5][(k & 31) + 2], x[k >> 5][(k & 31) + 3]), mul2, l2.y), e[2], e[3]);
+            for (int k = 0; k < W; k += 16) {
+              float e[16];
 #pragma unroll
-              for (int i = 0; i < 4; ++i) e[i] = ex2(e[i]);
-              if constexpr (decltype(masked)::value) {
-                const int4 lm = *reinterpret_cast<const int4*>(&s_lim[slot][c + k]);
-                e[0] = key < lm.x ? e[0] : 0.f;
-                e[1] = key < lm.y ? e[1] : 0.f;
-                e[2] = key < lm.z ? e[2] : 0.f;
-                e[3] = key < lm.w ? e[3] : 0.f;
+              for (int i = 0; i < 16; i += 4) {
+                const ulonglong2 l2 = *reinterpret_cast<const ulonglong2*>(&s_nlse[slot][c + k + i]);
+                const uint32_t* y = &x[(k + i) >> 5][(k + i) & 31];
+                unpack64(fma2(pack64(y[0], y[1]), mul2, l2.x), e[i], e[i + 1]);
+                unpack64(fma2(pack64(y[2], y[3]), mul2, l2.y), e[i + 2], e[i + 3]);
               }
-              sum[(k >> 1) & 2] = add2(sum[(k >> 1) & 2], pack64(__float_as_uint(e[0]), __float_as_uint(e[1])));
-              sum[((k >> 1) & 2) + 1] = add2(sum[((k >> 1) & 2) + 1], pack64(__float_as_uint(e[2]), __float_as_uint(e[3])));
+#pragma unroll
+              for (int i = 0; i < 16; ++i) e[i] = ex2(e[i]);
+              if constexpr (decltype(masked)::value) {
+#pragma unroll
+                for (int i = 0; i < 16; i += 4) {
+                  const int4 lm = *reinterpret_cast<const int4*>(&s_lim[slot][c + k + i]);
+                  e[i] = key < lm.x ? e[i] : 0.f;
+                  e[i + 1] = key < lm.y ? e[i + 1] : 0.f;
+                  e[i + 2] = key < lm.z ? e[i + 2] : 0.f;
+                  e[i + 3] = key < lm.w ? e[i + 3] : 0.f;
+                }
+              }
+#pragma unroll
+              for (int i = 0; i < 16; i += 2)
+                sum[(i >> 1) & 3] = add2(sum[(i >> 1) & 3], pack64(__float_as_uint(e[i]), __float_as_uint(e[i + 1])));
             }
           };
           // some row of the tile does not see all keys of this half
@@ -458,7 +471,7 @@ __global__ void __launch_bounds__(kWeighThreads, 1)
       mbar_arrive(&b_qfull[pending & 1]);
       pending = -1;
     };
-    auto load = [&](int qt) {
+    auto load = [&](int qt, bool last) {     // last: the next load may be far away
       const int slot = qc & 1, use = qc >> 1;
       if (use > 0 && !__all_sync(0xffffffffu, mbar_try_wait(&b_qempty[slot], (uint32_t)((use - 1) & 1)))) {
         tell(true);                         // before a wait that may be long
@@ -500,16 +513,16 @@ __global__ void __launch_bounds__(kWeighThreads, 1)
       }
       tell(false);
       pending = qc++;
-      if (it.resident()) tell(true);        // the next load is a head away
+      if (last) tell(true);
       return true;
     };
     bool fresh = true;
     while (ok && !it.done()) {
       if (it.resident()) {
         // the head's later key tiles need no query tile that its first one here does not
-        for (int qt = it.qt0(); fresh && ok && qt < it.w.nqt; ++qt) ok = load(qt);
+        for (int qt = it.qt0(); fresh && ok && qt < it.w.nqt; ++qt) ok = load(qt, qt == it.w.nqt - 1);
       } else {
-        for (int qt = it.qt0(); ok && qt < it.w.nqt; ++qt) ok = load(qt);
+        for (int qt = it.qt0(); ok && qt < it.w.nqt; ++qt) ok = load(qt, false);
       }
       if (ok) fresh = it.next();
     }
