@@ -3,9 +3,8 @@
 // One cluster per (sequence, KV head) does the whole eviction in one launch, each CTA a
 // contiguous share of the slots:
 //   1. keys of its slots into shared memory (an order-preserving 32-bit key);
-//   2. the n'-th largest key by four histogram passes of 8 bits; the CTAs' histograms are
-//      summed through distributed shared memory (three passes of 11 bits read eight times
-//      the bins there and took 30 instead of 21 thousand clk for 8 CTAs);
+//   2. the n'-th largest key by histogram passes over its digits; the CTAs' histograms are
+//      summed through distributed shared memory;
 //   3. two walks in slot order (a warp a run of slots, ranks by ballots): the first counts
 //      the freed and the moved slots, the second numbers them, writes the kept slots'
 //      weights and positions and the two lists (slots and rows);
@@ -40,7 +39,6 @@ struct PagedEvictParams {
 constexpr int kEThreads = 512, kEWarps = kEThreads / 32;
 constexpr int kSlotsPerCta = 4096;          // a cluster of (capacity / this), 1 to 8, CTAs
 constexpr int kMaxKeySlots = 40960;         // keys of a CTA in shared memory; longer shares are read again
-constexpr int kBins = 256;                  // a digit of 8 bits
 constexpr int kMaxCluster = 8;
 
 // Descending order of slots as descending order of this key: protected slots first,
@@ -70,16 +68,28 @@ __device__ __forceinline__ int block_exclusive(int v, int* s_sums) {
   return before + incl - v;
 }
 
+// CL: a cluster of CTAs a (sequence, KV head), else one CTA
+template <bool CL>
 __global__ void __launch_bounds__(kEThreads, 2) paged_evict_kernel(const PagedEvictParams p) {
   extern __shared__ uint32_t s_keys[];
-  __shared__ __align__(16) int hist[4][kBins];
+  __shared__ __align__(16) int hist[CL ? 4 : 3][CL ? 256 : 2048];
   __shared__ int s_sums[kEWarps], s_eq[kEWarps], s_freed[kEWarps], s_moved[kEWarps];
   __shared__ int2 s_tot;                    // this CTA's freed and moved slots
   __shared__ uint32_t s_digit;
   __shared__ int s_need;
   cg::cluster_group cluster = cg::this_cluster();
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const int CS = (int)cluster.num_blocks(), rank = (int)cluster.block_rank();
+  const int CS = CL ? (int)cluster.num_blocks() : 1, rank = CL ? (int)cluster.block_rank() : 0;
+  constexpr int MC = CL ? kMaxCluster : 1;
+  auto sync_all = [&]() {
+    if constexpr (CL) cluster.sync();
+    else __syncthreads();
+  };
+  // shared memory of CTA r of the cluster
+  auto peer = [&](auto* x, int r) {
+    if constexpr (CL) return cluster.map_shared_rank(x, r);
+    else return x;
+  };
   const int item = blockIdx.x / CS, b = item / p.map.nk, g = item % p.map.nk;
   pdl_wait();
   pdl_trigger();
@@ -113,7 +123,11 @@ __global__ void __launch_bounds__(kEThreads, 2) paged_evict_kernel(const PagedEv
   };
   const bool cached = share <= p.key_slots;
   auto key_of = [&](int j) { return cached ? s_keys[j - lo] : make_key(j); };
-  for (int i = tid; i < 4 * kBins; i += kEThreads) (&hist[0][0])[i] = 0;
+  // Digits of the key: 11, 11 and 10 bits in a CTA alone (evict of 64 of 2112 slots: 18.5
+  // instead of 20.8 us); four of 8 bits in a cluster, which reads every CTA's bins (30 and 21
+  // thousand clk for 8 CTAs)
+  const int n_pass = CL ? 4 : 3;
+  for (int i = tid; i < (int)(sizeof(hist) / 4); i += kEThreads) (&hist[0][0])[i] = 0;
   if (cached) {
 #pragma unroll 8
     for (int j = lo + tid; j < hi; j += kEThreads) s_keys[j - lo] = make_key(j);
@@ -124,26 +138,26 @@ __global__ void __launch_bounds__(kEThreads, 2) paged_evict_kernel(const PagedEv
   uint32_t prefix = 0;
   int need = keep;                          // slots still to take among keys with this prefix
 #pragma unroll 1
-  for (int pass = 0; pass < 4; ++pass) {
-    const int shift = 24 - 8 * pass;
+  for (int pass = 0; pass < n_pass; ++pass) {
+    const int bits = CL ? 8 : pass < 2 ? 11 : 10, shift = CL ? 24 - 8 * pass : pass == 0 ? 21 : pass == 1 ? 10 : 0;
     for (int j = lo + tid; j < hi; j += kEThreads) {
       const uint32_t k = key_of(j);
-      if (pass == 0 || k >> (shift + 8) == prefix) atomicAdd(&hist[pass][(k >> shift) & 255u], 1);
+      if (pass == 0 || k >> (shift + bits) == prefix) atomicAdd(&hist[pass][(k >> shift) & ((1u << bits) - 1)], 1);
     }
-    cluster.sync();
+    sync_all();
     // thread t holds the bins 4t .. 4t + 3 counted from the top, summed over the cluster
     int c[4] = {0, 0, 0, 0};
-    const int top = kBins - 4 - 4 * tid;
+    const int top = (1 << bits) - 4 - 4 * tid;
     if (top >= 0) {
-      int4 v[kMaxCluster];
+      int4 v[MC];
 #pragma unroll
-      for (int i = 0; i < kMaxCluster; ++i) {   // all under way together; each CTA starts at its own
+      for (int i = 0; i < MC; ++i) {   // all under way together; each CTA starts at its own
         v[i] = make_int4(0, 0, 0, 0);
         if (i < CS)
-          v[i] = *reinterpret_cast<const int4*>(cluster.map_shared_rank(&hist[pass][top], (rank + i) & (CS - 1)));
+          v[i] = *reinterpret_cast<const int4*>(peer(&hist[pass][top], (rank + i) & (CS - 1)));
       }
 #pragma unroll
-      for (int i = 0; i < kMaxCluster; ++i) {
+      for (int i = 0; i < MC; ++i) {
         c[0] += v[i].w;
         c[1] += v[i].z;
         c[2] += v[i].y;
@@ -160,16 +174,16 @@ __global__ void __launch_bounds__(kEThreads, 2) paged_evict_kernel(const PagedEv
       before += c[i];
     }
     __syncthreads();
-    prefix = prefix << 8 | s_digit;
+    prefix = prefix << bits | s_digit;
     need = s_need;
   }
   // keys above `prefix` stay, and of those that equal it the first `need` in slot order;
   // the CTAs before this one hold eq_before of them
-  const uint32_t digit = prefix & 255u;
+  const uint32_t digit = prefix & (CL ? 255u : 1023u);
   int eq_before = 0;
 #pragma unroll
-  for (int r = 0; r < kMaxCluster; ++r)
-    if (r < rank) eq_before += *cluster.map_shared_rank(&hist[3][digit], r);
+  for (int r = 0; r < MC; ++r)
+    if (r < rank) eq_before += *peer(&hist[n_pass - 1][digit], r);
 
   // walks: warp w takes slots [wlo, whi) in order
   const int run = ((hi - lo + kEWarps - 1) / kEWarps + 31) & ~31;
@@ -214,13 +228,13 @@ __global__ void __launch_bounds__(kEThreads, 2) paged_evict_kernel(const PagedEv
   if (warp == kEWarps - 1 && lane == 0) {
     s_tot = make_int2(n_freed + s_freed[warp], n_moved + s_moved[warp]);
   }
-  cluster.sync();
+  sync_all();
   int count = 0;                            // rows that move, in the whole cluster
-  int2 tot[kMaxCluster];
+  int2 tot[MC];
 #pragma unroll
-  for (int r = 0; r < kMaxCluster; ++r) tot[r] = r < CS ? *cluster.map_shared_rank(&s_tot, r) : make_int2(0, 0);
+  for (int r = 0; r < MC; ++r) tot[r] = r < CS ? *peer(&s_tot, r) : make_int2(0, 0);
 #pragma unroll
-  for (int r = 0; r < kMaxCluster; ++r) {
+  for (int r = 0; r < MC; ++r) {
     if (r < rank) {
       n_freed += tot[r].x;
       n_moved += tot[r].y;
@@ -263,7 +277,7 @@ __global__ void __launch_bounds__(kEThreads, 2) paged_evict_kernel(const PagedEv
       }
     }
   }
-  cluster.sync();                           // the lists are complete (and no histogram is read any more)
+  sync_all();                           // the lists are complete (and no histogram is read any more)
 
   // weights and positions of the moved slots
   for (int i = rank * kEThreads + tid; i < count; i += CS * kEThreads) {
@@ -356,8 +370,12 @@ int swa_paged_evict(const swa_paged_evict_args* a, cudaStream_t stream) {
   while (cs < kMaxCluster && (long long)cs * kSlotsPerCta < p.map.cap) cs *= 2;
   const int share = ((p.map.cap + cs - 1) / cs + 31) & ~31;
   p.key_slots = share < kMaxKeySlots ? share : kMaxKeySlots;
-  const cudaError_t e = allow_smem<paged_evict_kernel>(kMaxKeySlots * 4);
+  const cudaError_t e = cs > 1 ? allow_smem<paged_evict_kernel<true>>(kMaxKeySlots * 4)
+                               : allow_smem<paged_evict_kernel<false>>(kMaxKeySlots * 4);
   if (e != cudaSuccess) return cuda_status(e);
+  if (cs == 1)
+    return finish_launch(launch_pdl(paged_evict_kernel<false>, dim3((unsigned)items), dim3(kEThreads),
+                                    (size_t)p.key_slots * 4, stream, p));
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)(items * cs));
   cfg.blockDim = dim3(kEThreads);
@@ -371,7 +389,7 @@ int swa_paged_evict(const swa_paged_evict_args* a, cudaStream_t stream) {
   attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 2;
-  return finish_launch(cudaLaunchKernelEx(&cfg, paged_evict_kernel, p));
+  return finish_launch(cudaLaunchKernelEx(&cfg, paged_evict_kernel<true>, p));
 }
 
 }  // extern "C"
