@@ -72,10 +72,11 @@ class Batch:
         for b in range(B):
             self.table[b, :need[b]] = order[at:at + need[b]].to(torch.int32)
             at += need[b]
-            for j in range(lens[b]):
-                p = int(self.table[b, j // page])
-                k[p, :, j % page] = torch.randn(nk, hd, generator=g) * sharp
-                v[p, :, j % page] = torch.randn(nk, hd, generator=g)
+            for i in range(need[b]):
+                p, n = int(self.table[b, i]), min(page, lens[b] - i * page)
+                if n > 0:
+                    k[p, :, :n] = torch.randn(nk, n, hd, generator=g) * sharp
+                    v[p, :, :n] = torch.randn(nk, n, hd, generator=g)
         self.k, self.v = k.to(dtype).cuda(), v.to(dtype).cuda()
         self.start = [0]
         for x in t:
@@ -368,6 +369,43 @@ def test_attend_reports():
     bt.check(o, l, tuple(pick(x) for x in ref))
 
 
+def _many(seed, B, lo, hi, rows):
+    """Many short sequences: several items and units a CTA, odd and even ones, some without
+    rows or keys."""
+    g = torch.Generator().manual_seed(seed)
+    lens = torch.randint(lo, hi + 1, (B,), generator=g).tolist()
+    t = [rows[int(x)] for x in torch.randint(0, len(rows), (B,), generator=g)]
+    for b in range(0, B, 37):
+        lens[b] = 0
+    return t, lens
+
+
+MANY = [
+    dict(seed=1, B=400, lo=0, hi=300, rows=[0, 1, 1, 1, 2], nh=4, nk=2, hd=64, page=16),
+    dict(seed=2, B=700, lo=1, hi=90, rows=[0, 1], nh=2, nk=1, hd=128, page=32),
+    dict(seed=3, B=230, lo=100, hi=600, rows=[1, 3], nh=8, nk=2, hd=128, page=64),
+    dict(seed=4, B=120, lo=1, hi=700, rows=[1, 2], nh=4, nk=2, hd=256, page=128),
+    # short sequences and chunks in one call
+    dict(seed=5, B=150, lo=60, hi=300, rows=[0, 1, 1, 7, 40], nh=8, nk=2, hd=64, page=16),
+    dict(seed=6, B=60, lo=100, hi=500, rows=[1, 90, 33], nh=4, nk=1, hd=128, page=256),
+    dict(seed=7, B=40, lo=130, hi=500, rows=[1, 129], nh=2, nk=1, hd=256, page=16),
+]
+
+
+@pytest.mark.parametrize("kw", MANY)
+def test_attend_many_sequences(kw):
+    kw = dict(kw)
+    t, lens = _many(*(kw.pop(x) for x in ("seed", "B", "lo", "hi", "rows")))
+    bt = Batch(t=t, lens=lens, dtype=BF, seed=16, pad=3, **kw)
+    out, lse, err = bt.attend()
+    assert err == 0
+    bt.check(out, lse)
+    # a loose bound of the rows takes the other path and gives the same values
+    out, lse, err = bt.attend(max_rows=1000)
+    assert err == 0
+    bt.check(out, lse)
+
+
 def test_attend_same_bits_and_streams():
     """The same call gives the same bits; on another stream; two at once with their own
     workspaces; captured and replayed with a poisoned workspace."""
@@ -464,6 +502,45 @@ def test_weigh(kw, dtype):
         assert torch.equal(w[b, :, :n].cuda() + z[b, :, :n], out[b, :, :n])
 
 
+@pytest.mark.parametrize("kw", MANY + [
+    # query tiles kept (two of them), and streamed (more)
+    dict(seed=8, B=150, lo=300, hi=1500, rows=[40, 64], nh=8, nk=2, hd=128, page=64),
+    dict(seed=9, B=70, lo=500, hi=1500, rows=[100, 20], nh=8, nk=2, hd=64, page=32),
+    dict(seed=10, B=80, lo=200, hi=900, rows=[100, 3], nh=8, nk=2, hd=256, page=64),
+])
+def test_weigh_many_units(kw):
+    """Several units a CTA, of one half and of two, and back to back calls."""
+    kw = dict(kw)
+    t, lens = _many(*(kw.pop(x) for x in ("seed", "B", "lo", "hi", "rows")))
+    bt = Batch(t=t, lens=lens, dtype=HF, seed=23, pad=1, **kw)
+    err = torch.zeros(1, dtype=torch.int32, device="cuda")
+    lse = torch.zeros(bt.T, bt.nh, device="cuda")
+    # lse as the attention gives it (tested above); the exact weights against it
+    swa.paged_attend(bt.q, *bt.args, bt.scale, max_rows=max(t), lse=lse, err=err)
+    runs = [swa.paged_weigh(bt.q, lse, bt.k, *bt.args[2:], bt.scale, max_rows=max(t), err=err) for _ in range(20)]
+    torch.cuda.synchronize()
+    assert int(err.item()) == 0
+    for r in runs[1:]:
+        assert torch.equal(r, runs[0])
+    k, q, l = bt.k.double(), bt.q.double(), lse.double()
+    hpg, got = bt.nh // bt.nk, runs[0].double()
+    for b in range(len(t)):
+        n, r0, r1 = lens[b], bt.start[b], bt.start[b + 1]
+        idx = torch.arange(n)
+        rows = k[bt.table[b][idx // bt.page].long().cuda(), :, (idx % bt.page).cuda()]       # [n][nk][hd]
+        x = torch.einsum("rghd,ngd->rghn", q[r0:r1].view(r1 - r0, bt.nk, hpg, bt.hd), rows) * bt.scale
+        sabs = torch.einsum("rghd,ngd->rghn", q[r0:r1].abs().view(r1 - r0, bt.nk, hpg, bt.hd), rows.abs()) * bt.scale
+        i = torch.arange(r1 - r0, device="cuda")
+        seen = torch.arange(n, device="cuda")[None, :] < (n - (r1 - r0) + i + 1)[:, None]
+        w = torch.exp(x - l[r0:r1].view(r1 - r0, bt.nk, hpg, 1))
+        w = torch.where(seen[:, None, None, :], w, torch.zeros_like(w)).sum((0, 2))          # [nk][n]
+        d = bt.hd * 2.0 ** -24 * (float(sabs.max()) if sabs.numel() else 0.0)
+        lm = float(l[r0:r1].nan_to_num(neginf=0).abs().max()) if r1 > r0 else 0.0
+        tol = (d + 2.0 ** -19 + 2.0 ** -22 * lm + ((r1 - r0) * hpg + 1) * 2.0 ** -24) * w + 1e-30
+        assert ((got[b, :, :n] - w).abs() <= tol).all(), b
+        assert (got[b, :, n:] == 0).all()
+
+
 # ------------------------------------------------------------------ evict
 EVICT = [
     dict(lens=[1], nk=1, hd=64, page=16, keep=1),
@@ -550,6 +627,57 @@ def test_evict_reports():
 
 
 # ------------------------------------------------------------------ a run of them
+def test_step_captured_and_on_a_stream():
+    """Append, attend, weigh and evict of one decode step, eager, on another stream, and
+    captured into a graph whose workspaces are its own: the same bits."""
+    B, nh, nk, hd, page, lens = 6, 8, 2, 128, 32, [700, 33, 64, 1, 1000, 257]
+    g = torch.Generator().manual_seed(51)
+    turns = swa.rotary_turns(hd)
+    x = torch.randn(B, (nh + 2 * nk), hd, generator=g).to(BF).cuda()
+    q, k, v = x[:, :nh], x[:, nh:nh + nk], x[:, nh + nk:]
+    pos = dev([n - 1 for n in lens])
+
+    def fresh():
+        bt = Batch(t=[1] * B, lens=lens, nh=nh, nk=nk, hd=hd, page=page, seed=52)
+        gg = torch.Generator().manual_seed(53)
+        w = torch.rand(B, nk, bt.cap, generator=gg).cuda()
+        p = torch.arange(bt.cap, dtype=torch.int32).repeat(B, nk, 1).cuda()
+        return bt, w, p, [torch.zeros(B, nh, hd, dtype=BF, device="cuda"), torch.zeros(B, nh, device="cuda"),
+                          torch.zeros(B, nk, bt.cap, device="cuda"), torch.zeros(B, nk, bt.cap, device="cuda"),
+                          torch.zeros(B, nk, bt.cap, dtype=torch.int32, device="cuda"), torch.zeros(B, dtype=torch.int32, device="cuda")]
+
+    def step(bt, w, p, o, stream=None):
+        qr = swa.paged_append(k, v, pos, *bt.args, q=q, turns=turns, slot_pos=p, weight=w, stream=stream)
+        swa.paged_attend(qr, *bt.args, hd ** -0.5, max_rows=1, out=o[0], lse=o[1], stream=stream)
+        swa.paged_weigh(qr, o[1], bt.k, *bt.args[2:], hd ** -0.5, max_rows=1, weight=w, out=o[2], stream=stream)
+        swa.paged_evict(bt.k, bt.v, bt.args[2], bt.args[4], o[2], p, 100, weight_out=o[3], slot_pos_out=o[4], lens_out=o[5],
+                        stream=stream)
+        return [y.clone() for y in o] + [bt.k.nan_to_num(9), bt.v.nan_to_num(9)]
+    a = fresh()
+    want = step(*a)
+    torch.cuda.synchronize()
+    s = torch.cuda.Stream()
+    b = fresh()
+    torch.cuda.synchronize()
+    step(*b, stream=s)
+    torch.cuda.synchronize()
+    for y, z in zip([*b[3], b[0].k.nan_to_num(9), b[0].v.nan_to_num(9)], want):
+        assert torch.equal(y, z)
+    c = fresh()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        step(*c)
+    k0, v0, w0, p0 = c[0].k.clone(), c[0].v.clone(), c[1].clone(), c[2].clone()
+    for _ in range(2):
+        for y, z in ((c[0].k, k0), (c[0].v, v0), (c[1], w0), (c[2], p0)):
+            y.copy_(z)
+        graph.replay()
+        torch.cuda.synchronize()
+        for y, z in zip([*c[3], c[0].k.nan_to_num(9), c[0].v.nan_to_num(9)], want):
+            assert torch.equal(y, z)
+
+
 def test_layer_steps_with_a_budget():
     """A prompt chunk, then decode steps: append, attend, weigh, and an eviction whenever
     the cache passes its budget, against the same steps in float64 on the values the cache
