@@ -110,12 +110,37 @@ __device__ __forceinline__ void store8(T* p, const float (&x)[8]) {
   *reinterpret_cast<uint4*>(p) = make_uint4(pack2(x[0], x[1], p), pack2(x[2], x[3], p), pack2(x[4], x[5], p),
                                             pack2(x[6], x[7], p));
 }
-__device__ __forceinline__ float load1(const float* p) { return *p; }
-__device__ __forceinline__ float load1(const __nv_bfloat16* p) { return __bfloat162float(*p); }
-__device__ __forceinline__ float load1(const __half* p) { return __half2float(*p); }
-__device__ __forceinline__ void store1(float* p, float x) { *p = x; }
-__device__ __forceinline__ void store1(__nv_bfloat16* p, float x) { *p = __float2bfloat16_rn(x); }
-__device__ __forceinline__ void store1(__half* p, float x) { *p = __float2half_rn(x); }
+__device__ __forceinline__ float to_f32(float x) { return x; }
+__device__ __forceinline__ float to_f32(__nv_bfloat16 x) { return __bfloat162float(x); }
+__device__ __forceinline__ float to_f32(__half x) { return __half2float(x); }
+__device__ __forceinline__ void round_to(float& d, float x) { d = x; }
+__device__ __forceinline__ void round_to(__nv_bfloat16& d, float x) { d = __float2bfloat16_rn(x); }
+__device__ __forceinline__ void round_to(__half& d, float x) { d = __float2half_rn(x); }
+
+// N = 1, 2, 4 or 8 elements at a multiple of N, in one access each up to 16 bytes
+template <int N, typename T>
+__device__ __forceinline__ void load_n(const T* p, float (&x)[N]) {
+  if constexpr (N == 8) {
+    load8(p, x);
+  } else {
+    struct alignas(sizeof(T) * N) Vec { T e[N]; };
+    const Vec v = *reinterpret_cast<const Vec*>(p);
+#pragma unroll
+    for (int i = 0; i < N; ++i) x[i] = to_f32(v.e[i]);
+  }
+}
+template <int N, typename T>
+__device__ __forceinline__ void store_n(T* p, const float (&x)[N]) {
+  if constexpr (N == 8) {
+    store8(p, x);
+  } else {
+    struct alignas(sizeof(T) * N) Vec { T e[N]; };
+    Vec v;
+#pragma unroll
+    for (int i = 0; i < N; ++i) round_to(v.e[i], x[i]);
+    *reinterpret_cast<Vec*>(p) = v;
+  }
+}
 
 __device__ __forceinline__ float ex2(float x) {
   float y;

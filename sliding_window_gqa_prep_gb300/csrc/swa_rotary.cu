@@ -14,8 +14,7 @@
 // thread takes units (8 pairs, or 8 features when interleaved: 16-byte accesses for 16-bit
 // types) of the rows' heads in turn. With the angles in registers instead, recomputed for
 // every few heads, a prompt of 6000 f32 rows of 48 heads entered the cache at 3.6 TB/s.
-// Units whose halves do not start at multiples of 8 features take the same kernel with
-// one pair (two features) a unit.
+// Halves that do not start at multiples of 8 features take units of 4, 2 or 1 pairs.
 #include <cmath>
 
 #include "swa_paged.cuh"
@@ -61,7 +60,7 @@ __device__ __forceinline__ int find_seq(const int32_t* row_start, int B, int row
   return lo;
 }
 
-// V: pairs (half layout) or features (interleaved) of a unit
+// V: pairs (half layout: 1, 2, 4 or 8) or features (interleaved: 8) of a unit
 template <typename TI, typename TO, bool INTER, int V, bool APPEND>
 __global__ void __launch_bounds__(kRotThreads) rotary_kernel(const RotaryParams p) {
   __shared__ __align__(16) float s_cos[kRotRows * kRotPairs], s_sin[kRotRows * kRotPairs];
@@ -115,7 +114,7 @@ __global__ void __launch_bounds__(kRotThreads) rotary_kernel(const RotaryParams 
   __syncthreads();
 
   constexpr int NP = INTER ? V / 2 : V;                 // pairs of a unit
-  const int rot_units = INTER ? p.rot / V : half / V;
+  const int rot_units = INTER ? (p.rot + V - 1) / V : half / V;   // interleaved: the last may be turned in part
   const int nh = h1 - h0, items = nr * nh * p.units;
 #pragma unroll 2
   for (int x = tid; x < items; x += kRotThreads) {
@@ -151,62 +150,48 @@ __global__ void __launch_bounds__(kRotThreads) rotary_kernel(const RotaryParams 
     }
     const float* cs = s_cos + r * half + e0;
     const float* sn = s_sin + r * half + e0;
-    if constexpr (V == 8) {
-      float a[8];
-      load8(src + f0, a);
-      if constexpr (INTER) {
-        if (rotate) {
+    float a[V];
+    load_n(src + f0, a);
+    if constexpr (INTER) {
+      if (rotate) {
+        const int np = min(NP, half - e0);
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {
+        for (int i = 0; i < NP; ++i) {
+          if (i < np) {
             const float c = cs[i], s = sn[i], u0 = a[2 * i], v0 = a[2 * i + 1];
             a[2 * i] = u0 * c - v0 * s;
             a[2 * i + 1] = v0 * c + u0 * s;
           }
         }
-        store8(dst + f0, a);
-      } else if (turn) {
-        float b[8];
-        load8(src + half + f0, b);
-        if (rotate) {
-          float c[8], s[8];
-          load8(cs, c);
-          load8(sn, s);
+      }
+    } else if (turn) {
+      float b[V];
+      load_n(src + half + f0, b);
+      if (rotate) {
+        float c[V], s[V];
+        load_n(cs, c);
+        load_n(sn, s);
 #pragma unroll
-          for (int i = 0; i < 8; ++i) {
-            const float u0 = a[i], v0 = b[i];
-            a[i] = u0 * c[i] - v0 * s[i];
-            b[i] = v0 * c[i] + u0 * s[i];
-          }
+        for (int i = 0; i < V; ++i) {
+          const float u0 = a[i], v0 = b[i];
+          a[i] = u0 * c[i] - v0 * s[i];
+          b[i] = v0 * c[i] + u0 * s[i];
         }
-        store8(dst + f0, a);
-        store8(dst + half + f0, b);
-      } else {
-        store8(dst + f0, a);
       }
-    } else {
-      const int f1 = INTER ? f0 + 1 : f0 + half;
-      if (turn) {
-        const float u0 = load1(src + f0), v0 = load1(src + f1);
-        store1(dst + f0, rotate ? u0 * cs[0] - v0 * sn[0] : u0);
-        store1(dst + f1, rotate ? v0 * cs[0] + u0 * sn[0] : v0);
-      } else {
-        store1(dst + f0, load1(src + f0));
-        if constexpr (INTER) store1(dst + f1, load1(src + f1));
-      }
+      store_n(dst + half + f0, b);
     }
+    store_n(dst + f0, a);
   }
 }
 
 // Units of a row (pairs of the rotated part, then the copied part), and the block's rows
 // and heads: all heads of kRotRows rows once that gives every SM four blocks, else one
 // row and as many heads as give each thread a unit.
-static bool rotary_units(RotaryParams& p, bool inter, bool* wide) {
+static bool rotary_units(RotaryParams& p, bool inter, int* v) {
   const int half = p.rot / 2, rest = p.hd - p.rot;
-  *wide = inter ? p.rot % 8 == 0 : half % 8 == 0;      // hd is a multiple of 8, so the rest is too
-  if (inter)
-    p.units = p.hd / (*wide ? 8 : 2);
-  else
-    p.units = *wide ? half / 8 + rest / 8 : half + rest;
+  // the halves start at multiples of v, and then the rest does (hd is a multiple of 8)
+  *v = inter || half % 8 == 0 ? 8 : half % 4 == 0 ? 4 : half % 2 == 0 ? 2 : 1;
+  p.units = inter ? p.hd / 8 : half / *v + rest / *v;
   const long long sms = num_sms() > 0 ? num_sms() : 148;
   p.R = p.T >= 4 * sms * kRotRows ? kRotRows : 1;
   p.Hg = p.R > 1 || p.T >= 4 * sms ? p.H : (kRotThreads + p.units - 1) / p.units;
@@ -217,15 +202,19 @@ static bool rotary_units(RotaryParams& p, bool inter, bool* wide) {
 }
 
 template <typename TI, typename TO, bool APPEND>
-static int launch_rotary(const RotaryParams& p, bool inter, bool wide, cudaStream_t s) {
+static int launch_rotary(const RotaryParams& p, bool inter, int v, cudaStream_t s) {
   const dim3 grid((unsigned)((p.T + p.R - 1) / p.R), (unsigned)((p.H + p.Hg - 1) / p.Hg)), block(kRotThreads);
   cudaError_t e;
   if (inter)
-    e = wide ? launch_pdl(rotary_kernel<TI, TO, true, 8, APPEND>, grid, block, 0, s, p)
-             : launch_pdl(rotary_kernel<TI, TO, true, 2, APPEND>, grid, block, 0, s, p);
+    e = launch_pdl(rotary_kernel<TI, TO, true, 8, APPEND>, grid, block, 0, s, p);
+  else if (v == 8)
+    e = launch_pdl(rotary_kernel<TI, TO, false, 8, APPEND>, grid, block, 0, s, p);
+  else if (v == 4)
+    e = launch_pdl(rotary_kernel<TI, TO, false, 4, APPEND>, grid, block, 0, s, p);
+  else if (v == 2)
+    e = launch_pdl(rotary_kernel<TI, TO, false, 2, APPEND>, grid, block, 0, s, p);
   else
-    e = wide ? launch_pdl(rotary_kernel<TI, TO, false, 8, APPEND>, grid, block, 0, s, p)
-             : launch_pdl(rotary_kernel<TI, TO, false, 1, APPEND>, grid, block, 0, s, p);
+    e = launch_pdl(rotary_kernel<TI, TO, false, 1, APPEND>, grid, block, 0, s, p);
   return finish_launch(e);
 }
 
@@ -314,12 +303,12 @@ int swa_rotary(const swa_rotary_args* a, cudaStream_t stream) {
   p.out = a->out; p.out_row = a->out_row; p.out_head = a->out_head;
   p.pos = a->pos; p.turns = a->turns;
   const bool inter = a->interleaved != 0;
-  bool wide;
-  if (!rotary_units(p, inter, &wide)) return SWA_E_SHAPE;
+  int v;
+  if (!rotary_units(p, inter, &v)) return SWA_E_SHAPE;
   switch (a->dtype) {
-    case SWA_F32: return launch_rotary<float, float, false>(p, inter, wide, stream);
-    case SWA_BF16: return launch_rotary<__nv_bfloat16, __nv_bfloat16, false>(p, inter, wide, stream);
-    default: return launch_rotary<__half, __half, false>(p, inter, wide, stream);
+    case SWA_F32: return launch_rotary<float, float, false>(p, inter, v, stream);
+    case SWA_BF16: return launch_rotary<__nv_bfloat16, __nv_bfloat16, false>(p, inter, v, stream);
+    default: return launch_rotary<__half, __half, false>(p, inter, v, stream);
   }
 }
 
@@ -365,13 +354,13 @@ int swa_paged_append(const swa_paged_append_args* a, cudaStream_t stream) {
   p.map = paged_map(&c);
   p.slot_pos = a->slot_pos; p.weight = a->weight; p.err = a->err;
   const bool inter = a->interleaved != 0;
-  bool wide;
-  if (!rotary_units(p, inter, &wide)) return SWA_E_SHAPE;
+  int v;
+  if (!rotary_units(p, inter, &v)) return SWA_E_SHAPE;
   if (a->src == SWA_F32)
-    return c.dtype == SWA_BF16 ? launch_rotary<float, __nv_bfloat16, true>(p, inter, wide, stream)
-                               : launch_rotary<float, __half, true>(p, inter, wide, stream);
-  return c.dtype == SWA_BF16 ? launch_rotary<__nv_bfloat16, __nv_bfloat16, true>(p, inter, wide, stream)
-                             : launch_rotary<__half, __half, true>(p, inter, wide, stream);
+    return c.dtype == SWA_BF16 ? launch_rotary<float, __nv_bfloat16, true>(p, inter, v, stream)
+                               : launch_rotary<float, __half, true>(p, inter, v, stream);
+  return c.dtype == SWA_BF16 ? launch_rotary<__nv_bfloat16, __nv_bfloat16, true>(p, inter, v, stream)
+                             : launch_rotary<__half, __half, true>(p, inter, v, stream);
 }
 
 }  // extern "C"
