@@ -117,29 +117,25 @@ __device__ __forceinline__ void round_to(float& d, float x) { d = x; }
 __device__ __forceinline__ void round_to(__nv_bfloat16& d, float x) { d = __float2bfloat16_rn(x); }
 __device__ __forceinline__ void round_to(__half& d, float x) { d = __float2half_rn(x); }
 
-// N = 1, 2, 4 or 8 elements at a multiple of N, in one access each up to 16 bytes
+// N = 1, 2, 4 or 8 elements at a multiple of N, as they lie in memory (accesses of up to
+// 16 bytes) and as f32
+template <typename T, int N>
+struct alignas(sizeof(T) * N < 16 ? sizeof(T) * N : 16) Pack {
+  T e[N];
+};
 template <int N, typename T>
-__device__ __forceinline__ void load_n(const T* p, float (&x)[N]) {
-  if constexpr (N == 8) {
-    load8(p, x);
-  } else {
-    struct alignas(sizeof(T) * N) Vec { T e[N]; };
-    const Vec v = *reinterpret_cast<const Vec*>(p);
+__device__ __forceinline__ Pack<T, N> load_pack(const T* p) { return *reinterpret_cast<const Pack<T, N>*>(p); }
+template <int N, typename T>
+__device__ __forceinline__ void unpack(const Pack<T, N>& v, float (&x)[N]) {
 #pragma unroll
-    for (int i = 0; i < N; ++i) x[i] = to_f32(v.e[i]);
-  }
+  for (int i = 0; i < N; ++i) x[i] = to_f32(v.e[i]);
 }
 template <int N, typename T>
-__device__ __forceinline__ void store_n(T* p, const float (&x)[N]) {
-  if constexpr (N == 8) {
-    store8(p, x);
-  } else {
-    struct alignas(sizeof(T) * N) Vec { T e[N]; };
-    Vec v;
+__device__ __forceinline__ void store_pack(T* p, const float (&x)[N]) {
+  Pack<T, N> v;
 #pragma unroll
-    for (int i = 0; i < N; ++i) round_to(v.e[i], x[i]);
-    *reinterpret_cast<Vec*>(p) = v;
-  }
+  for (int i = 0; i < N; ++i) round_to(v.e[i], x[i]);
+  *reinterpret_cast<Pack<T, N>*>(p) = v;
 }
 
 __device__ __forceinline__ float ex2(float x) {

@@ -23,6 +23,7 @@ namespace swa {
 
 struct RotaryParams {
   int T, H, hd, rot, R, Hg, units, inverse;   // R rows and Hg heads a block
+  uint64_t units_inv, heads_inv;              // ceil(2^32 / d) of units and Hg: x / d = x * inv >> 32, x < 2^20, d <= 2^11
   float mag;
   const void* x;               // rows of heads [0, H) (swa_rotary) or of q (append)
   long long x_row, x_head;
@@ -69,8 +70,54 @@ __global__ void __launch_bounds__(kRotThreads) rotary_kernel(const RotaryParams 
   const int tid = threadIdx.x;
   const int row0 = blockIdx.x * p.R, nr = min(p.R, p.T - row0), h0 = blockIdx.y * p.Hg, h1 = min(h0 + p.Hg, p.H);
   const int half = p.rot >> 1;
+  constexpr int NP = INTER ? V / 2 : V;                 // pairs of a unit
+  const int rot_units = INTER ? (p.rot + V - 1) / V : half / V;   // interleaved: the last may be turned in part
+  const int nh = h1 - h0, items = nr * nh * p.units;
+  // Unit x of the block: row, head and first feature
+  struct Unit {
+    int u, h, r, f0;
+    bool turn;
+  };
+  auto unit = [&](int x) {
+    Unit q;
+    const int y = (int)((uint64_t)(unsigned)x * p.units_inv >> 32);
+    q.u = x - y * p.units;
+    q.r = (int)((uint64_t)(unsigned)y * p.heads_inv >> 32);
+    if (nh != p.Hg) q.r = y / nh;                       // the last group of heads
+    q.h = h0 + y - q.r * nh;
+    q.turn = q.u < rot_units;
+    q.f0 = INTER ? q.u * V : q.turn ? q.u * NP : p.rot + (q.u - rot_units) * V;
+    return q;
+  };
+  // U units of a thread at a time. Those of the next step are loaded before this step's are
+  // stored, and the first ones before the angles: out may be x, so the compiler keeps every
+  // load behind the stores before it.
+  constexpr int U = sizeof(TI) == 4 ? 1 : 2, STEP = U * kRotThreads;
+  struct Loaded {
+    Pack<TI, V> a[U], b[U];
+  };
+  auto load = [&](int x0, Loaded& l) {
+#pragma unroll
+    for (int k = 0; k < U; ++k) {
+      const int x = x0 + k * kRotThreads;
+      if (x >= items) continue;
+      const Unit q = unit(x);
+      const long long row = row0 + q.r;
+      const TI* src;
+      if (!APPEND || q.h < p.nh)
+        src = static_cast<const TI*>(p.x) + row * p.x_row + (long long)q.h * p.x_head;
+      else if (q.h < p.nh + p.nk)
+        src = static_cast<const TI*>(p.k) + row * p.k_row + (long long)(q.h - p.nh) * p.hd;
+      else
+        src = static_cast<const TI*>(p.v) + row * p.v_row + (long long)(q.h - p.nh - p.nk) * p.hd;
+      l.a[k] = load_pack<V>(src + q.f0);
+      if (!INTER && q.turn) l.b[k] = load_pack<V>(src + half + q.f0);
+    }
+  };
   pdl_wait();
   pdl_trigger();
+  Loaded cur;
+  load(tid, cur);
 
   for (int i = tid; i < nr * half; i += kRotThreads) {
     const int r = i / half, e = i % half;
@@ -113,74 +160,71 @@ __global__ void __launch_bounds__(kRotThreads) rotary_kernel(const RotaryParams 
   }
   __syncthreads();
 
-  constexpr int NP = INTER ? V / 2 : V;                 // pairs of a unit
-  const int rot_units = INTER ? (p.rot + V - 1) / V : half / V;   // interleaved: the last may be turned in part
-  const int nh = h1 - h0, items = nr * nh * p.units;
-#pragma unroll 2
-  for (int x = tid; x < items; x += kRotThreads) {
-    const int u = x % p.units, y = x / p.units, h = h0 + y % nh, r = y / nh;
-    const long long row = row0 + r;
-    const bool turn = u < rot_units;
-    const int e0 = u * NP;                              // first pair
-    const int f0 = INTER ? u * V : turn ? e0 : p.rot + (u - rot_units) * V;   // first feature
-    const TI* src;
-    TO* dst;
-    bool rotate = turn;
-    if constexpr (APPEND) {
-      if (!s_live[r]) continue;
-      if (h < p.nh) {
-        src = static_cast<const TI*>(p.x) + row * p.x_row + (long long)h * p.hd;
-        dst = static_cast<TO*>(p.out) + row * p.out_row + (long long)h * p.hd;
-      } else {
-        const bool is_k = h < p.nh + p.nk;
-        const int g = h - p.nh - (is_k ? 0 : p.nk);
-        if (s_slot[r] < 0) continue;
-        src = (is_k ? static_cast<const TI*>(p.k) + row * p.k_row : static_cast<const TI*>(p.v) + row * p.v_row) +
-              (long long)g * p.hd;
-        dst = static_cast<TO*>(is_k ? p.cache_k : p.cache_v) + s_slot[r] + (long long)g * p.hd_page;
-        rotate = turn && is_k;
-        if (is_k && u == 0) {
-          if (p.slot_pos) p.slot_pos[s_aux[r] + (long long)g * p.map.cap] = p.pos[row];
-          if (p.weight) p.weight[s_aux[r] + (long long)g * p.map.cap] = 0.f;
-        }
-      }
-    } else {
-      src = static_cast<const TI*>(p.x) + row * p.x_row + (long long)h * p.x_head;
-      dst = static_cast<TO*>(p.out) + row * p.out_row + (long long)h * p.out_head;
-    }
-    const float* cs = s_cos + r * half + e0;
-    const float* sn = s_sin + r * half + e0;
-    float a[V];
-    load_n(src + f0, a);
-    if constexpr (INTER) {
-      if (rotate) {
-        const int np = min(NP, half - e0);
+  for (int x0 = tid; x0 < items; x0 += STEP) {
+    Loaded next;
+    load(x0 + STEP, next);
 #pragma unroll
-        for (int i = 0; i < NP; ++i) {
-          if (i < np) {
-            const float c = cs[i], s = sn[i], u0 = a[2 * i], v0 = a[2 * i + 1];
-            a[2 * i] = u0 * c - v0 * s;
-            a[2 * i + 1] = v0 * c + u0 * s;
+    for (int k = 0; k < U; ++k) {
+      const int x = x0 + k * kRotThreads;
+      if (x >= items) continue;
+      const Unit q = unit(x);
+      const long long row = row0 + q.r;
+      TO* dst;
+      bool rotate = q.turn;
+      if constexpr (APPEND) {
+        if (!s_live[q.r]) continue;
+        if (q.h < p.nh) {
+          dst = static_cast<TO*>(p.out) + row * p.out_row + (long long)q.h * p.hd;
+        } else {
+          const bool is_k = q.h < p.nh + p.nk;
+          const int g = q.h - p.nh - (is_k ? 0 : p.nk);
+          if (s_slot[q.r] < 0) continue;
+          dst = static_cast<TO*>(is_k ? p.cache_k : p.cache_v) + s_slot[q.r] + (long long)g * p.hd_page;
+          rotate = q.turn && is_k;
+          if (is_k && q.u == 0) {
+            if (p.slot_pos) p.slot_pos[s_aux[q.r] + (long long)g * p.map.cap] = p.pos[row];
+            if (p.weight) p.weight[s_aux[q.r] + (long long)g * p.map.cap] = 0.f;
           }
         }
+      } else {
+        dst = static_cast<TO*>(p.out) + row * p.out_row + (long long)q.h * p.out_head;
       }
-    } else if (turn) {
-      float b[V];
-      load_n(src + half + f0, b);
-      if (rotate) {
-        float c[V], s[V];
-        load_n(cs, c);
-        load_n(sn, s);
+      const int e0 = q.u * NP;                          // first pair
+      const float* cs = s_cos + q.r * half + e0;
+      const float* sn = s_sin + q.r * half + e0;
+      float a[V];
+      unpack(cur.a[k], a);
+      if constexpr (INTER) {
+        if (rotate) {
+          const int np = min(NP, half - e0);
 #pragma unroll
-        for (int i = 0; i < V; ++i) {
-          const float u0 = a[i], v0 = b[i];
-          a[i] = u0 * c[i] - v0 * s[i];
-          b[i] = v0 * c[i] + u0 * s[i];
+          for (int i = 0; i < NP; ++i) {
+            if (i < np) {
+              const float c = cs[i], s = sn[i], u0 = a[2 * i], v0 = a[2 * i + 1];
+              a[2 * i] = u0 * c - v0 * s;
+              a[2 * i + 1] = v0 * c + u0 * s;
+            }
+          }
         }
+      } else if (q.turn) {
+        float b[V];
+        unpack(cur.b[k], b);
+        if (rotate) {
+          float c[V], s[V];
+          unpack(load_pack<V>(cs), c);
+          unpack(load_pack<V>(sn), s);
+#pragma unroll
+          for (int i = 0; i < V; ++i) {
+            const float u0 = a[i], v0 = b[i];
+            a[i] = u0 * c[i] - v0 * s[i];
+            b[i] = v0 * c[i] + u0 * s[i];
+          }
+        }
+        store_pack(dst + half + q.f0, b);
       }
-      store_n(dst + half + f0, b);
+      store_pack(dst + q.f0, a);
     }
-    store_n(dst + f0, a);
+    cur = next;
   }
 }
 
@@ -196,8 +240,10 @@ static bool rotary_units(RotaryParams& p, bool inter, int* v) {
   p.R = p.T >= 4 * sms * kRotRows ? kRotRows : 1;
   p.Hg = p.R > 1 || p.T >= 4 * sms ? p.H : (kRotThreads + p.units - 1) / p.units;
   if (p.Hg > p.H) p.Hg = p.H;
-  const long long most = (1 << 20) / p.units;           // items of a block stay well below 2^31
+  const long long most = (1 << 18) / p.units < 2048 ? (1 << 18) / p.units : 2048;   // items of a block: 2^20 at most
   if (p.Hg > most) p.Hg = (int)most;
+  p.units_inv = ((1ull << 32) + p.units - 1) / p.units;
+  p.heads_inv = ((1ull << 32) + p.Hg - 1) / p.Hg;
   return (p.H + p.Hg - 1) / p.Hg <= 65535;
 }
 
@@ -345,7 +391,7 @@ int swa_paged_append(const swa_paged_append_args* a, cudaStream_t stream) {
   }
   RotaryParams p{};
   p.T = a->T; p.H = (int)H; p.hd = c.hd; p.rot = a->rot; p.mag = a->mag;
-  p.x = a->q; p.x_row = a->q_row;
+  p.x = a->q; p.x_row = a->q_row; p.x_head = c.hd;
   p.out = a->q_out; p.out_row = qd;
   p.pos = a->pos; p.turns = a->turns;
   p.nh = nh; p.nk = c.nk; p.hd_page = c.page * c.hd;

@@ -128,7 +128,8 @@ class Batch:
 ROTARY = [
     dict(T=1, H=1, hd=8, rot=8), dict(T=7, H=3, hd=64, rot=64), dict(T=5, H=40, hd=128, rot=64),
     dict(T=3, H=2, hd=64, rot=20), dict(T=2, H=5, hd=256, rot=2), dict(T=301, H=9, hd=128, rot=128),
-    dict(T=4000, H=6, hd=64, rot=48), dict(T=2, H=2, hd=1024, rot=1000),
+    dict(T=4000, H=6, hd=64, rot=48), dict(T=2, H=2, hd=1024, rot=1000), dict(T=2, H=2500, hd=8, rot=6),
+    dict(T=700, H=5, hd=32, rot=28), dict(T=33, H=3, hd=256, rot=136),
 ]
 
 
