@@ -648,7 +648,7 @@ int swa_paged_append(const swa_paged_append_args* args, cudaStream_t stream);
  *        that overlap on the GPU
  *   ev_start, ev_stop  optional, recorded around the attention kernels
  * The result does not depend on timing: the same call gives the same bits.
- * Errors: SWA_E_NULL, SWA_E_SHAPE (also T * nh >= 2^31), SWA_E_ALIGN,
+ * Errors: SWA_E_NULL, SWA_E_SHAPE (also T * nh >= 2^31 - 256), SWA_E_ALIGN,
  * SWA_E_WORKSPACE, SWA_E_CUDA. T = 0: nothing is launched.
  */
 typedef struct swa_paged_attend_args {
@@ -681,7 +681,8 @@ int swa_paged_attend(const swa_paged_attend_args* args, cudaStream_t stream);
  *   weight [B][nk][cap] f32 or NULL (zeros); out [B][nk][cap] f32, may be
  *         weight itself, else must not overlap it
  * The sums run in f32 in a fixed order. cache.v is not read.
- * Errors: SWA_E_NULL, SWA_E_SHAPE, SWA_E_ALIGN, SWA_E_CUDA.
+ * Errors: SWA_E_NULL, SWA_E_SHAPE (also T * nh >= 2^31 - 256), SWA_E_ALIGN,
+ * SWA_E_CUDA.
  */
 typedef struct swa_paged_weigh_args {
   swa_paged_cache cache;

@@ -48,7 +48,7 @@ struct ChunkPlan {
   long long items;             // upper bound of its items (grid)
   size_t off_ml, off_desc, bytes;
 };
-ChunkPlan chunk_plan(const swa_paged_attend_args* a);
+ChunkPlan chunk_plan(const swa_paged_attend_args* a, int max_rows);
 int launch_paged_chunk(const swa_paged_attend_args* a, const PagedAttendParams& p, const ChunkPlan& plan, int small,
                        char* ws, cudaStream_t s);
 

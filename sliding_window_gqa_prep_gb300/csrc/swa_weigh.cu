@@ -15,6 +15,11 @@
 // that a query tile serves 256 keys and nothing is exchanged. A sequence of at most two
 // query tiles keeps them in shared memory for all its keys, else they are streamed per
 // unit. The sums run in a fixed order: no atomics.
+// Measured: one token of 64 sequences of 2048 to 4160 keys, 16 query heads on 4, hd 128: 37 us,
+// 5.5 TB/s of K and weights. The last 32 to 64 rows of four prompts of 16384 to 32768 keys, 32
+// heads on 8: 51 us (3.7 TB/s, 650 TFLOP/s), bound by the roles' latencies: a product costs
+// its issuing warp about 1500 clk with its waits and commits, and 128 columns of sums a
+// warpgroup 1650. Tried: four warpgroups of sums (54 us), K called into L2 ahead (54 us).
 #include <cmath>
 
 #include "swa_paged_tc.cuh"
@@ -564,7 +569,7 @@ int swa_paged_weigh(const swa_paged_weigh_args* a, cudaStream_t stream) {
   if (rc != SWA_OK) return rc;
   if (!a->out || (a->T > 0 && (!a->q || !a->lse))) return SWA_E_NULL;
   if (a->T < 0 || a->max_rows < 1 || a->nh < 1 || a->nh % c.nk || a->nh / c.nk > 32) return SWA_E_SHAPE;
-  if ((long long)a->T * a->nh >= (1LL << 31) || (long long)a->max_rows * (a->nh / c.nk) >= (1LL << 31) - 64) return SWA_E_SHAPE;
+  if ((long long)a->T * a->nh >= (1LL << 31) - 256) return SWA_E_SHAPE;   // query vectors and their tiles in 32 bits
   if (!(a->scale >= 0.f) || std::isinf(a->scale)) return SWA_E_SHAPE;
   if (a->T > 0 && (a->q_row < (long long)a->nh * c.hd || a->q_row > (1LL << 40))) return SWA_E_SHAPE;
   if (!aligned16p(a->q) || (a->T > 0 && (a->q_row & 7)) || (reinterpret_cast<uintptr_t>(a->lse) & 3u) ||
@@ -574,7 +579,7 @@ int swa_paged_weigh(const swa_paged_weigh_args* a, cudaStream_t stream) {
   p.map = paged_map(&c);
   const size_t bytes = (size_t)c.B * c.nk * p.map.cap * 4;
   if (a->weight && a->weight != a->out && bytes_overlap(a->weight, bytes, a->out, bytes)) return SWA_E_SHAPE;
-  p.T = a->T; p.nh = a->nh; p.hpg = a->nh / c.nk; p.max_rows = a->max_rows;
+  p.T = a->T; p.nh = a->nh; p.hpg = a->nh / c.nk; p.max_rows = a->max_rows < a->T ? a->max_rows : a->T;
   p.hpg_shift = 31;
   while ((1 << (p.hpg_shift - 31)) < p.hpg) ++p.hpg_shift;
   p.hpg_mul = (uint32_t)(((1ull << p.hpg_shift) + p.hpg - 1) / p.hpg);

@@ -253,7 +253,7 @@ def test_weigh_refusals(lib):
         assert call(_weigh(cache=kw)) == rc, kw
     for kw in (dict(q=None), dict(lse=None), dict(out=None)):
         assert call(_weigh(**kw)) == _abi.SWA_E_NULL, kw
-    for kw in (dict(T=-1), dict(max_rows=0), dict(max_rows=2147483647), dict(nh=5), dict(nh=66), dict(scale=-1.0),
+    for kw in (dict(T=-1), dict(max_rows=0), dict(T=1 << 30), dict(nh=5), dict(nh=66), dict(scale=-1.0),
                dict(scale=float("inf")), dict(q_row=8), dict(out=FAKE + 4)):
         assert call(_weigh(**kw)) == _abi.SWA_E_SHAPE, kw
     for kw in (dict(q=FAKE + 8), dict(q_row=514), dict(lse=FAKE + 2), dict(weight=FAKE + 1), dict(out=BIG + 2)):
