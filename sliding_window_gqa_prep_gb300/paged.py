@@ -78,17 +78,20 @@ def _rows(x, name, dev, dtype, shape) -> Tuple[int, int]:
 def _placed(fn):
     """Runs a call on the device of its first tensor and on `stream`: as it is when that is
     the current device and its current stream, inside both contexts otherwise."""
+    name = fn.__code__.co_varnames[0]
+
     @functools.wraps(fn)
-    def call(first, *args, stream=None, **kw):
+    def call(*args, stream=None, **kw):
+        first = args[0] if args else kw.get(name)
         if not isinstance(first, torch.Tensor) or not first.is_cuda:
-            raise ValueError("expected CUDA tensors")
+            raise ValueError(f"{name} must be a CUDA tensor")
         dev = first.get_device()
         if stream is None and torch._C._cuda_getDevice() == dev:
-            return fn(first, *args, dev=dev, stream=torch._C._cuda_getCurrentRawStream(dev), **kw)
+            return fn(*args, dev=dev, stream=torch._C._cuda_getCurrentRawStream(dev), **kw)
         if stream is not None and stream.device.index != dev:
             raise ValueError(f"stream is on {stream.device}, the tensors are on cuda:{dev}")
         with torch.cuda.device(dev), torch.cuda.stream(stream):
-            return fn(first, *args, dev=dev, stream=torch._C._cuda_getCurrentRawStream(dev), **kw)
+            return fn(*args, dev=dev, stream=torch._C._cuda_getCurrentRawStream(dev), **kw)
     return call
 
 

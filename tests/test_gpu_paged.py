@@ -202,7 +202,17 @@ def test_rotary_strided_and_in_place():
         swa.rotary(got, pos[:3], turns)
     with pytest.raises(ValueError):
         swa.rotary(got, pos.cpu(), turns)
+    with pytest.raises(ValueError):
+        swa.rotary(got, pos, turns, out=got[:, :4])                 # another shape
+    with pytest.raises(ValueError):
+        swa.rotary(got, pos, turns, out=got.float())                # another type
     assert swa.rotary(got[:0], pos[:0], turns).shape == (0, 8, 64)
+    assert torch.equal(swa.rotary(x=qkv[:, :6], pos=pos, turns=turns), want)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    y = swa.rotary(qkv[:, :6], pos, turns, stream=side)
+    side.synchronize()
+    assert torch.equal(y, want)
 
 
 # ------------------------------------------------------------------ append
@@ -450,6 +460,26 @@ def test_attend_far_offsets():
         a = swa.paged_attend(q, ck, cv, dev([[pages - 1, pages - 3, pages - 2]]), start, lens, 0.1, max_rows=t)
         b = swa.paged_attend(q, small_k, small_v, dev([[2, 0, 1]]), start, lens, 0.1, max_rows=t)
         assert torch.equal(a, b) and not a.isnan().any()
+
+
+def test_attend_refusals_of_the_binding():
+    bt = Batch(t=[1, 2], lens=[90, 70], nh=4, nk=2, hd=64, page=16, seed=17)
+    k, v, tab, start, lens = bt.args
+    call = lambda q=bt.q, k=k, v=v, tab=tab, start=start, lens=lens, **kw: swa.paged_attend(
+        q, k, v, tab, start, lens, 0.1, **{"max_rows": 2, **kw})
+    for kw in (dict(q=bt.q.float()), dict(q=bt.q[:, :, :32]), dict(v=v.to(HF)), dict(tab=tab.long()), dict(start=start[:2]),
+               dict(lens=lens.cpu()), dict(k=k.transpose(1, 2)), dict(start=None), dict(out=torch.empty(3, 4, 64, device="cuda").half()),
+               dict(lse=torch.empty(3, 2, device="cuda")), dict(q=bt.q.transpose(0, 1))):
+        with pytest.raises(ValueError):
+            call(**kw)
+    for kw in (dict(max_rows=0), dict(q=torch.zeros(3, 5, 64, dtype=BF, device="cuda")),
+               dict(workspace=torch.empty(512, dtype=torch.uint8, device="cuda")[8:])):
+        with pytest.raises(swa.SwaError):
+            call(**kw)
+    out = call()
+    assert out.shape == (3, 4, 64) and out.dtype == BF
+    assert call(out=torch.zeros(3, 4, 64, device="cuda")).dtype == FP
+    assert swa.paged_attend(bt.q[:0], k, v, tab, dev([0, 0, 0]), lens, 0.1, max_rows=1).shape == (0, 4, 64)
 
 
 # ------------------------------------------------------------------ weigh
