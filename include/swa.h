@@ -574,8 +574,9 @@ int swa_rotary_turns(const swa_rotary_schedule* s, double* freqs, uint64_t* turn
  *   2 <= rot <= hd; strides positive multiples of 16 bytes, heads (hd) and
  *   rows (H heads) not overlapping: x_head >= hd and x_row >= H * x_head, or
  *   x_row >= hd and x_head >= T * x_row. mag finite. T >= 0 (0: no work).
- * Errors: SWA_E_NULL, SWA_E_SHAPE (also T * H * hd >= 2^40), SWA_E_ALIGN,
- * SWA_E_CUDA. One launch.
+ * Errors: SWA_E_NULL, SWA_E_SHAPE (also T * H * hd >= 2^40 and, here and in the
+ * paged calls, rows that span more than 2^44 elements), SWA_E_ALIGN, SWA_E_CUDA.
+ * One launch.
  */
 typedef struct swa_rotary_args {
   int T, H, hd, rot, dtype, interleaved, inverse;
@@ -598,11 +599,13 @@ int swa_rotary(const swa_rotary_args* args, cudaStream_t stream);
  *         elements (heads dense), of type src (SWA_F32, SWA_BF16, SWA_F16;
  *         SWA_F32 or the cache's type); rows at multiples of 16 bytes
  *   q_out [T][nh][hd] dense, of the cache's type (required with q); must not
- *         overlap q unless it is q itself, of the same type and dense
+ *         overlap k, v, or q unless it is q itself, of the same type and dense
  *   pos   [T] i32 (required with rot > 0 or slot_pos)
  *   turns [rot/2] u64 (required with rot > 0); rot 0 or even, <= hd
  *   slot_pos [B][nk][cap] i32, weight [B][nk][cap] f32 (each optional): the
  *         new slots get the row's position and weight 0 (swa_paged_evict)
+ * cache.k and cache.v must not overlap here (a pool that serves as both can be
+ * read by the other calls); the rows must not lie in the pools (not checked).
  * Rows whose slot is below 0 (a chunk longer than lens[b]) set SWA_DERR_META
  * and are not stored (their q is). Slots must not be given twice, and pages
  * that are written must belong to one sequence: this is not checked.
@@ -640,7 +643,7 @@ int swa_paged_append(const swa_paged_append_args* args, cudaStream_t stream);
  *   q    [T][nh][hd] of the cache's type, rows q_row elements apart (heads
  *        dense, rows at multiples of 16 bytes); nh / nk <= 32
  *   out  [T][nh][hd] dense, of the cache's type, or f32 with out_f32 = 1
- *   lse  [T][nh] f32, optional
+ *   lse  [T][nh] f32, optional; q, out and lse must not overlap
  *   scale  finite, >= 0
  *   max_rows  upper bound of t_b: it chooses the kernel and sizes the grid.
  *   workspace  device scratch of swa_paged_attend_workspace_size(args) bytes,
@@ -679,7 +682,9 @@ int swa_paged_attend(const swa_paged_attend_args* args, cudaStream_t stream);
  *         the last rows of a chunk, with a row_start of their own)
  *   lse   [T][nh] f32 of the same rows (swa_paged_attend)
  *   weight [B][nk][cap] f32 or NULL (zeros); out [B][nk][cap] f32, may be
- *         weight itself, else must not overlap it
+ *         weight itself, else must not overlap it, nor q or lse
+ * K must be finite below lens[b]: a slot with an infinity or NaN in K may get any
+ * weight, NaN among them (other slots do not). Behind lens[b] nothing is used.
  * The sums run in f32 in a fixed order. cache.v is not read.
  * Errors: SWA_E_NULL, SWA_E_SHAPE (also T * nh >= 2^31 - 256), SWA_E_ALIGN,
  * SWA_E_CUDA.

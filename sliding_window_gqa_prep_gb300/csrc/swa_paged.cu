@@ -603,7 +603,8 @@ static bool attend_sizes_ok(const swa_paged_attend_args* a) {
   const swa_paged_cache& c = a->cache;
   if (c.B < 1 || c.B > 65535 || c.nk < 1 || c.nk > 65535 || (long long)c.B * c.nk > (1 << 24)) return false;
   if ((c.hd != 64 && c.hd != 128 && c.hd != 256) || (c.dtype != SWA_BF16 && c.dtype != SWA_F16)) return false;
-  if (c.page < 16 || c.page > 256 || c.max_pages < 1 || c.max_pages > (1 << 30) / c.page) return false;
+  if (c.page < 16 || c.page > 256 || (c.page & (c.page - 1))) return false;
+  if (c.max_pages < 1 || c.max_pages > (1 << 30) / c.page) return false;
   if (a->T < 0 || a->max_rows < 1 || a->nh < 1 || a->nh % c.nk || a->nh / c.nk > 32) return false;
   return (long long)a->T * a->nh < (1LL << 31) - 256;
 }
@@ -629,13 +630,18 @@ int swa_paged_attend(const swa_paged_attend_args* a, cudaStream_t stream) {
   if (!attend_sizes_ok(a) || !(a->scale >= 0.f) || std::isinf(a->scale)) return SWA_E_SHAPE;
   if (a->T == 0) return SWA_OK;
   if (!a->q || !a->out) return SWA_E_NULL;
-  if (a->q_row < (long long)a->nh * c.hd || a->q_row > (1LL << 40)) return SWA_E_SHAPE;
+  const long long qn = rows_span(a->T, (long long)a->nh * c.hd, a->q_row);
+  if (qn < 0) return SWA_E_SHAPE;
   if (!aligned16p(a->q) || !aligned16p(a->out) || (a->q_row & 7) || (reinterpret_cast<uintptr_t>(a->lse) & 3u))
     return SWA_E_ALIGN;
   PagedPlan pl;
   attend_plan(a, &pl);
   if (pl.bytes && (!a->workspace || a->workspace_bytes < pl.bytes)) return SWA_E_WORKSPACE;
   if (reinterpret_cast<uintptr_t>(a->workspace) & 255u) return SWA_E_ALIGN;
+  const size_t rows = (size_t)a->T * a->nh, on = rows * c.hd * (a->out_f32 ? 4 : 2), ln = a->lse ? rows * 4 : 0;
+  if (bytes_overlap(a->q, (size_t)qn * 2, a->out, on) ||
+      (a->lse && (bytes_overlap(a->q, (size_t)qn * 2, a->lse, ln) || bytes_overlap(a->out, on, a->lse, ln))))
+    return SWA_E_SHAPE;
   PagedAttendParams p{};
   p.map = paged_map(&c);
   p.T = a->T; p.nh = a->nh; p.hpg = a->nh / c.nk; p.max_rows = a->max_rows < a->T ? a->max_rows : a->T;

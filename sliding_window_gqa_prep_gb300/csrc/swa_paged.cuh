@@ -21,6 +21,12 @@ int paged_cache_status(const swa_paged_cache* c, bool rows);
 PagedMap paged_map(const swa_paged_cache* c);
 // [a, a + an) and [b, b + bn) share a byte
 bool bytes_overlap(const void* a, size_t an, const void* b, size_t bn);
+// Elements that T >= 1 rows of n elements, `row` apart, span; -1 when rows overlap or the
+// span passes 2^44 (no memory holds it, and products of offsets stay in 64 bits)
+inline long long rows_span(long long T, long long n, long long row) {
+  if (n < 1 || row < n || row > (1LL << 40) || row > (1LL << 44) / T) return -1;
+  return (T - 1) * row + n;
+}
 inline bool aligned16p(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 inline size_t up256s(size_t x) { return (x + 255) & ~(size_t)255; }
 

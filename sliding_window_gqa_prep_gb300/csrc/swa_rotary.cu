@@ -320,10 +320,8 @@ int swa_rotary_turns(const swa_rotary_schedule* s, double* freqs, uint64_t* turn
 
 // Extent in elements of T rows of H heads, or -1 when rows and heads overlap.
 static long long extent(long long T, long long H, long long hd, long long row, long long head) {
-  const long long lim = 1LL << 40;
-  if (row < 1 || head < hd || row < hd || row > lim || head > lim) return -1;
-  const long long heads = (H - 1) * head + hd, rows = (T - 1) * row + hd;   // < 2^63: H, T < 2^21, 2^31
-  if (!(row >= heads || head >= rows)) return -1;
+  const long long heads = rows_span(H, hd, head), rows = rows_span(T, hd, row);
+  if (heads < 0 || rows < 0 || !(row >= heads || head >= rows)) return -1;
   return (T - 1) * row + heads;
 }
 
@@ -377,10 +375,10 @@ int swa_paged_append(const swa_paged_append_args* a, cudaStream_t stream) {
   if (a->slot_pos && !a->pos) return SWA_E_NULL;
   if (a->q && a->nh < 1) return SWA_E_SHAPE;
   const int w = type_bytes(a->src);
-  const long long kd = (long long)c.nk * c.hd, qd = (long long)nh * c.hd, lim = 1LL << 40;
-  if (a->k_row < kd || a->v_row < kd || a->k_row > lim || a->v_row > lim ||
-      (a->q && (a->q_row < qd || a->q_row > lim)))
-    return SWA_E_SHAPE;
+  const long long kd = (long long)c.nk * c.hd, qd = (long long)nh * c.hd;
+  const long long kn = rows_span(a->T, kd, a->k_row), vn = rows_span(a->T, kd, a->v_row);
+  const long long qn = a->q ? rows_span(a->T, qd, a->q_row) : 0;
+  if (kn < 0 || vn < 0 || qn < 0) return SWA_E_SHAPE;
   if (!aligned16p(a->k) || !aligned16p(a->v) || !aligned16p(a->q) || !aligned16p(a->q_out) ||
       ((a->k_row | a->v_row | (a->q ? a->q_row : 0)) * w & 15) || (reinterpret_cast<uintptr_t>(a->pos) & 3u) ||
       (reinterpret_cast<uintptr_t>(a->turns) & 7u) || (reinterpret_cast<uintptr_t>(a->slot_pos) & 3u) ||
@@ -388,9 +386,13 @@ int swa_paged_append(const swa_paged_append_args* a, cudaStream_t stream) {
     return SWA_E_ALIGN;
   if (a->q) {
     const bool same = a->q == a->q_out && a->src == c.dtype && a->q_row == qd;
-    if (!same && bytes_overlap(a->q, (size_t)((a->T - 1) * a->q_row + qd) * w, a->q_out, (size_t)a->T * qd * 2))
+    const size_t on = (size_t)a->T * qd * 2;
+    if ((!same && bytes_overlap(a->q, (size_t)qn * w, a->q_out, on)) ||
+        bytes_overlap(a->k, (size_t)kn * w, a->q_out, on) || bytes_overlap(a->v, (size_t)vn * w, a->q_out, on))
       return SWA_E_SHAPE;
   }
+  const size_t pool = (size_t)c.num_pages * c.nk * c.page * c.hd * 2;
+  if (bytes_overlap(c.k, pool, c.v, pool)) return SWA_E_SHAPE;
   RotaryParams p{};
   p.T = a->T; p.H = (int)H; p.hd = c.hd; p.rot = a->rot; p.mag = a->mag;
   p.x = a->q; p.x_row = a->q_row; p.x_head = c.hd;

@@ -571,7 +571,8 @@ int swa_paged_weigh(const swa_paged_weigh_args* a, cudaStream_t stream) {
   if (a->T < 0 || a->max_rows < 1 || a->nh < 1 || a->nh % c.nk || a->nh / c.nk > 32) return SWA_E_SHAPE;
   if ((long long)a->T * a->nh >= (1LL << 31) - 256) return SWA_E_SHAPE;   // query vectors and their tiles in 32 bits
   if (!(a->scale >= 0.f) || std::isinf(a->scale)) return SWA_E_SHAPE;
-  if (a->T > 0 && (a->q_row < (long long)a->nh * c.hd || a->q_row > (1LL << 40))) return SWA_E_SHAPE;
+  const long long qn = a->T > 0 ? rows_span(a->T, (long long)a->nh * c.hd, a->q_row) : 0;
+  if (qn < 0) return SWA_E_SHAPE;
   if (!aligned16p(a->q) || (a->T > 0 && (a->q_row & 7)) || (reinterpret_cast<uintptr_t>(a->lse) & 3u) ||
       (reinterpret_cast<uintptr_t>(a->weight) & 3u) || (reinterpret_cast<uintptr_t>(a->out) & 3u))
     return SWA_E_ALIGN;
@@ -579,6 +580,9 @@ int swa_paged_weigh(const swa_paged_weigh_args* a, cudaStream_t stream) {
   p.map = paged_map(&c);
   const size_t bytes = (size_t)c.B * c.nk * p.map.cap * 4;
   if (a->weight && a->weight != a->out && bytes_overlap(a->weight, bytes, a->out, bytes)) return SWA_E_SHAPE;
+  if (a->T > 0 && (bytes_overlap(a->q, (size_t)qn * 2, a->out, bytes) ||
+                   bytes_overlap(a->lse, (size_t)a->T * a->nh * 4, a->out, bytes)))
+    return SWA_E_SHAPE;
   p.T = a->T; p.nh = a->nh; p.hpg = a->nh / c.nk; p.max_rows = a->max_rows < a->T ? a->max_rows : a->T;
   p.hpg_shift = 31;
   while ((1 << (p.hpg_shift - 31)) < p.hpg) ++p.hpg_shift;

@@ -709,6 +709,42 @@ def test_step_captured_and_on_a_stream():
             assert torch.equal(y, z)
 
 
+@pytest.mark.parametrize("kw", [dict(t=[1, 1, 1], lens=[1500, 1400, 700]), dict(t=[90, 33, 1], lens=[1500, 1400, 700])])
+def test_graphs_at_once_over_shared_pages(kw):
+    """Sequences that read the same pages (a prefix they share), and two captured graphs over
+    them replayed on two streams together: the bits of the calls alone."""
+    bt = Batch(nh=8, nk=2, hd=128, page=64, seed=54, **kw)
+    table = bt.table.clone()
+    table[1, :10] = table[0, :10]
+    table[2, :10] = table[0, :10]
+    bt.table, bt.args = table, (bt.k, bt.v, table.cuda(), *bt.args[3:])
+    out, lse, err = bt.attend()
+    assert err == 0
+    bt.check(out, lse)
+    rows = max(bt.t)
+    want = out, lse, swa.paged_weigh(bt.q, lse, bt.k, *bt.args[2:], bt.scale, max_rows=rows)
+    graphs, got = [], []
+    for _ in range(2):
+        o, l = torch.zeros_like(out), torch.zeros_like(lse)
+        w = torch.zeros_like(want[2])
+        torch.cuda.synchronize()
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            swa.paged_attend(bt.q, *bt.args, bt.scale, max_rows=rows, out=o, lse=l)
+            swa.paged_weigh(bt.q, l, bt.k, *bt.args[2:], bt.scale, max_rows=rows, out=w)
+        graphs.append(g)
+        got.append((o, l, w))
+    streams = [torch.cuda.Stream() for _ in graphs]
+    torch.cuda.synchronize()
+    for _ in range(10):
+        for s, g in zip(streams, graphs):
+            with torch.cuda.stream(s):
+                g.replay()
+    torch.cuda.synchronize()
+    for o, l, w in got:
+        assert torch.equal(o, want[0]) and torch.equal(l, want[1]) and torch.equal(w, want[2])
+
+
 def test_layer_steps_with_a_budget():
     """A prompt chunk, then decode steps: append, attend, weigh, and an eviction whenever
     the cache passes its budget, against the same steps in float64 on the values the cache

@@ -172,6 +172,10 @@ def test_rotary_refusals(lib):
                dict(pos=FAKE + 2), dict(turns=FAKE + 4)):
         assert call(_rotary(**kw)) == _abi.SWA_E_ALIGN, kw
     assert call(_rotary(T=0, x=None)) == _abi.SWA_OK                    # nothing to do
+    # strides whose offsets would pass 64 bits
+    for kw in (dict(T=1 << 30, H=1, x_row=1 << 39, out_row=1 << 39), dict(H=1 << 20, x_head=1 << 39, out_head=1 << 39),
+               dict(T=1, H=1, x_row=(1 << 40) + 8), dict(T=1 << 20, H=1, hd=8, rot=8, out_row=1 << 25)):
+        assert call(_rotary(**kw)) == _abi.SWA_E_SHAPE, kw
 
 
 def _append(cache=None, **kw):
@@ -203,6 +207,12 @@ def test_append_refusals(lib):
                dict(slot_pos=FAKE + 2), dict(weight=FAKE + 3)):
         assert call(_append(**kw)) == _abi.SWA_E_ALIGN, kw
     assert call(_append(T=0)) == _abi.SWA_OK
+    apart = dict(cache=dict(v=BIG << 1))
+    # q_out over k's or v's rows; one pool for both; row offsets that would pass 64 bits
+    for kw in (dict(k=BIG + 1024, **apart), dict(v=BIG - 1024, **apart), dict(), dict(cache=dict(v=FAKE + 65520)),
+               dict(T=1 << 28, nh=1, q_row=1 << 39, **apart), dict(T=1 << 28, nh=1, k_row=1 << 39, **apart),
+               dict(T=1 << 28, nh=1, v_row=1 << 39, **apart)):
+        assert call(_append(**kw)) == _abi.SWA_E_SHAPE, kw
 
 
 def _attend(cache=None, **kw):
@@ -231,6 +241,11 @@ def test_attend_refusals(lib):
     for kw in (dict(workspace=None), dict(workspace_bytes=64)):
         assert call(_attend(cache=dict(max_pages=64), **kw)) == _abi.SWA_E_WORKSPACE, kw
     assert call(_attend(T=0)) == _abi.SWA_OK
+    # q, out and lse may not share a byte: 4 rows of 4 heads of 128 in bf16 are 4096 bytes, of lse 64
+    for kw in (dict(), dict(out=FAKE + 4080), dict(out=BIG, lse=FAKE + 4092), dict(out=BIG, lse=BIG + 4092),
+               dict(out=BIG, lse=BIG + 8188, out_f32=1), dict(out=BIG, T=1 << 28, q_row=1 << 39)):
+        assert call(_attend(**kw)) == _abi.SWA_E_SHAPE, kw
+    assert lib.swa_paged_attend_workspace_size(ctypes.byref(_attend(cache=dict(page=48)))) == 0
     assert lib.swa_paged_attend_workspace_size(None) == 0
     assert lib.swa_paged_attend_workspace_size(ctypes.byref(_attend(nh=5))) == 0
     assert lib.swa_paged_attend_workspace_size(ctypes.byref(_attend())) > 0
@@ -258,6 +273,9 @@ def test_weigh_refusals(lib):
         assert call(_weigh(**kw)) == _abi.SWA_E_SHAPE, kw
     for kw in (dict(q=FAKE + 8), dict(q_row=514), dict(lse=FAKE + 2), dict(weight=FAKE + 1), dict(out=BIG + 2)):
         assert call(_weigh(**kw)) == _abi.SWA_E_ALIGN, kw
+    # out (1024 bytes) over q or lse; row offsets that would pass 64 bits
+    for kw in (dict(out=FAKE), dict(q=BIG + 1008), dict(lse=BIG + 1020), dict(lse=BIG - 60), dict(T=1 << 28, q_row=1 << 39)):
+        assert call(_weigh(**kw)) == _abi.SWA_E_SHAPE, kw
 
 
 def _evict(cache=None, **kw):
