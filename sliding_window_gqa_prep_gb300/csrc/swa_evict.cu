@@ -2,18 +2,22 @@
 //
 // One cluster per (sequence, KV head) does the whole eviction in one launch, each CTA a
 // contiguous share of the slots:
-//   1. keys of its slots into shared memory (an order-preserving 32-bit key);
+//   1. keys of its slots (an order-preserving 32-bit key), 8 slots a thread in registers
+//      (longer shares in shared memory), all loads under way together;
 //   2. the n'-th largest key by histogram passes over its digits; the CTAs' histograms are
 //      summed through distributed shared memory;
-//   3. two walks in slot order (a warp a run of slots, ranks by ballots): the first counts
-//      the freed and the moved slots, the second numbers them, writes the kept slots'
-//      weights and positions and the two lists (slots and rows);
+//   3. each warp counts its run of slots that stay before and behind n'; sums over the warps
+//      and CTAs number the freed and the moved slots, and a walk in slot order writes the
+//      kept slots' weights and positions and the two lists (slots and rows);
 //   4. the rows that move are copied. A source lies at or
 //      behind n', its destination before it: no row is both read and written.
 // Steps 1 to 3 are chains of barriers and short passes, so the CTAs' shares stay small
-// (kSlotsPerCta) while the cluster may grow (8 CTAs at most); copies are bound by memory.
-// Measured: 32 sequences, 8 heads, 64 of 2112 slots: 17 us (keys 4, passes 4, walks 6, copies
-// 3); four of 16384 to 32768 slots down to 4096: 47 us, 19 of them copies at 5.9 TB/s.
+// (kSlotsPerCta) while the cluster may grow (8 CTAs at most) and the passes are kept short in
+// instructions; copies are bound by memory.
+// Measured: 32 sequences, 8 heads, 64 of 2112 slots: 13.5 us (keys 2.6, passes 3, counts and
+// walk 2.8, copies 2.5); four of 16384 to 32768 slots down to 4096: 36.7 us, of them copies
+// 17.5 at 6.6 TB/s, passes 7, counts and walk 5, keys 3. (Keys of a slot at a time, kept in shared
+// memory, and two walks: 17 and 46.7 us.)
 #include <cooperative_groups.h>
 
 #include "swa_paged.cuh"
@@ -34,12 +38,13 @@ struct PagedEvictParams {
   void* ck;
   void* cv;
   int2* ws_dst;                // [B][nk][list_cap]: freed slots and their rows in the pool
-  int2* ws_src;                // [B][nk][list_cap]: moved ones
+  int4* ws_src;                // [B][nk][list_cap]: moved ones: row, weight, position
   uint32_t* err;
 };
 
 constexpr int kEThreads = 512, kEWarps = kEThreads / 32;
-constexpr int kSlotsPerCta = 4096;          // a cluster of (capacity / this), 1 to 8, CTAs
+constexpr int kEN = 8;                      // slots of a thread at a time: 32 kEN in a row a warp
+constexpr int kSlotsPerCta = kEThreads * kEN;   // 4096: a cluster of (capacity / this), 1 to 8, CTAs
 constexpr int kMaxKeySlots = 40960;         // keys of a CTA in shared memory; longer shares are read again
 constexpr int kMaxCluster = 8;
 
@@ -52,30 +57,14 @@ __device__ __forceinline__ uint32_t evict_key(float w, bool safe) {
   return (u & 0x80000000u) ? ~u : u | 0x80000000u;     // +inf: 0xff800000
 }
 
-// Exclusive sums over the block of a per-thread count; s_sums holds a value a warp.
-__device__ __forceinline__ int block_exclusive(int v, int* s_sums) {
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  int incl = v;
-#pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const int x = __shfl_up_sync(0xffffffffu, incl, o);
-    if (lane >= o) incl += x;
-  }
-  __syncthreads();
-  if (lane == 31) s_sums[warp] = incl;
-  __syncthreads();
-  int before = lane < warp && lane < kEWarps ? s_sums[lane] : 0;
-#pragma unroll
-  for (int o = 16; o; o >>= 1) before += __shfl_xor_sync(0xffffffffu, before, o);
-  return before + incl - v;
-}
-
-// CL: a cluster of CTAs a (sequence, KV head), else one CTA
-template <bool CL>
+// CL: a cluster of CTAs a (sequence, KV head), else one CTA. REG: a CTA has kSlotsPerCta
+// slots at most, whose keys stay in its threads' registers.
+template <bool CL, bool REG>
 __global__ void __launch_bounds__(kEThreads, 2) paged_evict_kernel(const PagedEvictParams p) {
-  extern __shared__ uint32_t s_keys[];
+  extern __shared__ uint32_t s_keys[];      // not REG
   __shared__ __align__(16) int hist[CL ? 4 : 3][CL ? 256 : 2048];
-  __shared__ int s_sums[kEWarps], s_eq[kEWarps], s_freed[kEWarps], s_moved[kEWarps];
+  __shared__ int s_sums[kEWarps];
+  __shared__ int4 s_cnt[kEWarps];
   __shared__ int2 s_tot;                    // this CTA's freed and moved slots
   __shared__ uint32_t s_digit;
   __shared__ int s_need;
@@ -119,20 +108,74 @@ __global__ void __launch_bounds__(kEThreads, 2) paged_evict_kernel(const PagedEv
     }
     return;
   }
-  auto make_key = [&](int j) {
-    const int ps = pos[j];
-    return evict_key(w[j], ps < p.sinks || (any_recent && ps >= recent));
+  // warp w takes slots [wlo, whi) of the CTA's
+  const int run = ((hi - lo + kEWarps - 1) / kEWarps + 31) & ~31;
+  const int wlo = min(hi, lo + warp * run), whi = min(hi, wlo + run);
+  // key of slot j; 0, which is no slot's, behind the warp's last one
+  auto make_key = [&](int j, float x, int ps) {
+    return j < whi ? evict_key(x, ps < p.sinks || (any_recent && ps >= recent)) : 0u;
   };
-  const bool cached = share <= p.key_slots;
-  auto key_of = [&](int j) { return cached ? s_keys[j - lo] : make_key(j); };
+  uint32_t key[kEN];
+  float wv[kEN];
+  int pv[kEN], pg[kEN];
+  auto load_slots = [&](int base) {         // all under way together
+#pragma unroll
+    for (int u = 0; u < kEN; ++u) {
+      wv[u] = 0.f;
+      pv[u] = 0;
+      if (base + u * 32 + lane < whi) {
+        wv[u] = (w + base + lane)[u * 32];
+        pv[u] = (pos + base + lane)[u * 32];
+      }
+    }
+  };
+  const int32_t* table = p.map.table + (size_t)b * p.map.max_pages;
+  auto load_pages = [&](int base) {
+#pragma unroll
+    for (int u = 0; u < kEN; ++u) {
+      pg[u] = -1;
+      if (base + u * 32 + lane < whi) pg[u] = table[(base + u * 32 + lane) >> p.map.page_shift];
+    }
+  };
+  const bool cached = !REG && share <= p.key_slots;
+  auto load_keys = [&](int base) {
+    if (!cached) load_slots(base);
+#pragma unroll
+    for (int u = 0; u < kEN; ++u) {
+      const int j = base + u * 32 + lane;
+      key[u] = !cached ? make_key(j, wv[u], pv[u]) : j < whi ? s_keys[j - lo] : 0u;
+    }
+  };
+  // f(slot, key) of the warp's slots in order, 32 at a time
+  auto each = [&](auto f) {
+    for (int base = wlo; base < whi; base += 32 * kEN) {
+      if constexpr (!REG) load_keys(base);
+#pragma unroll
+      for (int u = 0; u < kEN; ++u)
+        if (base + u * 32 < whi) f(base + u * 32 + lane, key[u]);
+      if constexpr (REG) break;
+    }
+  };
   // Digits of the key: 11, 11 and 10 bits in a CTA alone (evict of 64 of 2112 slots: 18.5
   // instead of 20.8 us); four of 8 bits in a cluster, which reads every CTA's bins (30 and 21
   // thousand clk for 8 CTAs)
   const int n_pass = CL ? 4 : 3;
   for (int i = tid; i < (int)(sizeof(hist) / 4); i += kEThreads) (&hist[0][0])[i] = 0;
-  if (cached) {
-#pragma unroll 8
-    for (int j = lo + tid; j < hi; j += kEThreads) s_keys[j - lo] = make_key(j);
+  if constexpr (REG) {
+    load_slots(wlo);
+    // the pages of these slots are looked up at the end: called into the cache now
+    if (lane < kEN) asm volatile("prefetch.global.L1 [%0];" :: "l"(table + (min(wlo + lane * 32, n - 1) >> p.map.page_shift)));
+#pragma unroll
+    for (int u = 0; u < kEN; ++u) key[u] = make_key(wlo + u * 32 + lane, wv[u], pv[u]);
+  } else if (cached) {
+    for (int base = wlo; base < whi; base += 32 * kEN) {
+      load_slots(base);
+#pragma unroll
+      for (int u = 0; u < kEN; ++u) {
+        const int j = base + u * 32 + lane;
+        if (j < whi) s_keys[j - lo] = make_key(j, wv[u], pv[u]);
+      }
+    }
   }
   __syncthreads();
 
@@ -142,15 +185,14 @@ __global__ void __launch_bounds__(kEThreads, 2) paged_evict_kernel(const PagedEv
 #pragma unroll 1
   for (int pass = 0; pass < n_pass; ++pass) {
     const int bits = CL ? 8 : pass < 2 ? 11 : 10, shift = CL ? 24 - 8 * pass : pass == 0 ? 21 : pass == 1 ? 10 : 0;
-    for (int j = lo + tid; j < hi; j += kEThreads) {
-      const uint32_t k = key_of(j);
-      if (pass == 0 || k >> (shift + bits) == prefix) atomicAdd(&hist[pass][(k >> shift) & ((1u << bits) - 1)], 1);
-    }
+    each([&](int, uint32_t k) {
+      if (pass == 0 ? k != 0 : k >> (shift + bits) == prefix) atomicAdd(&hist[pass][(k >> shift) & ((1u << bits) - 1)], 1);
+    });
     sync_all();
     // thread t holds the bins 4t .. 4t + 3 counted from the top, summed over the cluster
-    int c[4] = {0, 0, 0, 0};
-    const int top = (1 << bits) - 4 - 4 * tid;
-    if (top >= 0) {
+    const int threads = 1 << (bits - 2), top = 4 * (threads - 1 - tid);
+    if (tid < threads) {
+      int c[4] = {0, 0, 0, 0};
       int4 v[MC];
 #pragma unroll
       for (int i = 0; i < MC; ++i) {   // all under way together; each CTA starts at its own
@@ -165,15 +207,24 @@ __global__ void __launch_bounds__(kEThreads, 2) paged_evict_kernel(const PagedEv
         c[2] += v[i].y;
         c[3] += v[i].x;
       }
-    }
-    int before = block_exclusive(c[0] + c[1] + c[2] + c[3], s_sums);
+      const int sum = c[0] + c[1] + c[2] + c[3];
+      int before = sum;                     // of the warp's threads up to this one, then of all before it
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      if (before < need && need <= before + c[i]) {
-        s_digit = (uint32_t)(top + 3 - i);
-        s_need = need - before;
+      for (int o = 1; o < 32; o <<= 1) {
+        const int x = __shfl_up_sync(0xffffffffu, before, o);
+        if (lane >= o) before += x;
       }
-      before += c[i];
+      if (lane == 31) s_sums[warp] = before;
+      named_barrier(1, threads);
+      before += __reduce_add_sync(0xffffffffu, lane < warp ? s_sums[lane] : 0) - sum;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        if (before < need && need <= before + c[i]) {
+          s_digit = (uint32_t)(top + 3 - i);
+          s_need = need - before;
+        }
+        before += c[i];
+      }
     }
     __syncthreads();
     prefix = prefix << bits | s_digit;
@@ -187,48 +238,51 @@ __global__ void __launch_bounds__(kEThreads, 2) paged_evict_kernel(const PagedEv
   for (int r = 0; r < MC; ++r)
     if (r < rank) eq_before += *peer(&hist[n_pass - 1][digit], r);
 
-  // walks: warp w takes slots [wlo, whi) in order
-  const int run = ((hi - lo + kEWarps - 1) / kEWarps + 31) & ~31;
-  const int wlo = min(hi, lo + warp * run), whi = min(hi, wlo + run);
-  const unsigned below = (1u << lane) - 1;
-  int cnt = 0;
-  for (int j = wlo + lane; j - lane < whi; j += 32) cnt += __popc(__ballot_sync(0xffffffffu, j < whi && key_of(j) == prefix));
-  if (lane == 0) s_eq[warp] = cnt;
+  // counts of the warp's slots: equal to prefix below and from `keep` on, above it the same
+  int4 cnt = make_int4(0, 0, 0, 0);
+  each([&](int j, uint32_t k) {
+    const bool e = k == prefix, a = k > prefix, low = j < keep;
+    cnt.x += e && low;
+    cnt.y += e && !low;
+    cnt.z += a && low;
+    cnt.w += a && !low;
+  });
+  cnt.x = __reduce_add_sync(0xffffffffu, cnt.x);
+  cnt.y = __reduce_add_sync(0xffffffffu, cnt.y);
+  cnt.z = __reduce_add_sync(0xffffffffu, cnt.z);
+  cnt.w = __reduce_add_sync(0xffffffffu, cnt.w);
+  if (lane == 0) s_cnt[warp] = cnt;
   __syncthreads();
-  int eq = eq_before;
-  for (int i = 0; i < warp; ++i) eq += s_eq[i];
-  const int eq0 = eq;
-  // the slot's fate in the walk; `eq` runs along
-  auto step = [&](int j, bool& freed, bool& moved) {
-    const bool in = j < whi;
-    const uint32_t k = in ? key_of(j) : 0u;
-    const bool is_eq = in && k == prefix;
-    const unsigned m = __ballot_sync(0xffffffffu, is_eq);
-    const bool kept = in && (k > prefix || (is_eq && eq + __popc(m & below) < need));
-    eq += __popc(m);
-    freed = in && j < keep && !kept;
-    moved = kept && j >= keep;
-    return kept;
-  };
-  int n_freed = 0, n_moved = 0;
-  for (int j = wlo + lane; j - lane < whi; j += 32) {
-    bool freed, moved;
-    step(j, freed, moved);
-    n_freed += __popc(__ballot_sync(0xffffffffu, freed));
-    n_moved += __popc(__ballot_sync(0xffffffffu, moved));
-  }
-  if (lane == 0) {
-    s_freed[warp] = n_freed;
-    s_moved[warp] = n_moved;
-  }
-  __syncthreads();
-  n_freed = n_moved = 0;
-  for (int i = 0; i < warp; ++i) {
-    n_freed += s_freed[i];
-    n_moved += s_moved[i];
-  }
-  if (warp == kEWarps - 1 && lane == 0) {
-    s_tot = make_int2(n_freed + s_freed[warp], n_moved + s_moved[warp]);
+  // Each warp finds, lane i for warp i, how many slots are freed and moved: of its equal
+  // slots the first `take` stay, those below `keep` before the others.
+  int eq, n_freed, n_moved;                 // equal, freed and moved slots before this warp's
+  bool any_eq;                              // some of this warp's slots are equal
+  {
+    const int4 c = lane < kEWarps ? s_cnt[lane] : make_int4(0, 0, 0, 0);
+    const int i0 = min(hi, lo + lane * run), i1 = min(hi, i0 + run);
+    int incl = c.x + c.y;
+#pragma unroll
+    for (int o = 1; o < kEWarps; o <<= 1) {
+      const int x = __shfl_up_sync(0xffffffffu, incl, o);
+      if (lane >= o) incl += x;
+    }
+    const int before = eq_before + incl - c.x - c.y;
+    const int take = max(0, min(need - before, c.x + c.y)), take_low = min(take, c.x);
+    const int freed = lane < kEWarps ? max(0, min(i1, keep) - i0) - c.z - take_low : 0, moved = c.w + take - take_low;
+    int f = freed, m = moved;
+#pragma unroll
+    for (int o = 1; o < kEWarps; o <<= 1) {
+      const int x = __shfl_up_sync(0xffffffffu, f, o), y = __shfl_up_sync(0xffffffffu, m, o);
+      if (lane >= o) {
+        f += x;
+        m += y;
+      }
+    }
+    if (tid == kEWarps - 1) s_tot = make_int2(f, m);
+    eq = __shfl_sync(0xffffffffu, before, warp);
+    any_eq = __shfl_sync(0xffffffffu, c.x + c.y, warp) != 0;
+    n_freed = __shfl_sync(0xffffffffu, f - freed, warp);
+    n_moved = __shfl_sync(0xffffffffu, m - moved, warp);
   }
   sync_all();
   int count = 0;                            // rows that move, in the whole cluster
@@ -244,48 +298,57 @@ __global__ void __launch_bounds__(kEThreads, 2) paged_evict_kernel(const PagedEv
     count += tot[r].y;
   }
   int2* const dst = p.ws_dst + (size_t)item * p.list_cap;
-  int2* const src = p.ws_src + (size_t)item * p.list_cap;
-  const int32_t* table = p.map.table + (size_t)b * p.map.max_pages;
+  int4* const src = p.ws_src + (size_t)item * p.list_cap;
   const int mask = (1 << p.map.page_shift) - 1;
-  eq = eq0;
-  for (int j0 = wlo; j0 < whi; j0 += 128) {
-    float wv[4];
-    int pv[4], pg[4];
+  const unsigned below = (1u << lane) - 1;
+  for (int base = wlo; base < whi; base += 32 * kEN) {
+    load_pages(base);
+    load_slots(base);
+    if constexpr (!REG) {
 #pragma unroll
-    for (int u = 0; u < 4; ++u) {           // under way together: the ballots below follow one another
-      const int j = min(j0 + u * 32 + lane, n - 1);
-      wv[u] = w[j];
-      pv[u] = pos[j];
-      pg[u] = table[j >> p.map.page_shift];
+      for (int u = 0; u < kEN; ++u) key[u] = make_key(base + u * 32 + lane, wv[u], pv[u]);
     }
 #pragma unroll
-    for (int u = 0; u < 4; ++u) {
-      const int j = j0 + u * 32 + lane;
-      bool freed, moved;
-      const bool kept = step(j, freed, moved);
-      const unsigned mf = __ballot_sync(0xffffffffu, freed), mm = __ballot_sync(0xffffffffu, moved);
-      if (freed || moved) {
-        int row = -1;                       // of head 0 .. nk - 1 of all pages: below 2^31
-        if (page_ok(p.map, pg[u])) row = ((pg[u] * p.map.nk + g) << p.map.page_shift) + (j & mask);
-        else set_err(p.err, SWA_DERR_PAGE);
-        if (freed) dst[n_freed + __popc(mf & below)] = make_int2(j, row);
-        else src[n_moved + __popc(mm & below)] = make_int2(j, row);
+    for (int u = 0; u < kEN; ++u) {
+      const int j0 = base + u * 32, j = j0 + lane;
+      if (j0 >= whi) continue;
+      bool kept = key[u] > prefix;
+      if (any_eq) {
+        const bool is_eq = key[u] == prefix;
+        const unsigned m = __ballot_sync(0xffffffffu, is_eq);
+        kept |= is_eq && eq + __popc(m & below) < need;
+        eq += __popc(m);
       }
-      n_freed += __popc(mf);
-      n_moved += __popc(mm);
-      if (kept && j < keep) {
-        wo[j] = wv[u];
-        po[j] = pv[u];
+      const bool ok = page_ok(p.map, pg[u]);
+      const int row = ok ? ((pg[u] * p.map.nk + g) << p.map.page_shift) + (j & mask) : -1;   // below 2^31
+      if (!ok && j < whi && kept == (j >= keep)) set_err(p.err, SWA_DERR_PAGE);   // a freed or a moved slot's
+      if (j0 < keep) {
+        const bool freed = j < min(whi, keep) && !kept;
+        const unsigned m = __ballot_sync(0xffffffffu, freed);
+        if (freed) dst[n_freed + __popc(m & below)] = make_int2(j, row);
+        n_freed += __popc(m);
+        if (kept && j < keep) {
+          (wo + base + lane)[u * 32] = wv[u];
+          (po + base + lane)[u * 32] = pv[u];
+        }
+      }
+      if (j0 + 31 >= keep) {
+        const bool moved = kept && j >= keep;
+        const unsigned m = __ballot_sync(0xffffffffu, moved);
+        if (moved) src[n_moved + __popc(m & below)] = make_int4(row, __float_as_int(wv[u]), pv[u], 0);
+        n_moved += __popc(m);
       }
     }
+    if constexpr (REG) break;
   }
   sync_all();                           // the lists are complete (and no histogram is read any more)
 
   // weights and positions of the moved slots
   for (int i = rank * kEThreads + tid; i < count; i += CS * kEThreads) {
-    const int to = dst[i].x, of = src[i].x;
-    wo[to] = w[of];
-    po[to] = pos[of];
+    const int to = dst[i].x;
+    const int4 x = src[i];
+    wo[to] = __int_as_float(x.y);
+    po[to] = x.z;
   }
   // rows: ch = 8, 16 or 32 lanes a row of K (job 2 i) or V (2 i + 1), kRows of them under way
   constexpr int kRows = 8;
@@ -297,7 +360,7 @@ __global__ void __launch_bounds__(kEThreads, 2) paged_evict_kernel(const PagedEv
     for (int k = 0; k < kRows; ++k) {
       const int job = min(q + k * stride, jobs - 1);
       to[k] = dst[job >> 1].y;
-      of[k] = src[job >> 1].y;
+      of[k] = src[job >> 1].x;
     }
 #pragma unroll
     for (int k = 0; k < kRows; ++k) {
@@ -331,7 +394,7 @@ extern "C" {
 size_t swa_paged_evict_workspace_size(const swa_paged_evict_args* a) {
   if (!a || !evict_sizes_ok(a)) return 0;
   const size_t items = (size_t)a->cache.B * a->cache.nk;
-  return 2 * up256s(items * evict_list_cap(a) * sizeof(int2));
+  return up256s(items * evict_list_cap(a) * sizeof(int2)) + up256s(items * evict_list_cap(a) * sizeof(int4));
 }
 
 int swa_paged_evict(const swa_paged_evict_args* a, cudaStream_t stream) {
@@ -365,19 +428,20 @@ int swa_paged_evict(const swa_paged_evict_args* a, cudaStream_t stream) {
   p.ck = c.k; p.cv = c.v;
   char* ws = static_cast<char*>(a->workspace);
   p.ws_dst = reinterpret_cast<int2*>(ws);
-  p.ws_src = reinterpret_cast<int2*>(ws + need / 2);
+  p.ws_src = reinterpret_cast<int4*>(ws + up256s(items * p.list_cap * sizeof(int2)));
   p.err = a->err;
   // a CTA for every kSlotsPerCta slots of the capacity, 1, 2, 4 or 8 of them a cluster
   int cs = 1;
   while (cs < kMaxCluster && (long long)cs * kSlotsPerCta < p.map.cap) cs *= 2;
-  const int share = ((p.map.cap + cs - 1) / cs + 31) & ~31;
-  p.key_slots = share < kMaxKeySlots ? share : kMaxKeySlots;
-  const cudaError_t e = cs > 1 ? allow_smem<paged_evict_kernel<true>>(kMaxKeySlots * 4)
-                               : allow_smem<paged_evict_kernel<false>>(kMaxKeySlots * 4);
-  if (e != cudaSuccess) return cuda_status(e);
   if (cs == 1)
-    return finish_launch(launch_pdl(paged_evict_kernel<false>, dim3((unsigned)items), dim3(kEThreads),
-                                    (size_t)p.key_slots * 4, stream, p));
+    return finish_launch(launch_pdl(paged_evict_kernel<false, true>, dim3((unsigned)items), dim3(kEThreads), 0, stream, p));
+  const int share = ((p.map.cap + cs - 1) / cs + 31) & ~31;
+  const bool reg = share <= kSlotsPerCta;
+  if (!reg) {
+    p.key_slots = share < kMaxKeySlots ? share : kMaxKeySlots;
+    const cudaError_t e = allow_smem<paged_evict_kernel<true, false>>(kMaxKeySlots * 4);
+    if (e != cudaSuccess) return cuda_status(e);
+  }
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)(items * cs));
   cfg.blockDim = dim3(kEThreads);
@@ -391,7 +455,8 @@ int swa_paged_evict(const swa_paged_evict_args* a, cudaStream_t stream) {
   attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 2;
-  return finish_launch(cudaLaunchKernelEx(&cfg, paged_evict_kernel<true>, p));
+  return finish_launch(reg ? cudaLaunchKernelEx(&cfg, paged_evict_kernel<true, true>, p)
+                           : cudaLaunchKernelEx(&cfg, paged_evict_kernel<true, false>, p));
 }
 
 }  // extern "C"

@@ -640,6 +640,17 @@ def test_evict(kw, dtype, kind):
         call()                                               # the same inputs again: the same result
 
 
+@pytest.mark.parametrize("kind", ["spread", "ties", "special"])
+@pytest.mark.parametrize("kw", [
+    # the most slots that eight CTAs hold in registers; in shared memory; and more than that
+    dict(lens=[32768, 9000], nk=2, hd=64, page=256, keep=2000),
+    dict(lens=[40000, 100, 33000], nk=1, hd=128, page=64, keep=2500),
+    dict(lens=[350000], nk=1, hd=64, page=256, keep=3001),
+])
+def test_evict_long(kw, kind):
+    test_evict(kw, BF, kind)
+
+
 def test_evict_reports():
     bt = Batch(t=[0, 0], lens=[64, 30], nh=1, nk=1, hd=64, page=16, seed=33)
     table = bt.args[2].clone()
