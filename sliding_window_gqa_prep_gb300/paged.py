@@ -53,11 +53,14 @@ def _complain(x, name, dev, dtype, shape):
 
 
 def _arg(x, name, dev, dtype, shape=None) -> int:
-    """Device address of a checked dense tensor."""
-    if (not isinstance(x, torch.Tensor) or x.get_device() != dev or x.dtype != dtype
-            or (shape is not None and x.shape != shape) or not x.is_contiguous()):
-        _complain(x, name, dev, dtype, shape)
-    return x.data_ptr()
+    """Device address of a checked dense tensor. (Half of a small call's host time is spent
+    here: no more is asked than what has to be.)"""
+    try:
+        if x.get_device() == dev and x.dtype is dtype and (shape is None or x.shape == shape) and x.is_contiguous():
+            return x.data_ptr()
+    except AttributeError:
+        pass
+    _complain(x, name, dev, dtype, shape)
 
 
 def _opt(x, name, dev, dtype, shape=None) -> int:
@@ -75,24 +78,27 @@ def _rows(x, name, dev, dtype, shape) -> Tuple[int, int]:
     return x.data_ptr(), (row if T > 1 else H * hd)
 
 
-def _placed(fn):
-    """Runs a call on the device of its first tensor and on `stream`: as it is when that is
-    the current device and its current stream, inside both contexts otherwise."""
-    name = fn.__code__.co_varnames[0]
+_current_device, _current_stream = torch._C._cuda_getDevice, torch._C._cuda_getCurrentRawStream
 
-    @functools.wraps(fn)
-    def call(*args, stream=None, **kw):
-        first = args[0] if args else kw.get(name)
-        if not isinstance(first, torch.Tensor) or not first.is_cuda:
-            raise ValueError(f"{name} must be a CUDA tensor")
-        dev = first.get_device()
-        if stream is None and torch._C._cuda_getDevice() == dev:
-            return fn(*args, dev=dev, stream=torch._C._cuda_getCurrentRawStream(dev), **kw)
-        if stream is not None and stream.device.index != dev:
-            raise ValueError(f"stream is on {stream.device}, the tensors are on cuda:{dev}")
-        with torch.cuda.device(dev), torch.cuda.stream(stream):
-            return fn(*args, dev=dev, stream=torch._C._cuda_getCurrentRawStream(dev), **kw)
-    return call
+
+def _place(x, name, stream):
+    """The device of a call's first tensor and the handle of the stream it runs on: the current
+    one. No handle where another device or `stream` has to become current first (_there)."""
+    dev = x.get_device() if isinstance(x, torch.Tensor) else -1
+    if dev < 0:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    if stream is None and _current_device() == dev:
+        return dev, _current_stream(dev)
+    if stream is not None and stream.device.index != dev:
+        raise ValueError(f"stream is on {stream.device}, the tensors are on cuda:{dev}")
+    return dev, None
+
+
+def _there(fn, args):
+    """The call fn(**args) on the device args["dev"] and on args["stream"]."""
+    dev, stream, _ = args.pop("dev"), args.pop("stream"), args.pop("on")
+    with torch.cuda.device(dev), torch.cuda.stream(stream):
+        return fn(**args)
 
 
 _lib = _abi.load
@@ -127,13 +133,14 @@ def rotary_turns(rot, theta=10000.0, *, schedule="plain", factor=1.0, orig_len=0
     return torch.tensor([v - (1 << 64) if v >> 63 else v for v in t], dtype=torch.int64).to(device)
 
 
-@_placed
-def rotary(x, pos, turns, *, interleaved: bool = False, inverse: bool = False, mag: float = 1.0, out=None,
-           dev=None, stream=None):
+def rotary(x, pos, turns, *, interleaved: bool = False, inverse: bool = False, mag: float = 1.0, out=None, stream=None):
     """Rotary positions of packed rows x [T][H][hd] (f32, bf16 or f16; any row and head
     strides at multiples of 16 bytes): the first 2 * len(turns) features of every head turn
     by pos[row], the others are copied. inverse=True is the gradient of the call. out may
     be x."""
+    dev, on = _place(x, "x", stream)
+    if on is None:
+        return _there(rotary, locals())
     if x.dim() != 3 or x.dtype not in _TYPES:
         raise ValueError("x must be [T][H][hd] in float32, bfloat16 or float16")
     T, H, hd = x.shape
@@ -154,7 +161,7 @@ def rotary(x, pos, turns, *, interleaved: bool = False, inverse: bool = False, m
     a = _ROTARY.pack(T, H, hd, 2 * n, _TYPES[x.dtype], bool(interleaved), bool(inverse), mag,
                      x.data_ptr(), x_row, x_head, out.data_ptr(), o_row, o_head,
                      _arg(pos, "pos", dev, _I32, (T,)), _arg(turns, "turns", dev, _I64, (n,)))
-    _abi.check(_lib().swa_rotary(a, stream), "swa_rotary")
+    _abi.check(_lib().swa_rotary(a, on), "swa_rotary")
     return out
 
 
@@ -173,15 +180,17 @@ def _cache(cache_k, cache_v, page_table, row_start, lens, dev):
             _arg(lens, "lens", dev, _I32, (B,))), max_pages * page
 
 
-@_placed
 def paged_append(k, v, pos, cache_k, cache_v, page_table, row_start, lens, *, q=None, q_out=None, turns=None,
-                 interleaved: bool = False, mag: float = 1.0, slot_pos=None, weight=None, err=None, dev=None,
+                 interleaved: bool = False, mag: float = 1.0, slot_pos=None, weight=None, err=None,
                  stream=None):
     """A chunk's rows enter the cache: k [T][nk][hd] rotated by pos (when turns is given) and
     v, rounded to the cache's type, go to the slots lens[b] - t_b + i of their sequence;
     lens counts the chunk's rows. q [T][nh][hd] is rotated and rounded into q_out, which is
     returned (None without q). slot_pos and weight [B][nk][cap], when given, get the new
     slots' positions and weight 0."""
+    dev, on = _place(k, "k", stream)
+    if on is None:
+        return _there(paged_append, locals())
     cache, cap = _cache(cache_k, cache_v, page_table, row_start, lens, dev)
     B, nk, hd = cache[:3]
     if row_start is None:
@@ -207,7 +216,7 @@ def paged_append(k, v, pos, cache_k, cache_v, page_table, row_start, lens, *, q=
                      qo, _opt(pos, "pos", dev, _I32, (T,)), _opt(turns, "turns", dev, _I64, (n,)),
                      _opt(slot_pos, "slot_pos", dev, _I32, (B, nk, cap)), _opt(weight, "weight", dev, _F32, (B, nk, cap)),
                      _opt(err, "err", dev, _I32, (1,)))
-    _abi.check(_lib().swa_paged_append(a, stream), "swa_paged_append")
+    _abi.check(_lib().swa_paged_append(a, on), "swa_paged_append")
     return q_out
 
 
@@ -229,14 +238,16 @@ def _attend_need(dev, B, T, nh, nk, hd, page, max_pages, max_rows, dtype) -> int
     return int(_lib().swa_paged_attend_workspace_size(a))
 
 
-@_placed
 def paged_attend(q, cache_k, cache_v, page_table, row_start, lens, scale: float, *, max_rows: int, out=None,
-                 lse=None, workspace=None, err=None, ev_start=None, ev_stop=None, dev=None, stream=None):
+                 lse=None, workspace=None, err=None, ev_start=None, ev_stop=None, stream=None):
     """Causal attention of a chunk's rows q [T][nh][hd] (the cache's type) over the paged
     cache, their own keys already appended: row i of sequence b sees the slots below
     lens[b] - t_b + i + 1. max_rows bounds the rows of a sequence. out [T][nh][hd] in the
     cache's type or float32; lse [T][nh] f32, when given, gets log sum exp of the scores.
     Rows of no sequence are left as they were (zeros in a new out)."""
+    dev, on = _place(q, "q", stream)
+    if on is None:
+        return _there(paged_attend, locals())
     cache, _ = _cache(cache_k, cache_v, page_table, row_start, lens, dev)
     B, nk, hd, page, _, max_pages = cache[:6]
     if row_start is None:
@@ -260,18 +271,20 @@ def paged_attend(q, cache_k, cache_v, page_table, row_start, lens, scale: float,
     a = _ATTEND.pack(*cache, T, nh, max_rows, wide, scale, qp, q_row, op, _opt(lse, "lse", dev, _F32, (T, nh)),
                      ws, size, _opt(err, "err", dev, _I32, (1,)),
                      ev_start.cuda_event if ev_start is not None else 0, ev_stop.cuda_event if ev_stop is not None else 0)
-    _abi.check(_lib().swa_paged_attend(a, stream), "swa_paged_attend")
+    _abi.check(_lib().swa_paged_attend(a, on), "swa_paged_attend")
     return out
 
 
-@_placed
 def paged_weigh(q, lse, cache_k, page_table, row_start, lens, scale: float, *, max_rows: int, weight=None, out=None,
-                err=None, dev=None, stream=None):
+                err=None, stream=None):
     """The attention weight every cached key received from the rows q, added to weight
     [B][nk][cap] (None: zeros): out[b][g][j] = weight[b][g][j] + sum over rows that see slot j
     and heads of g of exp(scale <q, k_j> - lse). lse [T][nh] is paged_attend's for the same
     rows. out may be weight; entries from lens[b] on are left as they were (zeros in a new
     out)."""
+    dev, on = _place(q, "q", stream)
+    if on is None:
+        return _there(paged_weigh, locals())
     cache, cap = _cache(cache_k, None, page_table, row_start, lens, dev)
     B, nk, hd = cache[:3]
     if row_start is None:
@@ -285,7 +298,7 @@ def paged_weigh(q, lse, cache_k, page_table, row_start, lens, scale: float, *, m
     a = _WEIGH.pack(*cache, T, nh, max_rows, scale, qp, q_row, _arg(lse, "lse", dev, _F32, (T, nh)),
                     _opt(weight, "weight", dev, _F32, (B, nk, cap)), _arg(out, "out", dev, _F32, (B, nk, cap)),
                     _opt(err, "err", dev, _I32, (1,)))
-    _abi.check(_lib().swa_paged_weigh(a, stream), "swa_paged_weigh")
+    _abi.check(_lib().swa_paged_weigh(a, on), "swa_paged_weigh")
     return out
 
 
@@ -303,14 +316,16 @@ def _evict_need(B, nk, page, max_pages, keep) -> int:
         _EVICT.pack(B, nk, 0, page, 0, max_pages, 0, 0, 0, 0, 0, 0, keep, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0)))
 
 
-@_placed
 def paged_evict(cache_k, cache_v, page_table, lens, weight, slot_pos, keep: int, *, recent_from=None, sinks: int = 0,
-                weight_out=None, slot_pos_out=None, lens_out=None, workspace=None, err=None, dev=None, stream=None):
+                weight_out=None, slot_pos_out=None, lens_out=None, workspace=None, err=None, stream=None):
     """Cut every sequence's cache to at most `keep` keys per KV head: those at positions
     below sinks or from recent_from[b] on first, then by weight. Kept keys behind the new
     length move into the freed slots (within the pages, in place); weight and slot_pos
     [B][nk][cap] are read, their new values and the new lengths written to the outputs.
     Returns (lens_out, weight_out, slot_pos_out)."""
+    dev, on = _place(cache_k, "cache_k", stream)
+    if on is None:
+        return _there(paged_evict, locals())
     cache, cap = _cache(cache_k, cache_v, page_table, None, lens, dev)
     B, nk = cache[:2]
     shape = (B, nk, cap)
@@ -322,10 +337,13 @@ def paged_evict(cache_k, cache_v, page_table, lens, weight, slot_pos, keep: int,
     if lens_out is None:
         lens_out = torch.empty_like(lens)
     if workspace is None:
-        workspace = torch.empty(max(_evict_need(B, nk, cache[3], cache[5], keep), 1), device=cache_k.device, dtype=_U8)
+        size = max(_evict_need(B, nk, cache[3], cache[5], keep), 1)
+        workspace = torch.empty(size, device=cache_k.device, dtype=_U8)
+        ws = workspace.data_ptr()
+    else:
+        ws, size = _arg(workspace, "workspace", dev, _U8), workspace.numel()
     a = _EVICT.pack(*cache, keep, sinks, wp, pp, _opt(recent_from, "recent_from", dev, _I32, (B,)),
                     _arg(weight_out, "weight_out", dev, _F32, shape), _arg(slot_pos_out, "slot_pos_out", dev, _I32, shape),
-                    _arg(lens_out, "lens_out", dev, _I32, (B,)), _arg(workspace, "workspace", dev, _U8),
-                    workspace.numel(), _opt(err, "err", dev, _I32, (1,)))
-    _abi.check(_lib().swa_paged_evict(a, stream), "swa_paged_evict")
+                    _arg(lens_out, "lens_out", dev, _I32, (B,)), ws, size, _opt(err, "err", dev, _I32, (1,)))
+    _abi.check(_lib().swa_paged_evict(a, on), "swa_paged_evict")
     return lens_out, weight_out, slot_pos_out
