@@ -14,10 +14,10 @@
 // Steps 1 to 3 are chains of barriers and short passes, so the CTAs' shares stay small
 // (kSlotsPerCta) while the cluster may grow (8 CTAs at most) and the passes are kept short in
 // instructions; copies are bound by memory.
-// Measured: 32 sequences, 8 heads, 64 of 2112 slots: 13.5 us (keys 2.6, passes 3, counts and
-// walk 2.8, copies 2.5); four of 16384 to 32768 slots down to 4096: 36.7 us, of them copies
-// 17.5 at 6.6 TB/s, passes 7, counts and walk 5, keys 3. (Keys of a slot at a time, kept in shared
-// memory, and two walks: 17 and 46.7 us.)
+// Measured: 32 sequences, 8 heads, 64 of 2112 slots: 12.4 us (keys 2.6, passes 2.2, counts and
+// walk 2.8, copies 2.5); four of 16384 to 32768 slots down to 4096: 35.4 us, of them copies
+// 17.5 at 6.6 TB/s, passes 5.7, counts and walk 5, keys 3. (Keys of a slot at a time, kept in
+// shared memory, and two walks: 17 and 46.7 us; all passes always: 13.5 and 36.7.)
 #include <cooperative_groups.h>
 
 #include "swa_paged.cuh"
@@ -68,6 +68,7 @@ __global__ void __launch_bounds__(kEThreads, 2) paged_evict_kernel(const PagedEv
   __shared__ int2 s_tot;                    // this CTA's freed and moved slots
   __shared__ uint32_t s_digit;
   __shared__ int s_need;
+  __shared__ bool s_all;                    // every key of the bin stays
   cg::cluster_group cluster = cg::this_cluster();
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int CS = CL ? (int)cluster.num_blocks() : 1, rank = CL ? (int)cluster.block_rank() : 0;
@@ -222,6 +223,7 @@ __global__ void __launch_bounds__(kEThreads, 2) paged_evict_kernel(const PagedEv
         if (before < need && need <= before + c[i]) {
           s_digit = (uint32_t)(top + 3 - i);
           s_need = need - before;
+          s_all = need == before + c[i];
         }
         before += c[i];
       }
@@ -229,6 +231,13 @@ __global__ void __launch_bounds__(kEThreads, 2) paged_evict_kernel(const PagedEv
     __syncthreads();
     prefix = prefix << bits | s_digit;
     need = s_need;
+    // all keys with this prefix stay: those above the greatest key below it (of weights
+    // without ties: the last pass falls away 9 times in 10)
+    if (s_all && prefix != 0 && shift > 0) {
+      prefix = (prefix << shift) - 1;
+      need = 0;
+      break;
+    }
   }
   // keys above `prefix` stay, and of those that equal it the first `need` in slot order;
   // the CTAs before this one hold eq_before of them
