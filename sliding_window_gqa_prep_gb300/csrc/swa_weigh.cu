@@ -10,16 +10,18 @@
 // One CTA an SM. The units (sequence, KV head, 256 keys), each with its cost (tile_cost), are
 // laid end to end and cut evenly. Roles: warp 8 streams K tiles of 128
 // keys from the pages by TMA; warp 11 brings the query tiles (cp.async into the
-// swizzled layout, with each vector's lse and limit); warps 9 and 10 issue the products, two
+// swizzled layout, with each vector's lse and limit; the summing warps a pair that stays);
+// warps 9 and 10 issue the products, two
 // S buffers in TMEM for each half of a unit; a warpgroup (warps 0-3, 4-7) sums each half, so
 // that a query tile serves 256 keys and nothing is exchanged. A sequence of at most two
 // query tiles keeps them in shared memory for all its keys, else they are streamed per
 // unit. The sums run in a fixed order: no atomics.
 // Measured: one token of 64 sequences of 2048 to 4160 keys, 16 query heads on 4, hd 128: 37 us,
 // 5.5 TB/s of K and weights. The last 32 to 64 rows of four prompts of 16384 to 32768 keys, 32
-// heads on 8: 51 us (3.7 TB/s, 650 TFLOP/s), bound by the roles' latencies: a product costs
-// its issuing warp about 1500 clk with its waits and commits, and 128 columns of sums a
-// warpgroup 1650. Tried: four warpgroups of sums (54 us), K called into L2 ahead (54 us).
+// heads on 8: 46 us (4.1 TB/s, 720 TFLOP/s), bound by the sums: 128 columns take a warpgroup
+// 1650 clk, 1024 of them exponentials at the special functions' rate. Tried, when it took 51:
+// four warpgroups of sums (54 us), K called into L2 ahead (54), the next 32 columns of S loaded
+// while 32 are summed (53: S is freed later), 128 columns in registers (61: spills).
 #include <cmath>
 
 #include "swa_paged_tc.cuh"
@@ -149,7 +151,7 @@ __global__ void __launch_bounds__(kWeighThreads, 1)
       mbar_init(&b_kempty[i], 1);
     }
     for (int i = 0; i < 2; ++i) {
-      mbar_init(&b_qfull[i], 32);
+      mbar_init(&b_qfull[i], 2);
       mbar_init(&b_qempty[i], 2 + 8);
       mbar_init(&b_fin[i], 1);
     }
@@ -260,6 +262,39 @@ __global__ void __launch_bounds__(kWeighThreads, 1)
   uint32_t ignore = 0;
   WeighIter<QN> it{p, weigh_seq<QN>(p, s_b, ignore), s_b, s_g, s_tile, s_left};
   bool ok = true;
+  // Query tile qt's copy into a slot, by NTH threads: 16-byte chunks, CH a row, swizzled
+  auto copy_q = [&](int qt, int slot, int th, auto threads) {
+    constexpr int NTH = decltype(threads)::value;
+    const int v0 = qt * QN, n = min(QN, (it.w.nv - v0 + 31) & ~31), c = th % CH;
+    const uint32_t dst = smem_u32(sm_q + slot * C::QB) + (c >> 3) * (QN * 128);
+    const T* const qp = static_cast<const T*>(p.q) + c * 8;
+#pragma unroll 4
+    for (int r = th / CH; r < n; r += NTH / CH) {
+      const int vec = v0 + r;
+      const bool in = vec < it.w.nv;
+      const int i = in ? row_of(p, vec) : 0, h = in ? vec - i * p.hpg : 0;
+      const T* src = qp + (in ? (size_t)(it.w.s.r0 + i) * p.q_row + (size_t)(it.g * p.hpg + h) * D : 0);
+      asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;"
+                   :: "r"(dst + r * 128 + (((c & 7) ^ (r & 7)) << 4)), "l"(src), "r"(in ? 16 : 0)
+                   : "memory");
+    }
+    asm volatile("cp.async.commit_group;" ::: "memory");
+  };
+  // lse of query vector vec (infinite, for a weight of 0, where there is none); its limit
+  auto lse_of = [&](int vec) {
+    if (vec >= it.w.nv) return INFINITY;
+    const int i = row_of(p, vec);
+    return p.lse[(size_t)(it.w.s.r0 + i) * p.nh + it.g * p.hpg + vec - i * p.hpg];
+  };
+  auto note_q = [&](int slot, int v, int vec, float lse) {
+    s_nlse[slot][v] = lse * -1.4426950408889634f;
+    s_lim[slot][v] = vec < it.w.nv ? min(it.w.s.len, it.w.s.len - it.w.s.t + row_of(p, vec) + 1) : 0;
+  };
+
+  // A pair of query tiles that a head keeps is brought by the summing warps: it needs both slots,
+  // so it cannot come ahead of its use, and one warp takes 5 us for it (50.6 instead of 45.7 us
+  // for the prompts above). Others come ahead, by warp 11.
+  auto pair = [&]() { return it.resident() && it.w.nqt - it.qt0() == 2; };
 
   if (warp < 8) {
     // ------------------------------------------------------------ sums: thread = key
@@ -267,6 +302,27 @@ __global__ void __launch_bounds__(kWeighThreads, 1)
     const uint32_t lanes = tmem + ((uint32_t)((warp & 3) * 32) << 16) + h * 2 * QN;
     const uint64_t mul2 = pack64(__float_as_uint(p.qmul), __float_as_uint(p.qmul));
     int jc = 0, qc = 0, q_base = it.qt0(), q_seen = 0;      // q_seen: query tiles known to be there
+    // Each thread waits for each use of a slot (b_qfull and b_qempty in turn), so the waits'
+    // parities are unambiguous.
+    auto fill = [&]() {
+      if (!pair()) return;
+      const int q0 = it.qt0();
+      const int mt = tid / QN, mv = tid % QN, vec = (q0 + mt) * QN + mv;
+      const float lse = mt < 2 ? lse_of(vec) : 0.f;
+      for (int k = 0; k < 2; ++k) {
+        const int q = qc + k;
+        if (q >> 1) ok &= tc_wait(&b_qempty[q & 1], (uint32_t)(((q >> 1) - 1) & 1), &s_abort);
+        copy_q(q0 + k, q & 1, tid, Int<256>{});
+      }
+      if (mt < 2) note_q((qc + mt) & 1, mv, vec, lse);
+      asm volatile("cp.async.wait_group 0;" ::: "memory");
+      fence_proxy_async_smem();
+      __syncwarp();
+      named_barrier(1, 256);
+      if (tid == 0)
+        for (int k = 0; k < 2; ++k) mbar_arrive(&b_qfull[k]);
+    };
+    fill();
     while (!it.done()) {
       const int nqt = it.w.nqt, key = it.tile * kUnit + h * 128 + r;
       const bool res = it.resident(), here = h < it.halves();
@@ -358,7 +414,10 @@ __global__ void __launch_bounds__(kWeighThreads, 1)
           for (int i = q_base; i < nqt; ++i) mbar_arrive(&b_qempty[(qc + i - q_base) & 1]);
         qc += nqt - q_base;
       }
-      if (moved && !it.done()) q_base = it.qt0();
+      if (moved && !it.done()) {
+        q_base = it.qt0();
+        fill();
+      }
     }
     if (!ok) give_up();
   } else if (warp == 8) {
@@ -466,68 +525,52 @@ __global__ void __launch_bounds__(kWeighThreads, 1)
     if (!ok) give_up();
   } else if (warp == 11) {
     // ------------------------------------------------------------ query tiles
-    const int th = lane;
+    // (of pairs it only keeps count, so that it does not fall more than a use of a slot behind)
     int qc = 0, pending = -1;               // tiles started, the one whose arrival is still to be told
     auto tell = [&](bool all) {
       if (pending < 0) return;
       if (all) asm volatile("cp.async.wait_group 0;" ::: "memory");
       else asm volatile("cp.async.wait_group 1;" ::: "memory");
       fence_proxy_async_smem();
-      mbar_arrive(&b_qfull[pending & 1]);
+      __syncwarp();
+      if (lane < 2) mbar_arrive(&b_qfull[pending & 1]);
       pending = -1;
     };
-    auto load = [&](int qt, bool last) {     // last: the next load may be far away
+    auto load = [&](int qt) {
       const int slot = qc & 1, use = qc >> 1;
       if (use > 0 && !__all_sync(0xffffffffu, mbar_try_wait(&b_qempty[slot], (uint32_t)((use - 1) & 1)))) {
         tell(true);                         // before a wait that may be long
         if (!wait(&b_qempty[slot], use - 1)) return false;
       }
-      const int v0 = qt * QN, n = min(QN, (it.w.nv - v0 + 31) & ~31);
-      const uint32_t dst = smem_u32(sm_q + slot * C::QB);
-      const T* qp = static_cast<const T*>(p.q);
       // each thread's lse first: on its way while the copies are issued
       constexpr int LR = QN / 32;
       float lse[LR];
 #pragma unroll
-      for (int k = 0; k < LR; ++k) {
-        const int vec = v0 + th + k * 32;
-        lse[k] = INFINITY;                  // no query vector: weight 0
-        if (vec < it.w.nv) {
-          const int i = row_of(p, vec);
-          lse[k] = p.lse[(size_t)(it.w.s.r0 + i) * p.nh + it.g * p.hpg + vec - i * p.hpg];
-        }
-      }
-      // 32 lanes: CH chunks of 32 / CH rows at a time
-#pragma unroll 4
-      for (int r = th / CH; r < n; r += 32 / CH) {
-        const int c = th % CH, vec = v0 + r;
-        const bool in = vec < it.w.nv;
-        const int i = in ? row_of(p, vec) : 0, h = in ? vec - i * p.hpg : 0;
-        const T* src = qp + (in ? (size_t)(it.w.s.r0 + i) * p.q_row + (size_t)(it.g * p.hpg + h) * D + c * 8 : 0);
-        asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;"
-                     :: "r"(dst + (c >> 3) * (QN * 128) + r * 128 + (((c & 7) ^ (r & 7)) << 4)), "l"(src), "r"(in ? 16 : 0)
-                     : "memory");
-      }
-      asm volatile("cp.async.commit_group;" ::: "memory");
+      for (int k = 0; k < LR; ++k) lse[k] = lse_of(qt * QN + lane + k * 32);
+      copy_q(qt, slot, lane, Int<32>{});
 #pragma unroll
-      for (int k = 0; k < LR; ++k) {
-        const int vec = v0 + th + k * 32;
-        s_nlse[slot][th + k * 32] = lse[k] * -1.4426950408889634f;
-        s_lim[slot][th + k * 32] =
-            vec < it.w.nv ? min(it.w.s.len, it.w.s.len - it.w.s.t + row_of(p, vec) + 1) : 0;
-      }
+      for (int k = 0; k < LR; ++k) note_q(slot, lane + k * 32, qt * QN + lane + k * 32, lse[k]);
       tell(false);
       pending = qc++;
-      if (last) tell(true);
+      return true;
+    };
+    auto count = [&]() {
+      tell(true);
+      if (qc > 1 && !wait(&b_qempty[qc & 1], (qc >> 1) - 1)) return false;
+      if (lane == 0) mbar_arrive(&b_qfull[qc & 1]);
+      __syncwarp();
+      ++qc;
       return true;
     };
     bool fresh = true;
     while (ok && !it.done()) {
       if (it.resident()) {
         // the head's later key tiles need no query tile that its first one here does not
-        for (int qt = it.qt0(); fresh && ok && qt < it.w.nqt; ++qt) ok = load(qt, qt == it.w.nqt - 1);
+        const bool theirs = pair();
+        for (int qt = it.qt0(); fresh && ok && qt < it.w.nqt; ++qt) ok = theirs ? count() : load(qt);
+        if (!theirs) tell(true);            // the next load may be far away
       } else {
-        for (int qt = it.qt0(); ok && qt < it.w.nqt; ++qt) ok = load(qt, false);
+        for (int qt = it.qt0(); ok && qt < it.w.nqt; ++qt) ok = load(qt);
       }
       if (ok) fresh = it.next();
     }

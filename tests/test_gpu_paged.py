@@ -538,6 +538,9 @@ def test_weigh(kw, dtype):
     dict(seed=8, B=150, lo=300, hi=1500, rows=[40, 64], nh=8, nk=2, hd=128, page=64),
     dict(seed=9, B=70, lo=500, hi=1500, rows=[100, 20], nh=8, nk=2, hd=64, page=32),
     dict(seed=10, B=80, lo=200, hi=900, rows=[100, 3], nh=8, nk=2, hd=256, page=64),
+    # one, two and more of them in one share
+    dict(seed=11, B=170, lo=200, hi=900, rows=[20, 50, 0, 60, 100], nh=8, nk=2, hd=128, page=64),
+    dict(seed=12, B=170, lo=100, hi=700, rows=[12, 30, 31, 70], nh=4, nk=1, hd=256, page=32),
 ])
 def test_weigh_many_units(kw):
     """Several units a CTA, of one half and of two, and back to back calls."""
