@@ -18,10 +18,12 @@
 // unit. The sums run in a fixed order: no atomics.
 // Measured: one token of 64 sequences of 2048 to 4160 keys, 16 query heads on 4, hd 128: 37 us,
 // 5.5 TB/s of K and weights. The last 32 to 64 rows of four prompts of 16384 to 32768 keys, 32
-// heads on 8: 46 us (4.1 TB/s, 720 TFLOP/s), bound by the sums: 128 columns take a warpgroup
-// 1650 clk, 1024 of them exponentials at the special functions' rate. Tried, when it took 51:
-// four warpgroups of sums (54 us), K called into L2 ahead (54), the next 32 columns of S loaded
-// while 32 are summed (53: S is freed later), 128 columns in registers (61: spills).
+// heads on 8: 46 us (4.1 TB/s, 720 TFLOP/s), bound by the sums' latencies: 128 columns take a
+// warpgroup 1650 clk, 1024 of them exponentials at the special functions' rate (ncu: these and
+// the tensor pipe 35 % each, issue 40 %). Tried: four warpgroups of sums (54 us when this took
+// 51), K called into L2 ahead (54 for 51), the next 32 columns of S loaded while 32 are summed
+// (53 for 51: S is freed later), 128 columns in registers (61: spills), a key of each half a
+// thread over half of the columns, with one lse for both (51 for 46).
 #include <cmath>
 
 #include "swa_paged_tc.cuh"
