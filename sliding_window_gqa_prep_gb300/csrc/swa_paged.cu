@@ -57,8 +57,10 @@ typedef CUresult (*EncodeTiled)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, v
                                 const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle,
                                 CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
 
-// Tensor map of a pool: rows of hd elements, boxes of 64 features x min(page, KT) rows.
-int pool_map(const swa_paged_cache& c, void* base, int kt, CUtensorMap* m) {
+// Tensor map of 16-bit elements, 128-byte swizzle, zeros out of range; dims, strides (in
+// bytes, from the second dimension on) and box by rank.
+static int tensor_map(int dtype, const void* base, int rank, const cuuint64_t* dims, const cuuint64_t* strides,
+                      const cuuint32_t* box, CUtensorMap* m) {
   static EncodeTiled encode = nullptr;
   if (!encode) {
     void* f = nullptr;
@@ -68,13 +70,26 @@ int pool_map(const swa_paged_cache& c, void* base, int kt, CUtensorMap* m) {
     if (st != cudaDriverEntryPointSuccess || !f) return cuda_status(cudaErrorNotSupported);
     encode = reinterpret_cast<EncodeTiled>(f);
   }
+  const cuuint32_t es[3] = {1, 1, 1};
+  const CUresult r = encode(m, dtype == SWA_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, rank,
+                            const_cast<void*>(base), dims, strides, box, es, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                            CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  return r == CUDA_SUCCESS ? SWA_OK : cuda_status(cudaErrorInvalidValue);
+}
+
+// Tensor map of a pool: rows of hd elements, boxes of 64 features x min(page, KT) rows.
+int pool_map(const swa_paged_cache& c, void* base, int kt, CUtensorMap* m) {
   const cuuint64_t dims[2] = {(cuuint64_t)c.hd, (cuuint64_t)c.num_pages * c.nk * c.page};
   const cuuint64_t strides[1] = {(cuuint64_t)c.hd * 2};
-  const cuuint32_t box[2] = {64, (cuuint32_t)(c.page < kt ? c.page : kt)}, es[2] = {1, 1};
-  const CUresult r = encode(m, c.dtype == SWA_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 2,
-                            base, dims, strides, box, es, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
-                            CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
-  return r == CUDA_SUCCESS ? SWA_OK : cuda_status(cudaErrorInvalidValue);
+  const cuuint32_t box[2] = {64, (cuuint32_t)(c.page < kt ? c.page : kt)};
+  return tensor_map(c.dtype, base, 2, dims, strides, box, m);
+}
+
+int rows_map(const swa_paged_cache& c, const void* q, int T, int nh, long long row, int heads, int rows, CUtensorMap* m) {
+  const cuuint64_t dims[3] = {(cuuint64_t)c.hd, (cuuint64_t)nh, (cuuint64_t)T};
+  const cuuint64_t strides[2] = {(cuuint64_t)c.hd * 2, (cuuint64_t)row * 2};
+  const cuuint32_t box[3] = {64, (cuuint32_t)heads, (cuuint32_t)rows};
+  return tensor_map(c.dtype, q, 3, dims, strides, box, m);
 }
 
 // ---------------------------------------------------------------------------

@@ -10,6 +10,9 @@ namespace swa {
 // Tensor map of a page pool (K or V of a swa_paged_cache): rows of hd elements, boxes of
 // 64 features x min(page, kt) rows, 128-byte swizzle, zeros out of range (swa_paged.cu).
 int pool_map(const swa_paged_cache& c, void* base, int kt, CUtensorMap* m);
+// Tensor map of packed rows q [T][nh][hd], `row` elements apart, of the cache's type: boxes of
+// 64 features x `heads` heads x `rows` rows, 128-byte swizzle (swa_paged.cu).
+int rows_map(const swa_paged_cache& c, const void* q, int T, int nh, long long row, int heads, int rows, CUtensorMap* m);
 
 #ifdef __CUDACC__
 // kind::f16 with D in f32, A and B both f16 or both bf16, A K-major, B K-major or not
@@ -77,6 +80,10 @@ __device__ __forceinline__ void wait_ld(uint32_t (&x)[32]) {
 __device__ __forceinline__ void tma_2d(uint32_t dst, const CUtensorMap* map, int x, int y, uint64_t* bar) {
   asm volatile("cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%3, %4}], [%2];"
                :: "r"(dst), "l"(map), "r"(smem_u32(bar)), "r"(x), "r"(y) : "memory");
+}
+__device__ __forceinline__ void tma_3d(uint32_t dst, const CUtensorMap* map, int x, int y, int z, uint64_t* bar) {
+  asm volatile("cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%3, %4, %5}], [%2];"
+               :: "r"(dst), "l"(map), "r"(smem_u32(bar)), "r"(x), "r"(y), "r"(z) : "memory");
 }
 
 // A wait that gives up after kWaitLimitNs, for the whole CTA; the clock is read every 64th try only (the
