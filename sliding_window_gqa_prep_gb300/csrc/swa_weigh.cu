@@ -9,8 +9,9 @@
 //
 // One CTA an SM. The units (sequence, KV head, 256 keys), each with its cost (tile_cost), are
 // laid end to end and cut evenly. Roles: warp 8 streams K tiles of 128
-// keys from the pages by TMA; warp 11 brings the query tiles (cp.async into the
-// swizzled layout, with each vector's lse and limit; the summing warps a pair that stays);
+// keys from the pages by TMA; warp 11 brings the query tiles (whole ones by TMA, else cp.async
+// into the same swizzled layout, with each vector's lse and limit; the summing warps a pair
+// that stays);
 // warps 9 and 10 issue the products, two
 // S buffers in TMEM for each half of a unit; a warpgroup (warps 0-3, 4-7) sums each half, so
 // that a query tile serves 256 keys and nothing is exchanged. A sequence of at most two
@@ -23,7 +24,9 @@
 // the tensor pipe 35 % each, issue 40 %). Tried: four warpgroups of sums (54 us when this took
 // 51), K called into L2 ahead (54 for 51), the next 32 columns of S loaded while 32 are summed
 // (53 for 51: S is freed later), 128 columns in registers (61: spills), a key of each half a
-// thread over half of the columns, with one lse for both (51 for 46).
+// thread over half of the columns, with one lse for both (51 for 46). All rows of prompts of 2048
+// rows over 4096 to 8192 keys, four of them, 32 heads on 8, hd 128: 350 us, 794 TFLOP/s; 8 of 512
+// rows, 32 heads on 4, hd 64: 180 us, 445 TFLOP/s.
 #include <cmath>
 
 #include "swa_paged_tc.cuh"
@@ -32,7 +35,7 @@ namespace swa {
 
 template <int D>
 struct WeighCfg {
-  static constexpr int QN = D == 256 ? 64 : 128;       // query vectors of a tile
+  static constexpr int QN = D == 256 ? 64 : 128;       // most query vectors of a tile (tile_vecs)
   // K slots of 128 keys, half of them for each half of a unit: a wait sees only the parity
   // of a barrier's phase, so whoever waits on a slot has to wait for each of its uses
   static constexpr int NS = D == 64 ? 8 : D == 128 ? 4 : 2, NSH = NS / 2;
@@ -47,26 +50,34 @@ constexpr int kUnit = 256;     // keys of a unit
 // columns that the last query tile may lack, so that every unit costs something.
 constexpr int kUnitCost = 5;
 
+// x / d for 0 <= x < 2^31: shift = 31 + l with 2^l >= d and mul = ceil(2^shift / d) <= 2^32: the
+// product's excess is below x * 2^l < 2^shift, so the quotient is exact.
+struct Quot {
+  uint32_t mul, shift;
+  explicit Quot(int d = 2) : mul(0), shift(31) {
+    while ((1 << (shift - 31)) < d) ++shift;
+    mul = (uint32_t)(((1ull << shift) + d - 1) / d);
+  }
+  __device__ __forceinline__ int operator()(int x) const { return (int)((unsigned long long)(unsigned)x * mul >> shift); }
+};
+
 struct PagedWeighParams {
   PagedMap map;
   int T, nh, hpg, max_rows;
-  uint32_t hpg_mul, hpg_shift; // vec / hpg = vec * hpg_mul >> hpg_shift for 0 <= vec < 2^31 (row_of)
+  Quot by_hpg, by_rows;        // vec / hpg: a vector's row; row / tile_rows: a row's tile
+  // A query tile is as many whole rows as fit in QN vectors: tile_rows rows of hpg vectors
+  int tile_rows, tile_vecs;
   float qmul;
   const void* q;
   long long q_row;
-  int bulk_q;                  // map_q covers whole query tiles
+  int bulk_q;                  // map_q brings whole query tiles
   const float* lse;
   const float* weight;
   float* out;
   uint32_t* err;
 };
 
-// The chunk row of a query vector. hpg_shift = 31 + l with 2^l >= hpg and hpg_mul =
-// ceil(2^hpg_shift / hpg) <= 2^32: the product's excess is below vec * 2^l < 2^hpg_shift,
-// so the quotient is exact.
-__device__ __forceinline__ int row_of(const PagedWeighParams& p, int vec) {
-  return (int)((unsigned long long)(unsigned)vec * p.hpg_mul >> p.hpg_shift);
-}
+__device__ __forceinline__ int row_of(const PagedWeighParams& p, int vec) { return p.by_hpg(vec); }
 
 // A sequence's units of a KV head ("tiles" of kUnit keys) and the query tiles that see them.
 struct WeighSeq {
@@ -79,10 +90,10 @@ __device__ __forceinline__ WeighSeq weigh_seq(const PagedWeighParams& p, int b, 
   WeighSeq w;
   w.s = paged_seq(p.map, b, p.T, p.max_rows, bits);
   w.nv = w.s.t * p.hpg;
-  w.nqt = (w.nv + QN - 1) / QN;
+  w.nqt = w.s.t > 0 ? p.by_rows(w.s.t - 1) + 1 : 0;
   w.n_tiles = (w.s.len + kUnit - 1) / kUnit;
   w.n_full = w.nqt <= 1 ? w.n_tiles : w.s.len >= w.s.t ? min(w.n_tiles, (w.s.len - w.s.t) / kUnit + 1) : 0;
-  w.base = kUnitCost - (w.nqt > 0 ? (w.nqt * QN - w.nv) / 32 : 0);   // the last query tile's missing columns
+  w.base = kUnitCost - (w.nqt > 0 ? (w.nqt * p.tile_vecs - w.nv) / 32 : 0);   // the last query tile's missing columns
   return w;
 }
 // First query tile that sees keys of tile `tile`: its last row has a limit above the tile's
@@ -90,7 +101,7 @@ __device__ __forceinline__ WeighSeq weigh_seq(const PagedWeighParams& p, int b, 
 template <int QN>
 __device__ __forceinline__ int first_qt(const PagedWeighParams& p, const WeighSeq& w, int tile) {
   const long long row = (long long)tile * kUnit - (w.s.len - w.s.t);
-  return row <= 0 ? 0 : (int)min((long long)w.nqt, row * p.hpg / QN);
+  return row <= 0 ? 0 : row < w.s.t ? p.by_rows((int)row) : w.nqt;
 }
 template <int QN>
 __device__ __forceinline__ int tile_cost(const PagedWeighParams& p, const WeighSeq& w, int tile) {
@@ -169,6 +180,13 @@ __global__ void __launch_bounds__(kWeighThreads, 1)
   } else if (warp == 9) {
     tc_alloc(&s_tmem, 512);
   }
+  // rows of the query slots behind tile_vecs are read and never brought: zeros
+  for (int i = tid; i < 2 * (QN - p.tile_vecs) * CH; i += kWeighThreads) {
+    const int c = i % CH, r = p.tile_vecs + i / CH % (QN - p.tile_vecs), slot = i / CH / (QN - p.tile_vecs);
+    *reinterpret_cast<uint4*>(sm_q + slot * C::QB + (c >> 3) * (QN * 128) + r * 128 + (((c & 7) ^ (r & 7)) << 4)) =
+        make_uint4(0, 0, 0, 0);
+  }
+  fence_proxy_async_smem();
   pdl_wait();
   pdl_trigger();
 
@@ -266,20 +284,24 @@ __global__ void __launch_bounds__(kWeighThreads, 1)
   uint32_t ignore = 0;
   WeighIter<QN> it{p, weigh_seq<QN>(p, s_b, ignore), s_b, s_g, s_tile, s_left};
   bool ok = true;
-  // Query tile qt's copy into a slot, by NTH threads: 16-byte chunks, CH a row, swizzled. The
-  // row and head of a vector run along (a division a chunk: 146 instead of XX us for 51 sequences
-  // of up to 351 rows, 10 heads on 2, hd 256).
+  // Columns of query tile qt's product: its vectors, up to a multiple of 32
+  auto columns_of = [&](int qt) {
+    return min(QN, (min(p.tile_vecs, it.w.nv - qt * p.tile_vecs) + 31) & ~31);   // QN: known to the compiler
+  };
+  // Query tile qt's copy into a slot, by NTH threads: 16-byte chunks, CH a row, swizzled; zeros
+  // behind its vectors. The row and head of a vector run along (a division a chunk: 270 instead
+  // of 192 us for four prompts of 512 rows over 4096 to 8192 keys, 24 heads on 8, hd 128).
   auto copy_q = [&](int qt, int slot, int th, auto threads) {
     constexpr int STEP = decltype(threads)::value / CH;
-    const int v0 = qt * QN, n = min(QN, (it.w.nv - v0 + 31) & ~31), c = th % CH;
+    const int n = columns_of(qt), c = th % CH, end = min(it.w.nv, (qt + 1) * p.tile_vecs);
     const uint32_t dst = smem_u32(sm_q + slot * C::QB) + (c >> 3) * (QN * 128);
     const int di = STEP / p.hpg, dh = STEP - di * p.hpg;
-    int vec = v0 + th / CH, h = vec - row_of(p, vec) * p.hpg;
+    int vec = qt * p.tile_vecs + th / CH, h = vec - row_of(p, vec) * p.hpg;
     const long long ds = di * p.q_row + dh * D, dw = p.q_row - p.hpg * D;
     const T* src = static_cast<const T*>(p.q) + (size_t)(it.w.s.r0 + row_of(p, vec)) * p.q_row + (size_t)(it.g * p.hpg + h) * D + c * 8;
 #pragma unroll 4
     for (int r = th / CH; r < n; r += STEP) {
-      const bool in = vec < it.w.nv;
+      const bool in = vec < end;
       asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;"
                    :: "r"(dst + r * 128 + (((c & 7) ^ (r & 7)) << 4)), "l"(in ? src : static_cast<const T*>(p.q)), "r"(in ? 16 : 0)
                    : "memory");
@@ -293,7 +315,8 @@ __global__ void __launch_bounds__(kWeighThreads, 1)
     }
     asm volatile("cp.async.commit_group;" ::: "memory");
   };
-  // lse of query vector vec (infinite, for a weight of 0, where there is none); its limit
+  // lse of vector v of query tile qt (infinite, for a weight of 0, where there is none); its limit
+  auto vec_of = [&](int qt, int v) { return v < p.tile_vecs ? qt * p.tile_vecs + v : 0x7fffffff; };
   auto lse_of = [&](int vec) {
     if (vec >= it.w.nv) return INFINITY;
     const int i = row_of(p, vec);
@@ -320,7 +343,7 @@ __global__ void __launch_bounds__(kWeighThreads, 1)
     auto fill = [&]() {
       if (!pair()) return;
       const int q0 = it.qt0();
-      const int mt = tid / QN, mv = tid % QN, vec = (q0 + mt) * QN + mv;
+      const int mt = tid / QN, mv = tid % QN, vec = vec_of(q0 + mt, mv);
       const float lse = mt < 2 ? lse_of(vec) : 0.f;
       for (int k = 0; k < 2; ++k) {
         const int q = qc + k;
@@ -354,7 +377,7 @@ __global__ void __launch_bounds__(kWeighThreads, 1)
         if (here) {
           ok &= tc_wait(&b_s[2 * h + buf], (uint32_t)((jc >> 1) & 1), &s_abort);
           tc_fence_after();
-          const int n = min(QN, (it.w.nv - qt * QN + 31) & ~31);
+          const int n = columns_of(qt);
           // columns [c, c + W): weights into the sums
           auto columns = [&](int c, auto width, auto masked) {
             constexpr int W = decltype(width)::value;
@@ -398,7 +421,7 @@ __global__ void __launch_bounds__(kWeighThreads, 1)
           // some row of the tile does not see all keys of this half
           const bool mask =
               it.tile * kUnit + h * 128 + 128 >
-              it.w.s.len - it.w.s.t + row_of(p, qt * QN) + 1;
+              it.w.s.len - it.w.s.t + qt * p.tile_rows + 1;
           for (int c = 0; c < n; c += 64) {
             if (mask) {
               columns(c, Int<32>{}, std::true_type{});
@@ -503,7 +526,7 @@ __global__ void __launch_bounds__(kWeighThreads, 1)
           if (jc >= 2) until(&b_sfree[buf], (jc >> 1) - 1);
           tc_fence_after();
           if (leader) {
-            const int n = min(QN, (it.w.nv - qt * QN + 31) & ~31);
+            const int n = columns_of(qt);
             const uint32_t id = tc_idesc_16(BF, false, n);
             const uint64_t kd = k_desc + (uint64_t)((slot * C::KB) >> 4), qd = q_desc + (uint64_t)(((qi & 1) * C::QB) >> 4);
 #pragma unroll
@@ -551,29 +574,30 @@ __global__ void __launch_bounds__(kWeighThreads, 1)
     };
     auto load = [&](int qt) {
       const int slot = qc & 1, use = qc >> 1;
+      // each thread's lse first: on its way during the wait and the copies
+      constexpr int LR = QN / 32;
+      float lse[LR];
+#pragma unroll
+      for (int k = 0; k < LR; ++k) lse[k] = lse_of(vec_of(qt, lane + k * 32));
       if (use > 0 && !__all_sync(0xffffffffu, mbar_try_wait(&b_qempty[slot], (uint32_t)((use - 1) & 1)))) {
         tell(true);                         // before a wait that may be long
         if (!wait(&b_qempty[slot], use - 1)) return false;
       }
-      // each thread's lse first: on its way while the copies are issued
-      constexpr int LR = QN / 32;
-      float lse[LR];
-#pragma unroll
-      for (int k = 0; k < LR; ++k) lse[k] = lse_of(qt * QN + lane + k * 32);
-      // whole tiles of heads that divide it come by TMA: (64 features, hpg heads, rows) boxes
-      const bool bulk = p.bulk_q && (qt + 1) * QN <= it.w.nv;
+      // whole tiles come by TMA: boxes of 64 features, hpg heads and tile_rows rows (1258 instead
+      // of 375 us for four prompts of 2048 rows over 4096 to 8192 keys, when a warp copied them)
+      const bool bulk = p.bulk_q && (qt + 1) * p.tile_rows <= it.w.s.t;
       if (bulk) {
         tell(true);
-        if (lane == 0) mbar_arrive_expect_tx(&b_qfull[slot], C::QB);
+        if (lane == 0) mbar_arrive_expect_tx(&b_qfull[slot], p.tile_vecs * D * 2);
         __syncwarp();
         if (lane < D / 64)
           tma_3d(smem_u32(sm_q + slot * C::QB + lane * (QN * 128)), &map_q, lane * 64, it.g * p.hpg,
-                 it.w.s.r0 + row_of(p, qt * QN), &b_qfull[slot]);
+                 it.w.s.r0 + qt * p.tile_rows, &b_qfull[slot]);
       } else {
         copy_q(qt, slot, lane, Int<32>{});
       }
 #pragma unroll
-      for (int k = 0; k < LR; ++k) note_q(slot, lane + k * 32, qt * QN + lane + k * 32, lse[k]);
+      for (int k = 0; k < LR; ++k) note_q(slot, lane + k * 32, vec_of(qt, lane + k * 32), lse[k]);
       if (bulk) {
         __syncwarp();
         if (lane == 0) mbar_arrive(&b_qfull[slot]);
@@ -627,8 +651,12 @@ static int launch_weigh(const swa_paged_weigh_args* a, const PagedWeighParams& p
   int rc = pool_map(a->cache, a->cache.k, 128, &mk);
   constexpr int QN = WeighCfg<D>::QN;
   PagedWeighParams p = params;
-  p.bulk_q = QN % p.hpg == 0 && (long long)p.max_rows * p.hpg >= QN && a->q_row < (1LL << 39);   // else no such tile
-  if (rc == SWA_OK && p.bulk_q) rc = rows_map(a->cache, a->q, a->T, a->nh, a->q_row, p.hpg, QN / p.hpg, &mq);
+  p.tile_rows = QN / p.hpg;
+  p.tile_vecs = p.tile_rows * p.hpg;
+  p.by_hpg = Quot(p.hpg);
+  p.by_rows = Quot(p.tile_rows);
+  p.bulk_q = p.max_rows >= p.tile_rows && a->q_row < (1LL << 39);   // no such tile; strides below 2^40 bytes
+  if (rc == SWA_OK && p.bulk_q) rc = rows_map(a->cache, a->q, a->T, a->nh, a->q_row, p.hpg, p.tile_rows, &mq);
   else mq = mk;
   if (rc != SWA_OK) return rc;
   const cudaError_t e = allow_smem<paged_weigh_kernel<T, D>>(WeighCfg<D>::SMEM);
@@ -665,9 +693,6 @@ int swa_paged_weigh(const swa_paged_weigh_args* a, cudaStream_t stream) {
                    bytes_overlap(a->lse, (size_t)a->T * a->nh * 4, a->out, bytes)))
     return SWA_E_SHAPE;
   p.T = a->T; p.nh = a->nh; p.hpg = a->nh / c.nk; p.max_rows = a->max_rows < a->T ? a->max_rows : a->T;
-  p.hpg_shift = 31;
-  while ((1 << (p.hpg_shift - 31)) < p.hpg) ++p.hpg_shift;
-  p.hpg_mul = (uint32_t)(((1ull << p.hpg_shift) + p.hpg - 1) / p.hpg);
   p.qmul = a->scale * 1.4426950408889634f;
   p.q = a->q; p.q_row = a->q_row;
   p.lse = a->lse; p.weight = a->weight; p.out = a->out; p.err = a->err;

@@ -541,6 +541,10 @@ def test_weigh(kw, dtype):
     # one, two and more of them in one share
     dict(seed=11, B=170, lo=200, hi=900, rows=[20, 50, 0, 60, 100], nh=8, nk=2, hd=128, page=64),
     dict(seed=12, B=170, lo=100, hi=700, rows=[12, 30, 31, 70], nh=4, nk=1, hd=256, page=32),
+    # groups of heads that do not divide a query tile
+    dict(seed=13, B=60, lo=300, hi=900, rows=[100, 17], nh=10, nk=2, hd=256, page=64),
+    dict(seed=14, B=40, lo=100, hi=800, rows=[60, 9, 21], nh=24, nk=2, hd=64, page=16),
+    dict(seed=15, B=30, lo=100, hi=800, rows=[30, 7], nh=31, nk=1, hd=128, page=64),
 ])
 def test_weigh_many_units(kw):
     """Several units a CTA, of one half and of two, and back to back calls."""
