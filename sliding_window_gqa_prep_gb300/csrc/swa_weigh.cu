@@ -49,6 +49,7 @@ constexpr int kUnit = 256;     // keys of a unit
 // fixed work at least, and a query tile costs its columns and one more. kUnitCost covers the
 // columns that the last query tile may lack, so that every unit costs something.
 constexpr int kUnitCost = 5;
+constexpr int kNote = 4;       // query tiles whose lse and limits are in shared memory
 
 // x / d for 0 <= x < 2^31: shift = 31 + l with 2^l >= d and mul = ceil(2^shift / d) <= 2^32: the
 // product's excess is below x * 2^l < 2^shift, so the quotient is exact.
@@ -150,8 +151,11 @@ __global__ void __launch_bounds__(kWeighThreads, 1)
   constexpr bool BF = std::is_same<T, __nv_bfloat16>::value;
   extern __shared__ unsigned char sm_raw[];
   __shared__ __align__(8) uint64_t b_kfull[NS], b_kempty[NS], b_qfull[2], b_qempty[2], b_s[4], b_sfree[4], b_fin[2];
-  __shared__ __align__(16) float s_nlse[2][QN];             // -lse log2 e
-  __shared__ __align__(16) int s_lim[2][QN];
+  // lse and limits have a ring of their own: a query tile's slot is free once its products are
+  // done, while they are needed until its sums are
+  __shared__ __align__(8) uint64_t b_nfull[kNote], b_nempty[kNote], b_pair;
+  __shared__ __align__(16) float s_nlse[kNote][QN];             // -lse log2 e
+  __shared__ __align__(16) int s_lim[kNote][QN];
   __shared__ long long s_scan[kWeighThreads / 32];
   __shared__ long long s_left;
   __shared__ uint32_t s_tmem;
@@ -166,14 +170,19 @@ __global__ void __launch_bounds__(kWeighThreads, 1)
       mbar_init(&b_kempty[i], 1);
     }
     for (int i = 0; i < 2; ++i) {
-      mbar_init(&b_qfull[i], 2);
-      mbar_init(&b_qempty[i], 2 + 8);
+      mbar_init(&b_qfull[i], 1);
+      mbar_init(&b_qempty[i], 2);
       mbar_init(&b_fin[i], 1);
     }
     for (int i = 0; i < 4; ++i) {
       mbar_init(&b_s[i], 1);
       mbar_init(&b_sfree[i], 4);
     }
+    for (int i = 0; i < kNote; ++i) {
+      mbar_init(&b_nfull[i], 1);
+      mbar_init(&b_nempty[i], 8);
+    }
+    mbar_init(&b_pair, 1);
     mbar_fence_init();
     s_b = -1;
     s_abort = 0;
@@ -338,25 +347,24 @@ __global__ void __launch_bounds__(kWeighThreads, 1)
     const uint32_t lanes = tmem + ((uint32_t)((warp & 3) * 32) << 16) + h * 2 * QN;
     const uint64_t mul2 = pack64(__float_as_uint(p.qmul), __float_as_uint(p.qmul));
     int jc = 0, qc = 0, q_base = it.qt0(), q_seen = 0;      // q_seen: query tiles known to be there
-    // Each thread waits for each use of a slot (b_qfull and b_qempty in turn), so the waits'
-    // parities are unambiguous.
-    auto fill = [&]() {
+    int pairs = 0;
+    auto fill = [&]() {                     // once warp 11 has seen that the slots are free
       if (!pair()) return;
       const int q0 = it.qt0();
       const int mt = tid / QN, mv = tid % QN, vec = vec_of(q0 + mt, mv);
       const float lse = mt < 2 ? lse_of(vec) : 0.f;
-      for (int k = 0; k < 2; ++k) {
-        const int q = qc + k;
-        if (q >> 1) ok &= tc_wait(&b_qempty[q & 1], (uint32_t)(((q >> 1) - 1) & 1), &s_abort);
-        copy_q(q0 + k, q & 1, tid, Int<256>{});
-      }
-      if (mt < 2) note_q((qc + mt) & 1, mv, vec, lse);
+      ok &= tc_wait(&b_pair, (uint32_t)(pairs++ & 1), &s_abort);
+      for (int k = 0; k < 2; ++k) copy_q(q0 + k, (qc + k) & 1, tid, Int<256>{});
+      if (mt < 2) note_q((qc + mt) % kNote, mv, vec, lse);
       asm volatile("cp.async.wait_group 0;" ::: "memory");
       fence_proxy_async_smem();
       __syncwarp();
       named_barrier(1, 256);
       if (tid == 0)
-        for (int k = 0; k < 2; ++k) mbar_arrive(&b_qfull[k]);
+        for (int k = 0; k < 2; ++k) {
+          mbar_arrive(&b_qfull[(qc + k) & 1]);
+          mbar_arrive(&b_nfull[(qc + k) % kNote]);
+        }
     };
     fill();
     while (!it.done()) {
@@ -367,11 +375,11 @@ __global__ void __launch_bounds__(kWeighThreads, 1)
       const float w0 = mine && p.weight ? p.weight[at] : 0.f;   // under way during the products
       uint64_t sum[4] = {0, 0, 0, 0};
       for (int qt = it.qt0(); qt < nqt; ++qt) {
-        const int qi = res ? qc + qt - q_base : qc, buf = jc & 1, slot = qi & 1;
+        const int qi = res ? qc + qt - q_base : qc, buf = jc & 1, slot = qi % kNote;
         // lse and limits; a thread whose wait gave up goes on (its warp stays together) and
         // writes nothing
         if (qi >= q_seen) {
-          ok &= tc_wait(&b_qfull[slot], (uint32_t)((qi >> 1) & 1), &s_abort);
+          ok &= tc_wait(&b_nfull[slot], (uint32_t)((qi / kNote) & 1), &s_abort);
           q_seen = qi + 1;
         }
         if (here) {
@@ -436,7 +444,7 @@ __global__ void __launch_bounds__(kWeighThreads, 1)
         }
         if (!res) {
           __syncwarp();
-          if (lane == 0) mbar_arrive(&b_qempty[slot]);
+          if (lane == 0) mbar_arrive(&b_nempty[slot]);
           ++qc;
         }
       }
@@ -447,7 +455,7 @@ __global__ void __launch_bounds__(kWeighThreads, 1)
       if (moved && res) {
         __syncwarp();
         if (lane == 0)
-          for (int i = q_base; i < nqt; ++i) mbar_arrive(&b_qempty[(qc + i - q_base) & 1]);
+          for (int i = q_base; i < nqt; ++i) mbar_arrive(&b_nempty[(qc + i - q_base) % kNote]);
         qc += nqt - q_base;
       }
       if (moved && !it.done()) {
@@ -561,7 +569,6 @@ __global__ void __launch_bounds__(kWeighThreads, 1)
     if (!ok) give_up();
   } else if (warp == 11) {
     // ------------------------------------------------------------ query tiles
-    // (of pairs it only keeps count, so that it does not fall more than a use of a slot behind)
     int qc = 0, pending = -1;               // tiles started, the one whose arrival is still to be told
     auto tell = [&](bool all) {
       if (pending < 0) return;
@@ -569,23 +576,25 @@ __global__ void __launch_bounds__(kWeighThreads, 1)
       else asm volatile("cp.async.wait_group 1;" ::: "memory");
       fence_proxy_async_smem();
       __syncwarp();
-      if (lane < 2) mbar_arrive(&b_qfull[pending & 1]);
+      if (lane == 0) mbar_arrive(&b_qfull[pending & 1]);
       pending = -1;
     };
+    // phase `use - 1` of a slot's empty barrier; a tile under way is told before a long wait
+    auto until_free = [&](uint64_t* bar, int use) {
+      if (use == 0 || __all_sync(0xffffffffu, mbar_try_wait(bar, (uint32_t)((use - 1) & 1)))) return true;
+      tell(true);
+      return wait(bar, use - 1);
+    };
     auto load = [&](int qt) {
-      const int slot = qc & 1, use = qc >> 1;
-      // each thread's lse first: on its way during the wait and the copies
+      const int slot = qc & 1, note = qc % kNote;
       constexpr int LR = QN / 32;
       float lse[LR];
 #pragma unroll
-      for (int k = 0; k < LR; ++k) lse[k] = lse_of(vec_of(qt, lane + k * 32));
-      if (use > 0 && !__all_sync(0xffffffffu, mbar_try_wait(&b_qempty[slot], (uint32_t)((use - 1) & 1)))) {
-        tell(true);                         // before a wait that may be long
-        if (!wait(&b_qempty[slot], use - 1)) return false;
-      }
+      for (int k = 0; k < LR; ++k) lse[k] = lse_of(vec_of(qt, lane + k * 32));   // on its way during the waits
       // whole tiles come by TMA: boxes of 64 features, hpg heads and tile_rows rows (1258 instead
       // of 375 us for four prompts of 2048 rows over 4096 to 8192 keys, when a warp copied them)
       const bool bulk = p.bulk_q && (qt + 1) * p.tile_rows <= it.w.s.t;
+      if (!until_free(&b_qempty[slot], qc >> 1)) return false;
       if (bulk) {
         tell(true);
         if (lane == 0) mbar_arrive_expect_tx(&b_qfull[slot], p.tile_vecs * D * 2);
@@ -595,34 +604,37 @@ __global__ void __launch_bounds__(kWeighThreads, 1)
                  it.w.s.r0 + qt * p.tile_rows, &b_qfull[slot]);
       } else {
         copy_q(qt, slot, lane, Int<32>{});
-      }
-#pragma unroll
-      for (int k = 0; k < LR; ++k) note_q(slot, lane + k * 32, vec_of(qt, lane + k * 32), lse[k]);
-      if (bulk) {
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&b_qfull[slot]);
-        ++qc;
-      } else {
         tell(false);
-        pending = qc++;
+        pending = qc;
       }
+      const int q = qc++;
+      if (!until_free(&b_nempty[note], q / kNote)) return false;
+#pragma unroll
+      for (int k = 0; k < LR; ++k) note_q(note, lane + k * 32, vec_of(qt, lane + k * 32), lse[k]);
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&b_nfull[note]);
       return true;
     };
-    auto count = [&]() {
+    // both slots of a pair are free: told to the summing warps
+    auto give_pair = [&]() {
       tell(true);
-      if (qc > 1 && !wait(&b_qempty[qc & 1], (qc >> 1) - 1)) return false;
-      if (lane == 0) mbar_arrive(&b_qfull[qc & 1]);
+      for (int q = qc; q < qc + 2; ++q)
+        if (!until_free(&b_qempty[q & 1], q >> 1) || !until_free(&b_nempty[q % kNote], q / kNote)) return false;
+      if (lane == 0) mbar_arrive(&b_pair);
       __syncwarp();
-      ++qc;
+      qc += 2;
       return true;
     };
     bool fresh = true;
     while (ok && !it.done()) {
       if (it.resident()) {
         // the head's later key tiles need no query tile that its first one here does not
-        const bool theirs = pair();
-        for (int qt = it.qt0(); fresh && ok && qt < it.w.nqt; ++qt) ok = theirs ? count() : load(qt);
-        if (!theirs) tell(true);            // the next load may be far away
+        if (fresh && pair()) {
+          ok = give_pair();
+        } else if (fresh) {
+          for (int qt = it.qt0(); ok && qt < it.w.nqt; ++qt) ok = load(qt);
+          tell(true);                       // the next load may be far away
+        }
       } else {
         for (int qt = it.qt0(); ok && qt < it.w.nqt; ++qt) ok = load(qt);
       }
