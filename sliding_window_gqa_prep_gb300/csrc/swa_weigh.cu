@@ -11,8 +11,7 @@
 // laid end to end and cut evenly. Roles: warp 8 streams K tiles of 128
 // keys from the pages by TMA; warp 11 brings the query tiles (whole ones by TMA, else cp.async
 // into the same swizzled layout, with each vector's lse and limit; the summing warps a pair
-// that stays);
-// warps 9 and 10 issue the products, two
+// that stays); warps 9 and 10 issue the products, two
 // S buffers in TMEM for each half of a unit; a warpgroup (warps 0-3, 4-7) sums each half, so
 // that a query tile serves 256 keys and nothing is exchanged. A sequence of at most two
 // query tiles keeps them in shared memory for all its keys, else they are streamed per
@@ -25,7 +24,7 @@
 // 51), K called into L2 ahead (54 for 51), the next 32 columns of S loaded while 32 are summed
 // (53 for 51: S is freed later), 128 columns in registers (61: spills), a key of each half a
 // thread over half of the columns, with one lse for both (51 for 46). All rows of prompts of 2048
-// rows over 4096 to 8192 keys, four of them, 32 heads on 8, hd 128: 350 us, 794 TFLOP/s; 8 of 512
+// rows over 4096 to 8192 keys, four of them, 32 heads on 8, hd 128: 324 us, 855 TFLOP/s; 8 of 512
 // rows, 32 heads on 4, hd 64: 180 us, 445 TFLOP/s.
 #include <cmath>
 
@@ -299,7 +298,7 @@ __global__ void __launch_bounds__(kWeighThreads, 1)
   };
   // Query tile qt's copy into a slot, by NTH threads: 16-byte chunks, CH a row, swizzled; zeros
   // behind its vectors. The row and head of a vector run along (a division a chunk: 270 instead
-  // of 192 us for four prompts of 512 rows over 4096 to 8192 keys, 24 heads on 8, hd 128).
+  // of 192 us, when this copied all tiles, for four prompts of 512 rows over 4096 to 8192 keys, 24 heads on 8, hd 128).
   auto copy_q = [&](int qt, int slot, int th, auto threads) {
     constexpr int STEP = decltype(threads)::value / CH;
     const int n = columns_of(qt), c = th % CH, end = min(it.w.nv, (qt + 1) * p.tile_vecs);
