@@ -410,18 +410,29 @@ __global__ void __launch_bounds__(ChunkCfg<D>::THREADS, 1)
     float m = -INFINITY, l = 0.f;
     bool ok = true;
     if (mine > 0) {
-      // Q into shared memory: 16-byte chunks, rows of 128 bytes, swizzled
-      unsigned char* qs = sm + t * C::QB;
-      const T* qp = static_cast<const T*>(a.q);
-      constexpr int CH = D / 8;
-      for (int i = r; i < 128 * CH; i += 128) {
-        const int row = i / CH, c = i % CH;
-        uint4 v = make_uint4(0, 0, 0, 0);
-        if (row < nvec)
-          v = *reinterpret_cast<const uint4*>(qp + (size_t)(s.r0 + first + row / hpg) * a.q_row +
-                                              (size_t)(g * hpg + row % hpg) * D + c * 8);
-        *reinterpret_cast<uint4*>(qs + (c >> 3) * (128 * 128) + row * 128 + (((c & 7) ^ (row & 7)) << 4)) = v;
+      // Q into shared memory: 16-byte chunks, rows of 128 bytes, swizzled, zeros behind its
+      // vectors; all copies under way together, the row's address running along (loads through
+      // registers, one after the other, took 6700 clk at hd 64)
+      constexpr int CH = D / 8, STEP = 128 / CH;
+      const int c = r % CH, di = STEP / hpg, dh = STEP - di * hpg, t0 = r / CH / hpg;
+      int h = r / CH - t0 * hpg;
+      const T* src = static_cast<const T*>(a.q) + (size_t)(s.r0 + first + t0) * a.q_row + (size_t)(g * hpg + h) * D + c * 8;
+      const long long ds = di * a.q_row + dh * D, dw = a.q_row - hpg * D;
+      const uint32_t qs = smem_u32(sm + t * C::QB) + (c >> 3) * (128 * 128);
+#pragma unroll 8
+      for (int row = r / CH; row < 128; row += STEP) {
+        const bool in = row < nvec;
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;"
+                     :: "r"(qs + row * 128 + (((c & 7) ^ (row & 7)) << 4)), "l"(in ? src : static_cast<const T*>(a.q)), "r"(in ? 16 : 0)
+                     : "memory");
+        h += dh;
+        src += ds;
+        if (h >= hpg) {
+          h -= hpg;
+          src += dw;
+        }
       }
+      asm volatile("cp.async.wait_all;" ::: "memory");
       fence_proxy_async_smem();
       mbar_arrive(&b_q[t]);
     }
