@@ -20,11 +20,11 @@
 // Few items are split over the keys: grid.y shares of an item's tiles leave records
 // that chunk_merge_kernel joins.
 // Measured: four sequences of 2048 rows behind 6144 keys, 32 query heads on 8, hd 128, bf16:
-// 700 us, 1375 TFLOP/s; ragged ones of 1024 to 2048 rows over 2048 to 16384 keys: 550 us,
-// 1338 TFLOP/s (ncu: tensor pipe 59 %, special functions 30 %). What is left is the chain
+// 646 us, 1490 TFLOP/s; ragged ones of 1024 to 2048 rows over 2048 to 16384 keys: 526 us,
+// 1399 TFLOP/s (ncu: tensor pipe 64 %, special functions 32 %). What is left is the chain
 // S -> softmax -> P V -> S of a tile: about 330 clk from the last product issued to the
-// barrier seen, twice a step, and P V before the S that overwrites P. hd 64: 870 TFLOP/s,
-// the same chain for half the products; hd 256: 840, every 128 query vectors read K and V.
+// barrier seen, twice a step, and P V before the S that overwrites P. hd 64: 940 TFLOP/s,
+// the same chain for half the products; hd 256: 1057, every 128 query vectors read K and V.
 #include <cmath>
 
 #include "swa_paged_tc.cuh"
@@ -123,7 +123,7 @@ __global__ void __launch_bounds__(ChunkCfg<D>::THREADS, 1)
 
   // --- which item. CTAs start in the order of their numbers, so the longest sequences'
   // items come first and the SMs end together (the ragged prompts above: 579 us in the order
-  // of the batch). Every thread adds up the items in front of
+  // of the batch when this took 550). Every thread adds up the items in front of
   // its sequence's, which is quick for few sequences; many are taken as they come, by a scan.
   const int item_tok = NT * p.tile_tok;
   if (a.map.B <= kSortSeqs) {
@@ -412,7 +412,8 @@ __global__ void __launch_bounds__(ChunkCfg<D>::THREADS, 1)
     if (mine > 0) {
       // Q into shared memory: 16-byte chunks, rows of 128 bytes, swizzled, zeros behind its
       // vectors; all copies under way together, the row's address running along (loads through
-      // registers, one after the other, took 6700 clk at hd 64)
+      // registers, one after the other, took 6700 clk instead of 2800 at hd 64: 146 instead of 99 us
+      // for 16 sequences of up to 512 rows over 1024 keys, 32 heads on 8, hd 128)
       constexpr int CH = D / 8, STEP = 128 / CH;
       const int c = r % CH, di = STEP / hpg, dh = STEP - di * hpg, t0 = r / CH / hpg;
       int h = r / CH - t0 * hpg;
