@@ -27,6 +27,7 @@ __all__ = ["rotary_freqs", "rotary_turns", "rotary", "paged_append", "paged_atte
            "paged_attend_workspace_size", "paged_weigh", "paged_evict", "paged_evict_workspace_size"]
 
 _TYPES = {torch.float32: _abi.SWA_F32, torch.bfloat16: _abi.SWA_BF16, torch.float16: _abi.SWA_F16}
+_TYPES16 = {torch.bfloat16: _abi.SWA_BF16, torch.float16: _abi.SWA_F16}
 _KINDS = {"plain": 0, "linear": 1, "base": 2, "parts": 3}
 _I32, _I64, _F32, _U8 = torch.int32, torch.int64, torch.float32, torch.uint8
 
@@ -69,13 +70,18 @@ def _opt(x, name, dev, dtype, shape=None) -> int:
 
 def _rows(x, name, dev, dtype, shape) -> Tuple[int, int]:
     """Address and row stride of packed rows [T][heads][hd] with dense heads."""
-    if not isinstance(x, torch.Tensor) or x.get_device() != dev or x.dtype != dtype or x.shape != shape:
-        _complain(x, name, dev, dtype, shape)
-    T, H, hd = shape
-    row, head, one = x.stride()
-    if one != 1 or (head != hd and H > 1):
-        raise ValueError(f"{name}: the heads of a row must be dense")
-    return x.data_ptr(), (row if T > 1 else H * hd)
+    try:
+        if x.get_device() == dev and x.dtype is dtype and x.shape == shape:
+            T, H, hd = shape
+            if x.is_contiguous():
+                return x.data_ptr(), H * hd
+            row, head, one = x.stride()
+            if one != 1 or (head != hd and H > 1):
+                raise ValueError(f"{name}: the heads of a row must be dense")
+            return x.data_ptr(), (row if T > 1 else H * hd)
+    except AttributeError:
+        pass
+    _complain(x, name, dev, dtype, shape)
 
 
 _current_device, _current_stream = torch._C._cuda_getDevice, torch._C._cuda_getCurrentRawStream
@@ -167,16 +173,18 @@ def rotary(x, pos, turns, *, interleaved: bool = False, inverse: bool = False, m
 
 def _cache(cache_k, cache_v, page_table, row_start, lens, dev):
     """The fields of a swa_paged_cache and the capacity of a sequence."""
-    if cache_k.dim() != 4 or cache_k.dtype not in (torch.bfloat16, torch.float16):
+    dtype, shape, pages = cache_k.dtype, cache_k.shape, page_table.shape
+    if len(shape) != 4 or dtype not in _TYPES16:
         raise ValueError("cache_k must be [num_pages][nk][page][hd] in bfloat16 or float16")
-    if page_table.dim() != 2:
+    if len(pages) != 2:
         raise ValueError("page_table must be [B][max_pages]")
-    num_pages, nk, page, hd = cache_k.shape
-    B, max_pages = page_table.shape
-    k = _arg(cache_k, "cache_k", dev, cache_k.dtype)
-    v = k if cache_v is None else _arg(cache_v, "cache_v", dev, cache_k.dtype, cache_k.shape)
-    return (B, nk, hd, page, num_pages, max_pages, _TYPES[cache_k.dtype], k, v,
-            _arg(page_table, "page_table", dev, _I32), _opt(row_start, "row_start", dev, _I32, (B + 1,)),
+    num_pages, nk, page, hd = shape
+    B, max_pages = pages
+    k = _arg(cache_k, "cache_k", dev, dtype)
+    v = k if cache_v is None else _arg(cache_v, "cache_v", dev, dtype, shape)
+    return (B, nk, hd, page, num_pages, max_pages, _TYPES16[dtype], k, v,
+            _arg(page_table, "page_table", dev, _I32),
+            0 if row_start is None else _arg(row_start, "row_start", dev, _I32, (B + 1,)),
             _arg(lens, "lens", dev, _I32, (B,))), max_pages * page
 
 
