@@ -517,8 +517,16 @@ __global__ void __launch_bounds__(kMergeThreads) paged_merge_kernel(const PagedA
 // Launches
 // ---------------------------------------------------------------------------
 // Query vectors of a (sequence, KV head) up to which the split kernel takes it; more go
-// to the tensor-core kernel (swa_paged_chunk.cu).
-constexpr int kSplitVecs = 64;
+// to the tensor-core kernel (swa_paged_chunk.cu). 32 sequences of 2048 keys, 8 KV heads, split and
+// tensor-core kernel: 32 vectors at hd 64 45 and 45 us, at hd 128 64 and 56, 48 vectors 59 and 45,
+// 82 and 57; at hd 256 20 vectors 155 and 93 us. One sequence of 32768 keys, 32 vectors: hd 64 30
+// and 32 us, hd 128 41 and 45; 8 ragged ones: 24 and 26, 29 and 30. Where sequences have unequal
+// rows (B * max_rows > T) both kernels may have to run, one after the other, so up to 64 stay with
+// one: 26 sequences of up to 22 rows over 18 to 4453 keys, 6 heads on 3, hd 128: 48 instead of 75 us
+// (hd 256, 8 of up to 29 rows over 323 to 15713 keys: 99 instead of 56, so 16 there all the same).
+static int split_vecs(const swa_paged_attend_args* a, int max_rows) {
+  return a->cache.hd == 256 ? 16 : (long long)a->cache.B * max_rows > a->T ? 64 : 32;
+}
 
 // Keys of a sequence up to which a CTA takes a (sequence, KV head) whole: no scan over the
 // sequences and no second kernel.
@@ -568,7 +576,7 @@ template <typename F>
 static int by_type(int dtype, int hd, int rows, F f) {
 #define SWA_ROWS(T, D) (rows == 16 ? f((T*)nullptr, Int<D>{}, Int<16>{}) : rows == 32 ? f((T*)nullptr, Int<D>{}, Int<32>{}) \
                                                                                     : f((T*)nullptr, Int<D>{}, Int<64>{}))
-#define SWA_HD(T) (hd == 64 ? SWA_ROWS(T, 64) : hd == 128 ? SWA_ROWS(T, 128) : SWA_ROWS(T, 256))
+#define SWA_HD(T) (hd == 64 ? SWA_ROWS(T, 64) : hd == 128 ? SWA_ROWS(T, 128) : f((T*)nullptr, Int<256>{}, Int<16>{}))
   return dtype == SWA_BF16 ? SWA_HD(__nv_bfloat16) : SWA_HD(__half);
 #undef SWA_HD
 #undef SWA_ROWS
@@ -582,6 +590,7 @@ struct PagedPlan {
   SplitPlan split;
   ChunkPlan chunk;
   bool has_chunk;
+  int most;                              // query vectors of a sequence up to which it is the split kernel's
   size_t off_chunk, bytes;
 };
 
@@ -590,9 +599,11 @@ static void attend_plan(const swa_paged_attend_args* a, PagedPlan* pl) {
   const long long vecs = (long long)max_rows * hpg;
   SplitPlan& sp = pl->split;
   sp = SplitPlan{};
-  pl->has_chunk = vecs > kSplitVecs;
+  pl->most = split_vecs(a, max_rows);
+  pl->has_chunk = vecs > pl->most;
   if (!pl->has_chunk || (long long)a->cache.B * max_rows > a->T) {
-    sp.rows = vecs <= 16 ? 16 : vecs <= 32 ? 32 : 64;
+    const long long v = vecs < pl->most ? vecs : pl->most;
+    sp.rows = v <= 16 ? 16 : v <= 32 ? 32 : 64;
     sp.whole = (long long)a->cache.max_pages * a->cache.page <= kWholeKeys;
     const int occ = sp.whole ? 0 : by_type(a->cache.dtype, a->cache.hd, sp.rows, [](auto* t, auto d, auto r) {
       return split_occupancy<std::remove_pointer_t<decltype(t)>, decltype(d)::value, decltype(r)::value>();
@@ -660,7 +671,7 @@ int swa_paged_attend(const swa_paged_attend_args* a, cudaStream_t stream) {
   PagedAttendParams p{};
   p.map = paged_map(&c);
   p.T = a->T; p.nh = a->nh; p.hpg = a->nh / c.nk; p.max_rows = a->max_rows < a->T ? a->max_rows : a->T;
-  p.most = kSplitVecs;
+  p.most = pl.most;
   p.qmul = a->scale * 1.4426950408889634f;
   p.q = a->q; p.q_row = a->q_row; p.ck = c.k; p.cv = c.v;
   p.out = a->out; p.out_f32 = a->out_f32 != 0; p.lse = a->lse;
@@ -679,7 +690,7 @@ int swa_paged_attend(const swa_paged_attend_args* a, cudaStream_t stream) {
     if (rc != SWA_OK) return rc;
   }
   if (pl.has_chunk) {
-    rc = launch_paged_chunk(a, p, pl.chunk, pl.split.rows ? kSplitVecs : 0, ws + pl.off_chunk, stream);
+    rc = launch_paged_chunk(a, p, pl.chunk, pl.split.rows ? p.most : 0, ws + pl.off_chunk, stream);
     if (rc != SWA_OK) return rc;
   }
   if (a->ev_stop && (e = cudaEventRecord(a->ev_stop, stream)) != cudaSuccess) return cuda_status(e);

@@ -314,6 +314,10 @@ ATTEND = [
     dict(t=[300], lens=[200], nh=2, nk=1, hd=128, page=16),          # 100 rows see nothing
     dict(t=[35], lens=[1111], nh=32, nk=1, hd=128, page=256),
     dict(t=[513, 3], lens=[2000, 3], nh=1, nk=1, hd=128, page=16),
+    # equal rows of 33 to 64 vectors, and of 17 and more at hd 256: tensor cores
+    dict(t=[10, 10], lens=[10, 700], nh=8, nk=2, hd=128, page=32),
+    dict(t=[16], lens=[300], nh=4, nk=1, hd=64, page=16),
+    dict(t=[9, 9, 9], lens=[9, 64, 1000], nh=4, nk=2, hd=256, page=64),
 ]
 
 
