@@ -111,8 +111,6 @@ __global__ void __launch_bounds__(ChunkCfg<D>::THREADS, 1)
       mbar_init(&b_tail, 1);
       mbar_fence_init();
     }
-  } else if (warp == W_MMA) {
-    tc_alloc(&s_tmem, 512);
   }
   if (tid == 0) {
     s_b = -1;
@@ -120,6 +118,9 @@ __global__ void __launch_bounds__(ChunkCfg<D>::THREADS, 1)
   }
   pdl_wait();
   pdl_trigger();
+  // Not before the wait: a CTA that held TMEM while it waits for the kernel in front could keep
+  // it from that kernel's CTA on the same SM, which may still have its own to allocate.
+  if (warp == W_MMA) tc_alloc(&s_tmem, 512);
 
   // --- which item. CTAs start in the order of their numbers, so the longest sequences'
   // items come first and the SMs end together (the ragged prompts above: 579 us in the order

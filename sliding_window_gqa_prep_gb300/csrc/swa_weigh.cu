@@ -185,8 +185,6 @@ __global__ void __launch_bounds__(kWeighThreads, 1)
     mbar_fence_init();
     s_b = -1;
     s_abort = 0;
-  } else if (warp == 9) {
-    tc_alloc(&s_tmem, 512);
   }
   // rows of the query slots behind tile_vecs are read and never brought: zeros
   for (int i = tid; i < 2 * (QN - p.tile_vecs) * CH; i += kWeighThreads) {
@@ -197,6 +195,9 @@ __global__ void __launch_bounds__(kWeighThreads, 1)
   fence_proxy_async_smem();
   pdl_wait();
   pdl_trigger();
+  // Not before the wait: a CTA that held TMEM while it waits for the kernel in front could keep
+  // it from that kernel's CTA on the same SM, which may still have its own to allocate.
+  if (warp == 9) tc_alloc(&s_tmem, 512);
 
   // --- this CTA's share: units whose start lies in [u0, u1) of the summed costs
   {
