@@ -634,10 +634,11 @@ int swa_paged_append(const swa_paged_append_args* args, cudaStream_t stream);
  * [0, lens[b] - t_b + i + 1); query head h reads KV head h / (nh / nk):
  *   s = scale * <q, k>, p = exp(s - max s), out = sum p v / sum p,
  *   lse = log(sum exp(s)).
- * Scores, maxima and sums are f32; the weights p are rounded to the cache's
- * type for the value product (one rounding of each weight, relative 2^-8 or
- * 2^-11 at most); out is rounded once. A row that sees no key gets out = 0,
- * lse = -inf. What lies behind a sequence's last key in its pages is not used,
+ * Scores, maxima and sums are f32; the weights p enter the value product in the
+ * cache's type: in calls of at most 16 query vectors a KV head and sequence
+ * (min(max_rows, T) * nh / nk) as their rounding and what it leaves (relative
+ * 2^-16 in bf16, 2^-22 in f16, at most), in others rounded once (2^-8, 2^-11);
+ * out is rounded once. A row that sees no key gets out = 0, lse = -inf. What lies behind a sequence's last key in its pages is not used,
  * NaN and infinities included; keys that some row of the chunk sees must be
  * finite in V for the rows before them.
  *   q    [T][nh][hd] of the cache's type, rows q_row elements apart (heads

@@ -128,6 +128,12 @@ __global__ void __launch_bounds__(SplitCfg<D>::THREADS)
   using C = SplitCfg<D>;
   constexpr int RG = ROWS / 16, KG = 4 / RG, KW = kKeys / KG;   // row groups, key groups, keys of a warp
   constexpr int DS = C::DS, DV = D / DS, ST = C::ST, CW = C::CW, NWARPS = C::THREADS / 32;
+  // Weights are rounded to T for the value product. A block of 16 vectors adds what the rounding
+  // leaves, in a second product with the same V registers: the weight is then off by 2^-16 (f16:
+  // 2^-22) at most. It is bound by memory and pays 1 % (64 tokens as above: 98.6 and 99.8 us);
+  // wider blocks, whose warps are busy, would pay more: 4 % with 32 vectors over 32768 keys, 10 %
+  // with unequal rows and 20 % in a call that mixes 63 tokens with a prompt.
+  constexpr bool REST = ROWS == 16;
   extern __shared__ unsigned char sm_raw[];
   __shared__ __align__(8) uint64_t b_full[ST], b_empty[ST];
   __shared__ long long s_scan[NWARPS];
@@ -382,16 +388,27 @@ __global__ void __launch_bounds__(SplitCfg<D>::THREADS)
         }
 #pragma unroll
       for (int n = 0; n < KW / 16; ++n) {
-        const uint32_t pa[4] = {pack2(sc[2 * n][0], sc[2 * n][1], (const T*)nullptr),
-                                pack2(sc[2 * n][2], sc[2 * n][3], (const T*)nullptr),
-                                pack2(sc[2 * n + 1][0], sc[2 * n + 1][1], (const T*)nullptr),
-                                pack2(sc[2 * n + 1][2], sc[2 * n + 1][3], (const T*)nullptr)};
+        uint32_t pa[4], pr[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const float e0 = sc[2 * n + (j >> 1)][2 * (j & 1)], e1 = sc[2 * n + (j >> 1)][2 * (j & 1) + 1];
+          pa[j] = pack2(e0, e1, (const T*)nullptr);
+          if constexpr (REST) {
+            float h0, h1;
+            unpack2(pa[j], h0, h1, (const T*)nullptr);
+            pr[j] = pack2(e0 - h0, e1 - h1, (const T*)nullptr);
+          }
+        }
 #pragma unroll
         for (int dd = 0; dd < DV / 16; ++dd) {
           uint32_t f[4];
           ldsm4t(f, vb + at(kg * KW + n * 16 + (((lane >> 3) & 1) << 3) + (lane & 7), ds * (DV / 8) + dd * 2 + (lane >> 4)));
           mma16816<T>(o[2 * dd], pa, f[0], f[1]);
           mma16816<T>(o[2 * dd + 1], pa, f[2], f[3]);
+          if constexpr (REST) {
+            mma16816<T>(o[2 * dd], pr, f[0], f[1]);
+            mma16816<T>(o[2 * dd + 1], pr, f[2], f[3]);
+          }
         }
       }
       __syncwarp();

@@ -107,6 +107,15 @@ __device__ __forceinline__ uint32_t pack2(float a, float b, const __half*) {
   const __half2 v = __floats2half2_rn(a, b);
   return *reinterpret_cast<const uint32_t*>(&v);
 }
+__device__ __forceinline__ void unpack2(uint32_t v, float& a, float& b, const __nv_bfloat16*) {
+  a = __uint_as_float(v << 16);
+  b = __uint_as_float(v & 0xffff0000u);
+}
+__device__ __forceinline__ void unpack2(uint32_t v, float& a, float& b, const __half*) {
+  const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&v));
+  a = f.x;
+  b = f.y;
+}
 __device__ __forceinline__ void store8(float* p, const float (&x)[8]) {
   *reinterpret_cast<float4*>(p) = make_float4(x[0], x[1], x[2], x[3]);
   *reinterpret_cast<float4*>(p + 4) = make_float4(x[4], x[5], x[6], x[7]);
