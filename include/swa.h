@@ -530,10 +530,12 @@ typedef struct swa_paged_cache {
  * swa_rotary_turns — the frequencies of rotary positions, on the HOST.
  *   freqs [rot/2] f64 (output, may be NULL): f_e in radians per position
  *   turns [rot/2] u64 (output, may be NULL): f_e / 2 pi in turns, as 64-bit
- *     fixed point: floor(frac(f_e / 2 pi) * 2^64). The kernels take
- *     pos * turns modulo 2^64: positions are whole, so whole turns drop out
- *     and the angle is exact to 2^-33 turns at every position (the fraction is
- *     good to 2^-53 turns a position and pos < 2^31).
+ *     fixed point: floor(frac(f_e / 2 pi) * 2^64), every bit of it right for
+ *     the f64 f_e. The kernels take pos * turns modulo 2^64: positions are
+ *     whole, so whole turns drop out and the fraction of pos * f_e is good to
+ *     2^-33 turns at every position (2^-64 a position, |pos| <= 2^31). They keep
+ *     its upper 32 bits (2^-32 turns) and round these to f32 (2^-26 turns at
+ *     most). f_e itself is an f64, a few 2^-53 off its formula, relative.
  * Copy `turns` to the device once and keep it; a table of one's own may be
  * built the same way.
  * Schedules (rot even, >= 2; theta > 0; factor >= 1 where read):
@@ -545,7 +547,7 @@ typedef struct swa_paged_cache {
  *   SWA_ROTARY_PARTS   with r = orig_len * f_e / 2 pi turns over the trained
  *                      length: f_e where r >= high, f_e / factor where
  *                      r <= low, in between mixed linearly in r (low < high)
- * Errors: SWA_E_NULL (s NULL), SWA_E_SHAPE.
+ * Errors: SWA_E_NULL (s NULL), SWA_E_SHAPE (also a frequency of 2^64 or more).
  */
 #define SWA_ROTARY_PLAIN   0
 #define SWA_ROTARY_LINEAR  1

@@ -4,9 +4,9 @@
 // u' = u cos a - v sin a, v' = v cos a + u sin a with a = pos * f. The angle is
 // taken modulo one turn in integers: turns = f / 2 pi as a 64-bit fraction, and
 // pos * turns modulo 2^64 is the angle's fraction of a turn, exact but for the
-// fraction's own last bit. Its upper 32 bits, signed, times 2^-31 are half turns in
-// [-1, 1), what sincospif takes: no f64 arithmetic (two lanes an SM here) and no
-// range reduction, at any position.
+// fraction's own last bit (2^-33 turns at 2^31 positions). Its upper 32 bits, signed (2^-32 turns),
+// times 2^-31 are half turns in [-1, 1) once rounded to f32 (2^-26 turns at most), what sincospif
+// takes: no f64 arithmetic (two lanes an SM here) and no range reduction, at any position.
 //
 // Memory bound: each element is read and written once. A block takes R rows and a group
 // of heads: its threads first compute the rows' sines and cosines into shared memory (one
@@ -281,7 +281,27 @@ static int rotary_freqs(const swa_rotary_schedule* s, int e, double* f) {
     v = keep * v + (1 - keep) * v / s->factor;
   }
   *f = v;
-  return std::isfinite(v) && v >= 0;
+  return v >= 0 && v < 0x1p64;             // false for NaN too
+}
+
+// floor(frac(f / 2 pi) * 2^64) of the f64 f >= 0, f < 2^64, in integers: f = m 2^e with m < 2^53,
+// and m floor(2^256 / 2 pi) 2^(e - 256) is below f / 2 pi by less than 2^-192. (A quotient in f64
+// is off by 2^-53 of itself, which 2^31 positions make 2^-25 turns.)
+static uint64_t turn_fraction(double f) {
+  static const uint64_t inv[4] = {0x7f9458eaf7aef158u, 0x36d8a5664f10e410u, 0x7f09d5f47d4d3770u, 0x28be60db9391054au};
+  int e;
+  const uint64_t m = (uint64_t)std::ldexp(std::frexp(f, &e), 53);
+  uint64_t prod[5], carry = 0;             // m * inv, the lowest word first
+  for (int i = 0; i < 4; ++i) {
+    const unsigned __int128 t = (unsigned __int128)m * inv[i] + carry;
+    prod[i] = (uint64_t)t;
+    carry = (uint64_t)(t >> 64);
+  }
+  prod[4] = carry;
+  const int bit = 256 - 64 - (e - 53);     // its bit of weight 2^-64: 181 at least
+  if (bit >= 320) return 0;
+  const int w = bit >> 6, r = bit & 63;
+  return prod[w] >> r | (r && w < 4 ? prod[w + 1] << (64 - r) : 0);
 }
 
 }  // namespace swa
@@ -301,7 +321,7 @@ int swa_rotary_turns(const swa_rotary_schedule* s, double* freqs, uint64_t* turn
       !(s->orig_len > 0.0 && std::isfinite(s->orig_len) && s->high > s->low && std::isfinite(s->high) &&
         std::isfinite(s->low)))
     return SWA_E_SHAPE;
-  for (int e = 0; e < s->rot / 2; ++e) {   // nothing is written unless every frequency is finite
+  for (int e = 0; e < s->rot / 2; ++e) {   // nothing is written unless every frequency is one
     double f;
     if (!rotary_freqs(s, e, &f)) return SWA_E_SHAPE;
   }
@@ -309,11 +329,7 @@ int swa_rotary_turns(const swa_rotary_schedule* s, double* freqs, uint64_t* turn
     double f;
     rotary_freqs(s, e, &f);
     if (freqs) freqs[e] = f;
-    if (turns) {
-      const double t = f / 6.283185307179586476925;
-      // the fraction is below 1 and has at most 53 significant bits: exact in 64
-      turns[e] = (uint64_t)std::ldexp(t - std::floor(t), 64);
-    }
+    if (turns) turns[e] = turn_fraction(f);
   }
   return SWA_OK;
 }
