@@ -172,8 +172,12 @@ def rotary(x, pos, turns, *, interleaved: bool = False, inverse: bool = False, m
 
 
 def _cache(cache_k, cache_v, page_table, row_start, lens, dev):
-    """The fields of a swa_paged_cache and the capacity of a sequence."""
-    dtype, shape, pages = cache_k.dtype, cache_k.shape, page_table.shape
+    """The fields of a swa_paged_cache and the capacity of a sequence. (cache_v is cache_k where
+    the call reads no values.)"""
+    try:
+        dtype, shape, pages = cache_k.dtype, cache_k.shape, page_table.shape
+    except AttributeError:
+        raise ValueError("cache_k and page_table must be CUDA tensors") from None
     if len(shape) != 4 or dtype not in _TYPES16:
         raise ValueError("cache_k must be [num_pages][nk][page][hd] in bfloat16 or float16")
     if len(pages) != 2:
@@ -181,7 +185,7 @@ def _cache(cache_k, cache_v, page_table, row_start, lens, dev):
     num_pages, nk, page, hd = shape
     B, max_pages = pages
     k = _arg(cache_k, "cache_k", dev, dtype)
-    v = k if cache_v is None else _arg(cache_v, "cache_v", dev, dtype, shape)
+    v = k if cache_v is cache_k else _arg(cache_v, "cache_v", dev, dtype, shape)
     return (B, nk, hd, page, num_pages, max_pages, _TYPES16[dtype], k, v,
             _arg(page_table, "page_table", dev, _I32),
             0 if row_start is None else _arg(row_start, "row_start", dev, _I32, (B + 1,)),
@@ -293,7 +297,7 @@ def paged_weigh(q, lse, cache_k, page_table, row_start, lens, scale: float, *, m
     dev, on = _place(q, "q", stream)
     if on is None:
         return _there(paged_weigh, locals())
-    cache, cap = _cache(cache_k, None, page_table, row_start, lens, dev)
+    cache, cap = _cache(cache_k, cache_k, page_table, row_start, lens, dev)
     B, nk, hd = cache[:3]
     if row_start is None:
         raise ValueError("row_start is required")
