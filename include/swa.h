@@ -639,7 +639,10 @@ int swa_paged_append(const swa_paged_append_args* args, cudaStream_t stream);
  * Scores, maxima and sums are f32; the weights p enter the value product in the
  * cache's type: in calls of at most 16 query vectors a KV head and sequence
  * (min(max_rows, T) * nh / nk) as their rounding and what it leaves (relative
- * 2^-16 in bf16, 2^-22 in f16, at most), in others rounded once (2^-8, 2^-11);
+ * 2^-16 in bf16, 2^-22 in f16, at most), in others rounded once (2^-8, 2^-11).
+ * f16 has no bits below 2^-25: there each weight also loses up to 2^-40 of its
+ * row's largest, 2^-36 in the calls that run on the tensor cores' own kernel
+ * (more than 32 query vectors, 16 at hd 256, 64 with unequal rows).
  * out is rounded once. A row that sees no key gets out = 0, lse = -inf. What lies behind a sequence's last key in its pages is not used,
  * NaN and infinities included; keys that some row of the chunk sees must be
  * finite in V for the rows before them.

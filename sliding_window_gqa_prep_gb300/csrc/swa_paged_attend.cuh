@@ -31,8 +31,8 @@ struct PagedAttendParams {
 
 // Weights are 2^(s - max) times 2^kLog2 before they are rounded to T: f16 has no
 // exponents below 2^-24, and weights under it would count in the sum but not in the
-// product. Times 2^15 (the largest weight is then 2^15 < 65504) only weights below
-// 2^-40 are lost. bf16 has f32's exponents.
+// product. Times 2^15 (the largest weight is then 2^15 < 65504) a weight loses 2^-40 of the
+// largest at most. bf16 has f32's exponents.
 template <typename T>
 struct PScale {
   static constexpr float kLog2 = 0.f;

@@ -49,7 +49,7 @@ struct LazyMax {                                       // log2 of what a weight 
   static constexpr float kLazy = 8.f, kLog2 = 0.f;
 };
 template <>
-struct LazyMax<__half> {                               // 2^(4 + 11) = 2^15 < 65504; see PScale
+struct LazyMax<__half> {   // 2^(4 + 11) = 2^15 < 65504; a weight loses 2^-25 / 2^11 of the largest at most; see PScale
   static constexpr float kLazy = 4.f, kLog2 = 11.f;
 };
 

@@ -76,3 +76,45 @@ def test_weights_of_few_vectors_are_not_rounded_once(n, rows, hpg, hd, dtype):
         tol = (r + 2 * e + n * 2.0 ** -24) * absv + 2.0 ** -24 * np.abs(ref) + floor
         for h in range(hpg):
             assert (np.abs(out[i, h] - ref) <= tol).all(), np.abs(out[i, h] - ref).max()
+
+
+@pytest.mark.parametrize("dtype", [BF, HF])
+@pytest.mark.parametrize("hd", [64, 128, 256])
+@pytest.mark.parametrize("n,rows,hpg", [(300, 20, 1), (700, 8, 4), (900, 50, 2)])   # 20, 32 and 100 vectors
+def test_weights_of_many_vectors_are_rounded_once(n, rows, hpg, hd, dtype):
+    g = torch.Generator().manual_seed(n + hd)
+    scores, v = torch.randn(n, generator=g), torch.randn(n, hd, generator=g)
+    out, s, v = scored(scores, rows, hpg, hd, dtype, v)
+    e = 2.0 ** -22 * np.abs(s).max() + 2.0 ** -20
+    for i in range(rows):
+        ref, absv = reference(s, v, n - rows + i + 1)
+        # f16 has no bits below 2^-25, of a largest weight of 2^11 or 2^15
+        floor = n * 2.0 ** -36 * np.abs(v).max() if dtype == HF else 0.0
+        tol = (torch.finfo(dtype).eps / 2 + 2 * e + n * 2.0 ** -24) * absv + 2.0 ** -24 * np.abs(ref) + floor
+        for h in range(hpg):
+            assert (np.abs(out[i, h] - ref) <= tol).all(), np.abs(out[i, h] - ref).max()
+
+
+# log2 e * 1419 / 512 = 3.9984 and * 1420 / 512 = 4.0012: the tensor-core kernel's f16 form raises
+# its running maximum for a tile whose maximum is 2^4 times the last one or more
+@pytest.mark.parametrize("peaks", [
+    {3: 0.0}, {5000: 0.0}, {3: -1419 / 512, 5000: 0.0}, {3: -1420 / 512, 5000: 0.0},
+    {3: -8.0, 700: -1420 / 512, 5000: 0.0}, {3: 0.0, 5000: -1420 / 512},
+])
+@pytest.mark.parametrize("hd", [64, 128, 256])
+@pytest.mark.parametrize("rows,wide", [(1, None), (40, None), (150, None), (150, 2048)])
+def test_f16_small_weights_count(rows, wide, hd, peaks):
+    """8192 keys, nearly all at 3e-7 of the largest weight: a quarter of a percent together, which
+    must not vanish from the product where it counts in the sum."""
+    n = 8192
+    scores, v = torch.full((n,), -15.0), torch.ones(n, hd)
+    for j, x in peaks.items():
+        scores[j], v[j] = x, -1.0
+    out, s, v = scored(scores, rows, 1, hd, HF, v, max_pages=wide)
+    e = 2.0 ** -22 * np.abs(s).max() + 2.0 ** -20
+    for i in (0, rows // 2, rows - 1):
+        ref, absv = reference(s, v, n - rows + i + 1)
+        tol = (2.0 ** -11 + 2 * e + n * 2.0 ** -24) * absv + 2.0 ** -24 * np.abs(ref) + n * 2.0 ** -36
+        assert (np.abs(out[i, 0] - ref) <= tol).all(), np.abs(out[i, 0] - ref).max()
+        # the peaks alone would give -1
+        assert (ref > -1 + 4e-3).all()
