@@ -135,7 +135,7 @@ __global__ void __launch_bounds__(SplitCfg<D>::THREADS)
   // with unequal rows and 20 % in a call that mixes 63 tokens with a prompt.
   constexpr bool REST = ROWS == 16;
   extern __shared__ unsigned char sm_raw[];
-  __shared__ __align__(8) uint64_t b_full[ST], b_empty[ST];
+  __shared__ __align__(8) uint64_t b_full[ST], b_empty[ST];   // modelled in tests/test_paged_barriers_cpu.py
   __shared__ long long s_scan[NWARPS];
   __shared__ long long s_off, s_total;
   __shared__ int s_b, s_abort;

@@ -80,6 +80,8 @@ __global__ void __launch_bounds__(ChunkCfg<D>::THREADS, 1)
   constexpr int NT = C::NT, SB = C::SB, KT = C::KT, NS = C::NS;
   constexpr bool BF = std::is_same<T, __nv_bfloat16>::value;
   extern __shared__ unsigned char sm_raw[];
+  // tests/test_paged_barriers_cpu.py runs the roles below on a model of these barriers: what waits
+  // or arrives here has to be changed there too
   __shared__ __align__(8) uint64_t b_full[NS], b_empty[NS], b_q[NT], b_s[NT * SB], b_p[NT * SB][2], b_pv[NT], b_fin[NT], b_turn[NT], b_tail;
   __shared__ uint32_t s_tmem;
   __shared__ int s_abort, s_b, s_idx;

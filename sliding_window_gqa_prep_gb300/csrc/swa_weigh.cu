@@ -149,6 +149,8 @@ __global__ void __launch_bounds__(kWeighThreads, 1)
   constexpr int QN = C::QN, NS = C::NS, NSH = C::NSH, CH = D / 8;
   constexpr bool BF = std::is_same<T, __nv_bfloat16>::value;
   extern __shared__ unsigned char sm_raw[];
+  // tests/test_paged_barriers_cpu.py runs the roles below on a model of these barriers: what waits
+  // or arrives here has to be changed there too
   __shared__ __align__(8) uint64_t b_kfull[NS], b_kempty[NS], b_qfull[2], b_qempty[2], b_s[4], b_sfree[4], b_fin[2];
   // lse and limits have a ring of their own: a query tile's slot is free once its products are
   // done, while they are needed until its sums are
