@@ -31,14 +31,20 @@ inline bool aligned16p(const void* p) { return (reinterpret_cast<uintptr_t>(p) &
 inline size_t up256s(size_t x) { return (x + 255) & ~(size_t)255; }
 
 // Dynamic shared memory of a kernel, allowed once per device (an attribute call costs as
-// much host time as the rest of a launch's preparation).
+// much host time as the rest of a launch's preparation). With min_regs the kernel has to have been
+// compiled to that many registers a thread.
 template <auto Kernel>
-cudaError_t allow_smem(int bytes) {
+cudaError_t allow_smem(int bytes, int min_regs = 0) {
   static bool done[64] = {};
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
   if (dev >= 0 && dev < 64 && done[dev]) return cudaSuccess;
+  if (min_regs) {
+    cudaFuncAttributes fa;
+    if ((e = cudaFuncGetAttributes(&fa, Kernel)) != cudaSuccess) return e;
+    if (fa.numRegs < min_regs) return cudaErrorLaunchOutOfResources;
+  }
   e = cudaFuncSetAttribute(Kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
   if (e == cudaSuccess && dev >= 0 && dev < 64) done[dev] = true;
   return e;

@@ -41,6 +41,10 @@ struct ChunkCfg {
   static constexpr int QB = 128 * D * 2;               // bytes of a query tile
   static constexpr int THREADS = NT * 128 + 128;       // softmax warpgroups; loader, issuers, idle warps
   static constexpr int SMEM = NT * QB + NS * SLOT + 1024;   // + alignment
+  // Registers a thread: at launch, and after they moved over to the softmax threads (two tiles).
+  // They move inside what the CTA was launched with: shares that are more than that wait for ever.
+  static constexpr int REGS = NT == 2 ? 168 : 0, R_SOFT = 216, R_REST = 72;
+  static_assert(NT == 1 || NT * 128 * R_SOFT + 128 * R_REST <= THREADS * REGS, "registers of a CTA");
   static constexpr int C_O = NT * SB * KT;             // first O column
 };
 constexpr int kSortSeqs = 64;            // sequences of a call up to which they are taken longest first
@@ -228,10 +232,9 @@ __global__ void __launch_bounds__(ChunkCfg<D>::THREADS, 1)
     return __all_sync(0xffffffffu, tc_wait(bar, (uint32_t)(phase & 1), &s_abort));
   };
 
-  // The softmax threads hold a row of S: registers move over to them (384 threads are
-  // launched with 168 each: 2 * 128 * 216 + 128 * 72 = 384 * 168).
+  // The softmax threads hold a row of S: registers move over to them.
   if (warp >= W_LOAD) {
-  if constexpr (NT == 2) asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
+  if constexpr (NT == 2) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" :: "n"(C::R_REST));
   if (warp == W_LOAD) {
     // ------------------------------------------------------------ loader
     // a slot is boxes of `rows` keys x 64 features
@@ -400,7 +403,7 @@ __global__ void __launch_bounds__(ChunkCfg<D>::THREADS, 1)
   }
   } else {
     // ------------------------------------------------------------ softmax: thread = row
-    if constexpr (NT == 2) asm volatile("setmaxnreg.inc.sync.aligned.u32 216;");
+    if constexpr (NT == 2) asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" :: "n"(C::R_SOFT));
     const int t = warp >> 2, r = tid & 127, hpg = a.hpg;
     const int first = tok0 + t * p.tile_tok;
     const int ntok = max(0, min(p.tile_tok, s.t - first)), nvec = ntok * hpg;
@@ -633,7 +636,7 @@ static int launch(const swa_paged_attend_args* a, const PagedAttendParams& ap, c
   p.rec_acc = reinterpret_cast<float*>(ws);
   p.rec_ml = reinterpret_cast<float2*>(ws + pl.off_ml);
   p.rec_desc = reinterpret_cast<int4*>(ws + pl.off_desc);
-  const cudaError_t e = allow_smem<paged_chunk_kernel<T, D>>(ChunkCfg<D>::SMEM);
+  const cudaError_t e = allow_smem<paged_chunk_kernel<T, D>>(ChunkCfg<D>::SMEM, ChunkCfg<D>::REGS);
   if (e != cudaSuccess) return cuda_status(e);
   rc = finish_launch(launch_pdl(paged_chunk_kernel<T, D>, dim3((unsigned)pl.items, pl.splits), dim3(ChunkCfg<D>::THREADS),
                                 ChunkCfg<D>::SMEM, s, mk, mv, p));

@@ -42,3 +42,17 @@ def test_the_wrappers_are_what_the_kernels_use(name):
         with open(os.path.join(CSRC, f)) as h:
             n += h.read().count(name + (";" if name.startswith("grid") else "."))
     assert n == 1
+
+
+def test_register_shares_are_checked():
+    """Registers that setmaxnreg hands out come from what the CTA was launched with. The shares stand
+    against the launch's at compile time, and the compiler's count is checked before the first launch:
+    a build with fewer (other flags, another compiler) is an error, not a hang."""
+    users = [f for f in sorted(os.listdir(CSRC)) if "setmaxnreg." in open(os.path.join(CSRC, f)).read()]
+    assert users == ["swa_paged_chunk.cu"]
+    with open(os.path.join(CSRC, users[0])) as h:
+        s = h.read()
+    assert re.search(r"static_assert\([^;]*R_SOFT[^;]*R_REST[^;]*THREADS \* REGS", s)
+    assert 'setmaxnreg.dec.sync.aligned.u32 %0;" :: "n"(C::R_REST)' in s
+    assert 'setmaxnreg.inc.sync.aligned.u32 %0;" :: "n"(C::R_SOFT)' in s
+    assert re.search(r"allow_smem<paged_chunk_kernel<T, D>>\([^;]*ChunkCfg<D>::REGS\)", s)
