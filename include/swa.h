@@ -743,6 +743,7 @@ typedef struct swa_paged_evict_args {
   size_t workspace_bytes;
   uint32_t* err;
 } swa_paged_evict_args;
+/* Bytes of workspace for these sizes (0: invalid sizes). */
 size_t swa_paged_evict_workspace_size(const swa_paged_evict_args* args);
 int swa_paged_evict(const swa_paged_evict_args* args, cudaStream_t stream);
 

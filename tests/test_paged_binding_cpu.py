@@ -3,6 +3,7 @@
 import pytest
 import torch
 
+import sliding_window_gqa_prep_gb300 as swa
 from sliding_window_gqa_prep_gb300 import paged
 
 CPU = -1
@@ -39,3 +40,11 @@ def test_what_is_no_tensor_is_refused(which):
         a[which] = None
     with pytest.raises(ValueError):
         paged._cache(*a, CPU)
+
+
+def test_evict_workspace_of_sizes_past_the_limit():
+    """B * nk <= 2^24, as the call has it: beyond, the bytes passed 64 bits and came out as few."""
+    assert swa.paged_evict_workspace_size(65535, 256, 16, 1 << 26, 1 << 30) == 65535 * 256 * (1 << 30) * 24
+    for b, nk in ((65535, 257), (65535, 65535), (0, 1)):
+        with pytest.raises(swa.SwaError):
+            swa.paged_evict_workspace_size(b, nk, 16, 1 << 26, 1 << 30)
