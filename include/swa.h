@@ -513,9 +513,10 @@ int swa_flash(const swa_flash_args* args, cudaStream_t stream);
  *   lens       [B] i32: keys each sequence holds, the chunk's own rows among
  *              them. Row i of a chunk of t_b rows has slot lens[b] - t_b + i.
  *   B          1 .. 65535; nk 1 .. 65535; B * nk <= 2^24.
- * On the device, a length outside 0 .. cap is clamped (SWA_DERR_META), a
- * sequence with rows out of range is skipped (SWA_DERR_SEGMENT), and pages out
- * of range are reported (SWA_DERR_PAGE); every access stays in bounds.
+ * On the device, a length outside 0 .. cap is clamped (SWA_DERR_META;
+ * swa_paged_append stores nothing of such a sequence), a sequence with rows out
+ * of range is skipped (SWA_DERR_SEGMENT), and pages out of range are reported
+ * (SWA_DERR_PAGE); every access stays in bounds.
  */
 typedef struct swa_paged_cache {
   int B, nk, hd, page, num_pages, max_pages, dtype;

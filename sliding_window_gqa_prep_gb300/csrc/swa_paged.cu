@@ -13,8 +13,8 @@
 // that lies whole in one CTA is finished there; one that is cut leaves a
 // record (m, l, sum p v) per CTA, joined by paged_merge_kernel.
 // Measured, one token a sequence: 64 sequences of 1024 to 8192 keys, 16 query heads on 4,
-// hd 128, bf16: 98 us, 6.0 TB/s; 16 of 32768 to 131072 keys, 8 heads on 2, hd 256, f16:
-// 411 us, 7.0 TB/s (ncu: 87 % of the DRAM's peak, 1.001 times the bytes of K and V).
+// hd 128, bf16: 99 us, 6.0 TB/s; 16 of 32768 to 131072 keys, 8 heads on 2, hd 256, f16:
+// 410 us, 7.0 TB/s (ncu: 89 % of the DRAM's peak, 1.001 times the bytes of K and V).
 #include <cmath>
 
 #include "swa_mma16.cuh"
@@ -537,16 +537,21 @@ __global__ void __launch_bounds__(kMergeThreads) paged_merge_kernel(const PagedA
 // to the tensor-core kernel (swa_paged_chunk.cu). 32 sequences of 2048 keys, 8 KV heads, split and
 // tensor-core kernel: 32 vectors at hd 64 45 and 45 us, at hd 128 64 and 56, 48 vectors 59 and 45,
 // 82 and 57; at hd 256 20 vectors 155 and 93 us. One sequence of 32768 keys, 32 vectors: hd 64 30
-// and 32 us, hd 128 41 and 45; 8 ragged ones: 24 and 26, 29 and 30. Where sequences have unequal
+// and 32 us, hd 128 41 and 45; 8 ragged ones: 24 and 26, 29 and 30. So at hd 128 the rule costs a
+// batch of 17 to 32 vectors an eighth and gains a single sequence a tenth: it does not look at the
+// batch, because the lengths that would tell are the device's. Where sequences have unequal
 // rows (B * max_rows > T) both kernels may have to run, one after the other, so up to 64 stay with
 // one: 26 sequences of up to 22 rows over 18 to 4453 keys, 6 heads on 3, hd 128: 48 instead of 75 us
 // (hd 256, 8 of up to 29 rows over 323 to 15713 keys: 99 instead of 56, so 16 there all the same).
+// The block is then 64 vectors wide for single tokens too: 63 of them and a prompt of 512 rows, over
+// 4096 keys each, 32 heads on 8, hd 128, take 286 us, apart 187 and 45.
 static int split_vecs(const swa_paged_attend_args* a, int max_rows) {
   return a->cache.hd == 256 ? 16 : (long long)a->cache.B * max_rows > a->T ? 64 : 32;
 }
 
 // Keys of a sequence up to which a CTA takes a (sequence, KV head) whole: no scan over the
-// sequences and no second kernel.
+// sequences and no second kernel. By the table's width, since the lengths are the device's: one
+// token over 133 keys takes 10.3 us in a table of 144 and 14.7 in one of 4608.
 constexpr int kWholeKeys = 512;
 
 struct SplitPlan {
@@ -690,7 +695,7 @@ int swa_paged_attend(const swa_paged_attend_args* a, cudaStream_t stream) {
   p.T = a->T; p.nh = a->nh; p.hpg = a->nh / c.nk; p.max_rows = a->max_rows < a->T ? a->max_rows : a->T;
   p.most = pl.most;
   p.qmul = a->scale * 1.4426950408889634f;
-  p.q = a->q; p.q_row = a->q_row; p.ck = c.k; p.cv = c.v;
+  p.q = a->q; p.q_row = a->q_row;
   p.out = a->out; p.out_f32 = a->out_f32 != 0; p.lse = a->lse;
   p.err = a->err;
   char* ws = static_cast<char*>(a->workspace);

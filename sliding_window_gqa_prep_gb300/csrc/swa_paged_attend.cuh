@@ -18,8 +18,6 @@ struct PagedAttendParams {
   float qmul;                  // scale * log2(e): scores in log2 units
   const void* q;
   long long q_row;
-  const void* ck;
-  const void* cv;
   void* out;
   int out_f32;
   float* lse;

@@ -3,9 +3,10 @@
 //
 // Work item: NT tiles of 128 query vectors (rows x heads of one KV head) of one
 // sequence. S = Q K^T and O += P V per tile of KT keys are both matrix products with
-// 128 rows; between them stand 128 x KT exponentials, which at hd 128 take the 16 / clk
-// of an SM's special-function units as long as the two products take its tensor core
-// (4 * 128 * 128 * 128 / 8192 = 1024 clk each). So both must run all the time:
+// 128 rows; between them stand 128 x KT exponentials. At hd 128 the two products take an SM's
+// tensor core 4 * 128 * 128 * 128 / 8192 = 1024 clk, and the exponentials, at 32 a clk, half of
+// that. One tile's chain of S, softmax and P V would leave the tensor core idle for as long as the
+// softmax takes, so something else has to run under it:
 //   - hd 64 and 128: two tiles (NT = 2), each with its own softmax warpgroup and its
 //     own issuing warp, share every K and V tile; while one tile is in its softmax the
 //     tensor core works for the other. TMEM: S 2 x 128 and O 2 x hd columns.
@@ -20,11 +21,15 @@
 // Few items are split over the keys: grid.y shares of an item's tiles leave records
 // that chunk_merge_kernel joins.
 // Measured: four sequences of 2048 rows behind 6144 keys, 32 query heads on 8, hd 128, bf16:
-// 646 us, 1490 TFLOP/s; ragged ones of 1024 to 2048 rows over 2048 to 16384 keys: 526 us,
-// 1399 TFLOP/s (ncu: tensor pipe 64 %, special functions 32 %). What is left is the chain
+// 646 us, 1490 TFLOP/s; ragged ones of 1024 to 2048 rows over 2048 to 16384 keys: 523 us,
+// 1410 TFLOP/s (ncu: tensor pipe 64 %, special functions 32 %, issue 37 %). What is left is the chain
 // S -> softmax -> P V -> S of a tile: about 330 clk from the last product issued to the
-// barrier seen, twice a step, and P V before the S that overwrites P. hd 64: 940 TFLOP/s,
-// the same chain for half the products; hd 256: 1057, every 128 query vectors read K and V.
+// barrier seen, twice a step, and P V before the S that overwrites P. Four of 1024 to 2048 rows over
+// 8192 keys: hd 64 880 TFLOP/s, the same chain for half the products; hd 256 1180, every 128 query
+// vectors read K and V.
+// The weights are rounded to T once, which with T's own rounding of the result makes it 1.35 times as
+// inexact as 32-bit weights would (bf16: 0.0023 and 0.0017 of its norm). What the rounding leaves
+// would take a second P V, half as many products again.
 #include <cmath>
 
 #include "swa_paged_tc.cuh"
@@ -604,8 +609,12 @@ ChunkPlan chunk_plan(const swa_paged_attend_args* a, int max_rows) {
   // one sequence of max_rows rows has no more items than its rows need
   const long long most = (max_rows + item_tok - 1) / item_tok * c.B * c.nk;
   if (most < pl.items) pl.items = most;
-  // fewer items than SMs: cut the keys, at least four tiles a share (with twice as many shares, for
-  // even ends: 80 instead of 50 us for 256 rows over 32768 keys, 8 heads on 2, hd 128)
+  // Fewer items than SMs: cut the keys, at least four tiles a share of a sequence as long as the
+  // table is wide (with twice as many shares, for even ends: 80 instead of 50 us for 256 rows over
+  // 32768 keys, 8 heads on 2, hd 128). The lengths and the rows of each sequence are the device's, so
+  // what is counted here are bounds: a short sequence in a wide table is cut finer than pays (256 rows
+  // over 512 keys, 8 heads on 2: 18.4 us in a table of 512, 25 in one of 32768), and single tokens in
+  // the same call count as items (256 rows and 31 tokens over 16384 keys: 229 us, 43 and 107 apart).
   const long long sms = num_sms() > 0 ? num_sms() : 148;
   const long long tiles = ((long long)c.max_pages * c.page + kt - 1) / kt;
   long long sp = sms / pl.items;

@@ -18,14 +18,17 @@
 // unit. The sums run in a fixed order: no atomics.
 // Measured: one token of 64 sequences of 2048 to 4160 keys, 16 query heads on 4, hd 128: 37 us,
 // 5.5 TB/s of K and weights. The last 32 to 64 rows of four prompts of 16384 to 32768 keys, 32
-// heads on 8: 46 us (4.1 TB/s, 720 TFLOP/s), bound by the sums' latencies: 128 columns take a
-// warpgroup 1650 clk, 1024 of them exponentials at the special functions' rate (ncu: these and
-// the tensor pipe 35 % each, issue 40 %). Tried: four warpgroups of sums (54 us when this took
-// 51), K called into L2 ahead (54 for 51), the next 32 columns of S loaded while 32 are summed
-// (53 for 51: S is freed later), 128 columns in registers (61: spills), a key of each half a
-// thread over half of the columns, with one lse for both (51 for 46). All rows of prompts of 2048
-// rows over 4096 to 8192 keys, four of them, 32 heads on 8, hd 128: 324 us, 855 TFLOP/s; 8 of 512
-// rows, 32 heads on 4, hd 64: 180 us, 445 TFLOP/s.
+// heads on 8: 46.7 us (4.0 TB/s, 705 TFLOP/s). Of a CTA's 80 thousand clk, stamped: 13.7 until its
+// first S (4.5 its share, 1.6 to the first K asked for, 7.6 that K and the pair of query tiles), then
+// 36 tiles: 48.3 the sums (1700 for 128 columns, both warpgroups at once, 1024 of them exponentials
+// at the special functions' rate), 5.2 the waits for S, 12.7 the turns between (weights stored, the
+// next unit found); K is hardly waited for (2.8, under the sums). ncu: special functions and tensor
+// pipe 28 % each, issue 37 %. Of one token's 65 thousand clk 28.8 wait for K. Tried: four warpgroups
+// of sums (54 us when this took 51), K called into L2 ahead (54 for 51), the next 32 columns of S
+// loaded while 32 are summed (53 for 51: S is freed later), 128 columns in registers (61: spills), a
+// key of each half a thread over half of the columns, with one lse for both (51 for 46). All rows of
+// prompts of 2048 rows over 4096 to 8192 keys, four of them, 32 heads on 8, hd 128: 327 us, 848
+// TFLOP/s; 8 of 512 rows, 32 heads on 4, hd 64: 180 us, 445 TFLOP/s.
 #include <cmath>
 
 #include "swa_paged_tc.cuh"
