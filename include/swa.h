@@ -644,9 +644,10 @@ int swa_paged_append(const swa_paged_append_args* args, cudaStream_t stream);
  * f16 has no bits below 2^-25: there each weight also loses up to 2^-40 of its
  * row's largest, 2^-36 in the calls that run on the tensor cores' own kernel
  * (more than 32 query vectors, 16 at hd 256, 64 with unequal rows).
- * out is rounded once. A row that sees no key gets out = 0, lse = -inf. What lies behind a sequence's last key in its pages is not used,
- * NaN and infinities included; keys that some row of the chunk sees must be
- * finite in V for the rows before them.
+ * out is rounded once. A row that sees no key gets out = 0, lse = -inf. What
+ * lies behind a sequence's last key in its pages is not used, NaN and infinities
+ * included; keys that some row of the chunk sees must be finite in V for the
+ * rows before them.
  *   q    [T][nh][hd] of the cache's type, rows q_row elements apart (heads
  *        dense, rows at multiples of 16 bytes); nh / nk <= 32
  *   out  [T][nh][hd] dense, of the cache's type, or f32 with out_f32 = 1

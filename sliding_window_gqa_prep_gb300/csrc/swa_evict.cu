@@ -389,9 +389,9 @@ static size_t evict_list_cap(const swa_paged_evict_args* a) {
 }
 static bool evict_sizes_ok(const swa_paged_evict_args* a) {
   const swa_paged_cache& c = a->cache;
-  return c.B >= 1 && c.B <= 65535 && c.nk >= 1 && c.nk <= 65535 && (long long)c.B * c.nk <= (1 << 24) && c.page >= 16 && c.page <= 256 &&
-         (c.page & (c.page - 1)) == 0 && c.max_pages >= 1 && c.max_pages <= (1 << 30) / c.page && a->keep >= 1 &&
-         a->sinks >= 0;
+  return c.B >= 1 && c.B <= 65535 && c.nk >= 1 && c.nk <= 65535 && (long long)c.B * c.nk <= (1 << 24) &&
+         c.page >= 16 && c.page <= 256 && (c.page & (c.page - 1)) == 0 && c.max_pages >= 1 &&
+         c.max_pages <= (1 << 30) / c.page && a->keep >= 1 && a->sinks >= 0;
 }
 
 }  // namespace swa
