@@ -61,6 +61,8 @@ extern "C" {
 #define SWA_DERR_PAGE     8u /* paged calls: a page table entry names no page of
                                 the pool (its keys are read as zeros, its slots
                                 are not written) */
+#define SWA_DERR_FULL    16u /* swa_paged_fork: not enough free pages (the entries
+                                that lack one are -1) */
 
 /* Per-sequence ring state, as the per-group meta of o1c_msl.metal:
  *   win_len  — keys held in the ring (<= window)
@@ -748,6 +750,241 @@ typedef struct swa_paged_evict_args {
 /* Bytes of workspace for these sizes (0: invalid sizes). */
 size_t swa_paged_evict_workspace_size(const swa_paged_evict_args* args);
 int swa_paged_evict(const swa_paged_evict_args* args, cudaStream_t stream);
+
+/*
+ * ---------------------------------------------------------------------------
+ * The paged cache in 4 bits. A block of 16 features of a key or value holds 16
+ * codes and one scale: a value is level(code) * scale * 2^exp with
+ *   level  0, 0.5, 1, 1.5, 2, 3, 4, 6 for the code's lower three bits, negative
+ *          with bit 3 set (e2m1)
+ *   scale  e4m3 without sign (0 .. 448, 2^-9 apart at the lower end; 0x7f: NaN)
+ *   exp    one whole number for all keys, one for all values of the cache
+ * so that a key takes 4.5 bits a feature. A value has six significant bits at
+ * most: bf16 holds it, and f16 where 2^exp keeps it in range. Encoding takes
+ * scale = max|x| / (6 * 2^exp) of the block, rounded to the nearest e4m3 (ties
+ * to the even one, 448 at most), and for each x the nearest of level * scale *
+ * 2^exp (ties to the even code, 6 at most). A block whose scale rounds to 0 has
+ * codes 0; a block with an infinity or NaN has scale NaN and codes 0, and reads
+ * as NaN. exp moves the range (2^-9 to 448, times 6) to where the tensor's values
+ * are: with exp = 0 blocks whose largest value is below 0.09 lose bits of their
+ * scale.
+ *   k, v        [num_pages][nk][page][hd / 2] bytes: feature 2i in the lower half
+ *               of byte i, 2i + 1 in the upper one; 16-byte aligned
+ *   k_scale, v_scale  [num_pages][nk][page][hd / 16] bytes, 16-byte aligned
+ *   k_exp, v_exp      -32 .. 32
+ * Everything else as in swa_paged_cache.
+ * ---------------------------------------------------------------------------
+ */
+typedef struct swa_paged4_cache {
+  int B, nk, hd, page, num_pages, max_pages, k_exp, v_exp;
+  void* k;
+  void* k_scale;
+  void* v;
+  void* v_scale;
+  const int32_t* table;
+  const int32_t* row_start;
+  const int32_t* lens;
+} swa_paged4_cache;
+
+/*
+ * swa_paged4_append — the chunk's rows enter the 4-bit cache: k is rotated (as
+ * by swa_rotary, when rot > 0) and encoded, v encoded, at each row's slot; q,
+ * when given, is rotated and rounded to q_dtype. One launch. What is stored is
+ * the encoding of the rotated key itself, not of its rounding: where arithmetic
+ * in f32 does not settle a scale or a code, the row's angles are taken in f64.
+ *   k, v  [T][nk][hd], q [T][nh][hd] with row strides k_row, v_row, q_row in
+ *         elements (heads dense), of type src (SWA_F32, SWA_BF16, SWA_F16); rows
+ *         at multiples of 16 bytes
+ *   q_out [T][nh][hd] dense, of type q_dtype (SWA_BF16 or SWA_F16; required with
+ *         q); must not overlap k, v, or q unless it is q itself, of the same type
+ *         and dense
+ *   pos, turns, rot, interleaved, mag   as swa_paged_append
+ * The four pools must not overlap each other (SWA_E_SHAPE); the rows must not
+ * lie in them (not checked). Rows whose slot is below 0 set SWA_DERR_META and are
+ * not stored (their q is).
+ * Errors: SWA_E_NULL, SWA_E_SHAPE, SWA_E_ALIGN, SWA_E_CUDA.
+ */
+typedef struct swa_paged4_append_args {
+  swa_paged4_cache cache;
+  int T, nh, rot, src, q_dtype, interleaved;
+  float mag;
+  const void* q;
+  const void* k;
+  const void* v;
+  long long q_row, k_row, v_row;
+  void* q_out;
+  const int32_t* pos;
+  const uint64_t* turns;
+  uint32_t* err;
+} swa_paged4_append_args;
+int swa_paged4_append(const swa_paged4_append_args* args, cudaStream_t stream);
+
+/*
+ * swa_paged4_read — the last rows of every sequence as the cache holds them: row
+ * i of the t_b packed rows of sequence b gets the values of slot lens[b] - t_b +
+ * i (the slots that swa_paged4_append of the same row_start and lens wrote; the
+ * whole sequence with t_b = lens[b]).
+ *   k_out, v_out  [T][nk][hd] dense, of type dtype (SWA_F32, SWA_BF16, SWA_F16),
+ *                 16-byte aligned; one of them may be NULL; they must not overlap
+ *                 each other or the pools
+ * f32 and bf16 hold every value, f16 those within its range (others round). Rows
+ * of a slot below 0 (SWA_DERR_META) or in no page of the pool (SWA_DERR_PAGE) are
+ * zeros; rows of no sequence are left as they were.
+ * Errors: SWA_E_NULL, SWA_E_SHAPE, SWA_E_ALIGN, SWA_E_CUDA.
+ */
+typedef struct swa_paged4_read_args {
+  swa_paged4_cache cache;
+  int T, dtype;
+  void* k_out;
+  void* v_out;
+  uint32_t* err;
+} swa_paged4_read_args;
+int swa_paged4_read(const swa_paged4_read_args* args, cudaStream_t stream);
+
+/*
+ * swa_paged4_attend — causal attention of a chunk's rows over the 4-bit cache
+ * (their own keys already appended), as swa_paged_attend. With window > 0 row i
+ * of sequence b, whose own slot is p = lens[b] - t_b + i, sees of the slots 0 .. p
+ * those from p - window + 1 on (its own and window - 1 before it) and those below
+ * sinks; with window = 0 all of them (sinks is then not read). Slots that no row
+ * of a sequence sees are not used, NaN among them; keys that some row of the chunk
+ * sees must be finite in V for the other rows of its sequence.
+ * Keys and values enter the products exactly; q is scaled by a power of two a
+ * vector and rounded to f16 (bf16 and f16 values keep all bits down to 2^-39 of
+ * the vector's largest); scores, maxima and sums are f32; the weights enter the
+ * value product in f16, rounded once (relative 2^-11; below 2^-24 of the row's
+ * scale to a multiple of 2^-40 of it).
+ *   q    [T][nh][hd] of type q_dtype (SWA_BF16 or SWA_F16), rows q_row elements
+ *        apart (heads dense, rows at multiples of 16 bytes); nh / nk <= 32
+ *   out  [T][nh][hd] dense, of q's type, or f32 with out_f32 = 1
+ *   everything else as swa_paged_attend
+ * The result does not depend on timing: the same call gives the same bits.
+ * Errors: SWA_E_NULL, SWA_E_SHAPE (also window < 0, sinks < 0), SWA_E_ALIGN,
+ * SWA_E_WORKSPACE, SWA_E_CUDA. T = 0: nothing is launched.
+ */
+typedef struct swa_paged4_attend_args {
+  swa_paged4_cache cache;
+  int T, nh, max_rows, window, sinks, q_dtype, out_f32;
+  float scale;
+  const void* q;
+  long long q_row;
+  void* out;
+  float* lse;
+  void* workspace;
+  size_t workspace_bytes;
+  uint32_t* err;
+  cudaEvent_t ev_start, ev_stop;
+} swa_paged4_attend_args;
+/* Bytes of workspace for these sizes (0: invalid sizes; 1: none is needed, the
+ * workspace may be NULL). Queries the current device's SM count on first use. */
+size_t swa_paged4_attend_workspace_size(const swa_paged4_attend_args* args);
+int swa_paged4_attend(const swa_paged4_attend_args* args, cudaStream_t stream);
+
+/*
+ * ---------------------------------------------------------------------------
+ * Pages that sequences share, of any paged cache (4 or 16 bits). A page has as
+ * many holders as table entries name it, and those the caller adds (a prefix kept
+ * for later requests): refs [num_pages] i32 counts them, 0 is a free page. Table
+ * rows list a sequence's pages from the front; entries outside 0 .. num_pages - 1
+ * (-1) hold nothing.
+ *   pools   up to 8 arrays of num_pages pages of page_bytes[i] bytes each
+ *           (16-byte aligned, page_bytes a multiple of 16): K, V and their scales.
+ *           They must not overlap each other.
+ * ---------------------------------------------------------------------------
+ */
+#define SWA_MAX_POOLS 8
+typedef struct swa_page_pools {
+  int num_pages, pools;
+  void* base[SWA_MAX_POOLS];
+  long long page_bytes[SWA_MAX_POOLS];
+} swa_page_pools;
+
+/*
+ * swa_paged_fork — from one batch's tables to the next one's: sequences continue,
+ * branch, end and begin. New sequence r (of R) continues old sequence parent[r],
+ * with its length, or starts empty (parent[r] = -1). In this order:
+ *   1. every entry of the old table (B rows) lets go of its page;
+ *   2. the new rows hold the pages of their parents' keys (ceil(len / page) of
+ *      them; pages that a parent held behind its last key are let go);
+ *   3. a page that a new sequence writes next (the one of slot len, where len is
+ *      no multiple of page) and that has other holders is replaced by a copy, its
+ *      bytes in all pools; if every holder is a new sequence that would write it,
+ *      the first of them keeps the page itself;
+ *   4. each new sequence gets pages until it has room for room[r] slots behind
+ *      its length (NULL: none).
+ * Pages for 3 and 4 are the free ones (refs 0 after step 2), lowest first, to the
+ * sequences in order, a sequence's copy before its room. Freed pages are not
+ * cleared. Where the pages run out the entries that lack one are -1 and
+ * SWA_DERR_FULL is set; what is there is consistent.
+ *   table [B][max_pages], lens [B] i32: the old batch (lengths outside 0 ..
+ *         max_pages * page are clamped, SWA_DERR_META)
+ *   parent [R], room [R] or NULL i32: a parent outside -1 .. B - 1 is taken as -1,
+ *         room below 0 as 0, room past the table's width as that (SWA_DERR_META)
+ *   refs [num_pages] i32; refs_out may be refs itself. A count that falls below 0
+ *         is no free page (SWA_DERR_META). An entry of the old table that should
+ *         hold a key's page and names none is passed on as -1 (SWA_DERR_PAGE).
+ *   table_out [R][max_pages], lens_out [R], refs_out [num_pages] i32
+ *   left  [1] i32: free pages afterwards; below 0: as many were lacking
+ *   page  slots of a page, a power of two, 16 .. 256
+ *   workspace  swa_paged_fork_workspace_size(args) bytes, 256-byte aligned, no
+ *         initial contents needed, not shared by calls that overlap on the GPU
+ * The outputs must not overlap the inputs (refs apart), each other or the
+ * workspace (SWA_E_SHAPE). B, R 1 .. 65535, num_pages < 2^30, max_pages * page <=
+ * 2^30, B * max_pages and R * max_pages < 2^31. Repeating the call on the same
+ * inputs (refs_out apart from refs) gives the same outputs: pages that are copied
+ * are held, and copies go to free ones.
+ * Errors: SWA_E_NULL, SWA_E_SHAPE, SWA_E_ALIGN, SWA_E_WORKSPACE, SWA_E_CUDA.
+ */
+typedef struct swa_paged_fork_args {
+  swa_page_pools pools;
+  int B, R, page, max_pages;
+  const int32_t* table;
+  const int32_t* lens;
+  const int32_t* parent;
+  const int32_t* room;
+  const int32_t* refs;
+  int32_t* table_out;
+  int32_t* lens_out;
+  int32_t* refs_out;
+  int32_t* left;
+  void* workspace;
+  size_t workspace_bytes;
+  uint32_t* err;
+} swa_paged_fork_args;
+/* Bytes of workspace for these sizes (0: invalid sizes). */
+size_t swa_paged_fork_workspace_size(const swa_paged_fork_args* args);
+int swa_paged_fork(const swa_paged_fork_args* args, cudaStream_t stream);
+
+/*
+ * swa_paged_compact — the pages in use move to the front of the pools: with n
+ * pages of refs > 0, the i-th of them from page n on (ascending) moves to the i-th
+ * free page below n, in all pools; the others stay.
+ *   table [B][max_pages], refs [num_pages] i32; table_out and refs_out the same
+ *         afterwards (each may be its input itself). An entry that names a free
+ *         page becomes -1 (SWA_DERR_PAGE); entries that hold nothing stay.
+ *   moved [num_pages] i32: the new place of every page in use, -1 for free ones
+ *         (for holders outside the table)
+ *   used  [1] i32: n. Pages from n on are free afterwards, and may be given back.
+ * Pages with refs below 0 count as in use and keep their count (SWA_DERR_META).
+ * Sizes, workspace and repeated calls as swa_paged_fork.
+ * Errors: SWA_E_NULL, SWA_E_SHAPE, SWA_E_ALIGN, SWA_E_WORKSPACE, SWA_E_CUDA.
+ */
+typedef struct swa_paged_compact_args {
+  swa_page_pools pools;
+  int B, max_pages;
+  const int32_t* table;
+  const int32_t* refs;
+  int32_t* table_out;
+  int32_t* refs_out;
+  int32_t* moved;
+  int32_t* used;
+  void* workspace;
+  size_t workspace_bytes;
+  uint32_t* err;
+} swa_paged_compact_args;
+/* Bytes of workspace for these sizes (0: invalid sizes). */
+size_t swa_paged_compact_workspace_size(const swa_paged_compact_args* args);
+int swa_paged_compact(const swa_paged_compact_args* args, cudaStream_t stream);
 
 #ifdef __cplusplus
 }

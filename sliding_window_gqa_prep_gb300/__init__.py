@@ -16,6 +16,8 @@ Public calls (same names as the C ABI):
   TokenPath: holds a batch's ring state and runs whole steps
   rotary_turns, rotary, paged_append, paged_attend, paged_weigh, paged_evict: rotary
   positions and the paged cache of the layers that keep every key (paged.py)
+  paged4_append, paged4_read, paged4_attend: that cache in 4 bits; paged_fork,
+  paged_compact: pages that sequences share, of either cache (paged4.py)
 Meta tensors are int32 [B][4] = (win_len, win_head, far_len, window), read by
 the kernels as uint32; pos0 tensors are int32 [B].
 """
@@ -28,13 +30,14 @@ import torch
 
 from . import _abi
 from ._abi import (SwaError, SWA_DERR_META, SWA_DERR_PAGE, SWA_DERR_SEGMENT,  # noqa: F401
-                   SWA_DERR_TIMEOUT)
-from . import paged as _paged
+                   SWA_DERR_FULL, SWA_DERR_TIMEOUT)
+from . import paged as _paged, paged4 as _paged4
 from .paged import *  # noqa: F401,F403
+from .paged4 import *  # noqa: F401,F403
 
 __all__ = ["rope_table", "prep", "attend", "attend_workspace_size", "decode_step",
            "decode_workspace_size", "decode_launches", "rollback", "launch_count",
-           "TokenPath", "SwaError", "library"] + _paged.__all__
+           "TokenPath", "SwaError", "library"] + _paged.__all__ + _paged4.__all__
 
 
 def library() -> ctypes.CDLL:

@@ -20,6 +20,7 @@ SWA_DERR_META = 1
 SWA_DERR_TIMEOUT = 2
 SWA_DERR_SEGMENT = 4
 SWA_DERR_PAGE = 8
+SWA_DERR_FULL = 16
 
 SWA_F32 = 0
 SWA_BF16 = 1
@@ -158,6 +159,77 @@ class PagedEvictArgs(ctypes.Structure):
     ]
 
 
+class Paged4Cache(ctypes.Structure):
+    _fields_ = [
+        ("B", ctypes.c_int), ("nk", ctypes.c_int), ("hd", ctypes.c_int), ("page", ctypes.c_int),
+        ("num_pages", ctypes.c_int), ("max_pages", ctypes.c_int), ("k_exp", ctypes.c_int), ("v_exp", ctypes.c_int),
+        ("k", ctypes.c_void_p), ("k_scale", ctypes.c_void_p), ("v", ctypes.c_void_p), ("v_scale", ctypes.c_void_p),
+        ("table", ctypes.c_void_p), ("row_start", ctypes.c_void_p), ("lens", ctypes.c_void_p),
+    ]
+
+
+class Paged4AppendArgs(ctypes.Structure):
+    _fields_ = [
+        ("cache", Paged4Cache),
+        ("T", ctypes.c_int), ("nh", ctypes.c_int), ("rot", ctypes.c_int), ("src", ctypes.c_int),
+        ("q_dtype", ctypes.c_int), ("interleaved", ctypes.c_int), ("mag", ctypes.c_float),
+        ("q", ctypes.c_void_p), ("k", ctypes.c_void_p), ("v", ctypes.c_void_p),
+        ("q_row", ctypes.c_longlong), ("k_row", ctypes.c_longlong), ("v_row", ctypes.c_longlong),
+        ("q_out", ctypes.c_void_p), ("pos", ctypes.c_void_p), ("turns", ctypes.c_void_p), ("err", ctypes.c_void_p),
+    ]
+
+
+class Paged4ReadArgs(ctypes.Structure):
+    _fields_ = [
+        ("cache", Paged4Cache),
+        ("T", ctypes.c_int), ("dtype", ctypes.c_int),
+        ("k_out", ctypes.c_void_p), ("v_out", ctypes.c_void_p), ("err", ctypes.c_void_p),
+    ]
+
+
+class Paged4AttendArgs(ctypes.Structure):
+    _fields_ = [
+        ("cache", Paged4Cache),
+        ("T", ctypes.c_int), ("nh", ctypes.c_int), ("max_rows", ctypes.c_int), ("window", ctypes.c_int),
+        ("sinks", ctypes.c_int), ("q_dtype", ctypes.c_int), ("out_f32", ctypes.c_int),
+        ("scale", ctypes.c_float),
+        ("q", ctypes.c_void_p), ("q_row", ctypes.c_longlong), ("out", ctypes.c_void_p), ("lse", ctypes.c_void_p),
+        ("workspace", ctypes.c_void_p), ("workspace_bytes", ctypes.c_size_t), ("err", ctypes.c_void_p),
+        ("ev_start", ctypes.c_void_p), ("ev_stop", ctypes.c_void_p),
+    ]
+
+
+SWA_MAX_POOLS = 8
+
+
+class PagePools(ctypes.Structure):
+    _fields_ = [
+        ("num_pages", ctypes.c_int), ("pools", ctypes.c_int),
+        ("base", ctypes.c_void_p * SWA_MAX_POOLS), ("page_bytes", ctypes.c_longlong * SWA_MAX_POOLS),
+    ]
+
+
+class PagedForkArgs(ctypes.Structure):
+    _fields_ = [
+        ("pools", PagePools),
+        ("B", ctypes.c_int), ("R", ctypes.c_int), ("page", ctypes.c_int), ("max_pages", ctypes.c_int),
+        ("table", ctypes.c_void_p), ("lens", ctypes.c_void_p), ("parent", ctypes.c_void_p), ("room", ctypes.c_void_p),
+        ("refs", ctypes.c_void_p), ("table_out", ctypes.c_void_p), ("lens_out", ctypes.c_void_p),
+        ("refs_out", ctypes.c_void_p), ("left", ctypes.c_void_p),
+        ("workspace", ctypes.c_void_p), ("workspace_bytes", ctypes.c_size_t), ("err", ctypes.c_void_p),
+    ]
+
+
+class PagedCompactArgs(ctypes.Structure):
+    _fields_ = [
+        ("pools", PagePools),
+        ("B", ctypes.c_int), ("max_pages", ctypes.c_int),
+        ("table", ctypes.c_void_p), ("refs", ctypes.c_void_p), ("table_out", ctypes.c_void_p),
+        ("refs_out", ctypes.c_void_p), ("moved", ctypes.c_void_p), ("used", ctypes.c_void_p),
+        ("workspace", ctypes.c_void_p), ("workspace_bytes", ctypes.c_size_t), ("err", ctypes.c_void_p),
+    ]
+
+
 _lib = None
 
 
@@ -214,11 +286,13 @@ def load(build_if_missing: bool = True) -> ctypes.CDLL:
     lib.swa_flash_workspace_size.argtypes = [ctypes.POINTER(FlashArgs)]
     lib.swa_rotary_turns.restype = ctypes.c_int
     lib.swa_rotary_turns.argtypes = [ctypes.POINTER(RotarySchedule), ctypes.c_void_p, ctypes.c_void_p]
-    for name in ("swa_rotary", "swa_paged_append", "swa_paged_attend", "swa_paged_weigh", "swa_paged_evict"):
+    for name in ("swa_rotary", "swa_paged_append", "swa_paged_attend", "swa_paged_weigh", "swa_paged_evict",
+                 "swa_paged4_append", "swa_paged4_read", "swa_paged4_attend", "swa_paged_fork", "swa_paged_compact"):
         fn = getattr(lib, name)
         fn.restype = ctypes.c_int
         fn.argtypes = [ctypes.c_void_p, ctypes.c_void_p]   # a packed struct (bytes) or byref of one
-    for name in ("swa_paged_attend_workspace_size", "swa_paged_evict_workspace_size"):
+    for name in ("swa_paged_attend_workspace_size", "swa_paged_evict_workspace_size", "swa_paged4_attend_workspace_size",
+                 "swa_paged_fork_workspace_size", "swa_paged_compact_workspace_size"):
         fn = getattr(lib, name)
         fn.restype = ctypes.c_size_t
         fn.argtypes = [ctypes.c_void_p]
