@@ -1,29 +1,557 @@
-// Attention of a ragged chunk over the 4-bit paged cache (swa_paged4_attend).
+// Attention of a ragged chunk over the 4-bit paged cache: the kernel for few query vectors per
+// KV head (decode tokens, verify chunks) and the host side of swa_paged4_attend.
 //
-// A warp takes a query vector and walks the keys that its row sees, one at a time: the lanes hold
-// hd / 32 features each, the softmax runs along.
+// A key costs 4.5 bits a feature to read, and 16 bits at least to multiply: the codes have to become
+// f16 on the way. At the memory's rate an SM has 98 clk for the 2304 bytes of 16 keys and values
+// (hd 128); turning them into f16 takes 47 clk of its conversion unit (44 pairs of codes a clk,
+// measured) and 31 of its f16 multipliers (the scales), if that happens once and in the registers of
+// the product that reads them. So the keys are the rows of both products, whose operand A holds
+// what a warp has just converted, and up to 32 query vectors are the columns:
+//   S^T [16 keys x 8 vectors] = K [16 x hd] Q^T, in steps of 16 features. The sum over features may
+//     run in any order: lane (g, t) takes 16 bytes of key g at a time, features 32 t .. 32 t + 31,
+//     and Q^T is laid out alike.
+//   O^T [hd x 8 vectors] += V^T [hd x 16 keys] P^T. A pair of an operand is now two keys of one feature:
+//     the lower (upper) halves of two keys' bytes are put into one byte before the conversion.
+//   P^T comes out of S^T by movmatrix: 8 x 8 transposed, in registers.
+// A value code * scale is exact in f16. Weights enter the second product in f16, scaled by
+// 2^(kLog2 + up to kLazy) so that small ones keep their bits.
+// Every CTA gets the same number of 64-key tiles of the whole call, wherever the cuts fall; one warp copies
+// them from the pages (plain bulk copies: a head's keys of a page are consecutive), the others take
+// a quarter of a tile's keys each (or half, for half of the vectors), with a running maximum and sums of
+// their own, joined at an item's end.
+// Items that are cut leave a record (m, l, sum p v) per CTA, joined by paged_merge_kernel.
 #include <cmath>
 
-#include "swa_paged4.cuh"
-#include "swa_paged_attend.cuh"
+#include "swa_mma16.cuh"
+#include "swa_paged4_attend.cuh"
+#include "swa_paged_merge.cuh"
 
 namespace swa {
 
-struct Attend4Params {
-  PagedMap map;
-  Pools4 c;
-  int T, nh, hpg, max_rows, window, sinks, out_f32;
-  float qmul;                  // scale * log2(e) * 2^k_exp: scores in log2 units
-  const void* q;
-  long long q_row;
-  void* out;
-  float* lse;
-  uint32_t* err;
+constexpr int kKeys4 = 64;           // keys of a tile
+constexpr int kWarps4 = 4;           // warps that compute
+constexpr int kMin4 = 4;             // a CTA takes at least this many tiles
+
+// A warp has NV tiles of 8 query vectors; VG groups of warps share a tile's keys and have other vectors.
+template <int D, int NV, int VG>
+struct Split4Cfg {
+  static constexpr int THREADS = kWarps4 * 32 + 32;         // and the warp that copies
+  static constexpr int CODES = kKeys4 * D / 2, SCALES = kKeys4 * D / 16, STAGE = 2 * (CODES + SCALES);
+  static constexpr int ROWS = 8 * NV * VG;                  // query vectors
+  static constexpr bool QS = NV * D > 128;                  // Q^T waits in shared memory, not in registers
+  static constexpr int CTAS = NV * D <= 128 && VG == 1 && D == 64 ? 4 : 3;   // an SM: 96 or 128 registers a thread
+  static constexpr int JT = 4 / NV;                         // 16-feature tiles of O that the warps join at a time
+  static constexpr int JOIN = kWarps4 * JT * NV * 512;      // bytes: 8 KB
+  static constexpr int QB = QS ? ROWS * D * 2 : 0;
+  static constexpr int FIT = (226 * 1024 / CTAS - 1024 - JOIN - QB - 128 - 1024) / STAGE;
+  static constexpr int ST = FIT < 8 ? FIT : 8;
+  static constexpr int SMEM = ST * STAGE + JOIN + QB + 128; // + alignment
 };
 
+__device__ __forceinline__ uint32_t movmatrix(uint32_t a) {
+  uint32_t d;
+  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(d) : "r"(a));
+  return d;
+}
+// Each byte's lower half from a, its upper half from b's lower half; and the upper halves alike
+__device__ __forceinline__ uint32_t low_halves(uint32_t a, uint32_t b) { return (a & 0x0f0f0f0fu) | ((b << 4) & 0xf0f0f0f0u); }
+__device__ __forceinline__ uint32_t high_halves(uint32_t a, uint32_t b) { return ((a >> 4) & 0x0f0f0f0fu) | (b & 0xf0f0f0f0u); }
+template <int I>
+__device__ __forceinline__ uint32_t codes_pair(const uint32_t* w) { return e2m1x2_f16x2<(I & 3)>(w[I >> 2]); }
+
+// W words from shared memory, aligned to their number
+template <int W>
+__device__ __forceinline__ void lds_words(uint32_t (&r)[W], const unsigned char* p) {
+  if constexpr (W == 1) {
+    r[0] = *reinterpret_cast<const uint32_t*>(p);
+  } else if constexpr (W == 2) {
+    const uint2 v = *reinterpret_cast<const uint2*>(p);
+    r[0] = v.x; r[1] = v.y;
+  } else {
+    const uint4 v = *reinterpret_cast<const uint4*>(p);
+    r[0] = v.x; r[1] = v.y; r[2] = v.z; r[3] = v.w;
+  }
+}
+template <int I, int N, typename F>
+__device__ __forceinline__ void unrolled(F f) {
+  if constexpr (I < N) {
+    f(Int<I>{});
+    unrolled<I + 1, N>(f);
+  }
+}
+
+// One vector's features as the B operands of lane lt's columns (pairs of f16), scaled; the inverse
+// scale is returned. By a whole warp.
+template <int D>
+__device__ __forceinline__ float load_query4(const Attend4Params& p, long long at, bool in, int lt, uint32_t (&q)[D / 16][2]) {
+  constexpr int CH = D == 256 ? 2 : 1, N = D / 32 / CH;     // 16-byte loads of a run of features
+  const uint16_t* const src = static_cast<const uint16_t*>(p.a.q) + at;
+  float top = 0.f;
+#pragma unroll
+  for (int c = 0; c < CH; ++c)
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      const uint4 w = in ? *reinterpret_cast<const uint4*>(src + c * 128 + lt * (8 * N) + i * 8) : make_uint4(0, 0, 0, 0);
+      const int s = (c * N + i) * 2;
+      q[s][0] = w.x;
+      q[s][1] = w.y;
+      q[s + 1][0] = w.z;
+      q[s + 1][1] = w.w;
+    }
+  auto each = [&](auto f) {
+#pragma unroll
+    for (int s = 0; s < D / 16; ++s)
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        float x, y;
+        if (p.bf) unpack2(q[s][i], x, y, (const __nv_bfloat16*)nullptr);
+        else unpack2(q[s][i], x, y, (const __half*)nullptr);
+        f(q[s][i], x, y);
+      }
+  };
+  each([&](uint32_t&, float x, float y) { top = fmaxf(top, fmaxf(fabsf(x), fabsf(y))); });
+  top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
+  top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
+  float inv;
+  const float mul = query_scale(top, inv);
+  each([&](uint32_t& w, float x, float y) { w = pack2(x * mul, y * mul, (const __half*)nullptr); });
+  return inv;
+}
+
+__device__ __forceinline__ void store_pair4(const Attend4Params& p, long long at, float x, float y) {
+  if (p.a.out_f32) *reinterpret_cast<float2*>(static_cast<float*>(p.a.out) + at) = make_float2(x, y);
+  else *reinterpret_cast<uint32_t*>(static_cast<uint16_t*>(p.a.out) + at) =
+      p.bf ? pack2(x, y, (const __nv_bfloat16*)nullptr) : pack2(x, y, (const __half*)nullptr);
+}
+
+// Tiles of one (sequence, KV head): none where the sequence has no rows or more query
+// vectors than this kernel takes.
+__device__ __forceinline__ Tiles4 split4_tiles(const PagedSeq& s, const Attend4Params& p) {
+  if (s.t == 0 || (long long)s.t * p.a.hpg > p.a.most) return {0, 0, 0};
+  return key_tiles(s, p, kKeys4);
+}
+
+template <int D, int NV, int VG>
+__global__ void __launch_bounds__(Split4Cfg<D, NV, VG>::THREADS, Split4Cfg<D, NV, VG>::CTAS)
+    paged4_split_kernel(const __grid_constant__ Attend4Params p) {
+  using C = Split4Cfg<D, NV, VG>;
+  constexpr int ST = C::ST, KS = D / 16, NW = C::THREADS / 32, KG = kWarps4 / VG;
+  constexpr bool QS = C::QS;
+  extern __shared__ unsigned char sm_raw[];
+  __shared__ __align__(8) uint64_t b_full[ST], b_empty[ST];
+  __shared__ long long s_scan[NW];
+  __shared__ long long s_off, s_total;
+  __shared__ int s_b, s_abort;
+  __shared__ float2 s_ml[kWarps4][8 * NV];
+  __shared__ float s_shift[C::ROWS];
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  unsigned char* const sm = reinterpret_cast<unsigned char*>((reinterpret_cast<uintptr_t>(sm_raw) + 127) & ~(uintptr_t)127);
+  float* const join = reinterpret_cast<float*>(sm + ST * C::STAGE);
+  uint2* const s_q = reinterpret_cast<uint2*>(sm + ST * C::STAGE + C::JOIN);   // [8-vector tile][step][lane]
+  const PagedAttendParams& a = p.a;
+  if (tid == 0) {
+    for (int i = 0; i < ST; ++i) {
+      mbar_init(&b_full[i], 1);
+      mbar_init(&b_empty[i], kWarps4);
+    }
+    mbar_fence_init();
+    s_abort = 0;
+    s_b = -1;
+  }
+  pdl_wait();
+  pdl_trigger();
+
+  // --- this CTA's share of all tiles: a scan over the sequences
+  uint32_t bits = 0;
+  if (a.whole) {
+    if (tid == 0) {
+      const int b = blockIdx.x / a.map.nk;
+      const int n = split4_tiles(paged_seq(a.map, b, a.T, a.max_rows, bits), p).n;
+      if (bits) set_err(a.err, bits);
+      if (n > 0) s_b = b;
+      s_off = (long long)(blockIdx.x % a.map.nk) * n;
+      s_total = n;
+    }
+    __syncthreads();
+  } else {
+    const int E = (a.map.B + C::THREADS - 1) / C::THREADS;
+    long long mine = 0;
+    for (int e = 0; e < E; ++e) {
+      const int b = tid * E + e;
+      if (b < a.map.B) mine += (long long)a.map.nk * split4_tiles(paged_seq(a.map, b, a.T, a.max_rows, bits), p).n;
+    }
+    if (bits && blockIdx.x == 0) set_err(a.err, bits);
+    long long incl = mine;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const long long v = __shfl_up_sync(0xffffffffu, incl, o);
+      if (lane >= o) incl += v;
+    }
+    if (lane == 31) s_scan[warp] = incl;
+    __syncthreads();
+    long long before = incl - mine, total = 0;
+    for (int w = 0; w < NW; ++w) {
+      if (w < warp) before += s_scan[w];
+      total += s_scan[w];
+    }
+    long long per = (total + gridDim.x - 1) / gridDim.x;
+    if (per < kMin4) per = kMin4;
+    const long long u0 = per * blockIdx.x;
+    if (u0 >= before && u0 < before + mine) {
+      long long off = u0 - before;
+      for (int e = 0; e < E; ++e) {
+        const int b = tid * E + e;
+        uint32_t ignore = 0;
+        const long long n = (long long)a.map.nk * split4_tiles(paged_seq(a.map, b, a.T, a.max_rows, ignore), p).n;
+        if (off < n) {
+          s_b = b;
+          s_off = off;
+          break;
+        }
+        off -= n;
+      }
+    }
+    if (tid == 0) s_total = total;
+    __syncthreads();
+  }
+  const long long total = s_total;
+  long long per = (total + gridDim.x - 1) / gridDim.x;
+  if (per < kMin4) per = kMin4;
+  if (a.whole) per = total;
+  const long long u0 = a.whole ? 0 : per * blockIdx.x;
+  if (tid == 0 && !a.whole) a.ws_desc[blockIdx.x] = make_int4(-1, 0, 0, 0);
+  if (s_b < 0) return;
+  // the items of this share, walked by the copying warp and by the others alike
+  long long left = min(per, total - u0);
+  int b = s_b;
+  uint32_t ignore = 0;
+  PagedSeq s = paged_seq(a.map, b, a.T, a.max_rows, ignore);
+  Tiles4 tl = split4_tiles(s, p);
+  int tile0 = (int)(s_off % tl.n), g = (int)(s_off / tl.n);
+  auto next_item = [&](int tile1) {         // false at the end
+    left -= tile1 - tile0;
+    tile0 = 0;
+    if (left <= 0) return false;
+    if (++g == a.map.nk) {
+      g = 0;
+      do {
+        s = paged_seq(a.map, ++b, a.T, a.max_rows, ignore);
+        tl = split4_tiles(s, p);
+      } while (tl.n == 0);
+    }
+    return true;
+  };
+  int it = 0;                               // tiles of this share so far: stage it % ST
+
+  if (warp == kWarps4) {
+    // ------------------------------------------------------------ copies: a run of keys of one array a lane
+    const int page = 1 << a.map.page_shift, rows = min(page, kKeys4), runs = kKeys4 / rows;   // 4 * runs <= 32
+    const int arr = lane / runs, run = lane % runs;      // 0: K codes, 1: V codes, 2: K scales, 3: V scales
+    const bool mine = arr < 4, codes = arr < 2;
+    const uint8_t* const src = arr == 0 ? p.c.k : arr == 1 ? p.c.v : arr == 2 ? p.c.ks : p.c.vs;
+    const int row = codes ? D / 2 : D / 16;
+    const int dst = (codes ? arr * C::CODES : 2 * C::CODES + (arr - 2) * C::SCALES) + run * rows * row;
+    bool ok = true;
+    do {
+      const int tile1 = (int)min((long long)tl.n, tile0 + left);
+      const int32_t* table = a.map.table + (size_t)b * a.map.max_pages;
+      for (int x = tile0; ok && x < tile1; ++x, ++it) {
+        const int key = tl.at(x) * kKeys4 + run * rows, st = it % ST;
+        const uint8_t* from = nullptr;
+        bool blank = false;
+        if (mine && key < s.len) {          // looked up before the wait
+          const int id = table[key >> a.map.page_shift];
+          if (page_ok(a.map, id)) {
+            from = src + ((((long long)id * a.map.nk + g) << a.map.page_shift) + (key & (page - 1))) * row;
+          } else {
+            set_err(a.err, SWA_DERR_PAGE);
+            blank = !codes;                 // such keys read as zeros: by their scales
+          }
+        }
+        const uint32_t bytes = __reduce_add_sync(0xffffffffu, from ? rows * row : 0);
+        if (it >= ST) ok = __all_sync(0xffffffffu, tc_wait(&b_empty[st], (uint32_t)((it / ST - 1) & 1), &s_abort));
+        if (!ok) break;
+        if (blank) {
+          for (int i = 0; i < rows * row; i += 16) *reinterpret_cast<uint4*>(sm + st * C::STAGE + dst + i) = make_uint4(0, 0, 0, 0);
+          fence_proxy_async_smem();         // before a later copy into this stage
+        }
+        __syncwarp();
+        if (lane == 0) mbar_arrive_expect_tx(&b_full[st], bytes);
+        __syncwarp();
+        if (from) bulk_g2s(sm + st * C::STAGE + dst, from, rows * row, &b_full[st]);
+      }
+      if (!ok || !next_item(tile1)) break;
+    } while (true);
+    if (!ok) {
+      set_err(a.err, SWA_DERR_TIMEOUT);
+      // copies in flight land before the CTA exits (bounded)
+      for (int i = max(0, it - ST); i < it; ++i) mbar_wait_bounded(&b_full[i % ST], (uint32_t)((i / ST) & 1), kWaitLimitNs);
+    }
+    return;
+  }
+
+  // ------------------------------------------------------------ products
+  const int lg = lane >> 2, lt = lane & 3, hpg = a.hpg, vg = warp / KG;
+  // the key of the group's 16 that is row i of the products: lanes that read at the same time
+  // then find rows of both parities, and fewer of them in the same banks
+  auto key_of = [](int i) { return i ^ ((i >> 1) & 1); };
+  bool ok = true;                           // a thread whose wait gave up goes on and writes nothing
+  do {
+    const int tile1 = (int)min((long long)tl.n, tile0 + left);
+    const int nvec = s.t * hpg;
+    // --- Q^T as B operands in f16, each vector scaled by a power of two; scores' factors, limits
+    uint32_t qf[QS ? 1 : NV][KS][2];
+    float qm[NV][2];
+    int lim[NV][2];
+    auto query = [&](int tile, uint32_t (&q)[KS][2]) {      // of 8 vectors; the inverse scale of vector lg
+      const int r = tile * 8 + lg;
+      const bool in = r < nvec;
+      const int i = in ? r / hpg : 0, h = in ? r % hpg : 0;
+      return load_query4<D>(p, (long long)(s.r0 + i) * a.q_row + (long long)(g * hpg + h) * D, in, lt, q);
+    };
+    if constexpr (QS) {
+      for (int tile = warp; tile < C::ROWS / 8; tile += kWarps4) {
+        const float shift = query(tile, qf[0]);
+        if (lt == 0) s_shift[tile * 8 + lg] = shift;
+#pragma unroll
+        for (int i = 0; i < KS; ++i) s_q[(tile * KS + i) * 32 + lane] = make_uint2(qf[0][i][0], qf[0][i][1]);
+      }
+      named_barrier(1, kWarps4 * 32);
+    }
+#pragma unroll
+    for (int v = 0; v < NV; ++v) {
+      float shift = 0.f;
+      if constexpr (!QS) shift = query(vg * NV + v, qf[v]);
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        const int c = (vg * NV + v) * 8 + 2 * lt + e;
+        if constexpr (QS) qm[v][e] = a.qmul * s_shift[c];
+        else qm[v][e] = a.qmul * __shfl_sync(0xffffffffu, shift, (2 * lt + e) * 4);
+        lim[v][e] = c < nvec ? min(s.len, s.len - s.t + c / hpg + 1) : 0;
+      }
+    }
+    auto q_at = [&](int v, int i) {
+      if constexpr (QS) return s_q[((vg * NV + v) * KS + i) * 32 + lane];
+      else return make_uint2(qf[v][i][0], qf[v][i][1]);
+    };
+    const int lim_min = s.len - s.t + 1;                    // keys below it are before or at every row's own
+    const int lo_min = max(0, lim_min - p.window), lo_max = s.len - p.window;   // first keys of the rows' windows
+
+    float o[NV][KS][4], m[NV][2], l[NV][2];
+#pragma unroll
+    for (int v = 0; v < NV; ++v) {
+#pragma unroll
+      for (int j = 0; j < KS; ++j)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) o[v][j][e] = 0.f;
+      m[v][0] = m[v][1] = -INFINITY;
+      l[v][0] = l[v][1] = 0.f;
+    }
+
+    for (int x = tile0; x < tile1; ++x, ++it) {
+      const int st = it % ST;
+      ok &= tc_wait(&b_full[st], (uint32_t)((it / ST) & 1), &s_abort);
+      __syncwarp();
+#pragma unroll 1
+      for (int sub = 0; sub < VG; ++sub) {                  // this warp's keys, 16 at a time
+        const int at16 = (warp % KG) * VG + sub, k0 = tl.at(x) * kKeys4 + at16 * 16;
+        if (k0 >= s.len || (k0 + 16 <= lo_min && k0 >= p.sinks)) continue;
+        const unsigned char* const kb = sm + st * C::STAGE + at16 * 16 * (D / 2);
+        const unsigned char* const vb = kb + C::CODES;
+        const unsigned char* const ksb = sm + st * C::STAGE + 2 * C::CODES + at16 * 16 * (D / 16);
+        const unsigned char* const vsb = ksb + C::SCALES;
+        const bool mask = k0 + 16 > lim_min || k0 < lo_max;
+        float sc[NV][4];
+#pragma unroll
+        for (int v = 0; v < NV; ++v)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) sc[v][e] = 0.f;
+        const int ka = key_of(lg), kc = key_of(lg + 8);
+        // 4 features a step: a lane's codes are 64 (hd 256: 2 times 64) consecutive ones at most
+        constexpr int W = D == 64 ? 2 : 4, CH = D == 256 ? 2 : 1;
+#pragma unroll
+        for (int c = 0; c < CH; ++c) {
+          uint32_t wa[W], wc[W];
+          lds_words<W>(wa, kb + ka * (D / 2) + c * 64 + lt * (W * 4));
+          lds_words<W>(wc, kb + kc * (D / 2) + c * 64 + lt * (W * 4));
+          uint32_t sa[2], sb[2];            // a block's scale in both halves
+          if constexpr (D == 64) {
+            sa[0] = e4m3x2_f16x2(ksb[ka * 4 + lt] * 0x0101u);
+            sb[0] = e4m3x2_f16x2(ksb[kc * 4 + lt] * 0x0101u);
+          } else {
+            const uint32_t ua = e4m3x2_f16x2(*reinterpret_cast<const uint16_t*>(ksb + ka * (D / 16) + c * 8 + lt * 2));
+            const uint32_t uc = e4m3x2_f16x2(*reinterpret_cast<const uint16_t*>(ksb + kc * (D / 16) + c * 8 + lt * 2));
+            sa[0] = __byte_perm(ua, ua, 0x1010);
+            sa[1] = __byte_perm(ua, ua, 0x3232);
+            sb[0] = __byte_perm(uc, uc, 0x1010);
+            sb[1] = __byte_perm(uc, uc, 0x3232);
+          }
+          unrolled<0, KS / CH>([&](auto i) {
+            constexpr int I = decltype(i)::value, B = D == 64 ? 0 : I / 4;
+            const uint32_t f[4] = {hmul2(codes_pair<2 * I>(wa), sa[B]), hmul2(codes_pair<2 * I>(wc), sb[B]),
+                                   hmul2(codes_pair<2 * I + 1>(wa), sa[B]), hmul2(codes_pair<2 * I + 1>(wc), sb[B])};
+#pragma unroll
+            for (int v = 0; v < NV; ++v) {
+              const uint2 q = q_at(v, c * (KS / CH) + I);
+              mma16816<__half>(sc[v], f, q.x, q.y);
+            }
+          });
+        }
+        // scores in log2 units, masked: element e is (key row lg + 8 (e / 2), vector 2 lt + e % 2)
+        bool raise = false;
+#pragma unroll
+        for (int v = 0; v < NV; ++v)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            float y = sc[v][e] * qm[v][e & 1];
+            if (mask) {
+              const int key = k0 + (e < 2 ? ka : kc), top = lim[v][e & 1];
+              if (key >= top || (key < top - p.window && key >= p.sinks)) y = -INFINITY;
+            }
+            sc[v][e] = y;
+            raise |= y > m[v][e & 1] + kLazy4;
+          }
+        if (__any_sync(0xffffffffu, raise)) {
+#pragma unroll
+          for (int v = 0; v < NV; ++v)
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+              float mx = fmaxf(sc[v][e], sc[v][e + 2]);
+#pragma unroll
+              for (int d = 4; d < 32; d <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, d));
+              const float mn = fmaxf(m[v][e], mx);
+              const float f = mn == -INFINITY ? 1.f : ex2(m[v][e] - mn);   // m = -inf: 0
+              m[v][e] = mn;
+              l[v][e] *= f;
+#pragma unroll
+              for (int j = 0; j < KS; ++j) {
+                o[v][j][e] *= f;
+                o[v][j][e + 2] *= f;
+              }
+            }
+        }
+        uint32_t pf[NV][2];
+#pragma unroll
+        for (int v = 0; v < NV; ++v) {
+          const float off0 = kLog24 - (m[v][0] == -INFINITY ? 0.f : m[v][0]), off1 = kLog24 - (m[v][1] == -INFINITY ? 0.f : m[v][1]);
+          const float e0 = ex2(sc[v][0] + off0), e1 = ex2(sc[v][1] + off1), e2 = ex2(sc[v][2] + off0), e3 = ex2(sc[v][3] + off1);
+          l[v][0] += e0 + e2;
+          l[v][1] += e1 + e3;
+          pf[v][0] = movmatrix(pack2(e0, e1, (const __half*)nullptr));
+          pf[v][1] = movmatrix(pack2(e2, e3, (const __half*)nullptr));
+        }
+        // V^T: keys 2 lt, 2 lt + 1 (+ 8) of the products' rows, features (hd / 8) lg ..
+        constexpr int VW = D / 64;          // words of a key
+        uint32_t lo[2][VW], hi[2][VW], vs[2][2];
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          const int k1 = key_of(2 * lt + 8 * h), k2 = key_of(2 * lt + 8 * h + 1);
+          uint32_t w1[VW], w2[VW];
+          lds_words<VW>(w1, vb + k1 * (D / 2) + lg * (VW * 4));
+          lds_words<VW>(w2, vb + k2 * (D / 2) + lg * (VW * 4));
+#pragma unroll
+          for (int w = 0; w < VW; ++w) {
+            lo[h][w] = low_halves(w1[w], w2[w]);
+            hi[h][w] = high_halves(w1[w], w2[w]);
+          }
+          uint32_t u1, u2;
+          if constexpr (D == 256) {
+            u1 = *reinterpret_cast<const uint16_t*>(vsb + k1 * 16 + lg * 2);
+            u2 = *reinterpret_cast<const uint16_t*>(vsb + k2 * 16 + lg * 2);
+          } else {
+            u1 = vsb[k1 * (D / 16) + (D == 64 ? lg >> 1 : lg)];
+            u2 = vsb[k2 * (D / 16) + (D == 64 ? lg >> 1 : lg)];
+          }
+          if (mask) {                       // what no row sees may be NaN: zeros
+            if (k0 + k1 >= s.len || (k0 + k1 < lo_min && k0 + k1 >= p.sinks)) u1 = 0;
+            if (k0 + k2 >= s.len || (k0 + k2 < lo_min && k0 + k2 >= p.sinks)) u2 = 0;
+          }
+          vs[h][0] = e4m3x2_f16x2(__byte_perm(u1, u2, 0x0040));
+          if constexpr (D == 256) vs[h][1] = e4m3x2_f16x2(__byte_perm(u1, u2, 0x0051));
+        }
+        unrolled<0, KS>([&](auto j) {
+          constexpr int J = decltype(j)::value, B = D == 256 ? J / 8 : 0;
+          const uint32_t f[4] = {hmul2(codes_pair<J>(lo[0]), vs[0][B]), hmul2(codes_pair<J>(hi[0]), vs[0][B]),
+                                 hmul2(codes_pair<J>(lo[1]), vs[1][B]), hmul2(codes_pair<J>(hi[1]), vs[1][B])};
+#pragma unroll
+          for (int v = 0; v < NV; ++v) mma16816<__half>(o[v][J], f, pf[v][0], pf[v][1]);
+        });
+      }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&b_empty[st]);
+    }
+
+    // --- join the warps, JT tiles of O at a time
+#pragma unroll
+    for (int v = 0; v < NV; ++v)
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+#pragma unroll
+        for (int d = 4; d < 32; d <<= 1) l[v][e] += __shfl_xor_sync(0xffffffffu, l[v][e], d);
+        if (lg == 0) s_ml[warp][v * 8 + 2 * lt + e] = make_float2(m[v][e], l[v][e]);
+      }
+    const bool whole = tile0 == 0 && tile1 == tl.n;
+    // record of the item this CTA continues: slot 2c, of the one it starts: 2c + 1
+    const size_t rec = ((size_t)blockIdx.x * 2 + (tile0 == 0 ? 1 : 0)) * p.rows;
+#pragma unroll
+    for (int j0 = 0; j0 < KS; j0 += C::JT) {
+      if (j0 > 0) named_barrier(1, kWarps4 * 32);           // the tiles before are read
+#pragma unroll
+      for (int v = 0; v < NV; ++v)
+#pragma unroll
+        for (int j = 0; j < C::JT; ++j)
+#pragma unroll
+          for (int h = 0; h < 2; ++h)
+            *reinterpret_cast<float2*>(join + ((((warp * NV + v) * C::JT + j) * 2 + h) * 8 + lg) * 8 + 2 * lt) =
+                make_float2(o[v][j0 + j][2 * h], o[v][j0 + j][2 * h + 1]);
+      named_barrier(1, kWarps4 * 32);
+      if (s_abort) continue;
+      // a vector c of tile v of group w0 / KG, features 2 j and 2 j + 1 of lane group pg at a time
+      for (int y = tid; y < C::ROWS * C::JT * 8; y += kWarps4 * 32) {
+        const int c = y & 7, pg = (y >> 3) & 7, j = (y >> 6) % C::JT, v = (y >> 6) / C::JT % NV, w0 = (y >> 6) / (C::JT * NV) * KG;
+        const int pv = (w0 / KG * NV + v) * 8 + c;
+        if (pv >= nvec) continue;
+        float mt = -INFINITY, lt_ = 0.f, acc[2] = {0.f, 0.f};
+#pragma unroll
+        for (int w = 0; w < KG; ++w) mt = fmaxf(mt, s_ml[w0 + w][v * 8 + c].x);
+#pragma unroll
+        for (int w = 0; w < KG; ++w) {
+          const float2 ml = s_ml[w0 + w][v * 8 + c];
+          const float f = ml.x == -INFINITY ? 0.f : ex2(ml.x - mt + (p.rec_log2 - kLog24));
+          lt_ += f * ml.y;
+#pragma unroll
+          for (int h = 0; h < 2; ++h) acc[h] += f * join[(((((w0 + w) * NV + v) * C::JT + j) * 2 + h) * 8 + pg) * 8 + c];
+        }
+        const int f = pg * (D / 8) + 2 * (j0 + j);
+        acc[0] *= p.c.v_mul;
+        acc[1] *= p.c.v_mul;
+        if (whole) {
+          const float inv = lt_ > 0.f ? 1.f / lt_ : (lt_ == 0.f ? 0.f : lt_);   // no key: zeros; NaN stays
+          const int row = s.r0 + pv / hpg, head = g * hpg + pv % hpg;
+          store_pair4(p, ((long long)row * a.nh + head) * D + f, lt_ == 0.f ? 0.f : acc[0] * inv, lt_ == 0.f ? 0.f : acc[1] * inv);
+          if (f == 0 && a.lse)
+            a.lse[(size_t)row * a.nh + head] = lt_ == 0.f ? -INFINITY : (mt - p.rec_log2 + log2f(lt_)) * 0.6931471805599453f;
+        } else {
+          *reinterpret_cast<float2*>(a.ws_acc + (rec + pv) * D + f) = make_float2(acc[0], acc[1]);
+          if (f == 0) a.ws_ml[rec + pv] = make_float2(mt, lt_);
+        }
+      }
+    }
+    if (!whole && tile0 == 0 && tid == 0) {
+      // units of this item from here on / per CTA: the CTA that ends it
+      const long long end = u0 + (min(per, total - u0) - left) + tl.n - 1;
+      a.ws_desc[blockIdx.x] = make_int4(b, g, (int)(end / per), 0);
+    }
+    if (!next_item(tile1)) break;
+    named_barrier(1, kWarps4 * 32);         // s_ml and join are read
+  } while (true);
+  if (!ok) set_err(a.err, SWA_DERR_TIMEOUT);
+}
+
 template <typename T, int E>
-__global__ void __launch_bounds__(128) paged4_plain_kernel(const Attend4Params p) {
+__global__ void __launch_bounds__(128) paged4_plain_kernel(const Attend4Params q4) {
   constexpr int HD = 32 * E;
+  const PagedAttendParams& p = q4.a;
   const int lane = threadIdx.x & 31;
   const long long v = (long long)blockIdx.x * 4 + (threadIdx.x >> 5);
   pdl_wait();
@@ -32,12 +560,12 @@ __global__ void __launch_bounds__(128) paged4_plain_kernel(const Attend4Params p
   uint32_t bits = 0;
   const PagedSeq s = paged_seq(p.map, b, p.T, p.max_rows, bits);
   const int i = (int)(v / p.nh), h = (int)(v % p.nh), g = h / p.hpg;
-  if (i < s.t) {
-    const int lim = min(s.len, s.len - s.t + i + 1), lo = p.window ? max(0, lim - p.window) : 0;
+  if (i < s.t && (long long)s.t * p.hpg > p.most) {
+    const int lim = min(s.len, s.len - s.t + i + 1), lo = max(0, lim - q4.window);
     float q[E], o[E] = {}, m = -INFINITY, l = 0.f;
     unpack(load_pack<E>(static_cast<const T*>(p.q) + (long long)(s.r0 + i) * p.q_row + (long long)h * HD + lane * E), q);
     for (int j = 0; j < lim; ++j) {
-      if (j < lo && j >= p.sinks) j = lo;
+      if (j < lo && j >= q4.sinks) j = lo;
       const int page = p.map.table[(size_t)b * p.map.max_pages + (j >> p.map.page_shift)];
       const bool ok = page_ok(p.map, page);
       if (!ok) bits |= SWA_DERR_PAGE;
@@ -52,8 +580,8 @@ __global__ void __launch_bounds__(128) paged4_plain_kernel(const Attend4Params p
           y[e + 1] = t.y * u;
         }
       };
-      value(p.c.k, p.c.ks, k);
-      value(p.c.v, p.c.vs, w);
+      value(q4.c.k, q4.c.ks, k);
+      value(q4.c.v, q4.c.vs, w);
       for (int e = 0; e < E; ++e) x += q[e] * k[e];
       for (int d = 16; d; d >>= 1) x += __shfl_xor_sync(0xffffffffu, x, d);
       x *= p.qmul;
@@ -62,7 +590,7 @@ __global__ void __launch_bounds__(128) paged4_plain_kernel(const Attend4Params p
       l = l * a + e1;
       for (int e = 0; e < E; ++e) o[e] = o[e] * a + e1 * w[e];
     }
-    const float inv = l > 0.f ? p.c.v_mul / l : l;
+    const float inv = l > 0.f ? q4.c.v_mul / l : l;
     for (int e = 0; e < E; ++e) o[e] = l == 0.f ? 0.f : o[e] * inv;
     const long long at = ((long long)(s.r0 + i) * p.nh + h) * HD + lane * E;
     if (p.out_f32) store_pack(static_cast<float*>(p.out) + at, o);
@@ -70,6 +598,84 @@ __global__ void __launch_bounds__(128) paged4_plain_kernel(const Attend4Params p
     if (lane == 0 && p.lse) p.lse[(long long)(s.r0 + i) * p.nh + h] = l == 0.f ? -INFINITY : (m + log2f(l)) * 0.6931471805599453f;
   }
   if (bits) set_err(p.err, bits);
+}
+
+// ---------------------------------------------------------------------------
+// Launches
+// ---------------------------------------------------------------------------
+// Keys that a row may see up to which a CTA takes a (sequence, KV head) whole: no scan over the
+// sequences and no second kernel. By the table's width (or the window), since the lengths are the device's.
+constexpr int kWholeKeys4 = 512;
+
+struct Split4Plan {
+  int rows, whole, grid;       // query vectors of a block (0: no sequence for this kernel)
+  size_t off_ml, off_desc, bytes;
+};
+
+template <int D, int NV, int VG>
+static int split4_occupancy() {
+  static int cache[64] = {};
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return 1;
+  if (!cache[dev]) {
+    auto k = paged4_split_kernel<D, NV, VG>;
+    int n = 0;
+    if (allow_smem<paged4_split_kernel<D, NV, VG>>(Split4Cfg<D, NV, VG>::SMEM) != cudaSuccess ||
+        cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, k, Split4Cfg<D, NV, VG>::THREADS, Split4Cfg<D, NV, VG>::SMEM) != cudaSuccess || n < 1) {
+      (void)cudaGetLastError();
+      n = 1;
+    }
+    cache[dev] = n;
+  }
+  return cache[dev];
+}
+
+template <int D, int NV, int VG>
+static int launch_split4(const Attend4Params& p, const Split4Plan& sp, cudaStream_t s) {
+  const cudaError_t e = allow_smem<paged4_split_kernel<D, NV, VG>>(Split4Cfg<D, NV, VG>::SMEM);
+  if (e != cudaSuccess) return cuda_status(e);
+  const int rc = finish_launch(launch_pdl(paged4_split_kernel<D, NV, VG>, dim3(sp.grid), dim3(Split4Cfg<D, NV, VG>::THREADS),
+                                          Split4Cfg<D, NV, VG>::SMEM, s, p));
+  if (rc != SWA_OK || p.a.whole) return rc;
+  // a block a row up to 16, which then take rows in turn: most of sp.grid's columns are empty
+  const long long vecs = (long long)p.a.max_rows * p.a.hpg;
+  const dim3 grid(sp.grid, (unsigned)(vecs < 16 ? vecs : 16));
+  return finish_launch(p.bf ? launch_pdl(paged_merge_kernel<__nv_bfloat16, D>, grid, dim3(kMergeThreads), 0, s, p.a, p.rows)
+                            : launch_pdl(paged_merge_kernel<__half, D>, grid, dim3(kMergeThreads), 0, s, p.a, p.rows));
+}
+
+// rows: query vectors of a block, 8, 16 or 32 (hd 256: 8 or 16)
+template <typename F>
+static int by_size4(int hd, int rows, F f) {
+  if (hd == 256) return rows == 8 ? f(Int<256>{}, Int<1>{}, Int<1>{}) : f(Int<256>{}, Int<1>{}, Int<2>{});
+#define SWA_ROWS(D) (rows == 8 ? f(Int<D>{}, Int<1>{}, Int<1>{}) : rows == 16 ? f(Int<D>{}, Int<2>{}, Int<1>{}) : f(Int<D>{}, Int<2>{}, Int<2>{}))
+  return hd == 64 ? SWA_ROWS(64) : SWA_ROWS(128);
+#undef SWA_ROWS
+}
+
+// Query vectors of a (sequence, KV head) up to which the split kernel takes it
+static int split4_vecs(int hd) { return hd == 256 ? 16 : 32; }
+
+static void split4_plan(const swa_paged4_attend_args* a, long long vecs, Split4Plan* sp) {
+  const swa_paged4_cache& c = a->cache;
+  *sp = Split4Plan{};
+  sp->rows = vecs <= 8 ? 8 : vecs <= 16 ? 16 : 32;
+  long long keys = (long long)c.max_pages * c.page;
+  if (a->window) {
+    const long long w = (long long)a->window + a->sinks + a->max_rows + 2 * kKeys4;
+    keys = w < keys ? w : keys;
+  }
+  sp->whole = keys <= kWholeKeys4;
+  const int occ = sp->whole ? 0 : by_size4(c.hd, sp->rows, [](auto d, auto n, auto g) {
+    return split4_occupancy<decltype(d)::value, decltype(n)::value, decltype(g)::value>();
+  });
+  sp->grid = sp->whole ? c.B * c.nk : (num_sms() > 0 ? num_sms() : 148) * occ;
+  if (!sp->whole) {
+    const size_t recs = (size_t)sp->grid * 2 * sp->rows;
+    sp->off_ml = up256s(recs * c.hd * sizeof(float));
+    sp->off_desc = sp->off_ml + up256s(recs * sizeof(float2));
+    sp->bytes = sp->off_desc + up256s((size_t)sp->grid * sizeof(int4));
+  }
 }
 
 // Sizes alone (the workspace query); pointers are checked by the call.
@@ -84,6 +690,28 @@ static bool attend4_sizes_ok(const swa_paged4_attend_args* a) {
   return (long long)a->T * a->nh < (1LL << 31) - 256;
 }
 
+// Which kernels a call runs. All sequences have at most max_rows rows (and T): when these fit
+// the split kernel it runs alone. Otherwise the chunk kernel runs, and before it the split kernel if
+// some sequence may be shorter (B * max_rows > T); if not, the chunk kernel takes every sequence.
+struct Attend4Plan {
+  Split4Plan split;
+  bool has_chunk;
+  int most;                              // query vectors of a sequence up to which it is the split kernel's
+  size_t bytes;
+};
+
+static void attend4_plan(const swa_paged4_attend_args* a, Attend4Plan* pl) {
+  const int hpg = a->nh / a->cache.nk, max_rows = a->max_rows < a->T ? a->max_rows : a->T > 0 ? a->T : 1;
+  const long long vecs = (long long)max_rows * hpg;
+  *pl = Attend4Plan{};
+  pl->has_chunk = vecs > split4_vecs(a->cache.hd);
+  if (!pl->has_chunk || (long long)a->cache.B * max_rows > a->T) {
+    pl->most = split4_vecs(a->cache.hd);
+    split4_plan(a, vecs < pl->most ? vecs : pl->most, &pl->split);
+  }
+  pl->bytes = pl->split.bytes;
+}
+
 }  // namespace swa
 
 using namespace swa;
@@ -91,7 +719,10 @@ using namespace swa;
 extern "C" {
 
 size_t swa_paged4_attend_workspace_size(const swa_paged4_attend_args* a) {
-  return a && attend4_sizes_ok(a) ? 1 : 0;
+  if (!a || !attend4_sizes_ok(a)) return 0;
+  Attend4Plan pl;
+  attend4_plan(a, &pl);
+  return pl.bytes ? pl.bytes : 1;
 }
 
 int swa_paged4_attend(const swa_paged4_attend_args* a, cudaStream_t stream) {
@@ -106,29 +737,51 @@ int swa_paged4_attend(const swa_paged4_attend_args* a, cudaStream_t stream) {
   if (qn < 0) return SWA_E_SHAPE;
   if (!aligned16p(a->q) || !aligned16p(a->out) || (a->q_row & 7) || (reinterpret_cast<uintptr_t>(a->lse) & 3u))
     return SWA_E_ALIGN;
+  Attend4Plan pl;
+  attend4_plan(a, &pl);
+  if (pl.bytes && (!a->workspace || a->workspace_bytes < pl.bytes)) return SWA_E_WORKSPACE;
   if (reinterpret_cast<uintptr_t>(a->workspace) & 255u) return SWA_E_ALIGN;
   const size_t rows = (size_t)a->T * a->nh, on = rows * c.hd * (a->out_f32 ? 4 : 2), ln = a->lse ? rows * 4 : 0;
   if (bytes_overlap(a->q, (size_t)qn * 2, a->out, on) ||
       (a->lse && (bytes_overlap(a->q, (size_t)qn * 2, a->lse, ln) || bytes_overlap(a->out, on, a->lse, ln))))
     return SWA_E_SHAPE;
   Attend4Params p{};
-  p.map = paged4_map(&c);
+  PagedAttendParams& pa = p.a;
+  pa.map = paged4_map(&c);
+  pa.T = a->T; pa.nh = a->nh; pa.hpg = a->nh / c.nk; pa.max_rows = a->max_rows < a->T ? a->max_rows : a->T;
+  pa.most = pl.most;
   p.c = paged4_pools(&c);
-  p.T = a->T; p.nh = a->nh; p.hpg = a->nh / c.nk; p.max_rows = a->max_rows < a->T ? a->max_rows : a->T;
-  p.window = a->window; p.sinks = a->window ? a->sinks : 0;
-  p.qmul = a->scale * 1.4426950408889634f * p.c.k_mul;
-  p.q = a->q; p.q_row = a->q_row;
-  p.out = a->out; p.out_f32 = a->out_f32 != 0; p.lse = a->lse;
-  p.err = a->err;
+  pa.qmul = a->scale * 1.4426950408889634f * p.c.k_mul;
+  pa.q = a->q; pa.q_row = a->q_row;
+  pa.out = a->out; pa.out_f32 = a->out_f32 != 0; pa.lse = a->lse;
+  pa.err = a->err;
+  p.bf = a->q_dtype == SWA_BF16;
+  constexpr int kAll = 1 << 30;                            // no sequence is longer
+  p.window = a->window > 0 && a->window < kAll ? a->window : kAll;
+  p.sinks = a->window == 0 ? 0 : a->sinks < kAll ? a->sinks : kAll;
+  p.rec_log2 = p.bf ? PScale<__nv_bfloat16>::kLog2 : PScale<__half>::kLog2;
+  char* ws = static_cast<char*>(a->workspace);
   cudaError_t e;
   if (a->ev_start && (e = cudaEventRecord(a->ev_start, stream)) != cudaSuccess) return cuda_status(e);
-  const dim3 grid((unsigned)(((long long)p.max_rows * p.nh + 3) / 4), c.B), block(128);
-  const bool bf = a->q_dtype == SWA_BF16;
-  e = c.hd == 64    ? (bf ? launch_pdl(paged4_plain_kernel<__nv_bfloat16, 2>, grid, block, 0, stream, p) : launch_pdl(paged4_plain_kernel<__half, 2>, grid, block, 0, stream, p))
-      : c.hd == 128 ? (bf ? launch_pdl(paged4_plain_kernel<__nv_bfloat16, 4>, grid, block, 0, stream, p) : launch_pdl(paged4_plain_kernel<__half, 4>, grid, block, 0, stream, p))
-                    : (bf ? launch_pdl(paged4_plain_kernel<__nv_bfloat16, 8>, grid, block, 0, stream, p) : launch_pdl(paged4_plain_kernel<__half, 8>, grid, block, 0, stream, p));
-  rc = finish_launch(e);
-  if (rc != SWA_OK) return rc;
+  if (pl.split.rows) {
+    pa.whole = pl.split.whole;
+    p.rows = pl.split.rows;
+    pa.ws_acc = reinterpret_cast<float*>(ws);
+    pa.ws_ml = reinterpret_cast<float2*>(ws + pl.split.off_ml);
+    pa.ws_desc = reinterpret_cast<int4*>(ws + pl.split.off_desc);
+    rc = by_size4(c.hd, pl.split.rows, [&](auto d, auto n, auto g) {
+      return launch_split4<decltype(d)::value, decltype(n)::value, decltype(g)::value>(p, pl.split, stream);
+    });
+    if (rc != SWA_OK) return rc;
+  }
+  if (pl.has_chunk) {
+    const dim3 grid((unsigned)(((long long)pa.max_rows * pa.nh + 3) / 4), c.B), block(128);
+    e = c.hd == 64    ? (p.bf ? launch_pdl(paged4_plain_kernel<__nv_bfloat16, 2>, grid, block, 0, stream, p) : launch_pdl(paged4_plain_kernel<__half, 2>, grid, block, 0, stream, p))
+        : c.hd == 128 ? (p.bf ? launch_pdl(paged4_plain_kernel<__nv_bfloat16, 4>, grid, block, 0, stream, p) : launch_pdl(paged4_plain_kernel<__half, 4>, grid, block, 0, stream, p))
+                      : (p.bf ? launch_pdl(paged4_plain_kernel<__nv_bfloat16, 8>, grid, block, 0, stream, p) : launch_pdl(paged4_plain_kernel<__half, 8>, grid, block, 0, stream, p));
+    rc = finish_launch(e);
+    if (rc != SWA_OK) return rc;
+  }
   if (a->ev_stop && (e = cudaEventRecord(a->ev_stop, stream)) != cudaSuccess) return cuda_status(e);
   return SWA_OK;
 }

@@ -1,0 +1,48 @@
+// Shared by the attention kernels over the 4-bit paged cache: parameters, which tiles of keys a
+// sequence's rows see, and the queries' scales.
+#pragma once
+#include "swa_paged4.cuh"
+#include "swa_paged_attend.cuh"
+#include "swa_paged_tc.cuh"
+
+namespace swa {
+
+struct Attend4Params {
+  PagedAttendParams a;         // qmul: scale * log2(e) * 2^k_exp; q of type bf or f16
+  Pools4 c;
+  int bf;                      // q (and a 16-bit out) is bf16, else f16
+  int window, sinks;           // window: 2^30 and more where there is none (sinks is then 0)
+  int rows;                    // split kernel: query vectors of a record
+  float rec_log2;              // log2 of the records' factor: PScale<type>, as the merge takes it
+};
+
+// Weights are 2^(s - max) times 2^kLog24; the running maximum is raised when a score passes it by
+// kLazy4, so they stay below 2^15 < 65504, and one below 2^-14 loses 2^-25: 2^-36 of the row's scale.
+constexpr float kLazy4 = 4.f, kLog24 = 11.f;
+
+#ifdef __CUDACC__
+// Tiles of kt keys that a sequence's rows see: the sinks', then those from the first row's window on.
+struct Tiles4 {
+  int sink, first, n;          // tiles of sinks in front of tile `first`; all
+  __device__ __forceinline__ int at(int x) const { return x < sink ? x : x - sink + first; }
+};
+__device__ __forceinline__ Tiles4 key_tiles(const PagedSeq& s, const Attend4Params& p, int kt) {
+  Tiles4 t;
+  const int lo = max(0, s.len - s.t + 1 - p.window);        // the first row's first key
+  t.first = lo / kt;
+  t.sink = min((min(p.sinks, s.len) + kt - 1) / kt, t.first);
+  t.n = s.len > 0 ? t.sink + (s.len + kt - 1) / kt - t.first : 1;   // a row without keys is still written
+  return t;
+}
+
+// The power of two that brings a vector's largest value to [2^14, 2^15) (as far as f32 has it; 1 for
+// zeros, infinities and NaN), and its inverse
+__device__ __forceinline__ float query_scale(float top, float& inv) {
+  const int e = (int)(__float_as_uint(top) >> 23);          // biased; 0: below 2^-126
+  const int shift = top == 0.f || e == 255 ? 0 : min(127, 14 + 127 - e);
+  inv = __uint_as_float(shift >= 127 ? 0x00400000u : (uint32_t)(127 - shift) << 23);   // 2^-127 is subnormal
+  return __uint_as_float((uint32_t)(127 + shift) << 23);
+}
+#endif
+
+}  // namespace swa
