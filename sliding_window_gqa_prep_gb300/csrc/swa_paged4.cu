@@ -327,7 +327,7 @@ __global__ void __launch_bounds__(Split4Cfg<D, NV, VG>::THREADS, Split4Cfg<D, NV
         const int c = (vg * NV + v) * 8 + 2 * lt + e;
         if constexpr (QS) qm[v][e] = a.qmul * s_shift[c];
         else qm[v][e] = a.qmul * __shfl_sync(0xffffffffu, shift, (2 * lt + e) * 4);
-        lim[v][e] = c < nvec ? min(s.len, s.len - s.t + c / hpg + 1) : 0;
+        lim[v][e] = c < nvec ? max(0, min(s.len, s.len - s.t + c / hpg + 1)) : 0;
       }
     }
     auto q_at = [&](int v, int i) {
@@ -335,7 +335,7 @@ __global__ void __launch_bounds__(Split4Cfg<D, NV, VG>::THREADS, Split4Cfg<D, NV
       else return make_uint2(qf[v][i][0], qf[v][i][1]);
     };
     const int lim_min = s.len - s.t + 1;                    // keys below it are before or at every row's own
-    const int lo_min = max(0, lim_min - p.window), lo_max = s.len - p.window;   // first keys of the rows' windows
+    const int lo_min = first_key(lim_min, p.window), lo_max = first_key(s.len, p.window);   // the first and the last row's first key
 
     float o[NV][KS][4], m[NV][2], l[NV][2];
 #pragma unroll
@@ -548,58 +548,6 @@ __global__ void __launch_bounds__(Split4Cfg<D, NV, VG>::THREADS, Split4Cfg<D, NV
   if (!ok) set_err(a.err, SWA_DERR_TIMEOUT);
 }
 
-template <typename T, int E>
-__global__ void __launch_bounds__(128) paged4_plain_kernel(const Attend4Params q4) {
-  constexpr int HD = 32 * E;
-  const PagedAttendParams& p = q4.a;
-  const int lane = threadIdx.x & 31;
-  const long long v = (long long)blockIdx.x * 4 + (threadIdx.x >> 5);
-  pdl_wait();
-  pdl_trigger();
-  const int b = blockIdx.y;
-  uint32_t bits = 0;
-  const PagedSeq s = paged_seq(p.map, b, p.T, p.max_rows, bits);
-  const int i = (int)(v / p.nh), h = (int)(v % p.nh), g = h / p.hpg;
-  if (i < s.t && (long long)s.t * p.hpg > p.most) {
-    const int lim = min(s.len, s.len - s.t + i + 1), lo = max(0, lim - q4.window);
-    float q[E], o[E] = {}, m = -INFINITY, l = 0.f;
-    unpack(load_pack<E>(static_cast<const T*>(p.q) + (long long)(s.r0 + i) * p.q_row + (long long)h * HD + lane * E), q);
-    for (int j = 0; j < lim; ++j) {
-      if (j < lo && j >= q4.sinks) j = lo;
-      const int page = p.map.table[(size_t)b * p.map.max_pages + (j >> p.map.page_shift)];
-      const bool ok = page_ok(p.map, page);
-      if (!ok) bits |= SWA_DERR_PAGE;
-      const long long key = ok ? ((((long long)page * p.map.nk + g) << p.map.page_shift) + (j & ((1 << p.map.page_shift) - 1))) : 0;
-      float k[E], w[E], x = 0.f;
-      auto value = [&](const uint8_t* codes, const uint8_t* scales, float (&y)[E]) {
-        const float u = ok ? e4m3_f32(scales[key * (HD / 16) + lane * E / 16]) : 0.f;
-        for (int e = 0; e < E; e += 2) {
-          const uint32_t f = e2m1x2_f16x2<0>(codes[key * (HD / 2) + (lane * E + e) / 2]);
-          const float2 t = __half22float2(*reinterpret_cast<const __half2*>(&f));
-          y[e] = t.x * u;
-          y[e + 1] = t.y * u;
-        }
-      };
-      value(q4.c.k, q4.c.ks, k);
-      value(q4.c.v, q4.c.vs, w);
-      for (int e = 0; e < E; ++e) x += q[e] * k[e];
-      for (int d = 16; d; d >>= 1) x += __shfl_xor_sync(0xffffffffu, x, d);
-      x *= p.qmul;
-      const float mn = fmaxf(m, x), a = ex2(m - mn), e1 = ex2(x - mn);
-      m = mn;
-      l = l * a + e1;
-      for (int e = 0; e < E; ++e) o[e] = o[e] * a + e1 * w[e];
-    }
-    const float inv = l > 0.f ? q4.c.v_mul / l : l;
-    for (int e = 0; e < E; ++e) o[e] = l == 0.f ? 0.f : o[e] * inv;
-    const long long at = ((long long)(s.r0 + i) * p.nh + h) * HD + lane * E;
-    if (p.out_f32) store_pack(static_cast<float*>(p.out) + at, o);
-    else store_pack(static_cast<T*>(p.out) + at, o);
-    if (lane == 0 && p.lse) p.lse[(long long)(s.r0 + i) * p.nh + h] = l == 0.f ? -INFINITY : (m + log2f(l)) * 0.6931471805599453f;
-  }
-  if (bits) set_err(p.err, bits);
-}
-
 // ---------------------------------------------------------------------------
 // Launches
 // ---------------------------------------------------------------------------
@@ -695,9 +643,10 @@ static bool attend4_sizes_ok(const swa_paged4_attend_args* a) {
 // some sequence may be shorter (B * max_rows > T); if not, the chunk kernel takes every sequence.
 struct Attend4Plan {
   Split4Plan split;
+  ChunkPlan chunk;
   bool has_chunk;
   int most;                              // query vectors of a sequence up to which it is the split kernel's
-  size_t bytes;
+  size_t off_chunk, bytes;
 };
 
 static void attend4_plan(const swa_paged4_attend_args* a, Attend4Plan* pl) {
@@ -709,7 +658,11 @@ static void attend4_plan(const swa_paged4_attend_args* a, Attend4Plan* pl) {
     pl->most = split4_vecs(a->cache.hd);
     split4_plan(a, vecs < pl->most ? vecs : pl->most, &pl->split);
   }
-  pl->bytes = pl->split.bytes;
+  pl->off_chunk = pl->bytes = pl->split.bytes;
+  if (pl->has_chunk) {
+    pl->chunk = chunk4_plan(a, max_rows);
+    pl->bytes += pl->chunk.bytes;
+  }
 }
 
 }  // namespace swa
@@ -775,11 +728,7 @@ int swa_paged4_attend(const swa_paged4_attend_args* a, cudaStream_t stream) {
     if (rc != SWA_OK) return rc;
   }
   if (pl.has_chunk) {
-    const dim3 grid((unsigned)(((long long)pa.max_rows * pa.nh + 3) / 4), c.B), block(128);
-    e = c.hd == 64    ? (p.bf ? launch_pdl(paged4_plain_kernel<__nv_bfloat16, 2>, grid, block, 0, stream, p) : launch_pdl(paged4_plain_kernel<__half, 2>, grid, block, 0, stream, p))
-        : c.hd == 128 ? (p.bf ? launch_pdl(paged4_plain_kernel<__nv_bfloat16, 4>, grid, block, 0, stream, p) : launch_pdl(paged4_plain_kernel<__half, 4>, grid, block, 0, stream, p))
-                      : (p.bf ? launch_pdl(paged4_plain_kernel<__nv_bfloat16, 8>, grid, block, 0, stream, p) : launch_pdl(paged4_plain_kernel<__half, 8>, grid, block, 0, stream, p));
-    rc = finish_launch(e);
+    rc = launch_paged4_chunk(c.hd, p, pl.chunk, pl.split.rows ? pl.most : 0, ws + pl.off_chunk, stream);
     if (rc != SWA_OK) return rc;
   }
   if (a->ev_stop && (e = cudaEventRecord(a->ev_stop, stream)) != cudaSuccess) return cuda_status(e);

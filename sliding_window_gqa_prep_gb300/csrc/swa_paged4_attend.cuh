@@ -20,7 +20,14 @@ struct Attend4Params {
 // kLazy4, so they stay below 2^15 < 65504, and one below 2^-14 loses 2^-25: 2^-36 of the row's scale.
 constexpr float kLazy4 = 4.f, kLog24 = 11.f;
 
+// The tensor-core kernel for chunks of many query vectors (swa_paged4_chunk.cuh)
+ChunkPlan chunk4_plan(const swa_paged4_attend_args* a, int max_rows);
+int launch_paged4_chunk(int hd, const Attend4Params& p, const ChunkPlan& plan, int small, char* ws, cudaStream_t s);
+
 #ifdef __CUDACC__
+// First key in the window of a row that sees the slots below lim (none: lim <= 0)
+__device__ __forceinline__ int first_key(int lim, int window) { return max(0, max(0, lim) - window); }
+
 // Tiles of kt keys that a sequence's rows see: the sinks', then those from the first row's window on.
 struct Tiles4 {
   int sink, first, n;          // tiles of sinks in front of tile `first`; all
@@ -28,7 +35,7 @@ struct Tiles4 {
 };
 __device__ __forceinline__ Tiles4 key_tiles(const PagedSeq& s, const Attend4Params& p, int kt) {
   Tiles4 t;
-  const int lo = max(0, s.len - s.t + 1 - p.window);        // the first row's first key
+  const int lo = first_key(s.len - s.t + 1, p.window);      // the first row's
   t.first = lo / kt;
   t.sink = min((min(p.sinks, s.len) + kt - 1) / kt, t.first);
   t.n = s.len > 0 ? t.sink + (s.len + kt - 1) / kt - t.first : 1;   // a row without keys is still written

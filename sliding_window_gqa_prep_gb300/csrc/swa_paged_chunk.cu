@@ -665,3 +665,13 @@ int launch_paged_chunk(const swa_paged_attend_args* a, const PagedAttendParams& 
 }
 
 }  // namespace swa
+
+// The kernel of the 4-bit cache moves registers too: with these, so that all that does stands here.
+namespace swa {
+template <int N>
+__device__ __forceinline__ void regs_give() { asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" :: "n"(N)); }
+template <int N>
+__device__ __forceinline__ void regs_take() { asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" :: "n"(N)); }
+}  // namespace swa
+
+#include "swa_paged4_chunk.cuh"
