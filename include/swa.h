@@ -763,8 +763,8 @@ int swa_paged_evict(const swa_paged_evict_args* args, cudaStream_t stream);
  * most: bf16 holds it, and f16 where 2^exp keeps it in range. Encoding takes
  * scale = max|x| / (6 * 2^exp) of the block, rounded to the nearest e4m3 (ties
  * to the even one, 448 at most), and for each x the nearest of level * scale *
- * 2^exp (ties to the even code, 6 at most). A block whose scale rounds to 0 has
- * codes 0; a block with an infinity or NaN has scale NaN and codes 0, and reads
+ * 2^exp (ties to the even code, 6 at most; zero is code 0, without a sign). A
+ * block whose scale rounds to 0 has codes 0; a block with an infinity or NaN has scale NaN and codes 0, and reads
  * as NaN. exp moves the range (2^-9 to 448, times 6) to where the tensor's values
  * are: with exp = 0 blocks whose largest value is below 0.09 lose bits of their
  * scale.

@@ -31,7 +31,8 @@ def encode_block(x, exp):
     if s == 0:
         return np.zeros(16, np.int64), 0
     u = E4M3[s] * 2.0 ** exp
-    return np.array([nearest(abs(v) / u, LEVELS) + (8 if v < 0 else 0) for v in x]), s
+    c = [nearest(abs(v) / u, LEVELS) for v in x]
+    return np.array([i + 8 if i and v < 0 else i for i, v in zip(c, x)]), s
 
 
 def encode(x, exp):

@@ -1,15 +1,20 @@
 // Rows into and out of the 4-bit paged cache: swa_paged4_append (rotary positions, encoding,
 // and the rotation of q) and swa_paged4_read.
 //
-// Encoding is exact in the sense that the stored codes are those of the formula, not of its
-// f32 arithmetic: the borders between two levels (0.25, 0.75, 1.25, 1.75, 2.5, 3.5, 5 times
-// scale * 2^exp) have seven bits and a comparison of an f32 with them is exact, and a block's
-// largest value / 6 in f32 falls on the same side of a border between two scales as the exact
-// quotient (a border times 6 has seven bits, so a value next to it is at least 2/3 of an ulp of
-// the quotient away). Values that were not rotated are thus encoded exactly. A rotated value is
-// known up to kTol * (|u| + |v|); where that leaves a scale or a code open (one head in some
-// hundreds) the warp takes the angles and the encoding again in f64.
+// Encoding is exact in the sense that the stored codes are those of the formula, not of its f32
+// arithmetic. A border between two levels (0.25, 0.75, 1.25, 1.75, 2.5, 3.5, 5) times a scale has seven
+// bits, and so has six times a border between two scales: an f32 that is not on the border is so far
+// from it that the quotient, correctly rounded, is on the same side. The quotients x / 6 and x / scale
+// are correctly rounded by a product with the rounded reciprocal and one step of correction (all 2^23
+// mantissas were compared, for 6 and for the eight mantissas of a scale). Values that were not rotated
+// are thus encoded exactly. A rotated value is known up to kTol * (|u| + |v|); where that leaves
+// a scale or a code open (one head in some hundreds) the warp takes the angles and the encoding again in f64.
+//
+// Bound by memory and by the instructions of the encoding: a warp takes a head of a row, lane i its
+// features hd / 32 * i and on, so that a pair's other half is in a lane of the same warp, a block's largest value
+// a few shuffles away, and every access consecutive.
 #include <cmath>
+#include <cstring>
 
 #include "swa_paged4.cuh"
 
@@ -20,7 +25,7 @@ struct Rows4Params {
   Pools4 c;
   int T, hd, R;                // rows of a block
   // append: heads [0, nh) are q, [nh, nh + nk) k, [nh + nk, H) v
-  int nh, H, Hg, rot;          // heads of a block
+  int nh, H, Hg, rot, q_bf;    // Hg heads of a block; q_out is bf16, else f16
   float mag;
   const void* q;
   const void* k;
@@ -39,9 +44,9 @@ struct Rows4Params {
 constexpr int kRThreads = 256, kRWarps = kRThreads / 32;
 constexpr int kRRows = 4;          // most rows of a block (append)
 constexpr int kRPairs = 128;       // most pairs of a head
-// The angle's fraction of a turn rounded to f32 (2^-25 half turns: 9.4e-8), sincospif (2 ulp at most:
-// 1.2e-7), mag, two products and their sum (2^-24 each): below 4e-7 of |u| + |v|.
-constexpr float kTol = 0x1p-20f;
+// sincospif is good to an ulp (2^-24), the step by what the angle's f32 leaves to 2^-25, mag to 2^-25, the two
+// products' roundings 2^-25 each: 1.8e-7 of |u| + |v|, times mag.
+constexpr float kTol = 0x1p-22f;
 
 // The last b with row_start[b] <= row (0 if none), by a whole warp: 32 probes a step.
 __device__ __forceinline__ int find_seq4(const int32_t* row_start, int B, int row) {
@@ -84,232 +89,345 @@ __device__ __forceinline__ RowSlot row_slot(const PagedMap& m, int T, int row) {
   return s;
 }
 
-// Lower three bits of the code of y >= 0 in units u (scale * 2^exp): two borders at a time; each
-// comparison is one with a border next to y or one that y is far from. near: y is within tol of one.
-template <typename F>
-__device__ __forceinline__ uint32_t level_code(F y, F u, F tol, bool& near) {
-  const F b4 = F(1.75) * u;
-  const bool c4 = y >= b4;
-  const F b2 = (c4 ? F(3.5) : F(0.75)) * u;
-  const bool c2 = y >= b2;
-  const F b1 = (c4 ? (c2 ? F(5) : F(2.5)) : (c2 ? F(1.25) : F(0.25))) * u;
-  const bool c1 = y > b1;
-  near |= fabs(y - b4) <= tol || fabs(y - b2) <= tol || fabs(y - b1) <= tol;
-  return c4 * 4 + c2 * 2 + c1;
+// Codes -0 become 0, in all nibbles
+__device__ __forceinline__ uint32_t plain_zeros(uint32_t c) { return c & (((c & 0x77777777u) + 0x77777777u) | 0x77777777u); }
+// The codes of two values in units of their scale (ties to even, 6 at most), the first in the lower half
+__device__ __forceinline__ uint32_t f32x2_e2m1(float lo, float hi) {
+  uint32_t d;
+  asm("{\n\t.reg .b8 a;\n\tcvt.rn.satfinite.e2m1x2.f32 a, %1, %2;\n\tcvt.u32.u8 %0, a;\n\t}" : "=r"(d) : "f"(hi), "f"(lo));
+  return d;
 }
-
-// The same from angles in f64, for a warp whose head f32 left open. x, b: this lane's features and
-// their partners; sign: how the partner enters; e: the feature's pair, -1 where it does not turn.
 template <int E>
-__device__ __noinline__ void encode_exact(const float (&x)[E], const float (&b)[E], const int (&e)[E], const float (&sign)[E],
-                                          int pos, const uint64_t* turns, float mag, float div, float mul, uint32_t& codes,
-                                          uint32_t& scale) {
+__device__ __forceinline__ uint32_t codes_of(const float (&z)[E]) {
+  uint32_t c = 0;
+#pragma unroll
+  for (int j = 0; j < E; j += 2) c |= f32x2_e2m1(z[j], z[j + 1]) << (4 * j);
+  return plain_zeros(c);
+}
+
+// The encoding of the blocks that f32 left open, from angles in f64, by the warp of their head. x, b: a lane's
+// features and their partners with the sign that they enter by; e: the feature's pair, -1 where it does not
+// turn. A lane takes one feature of a block: a chain of f64 operations takes long.
+template <int E>
+__device__ __noinline__ void encode_exact(const float (&x)[E], const float (&b)[E], const int (&e)[E], unsigned open, int pos,
+                                          const uint64_t* turns, float mag, float div, uint32_t& codes, uint32_t& scale) {
   constexpr int L = kBlock4 / E;
-  double y[E], top = 0;
+  const int lane = threadIdx.x & 31;
+  while (open) {
+    const int block = (__ffs(open) - 1) / L, i = lane & 15, owner = block * L + i / E;
+    open &= ~(((1u << L) - 1) << (block * L));
+    float xi = 0.f, bi = 0.f;
+    int ei = -1;
 #pragma unroll
-  for (int j = 0; j < E; ++j) {
-    y[j] = x[j];
-    if (e[j] >= 0) {
-      double sn, cs;
-      sincospi((double)(int64_t)((uint64_t)(int64_t)pos * turns[e[j]]) * 0x1p-63, &sn, &cs);
-      y[j] = (x[j] * cs + (double)sign[j] * b[j] * sn) * mag;
+    for (int j = 0; j < E; ++j) {
+      const float xj = __shfl_sync(0xffffffffu, x[j], owner), bj = __shfl_sync(0xffffffffu, b[j], owner);
+      const int ej = __shfl_sync(0xffffffffu, e[j], owner);
+      if (i % E == j) {
+        xi = xj;
+        bi = bj;
+        ei = ej;
+      }
     }
-    top = fmax(top, fabs(y[j]));
-  }
+    double y = xi;
+    if (ei >= 0) {
+      double sn, cs;
+      sincospi((double)(int64_t)((uint64_t)(int64_t)pos * turns[ei]) * 0x1p-63, &sn, &cs);
+      y = ((double)xi * cs + (double)bi * sn) * mag;
+    }
+    y *= div;
+    const double m = fabs(y);
+    double top = m;
 #pragma unroll
-  for (int o = 1; o < L; o <<= 1) top = fmax(top, __shfl_xor_sync(0xffffffffu, top, o));
-  const double t = fmin(top * div / 6.0, 448.0);
-  const int k = t < 0x1p-6 ? -9 : ilogb(t) - 3;          // three bits behind the leading one
-  const double s = scalbn(rint(scalbn(t, -k)), k);
-  scale = f32_e4m3((float)s);
-  codes = 0;
+    for (int o = 1; o < 16; o <<= 1) top = fmax(top, __shfl_xor_sync(0xffffffffu, top, o));
+    const double t = fmin(top / 6.0, 448.0);
+    const int k = t < 0x1p-6 ? -9 : ilogb(t) - 3;        // three bits behind the leading one
+    const double s = scalbn(rint(scalbn(t, -k)), k);
+    uint32_t c = 0;
+    if (s > 0) c = (m > 0.25 * s) + (m >= 0.75 * s) + (m > 1.25 * s) + (m >= 1.75 * s) + (m > 2.5 * s) + (m >= 3.5 * s) + (m > 5.0 * s);
+    if (c && y < 0) c |= 8u;
+    uint32_t mine = 0;
 #pragma unroll
-  for (int j = 0; j < E; ++j) {
-    bool near = false;
-    const uint32_t c = s > 0 ? level_code<double>(fabs(y[j]), s * mul, 0.0, near) | (y[j] < 0 ? 8u : 0u) : 0u;
-    codes |= c << (4 * j);
+    for (int j = 0; j < E; ++j) mine |= __shfl_sync(0xffffffffu, c, (lane % L) * E + j) << (4 * j);
+    if (lane / L == block) {
+      codes = mine;
+      scale = f32_e4m3((float)s);
+    }
   }
 }
 
-template <typename TI, typename TQ, int E>
-__global__ void __launch_bounds__(kRThreads) paged4_append_kernel(const Rows4Params p, const int inter) {
+// PAIRS: how the features of a pair lie. 0: half of the turned ones apart, and a lane's partners are those
+// of one other lane; 1: next to each other; 2: as 0 with partners in two lanes (half % E != 0).
+template <typename TI, int E, int PAIRS>
+__global__ void __launch_bounds__(kRThreads, E == 8 ? 2 : 3) paged4_append_kernel(const __grid_constant__ Rows4Params p) {
   constexpr int HD = 32 * E, L = kBlock4 / E;            // lanes of a block
   __shared__ __align__(16) float s_cos[kRRows * kRPairs], s_sin[kRRows * kRPairs];
-  __shared__ long long s_at[kRRows];
-  __shared__ bool s_live[kRRows];
+  __shared__ long long s_at[kRRows];       // -2: of no sequence, -1: not stored
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const int row0 = blockIdx.x * p.R, nr = min(p.R, p.T - row0), h0 = blockIdx.y * p.Hg, nh = min(p.Hg, p.H - h0);
-  const int half = p.rot >> 1, f0 = lane * E, items = nr * nh;
-  const bool whole = half % E == 0;                      // a lane's partners are as consecutive and as aligned as its features
-  // Head x of the block: this lane's features, and their partners where pairs are halves apart
-  struct Item {
-    int r, h, kind;                                      // 0: q, 1: k, 2: v
-    Pack<TI, E> a, b;
+  const int row0 = blockIdx.x * p.R, nr = min(p.R, p.T - row0), h0 = blockIdx.y * p.Hg, n = min(p.Hg, p.H - h0);
+  const int half = p.rot >> 1, f0 = lane * E, nq = p.nh, nqk = p.nh + p.map.nk;
+  // A warp takes the heads warp, warp + 8, .. of the block, of each all rows at once; the next head's are loaded
+  // while these are worked on (where they are no more than 16 registers).
+  constexpr bool AHEAD = sizeof(TI) * E <= 16;
+  struct Rows {
+    Pack<TI, E> a[kRRows];
   };
-  auto load = [&](int x, Item& it) {
-    if (x >= items) return;
-    it.r = x / nh;
-    it.h = h0 + x - it.r * nh;
-    it.kind = it.h < p.nh ? 0 : it.h < p.nh + p.map.nk ? 1 : 2;
-    const long long row = row0 + it.r;
+  auto load = [&](Rows& t, int x) {
+    const int h = h0 + x;
     const TI* src;
-    if (it.kind == 0) {
-      src = static_cast<const TI*>(p.q) + row * p.q_row;
-    } else if (it.kind == 1) {
-      it.h -= p.nh;
-      src = static_cast<const TI*>(p.k) + row * p.k_row;
+    long long row;
+    if (h < nq) {
+      src = static_cast<const TI*>(p.q) + (long long)h * HD;
+      row = p.q_row;
+    } else if (h < nqk) {
+      src = static_cast<const TI*>(p.k) + (long long)(h - nq) * HD;
+      row = p.k_row;
     } else {
-      it.h -= p.nh + p.map.nk;
-      src = static_cast<const TI*>(p.v) + row * p.v_row;
+      src = static_cast<const TI*>(p.v) + (long long)(h - nqk) * HD;
+      row = p.v_row;
     }
-    src += (long long)it.h * HD;
-    it.a = load_pack<E>(src + f0);
-    if (inter || it.kind == 2 || f0 >= p.rot) return;
-    if (whole) {
-      it.b = load_pack<E>(src + (f0 < half ? f0 + half : f0 - half));
+    src += row0 * row + f0;
+#pragma unroll
+    for (int r = 0; r < kRRows; ++r, src += row)
+      if (r < nr) t.a[r] = load_pack<E>(src);
+  };
+  // The largest of a block's values (as bits: NaN and infinities above all), in units of 2^exp; its scale and
+  // the reciprocal
+  struct Scale {
+    float top, u, inv;
+    uint32_t bits;
+    bool bad, clip;
+  };
+  auto scale_of = [&](const float (&y)[E], float div) {
+    uint32_t m = 0;
+#pragma unroll
+    for (int j = 0; j < E; ++j) m = max(m, __float_as_uint(y[j]) & 0x7fffffffu);
+#pragma unroll
+    for (int o = 1; o < L; o <<= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, o));
+    Scale s;
+    s.bad = m >= 0x7f800000u;
+    s.top = __uint_as_float(m) * div;
+    s.clip = s.top > 4096.f;                             // 448 * 6 and more take the largest scale
+    s.top = fminf(s.top, 4096.f);
+    float q = s.top * (1.f / 6.f);
+    q = fmaf(fmaf(-6.f, q, s.top), 1.f / 6.f, q);
+    s.bits = f32_e4m3(q);
+    s.u = e4m3_f32(s.bits);
+    // correctly rounded: one step from an ulp away (tests/test_gpu_paged4.py has every scale)
+    float inv;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(inv) : "f"(s.u));
+    s.inv = s.u > 0.f ? fmaf(fmaf(-s.u, inv, 1.f), inv, inv) : 0.f;
+    return s;
+  };
+  auto quotients = [&](const float (&y)[E], float div, const Scale& s, float (&z)[E]) {
+#pragma unroll
+    for (int j = 0; j < E; ++j) {
+      const float x = s.clip ? fminf(fmaxf(y[j] * div, -4096.f), 4096.f) : y[j] * div, q = x * s.inv;
+      z[j] = fmaf(fmaf(-q, s.u, x), s.inv, q);
+    }
+  };
+  auto store = [&](bool is_k, long long at, int g, uint32_t codes, uint32_t scale) {
+    const long long key = at + ((long long)g << p.map.page_shift);
+    uint8_t* const to = (is_k ? p.c.k : p.c.v) + key * (HD / 2) + lane * (E / 2);
+    if constexpr (E == 2) *to = (uint8_t)codes;
+    else if constexpr (E == 4) *reinterpret_cast<uint16_t*>(to) = (uint16_t)codes;
+    else *reinterpret_cast<uint32_t*>(to) = codes;
+    if (lane % L == 0) (is_k ? p.c.ks : p.c.vs)[key * (HD / kBlock4) + lane / L] = (uint8_t)scale;
+  };
+  auto work_v = [&](long long at, int g, const Pack<TI, E>& raw) {
+    float x[E], z[E];
+    unpack(raw, x);
+    const Scale s = scale_of(x, p.v_div);
+    quotients(x, p.v_div, s, z);
+    store(false, at, g, s.bad ? 0u : codes_of(z), s.bad ? 0x7fu : s.bits);
+  };
+  // the rotation: y = x cos + b sin, b the partner with its sign, e the pair (-1: none); f0 < half and the partner's
+  // lane are the same for all rows
+  const bool low = f0 < half, exact_mag = p.mag == 1.f;
+  const int partner = (low ? lane + half / E : lane - half / E) & 31, pair0 = low ? f0 : f0 - half;
+  auto rotate = [&](int r, const Pack<TI, E>& raw, const TI* src, float (&x)[E], float (&b)[E], float (&y)[E], int (&e)[E]) {
+    unpack(raw, x);
+#pragma unroll
+    for (int j = 0; j < E; ++j) {
+      y[j] = x[j];
+      e[j] = -1;
+      b[j] = 0.f;
+    }
+    if (PAIRS == 0) {
+      Pack<TI, E> other;                                 // of lane +- half / E
+      constexpr int W = sizeof(raw) / 4;
+      uint32_t mine[W], theirs[W];
+      memcpy(mine, &raw, sizeof(raw));
+#pragma unroll
+      for (int i = 0; i < W; ++i) theirs[i] = __shfl_sync(0xffffffffu, mine[i], partner);
+      memcpy(&other, theirs, sizeof(other));
+      if (f0 < p.rot) {
+        float c[E], sn[E];
+        unpack(load_pack<E>(s_cos + r * half + pair0), c);
+        unpack(load_pack<E>(s_sin + r * half + pair0), sn);
+        unpack(other, b);
+#pragma unroll
+        for (int j = 0; j < E; ++j) {
+          e[j] = pair0 + j;
+          b[j] = low ? -b[j] : b[j];
+          y[j] = fmaf(b[j], sn[j], x[j] * c[j]);
+        }
+      }
     } else {
 #pragma unroll
-      for (int j = 0; j < E; ++j)
-        if (f0 + j < p.rot) it.b.e[j] = src[f0 + j < half ? f0 + j + half : f0 + j - half];
+      for (int j = 0; j < E; ++j) {
+        const int f = f0 + j;
+        if (f >= p.rot) continue;
+        if (PAIRS == 1) {
+          e[j] = f >> 1;
+          b[j] = f & 1 ? x[j ^ 1] : -x[j ^ 1];
+        } else {
+          e[j] = f < half ? f : f - half;
+          b[j] = f < half ? -to_f32(src[f + half]) : to_f32(src[f - half]);
+        }
+        const int i = r * half + e[j];
+        y[j] = fmaf(b[j], s_sin[i], x[j] * s_cos[i]);
+      }
     }
+  };
+  auto work_q = [&](int r, int h, const Pack<TI, E>& raw) {
+    float x[E], b[E], y[E];
+    int e[E];
+    rotate(r, raw, static_cast<const TI*>(p.q) + (row0 + r) * p.q_row + (long long)h * HD, x, b, y, e);
+    if (s_at[r] == -2) return;
+    const long long to = ((long long)(row0 + r) * nq + h) * HD + f0;
+    if (p.q_bf) store_pack(static_cast<__nv_bfloat16*>(p.q_out) + to, y);
+    else store_pack(static_cast<__half*>(p.q_out) + to, y);
+  };
+  auto work_k = [&](int r, int g, const Pack<TI, E>& raw) {
+    float x[E], b[E], y[E];
+    int e[E];
+    rotate(r, raw, static_cast<const TI*>(p.k) + (row0 + r) * p.k_row + (long long)g * HD, x, b, y, e);
+    const long long at = s_at[r];
+    if (at < 0) return;
+    const Scale s = scale_of(y, p.k_div);
+    float tol = 0.f, z[E], lo[E], hi[E];
+#pragma unroll
+    for (int j = 0; j < E; ++j)
+      if (e[j] >= 0 && !(exact_mag && s_sin[r * half + e[j]] == 0.f)) tol = fmaxf(tol, fabsf(x[j]) + fabsf(b[j]));   // no angle: y is exact
+    tol *= kTol * fabsf(p.mag) * p.k_div;
+    float tol_top = tol;
+#pragma unroll
+    for (int o = 1; o < L; o <<= 1) tol_top = fmaxf(tol_top, __shfl_xor_sync(0xffffffffu, tol_top, o));
+    quotients(y, p.k_div, s, z);
+#pragma unroll
+    for (int j = 0; j < E; ++j) {
+      lo[j] = z[j] - tol * s.inv;
+      hi[j] = z[j] + tol * s.inv;
+    }
+    uint32_t codes = codes_of(lo), scale = s.bits;
+    const bool open = !s.bad && (codes != codes_of(hi) || (tol_top > 0.f && f32_e4m3((s.top - tol_top) * (1.f / 6.f)) !=
+                                                                                f32_e4m3((s.top + tol_top) * (1.f / 6.f))));
+    const unsigned any = __ballot_sync(0xffffffffu, open);
+    if (any) encode_exact<E>(x, b, e, any, p.pos[row0 + r], p.turns, p.mag, p.k_div, codes, scale);
+    store(true, at, g, s.bad ? 0u : codes, s.bad ? 0x7fu : scale);
   };
   pdl_wait();
   pdl_trigger();
-  Item cur, next;
-  load(warp, cur);
+  Rows cur;
+  if (warp < n) load(cur, warp);
   for (int i = tid; i < nr * half; i += kRThreads) {
     const int r = i / half, e = i % half;
     const uint64_t frac = (uint64_t)(int64_t)p.pos[row0 + r] * p.turns[e];   // modulo 2^64: the fraction of a turn
+    const int32_t turn = (int32_t)(uint32_t)(frac >> 32);                    // in 2^-31 half turns
+    const float f = (float)turn;
     float sn, cs;
-    sincospif((float)(int32_t)(uint32_t)(frac >> 32) * 0x1p-31f, &sn, &cs);
-    s_cos[i] = cs * p.mag;
-    s_sin[i] = sn * p.mag;
+    sincospif(f * 0x1p-31f, &sn, &cs);
+    // what f lacks, in radians: below 2^-24, and 0 only where the angle is a whole number of half turns
+    const float rest = fmaf((float)(turn - (int32_t)f), 0x1p-31f * 3.14159265f, (float)(uint32_t)frac * (0x1p-63f * 3.14159265f));
+    s_cos[i] = fmaf(-sn, rest, cs) * p.mag;
+    s_sin[i] = fmaf(cs, rest, sn) * p.mag;
   }
-  const int r = kRWarps - 1 - warp;                      // the last warps: the first ones hold angles
-  if (r < nr) {
+  if (const int r = kRWarps - 1 - warp; r < nr) {        // the last warps: the first ones hold angles
     const RowSlot s = row_slot(p.map, p.T, row0 + r);
     if (lane == 0) {
-      s_live[r] = s.live;
-      s_at[r] = s.at;
+      s_at[r] = s.live ? s.at : -2;
       if (s.bits && blockIdx.y == 0) set_err(p.err, s.bits);
     }
   }
   __syncthreads();
-
-  for (int x = warp; x < items; x += kRWarps) {
-    load(x + kRWarps, next);
-    const long long at = s_at[cur.r];
-    if (s_live[cur.r] && (cur.kind == 0 || at >= 0)) {
-      float a[E], b[E], y[E], sign[E];
-      int e[E];
-      unpack(cur.a, a);
+#pragma unroll 1
+  for (int x = warp; x < n; x += kRWarps) {
+    Rows next;
+    if (AHEAD && x + kRWarps < n) load(next, x + kRWarps);
+    const int h = h0 + x;
+    if (h < nq) {
 #pragma unroll
-      for (int j = 0; j < E; ++j) {
-        const int f = f0 + j;
-        e[j] = -1;
-        sign[j] = 0.f;
-        b[j] = 0.f;
-        y[j] = a[j];
-        if (cur.kind == 2 || f >= p.rot) continue;
-        if (inter) {
-          e[j] = f >> 1;
-          sign[j] = f & 1 ? 1.f : -1.f;
-          b[j] = a[j ^ 1];
-        } else {
-          e[j] = f < half ? f : f - half;
-          sign[j] = f < half ? -1.f : 1.f;
-          b[j] = to_f32(cur.b.e[j]);
-        }
-        const int i = cur.r * half + e[j];
-        y[j] = a[j] * s_cos[i] + sign[j] * b[j] * s_sin[i];
-      }
-      if (cur.kind == 0) {
-        store_pack(static_cast<TQ*>(p.q_out) + ((long long)(row0 + cur.r) * p.nh + cur.h) * HD + f0, y);
-      } else {
-        const bool is_k = cur.kind == 1;
-        const float div = is_k ? p.k_div : p.v_div, mul = is_k ? p.c.k_mul : p.c.v_mul;
-        float top = 0.f, tol[E], tol_top = 0.f;
-        bool bad = false;
+      for (int r = 0; r < kRRows; ++r)
+        if (r < nr) work_q(r, h, cur.a[r]);
+    } else if (h < nqk) {
 #pragma unroll
-        for (int j = 0; j < E; ++j) {
-          top = fmaxf(top, fabsf(y[j]));
-          bad |= !(fabsf(y[j]) <= 3.402823466e38f);
-          tol[j] = e[j] >= 0 ? kTol * fabsf(p.mag) * (fabsf(a[j]) + fabsf(b[j])) : 0.f;
-          tol_top = fmaxf(tol_top, tol[j]);
-        }
+      for (int r = 0; r < kRRows; ++r)
+        if (r < nr) work_k(r, h - nq, cur.a[r]);
+    } else {
 #pragma unroll
-        for (int o = 1; o < L; o <<= 1) {
-          top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-          tol_top = fmaxf(tol_top, __shfl_xor_sync(0xffffffffu, tol_top, o));
-          bad |= __shfl_xor_sync(0xffffffffu, (int)bad, o) != 0;
-        }
-        uint32_t scale = f32_e4m3(top * div / 6.f), codes = 0;
-        bool open = tol_top > 0.f && f32_e4m3((top - tol_top) * div / 6.f) != f32_e4m3((top + tol_top) * div / 6.f);
-        const float u = e4m3_f32(scale) * mul;
-#pragma unroll
-        for (int j = 0; j < E; ++j) {
-          bool near = false;
-          const uint32_t c = u > 0.f ? level_code<float>(fabsf(y[j]), u, tol[j], near) | (y[j] < 0.f ? 8u : 0u) : 0u;
-          codes |= c << (4 * j);
-          open |= near && tol[j] > 0.f;
-        }
-        if (__any_sync(0xffffffffu, open && !bad))
-          encode_exact<E>(a, b, e, sign, p.pos[row0 + cur.r], p.turns, p.mag, div, mul, codes, scale);
-        if (bad) {
-          codes = 0;
-          scale = 0x7f;
-        }
-        const long long key = at + ((long long)cur.h << p.map.page_shift);
-        uint8_t* const to = (is_k ? p.c.k : p.c.v) + key * (HD / 2) + lane * (E / 2);
-        if constexpr (E == 2) *to = (uint8_t)codes;
-        else if constexpr (E == 4) *reinterpret_cast<uint16_t*>(to) = (uint16_t)codes;
-        else *reinterpret_cast<uint32_t*>(to) = codes;
-        if (lane % L == 0) (is_k ? p.c.ks : p.c.vs)[key * (HD / kBlock4) + lane / L] = (uint8_t)scale;
-      }
+      for (int r = 0; r < kRRows; ++r)
+        if (r < nr && s_at[r] >= 0) work_v(s_at[r], h - nqk, cur.a[r]);
     }
-    cur = next;
+    if (AHEAD) cur = next;
+    else if (x + kRWarps < n) load(cur, x + kRWarps);
   }
 }
 
-// A thread takes 8 features at a time.
+// A block takes some rows and heads (all of them, or one row's) in the order of the output; their keys' numbers
+// stand in shared memory. A thread has the same 8 features of every head that it takes.
+constexpr int kReadRows = 32, kReadHeads = 256, kReadKeys = 1024;   // most rows, heads and keys of a block
 template <typename TO, int HD>
-__global__ void __launch_bounds__(kRThreads) paged4_read_kernel(const Rows4Params p) {
-  constexpr int U = HD / 8;
-  __shared__ long long s_at[kRWarps];
-  __shared__ bool s_live[kRWarps];
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, nk = p.map.nk;
-  const int row0 = blockIdx.x * p.R, nr = min(p.R, p.T - row0);
+__global__ void __launch_bounds__(kRThreads, 6) paged4_read_kernel(const __grid_constant__ Rows4Params p) {
+  constexpr int U = HD / 8, STEP = kRThreads / U, N = 4;
+  __shared__ int s_key[kReadKeys];         // -2: of no sequence, -1: zeros
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int row0 = blockIdx.x * p.R, nr = min(p.R, p.T - row0), h0 = blockIdx.y * p.Hg, nh = min(p.Hg, p.map.nk - h0);
   pdl_wait();
   pdl_trigger();
-  if (warp < nr) {
-    const RowSlot s = row_slot(p.map, p.T, row0 + warp);
-    if (lane == 0) {
-      s_live[warp] = s.live;
-      s_at[warp] = s.at;
-      if (s.bits) set_err(p.err, s.bits);
-    }
+  for (int r = warp; r < nr; r += kRWarps) {
+    const RowSlot s = row_slot(p.map, p.T, row0 + r);
+    for (int g = lane; g < nh; g += 32)
+      s_key[r * nh + g] = !s.live ? -2 : s.at < 0 ? -1 : (int)(s.at + ((long long)(h0 + g) << p.map.page_shift));   // below 2^31
+    if (lane == 0 && s.bits && blockIdx.y == 0) set_err(p.err, s.bits);
   }
   __syncthreads();
-  const int units = 2 * nr * nk * U;                     // K of all rows, then V: below 2^26
-  for (int x = tid; x < units; x += kRThreads) {
-    const int u = x % U, y = x / U, z = y / nk, g = y - z * nk, r = z < nr ? z : z - nr;
-    const bool is_v = z >= nr;
-    TO* const out = static_cast<TO*>(is_v ? p.v_out : p.k_out);
-    if (!out || !s_live[r]) continue;
-    float f[8] = {};
-    if (s_at[r] >= 0) {
-      const long long key = s_at[r] + ((long long)g << p.map.page_shift);
-      const uint32_t c = *reinterpret_cast<const uint32_t*>((is_v ? p.c.v : p.c.k) + key * (HD / 2) + u * 4);
-      const float s = e4m3_f32((is_v ? p.c.vs : p.c.ks)[key * (HD / kBlock4) + u / 2]) * (is_v ? p.c.v_mul : p.c.k_mul);
-      const uint32_t h[4] = {e2m1x2_f16x2<0>(c), e2m1x2_f16x2<1>(c), e2m1x2_f16x2<2>(c), e2m1x2_f16x2<3>(c)};
+  const int u = tid % U, keys = nr * nh;
+  const long long base = ((long long)row0 * p.map.nk + h0) * HD + u * 8;
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const float2 t = __half22float2(*reinterpret_cast<const __half2*>(&h[i]));
-        f[2 * i] = t.x * s;
-        f[2 * i + 1] = t.y * s;
+  for (int side = 0; side < 2; ++side) {
+    TO* const out = static_cast<TO*>(side ? p.v_out : p.k_out) + base;
+    if (!(side ? p.v_out : p.k_out)) continue;
+    const uint8_t* const codes = (side ? p.c.v : p.c.k) + u * 4;
+    const uint8_t* const scales = (side ? p.c.vs : p.c.ks) + u / 2;
+    const float mul = side ? p.c.v_mul : p.c.k_mul;
+    for (int y0 = tid / U; y0 < keys; y0 += N * STEP) {
+      uint32_t c[N], s[N];
+      int key[N];
+#pragma unroll
+      for (int i = 0; i < N; ++i) {
+        const int y = y0 + i * STEP;
+        key[i] = y < keys ? s_key[y] : -2;
+        c[i] = s[i] = 0;
+        if (key[i] >= 0) {
+          c[i] = *reinterpret_cast<const uint32_t*>(codes + (long long)key[i] * (HD / 2));
+          s[i] = scales[(long long)key[i] * (HD / kBlock4)];
+        }
+      }
+#pragma unroll
+      for (int i = 0; i < N; ++i) {
+        if (key[i] == -2) continue;
+        const float m = e4m3_f32(s[i]) * mul;
+        const uint32_t h[4] = {e2m1x2_f16x2<0>(c[i]), e2m1x2_f16x2<1>(c[i]), e2m1x2_f16x2<2>(c[i]), e2m1x2_f16x2<3>(c[i])};
+        float f[8];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          const float2 t = __half22float2(*reinterpret_cast<const __half2*>(&h[k]));
+          f[2 * k] = t.x * m;
+          f[2 * k + 1] = t.y * m;
+        }
+        store_pack(out + (long long)(y0 + i * STEP) * HD, f);
       }
     }
-    store_pack(out + ((long long)(row0 + r) * nk + g) * HD + u * 8, f);
   }
 }
 
@@ -353,24 +471,37 @@ void paged4_spans(const swa_paged4_cache* c, Span4 (&s)[4]) {
   s[3] = {c->v_scale, keys * c->hd / kBlock4};
 }
 
-template <typename TI, typename TQ>
+template <typename TI, int E>
+static cudaError_t launch_pairs(const Rows4Params& p, int inter, dim3 grid, cudaStream_t s) {
+  const dim3 block(kRThreads);
+  if (inter) return launch_pdl(paged4_append_kernel<TI, E, 1>, grid, block, 0, s, p);
+  if (p.rot / 2 % E == 0) return launch_pdl(paged4_append_kernel<TI, E, 0>, grid, block, 0, s, p);
+  return launch_pdl(paged4_append_kernel<TI, E, 2>, grid, block, 0, s, p);
+}
+
+template <typename TI>
 static int launch_append(Rows4Params& p, int inter, cudaStream_t s) {
   // all heads of kRRows rows once that gives every SM four blocks, else a row and a head a warp
   const long long sms = num_sms() > 0 ? num_sms() : 148;
   p.R = p.T >= 4 * sms * kRRows ? kRRows : 1;
   p.Hg = p.T >= 4 * sms ? p.H : kRWarps;
   if ((p.H + p.Hg - 1) / p.Hg > 65535) p.Hg = (p.H + 65534) / 65535;
-  const dim3 grid((unsigned)((p.T + p.R - 1) / p.R), (unsigned)((p.H + p.Hg - 1) / p.Hg)), block(kRThreads);
-  return finish_launch(p.hd == 64    ? launch_pdl(paged4_append_kernel<TI, TQ, 2>, grid, block, 0, s, p, inter)
-                       : p.hd == 128 ? launch_pdl(paged4_append_kernel<TI, TQ, 4>, grid, block, 0, s, p, inter)
-                                     : launch_pdl(paged4_append_kernel<TI, TQ, 8>, grid, block, 0, s, p, inter));
+  const dim3 grid((unsigned)((p.T + p.R - 1) / p.R), (unsigned)((p.H + p.Hg - 1) / p.Hg));
+  return finish_launch(p.hd == 64 ? launch_pairs<TI, 2>(p, inter, grid, s) : p.hd == 128 ? launch_pairs<TI, 4>(p, inter, grid, s)
+                                                                                        : launch_pairs<TI, 8>(p, inter, grid, s));
 }
 
 template <typename TO>
 static int launch_read(Rows4Params& p, cudaStream_t s) {
   const long long sms = num_sms() > 0 ? num_sms() : 148;
-  p.R = p.T >= 8 * sms * kRWarps ? kRWarps : p.T >= 16 * sms ? 2 : 1;
-  const dim3 grid((unsigned)((p.T + p.R - 1) / p.R)), block(kRThreads);
+  // rows of a block: 8 heads a thread and array, if that leaves every SM two blocks
+  const long long row = (long long)p.map.nk * p.hd / 8, most = 8 * kRThreads / row;
+  long long R = p.T / (2 * sms);
+  R = R > most ? most : R;
+  R = R > kReadRows ? kReadRows : R < 1 || p.map.nk > kReadHeads ? 1 : R;
+  p.Hg = p.map.nk < kReadHeads ? p.map.nk : kReadHeads;
+  p.R = (int)(R * p.Hg > kReadKeys ? kReadKeys / p.Hg : R);
+  const dim3 grid((unsigned)((p.T + p.R - 1) / p.R), (unsigned)((p.map.nk + p.Hg - 1) / p.Hg)), block(kRThreads);
   return finish_launch(p.hd == 64    ? launch_pdl(paged4_read_kernel<TO, 64>, grid, block, 0, s, p)
                        : p.hd == 128 ? launch_pdl(paged4_read_kernel<TO, 128>, grid, block, 0, s, p)
                                      : launch_pdl(paged4_read_kernel<TO, 256>, grid, block, 0, s, p));
@@ -429,11 +560,11 @@ int swa_paged4_append(const swa_paged4_append_args* a, cudaStream_t stream) {
   p.k_div = 1.f / p.c.k_mul; p.v_div = 1.f / p.c.v_mul;
   p.err = a->err;
   const int inter = a->interleaved != 0;
-  const bool bf = a->q_dtype == SWA_BF16;
+  p.q_bf = a->q_dtype == SWA_BF16;
   switch (a->src) {
-    case SWA_F32: return bf ? launch_append<float, __nv_bfloat16>(p, inter, stream) : launch_append<float, __half>(p, inter, stream);
-    case SWA_BF16: return bf ? launch_append<__nv_bfloat16, __nv_bfloat16>(p, inter, stream) : launch_append<__nv_bfloat16, __half>(p, inter, stream);
-    default: return bf ? launch_append<__half, __nv_bfloat16>(p, inter, stream) : launch_append<__half, __half>(p, inter, stream);
+    case SWA_F32: return launch_append<float>(p, inter, stream);
+    case SWA_BF16: return launch_append<__nv_bfloat16>(p, inter, stream);
+    default: return launch_append<__half>(p, inter, stream);
   }
 }
 
