@@ -951,7 +951,8 @@ typedef struct swa_paged_fork_args {
   size_t workspace_bytes;
   uint32_t* err;
 } swa_paged_fork_args;
-/* Bytes of workspace for these sizes (0: invalid sizes). */
+/* Bytes of workspace for these sizes (0: invalid sizes; 1: none is needed, the
+ * workspace may be NULL). */
 size_t swa_paged_fork_workspace_size(const swa_paged_fork_args* args);
 int swa_paged_fork(const swa_paged_fork_args* args, cudaStream_t stream);
 
@@ -982,7 +983,8 @@ typedef struct swa_paged_compact_args {
   size_t workspace_bytes;
   uint32_t* err;
 } swa_paged_compact_args;
-/* Bytes of workspace for these sizes (0: invalid sizes). */
+/* Bytes of workspace for these sizes (0: invalid sizes; 1: none is needed, the
+ * workspace may be NULL). */
 size_t swa_paged_compact_workspace_size(const swa_paged_compact_args* args);
 int swa_paged_compact(const swa_paged_compact_args* args, cudaStream_t stream);
 

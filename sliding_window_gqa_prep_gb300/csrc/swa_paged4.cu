@@ -28,18 +28,18 @@
 
 namespace swa {
 
-constexpr int kKeys4 = 64;           // keys of a tile
 constexpr int kWarps4 = 4;           // warps that compute
-constexpr int kMin4 = 4;             // a CTA takes at least this many tiles
+constexpr int kMinKeys4 = 256;       // a CTA takes at least this many keys
 
 // A warp has NV tiles of 8 query vectors; VG groups of warps share a tile's keys and have other vectors.
 template <int D, int NV, int VG>
 struct Split4Cfg {
   static constexpr int THREADS = kWarps4 * 32 + 32;         // and the warp that copies
-  static constexpr int CODES = kKeys4 * D / 2, SCALES = kKeys4 * D / 16, STAGE = 2 * (CODES + SCALES);
+  static constexpr int KT = D == 256 ? 64 : 128;            // keys of a tile
+  static constexpr int CODES = KT * D / 2, SCALES = KT * D / 16, STAGE = 2 * (CODES + SCALES);
   static constexpr int ROWS = 8 * NV * VG;                  // query vectors
   static constexpr bool QS = NV * D > 128;                  // Q^T waits in shared memory, not in registers
-  static constexpr int CTAS = NV * D <= 128 && VG == 1 && D == 64 ? 4 : 3;   // an SM: 96 or 128 registers a thread
+  static constexpr int CTAS = D == 64 && NV == 1 ? 4 : 3;   // an SM: 96 or 128 registers a thread
   static constexpr int JT = 4 / NV;                         // 16-feature tiles of O that the warps join at a time
   static constexpr int JOIN = kWarps4 * JT * NV * 512;      // bytes: 8 KB
   static constexpr int QB = QS ? ROWS * D * 2 : 0;
@@ -59,19 +59,6 @@ __device__ __forceinline__ uint32_t high_halves(uint32_t a, uint32_t b) { return
 template <int I>
 __device__ __forceinline__ uint32_t codes_pair(const uint32_t* w) { return e2m1x2_f16x2<(I & 3)>(w[I >> 2]); }
 
-// W words from shared memory, aligned to their number
-template <int W>
-__device__ __forceinline__ void lds_words(uint32_t (&r)[W], const unsigned char* p) {
-  if constexpr (W == 1) {
-    r[0] = *reinterpret_cast<const uint32_t*>(p);
-  } else if constexpr (W == 2) {
-    const uint2 v = *reinterpret_cast<const uint2*>(p);
-    r[0] = v.x; r[1] = v.y;
-  } else {
-    const uint4 v = *reinterpret_cast<const uint4*>(p);
-    r[0] = v.x; r[1] = v.y; r[2] = v.z; r[3] = v.w;
-  }
-}
 template <int I, int N, typename F>
 __device__ __forceinline__ void unrolled(F f) {
   if constexpr (I < N) {
@@ -126,16 +113,16 @@ __device__ __forceinline__ void store_pair4(const Attend4Params& p, long long at
 
 // Tiles of one (sequence, KV head): none where the sequence has no rows or more query
 // vectors than this kernel takes.
-__device__ __forceinline__ Tiles4 split4_tiles(const PagedSeq& s, const Attend4Params& p) {
+__device__ __forceinline__ Tiles4 split4_tiles(const PagedSeq& s, const Attend4Params& p, int kt) {
   if (s.t == 0 || (long long)s.t * p.a.hpg > p.a.most) return {0, 0, 0};
-  return key_tiles(s, p, kKeys4);
+  return key_tiles(s, p, kt);
 }
 
 template <int D, int NV, int VG>
 __global__ void __launch_bounds__(Split4Cfg<D, NV, VG>::THREADS, Split4Cfg<D, NV, VG>::CTAS)
     paged4_split_kernel(const __grid_constant__ Attend4Params p) {
   using C = Split4Cfg<D, NV, VG>;
-  constexpr int ST = C::ST, KS = D / 16, NW = C::THREADS / 32, KG = kWarps4 / VG;
+  constexpr int ST = C::ST, KT = C::KT, KS = D / 16, NW = C::THREADS / 32, KG = kWarps4 / VG, SUBS = KT / 16 / KG;
   constexpr bool QS = C::QS;
   extern __shared__ unsigned char sm_raw[];
   __shared__ __align__(8) uint64_t b_full[ST], b_empty[ST];
@@ -146,8 +133,10 @@ __global__ void __launch_bounds__(Split4Cfg<D, NV, VG>::THREADS, Split4Cfg<D, NV
   __shared__ float s_shift[C::ROWS];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   unsigned char* const sm = reinterpret_cast<unsigned char*>((reinterpret_cast<uintptr_t>(sm_raw) + 127) & ~(uintptr_t)127);
+  const uint32_t smb = smem_u32(sm);
   float* const join = reinterpret_cast<float*>(sm + ST * C::STAGE);
   uint2* const s_q = reinterpret_cast<uint2*>(sm + ST * C::STAGE + C::JOIN);   // [8-vector tile][step][lane]
+  const uint32_t q_base = smb + ST * C::STAGE + C::JOIN + lane * 8;
   const PagedAttendParams& a = p.a;
   if (tid == 0) {
     for (int i = 0; i < ST; ++i) {
@@ -166,7 +155,7 @@ __global__ void __launch_bounds__(Split4Cfg<D, NV, VG>::THREADS, Split4Cfg<D, NV
   if (a.whole) {
     if (tid == 0) {
       const int b = blockIdx.x / a.map.nk;
-      const int n = split4_tiles(paged_seq(a.map, b, a.T, a.max_rows, bits), p).n;
+      const int n = split4_tiles(paged_seq(a.map, b, a.T, a.max_rows, bits), p, KT).n;
       if (bits) set_err(a.err, bits);
       if (n > 0) s_b = b;
       s_off = (long long)(blockIdx.x % a.map.nk) * n;
@@ -178,7 +167,7 @@ __global__ void __launch_bounds__(Split4Cfg<D, NV, VG>::THREADS, Split4Cfg<D, NV
     long long mine = 0;
     for (int e = 0; e < E; ++e) {
       const int b = tid * E + e;
-      if (b < a.map.B) mine += (long long)a.map.nk * split4_tiles(paged_seq(a.map, b, a.T, a.max_rows, bits), p).n;
+      if (b < a.map.B) mine += (long long)a.map.nk * split4_tiles(paged_seq(a.map, b, a.T, a.max_rows, bits), p, KT).n;
     }
     if (bits && blockIdx.x == 0) set_err(a.err, bits);
     long long incl = mine;
@@ -195,14 +184,14 @@ __global__ void __launch_bounds__(Split4Cfg<D, NV, VG>::THREADS, Split4Cfg<D, NV
       total += s_scan[w];
     }
     long long per = (total + gridDim.x - 1) / gridDim.x;
-    if (per < kMin4) per = kMin4;
+    if (per < kMinKeys4 / KT) per = kMinKeys4 / KT;
     const long long u0 = per * blockIdx.x;
     if (u0 >= before && u0 < before + mine) {
       long long off = u0 - before;
       for (int e = 0; e < E; ++e) {
         const int b = tid * E + e;
         uint32_t ignore = 0;
-        const long long n = (long long)a.map.nk * split4_tiles(paged_seq(a.map, b, a.T, a.max_rows, ignore), p).n;
+        const long long n = (long long)a.map.nk * split4_tiles(paged_seq(a.map, b, a.T, a.max_rows, ignore), p, KT).n;
         if (off < n) {
           s_b = b;
           s_off = off;
@@ -216,7 +205,7 @@ __global__ void __launch_bounds__(Split4Cfg<D, NV, VG>::THREADS, Split4Cfg<D, NV
   }
   const long long total = s_total;
   long long per = (total + gridDim.x - 1) / gridDim.x;
-  if (per < kMin4) per = kMin4;
+  if (per < kMinKeys4 / KT) per = kMinKeys4 / KT;
   if (a.whole) per = total;
   const long long u0 = a.whole ? 0 : per * blockIdx.x;
   if (tid == 0 && !a.whole) a.ws_desc[blockIdx.x] = make_int4(-1, 0, 0, 0);
@@ -226,7 +215,7 @@ __global__ void __launch_bounds__(Split4Cfg<D, NV, VG>::THREADS, Split4Cfg<D, NV
   int b = s_b;
   uint32_t ignore = 0;
   PagedSeq s = paged_seq(a.map, b, a.T, a.max_rows, ignore);
-  Tiles4 tl = split4_tiles(s, p);
+  Tiles4 tl = split4_tiles(s, p, KT);
   int tile0 = (int)(s_off % tl.n), g = (int)(s_off / tl.n);
   auto next_item = [&](int tile1) {         // false at the end
     left -= tile1 - tile0;
@@ -236,27 +225,26 @@ __global__ void __launch_bounds__(Split4Cfg<D, NV, VG>::THREADS, Split4Cfg<D, NV
       g = 0;
       do {
         s = paged_seq(a.map, ++b, a.T, a.max_rows, ignore);
-        tl = split4_tiles(s, p);
+        tl = split4_tiles(s, p, KT);
       } while (tl.n == 0);
     }
     return true;
   };
-  int it = 0;                               // tiles of this share so far: stage it % ST
-
   if (warp == kWarps4) {
     // ------------------------------------------------------------ copies: a run of keys of one array a lane
-    const int page = 1 << a.map.page_shift, rows = min(page, kKeys4), runs = kKeys4 / rows;   // 4 * runs <= 32
+    const int page = 1 << a.map.page_shift, rows = min(page, KT), runs = KT / rows;   // 4 * runs <= 32
     const int arr = lane / runs, run = lane % runs;      // 0: K codes, 1: V codes, 2: K scales, 3: V scales
     const bool mine = arr < 4, codes = arr < 2;
     const uint8_t* const src = arr == 0 ? p.c.k : arr == 1 ? p.c.v : arr == 2 ? p.c.ks : p.c.vs;
     const int row = codes ? D / 2 : D / 16;
     const int dst = (codes ? arr * C::CODES : 2 * C::CODES + (arr - 2) * C::SCALES) + run * rows * row;
     bool ok = true;
+    int it = 0;                             // tiles of this share so far: stage it % ST
     do {
       const int tile1 = (int)min((long long)tl.n, tile0 + left);
       const int32_t* table = a.map.table + (size_t)b * a.map.max_pages;
       for (int x = tile0; ok && x < tile1; ++x, ++it) {
-        const int key = tl.at(x) * kKeys4 + run * rows, st = it % ST;
+        const int key = tl.at(x) * KT + run * rows, st = it % ST;
         const uint8_t* from = nullptr;
         bool blank = false;
         if (mine && key < s.len) {          // looked up before the wait
@@ -296,6 +284,8 @@ __global__ void __launch_bounds__(Split4Cfg<D, NV, VG>::THREADS, Split4Cfg<D, NV
   // then find rows of both parities, and fewer of them in the same banks
   auto key_of = [](int i) { return i ^ ((i >> 1) & 1); };
   bool ok = true;                           // a thread whose wait gave up goes on and writes nothing
+  int st = 0;                               // the next tile's stage, and the parity of its barrier's phase
+  uint32_t phase = 0;
   do {
     const int tile1 = (int)min((long long)tl.n, tile0 + left);
     const int nvec = s.t * hpg;
@@ -325,62 +315,91 @@ __global__ void __launch_bounds__(Split4Cfg<D, NV, VG>::THREADS, Split4Cfg<D, NV
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
         const int c = (vg * NV + v) * 8 + 2 * lt + e;
-        if constexpr (QS) qm[v][e] = a.qmul * s_shift[c];
-        else qm[v][e] = a.qmul * __shfl_sync(0xffffffffu, shift, (2 * lt + e) * 4);
+        if constexpr (QS) shift = s_shift[c];
+        qm[v][e] = fmaxf(a.qmul * (QS ? shift : __shfl_sync(0xffffffffu, shift, (2 * lt + e) * 4)), 0x1p-126f);   // masked scores stay -inf
         lim[v][e] = c < nvec ? max(0, min(s.len, s.len - s.t + c / hpg + 1)) : 0;
       }
     }
     auto q_at = [&](int v, int i) {
-      if constexpr (QS) return s_q[((vg * NV + v) * KS + i) * 32 + lane];
-      else return make_uint2(qf[v][i][0], qf[v][i][1]);
+      if constexpr (QS) {
+        uint32_t w[2];
+        lds_words<2>(w, q_base + ((vg * NV + v) * KS + i) * 256);
+        return make_uint2(w[0], w[1]);
+      } else {
+        return make_uint2(qf[v][i][0], qf[v][i][1]);
+      }
     };
     const int lim_min = s.len - s.t + 1;                    // keys below it are before or at every row's own
     const int lo_min = first_key(lim_min, p.window), lo_max = first_key(s.len, p.window);   // the first and the last row's first key
 
-    float o[NV][KS][4], m[NV][2], l[NV][2];
+    // off: kLog24 less the running maximum, once a key was seen; bar: the products above which it is raised
+    float o[NV][KS][4], l[NV][2], off[NV][2], bar[NV][2];
+    int seen[NV];
 #pragma unroll
     for (int v = 0; v < NV; ++v) {
 #pragma unroll
       for (int j = 0; j < KS; ++j)
 #pragma unroll
         for (int e = 0; e < 4; ++e) o[v][j][e] = 0.f;
-      m[v][0] = m[v][1] = -INFINITY;
+      off[v][0] = off[v][1] = kLog24;
+      bar[v][0] = bar[v][1] = -INFINITY;
+      seen[v] = 0;
       l[v][0] = l[v][1] = 0.f;
     }
 
-    for (int x = tile0; x < tile1; ++x, ++it) {
-      const int st = it % ST;
-      ok &= tc_wait(&b_full[st], (uint32_t)((it / ST) & 1), &s_abort);
+    // this lane's keys of 16 in S (ka and ka + 8) and in P V (k1, k2 and these + 8), and its places in a stage
+    const int ka = key_of(lg), k1 = key_of(2 * lt), k2 = key_of(2 * lt + 1);
+    constexpr int W = D == 64 ? 2 : 4, CH = D == 256 ? 2 : 1;        // words of a key in S at a time, and how often
+    constexpr int VW = D / 64;                                       // words of a key in P V
+    const uint32_t group0 = smb + (warp % KG) * SUBS * 16 * (D / 2), scale0 = smb + 2 * C::CODES + (warp % KG) * SUBS * 16 * (D / 16);
+    const uint32_t at_k = group0 + ka * (D / 2) + lt * (W * 4), at_ks = scale0 + ka * (D / 16) + (D == 64 ? lt : lt * 2);
+    const uint32_t at_v1 = group0 + C::CODES + k1 * (D / 2) + lg * (VW * 4), at_v2 = at_v1 + (k2 - k1) * (D / 2);
+    const uint32_t at_vs1 = scale0 + C::SCALES + k1 * (D / 16) + (D == 64 ? lg >> 1 : D == 128 ? lg : lg * 2);
+    const uint32_t at_vs2 = at_vs1 + (k2 - k1) * (D / 16);
+#pragma unroll 1
+    for (int x = tile0; x < tile1; ++x) {
+      ok &= tc_wait(&b_full[st], phase, &s_abort);
       __syncwarp();
 #pragma unroll 1
-      for (int sub = 0; sub < VG; ++sub) {                  // this warp's keys, 16 at a time
-        const int at16 = (warp % KG) * VG + sub, k0 = tl.at(x) * kKeys4 + at16 * 16;
+      for (int sub = 0; sub < SUBS; ++sub) {                // this warp's keys, 16 at a time
+        const int k0 = tl.at(x) * KT + (warp % KG) * (SUBS * 16) + sub * 16;
         if (k0 >= s.len || (k0 + 16 <= lo_min && k0 >= p.sinks)) continue;
-        const unsigned char* const kb = sm + st * C::STAGE + at16 * 16 * (D / 2);
-        const unsigned char* const vb = kb + C::CODES;
-        const unsigned char* const ksb = sm + st * C::STAGE + 2 * C::CODES + at16 * 16 * (D / 16);
-        const unsigned char* const vsb = ksb + C::SCALES;
-        const bool mask = k0 + 16 > lim_min || k0 < lo_max;
+        const uint32_t codes = st * C::STAGE + sub * 16 * (D / 2), scales = st * C::STAGE + sub * 16 * (D / 16);
+        const bool mask = __any_sync(0xffffffffu, k0 + 16 > lim_min || k0 < lo_max);   // a branch, not selects
+        // V^T: keys 2 lt, 2 lt + 1 (+ 8) of the products' rows, features (hd / 8) lg ..;
+        // loaded and regrouped while S is computed
+        uint32_t lo[2][VW], hi[2][VW], u1[2], u2[2], vs[2][2];
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          uint32_t w1[VW], w2[VW];
+          lds_words<VW>(w1, at_v1 + codes + h * 8 * (D / 2));
+          lds_words<VW>(w2, at_v2 + codes + h * 8 * (D / 2));
+#pragma unroll
+          for (int w = 0; w < VW; ++w) {
+            lo[h][w] = low_halves(w1[w], w2[w]);
+            hi[h][w] = high_halves(w1[w], w2[w]);
+          }
+          u1[h] = D == 256 ? lds_u16(at_vs1 + scales + h * 8 * (D / 16)) : lds_u8(at_vs1 + scales + h * 8 * (D / 16));
+          u2[h] = D == 256 ? lds_u16(at_vs2 + scales + h * 8 * (D / 16)) : lds_u8(at_vs2 + scales + h * 8 * (D / 16));
+        }
         float sc[NV][4];
 #pragma unroll
         for (int v = 0; v < NV; ++v)
 #pragma unroll
           for (int e = 0; e < 4; ++e) sc[v][e] = 0.f;
-        const int ka = key_of(lg), kc = key_of(lg + 8);
-        // 4 features a step: a lane's codes are 64 (hd 256: 2 times 64) consecutive ones at most
-        constexpr int W = D == 64 ? 2 : 4, CH = D == 256 ? 2 : 1;
+        // 4 features a step
 #pragma unroll
         for (int c = 0; c < CH; ++c) {
           uint32_t wa[W], wc[W];
-          lds_words<W>(wa, kb + ka * (D / 2) + c * 64 + lt * (W * 4));
-          lds_words<W>(wc, kb + kc * (D / 2) + c * 64 + lt * (W * 4));
+          lds_words<W>(wa, at_k + codes + c * 64);
+          lds_words<W>(wc, at_k + codes + c * 64 + 8 * (D / 2));
           uint32_t sa[2], sb[2];            // a block's scale in both halves
           if constexpr (D == 64) {
-            sa[0] = e4m3x2_f16x2(ksb[ka * 4 + lt] * 0x0101u);
-            sb[0] = e4m3x2_f16x2(ksb[kc * 4 + lt] * 0x0101u);
+            sa[0] = e4m3x2_f16x2(lds_u8(at_ks + scales) * 0x0101u);
+            sb[0] = e4m3x2_f16x2(lds_u8(at_ks + scales + 8 * (D / 16)) * 0x0101u);
           } else {
-            const uint32_t ua = e4m3x2_f16x2(*reinterpret_cast<const uint16_t*>(ksb + ka * (D / 16) + c * 8 + lt * 2));
-            const uint32_t uc = e4m3x2_f16x2(*reinterpret_cast<const uint16_t*>(ksb + kc * (D / 16) + c * 8 + lt * 2));
+            const uint32_t ua = e4m3x2_f16x2(lds_u16(at_ks + scales + c * 8));
+            const uint32_t uc = e4m3x2_f16x2(lds_u16(at_ks + scales + c * 8 + 8 * (D / 16)));
             sa[0] = __byte_perm(ua, ua, 0x1010);
             sa[1] = __byte_perm(ua, ua, 0x3232);
             sb[0] = __byte_perm(uc, uc, 0x1010);
@@ -397,20 +416,21 @@ __global__ void __launch_bounds__(Split4Cfg<D, NV, VG>::THREADS, Split4Cfg<D, NV
             }
           });
         }
-        // scores in log2 units, masked: element e is (key row lg + 8 (e / 2), vector 2 lt + e % 2)
+        // masked scores: element e is (key row lg + 8 (e / 2), vector 2 lt + e % 2)
+        if (mask) {
+#pragma unroll
+          for (int v = 0; v < NV; ++v)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              const int key = k0 + ka + (e < 2 ? 0 : 8), top = lim[v][e & 1];
+              if (key >= top || (key < top - p.window && key >= p.sinks)) sc[v][e] = -INFINITY;
+            }
+        }
         bool raise = false;
 #pragma unroll
         for (int v = 0; v < NV; ++v)
 #pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            float y = sc[v][e] * qm[v][e & 1];
-            if (mask) {
-              const int key = k0 + (e < 2 ? ka : kc), top = lim[v][e & 1];
-              if (key >= top || (key < top - p.window && key >= p.sinks)) y = -INFINITY;
-            }
-            sc[v][e] = y;
-            raise |= y > m[v][e & 1] + kLazy4;
-          }
+          for (int e = 0; e < 2; ++e) raise |= fmaxf(sc[v][e], sc[v][e + 2]) > bar[v][e];
         if (__any_sync(0xffffffffu, raise)) {
 #pragma unroll
           for (int v = 0; v < NV; ++v)
@@ -419,9 +439,12 @@ __global__ void __launch_bounds__(Split4Cfg<D, NV, VG>::THREADS, Split4Cfg<D, NV
               float mx = fmaxf(sc[v][e], sc[v][e + 2]);
 #pragma unroll
               for (int d = 4; d < 32; d <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, d));
-              const float mn = fmaxf(m[v][e], mx);
-              const float f = mn == -INFINITY ? 1.f : ex2(m[v][e] - mn);   // m = -inf: 0
-              m[v][e] = mn;
+              const float old = kLog24 - off[v][e], mn = fmaxf(seen[v] >> e & 1 ? old : -INFINITY, mx * qm[v][e]);
+              if (mn == -INFINITY) continue;                // no key yet
+              const float f = seen[v] >> e & 1 ? ex2(old - mn) : 0.f;
+              seen[v] |= 1 << e;
+              off[v][e] = kLog24 - mn;
+              bar[v][e] = (mn + kLazy4) / qm[v][e];
               l[v][e] *= f;
 #pragma unroll
               for (int j = 0; j < KS; ++j) {
@@ -433,41 +456,27 @@ __global__ void __launch_bounds__(Split4Cfg<D, NV, VG>::THREADS, Split4Cfg<D, NV
         uint32_t pf[NV][2];
 #pragma unroll
         for (int v = 0; v < NV; ++v) {
-          const float off0 = kLog24 - (m[v][0] == -INFINITY ? 0.f : m[v][0]), off1 = kLog24 - (m[v][1] == -INFINITY ? 0.f : m[v][1]);
-          const float e0 = ex2(sc[v][0] + off0), e1 = ex2(sc[v][1] + off1), e2 = ex2(sc[v][2] + off0), e3 = ex2(sc[v][3] + off1);
-          l[v][0] += e0 + e2;
-          l[v][1] += e1 + e3;
-          pf[v][0] = movmatrix(pack2(e0, e1, (const __half*)nullptr));
-          pf[v][1] = movmatrix(pack2(e2, e3, (const __half*)nullptr));
+          float e[4];
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            e[i] = ex2(fmaf(sc[v][i], qm[v][i & 1], off[v][i & 1]));
+            l[v][i & 1] += e[i];
+          }
+          pf[v][0] = movmatrix(pack2(e[0], e[1], (const __half*)nullptr));
+          pf[v][1] = movmatrix(pack2(e[2], e[3], (const __half*)nullptr));
         }
-        // V^T: keys 2 lt, 2 lt + 1 (+ 8) of the products' rows, features (hd / 8) lg ..
-        constexpr int VW = D / 64;          // words of a key
-        uint32_t lo[2][VW], hi[2][VW], vs[2][2];
+        if (mask) {                         // what no row sees may be NaN: zeros
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            const int y1 = k0 + k1 + 8 * h, y2 = k0 + k2 + 8 * h;
+            if (y1 >= s.len || (y1 < lo_min && y1 >= p.sinks)) u1[h] = 0;
+            if (y2 >= s.len || (y2 < lo_min && y2 >= p.sinks)) u2[h] = 0;
+          }
+        }
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
-          const int k1 = key_of(2 * lt + 8 * h), k2 = key_of(2 * lt + 8 * h + 1);
-          uint32_t w1[VW], w2[VW];
-          lds_words<VW>(w1, vb + k1 * (D / 2) + lg * (VW * 4));
-          lds_words<VW>(w2, vb + k2 * (D / 2) + lg * (VW * 4));
-#pragma unroll
-          for (int w = 0; w < VW; ++w) {
-            lo[h][w] = low_halves(w1[w], w2[w]);
-            hi[h][w] = high_halves(w1[w], w2[w]);
-          }
-          uint32_t u1, u2;
-          if constexpr (D == 256) {
-            u1 = *reinterpret_cast<const uint16_t*>(vsb + k1 * 16 + lg * 2);
-            u2 = *reinterpret_cast<const uint16_t*>(vsb + k2 * 16 + lg * 2);
-          } else {
-            u1 = vsb[k1 * (D / 16) + (D == 64 ? lg >> 1 : lg)];
-            u2 = vsb[k2 * (D / 16) + (D == 64 ? lg >> 1 : lg)];
-          }
-          if (mask) {                       // what no row sees may be NaN: zeros
-            if (k0 + k1 >= s.len || (k0 + k1 < lo_min && k0 + k1 >= p.sinks)) u1 = 0;
-            if (k0 + k2 >= s.len || (k0 + k2 < lo_min && k0 + k2 >= p.sinks)) u2 = 0;
-          }
-          vs[h][0] = e4m3x2_f16x2(__byte_perm(u1, u2, 0x0040));
-          if constexpr (D == 256) vs[h][1] = e4m3x2_f16x2(__byte_perm(u1, u2, 0x0051));
+          vs[h][0] = e4m3x2_f16x2(__byte_perm(u1[h], u2[h], 0x0040));
+          if constexpr (D == 256) vs[h][1] = e4m3x2_f16x2(__byte_perm(u1[h], u2[h], 0x0051));
         }
         unrolled<0, KS>([&](auto j) {
           constexpr int J = decltype(j)::value, B = D == 256 ? J / 8 : 0;
@@ -479,6 +488,10 @@ __global__ void __launch_bounds__(Split4Cfg<D, NV, VG>::THREADS, Split4Cfg<D, NV
       }
       __syncwarp();
       if (lane == 0) mbar_arrive(&b_empty[st]);
+      if (++st == ST) {
+        st = 0;
+        phase ^= 1;
+      }
     }
 
     // --- join the warps, JT tiles of O at a time
@@ -488,7 +501,7 @@ __global__ void __launch_bounds__(Split4Cfg<D, NV, VG>::THREADS, Split4Cfg<D, NV
       for (int e = 0; e < 2; ++e) {
 #pragma unroll
         for (int d = 4; d < 32; d <<= 1) l[v][e] += __shfl_xor_sync(0xffffffffu, l[v][e], d);
-        if (lg == 0) s_ml[warp][v * 8 + 2 * lt + e] = make_float2(m[v][e], l[v][e]);
+        if (lg == 0) s_ml[warp][v * 8 + 2 * lt + e] = make_float2(seen[v] >> e & 1 ? kLog24 - off[v][e] : -INFINITY, l[v][e]);
       }
     const bool whole = tile0 == 0 && tile1 == tl.n;
     // record of the item this CTA continues: slot 2c, of the one it starts: 2c + 1
@@ -610,7 +623,7 @@ static void split4_plan(const swa_paged4_attend_args* a, long long vecs, Split4P
   sp->rows = vecs <= 8 ? 8 : vecs <= 16 ? 16 : 32;
   long long keys = (long long)c.max_pages * c.page;
   if (a->window) {
-    const long long w = (long long)a->window + a->sinks + a->max_rows + 2 * kKeys4;
+    const long long w = (long long)a->window + a->sinks + a->max_rows + 256;
     keys = w < keys ? w : keys;
   }
   sp->whole = keys <= kWholeKeys4;

@@ -50,6 +50,28 @@ __device__ __forceinline__ float query_scale(float top, float& inv) {
   inv = __uint_as_float(shift >= 127 ? 0x00400000u : (uint32_t)(127 - shift) << 23);   // 2^-127 is subnormal
   return __uint_as_float((uint32_t)(127 + shift) << 23);
 }
+
+// Loads from shared memory by its own addresses (a pointer that was rounded up is a generic one): W words,
+// aligned to their number; 16 and 8 bits. Volatile: they stay behind the waits.
+template <int W>
+__device__ __forceinline__ void lds_words(uint32_t (&r)[W], uint32_t at) {
+  if constexpr (W == 1) asm volatile("ld.shared.b32 %0, [%1];" : "=r"(r[0]) : "r"(at));
+  else if constexpr (W == 2) asm volatile("ld.shared.v2.b32 {%0, %1}, [%2];" : "=r"(r[0]), "=r"(r[1]) : "r"(at));
+  else asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(at));
+}
+__device__ __forceinline__ uint32_t lds_u16(uint32_t at) {
+  uint32_t r;
+  asm volatile("{\n\t.reg .b16 a;\n\tld.shared.b16 a, [%1];\n\tcvt.u32.u16 %0, a;\n\t}" : "=r"(r) : "r"(at));
+  return r;
+}
+__device__ __forceinline__ uint32_t lds_u8(uint32_t at) {
+  uint32_t r;
+  asm volatile("ld.shared.u8 %0, [%1];" : "=r"(r) : "r"(at));
+  return r;
+}
+__device__ __forceinline__ void sts_words(uint32_t at, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
+  asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" :: "r"(at), "r"(a), "r"(b), "r"(c), "r"(d) : "memory");
+}
 #endif
 
 }  // namespace swa

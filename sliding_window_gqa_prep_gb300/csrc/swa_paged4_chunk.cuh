@@ -263,33 +263,47 @@ __global__ void __launch_bounds__(Chunk4Cfg<D>::THREADS, 1) paged4_chunk_kernel(
     // 16-byte chunk i of these 32 features goes to chunk 4 (q & 1) + i of its 64-feature half; lanes of
     // other halves take their chunks in another order, so that eight lanes store to eight bank groups
     const int turn = D == 256 ? q >> 1 : D == 128 ? 2 * (q >> 1) : 0;
+    uint32_t to[4];                       // a thread's keys are the same modulo 8 (RP is a multiple of it)
+    static_assert(RP % 8 == 0, "rows of a pass");
+#pragma unroll
+    for (int i = 0; i < 4; ++i) to[i] = ((4 * (q & 1) + (i ^ turn)) ^ (r0 & 7)) << 4;
+    const uint32_t codes_at = smem_u32(sm_codes) + q * 16, scale_at = C::CODES - q * 16 + q * 2;
+    const uint32_t kv_at = smem_u32(sm_kv) + (q >> 1) * (KT * 128);
     const bool ok = in_order([&](int pos, int x, bool is_v) {
       const int raw = pos % NR, slot = pos % NS, key0 = tl.at(j0 + x) * KT;
       if (!wait(&b_raw[raw], pos / NR)) return false;
       if (pos >= NS && !wait(&b_empty[slot], pos / NS - 1)) return false;
-      const unsigned char* const src = sm_codes + raw * C::RAW;
-      unsigned char* const dst = sm_kv + slot * C::SLOT + (q >> 1) * (KT * 128);
+      const uint32_t src = codes_at + raw * C::RAW, dst = kv_at + slot * C::SLOT;
       // what no row sees may be NaN in V: zeros, by its scale
       const bool part = is_v && (key0 + KT > s.len || key0 < lo_min);
 #pragma unroll 2
       for (int r = r0; r < KT; r += RP) {
-        uint4 w = *reinterpret_cast<const uint4*>(src + r * (D / 2) + q * 16);
-        uint32_t u = *reinterpret_cast<const uint16_t*>(src + C::CODES + r * (D / 16) + q * 2);
+        uint32_t w[4];
+        lds_words<4>(w, src + r * (D / 2));
+        uint32_t u = lds_u16(src + scale_at + r * (D / 16));
         if (part && (key0 + r >= s.len || (key0 + r < lo_min && key0 + r >= sinks))) u = 0;
         uint32_t sc = e4m3x2_f16x2(u);
         if (D >= 128 && (turn & 2)) {
-          w = make_uint4(w.z, w.w, w.x, w.y);
+          const uint32_t x = w[0], y = w[1];
+          w[0] = w[2];
+          w[1] = w[3];
+          w[2] = x;
+          w[3] = y;
           sc = __byte_perm(sc, sc, 0x1032);
         }
-        if (D == 256 && (turn & 1)) w = make_uint4(w.y, w.x, w.w, w.z);
+        if (D == 256 && (turn & 1)) {
+          const uint32_t x = w[0], y = w[2];
+          w[0] = w[1];
+          w[1] = x;
+          w[2] = w[3];
+          w[3] = y;
+        }
         const uint32_t s0 = __byte_perm(sc, sc, 0x1010), s1 = __byte_perm(sc, sc, 0x3232);
-        const uint32_t v[4] = {w.x, w.y, w.z, w.w};
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
           const uint32_t m = i < 2 ? s0 : s1;
-          *reinterpret_cast<uint4*>(dst + r * 128 + (((4 * (q & 1) + (i ^ turn)) ^ (r & 7)) << 4)) =
-              make_uint4(hmul2(e2m1x2_f16x2<0>(v[i]), m), hmul2(e2m1x2_f16x2<1>(v[i]), m), hmul2(e2m1x2_f16x2<2>(v[i]), m),
-                         hmul2(e2m1x2_f16x2<3>(v[i]), m));
+          sts_words(dst + r * 128 + to[i], hmul2(e2m1x2_f16x2<0>(w[i]), m), hmul2(e2m1x2_f16x2<1>(w[i]), m),
+                    hmul2(e2m1x2_f16x2<2>(w[i]), m), hmul2(e2m1x2_f16x2<3>(w[i]), m));
         }
       }
       fence_proxy_async_smem();           // before the products read it
@@ -495,19 +509,22 @@ __global__ void __launch_bounds__(Chunk4Cfg<D>::THREADS, 1) paged4_chunk_kernel(
       uint64_t sum[2] = {0, 0};
 #pragma unroll
       for (int h = 0; h < 2; ++h) {                         // each half of P goes to P V on its own
-        uint32_t w[KT / 4];
 #pragma unroll
-        for (int k = 0; k < KT / 4; ++k) {
-          const int e = h * (KT / 2) + 2 * k;
-          float e0, e1;
-          unpack64(fma2(pack64(x[e >> 5][e & 31], x[e >> 5][(e & 31) + 1]), mul2, off2), e0, e1);
-          e0 = ex2(e0);
-          e1 = ex2(e1);
-          sum[k & 1] = add2(sum[k & 1], pack64(__float_as_uint(e0), __float_as_uint(e1)));
-          w[k] = pack2(e0, e1, (const __half*)nullptr);
+        for (int z = 0; z < 2; ++z) {
+          uint32_t w[KT / 8];
+#pragma unroll
+          for (int k = 0; k < KT / 8; ++k) {
+            const int e = h * (KT / 2) + z * (KT / 4) + 2 * k;
+            float e0, e1;
+            unpack64(fma2(pack64(x[e >> 5][e & 31], x[e >> 5][(e & 31) + 1]), mul2, off2), e0, e1);
+            e0 = ex2(e0);
+            e1 = ex2(e1);
+            sum[k & 1] = add2(sum[k & 1], pack64(__float_as_uint(e0), __float_as_uint(e1)));
+            w[k] = pack2(e0, e1, (const __half*)nullptr);
+          }
+          if constexpr (KT == 128) tc_st16(c_s + h * (KT / 4) + z * (KT / 8), w);
+          else tc_st8(c_s + h * (KT / 4) + z * (KT / 8), w);
         }
-        if constexpr (KT == 128) tc_st32(c_s + h * (KT / 4), w);
-        else tc_st16(c_s + h * (KT / 4), w);
         tc_wait_st();
         tc_fence_before();
         // A wait sees only the parity of a phase: the P V before the last must be known complete before the

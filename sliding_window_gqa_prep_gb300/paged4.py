@@ -22,7 +22,7 @@ import struct
 import torch
 
 from . import _abi
-from .paged import (_F32, _I32, _I64, _TYPES, _TYPES16, _U8, _arg, _lib, _opt, _place, _rows, _there)
+from .paged import (_F32, _I32, _I64, _TYPES, _TYPES16, _U8, _arg, _complain, _lib, _opt, _place, _rows, _there)
 
 __all__ = ["paged4_append", "paged4_read", "paged4_attend", "paged4_attend_workspace_size", "paged_fork",
            "paged_fork_workspace_size", "paged_compact", "paged_compact_workspace_size"]
@@ -182,15 +182,19 @@ def paged4_attend(q, cache_k, scale_k, cache_v, scale_v, page_table, row_start, 
 # ------------------------------------------------------------------ pages
 def _pools(pools, num_pages, dev):
     """The fields of a swa_page_pools: contiguous tensors whose first dimension is the page."""
-    if len(pools) > _abi.SWA_MAX_POOLS:
-        raise ValueError(f"at most {_abi.SWA_MAX_POOLS} pools, got {len(pools)}")
-    base, size = [0] * _abi.SWA_MAX_POOLS, [0] * _abi.SWA_MAX_POOLS
-    for i, p in enumerate(pools):
+    n = len(pools)
+    if n > _abi.SWA_MAX_POOLS:
+        raise ValueError(f"at most {_abi.SWA_MAX_POOLS} pools, got {n}")
+    base, size = [], []
+    for p in pools:
         if not isinstance(p, torch.Tensor) or p.dim() < 2 or p.shape[0] != num_pages:
-            raise ValueError(f"pools[{i}] must be a CUDA tensor [{num_pages}][..]")
-        base[i] = _arg(p, f"pools[{i}]", dev, p.dtype)
-        size[i] = p.numel() // num_pages * p.element_size()
-    return (num_pages, len(pools), *base, *size)
+            raise ValueError(f"pools[{len(base)}] must be a CUDA tensor [{num_pages}][..]")
+        if p.get_device() != dev or not p.is_contiguous():
+            _complain(p, f"pools[{len(base)}]", dev, p.dtype, None)
+        base.append(p.data_ptr())
+        size.append(p.nbytes // num_pages)
+    rest = [0] * (_abi.SWA_MAX_POOLS - n)
+    return (num_pages, n, *base, *rest, *size, *rest)
 
 
 def _table(page_table, dev):
@@ -205,6 +209,24 @@ def _pages(refs, dev):
     return _arg(refs, "refs", dev, _I32), refs.shape[0]
 
 
+def _made(given, name, dev, shape, device):
+    """An int32 output and its address: the caller's, checked, or a new one."""
+    if given is not None:
+        return given, _arg(given, name, dev, _I32, shape)
+    new = torch.empty(shape, device=device, dtype=_I32)
+    return new, new.data_ptr()
+
+
+def _workspace(given, need, dev, device):
+    """Address and bytes of a workspace of `need` bytes (1: none), and what keeps it."""
+    if given is not None:
+        return _arg(given, "workspace", dev, _U8), given.numel(), given
+    if need <= 1:
+        return 0, 0, None
+    new = torch.empty(need, device=device, dtype=_U8)
+    return new.data_ptr(), need, new
+
+
 @functools.lru_cache(maxsize=256)
 def _fork_need(num_pages, B, R, page, max_pages) -> int:
     z = [0] * _abi.SWA_MAX_POOLS
@@ -212,7 +234,7 @@ def _fork_need(num_pages, B, R, page, max_pages) -> int:
 
 
 def paged_fork_workspace_size(num_pages, B, R, page, max_pages) -> int:
-    """Workspace bytes of paged_fork from a batch of B sequences to one of R."""
+    """Workspace bytes of paged_fork from a batch of B sequences to one of R (1: none is needed)."""
     n = _fork_need(num_pages, B, R, page, max_pages)
     if n == 0:
         raise _abi.SwaError(_abi.SWA_E_SHAPE, "swa_paged_fork_workspace_size")
@@ -239,18 +261,14 @@ def paged_fork(pools, page_table, lens, refs, parent, page: int, *, room=None, t
     if not isinstance(parent, torch.Tensor) or parent.dim() != 1:
         raise ValueError("parent must be a CUDA tensor [R]")
     R = parent.shape[0]
-    like = {"device": page_table.device, "dtype": _I32}
-    table_out = torch.empty(R, max_pages, **like) if table_out is None else table_out
-    lens_out = torch.empty(R, **like) if lens_out is None else lens_out
-    refs_out = torch.empty(num_pages, **like) if refs_out is None else refs_out
-    left = torch.empty(1, **like) if left is None else left
-    if workspace is None:
-        workspace = torch.empty(_fork_need(num_pages, B, R, page, max_pages), device=page_table.device, dtype=_U8)
+    where = page_table.device
+    table_out, to = _made(table_out, "table_out", dev, (R, max_pages), where)
+    lens_out, lo = _made(lens_out, "lens_out", dev, (R,), where)
+    refs_out, ro = _made(refs_out, "refs_out", dev, (num_pages,), where)
+    left, fo = _made(left, "left", dev, (1,), where)
+    ws = _workspace(workspace, _fork_need(num_pages, B, R, page, max_pages), dev, where)
     a = _FORK.pack(*packed, B, R, page, max_pages, tp, _arg(lens, "lens", dev, _I32, (B,)), _arg(parent, "parent", dev, _I32),
-                   _opt(room, "room", dev, _I32, (R,)), rp, _arg(table_out, "table_out", dev, _I32, (R, max_pages)),
-                   _arg(lens_out, "lens_out", dev, _I32, (R,)), _arg(refs_out, "refs_out", dev, _I32, (num_pages,)),
-                   _arg(left, "left", dev, _I32, (1,)), _arg(workspace, "workspace", dev, _U8), workspace.numel(),
-                   _opt(err, "err", dev, _I32, (1,)))
+                   _opt(room, "room", dev, _I32, (R,)), rp, to, lo, ro, fo, ws[0], ws[1], _opt(err, "err", dev, _I32, (1,)))
     _abi.check(_lib().swa_paged_fork(a, on), "swa_paged_fork")
     return table_out, lens_out, refs_out, left
 
@@ -262,7 +280,7 @@ def _compact_need(num_pages, B, max_pages) -> int:
 
 
 def paged_compact_workspace_size(num_pages, B, max_pages) -> int:
-    """Workspace bytes of paged_compact."""
+    """Workspace bytes of paged_compact (1: none is needed)."""
     n = _compact_need(num_pages, B, max_pages)
     if n == 0:
         raise _abi.SwaError(_abi.SWA_E_SHAPE, "swa_paged_compact_workspace_size")
@@ -281,16 +299,12 @@ def paged_compact(pools, page_table, refs, *, table_out=None, refs_out=None, mov
     tp, B, max_pages = _table(page_table, dev)
     rp, num_pages = _pages(refs, dev)
     packed = _pools(pools, num_pages, dev)
-    like = {"device": page_table.device, "dtype": _I32}
-    table_out = torch.empty(B, max_pages, **like) if table_out is None else table_out
-    refs_out = torch.empty(num_pages, **like) if refs_out is None else refs_out
-    moved = torch.empty(num_pages, **like) if moved is None else moved
-    used = torch.empty(1, **like) if used is None else used
-    if workspace is None:
-        workspace = torch.empty(_compact_need(num_pages, B, max_pages), device=page_table.device, dtype=_U8)
-    a = _COMPACT.pack(*packed, B, max_pages, tp, rp, _arg(table_out, "table_out", dev, _I32, (B, max_pages)),
-                      _arg(refs_out, "refs_out", dev, _I32, (num_pages,)), _arg(moved, "moved", dev, _I32, (num_pages,)),
-                      _arg(used, "used", dev, _I32, (1,)), _arg(workspace, "workspace", dev, _U8), workspace.numel(),
-                      _opt(err, "err", dev, _I32, (1,)))
+    where = page_table.device
+    table_out, to = _made(table_out, "table_out", dev, (B, max_pages), where)
+    refs_out, ro = _made(refs_out, "refs_out", dev, (num_pages,), where)
+    moved, mo = _made(moved, "moved", dev, (num_pages,), where)
+    used, uo = _made(used, "used", dev, (1,), where)
+    ws = _workspace(workspace, _compact_need(num_pages, B, max_pages), dev, where)
+    a = _COMPACT.pack(*packed, B, max_pages, tp, rp, to, ro, mo, uo, ws[0], ws[1], _opt(err, "err", dev, _I32, (1,)))
     _abi.check(_lib().swa_paged_compact(a, on), "swa_paged_compact")
     return table_out, refs_out, moved, used

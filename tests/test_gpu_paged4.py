@@ -469,6 +469,7 @@ FORK = [
     dict(lens=[20, 35], parent=[0, 1], room=[1, 1], share=3),                # .. and one of them is past it
     dict(lens=[20, 20], parent=[0, 0], room=[1, 1], held=True),              # .. and a holder outside the table
     dict(lens=[5] * 40, parent=[i % 40 for i in range(0, 700, 7)], room=[2] * 100, num_pages=400),
+    dict(lens=[40, 33], parent=[0, 0, 0, 1], room=[1, 1, 1, 1], num_pages=9000),     # the passes on a cluster
     dict(lens=[100, 90], parent=[0, 1], room=[1, 1], extra=2),               # pages behind the last key are let go
     dict(lens=[40, 33], parent=[0, 0, 0, 1], room=[500, 1, 1, 1], num_pages=12, lacking=True),
     dict(lens=[33] * 5, parent=[0, 0, 0, 0, 1, 2, 3, 4], room=[0] * 8, num_pages=16, lacking=True),
@@ -513,7 +514,7 @@ def test_fork(kw, page):
     assert all(torch.equal(x, y) for x, y in zip(got, again))
     mine = args[2].clone()
     swa.paged_fork(pools, args[0], args[1], mine, args[3], page, room=None if room is None else dev(room), refs_out=mine)
-    assert torch.equal(mine, got[2])
+    assert torch.equal(mine, got[2]) and all(torch.equal(x.view(U8), y.view(U8)) for x, y in zip(pools, before))
 
 
 def test_fork_reports():

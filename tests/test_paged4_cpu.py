@@ -215,15 +215,18 @@ def test_fork_refusals(lib):
     assert call(_fork(page_bytes=24)) == _abi.SWA_E_ALIGN
     for kw in (dict(table=FAR + 2), dict(left=FAR + 8 * MB + 1), dict(workspace=FAR + 9 * MB + 128)):
         assert call(_fork(**kw)) == _abi.SWA_E_ALIGN, kw
-    for kw in (dict(workspace=None), dict(workspace_bytes=size(_fork()) - 1)):
-        assert call(_fork(**kw)) == _abi.SWA_E_WORKSPACE, kw
+    assert size(_fork()) == 1                                # few pages and entries: one launch, no workspace
+    for kw in (dict(workspace=None), dict(workspace_bytes=size(_fork(num_pages=10000)) - 1)):
+        assert call(_fork(num_pages=10000, **kw)) == _abi.SWA_E_WORKSPACE, kw
     a = _fork()
     a.pools.base[1] = FAKE + 639 // 16 * 16                   # 10 pages of 64 bytes each
     assert call(a) == _abi.SWA_E_SHAPE
     # outputs on inputs (48 bytes of table_out, 40 of refs_out), on each other, on pools and the workspace
     for kw in (dict(table_out=FAR), dict(table_out=FAR - 44), dict(lens_out=FAR + MB + 4), dict(refs_out=FAR + 2 * MB - 36), dict(left=FAR + 3 * MB + 8),
-               dict(refs_out=FAR + 4 * MB + 4), dict(left=FAR + 5 * MB + 44), dict(lens_out=FAKE + 636), dict(refs_out=FAR + 9 * MB), dict(table=FAR + 9 * MB)):
+               dict(refs_out=FAR + 4 * MB + 4), dict(left=FAR + 5 * MB + 44), dict(lens_out=FAKE + 636), dict(room=FAR + 7 * MB)):
         assert call(_fork(**kw)) == _abi.SWA_E_SHAPE, kw
+    for kw in (dict(refs_out=FAR + 9 * MB), dict(table=FAR + 9 * MB)):
+        assert call(_fork(num_pages=10000, **kw)) == _abi.SWA_E_SHAPE, kw
 
 
 def _compact(pools=2, page_bytes=64, num_pages=10, **kw):
@@ -253,11 +256,13 @@ def test_compact_refusals(lib):
     assert call(_compact(page_bytes=0)) == _abi.SWA_E_SHAPE and call(_compact(page_bytes=8 * 3)) == _abi.SWA_E_ALIGN
     for kw in (dict(moved=FAR + 2), dict(workspace=FAR + 6 * MB + 16)):
         assert call(_compact(**kw)) == _abi.SWA_E_ALIGN, kw
-    for kw in (dict(workspace=None), dict(workspace_bytes=size(_compact()) - 1)):
-        assert call(_compact(**kw)) == _abi.SWA_E_WORKSPACE, kw
+    assert size(_compact()) == 1
+    for kw in (dict(workspace=None), dict(workspace_bytes=size(_compact(num_pages=10000)) - 1)):
+        assert call(_compact(num_pages=10000, **kw)) == _abi.SWA_E_WORKSPACE, kw
     for kw in (dict(table_out=FAR + 4), dict(refs_out=FAR + MB - 4), dict(moved=FAR + MB), dict(used=FAR), dict(moved=FAR + 3 * MB + 36),
-               dict(used=FAKE), dict(moved=FAR + 6 * MB)):
+               dict(used=FAKE)):
         assert call(_compact(**kw)) == _abi.SWA_E_SHAPE, kw
+    assert call(_compact(num_pages=10000, moved=FAR + 6 * MB)) == _abi.SWA_E_SHAPE
 
 
 # ------------------------------------------------------------------ the binding
@@ -314,8 +319,9 @@ def test_pools_of_the_page_calls():
 
 
 def test_workspace_sizes():
-    assert swa.paged_fork_workspace_size(1000, 4, 8, 16, 10) > 1000 * 12
-    assert swa.paged_compact_workspace_size(1000, 4, 10) > 1000 * 12
+    assert swa.paged_fork_workspace_size(100000, 4, 8, 16, 10) > 100000 * 12
+    assert swa.paged_compact_workspace_size(100000, 4, 10) > 100000 * 12
+    assert swa.paged_fork_workspace_size(1000, 4, 8, 16, 10) == swa.paged_compact_workspace_size(1000, 4, 10) == 1
     for fn, a in ((swa.paged_fork_workspace_size, (1000, 4, 8, 17, 10)), (swa.paged_compact_workspace_size, (0, 4, 10)),
                   (swa.paged4_attend_workspace_size, (1, 4, 4, 3, 128, 16, 4, 4))):
         with pytest.raises(swa.SwaError):
