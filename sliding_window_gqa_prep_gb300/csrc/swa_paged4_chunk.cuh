@@ -3,9 +3,12 @@
 // query vectors, S and O in TMEM, a softmax warpgroup and an issuing warp a tile, and
 // two tiles (hd 64, 128) or two S buffers (hd 256) so that products run under the softmax.
 // What differs:
-//   - a warp copies codes and scales as they are (4.5 bits a feature) into a ring of their own,
-//     and a warpgroup turns them into f16 operands in the swizzled layout that the products
-//     read: once for the item's 256 query vectors, 0.4 of the time that the products take.
+//   - a warp copies codes and scales as they are (4.5 bits a feature) into rings of their own. They
+//     become f16 operands, in the swizzled layout that the products read, once for the item's 256 query
+//     vectors: with two tiles by the softmax warps, each between its weights and its next scores, V by those of
+//     the first tile and K by those of the second, who then find the slot free; at hd 256 by a warpgroup of
+//     its own. (Four more warps that did only this at hd 128 left the softmax threads 184 registers of the 220 that
+//     a row of S takes, and took their issue slots; both warpgroups with half a tile each waited for one another.)
 //   - all products are f16: codes * scale is exact there, q is scaled by a power of two a row.
 //   - tiles of keys that no row sees (between the sinks and the first row's window) are left
 //     out; a row's own limits are masks.
@@ -17,15 +20,15 @@ namespace swa {
 template <int D>
 struct Chunk4Cfg {
   static constexpr int NT = ChunkCfg<D>::NT, SB = ChunkCfg<D>::SB, KT = ChunkCfg<D>::KT;
-  static constexpr int NS = D == 64 ? 6 : 4;           // operand slots (a K or V tile in f16)
-  static constexpr int NR = D == 64 ? 4 : 3;           // slots of codes and scales
-  static constexpr int SLOT = KT * D * 2, CODES = KT * D / 2, RAW = CODES + KT * D / 16;
+  static constexpr bool OWN = NT == 2;                 // the softmax warps convert
+  static constexpr int RK = 2, RV = D == 64 ? 2 : 1;   // slots of K's and of V's codes and scales
+  static constexpr int SLOT = KT * D * 2, CODES = KT * D / 2, RAW = CODES + KT * D / 16;   // operands: two slots for K, two for V
   static constexpr int QB = 128 * D * 2;
-  static constexpr int THREADS = NT * 128 + 256;       // softmax; loader, issuers, idle warps; conversion
-  static constexpr int SMEM = NT * QB + NS * SLOT + NR * RAW + 1024;   // + alignment
+  static constexpr int THREADS = NT * 128 + (OWN ? 128 : 256);   // softmax; loader, issuers, idle warps; conversion
+  static constexpr int SMEM = NT * QB + 4 * SLOT + (RK + RV) * RAW + 1024;   // + alignment
   // Registers a thread at launch and after they moved to the softmax threads (two tiles)
-  static constexpr int REGS = NT == 2 ? 128 : 0, R_SOFT = 184, R_REST = 72;
-  static_assert(NT == 1 || NT * 128 * R_SOFT + 256 * R_REST <= THREADS * REGS, "registers of a CTA");
+  static constexpr int REGS = NT == 2 ? 168 : 0, R_SOFT = 216, R_REST = 72;
+  static_assert(NT == 1 || NT * 128 * R_SOFT + 128 * R_REST <= THREADS * REGS, "registers of a CTA");
   static constexpr int C_O = NT * SB * KT;             // first O column
 };
 
@@ -43,11 +46,11 @@ __device__ __forceinline__ int tiles_below(const Tiles4& tl, int lim, int kt) {
 template <int D>
 __global__ void __launch_bounds__(Chunk4Cfg<D>::THREADS, 1) paged4_chunk_kernel(const __grid_constant__ Chunk4Params p) {
   using C = Chunk4Cfg<D>;
-  constexpr int NT = C::NT, SB = C::SB, KT = C::KT, NS = C::NS, NR = C::NR;
+  constexpr int NT = C::NT, SB = C::SB, KT = C::KT, RK = C::RK, RV = C::RV;
   extern __shared__ unsigned char sm_raw[];
   // tests/test_paged4_barriers_cpu.py runs the roles below on a model of these barriers: what waits
   // or arrives here has to be changed there too
-  __shared__ __align__(8) uint64_t b_raw[NR], b_free[NR], b_full[NS], b_empty[NS], b_q[NT], b_s[NT * SB], b_p[NT * SB][2], b_pv[NT], b_fin[NT], b_turn[NT];
+  __shared__ __align__(8) uint64_t b_raw[RK + RV], b_free[RK + RV], b_full[4], b_empty[4], b_q[NT], b_s[NT * SB], b_p[NT * SB][2], b_pv[NT], b_fin[NT], b_turn[NT];
   __shared__ uint32_t s_tmem;
   __shared__ int s_abort, s_b, s_idx;
   __shared__ int s_scan[32];
@@ -56,16 +59,16 @@ __global__ void __launch_bounds__(Chunk4Cfg<D>::THREADS, 1) paged4_chunk_kernel(
   constexpr int W_LOAD = NT * 4, W_MMA = NT * 4 + 1, W_CONV = NT * 4 + 4;
   unsigned char* const sm = reinterpret_cast<unsigned char*>((reinterpret_cast<uintptr_t>(sm_raw) + 1023) & ~(uintptr_t)1023);
   unsigned char* const sm_kv = sm + NT * C::QB;
-  unsigned char* const sm_codes = sm_kv + NS * C::SLOT;
+  unsigned char* const sm_codes = sm_kv + 4 * C::SLOT;
   const PagedAttendParams& a = p.q.a;
   // what needs no global memory, before the wait for the kernel in front
   if (warp == W_LOAD) {
     if (lane == 0) {
-      for (int i = 0; i < NR; ++i) {
+      for (int i = 0; i < RK + RV; ++i) {
         mbar_init(&b_raw[i], 1);
         mbar_init(&b_free[i], 4);
       }
-      for (int i = 0; i < NS; ++i) {
+      for (int i = 0; i < 4; ++i) {        // K tiles 0 and 1 modulo 2, V tiles
         mbar_init(&b_full[i], 4);
         mbar_init(&b_empty[i], NT);
       }
@@ -198,19 +201,81 @@ __global__ void __launch_bounds__(Chunk4Cfg<D>::THREADS, 1) paged4_chunk_kernel(
   auto wait = [&](uint64_t* bar, int phase) -> bool {
     return __all_sync(0xffffffffu, tc_wait(bar, (uint32_t)(phase & 1), &s_abort));
   };
-  // K and V tiles in the order in which they are consumed: f(position, tile of this CTA, is V)
-  auto in_order = [&](auto f) {
+  // K and V tiles in the order in which they are copied and converted: K 0, K 1, V 0, then V x + 1 and K x + 2
+  // after the scores of x; f(tile, is V)
+  auto before_all = [&](auto f) {
     bool ok = true;
-    for (int x = 0; ok && x < n; ++x) {
-      if (SB == 1) {
-        ok = f(pos_k<SB>(x), x, false) && f(pos_v<SB>(x, n), x, true);
-      } else {
-        if (x == 0) ok = f(0, 0, false);
-        if (ok && x + 1 < n) ok = f(pos_k<SB>(x + 1), x + 1, false);
-        if (ok) ok = f(pos_v<SB>(x, n), x, true);
+    if (n > 0) ok = f(0, false);
+    if (ok && n > 1) ok = f(1, false);
+    if (ok && n > 0) ok = f(0, true);
+    return ok;
+  };
+  auto after_scores = [&](int x, auto f) {
+    bool ok = true;
+    if (x + 1 < n) ok = f(x + 1, true);
+    if (ok && x + 2 < n) ok = f(x + 2, false);
+    return ok;
+  };
+  auto in_order = [&](auto f) {
+    bool ok = before_all(f);
+    for (int x = 0; ok && x < n; ++x) ok = after_scores(x, f);
+    return ok;
+  };
+  // tile x's slot of codes and the use of it
+  auto raw_slot = [&](int x, bool is_v) { return is_v ? RK + x % RV : x % RK; };
+  auto raw_use = [&](int x, bool is_v) { return is_v ? x / RV : x / RK; };
+
+  // Codes to operands: tile x by a warpgroup whose thread is wt, 32 features a thread at a time
+  constexpr int LR = D / 32, RP = 128 / LR;               // lanes of a key, keys of a pass
+  auto convert = [&](int wt, int x, bool is_v) {
+    const int q = wt % LR, r0 = wt / LR, raw = raw_slot(x, is_v), slot = (is_v ? 2 : 0) + (x & 1), key0 = tl.at(j0 + x) * KT;
+    // 16-byte chunk i of these 32 features goes to chunk 4 (q & 1) + i of its 64-feature half; lanes of
+    // other halves take their chunks in another order, so that eight lanes store to eight bank groups
+    const int turn = D == 256 ? q >> 1 : D == 128 ? 2 * (q >> 1) : 0;
+    static_assert(RP % 8 == 0, "a thread's keys are the same modulo 8");
+    if (!wait(&b_raw[raw], raw_use(x, is_v))) return false;
+    if (x >= 2 && !wait(&b_empty[slot], (x >> 1) - 1)) return false;
+    const uint32_t src = smem_u32(sm_codes) + raw * C::RAW + q * 16, scales = smem_u32(sm_codes) + raw * C::RAW + C::CODES + q * 2;
+    const uint32_t dst = smem_u32(sm_kv) + slot * C::SLOT + (q >> 1) * (KT * 128);
+    // what no row sees may be NaN in V: zeros, by its scale
+    const bool part = is_v && (key0 + KT > s.len || key0 < lo_min);
+#pragma unroll 2
+    for (int r = r0; r < KT; r += RP) {
+      uint32_t w[4];
+      lds_words<4>(w, src + r * (D / 2));
+      uint32_t u = lds_u16(scales + r * (D / 16));
+      if (part && (key0 + r >= s.len || (key0 + r < lo_min && key0 + r >= sinks))) u = 0;
+      uint32_t sc = e4m3x2_f16x2(u);
+      if (D >= 128 && (turn & 2)) {
+        const uint32_t y = w[0], z = w[1];
+        w[0] = w[2];
+        w[1] = w[3];
+        w[2] = y;
+        w[3] = z;
+        sc = __byte_perm(sc, sc, 0x1032);
+      }
+      if (D == 256 && (turn & 1)) {
+        const uint32_t y = w[0], z = w[2];
+        w[0] = w[1];
+        w[1] = y;
+        w[2] = w[3];
+        w[3] = z;
+      }
+      const uint32_t s0 = __byte_perm(sc, sc, 0x1010), s1 = __byte_perm(sc, sc, 0x3232);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const uint32_t m = i < 2 ? s0 : s1;
+        sts_words(dst + r * 128 + (((4 * (q & 1) + (i ^ turn)) ^ (r0 & 7)) << 4), hmul2(e2m1x2_f16x2<0>(w[i]), m),
+                  hmul2(e2m1x2_f16x2<1>(w[i]), m), hmul2(e2m1x2_f16x2<2>(w[i]), m), hmul2(e2m1x2_f16x2<3>(w[i]), m));
       }
     }
-    return ok;
+    fence_proxy_async_smem();             // before the products read it
+    __syncwarp();
+    if (lane == 0) {
+      mbar_arrive(&b_free[raw]);
+      mbar_arrive(&b_full[slot]);
+    }
+    return true;
   };
 
   // The softmax threads hold a row of S: registers move over to them.
@@ -222,9 +287,11 @@ __global__ void __launch_bounds__(Chunk4Cfg<D>::THREADS, 1) paged4_chunk_kernel(
     const bool codes = lane < runs, mine = lane < 2 * runs;
     const int run = codes ? lane : lane - runs, row = codes ? D / 2 : D / 16;
     const int32_t* table = a.map.table + (size_t)b * a.map.max_pages;
-    int issued = 0;
-    const bool ok = in_order([&](int pos, int x, bool is_v) {
-      const int slot = pos % NR, key = tl.at(j0 + x) * KT + run * rows;
+    int last[RK + RV];                    // the last use of each slot that was copied to
+#pragma unroll
+    for (int i = 0; i < RK + RV; ++i) last[i] = -1;
+    const bool ok = in_order([&](int x, bool is_v) {
+      const int slot = raw_slot(x, is_v), use = raw_use(x, is_v), key = tl.at(j0 + x) * KT + run * rows;
       unsigned char* const dst = sm_codes + slot * C::RAW + (codes ? 0 : C::CODES) + run * rows * row;
       const uint8_t* from = nullptr;
       bool blank = false;
@@ -239,7 +306,7 @@ __global__ void __launch_bounds__(Chunk4Cfg<D>::THREADS, 1) paged4_chunk_kernel(
         }
       }
       const uint32_t bytes = __reduce_add_sync(0xffffffffu, from ? rows * row : 0);
-      if (pos >= NR && !wait(&b_free[slot], pos / NR - 1)) return false;
+      if (use > 0 && !wait(&b_free[slot], use - 1)) return false;
       if (blank) {
         for (int i = 0; i < rows * row; i += 16) *reinterpret_cast<uint4*>(dst + i) = make_uint4(0, 0, 0, 0);
         fence_proxy_async_smem();         // before a later copy into this slot
@@ -248,73 +315,19 @@ __global__ void __launch_bounds__(Chunk4Cfg<D>::THREADS, 1) paged4_chunk_kernel(
       if (lane == 0) mbar_arrive_expect_tx(&b_raw[slot], bytes);
       __syncwarp();
       if (from) bulk_g2s(dst, from, rows * row, &b_raw[slot]);
-      issued = pos + 1;
+      last[slot] = use;
       return true;
     });
     if (!ok) {
       give_up();
       // copies in flight land before the CTA exits (bounded)
-      for (int i = max(0, issued - NR); i < issued; ++i) mbar_wait_bounded(&b_raw[i % NR], (uint32_t)((i / NR) & 1), kWaitLimitNs);
+#pragma unroll
+      for (int i = 0; i < RK + RV; ++i)
+        if (last[i] >= 0) mbar_wait_bounded(&b_raw[i], (uint32_t)(last[i] & 1), kWaitLimitNs);
     }
-  } else if (warp >= W_CONV) {
-    // ------------------------------------------------------------ conversion: 32 features a thread at a time
-    constexpr int LR = D / 32, RP = 128 / LR;             // lanes of a key, keys of a pass
-    const int q = tid % LR, r0 = (tid - W_CONV * 32) / LR;
-    // 16-byte chunk i of these 32 features goes to chunk 4 (q & 1) + i of its 64-feature half; lanes of
-    // other halves take their chunks in another order, so that eight lanes store to eight bank groups
-    const int turn = D == 256 ? q >> 1 : D == 128 ? 2 * (q >> 1) : 0;
-    uint32_t to[4];                       // a thread's keys are the same modulo 8 (RP is a multiple of it)
-    static_assert(RP % 8 == 0, "rows of a pass");
-#pragma unroll
-    for (int i = 0; i < 4; ++i) to[i] = ((4 * (q & 1) + (i ^ turn)) ^ (r0 & 7)) << 4;
-    const uint32_t codes_at = smem_u32(sm_codes) + q * 16, scale_at = C::CODES - q * 16 + q * 2;
-    const uint32_t kv_at = smem_u32(sm_kv) + (q >> 1) * (KT * 128);
-    const bool ok = in_order([&](int pos, int x, bool is_v) {
-      const int raw = pos % NR, slot = pos % NS, key0 = tl.at(j0 + x) * KT;
-      if (!wait(&b_raw[raw], pos / NR)) return false;
-      if (pos >= NS && !wait(&b_empty[slot], pos / NS - 1)) return false;
-      const uint32_t src = codes_at + raw * C::RAW, dst = kv_at + slot * C::SLOT;
-      // what no row sees may be NaN in V: zeros, by its scale
-      const bool part = is_v && (key0 + KT > s.len || key0 < lo_min);
-#pragma unroll 2
-      for (int r = r0; r < KT; r += RP) {
-        uint32_t w[4];
-        lds_words<4>(w, src + r * (D / 2));
-        uint32_t u = lds_u16(src + scale_at + r * (D / 16));
-        if (part && (key0 + r >= s.len || (key0 + r < lo_min && key0 + r >= sinks))) u = 0;
-        uint32_t sc = e4m3x2_f16x2(u);
-        if (D >= 128 && (turn & 2)) {
-          const uint32_t x = w[0], y = w[1];
-          w[0] = w[2];
-          w[1] = w[3];
-          w[2] = x;
-          w[3] = y;
-          sc = __byte_perm(sc, sc, 0x1032);
-        }
-        if (D == 256 && (turn & 1)) {
-          const uint32_t x = w[0], y = w[2];
-          w[0] = w[1];
-          w[1] = x;
-          w[2] = w[3];
-          w[3] = y;
-        }
-        const uint32_t s0 = __byte_perm(sc, sc, 0x1010), s1 = __byte_perm(sc, sc, 0x3232);
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const uint32_t m = i < 2 ? s0 : s1;
-          sts_words(dst + r * 128 + to[i], hmul2(e2m1x2_f16x2<0>(w[i]), m), hmul2(e2m1x2_f16x2<1>(w[i]), m),
-                    hmul2(e2m1x2_f16x2<2>(w[i]), m), hmul2(e2m1x2_f16x2<3>(w[i]), m));
-        }
-      }
-      fence_proxy_async_smem();           // before the products read it
-      __syncwarp();
-      if (lane == 0) {
-        mbar_arrive(&b_free[raw]);
-        mbar_arrive(&b_full[slot]);
-      }
-      return true;
-    });
-    if (!ok) give_up();
+  } else if (!C::OWN && warp >= W_CONV) {
+    // ------------------------------------------------------------ conversion
+    if (!in_order([&](int x, bool is_v) { return convert(tid - W_CONV * 32, x, is_v); })) give_up();
   } else if (warp < W_MMA + NT && n > 0) {
     // ------------------------------------------------------------ issuers, one per query tile (as in the 16-bit kernel)
     constexpr uint32_t ID_S = tc_idesc_16(false, false, KT), ID_O = tc_idesc_16(false, true, D);
@@ -343,8 +356,8 @@ __global__ void __launch_bounds__(Chunk4Cfg<D>::THREADS, 1) paged4_chunk_kernel(
       }
     };
     auto s_mma = [&](int j) {                               // S of tile j
-      const int slot = pos_k<SB>(j) % NS;
-      until(&b_full[slot], pos_k<SB>(j) / NS);
+      const int slot = j & 1;
+      until(&b_full[slot], j >> 1);
       tc_fence_after();
       if (leader) {
         const uint64_t kd = k_desc + (uint64_t)((slot * C::SLOT) >> 4);
@@ -358,9 +371,9 @@ __global__ void __launch_bounds__(Chunk4Cfg<D>::THREADS, 1) paged4_chunk_kernel(
       __syncwarp();
     };
     auto pv_mma = [&](int j) {                              // O += P V of tile j
-      const int pos = pos_v<SB>(j, n), slot = pos % NS;
+      const int slot = 2 + (j & 1);
       const uint64_t vd = v_desc + (uint64_t)((slot * C::SLOT) >> 4);
-      until(&b_full[slot], pos / NS);
+      until(&b_full[slot], j >> 1);
       my_turn(j);
 #pragma unroll
       for (int h = 0; h < 2; ++h) {                         // P arrives in halves
@@ -373,7 +386,7 @@ __global__ void __launch_bounds__(Chunk4Cfg<D>::THREADS, 1) paged4_chunk_kernel(
           if (h == 1 && j + 1 == mine) pass_turn();
           if (h == 1) tc_commit(&b_pv[t]);
           // P came out of S, so K of this tile is done with
-          if (h == 0) mbar_arrive(&b_empty[pos_k<SB>(j) % NS]);
+          if (h == 0) mbar_arrive(&b_empty[j & 1]);
         }
         __syncwarp();
       }
@@ -381,7 +394,7 @@ __global__ void __launch_bounds__(Chunk4Cfg<D>::THREADS, 1) paged4_chunk_kernel(
     // O of tile j is there: its V is done with
     auto pv_done = [&](int j) {
       until(&b_pv[t], j);
-      if (leader) mbar_arrive(&b_empty[pos_v<SB>(j, n) % NS]);
+      if (leader) mbar_arrive(&b_empty[2 + (j & 1)]);
       __syncwarp();
     };
     if (mine > 0) {
@@ -397,11 +410,10 @@ __global__ void __launch_bounds__(Chunk4Cfg<D>::THREADS, 1) paged4_chunk_kernel(
       if (SB == 1 && j + 1 < mine) s_mma(j + 1);
     }
     for (int j = mine; j < n; ++j) {                        // the other tile's keys: hand the slots on
-      const int pk = pos_k<SB>(j), pv = pos_v<SB>(j, n);
-      until(&b_full[pk % NS], pk / NS);
-      if (leader) mbar_arrive(&b_empty[pk % NS]);
-      until(&b_full[pv % NS], pv / NS);
-      if (leader) mbar_arrive(&b_empty[pv % NS]);
+      until(&b_full[j & 1], j >> 1);
+      if (leader) mbar_arrive(&b_empty[j & 1]);
+      until(&b_full[2 + (j & 1)], j >> 1);
+      if (leader) mbar_arrive(&b_empty[2 + (j & 1)]);
       __syncwarp();
     }
     ok = __all_sync(0xffffffffu, ok);
@@ -460,6 +472,8 @@ __global__ void __launch_bounds__(Chunk4Cfg<D>::THREADS, 1) paged4_chunk_kernel(
     }
     const uint32_t lanes = tmem + ((uint32_t)((warp & 3) * 32) << 16);
     const uint32_t c_o = lanes + C::C_O + t * D;
+    auto mine_of = [&](int x, bool is_v) { return is_v != (t == 0) || convert(r, x, is_v); };   // V's tiles, or K's
+    if (C::OWN) ok = before_all(mine_of);
     for (int j = 0; j < mine; ++j) {
       const uint32_t c_s = lanes + (t * SB + j % SB) * KT;
       // a thread whose wait gave up goes on (its warp stays together) and writes nothing
@@ -535,7 +549,10 @@ __global__ void __launch_bounds__(Chunk4Cfg<D>::THREADS, 1) paged4_chunk_kernel(
       float l0, l1;
       unpack64(add2(sum[0], sum[1]), l0, l1);
       l += l0 + l1;
+      if (C::OWN) ok &= after_scores(j, mine_of);
     }
+    if (C::OWN)
+      for (int j = mine; ok && j < n; ++j) ok = after_scores(j, mine_of);   // the other tile's keys
     if (mine > 0) ok &= tc_wait(&b_pv[t], (uint32_t)((mine - 1) & 1), &s_abort);
     ok = __all_sync(0xffffffffu, ok);
     if (ok) {
