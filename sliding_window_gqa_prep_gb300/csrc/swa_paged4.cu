@@ -31,21 +31,25 @@ namespace swa {
 constexpr int kWarps4 = 4;           // warps that compute
 constexpr int kMinKeys4 = 256;       // a CTA takes at least this many keys
 
-// A warp has NV tiles of 8 query vectors; VG groups of warps share a tile's keys and have other vectors.
-template <int D, int NV, int VG>
+// A warp has NV tiles of 8 query vectors. VG groups of warps share a tile's keys and have other vectors; FS
+// warps share keys and vectors and have other features: they add their parts of the scores up through shared
+// memory (at hd 256, where a warp with all features would have room for 8 vectors only, or convert twice).
+template <int D, int NV, int VG, int FS>
 struct Split4Cfg {
   static constexpr int THREADS = kWarps4 * 32 + 32;         // and the warp that copies
   static constexpr int KT = D == 256 ? 64 : 128;            // keys of a tile
   static constexpr int CODES = KT * D / 2, SCALES = KT * D / 16, STAGE = 2 * (CODES + SCALES);
   static constexpr int ROWS = 8 * NV * VG;                  // query vectors
-  static constexpr bool QS = NV * D > 128;                  // Q^T waits in shared memory, not in registers
-  static constexpr int CTAS = D == 64 && NV == 1 ? 4 : 3;   // an SM: 96 or 128 registers a thread
+  static constexpr int DW = D / FS;                         // features of a warp
+  static constexpr bool QS = NV * DW > 128;                 // Q^T waits in shared memory, not in registers
+  static constexpr int CTAS = DW == 64 && NV == 1 ? 4 : 3;   // an SM: 96 or 128 registers a thread
   static constexpr int JT = 4 / NV;                         // 16-feature tiles of O that the warps join at a time
   static constexpr int JOIN = kWarps4 * JT * NV * 512;      // bytes: 8 KB
   static constexpr int QB = QS ? ROWS * D * 2 : 0;
-  static constexpr int FIT = (226 * 1024 / CTAS - 1024 - JOIN - QB - 128 - 1024) / STAGE;
+  static constexpr int XB = FS > 1 ? 2 * kWarps4 * NV * 512 : 0;   // parts of scores, two rounds
+  static constexpr int FIT = (226 * 1024 / CTAS - 1024 - JOIN - QB - XB - 128 - 1024) / STAGE;
   static constexpr int ST = FIT < 8 ? FIT : 8;
-  static constexpr int SMEM = ST * STAGE + JOIN + QB + 128; // + alignment
+  static constexpr int SMEM = ST * STAGE + JOIN + QB + XB + 128;   // + alignment
 };
 
 __device__ __forceinline__ uint32_t movmatrix(uint32_t a) {
@@ -67,27 +71,26 @@ __device__ __forceinline__ void unrolled(F f) {
   }
 }
 
-// One vector's features as the B operands of lane lt's columns (pairs of f16), scaled; the inverse
-// scale is returned. By a whole warp.
-template <int D>
-__device__ __forceinline__ float load_query4(const Attend4Params& p, long long at, bool in, int lt, uint32_t (&q)[D / 16][2]) {
-  constexpr int CH = D == 256 ? 2 : 1, N = D / 32 / CH;     // 16-byte loads of a run of features
-  const uint16_t* const src = static_cast<const uint16_t*>(p.a.q) + at;
+// Part `part` of FS of one vector's features as the B operands of lane lt's columns (pairs of f16), scaled by the
+// whole vector's largest value; the inverse scale is returned. By a whole warp.
+template <int D, int FS>
+__device__ __forceinline__ float load_query4(const Attend4Params& p, long long at, bool in, int lt, int part, uint32_t (&q)[D / FS / 16][2]) {
+  constexpr int DW = D / FS, N = DW / 32;                   // 16-byte loads of a lane
+  const uint16_t* const src = static_cast<const uint16_t*>(p.a.q) + at + lt * (8 * N);
   float top = 0.f;
-#pragma unroll
-  for (int c = 0; c < CH; ++c)
+  auto fetch = [&](int c) {
 #pragma unroll
     for (int i = 0; i < N; ++i) {
-      const uint4 w = in ? *reinterpret_cast<const uint4*>(src + c * 128 + lt * (8 * N) + i * 8) : make_uint4(0, 0, 0, 0);
-      const int s = (c * N + i) * 2;
-      q[s][0] = w.x;
-      q[s][1] = w.y;
-      q[s + 1][0] = w.z;
-      q[s + 1][1] = w.w;
+      const uint4 w = in ? *reinterpret_cast<const uint4*>(src + c * DW + i * 8) : make_uint4(0, 0, 0, 0);
+      q[2 * i][0] = w.x;
+      q[2 * i][1] = w.y;
+      q[2 * i + 1][0] = w.z;
+      q[2 * i + 1][1] = w.w;
     }
+  };
   auto each = [&](auto f) {
 #pragma unroll
-    for (int s = 0; s < D / 16; ++s)
+    for (int s = 0; s < DW / 16; ++s)
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
         float x, y;
@@ -96,7 +99,11 @@ __device__ __forceinline__ float load_query4(const Attend4Params& p, long long a
         f(q[s][i], x, y);
       }
   };
-  each([&](uint32_t&, float x, float y) { top = fmaxf(top, fmaxf(fabsf(x), fabsf(y))); });
+#pragma unroll
+  for (int c = FS - 1; c >= 0; --c) {                       // its own part last
+    fetch((part + c) % FS);
+    each([&](uint32_t&, float x, float y) { top = fmaxf(top, fmaxf(fabsf(x), fabsf(y))); });
+  }
   top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
   top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
   float inv;
@@ -118,11 +125,11 @@ __device__ __forceinline__ Tiles4 split4_tiles(const PagedSeq& s, const Attend4P
   return key_tiles(s, p, kt);
 }
 
-template <int D, int NV, int VG>
-__global__ void __launch_bounds__(Split4Cfg<D, NV, VG>::THREADS, Split4Cfg<D, NV, VG>::CTAS)
+template <int D, int NV, int VG, int FS>
+__global__ void __launch_bounds__(Split4Cfg<D, NV, VG, FS>::THREADS, Split4Cfg<D, NV, VG, FS>::CTAS)
     paged4_split_kernel(const __grid_constant__ Attend4Params p) {
-  using C = Split4Cfg<D, NV, VG>;
-  constexpr int ST = C::ST, KT = C::KT, KS = D / 16, NW = C::THREADS / 32, KG = kWarps4 / VG, SUBS = KT / 16 / KG;
+  using C = Split4Cfg<D, NV, VG, FS>;
+  constexpr int DW = C::DW, ST = C::ST, KT = C::KT, KS = DW / 16, NW = C::THREADS / 32, KG = kWarps4 / (VG * FS), SUBS = KT / 16 / KG;
   constexpr bool QS = C::QS;
   extern __shared__ unsigned char sm_raw[];
   __shared__ __align__(8) uint64_t b_full[ST], b_empty[ST];
@@ -279,11 +286,15 @@ __global__ void __launch_bounds__(Split4Cfg<D, NV, VG>::THREADS, Split4Cfg<D, NV
   }
 
   // ------------------------------------------------------------ products
-  const int lg = lane >> 2, lt = lane & 3, hpg = a.hpg, vg = warp / KG;
+  const int lg = lane >> 2, lt = lane & 3, hpg = a.hpg, fs = warp / KG % FS, vg = warp / (KG * FS);
   // the key of the group's 16 that is row i of the products: lanes that read at the same time
   // then find rows of both parities, and fewer of them in the same banks
   auto key_of = [](int i) { return i ^ ((i >> 1) & 1); };
   bool ok = true;                           // a thread whose wait gave up goes on and writes nothing
+  // FS = 2: where this warp's parts of scores go, those of the other one, and which of two rounds it is
+  const uint32_t x_base = smb + ST * C::STAGE + C::JOIN + C::QB + lane * 16;
+  const uint32_t x_mine = x_base + warp * (NV * 512), x_other = x_base + (warp ^ KG) * (NV * 512);
+  uint32_t turn = 0;
   int st = 0;                               // the next tile's stage, and the parity of its barrier's phase
   uint32_t phase = 0;
   do {
@@ -293,25 +304,26 @@ __global__ void __launch_bounds__(Split4Cfg<D, NV, VG>::THREADS, Split4Cfg<D, NV
     uint32_t qf[QS ? 1 : NV][KS][2];
     float qm[NV][2];
     int lim[NV][2];
-    auto query = [&](int tile, uint32_t (&q)[KS][2]) {      // of 8 vectors; the inverse scale of vector lg
+    auto query = [&](int tile, int part, uint32_t (&q)[KS][2]) {      // of 8 vectors; the inverse scale of vector lg
       const int r = tile * 8 + lg;
       const bool in = r < nvec;
       const int i = in ? r / hpg : 0, h = in ? r % hpg : 0;
-      return load_query4<D>(p, (long long)(s.r0 + i) * a.q_row + (long long)(g * hpg + h) * D, in, lt, q);
+      return load_query4<D, FS>(p, (long long)(s.r0 + i) * a.q_row + (long long)(g * hpg + h) * D, in, lt, part, q);
     };
     if constexpr (QS) {
-      for (int tile = warp; tile < C::ROWS / 8; tile += kWarps4) {
-        const float shift = query(tile, qf[0]);
-        if (lt == 0) s_shift[tile * 8 + lg] = shift;
+      for (int x = warp; x < C::ROWS / 8 * FS; x += kWarps4) {
+        const int tile = x / FS;
+        const float shift = query(tile, x % FS, qf[0]);
+        if (lt == 0) s_shift[tile * 8 + lg] = shift;        // (the same from every part)
 #pragma unroll
-        for (int i = 0; i < KS; ++i) s_q[(tile * KS + i) * 32 + lane] = make_uint2(qf[0][i][0], qf[0][i][1]);
+        for (int i = 0; i < KS; ++i) s_q[(x * KS + i) * 32 + lane] = make_uint2(qf[0][i][0], qf[0][i][1]);
       }
       named_barrier(1, kWarps4 * 32);
     }
 #pragma unroll
     for (int v = 0; v < NV; ++v) {
       float shift = 0.f;
-      if constexpr (!QS) shift = query(vg * NV + v, qf[v]);
+      if constexpr (!QS) shift = query(vg * NV + v, fs, qf[v]);
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
         const int c = (vg * NV + v) * 8 + 2 * lt + e;
@@ -323,7 +335,7 @@ __global__ void __launch_bounds__(Split4Cfg<D, NV, VG>::THREADS, Split4Cfg<D, NV
     auto q_at = [&](int v, int i) {
       if constexpr (QS) {
         uint32_t w[2];
-        lds_words<2>(w, q_base + ((vg * NV + v) * KS + i) * 256);
+        lds_words<2>(w, q_base + (((vg * NV + v) * FS + fs) * KS + i) * 256);
         return make_uint2(w[0], w[1]);
       } else {
         return make_uint2(qf[v][i][0], qf[v][i][1]);
@@ -349,12 +361,13 @@ __global__ void __launch_bounds__(Split4Cfg<D, NV, VG>::THREADS, Split4Cfg<D, NV
 
     // this lane's keys of 16 in S (ka and ka + 8) and in P V (k1, k2 and these + 8), and its places in a stage
     const int ka = key_of(lg), k1 = key_of(2 * lt), k2 = key_of(2 * lt + 1);
-    constexpr int W = D == 64 ? 2 : 4, CH = D == 256 ? 2 : 1;        // words of a key in S at a time, and how often
-    constexpr int VW = D / 64;                                       // words of a key in P V
-    const uint32_t group0 = smb + (warp % KG) * SUBS * 16 * (D / 2), scale0 = smb + 2 * C::CODES + (warp % KG) * SUBS * 16 * (D / 16);
-    const uint32_t at_k = group0 + ka * (D / 2) + lt * (W * 4), at_ks = scale0 + ka * (D / 16) + (D == 64 ? lt : lt * 2);
+    constexpr int W = DW == 64 ? 2 : 4;                              // words of a key in S
+    constexpr int VW = DW / 64;                                      // .. and in P V
+    const uint32_t group0 = smb + (warp % KG) * SUBS * 16 * (D / 2) + fs * (DW / 2);
+    const uint32_t scale0 = smb + 2 * C::CODES + (warp % KG) * SUBS * 16 * (D / 16) + fs * (DW / 16);
+    const uint32_t at_k = group0 + ka * (D / 2) + lt * (W * 4), at_ks = scale0 + ka * (D / 16) + (DW == 64 ? lt : lt * 2);
     const uint32_t at_v1 = group0 + C::CODES + k1 * (D / 2) + lg * (VW * 4), at_v2 = at_v1 + (k2 - k1) * (D / 2);
-    const uint32_t at_vs1 = scale0 + C::SCALES + k1 * (D / 16) + (D == 64 ? lg >> 1 : D == 128 ? lg : lg * 2);
+    const uint32_t at_vs1 = scale0 + C::SCALES + k1 * (D / 16) + (DW == 64 ? lg >> 1 : lg);
     const uint32_t at_vs2 = at_vs1 + (k2 - k1) * (D / 16);
 #pragma unroll 1
     for (int x = tile0; x < tile1; ++x) {
@@ -368,7 +381,7 @@ __global__ void __launch_bounds__(Split4Cfg<D, NV, VG>::THREADS, Split4Cfg<D, NV
         const bool mask = __any_sync(0xffffffffu, k0 + 16 > lim_min || k0 < lo_max);   // a branch, not selects
         // V^T: keys 2 lt, 2 lt + 1 (+ 8) of the products' rows, features (hd / 8) lg ..;
         // loaded and regrouped while S is computed
-        uint32_t lo[2][VW], hi[2][VW], u1[2], u2[2], vs[2][2];
+        uint32_t lo[2][VW], hi[2][VW], u1[2], u2[2], vs[2];
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
           uint32_t w1[VW], w2[VW];
@@ -379,8 +392,8 @@ __global__ void __launch_bounds__(Split4Cfg<D, NV, VG>::THREADS, Split4Cfg<D, NV
             lo[h][w] = low_halves(w1[w], w2[w]);
             hi[h][w] = high_halves(w1[w], w2[w]);
           }
-          u1[h] = D == 256 ? lds_u16(at_vs1 + scales + h * 8 * (D / 16)) : lds_u8(at_vs1 + scales + h * 8 * (D / 16));
-          u2[h] = D == 256 ? lds_u16(at_vs2 + scales + h * 8 * (D / 16)) : lds_u8(at_vs2 + scales + h * 8 * (D / 16));
+          u1[h] = lds_u8(at_vs1 + scales + h * 8 * (D / 16));
+          u2[h] = lds_u8(at_vs2 + scales + h * 8 * (D / 16));
         }
         float sc[NV][4];
 #pragma unroll
@@ -388,33 +401,43 @@ __global__ void __launch_bounds__(Split4Cfg<D, NV, VG>::THREADS, Split4Cfg<D, NV
 #pragma unroll
           for (int e = 0; e < 4; ++e) sc[v][e] = 0.f;
         // 4 features a step
+        uint32_t wa[W], wc[W], sa[2], sb[2];  // codes of the two keys; a block's scale in both halves
+        lds_words<W>(wa, at_k + codes);
+        lds_words<W>(wc, at_k + codes + 8 * (D / 2));
+        if constexpr (DW == 64) {
+          sa[0] = e4m3x2_f16x2(lds_u8(at_ks + scales) * 0x0101u);
+          sb[0] = e4m3x2_f16x2(lds_u8(at_ks + scales + 8 * (D / 16)) * 0x0101u);
+        } else {
+          const uint32_t ua = e4m3x2_f16x2(lds_u16(at_ks + scales)), uc = e4m3x2_f16x2(lds_u16(at_ks + scales + 8 * (D / 16)));
+          sa[0] = __byte_perm(ua, ua, 0x1010);
+          sa[1] = __byte_perm(ua, ua, 0x3232);
+          sb[0] = __byte_perm(uc, uc, 0x1010);
+          sb[1] = __byte_perm(uc, uc, 0x3232);
+        }
+        unrolled<0, KS>([&](auto i) {
+          constexpr int I = decltype(i)::value, B = DW == 64 ? 0 : I / 4;
+          const uint32_t f[4] = {hmul2(codes_pair<2 * I>(wa), sa[B]), hmul2(codes_pair<2 * I>(wc), sb[B]),
+                                 hmul2(codes_pair<2 * I + 1>(wa), sa[B]), hmul2(codes_pair<2 * I + 1>(wc), sb[B])};
 #pragma unroll
-        for (int c = 0; c < CH; ++c) {
-          uint32_t wa[W], wc[W];
-          lds_words<W>(wa, at_k + codes + c * 64);
-          lds_words<W>(wc, at_k + codes + c * 64 + 8 * (D / 2));
-          uint32_t sa[2], sb[2];            // a block's scale in both halves
-          if constexpr (D == 64) {
-            sa[0] = e4m3x2_f16x2(lds_u8(at_ks + scales) * 0x0101u);
-            sb[0] = e4m3x2_f16x2(lds_u8(at_ks + scales + 8 * (D / 16)) * 0x0101u);
-          } else {
-            const uint32_t ua = e4m3x2_f16x2(lds_u16(at_ks + scales + c * 8));
-            const uint32_t uc = e4m3x2_f16x2(lds_u16(at_ks + scales + c * 8 + 8 * (D / 16)));
-            sa[0] = __byte_perm(ua, ua, 0x1010);
-            sa[1] = __byte_perm(ua, ua, 0x3232);
-            sb[0] = __byte_perm(uc, uc, 0x1010);
-            sb[1] = __byte_perm(uc, uc, 0x3232);
+          for (int v = 0; v < NV; ++v) {
+            const uint2 q = q_at(v, I);
+            mma16816<__half>(sc[v], f, q.x, q.y);
           }
-          unrolled<0, KS / CH>([&](auto i) {
-            constexpr int I = decltype(i)::value, B = D == 64 ? 0 : I / 4;
-            const uint32_t f[4] = {hmul2(codes_pair<2 * I>(wa), sa[B]), hmul2(codes_pair<2 * I>(wc), sb[B]),
-                                   hmul2(codes_pair<2 * I + 1>(wa), sa[B]), hmul2(codes_pair<2 * I + 1>(wc), sb[B])};
+        });
+        if constexpr (FS == 2) {            // the other features' part, added in the same order by both
 #pragma unroll
-            for (int v = 0; v < NV; ++v) {
-              const uint2 q = q_at(v, c * (KS / CH) + I);
-              mma16816<__half>(sc[v], f, q.x, q.y);
-            }
-          });
+          for (int v = 0; v < NV; ++v)
+            sts_words(x_mine + turn + v * 512, __float_as_uint(sc[v][0]), __float_as_uint(sc[v][1]), __float_as_uint(sc[v][2]),
+                      __float_as_uint(sc[v][3]));
+          named_barrier(2 + vg * KG + warp % KG, 64);
+#pragma unroll
+          for (int v = 0; v < NV; ++v) {
+            uint32_t y[4];
+            lds_words<4>(y, x_other + turn + v * 512);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) sc[v][e] += __uint_as_float(y[e]);
+          }
+          turn ^= kWarps4 * NV * 512;
         }
         // masked scores: element e is (key row lg + 8 (e / 2), vector 2 lt + e % 2)
         if (mask) {
@@ -475,13 +498,12 @@ __global__ void __launch_bounds__(Split4Cfg<D, NV, VG>::THREADS, Split4Cfg<D, NV
         }
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
-          vs[h][0] = e4m3x2_f16x2(__byte_perm(u1[h], u2[h], 0x0040));
-          if constexpr (D == 256) vs[h][1] = e4m3x2_f16x2(__byte_perm(u1[h], u2[h], 0x0051));
+          vs[h] = e4m3x2_f16x2(__byte_perm(u1[h], u2[h], 0x0040));
         }
         unrolled<0, KS>([&](auto j) {
-          constexpr int J = decltype(j)::value, B = D == 256 ? J / 8 : 0;
-          const uint32_t f[4] = {hmul2(codes_pair<J>(lo[0]), vs[0][B]), hmul2(codes_pair<J>(hi[0]), vs[0][B]),
-                                 hmul2(codes_pair<J>(lo[1]), vs[1][B]), hmul2(codes_pair<J>(hi[1]), vs[1][B])};
+          constexpr int J = decltype(j)::value;
+          const uint32_t f[4] = {hmul2(codes_pair<J>(lo[0]), vs[0]), hmul2(codes_pair<J>(hi[0]), vs[0]),
+                                 hmul2(codes_pair<J>(lo[1]), vs[1]), hmul2(codes_pair<J>(hi[1]), vs[1])};
 #pragma unroll
           for (int v = 0; v < NV; ++v) mma16816<__half>(o[v][J], f, pf[v][0], pf[v][1]);
         });
@@ -520,9 +542,9 @@ __global__ void __launch_bounds__(Split4Cfg<D, NV, VG>::THREADS, Split4Cfg<D, NV
       named_barrier(1, kWarps4 * 32);
       if (s_abort) continue;
       // a vector c of tile v of group w0 / KG, features 2 j and 2 j + 1 of lane group pg at a time
-      for (int y = tid; y < C::ROWS * C::JT * 8; y += kWarps4 * 32) {
+      for (int y = tid; y < C::ROWS * FS * C::JT * 8; y += kWarps4 * 32) {
         const int c = y & 7, pg = (y >> 3) & 7, j = (y >> 6) % C::JT, v = (y >> 6) / C::JT % NV, w0 = (y >> 6) / (C::JT * NV) * KG;
-        const int pv = (w0 / KG * NV + v) * 8 + c;
+        const int pv = (w0 / (KG * FS) * NV + v) * 8 + c;
         if (pv >= nvec) continue;
         float mt = -INFINITY, lt_ = 0.f, acc[2] = {0.f, 0.f};
 #pragma unroll
@@ -535,7 +557,7 @@ __global__ void __launch_bounds__(Split4Cfg<D, NV, VG>::THREADS, Split4Cfg<D, NV
 #pragma unroll
           for (int h = 0; h < 2; ++h) acc[h] += f * join[(((((w0 + w) * NV + v) * C::JT + j) * 2 + h) * 8 + pg) * 8 + c];
         }
-        const int f = pg * (D / 8) + 2 * (j0 + j);
+        const int f = w0 / KG % FS * DW + pg * (DW / 8) + 2 * (j0 + j);
         acc[0] *= p.c.v_mul;
         acc[1] *= p.c.v_mul;
         if (whole) {
@@ -573,16 +595,16 @@ struct Split4Plan {
   size_t off_ml, off_desc, bytes;
 };
 
-template <int D, int NV, int VG>
+template <int D, int NV, int VG, int FS>
 static int split4_occupancy() {
   static int cache[64] = {};
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return 1;
   if (!cache[dev]) {
-    auto k = paged4_split_kernel<D, NV, VG>;
+    auto k = paged4_split_kernel<D, NV, VG, FS>;
     int n = 0;
-    if (allow_smem<paged4_split_kernel<D, NV, VG>>(Split4Cfg<D, NV, VG>::SMEM) != cudaSuccess ||
-        cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, k, Split4Cfg<D, NV, VG>::THREADS, Split4Cfg<D, NV, VG>::SMEM) != cudaSuccess || n < 1) {
+    if (allow_smem<paged4_split_kernel<D, NV, VG, FS>>(Split4Cfg<D, NV, VG, FS>::SMEM) != cudaSuccess ||
+        cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, k, Split4Cfg<D, NV, VG, FS>::THREADS, Split4Cfg<D, NV, VG, FS>::SMEM) != cudaSuccess || n < 1) {
       (void)cudaGetLastError();
       n = 1;
     }
@@ -591,12 +613,12 @@ static int split4_occupancy() {
   return cache[dev];
 }
 
-template <int D, int NV, int VG>
+template <int D, int NV, int VG, int FS>
 static int launch_split4(const Attend4Params& p, const Split4Plan& sp, cudaStream_t s) {
-  const cudaError_t e = allow_smem<paged4_split_kernel<D, NV, VG>>(Split4Cfg<D, NV, VG>::SMEM);
+  const cudaError_t e = allow_smem<paged4_split_kernel<D, NV, VG, FS>>(Split4Cfg<D, NV, VG, FS>::SMEM);
   if (e != cudaSuccess) return cuda_status(e);
-  const int rc = finish_launch(launch_pdl(paged4_split_kernel<D, NV, VG>, dim3(sp.grid), dim3(Split4Cfg<D, NV, VG>::THREADS),
-                                          Split4Cfg<D, NV, VG>::SMEM, s, p));
+  const int rc = finish_launch(launch_pdl(paged4_split_kernel<D, NV, VG, FS>, dim3(sp.grid), dim3(Split4Cfg<D, NV, VG, FS>::THREADS),
+                                          Split4Cfg<D, NV, VG, FS>::SMEM, s, p));
   if (rc != SWA_OK || p.a.whole) return rc;
   // a block a row up to 16, which then take rows in turn: most of sp.grid's columns are empty
   const long long vecs = (long long)p.a.max_rows * p.a.hpg;
@@ -608,8 +630,10 @@ static int launch_split4(const Attend4Params& p, const Split4Plan& sp, cudaStrea
 // rows: query vectors of a block, 8, 16 or 32 (hd 256: 8 or 16)
 template <typename F>
 static int by_size4(int hd, int rows, F f) {
-  if (hd == 256) return rows == 8 ? f(Int<256>{}, Int<1>{}, Int<1>{}) : f(Int<256>{}, Int<1>{}, Int<2>{});
-#define SWA_ROWS(D) (rows == 8 ? f(Int<D>{}, Int<1>{}, Int<1>{}) : rows == 16 ? f(Int<D>{}, Int<2>{}, Int<1>{}) : f(Int<D>{}, Int<2>{}, Int<2>{}))
+  if (hd == 256) return rows == 8 ? f(Int<256>{}, Int<1>{}, Int<1>{}, Int<2>{}) : f(Int<256>{}, Int<2>{}, Int<1>{}, Int<2>{});
+#define SWA_ROWS(D) \
+  (rows == 8 ? f(Int<D>{}, Int<1>{}, Int<1>{}, Int<1>{}) : rows == 16 ? f(Int<D>{}, Int<2>{}, Int<1>{}, Int<1>{}) \
+                                                                     : f(Int<D>{}, Int<2>{}, Int<2>{}, Int<1>{}))
   return hd == 64 ? SWA_ROWS(64) : SWA_ROWS(128);
 #undef SWA_ROWS
 }
@@ -627,8 +651,8 @@ static void split4_plan(const swa_paged4_attend_args* a, long long vecs, Split4P
     keys = w < keys ? w : keys;
   }
   sp->whole = keys <= kWholeKeys4;
-  const int occ = sp->whole ? 0 : by_size4(c.hd, sp->rows, [](auto d, auto n, auto g) {
-    return split4_occupancy<decltype(d)::value, decltype(n)::value, decltype(g)::value>();
+  const int occ = sp->whole ? 0 : by_size4(c.hd, sp->rows, [](auto d, auto n, auto g, auto f) {
+    return split4_occupancy<decltype(d)::value, decltype(n)::value, decltype(g)::value, decltype(f)::value>();
   });
   sp->grid = sp->whole ? c.B * c.nk : (num_sms() > 0 ? num_sms() : 148) * occ;
   if (!sp->whole) {
@@ -735,8 +759,8 @@ int swa_paged4_attend(const swa_paged4_attend_args* a, cudaStream_t stream) {
     pa.ws_acc = reinterpret_cast<float*>(ws);
     pa.ws_ml = reinterpret_cast<float2*>(ws + pl.split.off_ml);
     pa.ws_desc = reinterpret_cast<int4*>(ws + pl.split.off_desc);
-    rc = by_size4(c.hd, pl.split.rows, [&](auto d, auto n, auto g) {
-      return launch_split4<decltype(d)::value, decltype(n)::value, decltype(g)::value>(p, pl.split, stream);
+    rc = by_size4(c.hd, pl.split.rows, [&](auto d, auto n, auto g, auto f) {
+      return launch_split4<decltype(d)::value, decltype(n)::value, decltype(g)::value, decltype(f)::value>(p, pl.split, stream);
     });
     if (rc != SWA_OK) return rc;
   }

@@ -201,24 +201,14 @@ __global__ void __launch_bounds__(Chunk4Cfg<D>::THREADS, 1) paged4_chunk_kernel(
   auto wait = [&](uint64_t* bar, int phase) -> bool {
     return __all_sync(0xffffffffu, tc_wait(bar, (uint32_t)(phase & 1), &s_abort));
   };
-  // K and V tiles in the order in which they are copied and converted: K 0, K 1, V 0, then V x + 1 and K x + 2
-  // after the scores of x; f(tile, is V)
-  auto before_all = [&](auto f) {
-    bool ok = true;
-    if (n > 0) ok = f(0, false);
-    if (ok && n > 1) ok = f(1, false);
-    if (ok && n > 0) ok = f(0, true);
-    return ok;
-  };
-  auto after_scores = [&](int x, auto f) {
-    bool ok = true;
-    if (x + 1 < n) ok = f(x + 1, true);
-    if (ok && x + 2 < n) ok = f(x + 2, false);
-    return ok;
-  };
+  // K and V tiles in the order in which they are copied and converted, V x + 1 and K x + 2 after the scores of x: K 0,
+  // V 0, K 1, V 1, ..; f(tile, is V)
   auto in_order = [&](auto f) {
-    bool ok = before_all(f);
-    for (int x = 0; ok && x < n; ++x) ok = after_scores(x, f);
+    bool ok = true;
+    for (int x = -2; ok && x < n; ++x) {
+      if (x >= -1 && x + 1 < n) ok = f(x + 1, true);
+      if (ok && x + 2 < n) ok = f(x + 2, false);
+    }
     return ok;
   };
   // tile x's slot of codes and the use of it
@@ -472,8 +462,13 @@ __global__ void __launch_bounds__(Chunk4Cfg<D>::THREADS, 1) paged4_chunk_kernel(
     }
     const uint32_t lanes = tmem + ((uint32_t)((warp & 3) * 32) << 16);
     const uint32_t c_o = lanes + C::C_O + t * D;
-    auto mine_of = [&](int x, bool is_v) { return is_v != (t == 0) || convert(r, x, is_v); };   // V's tiles, or K's
-    if (C::OWN) ok = before_all(mine_of);
+    // After the scores of tile j a later one (own or not) is converted: V j + 1 by the first query tile's threads,
+    // K j + 2 by the second's
+    const int ahead = t == 0 ? 1 : 2;
+    if (C::OWN) {
+#pragma unroll 1
+      for (int x = 0; x < min(ahead, n); ++x) ok &= convert(r, x, t == 0);
+    }
     for (int j = 0; j < mine; ++j) {
       const uint32_t c_s = lanes + (t * SB + j % SB) * KT;
       // a thread whose wait gave up goes on (its warp stays together) and writes nothing
@@ -505,7 +500,7 @@ __global__ void __launch_bounds__(Chunk4Cfg<D>::THREADS, 1) paged4_chunk_kernel(
         // with one S buffer S of this tile came after P V of the last one
         if (SB == 2) ok &= tc_wait(&b_pv[t], (uint32_t)((j - 1) & 1), &s_abort);
         if (SB == 2) tc_fence_after();
-#pragma unroll
+#pragma unroll 1
         for (int i = 0; i < D / 32; ++i) {
           uint32_t o[32];
           tc_ld32(c_o + i * 32, o);
@@ -549,10 +544,12 @@ __global__ void __launch_bounds__(Chunk4Cfg<D>::THREADS, 1) paged4_chunk_kernel(
       float l0, l1;
       unpack64(add2(sum[0], sum[1]), l0, l1);
       l += l0 + l1;
-      if (C::OWN) ok &= after_scores(j, mine_of);
+      if (C::OWN && j + ahead < n) ok &= convert(r, j + ahead, t == 0);
     }
-    if (C::OWN)
-      for (int j = mine; ok && j < n; ++j) ok = after_scores(j, mine_of);   // the other tile's keys
+    if (C::OWN) {                                           // the other tile's keys
+#pragma unroll 1
+      for (int x = mine + ahead; x < n; ++x) ok &= convert(r, x, t == 0);
+    }
     if (mine > 0) ok &= tc_wait(&b_pv[t], (uint32_t)((mine - 1) & 1), &s_abort);
     ok = __all_sync(0xffffffffu, ok);
     if (ok) {
