@@ -42,7 +42,9 @@ struct Split4Cfg {
   static constexpr int ROWS = 8 * NV * VG;                  // query vectors
   static constexpr int DW = D / FS;                         // features of a warp
   static constexpr bool QS = NV * DW > 128;                 // Q^T waits in shared memory, not in registers
-  static constexpr int CTAS = DW == 64 && NV == 1 ? 4 : 3;   // an SM: 96 or 128 registers a thread
+  // CTAs an SM: 96 registers a thread for four, 128 for three, 168 for two (NV = 2 with 128 features spills with 128:
+  // 16 vectors over 32 x 6144 keys, 8 KV heads, 93 us with three, 85 with two)
+  static constexpr int CTAS = DW == 64 ? 5 - NV : 4 - NV;
   static constexpr int JT = 4 / NV;                         // 16-feature tiles of O that the warps join at a time
   static constexpr int JOIN = kWarps4 * JT * NV * 512;      // bytes: 8 KB
   static constexpr int QB = QS ? ROWS * D * 2 : 0;
