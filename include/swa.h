@@ -764,10 +764,10 @@ int swa_paged_evict(const swa_paged_evict_args* args, cudaStream_t stream);
  * scale = max|x| / (6 * 2^exp) of the block, rounded to the nearest e4m3 (ties
  * to the even one, 448 at most), and for each x the nearest of level * scale *
  * 2^exp (ties to the even code, 6 at most; zero is code 0, without a sign). A
- * block whose scale rounds to 0 has codes 0; a block with an infinity or NaN has scale NaN and codes 0, and reads
- * as NaN. exp moves the range (2^-9 to 448, times 6) to where the tensor's values
- * are: with exp = 0 blocks whose largest value is below 0.09 lose bits of their
- * scale.
+ * block whose scale rounds to 0 has codes 0; a block with an infinity or NaN has
+ * scale NaN and codes 0, and reads as NaN. exp moves the range (2^-9 to 448, times
+ * 6) to where the tensor's values are: with exp = 0 blocks whose largest value is
+ * below 0.09 lose bits of their scale.
  *   k, v        [num_pages][nk][page][hd / 2] bytes: feature 2i in the lower half
  *               of byte i, 2i + 1 in the upper one; 16-byte aligned
  *   k_scale, v_scale  [num_pages][nk][page][hd / 16] bytes, 16-byte aligned
@@ -852,8 +852,8 @@ int swa_paged4_read(const swa_paged4_read_args* args, cudaStream_t stream);
  * Keys and values enter the products exactly; q is scaled by a power of two a
  * vector and rounded to f16 (bf16 and f16 values keep all bits down to 2^-39 of
  * the vector's largest); scores, maxima and sums are f32; the weights enter the
- * value product in f16, rounded once (relative 2^-11; below 2^-24 of the row's
- * scale to a multiple of 2^-40 of it).
+ * value product in f16, rounded once (relative 2^-11; below 2^-25 of the row's
+ * largest to a multiple of 2^-35 of that).
  *   q    [T][nh][hd] of type q_dtype (SWA_BF16 or SWA_F16), rows q_row elements
  *        apart (heads dense, rows at multiples of 16 bytes); nh / nk <= 32
  *   out  [T][nh][hd] dense, of q's type, or f32 with out_f32 = 1
@@ -958,7 +958,7 @@ int swa_paged_fork(const swa_paged_fork_args* args, cudaStream_t stream);
 
 /*
  * swa_paged_compact — the pages in use move to the front of the pools: with n
- * pages of refs > 0, the i-th of them from page n on (ascending) moves to the i-th
+ * pages in use (refs not 0), the i-th of them from page n on (ascending) moves to the i-th
  * free page below n, in all pools; the others stay.
  *   table [B][max_pages], refs [num_pages] i32; table_out and refs_out the same
  *         afterwards (each may be its input itself). An entry that names a free

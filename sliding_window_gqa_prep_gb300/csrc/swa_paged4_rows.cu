@@ -294,6 +294,7 @@ __global__ void __launch_bounds__(kRThreads, E == 8 ? 2 : 3) paged4_append_kerne
     int e[E];
     rotate(r, raw, static_cast<const TI*>(p.q) + (row0 + r) * p.q_row + (long long)h * HD, x, b, y, e);
     if (s_at[r] == -2) return;
+    if (PAIRS == 2) __syncwarp();                        // q_out may be q, whose partners other lanes read
     const long long to = ((long long)(row0 + r) * nq + h) * HD + f0;
     if (p.q_bf) store_pack(static_cast<__nv_bfloat16*>(p.q_out) + to, y);
     else store_pack(static_cast<__half*>(p.q_out) + to, y);

@@ -277,6 +277,20 @@ def test_scores_of_one_key_above_all_others():
         bt.check(out, lse)
 
 
+@pytest.mark.parametrize("hd,rot,interleaved", [(64, 64, False), (64, 10, True), (128, 128, False), (128, 44, False), (256, 256, False), (256, 20, False)])
+@pytest.mark.parametrize("T", [3, 700])
+def test_queries_rotated_in_place(hd, rot, interleaved, T):
+    """q_out may be q: the same bits as apart, partners in the lane, in another one and in two."""
+    bt = Batch4(t=[T], lens=[T + 5], nh=10, nk=2, hd=hd, page=16)
+    k = torch.randn(T, 2, hd, device="cuda").to(BF)
+    kw = dict(turns=swa.rotary_turns(rot), interleaved=interleaved)
+    pos = dev(range(5, T + 5))
+    apart = swa.paged4_append(k, k, pos, *bt.args, q=bt.q, **kw)
+    own = bt.q.clone()
+    assert swa.paged4_append(k, k, pos, *bt.args, q=own, q_out=own, **kw) is own
+    assert torch.equal(own, apart) and not torch.equal(own, bt.q)
+
+
 def test_refusals_of_the_binding():
     bt = Batch4(t=[2], lens=[20], nh=4, nk=2, hd=64, page=16)
     x = torch.randn(2, 2, 64, device="cuda").to(BF)
