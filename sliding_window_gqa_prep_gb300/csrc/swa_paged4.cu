@@ -29,7 +29,7 @@
 namespace swa {
 
 constexpr int kWarps4 = 4;           // warps that compute
-constexpr int kMinKeys4 = 256;       // a CTA takes at least this many keys
+constexpr int kMinKeys4 = 128;       // a CTA takes at least this many keys (one sequence of 1024, 2 KV heads: 8.6 us, 9.6 with 256)
 
 // A warp has NV tiles of 8 query vectors. VG groups of warps share a tile's keys and have other vectors; FS
 // warps share keys and vectors and have other features: they add their parts of the scores up through shared
@@ -45,10 +45,13 @@ struct Split4Cfg {
   // CTAs an SM: 96 registers a thread for four, 128 for three, 168 for two (NV = 2 with 128 features spills with 128:
   // 16 vectors over 32 x 6144 keys, 8 KV heads, 93 us with three, 85 with two)
   static constexpr int CTAS = DW == 64 ? 5 - NV : 4 - NV;
+  // Groups of 16 keys that a warp takes at a time: two where a tile has them, and the exchange of scores room
+  // (64 x 1024 .. 8192 keys, 4 vectors of 128 features 89 us with one, 85 with two)
+  static constexpr int G = (FS == 1 || NV == 1) && KT / 16 / (kWarps4 / (VG * FS)) >= 2 ? 2 : 1;
   static constexpr int JT = 4 / NV;                         // 16-feature tiles of O that the warps join at a time
   static constexpr int JOIN = kWarps4 * JT * NV * 512;      // bytes: 8 KB
   static constexpr int QB = QS ? ROWS * D * 2 : 0;
-  static constexpr int XB = FS > 1 ? 2 * kWarps4 * NV * 512 : 0;   // parts of scores, two rounds
+  static constexpr int XB = FS > 1 ? 2 * kWarps4 * G * NV * 512 : 0;   // parts of scores, two rounds
   static constexpr int FIT = (226 * 1024 / CTAS - 1024 - JOIN - QB - XB - 128 - 1024) / STAGE;
   static constexpr int ST = FIT < 8 ? FIT : 8;
   static constexpr int SMEM = ST * STAGE + JOIN + QB + XB + 128;   // + alignment
@@ -131,7 +134,7 @@ template <int D, int NV, int VG, int FS>
 __global__ void __launch_bounds__(Split4Cfg<D, NV, VG, FS>::THREADS, Split4Cfg<D, NV, VG, FS>::CTAS)
     paged4_split_kernel(const __grid_constant__ Attend4Params p) {
   using C = Split4Cfg<D, NV, VG, FS>;
-  constexpr int DW = C::DW, ST = C::ST, KT = C::KT, KS = DW / 16, NW = C::THREADS / 32, KG = kWarps4 / (VG * FS), SUBS = KT / 16 / KG;
+  constexpr int DW = C::DW, ST = C::ST, KT = C::KT, KS = DW / 16, NW = C::THREADS / 32, KG = kWarps4 / (VG * FS), SUBS = KT / 16 / KG, G = C::G;
   constexpr bool QS = C::QS;
   extern __shared__ unsigned char sm_raw[];
   __shared__ __align__(8) uint64_t b_full[ST], b_empty[ST];
@@ -295,7 +298,7 @@ __global__ void __launch_bounds__(Split4Cfg<D, NV, VG, FS>::THREADS, Split4Cfg<D
   bool ok = true;                           // a thread whose wait gave up goes on and writes nothing
   // FS = 2: where this warp's parts of scores go, those of the other one, and which of two rounds it is
   const uint32_t x_base = smb + ST * C::STAGE + C::JOIN + C::QB + lane * 16;
-  const uint32_t x_mine = x_base + warp * (NV * 512), x_other = x_base + (warp ^ KG) * (NV * 512);
+  const uint32_t x_mine = x_base + warp * (G * NV * 512), x_other = x_base + (warp ^ KG) * (G * NV * 512);
   uint32_t turn = 0;
   int st = 0;                               // the next tile's stage, and the parity of its barrier's phase
   uint32_t phase = 0;
@@ -376,92 +379,117 @@ __global__ void __launch_bounds__(Split4Cfg<D, NV, VG, FS>::THREADS, Split4Cfg<D
       ok &= tc_wait(&b_full[st], phase, &s_abort);
       __syncwarp();
 #pragma unroll 1
-      for (int sub = 0; sub < SUBS; ++sub) {                // this warp's keys, 16 at a time
+      for (int sub = 0; sub < SUBS; sub += G) {             // this warp's keys, 16 G at a time
         const int k0 = tl.at(x) * KT + (warp % KG) * (SUBS * 16) + sub * 16;
-        if (k0 >= s.len || (k0 + 16 <= lo_min && k0 >= p.sinks)) continue;
+        if (k0 >= s.len || (k0 + 16 * G <= lo_min && k0 >= p.sinks)) continue;
         const uint32_t codes = st * C::STAGE + sub * 16 * (D / 2), scales = st * C::STAGE + sub * 16 * (D / 16);
-        const bool mask = __any_sync(0xffffffffu, k0 + 16 > lim_min || k0 < lo_max);   // a branch, not selects
-        // V^T: keys 2 lt, 2 lt + 1 (+ 8) of the products' rows, features (hd / 8) lg ..;
-        // loaded and regrouped while S is computed
-        uint32_t lo[2][VW], hi[2][VW], u1[2], u2[2], vs[2];
+        const bool mask = __any_sync(0xffffffffu, k0 + 16 * G > lim_min || k0 < lo_max);   // a branch, not selects
+        float sc[G][NV][4];
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          uint32_t w1[VW], w2[VW];
-          lds_words<VW>(w1, at_v1 + codes + h * 8 * (D / 2));
-          lds_words<VW>(w2, at_v2 + codes + h * 8 * (D / 2));
-#pragma unroll
-          for (int w = 0; w < VW; ++w) {
-            lo[h][w] = low_halves(w1[w], w2[w]);
-            hi[h][w] = high_halves(w1[w], w2[w]);
-          }
-          u1[h] = lds_u8(at_vs1 + scales + h * 8 * (D / 16));
-          u2[h] = lds_u8(at_vs2 + scales + h * 8 * (D / 16));
-        }
-        float sc[NV][4];
-#pragma unroll
-        for (int v = 0; v < NV; ++v)
-#pragma unroll
-          for (int e = 0; e < 4; ++e) sc[v][e] = 0.f;
-        // 4 features a step
-        uint32_t wa[W], wc[W], sa[2], sb[2];  // codes of the two keys; a block's scale in both halves
-        lds_words<W>(wa, at_k + codes);
-        lds_words<W>(wc, at_k + codes + 8 * (D / 2));
-        if constexpr (DW == 64) {
-          sa[0] = e4m3x2_f16x2(lds_u8(at_ks + scales) * 0x0101u);
-          sb[0] = e4m3x2_f16x2(lds_u8(at_ks + scales + 8 * (D / 16)) * 0x0101u);
-        } else {
-          const uint32_t ua = e4m3x2_f16x2(lds_u16(at_ks + scales)), uc = e4m3x2_f16x2(lds_u16(at_ks + scales + 8 * (D / 16)));
-          sa[0] = __byte_perm(ua, ua, 0x1010);
-          sa[1] = __byte_perm(ua, ua, 0x3232);
-          sb[0] = __byte_perm(uc, uc, 0x1010);
-          sb[1] = __byte_perm(uc, uc, 0x3232);
-        }
-        unrolled<0, KS>([&](auto i) {
-          constexpr int I = decltype(i)::value, B = DW == 64 ? 0 : I / 4;
-          const uint32_t f[4] = {hmul2(codes_pair<2 * I>(wa), sa[B]), hmul2(codes_pair<2 * I>(wc), sb[B]),
-                                 hmul2(codes_pair<2 * I + 1>(wa), sa[B]), hmul2(codes_pair<2 * I + 1>(wc), sb[B])};
-#pragma unroll
-          for (int v = 0; v < NV; ++v) {
-            const uint2 q = q_at(v, I);
-            mma16816<__half>(sc[v], f, q.x, q.y);
-          }
-        });
-        if constexpr (FS == 2) {            // the other features' part, added in the same order by both
+        for (int y = 0; y < G; ++y) {
 #pragma unroll
           for (int v = 0; v < NV; ++v)
-            sts_words(x_mine + turn + v * 512, __float_as_uint(sc[v][0]), __float_as_uint(sc[v][1]), __float_as_uint(sc[v][2]),
-                      __float_as_uint(sc[v][3]));
+#pragma unroll
+            for (int e = 0; e < 4; ++e) sc[y][v][e] = 0.f;
+          // 4 features a step
+          uint32_t wa[W], wc[W], sa[2], sb[2];  // codes of the two keys; a block's scale in both halves
+          lds_words<W>(wa, at_k + codes + y * 16 * (D / 2));
+          lds_words<W>(wc, at_k + codes + (y * 16 + 8) * (D / 2));
+          const uint32_t at = at_ks + scales + y * 16 * (D / 16);
+          if constexpr (DW == 64) {
+            sa[0] = e4m3x2_f16x2(lds_u8(at) * 0x0101u);
+            sb[0] = e4m3x2_f16x2(lds_u8(at + 8 * (D / 16)) * 0x0101u);
+          } else {
+            const uint32_t ua = e4m3x2_f16x2(lds_u16(at)), uc = e4m3x2_f16x2(lds_u16(at + 8 * (D / 16)));
+            sa[0] = __byte_perm(ua, ua, 0x1010);
+            sa[1] = __byte_perm(ua, ua, 0x3232);
+            sb[0] = __byte_perm(uc, uc, 0x1010);
+            sb[1] = __byte_perm(uc, uc, 0x3232);
+          }
+          unrolled<0, KS>([&](auto i) {
+            constexpr int I = decltype(i)::value, B = DW == 64 ? 0 : I / 4;
+            const uint32_t f[4] = {hmul2(codes_pair<2 * I>(wa), sa[B]), hmul2(codes_pair<2 * I>(wc), sb[B]),
+                                   hmul2(codes_pair<2 * I + 1>(wa), sa[B]), hmul2(codes_pair<2 * I + 1>(wc), sb[B])};
+#pragma unroll
+            for (int v = 0; v < NV; ++v) {
+              const uint2 q = q_at(v, I);
+              mma16816<__half>(sc[y][v], f, q.x, q.y);
+            }
+          });
+        }
+        // V^T: keys 2 lt, 2 lt + 1 (+ 8) of the products' rows, features (hd / 8) lg ..;
+        // loaded and regrouped before the weights are known
+        uint32_t lo[G][2][VW], hi[G][2][VW], u1[G][2], u2[G][2];
+#pragma unroll
+        for (int y = 0; y < G; ++y)
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            uint32_t w1[VW], w2[VW];
+            lds_words<VW>(w1, at_v1 + codes + (y * 16 + h * 8) * (D / 2));
+            lds_words<VW>(w2, at_v2 + codes + (y * 16 + h * 8) * (D / 2));
+#pragma unroll
+            for (int w = 0; w < VW; ++w) {
+              lo[y][h][w] = low_halves(w1[w], w2[w]);
+              hi[y][h][w] = high_halves(w1[w], w2[w]);
+            }
+            u1[y][h] = lds_u8(at_vs1 + scales + (y * 16 + h * 8) * (D / 16));
+            u2[y][h] = lds_u8(at_vs2 + scales + (y * 16 + h * 8) * (D / 16));
+          }
+        if constexpr (FS == 2) {            // the other features' part, added in the same order by both
+#pragma unroll
+          for (int y = 0; y < G; ++y)
+#pragma unroll
+            for (int v = 0; v < NV; ++v)
+              sts_words(x_mine + turn + (y * NV + v) * 512, __float_as_uint(sc[y][v][0]), __float_as_uint(sc[y][v][1]),
+                        __float_as_uint(sc[y][v][2]), __float_as_uint(sc[y][v][3]));
           named_barrier(2 + vg * KG + warp % KG, 64);
 #pragma unroll
-          for (int v = 0; v < NV; ++v) {
-            uint32_t y[4];
-            lds_words<4>(y, x_other + turn + v * 512);
+          for (int y = 0; y < G; ++y)
 #pragma unroll
-            for (int e = 0; e < 4; ++e) sc[v][e] += __uint_as_float(y[e]);
-          }
-          turn ^= kWarps4 * NV * 512;
+            for (int v = 0; v < NV; ++v) {
+              uint32_t z[4];
+              lds_words<4>(z, x_other + turn + (y * NV + v) * 512);
+#pragma unroll
+              for (int e = 0; e < 4; ++e) sc[y][v][e] += __uint_as_float(z[e]);
+            }
+          turn ^= kWarps4 * G * NV * 512;
         }
         // masked scores: element e is (key row lg + 8 (e / 2), vector 2 lt + e % 2)
         if (mask) {
 #pragma unroll
-          for (int v = 0; v < NV; ++v)
+          for (int y = 0; y < G; ++y) {
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              const int key = k0 + ka + (e < 2 ? 0 : 8), top = lim[v][e & 1];
-              if (key >= top || (key < top - p.window && key >= p.sinks)) sc[v][e] = -INFINITY;
+            for (int v = 0; v < NV; ++v)
+#pragma unroll
+              for (int e = 0; e < 4; ++e) {
+                const int key = k0 + y * 16 + ka + (e < 2 ? 0 : 8), top = lim[v][e & 1];
+                if (key >= top || (key < top - p.window && key >= p.sinks)) sc[y][v][e] = -INFINITY;
+              }
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {   // what no row sees may be NaN: zeros
+              const int y1 = k0 + y * 16 + k1 + 8 * h, y2 = k0 + y * 16 + k2 + 8 * h;
+              if (y1 >= s.len || (y1 < lo_min && y1 >= p.sinks)) u1[y][h] = 0;
+              if (y2 >= s.len || (y2 < lo_min && y2 >= p.sinks)) u2[y][h] = 0;
             }
+          }
         }
+        auto top_of = [&](int v, int e) {
+          float mx = fmaxf(sc[0][v][e], sc[0][v][e + 2]);
+#pragma unroll
+          for (int y = 1; y < G; ++y) mx = fmaxf(mx, fmaxf(sc[y][v][e], sc[y][v][e + 2]));
+          return mx;
+        };
         bool raise = false;
 #pragma unroll
         for (int v = 0; v < NV; ++v)
 #pragma unroll
-          for (int e = 0; e < 2; ++e) raise |= fmaxf(sc[v][e], sc[v][e + 2]) > bar[v][e];
+          for (int e = 0; e < 2; ++e) raise |= top_of(v, e) > bar[v][e];
         if (__any_sync(0xffffffffu, raise)) {
 #pragma unroll
           for (int v = 0; v < NV; ++v)
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
-              float mx = fmaxf(sc[v][e], sc[v][e + 2]);
+              float mx = top_of(v, e);
 #pragma unroll
               for (int d = 4; d < 32; d <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, d));
               const float old = kLog24 - off[v][e], mn = fmaxf(seen[v] >> e & 1 ? old : -INFINITY, mx * qm[v][e]);
@@ -478,37 +506,32 @@ __global__ void __launch_bounds__(Split4Cfg<D, NV, VG, FS>::THREADS, Split4Cfg<D
               }
             }
         }
-        uint32_t pf[NV][2];
+        uint32_t pf[G][NV][2], vs[G][2];
 #pragma unroll
-        for (int v = 0; v < NV; ++v) {
-          float e[4];
+        for (int y = 0; y < G; ++y) {
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            e[i] = ex2(fmaf(sc[v][i], qm[v][i & 1], off[v][i & 1]));
-            l[v][i & 1] += e[i];
+          for (int v = 0; v < NV; ++v) {
+            float e[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              e[i] = ex2(fmaf(sc[y][v][i], qm[v][i & 1], off[v][i & 1]));
+              l[v][i & 1] += e[i];
+            }
+            pf[y][v][0] = movmatrix(pack2(e[0], e[1], (const __half*)nullptr));
+            pf[y][v][1] = movmatrix(pack2(e[2], e[3], (const __half*)nullptr));
           }
-          pf[v][0] = movmatrix(pack2(e[0], e[1], (const __half*)nullptr));
-          pf[v][1] = movmatrix(pack2(e[2], e[3], (const __half*)nullptr));
-        }
-        if (mask) {                         // what no row sees may be NaN: zeros
 #pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            const int y1 = k0 + k1 + 8 * h, y2 = k0 + k2 + 8 * h;
-            if (y1 >= s.len || (y1 < lo_min && y1 >= p.sinks)) u1[h] = 0;
-            if (y2 >= s.len || (y2 < lo_min && y2 >= p.sinks)) u2[h] = 0;
-          }
+          for (int h = 0; h < 2; ++h) vs[y][h] = e4m3x2_f16x2(__byte_perm(u1[y][h], u2[y][h], 0x0040));
         }
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          vs[h] = e4m3x2_f16x2(__byte_perm(u1[h], u2[h], 0x0040));
-        }
-        unrolled<0, KS>([&](auto j) {
-          constexpr int J = decltype(j)::value;
-          const uint32_t f[4] = {hmul2(codes_pair<J>(lo[0]), vs[0]), hmul2(codes_pair<J>(hi[0]), vs[0]),
-                                 hmul2(codes_pair<J>(lo[1]), vs[1]), hmul2(codes_pair<J>(hi[1]), vs[1])};
+        for (int y = 0; y < G; ++y)
+          unrolled<0, KS>([&](auto j) {
+            constexpr int J = decltype(j)::value;
+            const uint32_t f[4] = {hmul2(codes_pair<J>(lo[y][0]), vs[y][0]), hmul2(codes_pair<J>(hi[y][0]), vs[y][0]),
+                                   hmul2(codes_pair<J>(lo[y][1]), vs[y][1]), hmul2(codes_pair<J>(hi[y][1]), vs[y][1])};
 #pragma unroll
-          for (int v = 0; v < NV; ++v) mma16816<__half>(o[v][J], f, pf[v][0], pf[v][1]);
-        });
+            for (int v = 0; v < NV; ++v) mma16816<__half>(o[v][J], f, pf[y][v][0], pf[y][v][1]);
+          });
       }
       __syncwarp();
       if (lane == 0) mbar_arrive(&b_empty[st]);
