@@ -22,7 +22,6 @@
 // Items that are cut leave a record (m, l, sum p v) per CTA, joined by paged_merge_kernel.
 #include <cmath>
 
-#include "swa_mma16.cuh"
 #include "swa_paged4_attend.cuh"
 #include "swa_paged_merge.cuh"
 
@@ -48,8 +47,9 @@ struct Split4Cfg {
   // Groups of 16 keys that a warp takes at a time: two where a tile has them, and the exchange of scores room
   // (64 x 1024 .. 8192 keys, 4 vectors of 128 features 89 us with one, 85 with two)
   static constexpr int G = (FS == 1 || NV == 1) && KT / 16 / (kWarps4 / (VG * FS)) >= 2 ? 2 : 1;
-  static constexpr int JT = 4 / NV;                         // 16-feature tiles of O that the warps join at a time
-  static constexpr int JOIN = kWarps4 * JT * NV * 512;      // bytes: 8 KB
+  // The warps of a group join their O in shared memory, in two rounds where one would take the stages' room
+  static constexpr int JR = NV * D > 128 ? 2 : 1, JT = DW / 16 / JR, JROW = 16 * JT + 4;   // a vector's floats, and 4 apart
+  static constexpr int JOIN = kWarps4 * 8 * NV * JROW * 4;
   static constexpr int QB = QS ? ROWS * D * 2 : 0;
   static constexpr int XB = FS > 1 ? 2 * kWarps4 * G * NV * 512 : 0;   // parts of scores, two rounds
   static constexpr int FIT = (226 * 1024 / CTAS - 1024 - JOIN - QB - XB - 128 - 1024) / STAGE;
@@ -61,6 +61,18 @@ __device__ __forceinline__ uint32_t movmatrix(uint32_t a) {
   uint32_t d;
   asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(d) : "r"(a));
   return d;
+}
+// c += a b (ZERO: c = a b)
+template <bool ZERO>
+__device__ __forceinline__ void mma_f16(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+  if constexpr (ZERO)
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%10,%10,%10};"
+        : "=f"(c[0]), "=f"(c[1]), "=f"(c[2]), "=f"(c[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "f"(0.f));
+  else
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 // Each byte's lower half from a, its upper half from b's lower half; and the upper halves alike
 __device__ __forceinline__ uint32_t low_halves(uint32_t a, uint32_t b) { return (a & 0x0f0f0f0fu) | ((b << 4) & 0xf0f0f0f0u); }
@@ -117,10 +129,11 @@ __device__ __forceinline__ float load_query4(const Attend4Params& p, long long a
   return inv;
 }
 
-__device__ __forceinline__ void store_pair4(const Attend4Params& p, long long at, float x, float y) {
-  if (p.a.out_f32) *reinterpret_cast<float2*>(static_cast<float*>(p.a.out) + at) = make_float2(x, y);
-  else *reinterpret_cast<uint32_t*>(static_cast<uint16_t*>(p.a.out) + at) =
-      p.bf ? pack2(x, y, (const __nv_bfloat16*)nullptr) : pack2(x, y, (const __half*)nullptr);
+__device__ __forceinline__ void store_four4(const Attend4Params& p, long long at, float x, float y, float z, float w) {
+  if (p.a.out_f32) *reinterpret_cast<float4*>(static_cast<float*>(p.a.out) + at) = make_float4(x, y, z, w);
+  else *reinterpret_cast<uint2*>(static_cast<uint16_t*>(p.a.out) + at) =
+      p.bf ? make_uint2(pack2(x, y, (const __nv_bfloat16*)nullptr), pack2(z, w, (const __nv_bfloat16*)nullptr))
+           : make_uint2(pack2(x, y, (const __half*)nullptr), pack2(z, w, (const __half*)nullptr));
 }
 
 // Tiles of one (sequence, KV head): none where the sequence has no rows or more query
@@ -142,7 +155,7 @@ __global__ void __launch_bounds__(Split4Cfg<D, NV, VG, FS>::THREADS, Split4Cfg<D
   __shared__ long long s_off, s_total;
   __shared__ int s_b, s_abort;
   __shared__ float2 s_ml[kWarps4][8 * NV];
-  __shared__ float s_shift[C::ROWS];
+  __shared__ float s_shift[C::ROWS], s_inv[C::ROWS];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   unsigned char* const sm = reinterpret_cast<unsigned char*>((reinterpret_cast<uintptr_t>(sm_raw) + 127) & ~(uintptr_t)127);
   const uint32_t smb = smem_u32(sm);
@@ -291,7 +304,8 @@ __global__ void __launch_bounds__(Split4Cfg<D, NV, VG, FS>::THREADS, Split4Cfg<D
   }
 
   // ------------------------------------------------------------ products
-  const int lg = lane >> 2, lt = lane & 3, hpg = a.hpg, fs = warp / KG % FS, vg = warp / (KG * FS);
+  const int lg = lane >> 2, lt = lane & 3, hpg = a.hpg, hpg_inv = 65536 / hpg + 1, fs = warp / KG % FS, vg = warp / (KG * FS);
+  auto row_of = [&](int x) { return x * hpg_inv >> 16; };   // x / hpg (x < 32: a vector)
   // the key of the group's 16 that is row i of the products: lanes that read at the same time
   // then find rows of both parities, and fewer of them in the same banks
   auto key_of = [](int i) { return i ^ ((i >> 1) & 1); };
@@ -312,7 +326,7 @@ __global__ void __launch_bounds__(Split4Cfg<D, NV, VG, FS>::THREADS, Split4Cfg<D
     auto query = [&](int tile, int part, uint32_t (&q)[KS][2]) {      // of 8 vectors; the inverse scale of vector lg
       const int r = tile * 8 + lg;
       const bool in = r < nvec;
-      const int i = in ? r / hpg : 0, h = in ? r % hpg : 0;
+      const int i = in ? row_of(r) : 0, h = in ? r - i * hpg : 0;
       return load_query4<D, FS>(p, (long long)(s.r0 + i) * a.q_row + (long long)(g * hpg + h) * D, in, lt, part, q);
     };
     if constexpr (QS) {
@@ -334,7 +348,7 @@ __global__ void __launch_bounds__(Split4Cfg<D, NV, VG, FS>::THREADS, Split4Cfg<D
         const int c = (vg * NV + v) * 8 + 2 * lt + e;
         if constexpr (QS) shift = s_shift[c];
         qm[v][e] = fmaxf(a.qmul * (QS ? shift : __shfl_sync(0xffffffffu, shift, (2 * lt + e) * 4)), 0x1p-126f);   // masked scores stay -inf
-        lim[v][e] = c < nvec ? max(0, min(s.len, s.len - s.t + c / hpg + 1)) : 0;
+        lim[v][e] = c < nvec ? max(0, min(s.len, s.len - s.t + row_of(c) + 1)) : 0;
       }
     }
     auto q_at = [&](int v, int i) {
@@ -384,57 +398,60 @@ __global__ void __launch_bounds__(Split4Cfg<D, NV, VG, FS>::THREADS, Split4Cfg<D
         if (k0 >= s.len || (k0 + 16 * G <= lo_min && k0 >= p.sinks)) continue;
         const uint32_t codes = st * C::STAGE + sub * 16 * (D / 2), scales = st * C::STAGE + sub * 16 * (D / 16);
         const bool mask = __any_sync(0xffffffffu, k0 + 16 * G > lim_min || k0 < lo_max);   // a branch, not selects
+        // V^T: keys 2 lt, 2 lt + 1 (+ 8) of the products' rows, features (hd / 8) lg ..; loaded and regrouped before
+        // the weights are known, and before S where the registers allow
+        uint32_t lo[G][2][VW], hi[G][2][VW], u1[G][2], u2[G][2];
+        auto load_v = [&]() {
+#pragma unroll
+          for (int y = 0; y < G; ++y)
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+              uint32_t w1[VW], w2[VW];
+              lds_words<VW>(w1, at_v1 + codes + (y * 16 + h * 8) * (D / 2));
+              lds_words<VW>(w2, at_v2 + codes + (y * 16 + h * 8) * (D / 2));
+#pragma unroll
+              for (int w = 0; w < VW; ++w) {
+                lo[y][h][w] = low_halves(w1[w], w2[w]);
+                hi[y][h][w] = high_halves(w1[w], w2[w]);
+              }
+              u1[y][h] = lds_u8(at_vs1 + scales + (y * 16 + h * 8) * (D / 16));
+              u2[y][h] = lds_u8(at_vs2 + scales + (y * 16 + h * 8) * (D / 16));
+            }
+        };
+        if constexpr (G == 1) load_v();
         float sc[G][NV][4];
+        // 4 features a step; the groups in turn, since a step's products wait for the step's before
+        uint32_t wa[G][W], wc[G][W], sa[G][2], sb[G][2];   // codes of the two keys; a block's scale in both halves
 #pragma unroll
         for (int y = 0; y < G; ++y) {
-#pragma unroll
-          for (int v = 0; v < NV; ++v)
-#pragma unroll
-            for (int e = 0; e < 4; ++e) sc[y][v][e] = 0.f;
-          // 4 features a step
-          uint32_t wa[W], wc[W], sa[2], sb[2];  // codes of the two keys; a block's scale in both halves
-          lds_words<W>(wa, at_k + codes + y * 16 * (D / 2));
-          lds_words<W>(wc, at_k + codes + (y * 16 + 8) * (D / 2));
+          lds_words<W>(wa[y], at_k + codes + y * 16 * (D / 2));
+          lds_words<W>(wc[y], at_k + codes + (y * 16 + 8) * (D / 2));
           const uint32_t at = at_ks + scales + y * 16 * (D / 16);
           if constexpr (DW == 64) {
-            sa[0] = e4m3x2_f16x2(lds_u8(at) * 0x0101u);
-            sb[0] = e4m3x2_f16x2(lds_u8(at + 8 * (D / 16)) * 0x0101u);
+            sa[y][0] = e4m3x2_f16x2(lds_u8(at) * 0x0101u);
+            sb[y][0] = e4m3x2_f16x2(lds_u8(at + 8 * (D / 16)) * 0x0101u);
           } else {
             const uint32_t ua = e4m3x2_f16x2(lds_u16(at)), uc = e4m3x2_f16x2(lds_u16(at + 8 * (D / 16)));
-            sa[0] = __byte_perm(ua, ua, 0x1010);
-            sa[1] = __byte_perm(ua, ua, 0x3232);
-            sb[0] = __byte_perm(uc, uc, 0x1010);
-            sb[1] = __byte_perm(uc, uc, 0x3232);
+            sa[y][0] = __byte_perm(ua, ua, 0x1010);
+            sa[y][1] = __byte_perm(ua, ua, 0x3232);
+            sb[y][0] = __byte_perm(uc, uc, 0x1010);
+            sb[y][1] = __byte_perm(uc, uc, 0x3232);
           }
-          unrolled<0, KS>([&](auto i) {
-            constexpr int I = decltype(i)::value, B = DW == 64 ? 0 : I / 4;
-            const uint32_t f[4] = {hmul2(codes_pair<2 * I>(wa), sa[B]), hmul2(codes_pair<2 * I>(wc), sb[B]),
-                                   hmul2(codes_pair<2 * I + 1>(wa), sa[B]), hmul2(codes_pair<2 * I + 1>(wc), sb[B])};
+        }
+        unrolled<0, KS>([&](auto i) {
+          constexpr int I = decltype(i)::value, B = DW == 64 ? 0 : I / 4;
+#pragma unroll
+          for (int y = 0; y < G; ++y) {
+            const uint32_t f[4] = {hmul2(codes_pair<2 * I>(wa[y]), sa[y][B]), hmul2(codes_pair<2 * I>(wc[y]), sb[y][B]),
+                                   hmul2(codes_pair<2 * I + 1>(wa[y]), sa[y][B]), hmul2(codes_pair<2 * I + 1>(wc[y]), sb[y][B])};
 #pragma unroll
             for (int v = 0; v < NV; ++v) {
               const uint2 q = q_at(v, I);
-              mma16816<__half>(sc[y][v], f, q.x, q.y);
+              mma_f16<I == 0>(sc[y][v], f, q.x, q.y);
             }
-          });
-        }
-        // V^T: keys 2 lt, 2 lt + 1 (+ 8) of the products' rows, features (hd / 8) lg ..;
-        // loaded and regrouped before the weights are known
-        uint32_t lo[G][2][VW], hi[G][2][VW], u1[G][2], u2[G][2];
-#pragma unroll
-        for (int y = 0; y < G; ++y)
-#pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            uint32_t w1[VW], w2[VW];
-            lds_words<VW>(w1, at_v1 + codes + (y * 16 + h * 8) * (D / 2));
-            lds_words<VW>(w2, at_v2 + codes + (y * 16 + h * 8) * (D / 2));
-#pragma unroll
-            for (int w = 0; w < VW; ++w) {
-              lo[y][h][w] = low_halves(w1[w], w2[w]);
-              hi[y][h][w] = high_halves(w1[w], w2[w]);
-            }
-            u1[y][h] = lds_u8(at_vs1 + scales + (y * 16 + h * 8) * (D / 16));
-            u2[y][h] = lds_u8(at_vs2 + scales + (y * 16 + h * 8) * (D / 16));
           }
+        });
+        if constexpr (G > 1) load_v();
         if constexpr (FS == 2) {            // the other features' part, added in the same order by both
 #pragma unroll
           for (int y = 0; y < G; ++y)
@@ -530,7 +547,7 @@ __global__ void __launch_bounds__(Split4Cfg<D, NV, VG, FS>::THREADS, Split4Cfg<D
             const uint32_t f[4] = {hmul2(codes_pair<J>(lo[y][0]), vs[y][0]), hmul2(codes_pair<J>(hi[y][0]), vs[y][0]),
                                    hmul2(codes_pair<J>(lo[y][1]), vs[y][1]), hmul2(codes_pair<J>(hi[y][1]), vs[y][1])};
 #pragma unroll
-            for (int v = 0; v < NV; ++v) mma16816<__half>(o[v][J], f, pf[y][v][0], pf[y][v][1]);
+            for (int v = 0; v < NV; ++v) mma_f16<false>(o[v][J], f, pf[y][v][0], pf[y][v][1]);
           });
       }
       __syncwarp();
@@ -541,7 +558,7 @@ __global__ void __launch_bounds__(Split4Cfg<D, NV, VG, FS>::THREADS, Split4Cfg<D
       }
     }
 
-    // --- join the warps, JT tiles of O at a time
+    // --- join the warps of a group: each scales its part to their maximum, then they are added up
 #pragma unroll
     for (int v = 0; v < NV; ++v)
 #pragma unroll
@@ -553,47 +570,69 @@ __global__ void __launch_bounds__(Split4Cfg<D, NV, VG, FS>::THREADS, Split4Cfg<D
     const bool whole = tile0 == 0 && tile1 == tl.n;
     // record of the item this CTA continues: slot 2c, of the one it starts: 2c + 1
     const size_t rec = ((size_t)blockIdx.x * 2 + (tile0 == 0 ? 1 : 0)) * p.rows;
+    named_barrier(1, kWarps4 * 32);
+#pragma unroll
+    for (int v = 0; v < NV; ++v)
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        const int c = v * 8 + 2 * lt + e, pv = vg * (8 * NV) + c;
+        float mt = -INFINITY, sum = 0.f, mine = 0.f;
+#pragma unroll
+        for (int w = 0; w < KG; ++w) mt = fmaxf(mt, s_ml[warp - warp % KG + w][c].x);
+#pragma unroll
+        for (int w = 0; w < KG; ++w) {
+          const float2 ml = s_ml[warp - warp % KG + w][c];
+          const float f = ml.x == -INFINITY ? 0.f : ex2(ml.x - mt + (p.rec_log2 - kLog24));
+          sum += f * ml.y;
+          if (w == warp % KG) mine = f * p.c.v_mul;
+        }
+#pragma unroll
+        for (int j = 0; j < KS; ++j) {
+          o[v][j][e] *= mine;
+          o[v][j][e + 2] *= mine;
+        }
+        if (lg > 0 || warp % (KG * FS)) continue;           // a lane for each vector
+        s_inv[pv] = sum > 0.f ? 1.f / sum : (sum == 0.f ? 0.f : sum);   // no key: zeros; NaN stays
+        if (pv >= nvec || s_abort) continue;
+        if (!whole) a.ws_ml[rec + pv] = make_float2(mt, sum);
+        else if (a.lse)
+          a.lse[(size_t)(s.r0 + row_of(pv)) * a.nh + g * hpg + pv - row_of(pv) * hpg] = sum == 0.f ? -INFINITY : (mt - p.rec_log2 + log2f(sum)) * 0.6931471805599453f;
+      }
 #pragma unroll
     for (int j0 = 0; j0 < KS; j0 += C::JT) {
-      if (j0 > 0) named_barrier(1, kWarps4 * 32);           // the tiles before are read
+      if (j0 > 0) named_barrier(1, kWarps4 * 32);           // the part before is read
 #pragma unroll
       for (int v = 0; v < NV; ++v)
 #pragma unroll
-        for (int j = 0; j < C::JT; ++j)
+        for (int e = 0; e < 2; ++e)
 #pragma unroll
-          for (int h = 0; h < 2; ++h)
-            *reinterpret_cast<float2*>(join + ((((warp * NV + v) * C::JT + j) * 2 + h) * 8 + lg) * 8 + 2 * lt) =
-                make_float2(o[v][j0 + j][2 * h], o[v][j0 + j][2 * h + 1]);
+          for (int j = 0; j < C::JT; j += 2)
+            *reinterpret_cast<float4*>(join + (warp * (8 * NV) + v * 8 + 2 * lt + e) * C::JROW + lg * (2 * C::JT) + 2 * j) =
+                make_float4(o[v][j0 + j][e], o[v][j0 + j][e + 2], o[v][j0 + j + 1][e], o[v][j0 + j + 1][e + 2]);
       named_barrier(1, kWarps4 * 32);
       if (s_abort) continue;
-      // a vector c of tile v of group w0 / KG, features 2 j and 2 j + 1 of lane group pg at a time
-      for (int y = tid; y < C::ROWS * FS * C::JT * 8; y += kWarps4 * 32) {
-        const int c = y & 7, pg = (y >> 3) & 7, j = (y >> 6) % C::JT, v = (y >> 6) / C::JT % NV, w0 = (y >> 6) / (C::JT * NV) * KG;
-        const int pv = (w0 / (KG * FS) * NV + v) * 8 + c;
+      // four features of a vector at a time: in group y / .. , vector c of its own
+      constexpr int QUADS = 4 * C::JT;
+      for (int y = tid; y < C::ROWS * FS * QUADS; y += kWarps4 * 32) {
+        const int quad = y % QUADS, c = y / QUADS % (8 * NV), gr = y / (QUADS * 8 * NV), pv = gr / FS * (8 * NV) + c;
         if (pv >= nvec) continue;
-        float mt = -INFINITY, lt_ = 0.f, acc[2] = {0.f, 0.f};
-#pragma unroll
-        for (int w = 0; w < KG; ++w) mt = fmaxf(mt, s_ml[w0 + w][v * 8 + c].x);
+        float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
         for (int w = 0; w < KG; ++w) {
-          const float2 ml = s_ml[w0 + w][v * 8 + c];
-          const float f = ml.x == -INFINITY ? 0.f : ex2(ml.x - mt + (p.rec_log2 - kLog24));
-          lt_ += f * ml.y;
-#pragma unroll
-          for (int h = 0; h < 2; ++h) acc[h] += f * join[(((((w0 + w) * NV + v) * C::JT + j) * 2 + h) * 8 + pg) * 8 + c];
+          const float4 x = *reinterpret_cast<const float4*>(join + ((gr * KG + w) * (8 * NV) + c) * C::JROW + quad * 4);
+          acc.x += x.x;
+          acc.y += x.y;
+          acc.z += x.z;
+          acc.w += x.w;
         }
-        const int f = w0 / KG % FS * DW + pg * (DW / 8) + 2 * (j0 + j);
-        acc[0] *= p.c.v_mul;
-        acc[1] *= p.c.v_mul;
+        const int f = gr % FS * DW + quad / (C::JT / 2) * (DW / 8) + 2 * j0 + quad % (C::JT / 2) * 4;
         if (whole) {
-          const float inv = lt_ > 0.f ? 1.f / lt_ : (lt_ == 0.f ? 0.f : lt_);   // no key: zeros; NaN stays
-          const int row = s.r0 + pv / hpg, head = g * hpg + pv % hpg;
-          store_pair4(p, ((long long)row * a.nh + head) * D + f, lt_ == 0.f ? 0.f : acc[0] * inv, lt_ == 0.f ? 0.f : acc[1] * inv);
-          if (f == 0 && a.lse)
-            a.lse[(size_t)row * a.nh + head] = lt_ == 0.f ? -INFINITY : (mt - p.rec_log2 + log2f(lt_)) * 0.6931471805599453f;
+          const float inv = s_inv[pv];
+          const bool none = inv == 0.f;
+          store_four4(p, ((long long)(s.r0 + row_of(pv)) * a.nh + g * hpg + pv - row_of(pv) * hpg) * D + f, none ? 0.f : acc.x * inv, none ? 0.f : acc.y * inv,
+                      none ? 0.f : acc.z * inv, none ? 0.f : acc.w * inv);
         } else {
-          *reinterpret_cast<float2*>(a.ws_acc + (rec + pv) * D + f) = make_float2(acc[0], acc[1]);
-          if (f == 0) a.ws_ml[rec + pv] = make_float2(mt, lt_);
+          *reinterpret_cast<float4*>(a.ws_acc + (rec + pv) * D + f) = acc;
         }
       }
     }
