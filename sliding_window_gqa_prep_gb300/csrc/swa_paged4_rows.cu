@@ -42,8 +42,12 @@ struct Rows4Params {
 };
 
 constexpr int kRThreads = 256, kRWarps = kRThreads / 32;
-constexpr int kRRows = 4;          // most rows of a block (append)
-constexpr int kRPairs = 128;       // most pairs of a head
+constexpr int kE = 8;              // features of a lane (append): half a block
+template <int HD>
+struct AppendCfg {
+  static constexpr int LANES = HD / kE, ROWS_WARP = 32 / LANES;   // of a head; rows that a warp takes at once
+  static constexpr int ROWS = HD == 64 ? 8 : 4;                   // most rows of a block
+};
 // sincospif is good to an ulp (2^-24), the step by what the angle's f32 leaves to 2^-25, mag to 2^-25, the two
 // products' roundings 2^-25 each: 1.8e-7 of |u| + |v|, times mag.
 constexpr float kTol = 0x1p-22f;
@@ -105,24 +109,24 @@ __device__ __forceinline__ uint32_t codes_of(const float (&z)[E]) {
   return plain_zeros(c);
 }
 
-// The encoding of the blocks that f32 left open, from angles in f64, by the warp of their head. x, b: a lane's
-// features and their partners with the sign that they enter by; e: the feature's pair, -1 where it does not
-// turn. A lane takes one feature of a block: a chain of f64 operations takes long.
-template <int E>
-__device__ __noinline__ void encode_exact(const float (&x)[E], const float (&b)[E], const int (&e)[E], unsigned open, int pos,
+// The encoding of the blocks that f32 left open, from angles in f64, by a warp. x, b: a lane's features and their
+// partners with the sign that they enter by; e: the feature's pair, -1 where it does not turn; pos: its row's.
+// A lane takes one feature of a block: a chain of f64 operations takes long.
+__device__ __noinline__ void encode_exact(const float (&x)[kE], const float (&b)[kE], const int (&e)[kE], unsigned open, int pos,
                                           const uint64_t* turns, float mag, float div, uint32_t& codes, uint32_t& scale) {
-  constexpr int L = kBlock4 / E;
+  constexpr int L = kBlock4 / kE;
   const int lane = threadIdx.x & 31;
   while (open) {
-    const int block = (__ffs(open) - 1) / L, i = lane & 15, owner = block * L + i / E;
+    const int block = (__ffs(open) - 1) / L, i = lane & 15, owner = block * L + i / kE;
     open &= ~(((1u << L) - 1) << (block * L));
     float xi = 0.f, bi = 0.f;
     int ei = -1;
+    const int at = __shfl_sync(0xffffffffu, pos, owner);
 #pragma unroll
-    for (int j = 0; j < E; ++j) {
+    for (int j = 0; j < kE; ++j) {
       const float xj = __shfl_sync(0xffffffffu, x[j], owner), bj = __shfl_sync(0xffffffffu, b[j], owner);
       const int ej = __shfl_sync(0xffffffffu, e[j], owner);
-      if (i % E == j) {
+      if (i % kE == j) {
         xi = xj;
         bi = bj;
         ei = ej;
@@ -131,7 +135,7 @@ __device__ __noinline__ void encode_exact(const float (&x)[E], const float (&b)[
     double y = xi;
     if (ei >= 0) {
       double sn, cs;
-      sincospi((double)(int64_t)((uint64_t)(int64_t)pos * turns[ei]) * 0x1p-63, &sn, &cs);
+      sincospi((double)(int64_t)((uint64_t)(int64_t)at * turns[ei]) * 0x1p-63, &sn, &cs);
       y = ((double)xi * cs + (double)bi * sn) * mag;
     }
     y *= div;
@@ -147,7 +151,7 @@ __device__ __noinline__ void encode_exact(const float (&x)[E], const float (&b)[
     if (c && y < 0) c |= 8u;
     uint32_t mine = 0;
 #pragma unroll
-    for (int j = 0; j < E; ++j) mine |= __shfl_sync(0xffffffffu, c, (lane % L) * E + j) << (4 * j);
+    for (int j = 0; j < kE; ++j) mine |= __shfl_sync(0xffffffffu, c, (lane % L) * kE + j) << (4 * j);
     if (lane / L == block) {
       codes = mine;
       scale = f32_e4m3((float)s);
@@ -156,20 +160,21 @@ __device__ __noinline__ void encode_exact(const float (&x)[E], const float (&b)[
 }
 
 // PAIRS: how the features of a pair lie. 0: half of the turned ones apart, and a lane's partners are those
-// of one other lane; 1: next to each other; 2: as 0 with partners in two lanes (half % E != 0).
-template <typename TI, int E, int PAIRS>
-__global__ void __launch_bounds__(kRThreads, E == 8 ? 2 : 3) paged4_append_kernel(const __grid_constant__ Rows4Params p) {
-  constexpr int HD = 32 * E, L = kBlock4 / E;            // lanes of a block
-  __shared__ __align__(16) float s_cos[kRRows * kRPairs], s_sin[kRRows * kRPairs];
-  __shared__ long long s_at[kRRows];       // -2: of no sequence, -1: not stored
+// of one other lane; 1: next to each other; 2: as 0 with partners in two lanes (half % kE != 0).
+template <typename TI, int HD, int PAIRS>
+__global__ void __launch_bounds__(kRThreads, 3) paged4_append_kernel(const __grid_constant__ Rows4Params p) {
+  using C = AppendCfg<HD>;
+  constexpr int LH = C::LANES, RP = C::ROWS_WARP, TIMES = C::ROWS / RP, L = kBlock4 / kE;   // L: lanes of a block
+  __shared__ __align__(16) float s_cos[C::ROWS * (HD / 2)], s_sin[2][C::ROWS * (HD / 2)];   // [0]: -sin, of a pair's first feature
+  __shared__ long long s_at[C::ROWS];      // -2: of no sequence, -1: not stored
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int row0 = blockIdx.x * p.R, nr = min(p.R, p.T - row0), h0 = blockIdx.y * p.Hg, n = min(p.Hg, p.H - h0);
-  const int half = p.rot >> 1, f0 = lane * E, nq = p.nh, nqk = p.nh + p.map.nk;
-  // A warp takes the heads warp, warp + 8, .. of the block, of each all rows at once; the next head's are loaded
-  // while these are worked on (where they are no more than 16 registers).
-  constexpr bool AHEAD = sizeof(TI) * E <= 16;
+  const int half = p.rot >> 1, sub = lane % LH, f0 = sub * kE, row_w = lane / LH, nq = p.nh, nqk = p.nh + p.map.nk;
+  // A warp takes the heads warp, warp + 8, .. of the block, of each all rows; the next head's are loaded while these
+  // are worked on (where they are no more than 16 registers).
+  constexpr bool AHEAD = sizeof(TI) * kE * TIMES <= 64;
   struct Rows {
-    Pack<TI, E> a[kRRows];
+    Pack<TI, kE> a[TIMES];
   };
   auto load = [&](Rows& t, int x) {
     const int h = h0 + x;
@@ -185,29 +190,37 @@ __global__ void __launch_bounds__(kRThreads, E == 8 ? 2 : 3) paged4_append_kerne
       src = static_cast<const TI*>(p.v) + (long long)(h - nqk) * HD;
       row = p.v_row;
     }
-    src += row0 * row + f0;
+    src += (row0 + row_w) * row + f0;
 #pragma unroll
-    for (int r = 0; r < kRRows; ++r, src += row)
-      if (r < nr) t.a[r] = load_pack<E>(src);
+    for (int i = 0; i < TIMES; ++i, src += RP * row) {
+      t.a[i] = Pack<TI, kE>{};
+      if (i * RP + row_w < nr) t.a[i] = load_pack<kE>(src);
+    }
   };
   // The largest of a block's values (as bits: NaN and infinities above all), in units of 2^exp; its scale and
   // the reciprocal
   struct Scale {
     float top, u, inv;
     uint32_t bits;
-    bool bad, clip;
+    bool bad;
   };
-  auto scale_of = [&](const float (&y)[E], float div) {
+  // y in units of 2^exp afterwards
+  auto scale_of = [&](float (&y)[kE], float div) {
     uint32_t m = 0;
 #pragma unroll
-    for (int j = 0; j < E; ++j) m = max(m, __float_as_uint(y[j]) & 0x7fffffffu);
+    for (int j = 0; j < kE; ++j) m = max(m, __float_as_uint(y[j]) & 0x7fffffffu);
 #pragma unroll
     for (int o = 1; o < L; o <<= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, o));
     Scale s;
     s.bad = m >= 0x7f800000u;
     s.top = __uint_as_float(m) * div;
-    s.clip = s.top > 4096.f;                             // 448 * 6 and more take the largest scale
-    s.top = fminf(s.top, 4096.f);
+#pragma unroll
+    for (int j = 0; j < kE; ++j) y[j] *= div;
+    if (__any_sync(0xffffffffu, s.top > 4096.f)) {       // 448 * 6 and more take the largest scale
+      s.top = fminf(s.top, 4096.f);
+#pragma unroll
+      for (int j = 0; j < kE; ++j) y[j] = fminf(fmaxf(y[j], -4096.f), 4096.f);
+    }
     float q = s.top * (1.f / 6.f);
     q = fmaf(fmaf(-6.f, q, s.top), 1.f / 6.f, q);
     s.bits = f32_e4m3(q);
@@ -218,42 +231,48 @@ __global__ void __launch_bounds__(kRThreads, E == 8 ? 2 : 3) paged4_append_kerne
     s.inv = s.u > 0.f ? fmaf(fmaf(-s.u, inv, 1.f), inv, inv) : 0.f;
     return s;
   };
-  auto quotients = [&](const float (&y)[E], float div, const Scale& s, float (&z)[E]) {
+  auto quotients = [&](float (&y)[kE], const Scale& s) {
 #pragma unroll
-    for (int j = 0; j < E; ++j) {
-      const float x = s.clip ? fminf(fmaxf(y[j] * div, -4096.f), 4096.f) : y[j] * div, q = x * s.inv;
-      z[j] = fmaf(fmaf(-q, s.u, x), s.inv, q);
+    for (int j = 0; j < kE; ++j) {
+      const float q = y[j] * s.inv;
+      y[j] = fmaf(fmaf(-q, s.u, y[j]), s.inv, q);
     }
   };
-  auto store = [&](bool is_k, long long at, int g, uint32_t codes, uint32_t scale) {
+  auto store = [&](uint8_t* to_codes, uint8_t* to_scales, long long at, int g, uint32_t codes, uint32_t scale) {
+    if (at < 0) return;
     const long long key = at + ((long long)g << p.map.page_shift);
-    uint8_t* const to = (is_k ? p.c.k : p.c.v) + key * (HD / 2) + lane * (E / 2);
-    if constexpr (E == 2) *to = (uint8_t)codes;
-    else if constexpr (E == 4) *reinterpret_cast<uint16_t*>(to) = (uint16_t)codes;
-    else *reinterpret_cast<uint32_t*>(to) = codes;
-    if (lane % L == 0) (is_k ? p.c.ks : p.c.vs)[key * (HD / kBlock4) + lane / L] = (uint8_t)scale;
+    *reinterpret_cast<uint32_t*>(to_codes + key * (HD / 2) + sub * (kE / 2)) = codes;
+    if (sub % L == 0) to_scales[key * (HD / kBlock4) + sub / L] = (uint8_t)scale;
   };
-  auto work_v = [&](long long at, int g, const Pack<TI, E>& raw) {
-    float x[E], z[E];
+  auto row_of = [&](int i) { return min(i * RP + row_w, nr - 1); };   // a lane without a row takes the last one's place
+  auto at_of = [&](int i) { return i * RP + row_w < nr ? s_at[i * RP + row_w] : -2; };
+  auto work_v = [&](int i, int g, const Pack<TI, kE>& raw) {
+    const long long at = at_of(i);
+    float x[kE];
     unpack(raw, x);
     const Scale s = scale_of(x, p.v_div);
-    quotients(x, p.v_div, s, z);
-    store(false, at, g, s.bad ? 0u : codes_of(z), s.bad ? 0x7fu : s.bits);
+    quotients(x, s);
+    store(p.c.v, p.c.vs, at, g, s.bad ? 0u : codes_of(x), s.bad ? 0x7fu : s.bits);
   };
-  // the rotation: y = x cos + b sin, b the partner with its sign, e the pair (-1: none); f0 < half and the partner's
-  // lane are the same for all rows
-  const bool low = f0 < half, exact_mag = p.mag == 1.f;
-  const int partner = (low ? lane + half / E : lane - half / E) & 31, pair0 = low ? f0 : f0 - half;
-  auto rotate = [&](int r, const Pack<TI, E>& raw, const TI* src, float (&x)[E], float (&b)[E], float (&y)[E], int (&e)[E]) {
+  // the rotation: y = x cos + b sin, b the partner with its sign; f0 < half and the partner's lane are the same
+  // for all rows
+  const bool low = f0 < half;
+  const int partner = (low ? lane + half / kE : lane - half / kE) & 31, pair0 = low ? f0 : f0 - half;
+  auto pair_of = [&](int j) {              // of feature f0 + j, -1: it does not turn
+    const int f = f0 + j;
+    if (f >= p.rot) return -1;
+    return PAIRS == 1 ? f >> 1 : f < half ? f : f - half;
+  };
+  auto first_of = [&](int j) { return PAIRS == 1 ? !(j & 1) : PAIRS == 0 ? low : f0 + j < half; };   // of its pair
+  auto rotate = [&](int r, const Pack<TI, kE>& raw, const TI* src, float (&x)[kE], float (&b)[kE], float (&y)[kE]) {
     unpack(raw, x);
 #pragma unroll
-    for (int j = 0; j < E; ++j) {
+    for (int j = 0; j < kE; ++j) {
       y[j] = x[j];
-      e[j] = -1;
       b[j] = 0.f;
     }
     if (PAIRS == 0) {
-      Pack<TI, E> other;                                 // of lane +- half / E
+      Pack<TI, kE> other;                                // of lane +- half / kE
       constexpr int W = sizeof(raw) / 4;
       uint32_t mine[W], theirs[W];
       memcpy(mine, &raw, sizeof(raw));
@@ -261,71 +280,72 @@ __global__ void __launch_bounds__(kRThreads, E == 8 ? 2 : 3) paged4_append_kerne
       for (int i = 0; i < W; ++i) theirs[i] = __shfl_sync(0xffffffffu, mine[i], partner);
       memcpy(&other, theirs, sizeof(other));
       if (f0 < p.rot) {
-        float c[E], sn[E];
-        unpack(load_pack<E>(s_cos + r * half + pair0), c);
-        unpack(load_pack<E>(s_sin + r * half + pair0), sn);
+        float c[kE], sn[kE];
+        unpack(load_pack<kE>(s_cos + r * half + pair0), c);
+        unpack(load_pack<kE>(s_sin[!low] + r * half + pair0), sn);
         unpack(other, b);
 #pragma unroll
-        for (int j = 0; j < E; ++j) {
-          e[j] = pair0 + j;
-          b[j] = low ? -b[j] : b[j];
-          y[j] = fmaf(b[j], sn[j], x[j] * c[j]);
-        }
+        for (int j = 0; j < kE; ++j) y[j] = fmaf(b[j], sn[j], x[j] * c[j]);
       }
     } else {
 #pragma unroll
-      for (int j = 0; j < E; ++j) {
-        const int f = f0 + j;
-        if (f >= p.rot) continue;
-        if (PAIRS == 1) {
-          e[j] = f >> 1;
-          b[j] = f & 1 ? x[j ^ 1] : -x[j ^ 1];
-        } else {
-          e[j] = f < half ? f : f - half;
-          b[j] = f < half ? -to_f32(src[f + half]) : to_f32(src[f - half]);
-        }
-        const int i = r * half + e[j];
-        y[j] = fmaf(b[j], s_sin[i], x[j] * s_cos[i]);
+      for (int j = 0; j < kE; ++j) {
+        const int f = f0 + j, e = pair_of(j);
+        if (e < 0) continue;
+        if (PAIRS == 1) b[j] = x[j ^ 1];
+        else b[j] = to_f32(src[f < half ? f + half : f - half]);
+        y[j] = fmaf(b[j], s_sin[!first_of(j)][r * half + e], x[j] * s_cos[r * half + e]);
       }
     }
   };
-  auto work_q = [&](int r, int h, const Pack<TI, E>& raw) {
-    float x[E], b[E], y[E];
-    int e[E];
-    rotate(r, raw, static_cast<const TI*>(p.q) + (row0 + r) * p.q_row + (long long)h * HD, x, b, y, e);
-    if (s_at[r] == -2) return;
+  auto work_q = [&](int i, int h, const Pack<TI, kE>& raw) {
+    const int r = row_of(i);
+    float x[kE], b[kE], y[kE];
+    rotate(r, raw, static_cast<const TI*>(p.q) + (row0 + r) * p.q_row + (long long)h * HD, x, b, y);
     if (PAIRS == 2) __syncwarp();                        // q_out may be q, whose partners other lanes read
+    if (at_of(i) == -2) return;
     const long long to = ((long long)(row0 + r) * nq + h) * HD + f0;
     if (p.q_bf) store_pack(static_cast<__nv_bfloat16*>(p.q_out) + to, y);
     else store_pack(static_cast<__half*>(p.q_out) + to, y);
   };
-  auto work_k = [&](int r, int g, const Pack<TI, E>& raw) {
-    float x[E], b[E], y[E];
-    int e[E];
-    rotate(r, raw, static_cast<const TI*>(p.k) + (row0 + r) * p.k_row + (long long)g * HD, x, b, y, e);
-    const long long at = s_at[r];
-    if (at < 0) return;
+  auto work_k = [&](int i, int g, const Pack<TI, kE>& raw) {
+    const int r = row_of(i);
+    const long long at = at_of(i);
+    float x[kE], b[kE], y[kE];
+    rotate(r, raw, static_cast<const TI*>(p.k) + (row0 + r) * p.k_row + (long long)g * HD, x, b, y);
     const Scale s = scale_of(y, p.k_div);
-    float tol = 0.f, z[E], lo[E], hi[E];
+    // how far y may be from the rotated value; at position 0 it is that
+    const int pos = p.rot ? p.pos[row0 + r] : 0;
+    float tol = 0.f;
 #pragma unroll
-    for (int j = 0; j < E; ++j)
-      if (e[j] >= 0 && !(exact_mag && s_sin[r * half + e[j]] == 0.f)) tol = fmaxf(tol, fabsf(x[j]) + fabsf(b[j]));   // no angle: y is exact
-    tol *= kTol * fabsf(p.mag) * p.k_div;
+    for (int j = 0; j < kE; ++j)
+      if (PAIRS == 0 || pair_of(j) >= 0) tol = fmaxf(tol, fabsf(x[j]) + fabsf(b[j]));
+    tol = (pos == 0 && p.mag == 1.f) || f0 >= p.rot ? 0.f : tol * (kTol * fabsf(p.mag) * p.k_div);
     float tol_top = tol;
 #pragma unroll
     for (int o = 1; o < L; o <<= 1) tol_top = fmaxf(tol_top, __shfl_xor_sync(0xffffffffu, tol_top, o));
-    quotients(y, p.k_div, s, z);
+    quotients(y, s);
+    float hi[kE];
+    const float d = tol * s.inv;
 #pragma unroll
-    for (int j = 0; j < E; ++j) {
-      lo[j] = z[j] - tol * s.inv;
-      hi[j] = z[j] + tol * s.inv;
+    for (int j = 0; j < kE; ++j) {
+      hi[j] = y[j] + d;
+      y[j] -= d;
     }
-    uint32_t codes = codes_of(lo), scale = s.bits;
-    const bool open = !s.bad && (codes != codes_of(hi) || (tol_top > 0.f && f32_e4m3((s.top - tol_top) * (1.f / 6.f)) !=
-                                                                                f32_e4m3((s.top + tol_top) * (1.f / 6.f))));
+    uint32_t codes = codes_of(y), scale = s.bits;
+    const bool open = at >= 0 && !s.bad && tol_top > 0.f &&
+                      (codes != codes_of(hi) || f32_e4m3((s.top - tol_top) * (1.f / 6.f)) != f32_e4m3((s.top + tol_top) * (1.f / 6.f)));
     const unsigned any = __ballot_sync(0xffffffffu, open);
-    if (any) encode_exact<E>(x, b, e, any, p.pos[row0 + r], p.turns, p.mag, p.k_div, codes, scale);
-    store(true, at, g, s.bad ? 0u : codes, s.bad ? 0x7fu : scale);
+    if (any) {
+      int e[kE];
+#pragma unroll
+      for (int j = 0; j < kE; ++j) {
+        e[j] = pair_of(j);
+        if (first_of(j)) b[j] = -b[j];
+      }
+      encode_exact(x, b, e, any, pos, p.turns, p.mag, p.k_div, codes, scale);
+    }
+    store(p.c.k, p.c.ks, at, g, s.bad ? 0u : codes, s.bad ? 0x7fu : scale);
   };
   pdl_wait();
   pdl_trigger();
@@ -341,7 +361,9 @@ __global__ void __launch_bounds__(kRThreads, E == 8 ? 2 : 3) paged4_append_kerne
     // what f lacks, in radians: below 2^-24, and 0 only where the angle is a whole number of half turns
     const float rest = fmaf((float)(turn - (int32_t)f), 0x1p-31f * 3.14159265f, (float)(uint32_t)frac * (0x1p-63f * 3.14159265f));
     s_cos[i] = fmaf(-sn, rest, cs) * p.mag;
-    s_sin[i] = fmaf(cs, rest, sn) * p.mag;
+    sn = fmaf(cs, rest, sn) * p.mag;
+    s_sin[0][i] = -sn;
+    s_sin[1][i] = sn;
   }
   if (const int r = kRWarps - 1 - warp; r < nr) {        // the last warps: the first ones hold angles
     const RowSlot s = row_slot(p.map, p.T, row0 + r);
@@ -358,16 +380,16 @@ __global__ void __launch_bounds__(kRThreads, E == 8 ? 2 : 3) paged4_append_kerne
     const int h = h0 + x;
     if (h < nq) {
 #pragma unroll
-      for (int r = 0; r < kRRows; ++r)
-        if (r < nr) work_q(r, h, cur.a[r]);
+      for (int i = 0; i < TIMES; ++i)
+        if (i * RP < nr) work_q(i, h, cur.a[i]);
     } else if (h < nqk) {
 #pragma unroll
-      for (int r = 0; r < kRRows; ++r)
-        if (r < nr) work_k(r, h - nq, cur.a[r]);
+      for (int i = 0; i < TIMES; ++i)
+        if (i * RP < nr) work_k(i, h - nq, cur.a[i]);
     } else {
 #pragma unroll
-      for (int r = 0; r < kRRows; ++r)
-        if (r < nr && s_at[r] >= 0) work_v(s_at[r], h - nqk, cur.a[r]);
+      for (int i = 0; i < TIMES; ++i)
+        if (i * RP < nr) work_v(i, h - nqk, cur.a[i]);
     }
     if (AHEAD) cur = next;
     else if (x + kRWarps < n) load(cur, x + kRWarps);
@@ -472,24 +494,25 @@ void paged4_spans(const swa_paged4_cache* c, Span4 (&s)[4]) {
   s[3] = {c->v_scale, keys * c->hd / kBlock4};
 }
 
-template <typename TI, int E>
-static cudaError_t launch_pairs(const Rows4Params& p, int inter, dim3 grid, cudaStream_t s) {
-  const dim3 block(kRThreads);
-  if (inter) return launch_pdl(paged4_append_kernel<TI, E, 1>, grid, block, 0, s, p);
-  if (p.rot / 2 % E == 0) return launch_pdl(paged4_append_kernel<TI, E, 0>, grid, block, 0, s, p);
-  return launch_pdl(paged4_append_kernel<TI, E, 2>, grid, block, 0, s, p);
+template <typename TI, int HD>
+static cudaError_t launch_pairs(Rows4Params& p, int inter, cudaStream_t s) {
+  // all heads of the most rows a block once that gives every SM four blocks, else those that a warp takes at once, and a head
+  // a warp
+  using C = AppendCfg<HD>;
+  const long long sms = num_sms() > 0 ? num_sms() : 148;
+  p.R = p.T >= 4 * sms * C::ROWS ? C::ROWS : C::ROWS_WARP;
+  p.Hg = p.T >= 4 * sms * p.R ? p.H : kRWarps;
+  if ((p.H + p.Hg - 1) / p.Hg > 65535) p.Hg = (p.H + 65534) / 65535;
+  const dim3 grid((unsigned)((p.T + p.R - 1) / p.R), (unsigned)((p.H + p.Hg - 1) / p.Hg)), block(kRThreads);
+  if (inter) return launch_pdl(paged4_append_kernel<TI, HD, 1>, grid, block, 0, s, p);
+  if (p.rot / 2 % kE == 0) return launch_pdl(paged4_append_kernel<TI, HD, 0>, grid, block, 0, s, p);
+  return launch_pdl(paged4_append_kernel<TI, HD, 2>, grid, block, 0, s, p);
 }
 
 template <typename TI>
 static int launch_append(Rows4Params& p, int inter, cudaStream_t s) {
-  // all heads of kRRows rows once that gives every SM four blocks, else a row and a head a warp
-  const long long sms = num_sms() > 0 ? num_sms() : 148;
-  p.R = p.T >= 4 * sms * kRRows ? kRRows : 1;
-  p.Hg = p.T >= 4 * sms ? p.H : kRWarps;
-  if ((p.H + p.Hg - 1) / p.Hg > 65535) p.Hg = (p.H + 65534) / 65535;
-  const dim3 grid((unsigned)((p.T + p.R - 1) / p.R), (unsigned)((p.H + p.Hg - 1) / p.Hg));
-  return finish_launch(p.hd == 64 ? launch_pairs<TI, 2>(p, inter, grid, s) : p.hd == 128 ? launch_pairs<TI, 4>(p, inter, grid, s)
-                                                                                        : launch_pairs<TI, 8>(p, inter, grid, s));
+  return finish_launch(p.hd == 64 ? launch_pairs<TI, 64>(p, inter, s) : p.hd == 128 ? launch_pairs<TI, 128>(p, inter, s)
+                                                                                   : launch_pairs<TI, 256>(p, inter, s));
 }
 
 template <typename TO>
