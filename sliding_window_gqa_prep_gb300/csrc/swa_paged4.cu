@@ -14,12 +14,16 @@
 //     the lower (upper) halves of two keys' bytes are put into one byte before the conversion.
 //   P^T comes out of S^T by movmatrix: 8 x 8 transposed, in registers.
 // A value code * scale is exact in f16. Weights enter the second product in f16, scaled by
-// 2^(kLog2 + up to kLazy) so that small ones keep their bits.
-// Every CTA gets the same number of 64-key tiles of the whole call, wherever the cuts fall; one warp copies
+// 2^(kLog24 + up to kLazy4) so that small ones keep their bits.
+// Every CTA gets the same number of tiles of the whole call, wherever the cuts fall; one warp copies
 // them from the pages (plain bulk copies: a head's keys of a page are consecutive), the others take
-// a quarter of a tile's keys each (or half, for half of the vectors), with a running maximum and sums of
-// their own, joined at an item's end.
+// a quarter of a tile's keys each (or half, for half of the vectors or features), with a running maximum and
+// sums of their own, joined at an item's end.
 // Items that are cut leave a record (m, l, sum p v) per CTA, joined by paged_merge_kernel.
+// 64 sequences of 1024 .. 8192 keys, 8 KV heads of hd 128, one token of 4 vectors a head (367 MB): 83 us, 4.4 TB/s.
+// The copies alone take 66, the products with the conversions 77: some 300 instructions of a warp for 16 keys, at 0.6 a clk
+// of each of the SM's four schedulers. (Four CTAs an SM with 96 registers: 95 us, by what no longer fits; four CTAs
+// without a warp that copies, the last to read a stage refilling it: 101.)
 #include <cmath>
 
 #include "swa_paged4_attend.cuh"
@@ -652,7 +656,12 @@ __global__ void __launch_bounds__(Split4Cfg<D, NV, VG, FS>::THREADS, Split4Cfg<D
 // ---------------------------------------------------------------------------
 // Keys that a row may see up to which a CTA takes a (sequence, KV head) whole: no scan over the
 // sequences and no second kernel. By the table's width (or the window), since the lengths are the device's.
-constexpr int kWholeKeys4 = 512;
+// Measured with one row of 4 vectors, whole against cut: 512 keys at hd 64 / 128 / 256, 32 items 6.9 / 7.7 / 12.0 us
+// against 9.5 / 9.3 / 13.0; 1024 keys, 32 items 9.3 / 10.7 / 19.0 against 9.7 / 9.5 / 13.9, 128 items 9.4 / 10.9 / 19.6
+// against 12.9 / 13.5 / 19.2.
+static long long whole_keys4(const swa_paged4_cache& c, long long sms) {
+  return c.hd == 64 || (c.hd == 128 && (long long)c.B * c.nk * 2 >= sms) ? 1024 : 512;
+}
 
 struct Split4Plan {
   int rows, whole, grid;       // query vectors of a block (0: no sequence for this kernel)
@@ -702,7 +711,8 @@ static int by_size4(int hd, int rows, F f) {
 #undef SWA_ROWS
 }
 
-// Query vectors of a (sequence, KV head) up to which the split kernel takes it
+// Query vectors of a (sequence, KV head) up to which the split kernel takes it: as many as its columns hold. (With
+// that many over 32 x 4096 .. 8192 keys it takes 56 / 80 / 88 us at hd 64 / 128 / 256, the chunk kernel 131 / 164 / 261.)
 static int split4_vecs(int hd) { return hd == 256 ? 16 : 32; }
 
 static void split4_plan(const swa_paged4_attend_args* a, long long vecs, Split4Plan* sp) {
@@ -714,11 +724,12 @@ static void split4_plan(const swa_paged4_attend_args* a, long long vecs, Split4P
     const long long w = (long long)a->window + a->sinks + a->max_rows + 256;
     keys = w < keys ? w : keys;
   }
-  sp->whole = keys <= kWholeKeys4;
+  const long long sms = num_sms() > 0 ? num_sms() : 148;
+  sp->whole = keys <= whole_keys4(c, sms);
   const int occ = sp->whole ? 0 : by_size4(c.hd, sp->rows, [](auto d, auto n, auto g, auto f) {
     return split4_occupancy<decltype(d)::value, decltype(n)::value, decltype(g)::value, decltype(f)::value>();
   });
-  sp->grid = sp->whole ? c.B * c.nk : (num_sms() > 0 ? num_sms() : 148) * occ;
+  sp->grid = sp->whole ? c.B * c.nk : (int)sms * occ;
   if (!sp->whole) {
     const size_t recs = (size_t)sp->grid * 2 * sp->rows;
     sp->off_ml = up256s(recs * c.hd * sizeof(float));

@@ -19,7 +19,9 @@ namespace cg = cooperative_groups;
 
 constexpr int kPCtas = 8, kPThreads = 512;    // of the cluster
 constexpr int kOneThreads = 1024;             // of a CTA that makes all passes
-constexpr int kOnePages = 8192, kOneSeqs = 2048, kOneEntries = 32768;   // what it takes: pages, sequences of a batch, table entries
+// What it takes: pages and sequences that fit in shared memory, and table entries up to where the cluster is as fast (one
+// launch against two, us: fork of 64 x 64 entries 8.4, 11.7; 256 x 64 21.1, 21.0; compact of 600 pages 5.4, 9.1; 6000 13.6, 15.8).
+constexpr int kOnePages = 8192, kOneSeqs = 2048, kOneEntries = 32768;
 constexpr int kCopyThreads = 256, kCopyUnit = kCopyThreads * 8 * 16;   // bytes that this many threads copy at a time
 
 struct PageCopies {
