@@ -10,9 +10,10 @@
 // are thus encoded exactly. A rotated value is known up to kTol * (|u| + |v|); where that leaves
 // a scale or a code open (one head in some hundreds) the warp takes the angles and the encoding again in f64.
 //
-// Bound by memory and by the instructions of the encoding: a warp takes a head of a row, lane i its
-// features hd / 32 * i and on, so that a pair's other half is in a lane of the same warp, a block's largest value
-// a few shuffles away, and every access consecutive.
+// Bound by memory and by the instructions of the encoding: a lane takes half a block of a row's head, a warp one head
+// of one to four rows, so that a pair's other half is in a lane of the same warp, a block's largest value one shuffle away,
+// and every access consecutive. 8192 rows of 32 heads of q and 8 of k and v, hd 128, from f32: 62 us, where their bytes
+// take 41; 24 of them are the encoding of k and v (33 with positions).
 #include <cmath>
 #include <cstring>
 
@@ -101,6 +102,12 @@ __device__ __forceinline__ uint32_t f32x2_e2m1(float lo, float hi) {
   asm("{\n\t.reg .b8 a;\n\tcvt.rn.satfinite.e2m1x2.f32 a, %1, %2;\n\tcvt.u32.u8 %0, a;\n\t}" : "=r"(d) : "f"(hi), "f"(lo));
   return d;
 }
+// The largest of three, NaN if one is
+__device__ __forceinline__ float nan_max(float a, float b, float c) {
+  float d;
+  asm("max.NaN.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+  return d;
+}
 template <int E>
 __device__ __forceinline__ uint32_t codes_of(const float (&z)[E]) {
   uint32_t c = 0;
@@ -162,7 +169,7 @@ __device__ __noinline__ void encode_exact(const float (&x)[kE], const float (&b)
 // PAIRS: how the features of a pair lie. 0: half of the turned ones apart, and a lane's partners are those
 // of one other lane; 1: next to each other; 2: as 0 with partners in two lanes (half % kE != 0).
 template <typename TI, int HD, int PAIRS>
-__global__ void __launch_bounds__(kRThreads, 3) paged4_append_kernel(const __grid_constant__ Rows4Params p) {
+__global__ void __launch_bounds__(kRThreads, sizeof(TI) == 2 ? 4 : 3) paged4_append_kernel(const __grid_constant__ Rows4Params p) {
   using C = AppendCfg<HD>;
   constexpr int LH = C::LANES, RP = C::ROWS_WARP, TIMES = C::ROWS / RP, L = kBlock4 / kE;   // L: lanes of a block
   __shared__ __align__(16) float s_cos[C::ROWS * (HD / 2)], s_sin[2][C::ROWS * (HD / 2)];   // [0]: -sin, of a pair's first feature
@@ -170,9 +177,10 @@ __global__ void __launch_bounds__(kRThreads, 3) paged4_append_kernel(const __gri
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int row0 = blockIdx.x * p.R, nr = min(p.R, p.T - row0), h0 = blockIdx.y * p.Hg, n = min(p.Hg, p.H - h0);
   const int half = p.rot >> 1, sub = lane % LH, f0 = sub * kE, row_w = lane / LH, nq = p.nh, nqk = p.nh + p.map.nk;
-  // A warp takes the heads warp, warp + 8, .. of the block, of each all rows; the next head's are loaded while these
-  // are worked on (where they are no more than 16 registers).
-  constexpr bool AHEAD = sizeof(TI) * kE * TIMES <= 64;
+  // A warp takes the heads warp, warp + 8, .. of the block, of each all rows. The next head's are loaded while these
+  // are worked on where they lie in more than 16 bytes a lane; else another CTA fits (8192 rows of 32 + 16 heads, hd 128:
+  // f32 62 us, 65 the other way; bf16 62, 66).
+  constexpr bool AHEAD = sizeof(TI) == 4 && HD < 256;
   struct Rows {
     Pack<TI, kE> a[TIMES];
   };
@@ -197,8 +205,7 @@ __global__ void __launch_bounds__(kRThreads, 3) paged4_append_kernel(const __gri
       if (i * RP + row_w < nr) t.a[i] = load_pack<kE>(src);
     }
   };
-  // The largest of a block's values (as bits: NaN and infinities above all), in units of 2^exp; its scale and
-  // the reciprocal
+  // The largest of a block's values (NaN where one is) in units of 2^exp; its scale and the reciprocal
   struct Scale {
     float top, u, inv;
     uint32_t bits;
@@ -206,16 +213,19 @@ __global__ void __launch_bounds__(kRThreads, 3) paged4_append_kernel(const __gri
   };
   // y in units of 2^exp afterwards
   auto scale_of = [&](float (&y)[kE], float div) {
-    uint32_t m = 0;
+    float m = fabsf(y[0]);
 #pragma unroll
-    for (int j = 0; j < kE; ++j) m = max(m, __float_as_uint(y[j]) & 0x7fffffffu);
+    for (int j = 1; j + 1 < kE; j += 2) m = nan_max(m, fabsf(y[j]), fabsf(y[j + 1]));
+    m = nan_max(m, fabsf(y[kE - 1]), m);
 #pragma unroll
-    for (int o = 1; o < L; o <<= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, o));
+    for (int o = 1; o < L; o <<= 1) m = nan_max(m, __shfl_xor_sync(0xffffffffu, m, o), m);
     Scale s;
-    s.bad = m >= 0x7f800000u;
-    s.top = __uint_as_float(m) * div;
+    s.bad = !(m < INFINITY);
+    s.top = m * div;
+    if (div != 1.f) {
 #pragma unroll
-    for (int j = 0; j < kE; ++j) y[j] *= div;
+      for (int j = 0; j < kE; ++j) y[j] *= div;
+    }
     if (__any_sync(0xffffffffu, s.top > 4096.f)) {       // 448 * 6 and more take the largest scale
       s.top = fminf(s.top, 4096.f);
 #pragma unroll
@@ -287,14 +297,24 @@ __global__ void __launch_bounds__(kRThreads, 3) paged4_append_kernel(const __gri
 #pragma unroll
         for (int j = 0; j < kE; ++j) y[j] = fmaf(b[j], sn[j], x[j] * c[j]);
       }
+    } else if (PAIRS == 1) {
+#pragma unroll
+      for (int j = 0; j < kE; j += 2) {
+        if (f0 + j >= p.rot) continue;
+        const int i = r * half + (f0 + j) / 2;
+        const float c = s_cos[i], sn = s_sin[1][i];
+        b[j] = x[j + 1];
+        b[j + 1] = x[j];
+        y[j] = fmaf(-x[j + 1], sn, x[j] * c);
+        y[j + 1] = fmaf(x[j], sn, x[j + 1] * c);
+      }
     } else {
 #pragma unroll
       for (int j = 0; j < kE; ++j) {
         const int f = f0 + j, e = pair_of(j);
         if (e < 0) continue;
-        if (PAIRS == 1) b[j] = x[j ^ 1];
-        else b[j] = to_f32(src[f < half ? f + half : f - half]);
-        y[j] = fmaf(b[j], s_sin[!first_of(j)][r * half + e], x[j] * s_cos[r * half + e]);
+        b[j] = to_f32(src[f < half ? f + half : f - half]);
+        y[j] = fmaf(b[j], s_sin[f >= half][r * half + e], x[j] * s_cos[r * half + e]);
       }
     }
   };
@@ -496,8 +516,8 @@ void paged4_spans(const swa_paged4_cache* c, Span4 (&s)[4]) {
 
 template <typename TI, int HD>
 static cudaError_t launch_pairs(Rows4Params& p, int inter, cudaStream_t s) {
-  // all heads of the most rows a block once that gives every SM four blocks, else those that a warp takes at once, and a head
-  // a warp
+  // All heads of the most rows a block once that gives every SM four blocks, else the rows that a warp takes at once, and
+  // a head a warp. (8192 rows of 32 + 16 heads in f32: 62 us, with fewer rows 72, with 8 heads a block 86.)
   using C = AppendCfg<HD>;
   const long long sms = num_sms() > 0 ? num_sms() : 148;
   p.R = p.T >= 4 * sms * C::ROWS ? C::ROWS : C::ROWS_WARP;
@@ -518,7 +538,8 @@ static int launch_append(Rows4Params& p, int inter, cudaStream_t s) {
 template <typename TO>
 static int launch_read(Rows4Params& p, cudaStream_t s) {
   const long long sms = num_sms() > 0 ? num_sms() : 148;
-  // rows of a block: 8 heads a thread and array, if that leaves every SM two blocks
+  // rows of a block: 8 heads a thread and array, if that leaves every SM two blocks (46000 rows of 8 heads, hd 128: 43 us, with
+  // one row a block 112)
   const long long row = (long long)p.map.nk * p.hd / 8, most = 8 * kRThreads / row;
   long long R = p.T / (2 * sms);
   R = R > most ? most : R;
