@@ -40,7 +40,7 @@ def exchange_run(rounds, buffers, seed):
 
 def test_exchange_of_scores():
     text = source("swa_paged4.cu")
-    assert "XB = FS > 1 ? 2 * kWarps4 * NV * 512" in text and "turn ^= kWarps4 * NV * 512;" in text
+    assert "XB = FS > 1 ? 2 * kWarps4 * G * NV * 512" in text and "turn ^= kWarps4 * G * NV * 512;" in text
     for seed in range(100):
         exchange_run(20, 2, seed)
     with pytest.raises(AssertionError):
