@@ -291,6 +291,26 @@ def test_queries_rotated_in_place(hd, rot, interleaved, T):
     assert torch.equal(own, apart) and not torch.equal(own, bt.q)
 
 
+def test_calls_without_rows():
+    """No rows: nothing is launched and nothing changes, in eager calls and in a captured one."""
+    bt = Batch4(t=[0, 0], lens=[5, 0], nh=4, nk=2, hd=64, page=16)
+    none, q = torch.empty(0, 2, 64, dtype=BF, device="cuda"), torch.empty(0, 4, 64, dtype=BF, device="cuda")
+    before, err = [y.clone() for y in (bt.k, bt.ks.view(U8))], zero()
+
+    def calls():
+        return (swa.paged4_append(none, none, None, *bt.args, q=q, err=err), *swa.paged4_read(*bt.args, T=0, err=err),
+                swa.paged4_attend(q, *bt.args, 0.1, max_rows=1, err=err))
+    assert [y.shape[0] for y in calls()] == [0] * 4
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        calls()
+    graph.replay()
+    torch.cuda.synchronize()
+    assert int(err.item()) == 0 and torch.equal(before[0], bt.k) and torch.equal(before[1], bt.ks.view(U8))
+    out, lens, refs, left = swa.paged_fork([], bt.args[4], dev([5, 0]), dev([1] * bt.k.shape[0]), dev([-1]), 16)     # no pools: the tables alone
+    assert out.tolist() == [[-1] * bt.max_pages] and lens.tolist() == [0] and left.item() == int((refs == 0).sum())
+
+
 def test_refusals_of_the_binding():
     bt = Batch4(t=[2], lens=[20], nh=4, nk=2, hd=64, page=16)
     x = torch.randn(2, 2, 64, device="cuda").to(BF)
