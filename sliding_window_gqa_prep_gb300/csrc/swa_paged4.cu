@@ -48,9 +48,11 @@ struct Split4Cfg {
   // CTAs an SM: 96 registers a thread for four, 128 for three, 168 for two (NV = 2 with 128 features spills with 128:
   // 16 vectors over 32 x 6144 keys, 8 KV heads, 93 us with three, 85 with two)
   static constexpr int CTAS = DW == 64 ? 5 - NV : 4 - NV;
-  // Groups of 16 keys that a warp takes at a time: two where a tile has them, and the exchange of scores room
-  // (64 x 1024 .. 8192 keys, 4 vectors of 128 features 89 us with one, 85 with two)
-  static constexpr int G = (FS == 1 || NV == 1) && KT / 16 / (kWarps4 / (VG * FS)) >= 2 ? 2 : 1;
+  static constexpr int G = 2;                               // groups of 16 keys that a warp takes at a time (one: 64 x 1024 .. 8192
+                                                            // keys, 4 vectors, hd 128, 89 us; two: 85)
+  // V is loaded before S is computed where 16 vectors of half the features wait for the other half's S (drafts of
+  // 16 vectors at hd 256: 66 us, after it 67; one vector at hd 128: 54 before it, 51 after)
+  static constexpr bool V_FIRST = FS == 2 && NV == 2;
   // The warps of a group join their O in shared memory, in two rounds where one would take the stages' room
   static constexpr int JR = NV * D > 128 ? 2 : 1, JT = DW / 16 / JR, JROW = 16 * JT + 4;   // a vector's floats, and 4 apart
   static constexpr int JOIN = kWarps4 * 8 * NV * JROW * 4;
@@ -153,6 +155,7 @@ __global__ void __launch_bounds__(Split4Cfg<D, NV, VG, FS>::THREADS, Split4Cfg<D
   using C = Split4Cfg<D, NV, VG, FS>;
   constexpr int DW = C::DW, ST = C::ST, KT = C::KT, KS = DW / 16, NW = C::THREADS / 32, KG = kWarps4 / (VG * FS), SUBS = KT / 16 / KG, G = C::G;
   constexpr bool QS = C::QS;
+  static_assert(SUBS % G == 0, "a warp's keys of a tile in whole turns");
   extern __shared__ unsigned char sm_raw[];
   __shared__ __align__(8) uint64_t b_full[ST], b_empty[ST];
   __shared__ long long s_scan[NW];
@@ -403,7 +406,7 @@ __global__ void __launch_bounds__(Split4Cfg<D, NV, VG, FS>::THREADS, Split4Cfg<D
         const uint32_t codes = st * C::STAGE + sub * 16 * (D / 2), scales = st * C::STAGE + sub * 16 * (D / 16);
         const bool mask = __any_sync(0xffffffffu, k0 + 16 * G > lim_min || k0 < lo_max);   // a branch, not selects
         // V^T: keys 2 lt, 2 lt + 1 (+ 8) of the products' rows, features (hd / 8) lg ..; loaded and regrouped before
-        // the weights are known, and before S where the registers allow
+        // the weights are known
         uint32_t lo[G][2][VW], hi[G][2][VW], u1[G][2], u2[G][2];
         auto load_v = [&]() {
 #pragma unroll
@@ -422,7 +425,7 @@ __global__ void __launch_bounds__(Split4Cfg<D, NV, VG, FS>::THREADS, Split4Cfg<D
               u2[y][h] = lds_u8(at_vs2 + scales + (y * 16 + h * 8) * (D / 16));
             }
         };
-        if constexpr (G == 1) load_v();
+        if constexpr (C::V_FIRST) load_v();
         float sc[G][NV][4];
         // 4 features a step; the groups in turn, since a step's products wait for the step's before
         uint32_t wa[G][W], wc[G][W], sa[G][2], sb[G][2];   // codes of the two keys; a block's scale in both halves
@@ -455,7 +458,7 @@ __global__ void __launch_bounds__(Split4Cfg<D, NV, VG, FS>::THREADS, Split4Cfg<D
             }
           }
         });
-        if constexpr (G > 1) load_v();
+        if constexpr (!C::V_FIRST) load_v();
         if constexpr (FS == 2) {            // the other features' part, added in the same order by both
 #pragma unroll
           for (int y = 0; y < G; ++y)
