@@ -15,12 +15,12 @@
 //   P^T comes out of S^T by movmatrix: 8 x 8 transposed, in registers.
 // A value code * scale is exact in f16. Weights enter the second product in f16, scaled by
 // 2^(kLog24 + up to kLazy4) so that small ones keep their bits.
-// Every CTA gets the same number of tiles of the whole call, wherever the cuts fall; one warp copies
+// Every CTA gets the same share of the whole call's tiles and items' starts, wherever the cuts fall; one warp copies
 // them from the pages (plain bulk copies: a head's keys of a page are consecutive), the others take
 // a quarter of a tile's keys each (or half, for half of the vectors or features), with a running maximum and
 // sums of their own, joined at an item's end.
 // Items that are cut leave a record (m, l, sum p v) per CTA, joined by paged_merge_kernel.
-// 64 sequences of 1024 .. 8192 keys, 8 KV heads of hd 128, one token of 4 vectors a head (367 MB): 83 us, 4.4 TB/s.
+// 64 sequences of 1024 .. 8192 keys, 8 KV heads of hd 128, one token of 4 vectors a head (367 MB): 78 us, 4.7 TB/s.
 // The copies alone take 66, the products with the conversions 77: some 300 instructions of a warp for 16 keys, at 0.6 a clk
 // of each of the SM's four schedulers. (Four CTAs an SM with 96 registers: 95 us, by what no longer fits; four CTAs
 // without a warp that copies, the last to read a stage refilling it: 101.)
@@ -32,6 +32,7 @@
 namespace swa {
 
 constexpr int kWarps4 = 4;           // warps that compute
+constexpr int kWeighed = 8;          // tiles a CTA from which on an item's start counts (below that the cuts matter more)
 constexpr int kMinKeys4 = 128;       // a CTA takes at least this many keys (one sequence of 1024, 2 KV heads: 8.6 us, 9.6 with 256)
 
 // A warp has NV tiles of 8 query vectors. VG groups of warps share a tile's keys and have other vectors; FS
@@ -41,6 +42,10 @@ template <int D, int NV, int VG, int FS>
 struct Split4Cfg {
   static constexpr int THREADS = kWarps4 * 32 + 32;         // and the warp that copies
   static constexpr int KT = D == 256 ? 64 : 128;            // keys of a tile
+  // Tiles that take as long as an item's start and join (3.3 us, a tile 1.3, at hd 128 and 4 vectors; 5.3 and 1.6 for 16
+  // vectors at hd 256). Shares count them: the last CTA of 64 x 1024 .. 8192 keys ended at 80 us with tiles alone, half of the
+  // others before 68; the call takes 83 us without, 80 / 78 / 79 with 2 / 3 / 4.
+  static constexpr int START = FS == 2 && NV == 2 ? 4 : 3;
   static constexpr int CODES = KT * D / 2, SCALES = KT * D / 16, STAGE = 2 * (CODES + SCALES);
   static constexpr int ROWS = 8 * NV * VG;                  // query vectors
   static constexpr int DW = D / FS;                         // features of a warp
@@ -158,8 +163,8 @@ __global__ void __launch_bounds__(Split4Cfg<D, NV, VG, FS>::THREADS, Split4Cfg<D
   static_assert(SUBS % G == 0, "a warp's keys of a tile in whole turns");
   extern __shared__ unsigned char sm_raw[];
   __shared__ __align__(8) uint64_t b_full[ST], b_empty[ST];
-  __shared__ long long s_scan[NW];
-  __shared__ long long s_off, s_total;
+  __shared__ longlong2 s_scan[NW];
+  __shared__ long long s_off;
   __shared__ int s_b, s_abort;
   __shared__ float2 s_ml[kWarps4][8 * NV];
   __shared__ float s_shift[C::ROWS], s_inv[C::ROWS];
@@ -182,8 +187,10 @@ __global__ void __launch_bounds__(Split4Cfg<D, NV, VG, FS>::THREADS, Split4Cfg<D
   pdl_wait();
   pdl_trigger();
 
-  // --- this CTA's share of all tiles: a scan over the sequences
+  // --- this CTA's share of all tiles: a scan over the sequences, of their tiles and of the items that have some
   uint32_t bits = 0;
+  int weight = 0;                           // what an item's start costs, in tiles
+  long long total = 0, per = 0;
   if (a.whole) {
     if (tid == 0) {
       const int b = blockIdx.x / a.map.nk;
@@ -191,39 +198,51 @@ __global__ void __launch_bounds__(Split4Cfg<D, NV, VG, FS>::THREADS, Split4Cfg<D
       if (bits) set_err(a.err, bits);
       if (n > 0) s_b = b;
       s_off = (long long)(blockIdx.x % a.map.nk) * n;
-      s_total = n;
+      s_scan[0] = make_longlong2(n, 1);
     }
     __syncthreads();
+    total = per = s_scan[0].x;
   } else {
     const int E = (a.map.B + C::THREADS - 1) / C::THREADS;
-    long long mine = 0;
+    longlong2 mine = make_longlong2(0, 0);
     for (int e = 0; e < E; ++e) {
       const int b = tid * E + e;
-      if (b < a.map.B) mine += (long long)a.map.nk * split4_tiles(paged_seq(a.map, b, a.T, a.max_rows, bits), p, KT).n;
+      const int n = b < a.map.B ? split4_tiles(paged_seq(a.map, b, a.T, a.max_rows, bits), p, KT).n : 0;
+      mine.x += (long long)a.map.nk * n;
+      mine.y += n > 0 ? a.map.nk : 0;
     }
     if (bits && blockIdx.x == 0) set_err(a.err, bits);
-    long long incl = mine;
+    longlong2 incl = mine;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
-      const long long v = __shfl_up_sync(0xffffffffu, incl, o);
-      if (lane >= o) incl += v;
+      const long long x = __shfl_up_sync(0xffffffffu, incl.x, o), y = __shfl_up_sync(0xffffffffu, incl.y, o);
+      if (lane >= o) {
+        incl.x += x;
+        incl.y += y;
+      }
     }
     if (lane == 31) s_scan[warp] = incl;
     __syncthreads();
-    long long before = incl - mine, total = 0;
+    longlong2 before = make_longlong2(incl.x - mine.x, incl.y - mine.y), sum = make_longlong2(0, 0);
     for (int w = 0; w < NW; ++w) {
-      if (w < warp) before += s_scan[w];
-      total += s_scan[w];
+      if (w < warp) {
+        before.x += s_scan[w].x;
+        before.y += s_scan[w].y;
+      }
+      sum.x += s_scan[w].x;
+      sum.y += s_scan[w].y;
     }
-    long long per = (total + gridDim.x - 1) / gridDim.x;
-    if (per < kMinKeys4 / KT) per = kMinKeys4 / KT;
-    const long long u0 = per * blockIdx.x;
-    if (u0 >= before && u0 < before + mine) {
-      long long off = u0 - before;
+    if (sum.x >= (long long)kWeighed * gridDim.x) weight = C::START;
+    total = sum.x + weight * sum.y;
+    per = max((total + gridDim.x - 1) / gridDim.x, (long long)(kMinKeys4 / KT));
+    const long long at = per * blockIdx.x - (before.x + weight * before.y);
+    if (at >= 0 && at < mine.x + weight * mine.y) {
+      long long off = at;
       for (int e = 0; e < E; ++e) {
         const int b = tid * E + e;
         uint32_t ignore = 0;
-        const long long n = (long long)a.map.nk * split4_tiles(paged_seq(a.map, b, a.T, a.max_rows, ignore), p, KT).n;
+        const int tiles = split4_tiles(paged_seq(a.map, b, a.T, a.max_rows, ignore), p, KT).n;
+        const long long n = tiles ? (long long)a.map.nk * (tiles + weight) : 0;
         if (off < n) {
           s_b = b;
           s_off = off;
@@ -232,27 +251,28 @@ __global__ void __launch_bounds__(Split4Cfg<D, NV, VG, FS>::THREADS, Split4Cfg<D
         off -= n;
       }
     }
-    if (tid == 0) s_total = total;
     __syncthreads();
   }
-  const long long total = s_total;
-  long long per = (total + gridDim.x - 1) / gridDim.x;
-  if (per < kMinKeys4 / KT) per = kMinKeys4 / KT;
-  if (a.whole) per = total;
-  const long long u0 = a.whole ? 0 : per * blockIdx.x;
+  const long long u0 = a.whole ? 0 : per * blockIdx.x, u1 = min(u0 + per, total);
   if (tid == 0 && !a.whole) a.ws_desc[blockIdx.x] = make_int4(-1, 0, 0, 0);
   if (s_b < 0) return;
   // the items of this share, walked by the copying warp and by the others alike
-  long long left = min(per, total - u0);
   int b = s_b;
   uint32_t ignore = 0;
   PagedSeq s = paged_seq(a.map, b, a.T, a.max_rows, ignore);
   Tiles4 tl = split4_tiles(s, p, KT);
-  int tile0 = (int)(s_off % tl.n), g = (int)(s_off / tl.n);
-  auto next_item = [&](int tile1) {         // false at the end
-    left -= tile1 - tile0;
-    tile0 = 0;
-    if (left <= 0) return false;
+  int g = (int)(s_off / (tl.n + weight));
+  long long item = u0 - s_off % (tl.n + weight);            // its first unit
+  // the tiles of the share in it: [tile0, tile1), none where the share ends in front of its first
+  int tile0, tile1;
+  auto tiles_of_item = [&]() {
+    tile0 = (int)max(0LL, u0 - item - weight);
+    tile1 = (int)max(0LL, min(u1 - item - weight, (long long)tl.n));
+    return tile0 < tile1;
+  };
+  auto next_item = [&]() {                  // false at the end
+    item += tl.n + weight;
+    if (item >= u1) return false;
     if (++g == a.map.nk) {
       g = 0;
       do {
@@ -260,8 +280,9 @@ __global__ void __launch_bounds__(Split4Cfg<D, NV, VG, FS>::THREADS, Split4Cfg<D
         tl = split4_tiles(s, p, KT);
       } while (tl.n == 0);
     }
-    return true;
+    return tiles_of_item();
   };
+  if (!tiles_of_item() && !next_item()) return;
   if (warp == kWarps4) {
     // ------------------------------------------------------------ copies: a run of keys of one array a lane
     const int page = 1 << a.map.page_shift, rows = min(page, KT), runs = KT / rows;   // 4 * runs <= 32
@@ -273,7 +294,6 @@ __global__ void __launch_bounds__(Split4Cfg<D, NV, VG, FS>::THREADS, Split4Cfg<D
     bool ok = true;
     int it = 0;                             // tiles of this share so far: stage it % ST
     do {
-      const int tile1 = (int)min((long long)tl.n, tile0 + left);
       const int32_t* table = a.map.table + (size_t)b * a.map.max_pages;
       for (int x = tile0; ok && x < tile1; ++x, ++it) {
         const int key = tl.at(x) * KT + run * rows, st = it % ST;
@@ -300,7 +320,7 @@ __global__ void __launch_bounds__(Split4Cfg<D, NV, VG, FS>::THREADS, Split4Cfg<D
         __syncwarp();
         if (from) bulk_g2s(sm + st * C::STAGE + dst, from, rows * row, &b_full[st]);
       }
-      if (!ok || !next_item(tile1)) break;
+      if (!ok || !next_item()) break;
     } while (true);
     if (!ok) {
       set_err(a.err, SWA_DERR_TIMEOUT);
@@ -324,7 +344,6 @@ __global__ void __launch_bounds__(Split4Cfg<D, NV, VG, FS>::THREADS, Split4Cfg<D
   int st = 0;                               // the next tile's stage, and the parity of its barrier's phase
   uint32_t phase = 0;
   do {
-    const int tile1 = (int)min((long long)tl.n, tile0 + left);
     const int nvec = s.t * hpg;
     // --- Q^T as B operands in f16, each vector scaled by a power of two; scores' factors, limits
     uint32_t qf[QS ? 1 : NV][KS][2];
@@ -643,12 +662,8 @@ __global__ void __launch_bounds__(Split4Cfg<D, NV, VG, FS>::THREADS, Split4Cfg<D
         }
       }
     }
-    if (!whole && tile0 == 0 && tid == 0) {
-      // units of this item from here on / per CTA: the CTA that ends it
-      const long long end = u0 + (min(per, total - u0) - left) + tl.n - 1;
-      a.ws_desc[blockIdx.x] = make_int4(b, g, (int)(end / per), 0);
-    }
-    if (!next_item(tile1)) break;
+    if (!whole && tile0 == 0 && tid == 0) a.ws_desc[blockIdx.x] = make_int4(b, g, (int)((item + weight + tl.n - 1) / per), 0);   // .. CTA that ends it
+    if (!next_item()) break;
     named_barrier(1, kWarps4 * 32);         // s_ml and join are read
   } while (true);
   if (!ok) set_err(a.err, SWA_DERR_TIMEOUT);
