@@ -465,7 +465,7 @@ __global__ void __launch_bounds__(SplitCfg<D>::THREADS)
     if (!whole && tile0 == 0 && tid == 0) {
       // units of this item from here on / per CTA: the CTA that ends it
       const long long end = u0 + (min(per, total - u0) - left) + n_tiles - 1;
-      p.ws_desc[blockIdx.x] = make_int4(b, g, (int)(end / per), 0);
+      p.ws_desc[blockIdx.x] = make_int4(s.r0, g, (int)(end / per), s.t);
     }
     if (!next_item(tile1)) break;
     named_barrier(1, 4 * DS * 32);          // s_ml and ob are read

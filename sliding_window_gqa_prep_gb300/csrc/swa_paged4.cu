@@ -21,9 +21,10 @@
 // sums of their own, joined at an item's end.
 // Items that are cut leave a record (m, l, sum p v) per CTA, joined by paged_merge_kernel.
 // 64 sequences of 1024 .. 8192 keys, 8 KV heads of hd 128, one token of 4 vectors a head (367 MB): 78 us, 4.7 TB/s.
-// The copies alone take 66, the products with the conversions 77: some 300 instructions of a warp for 16 keys, at 0.6 a clk
-// of each of the SM's four schedulers. (Four CTAs an SM with 96 registers: 95 us, by what no longer fits; four CTAs
-// without a warp that copies, the last to read a stage refilling it: 101.)
+// The copies alone take 65, the products with the conversions 73: some 300 instructions of a warp for 16 keys, at 0.6 a clk
+// of each of the SM's four schedulers. (Where the call took 85 us, four CTAs an SM with 96 registers took 95, by what no
+// longer fits; four CTAs without a warp that copies, the last to read a stage refilling it, 101.)
+// 32 times 16 vectors (4 drafts) over a window of 4096 keys, 4 KV heads of hd 256 (153 MB): 62 us; copies alone 39, products 59.
 #include <cmath>
 
 #include "swa_paged4_attend.cuh"
@@ -662,7 +663,7 @@ __global__ void __launch_bounds__(Split4Cfg<D, NV, VG, FS>::THREADS, Split4Cfg<D
         }
       }
     }
-    if (!whole && tile0 == 0 && tid == 0) a.ws_desc[blockIdx.x] = make_int4(b, g, (int)((item + weight + tl.n - 1) / per), 0);   // .. CTA that ends it
+    if (!whole && tile0 == 0 && tid == 0) a.ws_desc[blockIdx.x] = make_int4(s.r0, g, (int)((item + weight + tl.n - 1) / per), s.t);   // .. CTA that ends it
     if (!next_item()) break;
     named_barrier(1, kWarps4 * 32);         // s_ml and join are read
   } while (true);

@@ -23,7 +23,7 @@ struct PagedAttendParams {
   float* lse;
   float* ws_acc;               // [records][rows][hd] (split kernel)
   float2* ws_ml;               // [records][rows] (m in log2 units, l)
-  int4* ws_desc;               // per CTA: the item it left unfinished (b, g, last CTA, 0), b < 0: none
+  int4* ws_desc;               // per CTA: the item it left unfinished (first row, g, last CTA, rows), first row < 0: none
   uint32_t* err;
 };
 

@@ -20,12 +20,12 @@ __global__ void __launch_bounds__(kMergeThreads) paged_merge_kernel(const PagedA
   pdl_trigger();
   const int4 dsc = p.ws_desc[blockIdx.x];
   if (dsc.x < 0) return;
-  uint32_t ignore = 0;
-  const PagedSeq s = paged_seq(p.map, dsc.x, p.T, p.max_rows, ignore);
-  for (int row = blockIdx.y; row < s.t * p.hpg; row += gridDim.y) {
+  for (int row = blockIdx.y; row < dsc.w * p.hpg; row += gridDim.y) {
     const int c0 = blockIdx.x, n = dsc.z - c0 + 1;
     const int tid = threadIdx.x, grp = tid / L, c = tid % L;
     auto rec = [&](int i) { return ((size_t)(c0 + i) * 2 + (i == 0 ? 1 : 0)) * rows + row; };
+    float y[8];                               // a group's first record, asked for before the maximum is known
+    if (grp < n) load8(p.ws_acc + rec(grp) * D + c * 8, y);
     float mt = -INFINITY;
     for (int i = tid; i < n; i += kMergeThreads) mt = fmaxf(mt, p.ws_ml[rec(i)].x);
 #pragma unroll
@@ -39,8 +39,7 @@ __global__ void __launch_bounds__(kMergeThreads) paged_merge_kernel(const PagedA
     for (int i = grp; i < n; i += NG) {
       const float2 ml = p.ws_ml[rec(i)];
       const float a = ml.x == -INFINITY ? 0.f : ex2(ml.x - mt);
-      float y[8];
-      load8(p.ws_acc + rec(i) * D + c * 8, y);
+      if (i > grp) load8(p.ws_acc + rec(i) * D + c * 8, y);
       lt += a * ml.y;
 #pragma unroll
       for (int j = 0; j < 8; ++j) acc[j] += a * y[j];
@@ -57,7 +56,7 @@ __global__ void __launch_bounds__(kMergeThreads) paged_merge_kernel(const PagedA
 #pragma unroll
         for (int j = 0; j < 8; ++j) acc[j] += y[j];
       }
-      paged_store_row<T>(p, s.r0 + row / p.hpg, dsc.y * p.hpg + row % p.hpg, D, c * 8, mt, lt, PScale<T>::kLog2, acc, c == 0);
+      paged_store_row<T>(p, dsc.x + row / p.hpg, dsc.y * p.hpg + row % p.hpg, D, c * 8, mt, lt, PScale<T>::kLog2, acc, c == 0);
     }
     __syncthreads();                          // s_acc and s_l are read
   }
