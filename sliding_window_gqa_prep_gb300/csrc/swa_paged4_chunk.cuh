@@ -8,10 +8,15 @@
 //     vectors: with two tiles by the softmax warps, each between its weights and its next scores, V by those of
 //     the first tile and K by those of the second, who then find the slot free; at hd 256 by a warpgroup of
 //     its own. (Four more warps that did only this at hd 128 left the softmax threads 184 registers of the 220 that
-//     a row of S takes, and took their issue slots; both warpgroups with half a tile each waited for one another.)
+//     a row of S takes, and took their issue slots: 654 us where this takes 562; both warpgroups with half a tile each
+//     waited for one another: 638.)
 //   - all products are f16: codes * scale is exact there, q is scaled by a power of two a row.
 //   - tiles of keys that no row sees (between the sinks and the first row's window) are left
 //     out; a row's own limits are masks.
+// 4 chunks of up to 2048 rows over 2048 .. 16384 keys, 32 heads on 8, hd 128: 562 us, 1115 TFLOP/s (451 us without the
+// conversions). The tensor pipe is busy for 49 % of it (both operands of Q K^T come from shared memory), the issue slots for 50 %;
+// a tile's chain of scores, softmax and values has no second S buffer to hide in. (Two softmax warpgroups a query tile, half
+// a row each: 594. An eighth or a quarter of the exponentials as polynomials: 587, 617.)
 #pragma once
 #include "swa_paged4_attend.cuh"
 
