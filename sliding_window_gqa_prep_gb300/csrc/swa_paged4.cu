@@ -675,12 +675,10 @@ __global__ void __launch_bounds__(Split4Cfg<D, NV, VG, FS>::THREADS, Split4Cfg<D
 // ---------------------------------------------------------------------------
 // Keys that a row may see up to which a CTA takes a (sequence, KV head) whole: no scan over the
 // sequences and no second kernel. By the table's width (or the window), since the lengths are the device's.
-// Measured with one row of 4 vectors, whole against cut: 512 keys at hd 64 / 128 / 256, 32 items 6.9 / 7.7 / 12.0 us
-// against 9.5 / 9.3 / 13.0; 1024 keys, 32 items 9.3 / 10.7 / 19.0 against 9.7 / 9.5 / 13.9, 128 items 9.4 / 10.9 / 19.6
-// against 12.9 / 13.5 / 19.2.
-static long long whole_keys4(const swa_paged4_cache& c, long long sms) {
-  return c.hd == 64 || (c.hd == 128 && (long long)c.B * c.nk * 2 >= sms) ? 1024 : 512;
-}
+// Measured with one row of 8 vectors and one KV head, whole against cut, for 1, 16 and 64 sequences: 1024 keys at hd 128 9.6,
+// 10.3, 10.4 us against 9.9, 10.6, 12.1; at hd 256 768 keys 14.7, 15.8, 15.7 against 11.7, 15.2, 17.3, 1024 keys 16.3, 18.8,
+// 19.2 against 11.6, 15.2, 18.3. These are the GPU's times; called one by one from Python the cut form takes 19.
+static long long whole_keys4(int hd) { return hd == 256 ? 768 : 1024; }
 
 struct Split4Plan {
   int rows, whole, grid;       // query vectors of a block (0: no sequence for this kernel)
@@ -743,12 +741,11 @@ static void split4_plan(const swa_paged4_attend_args* a, long long vecs, Split4P
     const long long w = (long long)a->window + a->sinks + a->max_rows + 256;
     keys = w < keys ? w : keys;
   }
-  const long long sms = num_sms() > 0 ? num_sms() : 148;
-  sp->whole = keys <= whole_keys4(c, sms);
+  sp->whole = keys <= whole_keys4(c.hd);
   const int occ = sp->whole ? 0 : by_size4(c.hd, sp->rows, [](auto d, auto n, auto g, auto f) {
     return split4_occupancy<decltype(d)::value, decltype(n)::value, decltype(g)::value, decltype(f)::value>();
   });
-  sp->grid = sp->whole ? c.B * c.nk : (int)sms * occ;
+  sp->grid = sp->whole ? c.B * c.nk : (num_sms() > 0 ? num_sms() : 148) * occ;
   if (!sp->whole) {
     const size_t recs = (size_t)sp->grid * 2 * sp->rows;
     sp->off_ml = up256s(recs * c.hd * sizeof(float));
