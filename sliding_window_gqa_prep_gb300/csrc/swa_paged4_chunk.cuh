@@ -619,6 +619,15 @@ ChunkPlan chunk4_plan(const swa_paged4_attend_args* a, int max_rows) {
   }
   long long sp = sms / pl.items;
   if (sp > (tiles + 3) / 4) sp = (tiles + 3) / 4;
+  // About as many items as SMs: the longest sequence's CTA, or a second round of a few, would decide. Shares of 2560 keys at
+  // least, so that two of them fall to each SM (38 sequences of 21 or 40 rows, 16 heads on 4, 152 items: hd 256 over
+  // 3729 .. 12025 keys 306 us whole, 246 in two; 8000 keys each 225, 245; 160 items of 8000 keys 424, 346; hd 128, 80 items
+  // 178 whole, 118 in three; but 192 items of 2000 .. 4000 keys 117, 133)
+  if (pl.items * 3 <= sms * 4) {
+    long long even = (2 * sms + pl.items - 1) / pl.items;
+    if (even > tiles * kt / 2560) even = tiles * kt / 2560;
+    if (sp < even) sp = even;
+  }
   pl.splits = (int)(sp < 1 ? 1 : sp);
   if (pl.splits > 1) {
     const size_t recs = (size_t)pl.items * pl.splits * nt * 128;
