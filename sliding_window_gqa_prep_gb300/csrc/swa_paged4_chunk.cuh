@@ -6,10 +6,11 @@
 //   - a warp copies codes and scales as they are (4.5 bits a feature) into rings of their own. They
 //     become f16 operands, in the swizzled layout that the products read, once for the item's 256 query
 //     vectors: with two tiles by the softmax warps, each between its weights and its next scores, V by those of
-//     the first tile and K by those of the second, who then find the slot free; at hd 256 by a warpgroup of
-//     its own. (Four more warps that did only this at hd 128 left the softmax threads 184 registers of the 220 that
-//     a row of S takes, and took their issue slots: 654 us where this takes 562; both warpgroups with half a tile each
-//     waited for one another: 638.)
+//     the first tile and K by those of the second, who then find the slot free; at hd 256 by two warpgroups of
+//     their own, whose registers partly go to the softmax threads (38 sequences of 21 rows, 16 heads on 4, over 3729 .. 12025
+//     keys: 202 us; with one 227, and with a ring of codes for K and one for V 247; without conversions 184). (Four more
+//     warps that did only this at hd 128 left the softmax threads 184 registers of the 220 that a row of S takes, and took
+//     their issue slots: 654 us where this takes 562; both warpgroups with half a tile each waited for one another: 638.)
 //   - all products are f16: codes * scale is exact there, q is scaled by a power of two a row.
 //   - tiles of keys that no row sees (between the sinks and the first row's window) are left
 //     out; a row's own limits are masks.
@@ -29,11 +30,12 @@ struct Chunk4Cfg {
   static constexpr int RK = 2, RV = D == 64 ? 2 : 1;   // slots of K's and of V's codes and scales
   static constexpr int SLOT = KT * D * 2, CODES = KT * D / 2, RAW = CODES + KT * D / 16;   // operands: two slots for K, two for V
   static constexpr int QB = 128 * D * 2;
-  static constexpr int THREADS = NT * 128 + (OWN ? 128 : 256);   // softmax; loader, issuers, idle warps; conversion
+  static constexpr int CW = OWN ? 4 : 8;                // warps that convert a tile
+  static constexpr int THREADS = NT * 128 + 128 + (OWN ? 0 : 32 * CW);   // softmax; loader, issuers, idle warps; conversion
   static constexpr int SMEM = NT * QB + 4 * SLOT + (RK + RV) * RAW + 1024;   // + alignment
-  // Registers a thread at launch and after they moved to the softmax threads (two tiles)
-  static constexpr int REGS = NT == 2 ? 168 : 0, R_SOFT = 216, R_REST = 72;
-  static_assert(NT == 1 || NT * 128 * R_SOFT + 128 * R_REST <= THREADS * REGS, "registers of a CTA");
+  // Registers a thread at launch and after they moved to the softmax threads
+  static constexpr int REGS = NT == 2 ? 168 : 128, R_SOFT = NT == 2 ? 216 : 200, R_REST = NT == 2 ? 72 : 104;
+  static_assert(NT * 128 * R_SOFT + (THREADS - NT * 128) * R_REST <= THREADS * REGS, "registers of a CTA");
   static constexpr int C_O = NT * SB * KT;             // first O column
 };
 
@@ -71,10 +73,10 @@ __global__ void __launch_bounds__(Chunk4Cfg<D>::THREADS, 1) paged4_chunk_kernel(
     if (lane == 0) {
       for (int i = 0; i < RK + RV; ++i) {
         mbar_init(&b_raw[i], 1);
-        mbar_init(&b_free[i], 4);
+        mbar_init(&b_free[i], C::CW);
       }
       for (int i = 0; i < 4; ++i) {        // K tiles 0 and 1 modulo 2, V tiles
-        mbar_init(&b_full[i], 4);
+        mbar_init(&b_full[i], C::CW);
         mbar_init(&b_empty[i], NT);
       }
       for (int t = 0; t < NT; ++t) {
@@ -216,12 +218,12 @@ __global__ void __launch_bounds__(Chunk4Cfg<D>::THREADS, 1) paged4_chunk_kernel(
     }
     return ok;
   };
-  // tile x's slot of codes and the use of it
-  auto raw_slot = [&](int x, bool is_v) { return is_v ? RK + x % RV : x % RK; };
-  auto raw_use = [&](int x, bool is_v) { return is_v ? x / RV : x / RK; };
+  // tile x's slot of codes and the use of it: K's and V's own where different warps convert them, else all in their order
+  auto raw_slot = [&](int x, bool is_v) { return !C::OWN ? (2 * x + is_v) % (RK + RV) : is_v ? RK + x % RV : x % RK; };
+  auto raw_use = [&](int x, bool is_v) { return !C::OWN ? (2 * x + is_v) / (RK + RV) : is_v ? x / RV : x / RK; };
 
-  // Codes to operands: tile x by a warpgroup whose thread is wt, 32 features a thread at a time
-  constexpr int LR = D / 32, RP = 128 / LR;               // lanes of a key, keys of a pass
+  // Codes to operands: tile x by one or two warpgroups whose thread is wt, 32 features a thread at a time
+  constexpr int LR = D / 32, RP = 32 * C::CW / LR;        // lanes of a key, keys of a pass
   auto convert = [&](int wt, int x, bool is_v) {
     const int q = wt % LR, r0 = wt / LR, raw = raw_slot(x, is_v), slot = (is_v ? 2 : 0) + (x & 1), key0 = tl.at(j0 + x) * KT;
     // 16-byte chunk i of these 32 features goes to chunk 4 (q & 1) + i of its 64-feature half; lanes of
@@ -275,7 +277,7 @@ __global__ void __launch_bounds__(Chunk4Cfg<D>::THREADS, 1) paged4_chunk_kernel(
 
   // The softmax threads hold a row of S: registers move over to them.
   if (warp >= W_LOAD) {
-  if constexpr (NT == 2) regs_give<C::R_REST>();
+  regs_give<C::R_REST>();
   if (warp == W_LOAD) {
     // ------------------------------------------------------------ loader: a run of codes or of scales a lane
     const int page = 1 << a.map.page_shift, rows = min(page, KT), runs = KT / rows;   // 2 * runs <= 16
@@ -421,7 +423,7 @@ __global__ void __launch_bounds__(Chunk4Cfg<D>::THREADS, 1) paged4_chunk_kernel(
   }
   } else {
     // ------------------------------------------------------------ softmax: thread = row
-    if constexpr (NT == 2) regs_take<C::R_SOFT>();
+    regs_take<C::R_SOFT>();
     const int t = warp >> 2, r = tid & 127, hpg = a.hpg;
     const int first = tok0 + t * p.c.tile_tok;
     const int ntok = max(0, min(p.c.tile_tok, s.t - first)), nvec = ntok * hpg;
@@ -621,7 +623,7 @@ ChunkPlan chunk4_plan(const swa_paged4_attend_args* a, int max_rows) {
   if (sp > (tiles + 3) / 4) sp = (tiles + 3) / 4;
   // About as many items as SMs: the longest sequence's CTA, or a second round of a few, would decide. Shares of 2560 keys at
   // least, so that two of them fall to each SM (38 sequences of 21 or 40 rows, 16 heads on 4, 152 items: hd 256 over
-  // 3729 .. 12025 keys 306 us whole, 246 in two; 8000 keys each 225, 245; 160 items of 8000 keys 424, 346; hd 128, 80 items
+  // 3729 .. 12025 keys, when the kernel was slower, 306 us whole, 246 in two; 8000 keys each 225, 245; 160 items of 8000 keys 424, 346; hd 128, 80 items
   // 178 whole, 118 in three; but 192 items of 2000 .. 4000 keys 117, 133)
   if (pl.items * 3 <= sms * 4) {
     long long even = (2 * sms + pl.items - 1) / pl.items;

@@ -50,7 +50,7 @@ def test_exchange_of_scores():
 
 def chunk_run(NT, SB, RK, RV, mine, seed, last_but_one=True):
     """mine: key tiles that each query tile sees; the CTA's share n has the larger of them. With two query
-    tiles their softmax warps convert (V: the first's, K: the second's), else a warpgroup of its own."""
+    tiles their softmax warps convert (V: the first's, K: the second's), else warps of their own."""
     rng, n = random.Random(seed), max(mine)
     own = NT == 2
     raw, free = [Bar(1) for _ in range(RK + RV)], [Bar(1) for _ in range(RK + RV)]     # 4 warps: 1 here
@@ -69,7 +69,9 @@ def chunk_run(NT, SB, RK, RV, mine, seed, last_but_one=True):
                 yield x + 2, False
 
     def raw_of(x, is_v):
-        """(slot, use)"""
+        """(slot, use): K's and V's own rings where different warps convert them, else one"""
+        if not own:
+            return (2 * x + is_v) % (RK + RV), (2 * x + is_v) // (RK + RV)
         return (RK + x % RV, x // RV) if is_v else (x % RK, x // RK)
 
     def loader():
@@ -186,7 +188,7 @@ def test_chunk_kernel(D):
     assert "NT = ChunkCfg<D>::NT, SB = ChunkCfg<D>::SB" in text and "OWN = NT == 2;" in text
     NT, SB = (constant(base, x, D) for x in ("NT", "SB"))
     RK, RV = (constant(text, x, D) for x in ("RK", "RV"))
-    assert arrivals(text) == {"b_raw": "1", "b_free": "4", "b_full": "4", "b_empty": "NT", "b_q": "128", "b_pv": "1", "b_fin": "1",
+    assert arrivals(text) == {"b_raw": "1", "b_free": "C::CW", "b_full": "C::CW", "b_empty": "NT", "b_q": "128", "b_pv": "1", "b_fin": "1",
                               "b_turn": "1", "b_s": "1", "b_p": "128"}
     rng = random.Random(D)
     for seed in range(400):
@@ -204,7 +206,7 @@ def test_chunk_kernel_needs_its_wait_for_the_last_but_one_product():
 def test_register_shares_of_the_chunk_kernel_are_checked():
     """As for the 16-bit kernel: the shares that setmaxnreg hands out stand against the launch's."""
     text = source("swa_paged4_chunk.cuh")
-    assert re.search(r"static_assert\(NT == 1 \|\| NT \* 128 \* R_SOFT \+ 128 \* R_REST <= THREADS \* REGS", text)
+    assert re.search(r"static_assert\(NT \* 128 \* R_SOFT \+ \(THREADS - NT \* 128\) \* R_REST <= THREADS \* REGS", text)
     assert "regs_give<C::R_REST>()" in text and "regs_take<C::R_SOFT>()" in text
     assert re.search(r"allow_smem<paged4_chunk_kernel<D>>\([^;]*Chunk4Cfg<D>::REGS\)", text)
 
