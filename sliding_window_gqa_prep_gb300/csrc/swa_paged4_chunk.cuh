@@ -625,7 +625,9 @@ ChunkPlan chunk4_plan(const swa_paged4_attend_args* a, int max_rows) {
   // least, so that two of them fall to each SM (38 sequences of 21 or 40 rows, 16 heads on 4, 152 items: hd 256 over
   // 3729 .. 12025 keys, when the kernel was slower, 306 us whole, 246 in two; 8000 keys each 225, 245; 160 items of 8000 keys 424, 346; hd 128, 80 items
   // 178 whole, 118 in three; but 192 items of 2000 .. 4000 keys 117, 133)
-  if (pl.items * 3 <= sms * 4) {
+  // (One sequence's items are about equal: only where SMs would be left over. Where the keys are cut anyway twice as many shares
+  // cost more: 64 rows over 131072 keys, 8 items in 19, 138 us, in 38 177.)
+  if (sp < 2 && pl.items * 3 <= sms * 4 && (c.B > 1 || pl.items * 4 < sms * 3)) {
     long long even = (2 * sms + pl.items - 1) / pl.items;
     if (even > tiles * kt / 2560) even = tiles * kt / 2560;
     if (sp < even) sp = even;
