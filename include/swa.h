@@ -852,8 +852,11 @@ int swa_paged4_read(const swa_paged4_read_args* args, cudaStream_t stream);
  * Keys and values enter the products exactly; q is scaled by a power of two a
  * vector and rounded to f16 (bf16 and f16 values keep all bits down to 2^-39 of
  * the vector's largest); scores, maxima and sums are f32; the weights enter the
- * value product in f16, rounded once (relative 2^-11; below 2^-25 of the row's
- * largest to a multiple of 2^-35 of that).
+ * value product in f16: in calls of at most 16 query vectors a KV head and
+ * sequence (min(max_rows, T) * nh / nk) with an f16 or f32 out as their rounding
+ * and what it leaves (relative 2^-22 at most), in others rounded once (2^-11; a
+ * bf16 out is itself rounded by 2^-8). There are no bits below 2^-25: each weight
+ * also loses up to 2^-36 of its row's largest.
  *   q    [T][nh][hd] of type q_dtype (SWA_BF16 or SWA_F16), rows q_row elements
  *        apart (heads dense, rows at multiples of 16 bytes); nh / nk <= 32
  *   out  [T][nh][hd] dense, of q's type, or f32 with out_f32 = 1

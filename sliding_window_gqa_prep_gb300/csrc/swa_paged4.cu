@@ -14,7 +14,7 @@
 //     the lower (upper) halves of two keys' bytes are put into one byte before the conversion.
 //   P^T comes out of S^T by movmatrix: 8 x 8 transposed, in registers.
 // A value code * scale is exact in f16. Weights enter the second product in f16, scaled by
-// 2^(kLog24 + up to kLazy4) so that small ones keep their bits.
+// 2^(kLog24 + up to kLazy4) so that small ones keep their bits, with what that rounding leaves where the result shows it.
 // Every CTA gets the same share of the whole call's tiles and items' starts, wherever the cuts fall; one warp copies
 // them from the pages (plain bulk copies: a head's keys of a page are consecutive), the others take
 // a quarter of a tile's keys each (or half, for half of the vectors or features), with a running maximum and
@@ -24,7 +24,7 @@
 // The copies alone take 65, the products with the conversions 73: some 300 instructions of a warp for 16 keys, at 0.6 a clk
 // of each of the SM's four schedulers. (Where the call took 85 us, four CTAs an SM with 96 registers took 95, by what no
 // longer fits; four CTAs without a warp that copies, the last to read a stage refilling it, 101.)
-// 32 times 16 vectors (4 drafts) over a window of 4096 keys, 4 KV heads of hd 256 (153 MB): 62 us; copies alone 39, products 59.
+// 32 times 16 vectors (4 drafts) over a window of 4096 keys, 4 KV heads of hd 256 (153 MB): 62 us, 73 with the rest of f16 weights; copies alone 39, products 59.
 #include <cmath>
 
 #include "swa_paged4_attend.cuh"
@@ -155,7 +155,14 @@ __device__ __forceinline__ Tiles4 split4_tiles(const PagedSeq& s, const Attend4P
   return key_tiles(s, p, kt);
 }
 
-template <int D, int NV, int VG, int FS>
+// REST: what the weights' rounding to f16 leaves enters the value product too, and a weight is off by 2^-22, not 2^-11. For
+// results in f16 and f32: with one rounding 64 tokens (32 drafts of 4 under a window) in f16 were 2.33e-4 (2.36e-4) of
+// the norm from 64 bits, with the rest 2.07e-4 (2.09e-4), as with weights of 32 bits. A result in bf16 is itself rounded
+// by 2^-8, and is 1.65e-3 away in all of these.
+//   1: in a second product with the same V. 64 x 1024 .. 8192 keys, 32 heads on 8: 78.6 -> 88.3 us; drafts 62.9 -> 72.8
+//   2: up to four vectors: in the columns 4 .. 7 of the product, whose scores are those of columns 0 .. 3. 78.6 -> 81.3 us
+// Blocks of 32 vectors, and the chunk kernel, round once: a second product would cost them more than that.
+template <int D, int NV, int VG, int FS, int REST>
 __global__ void __launch_bounds__(Split4Cfg<D, NV, VG, FS>::THREADS, Split4Cfg<D, NV, VG, FS>::CTAS)
     paged4_split_kernel(const __grid_constant__ Attend4Params p) {
   using C = Split4Cfg<D, NV, VG, FS>;
@@ -351,7 +358,7 @@ __global__ void __launch_bounds__(Split4Cfg<D, NV, VG, FS>::THREADS, Split4Cfg<D
     float qm[NV][2];
     int lim[NV][2];
     auto query = [&](int tile, int part, uint32_t (&q)[KS][2]) {      // of 8 vectors; the inverse scale of vector lg
-      const int r = tile * 8 + lg;
+      const int r = REST == 2 ? lg & 3 : tile * 8 + lg;
       const bool in = r < nvec;
       const int i = in ? row_of(r) : 0, h = in ? r - i * hpg : 0;
       return load_query4<D, FS>(p, (long long)(s.r0 + i) * a.q_row + (long long)(g * hpg + h) * D, in, lt, part, q);
@@ -372,7 +379,7 @@ __global__ void __launch_bounds__(Split4Cfg<D, NV, VG, FS>::THREADS, Split4Cfg<D
       if constexpr (!QS) shift = query(vg * NV + v, fs, qf[v]);
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
-        const int c = (vg * NV + v) * 8 + 2 * lt + e;
+        const int c = REST == 2 ? 2 * (lt & 1) + e : (vg * NV + v) * 8 + 2 * lt + e;
         if constexpr (QS) shift = s_shift[c];
         qm[v][e] = fmaxf(a.qmul * (QS ? shift : __shfl_sync(0xffffffffu, shift, (2 * lt + e) * 4)), 0x1p-126f);   // masked scores stay -inf
         lim[v][e] = c < nvec ? max(0, min(s.len, s.len - s.t + row_of(c) + 1)) : 0;
@@ -550,7 +557,7 @@ __global__ void __launch_bounds__(Split4Cfg<D, NV, VG, FS>::THREADS, Split4Cfg<D
               }
             }
         }
-        uint32_t pf[G][NV][2], vs[G][2];
+        uint32_t pf[G][NV][2], pr[G][REST == 1 ? NV : 1][2], vs[G][2];
 #pragma unroll
         for (int y = 0; y < G; ++y) {
 #pragma unroll
@@ -561,8 +568,18 @@ __global__ void __launch_bounds__(Split4Cfg<D, NV, VG, FS>::THREADS, Split4Cfg<D
               e[i] = ex2(fmaf(sc[y][v][i], qm[v][i & 1], off[v][i & 1]));
               l[v][i & 1] += e[i];
             }
-            pf[y][v][0] = movmatrix(pack2(e[0], e[1], (const __half*)nullptr));
-            pf[y][v][1] = movmatrix(pack2(e[2], e[3], (const __half*)nullptr));
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+              uint32_t w = pack2(e[2 * i], e[2 * i + 1], (const __half*)nullptr), rest = 0;
+              if constexpr (REST > 0) {
+                float h0, h1;
+                unpack2(w, h0, h1, (const __half*)nullptr);
+                rest = pack2(e[2 * i] - h0, e[2 * i + 1] - h1, (const __half*)nullptr);
+              }
+              if (REST == 2 && lt >= 2) w = rest;
+              pf[y][v][i] = movmatrix(w);
+              if constexpr (REST == 1) pr[y][v][i] = movmatrix(rest);
+            }
           }
 #pragma unroll
           for (int h = 0; h < 2; ++h) vs[y][h] = e4m3x2_f16x2(__byte_perm(u1[y][h], u2[y][h], 0x0040));
@@ -574,7 +591,10 @@ __global__ void __launch_bounds__(Split4Cfg<D, NV, VG, FS>::THREADS, Split4Cfg<D
             const uint32_t f[4] = {hmul2(codes_pair<J>(lo[y][0]), vs[y][0]), hmul2(codes_pair<J>(hi[y][0]), vs[y][0]),
                                    hmul2(codes_pair<J>(lo[y][1]), vs[y][1]), hmul2(codes_pair<J>(hi[y][1]), vs[y][1])};
 #pragma unroll
-            for (int v = 0; v < NV; ++v) mma_f16<false>(o[v][J], f, pf[y][v][0], pf[y][v][1]);
+            for (int v = 0; v < NV; ++v) {
+              mma_f16<false>(o[v][J], f, pf[y][v][0], pf[y][v][1]);
+              if constexpr (REST == 1) mma_f16<false>(o[v][J], f, pr[y][v][0], pr[y][v][1]);
+            }
           });
       }
       __syncwarp();
@@ -594,6 +614,12 @@ __global__ void __launch_bounds__(Split4Cfg<D, NV, VG, FS>::THREADS, Split4Cfg<D
         for (int d = 4; d < 32; d <<= 1) l[v][e] += __shfl_xor_sync(0xffffffffu, l[v][e], d);
         if (lg == 0) s_ml[warp][v * 8 + 2 * lt + e] = make_float2(seen[v] >> e & 1 ? kLog24 - off[v][e] : -INFINITY, l[v][e]);
       }
+    if constexpr (REST == 2) {              // the rest's columns join their vectors'
+#pragma unroll
+      for (int j = 0; j < KS; ++j)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) o[0][j][e] += __shfl_xor_sync(0xffffffffu, o[0][j][e], 2);
+    }
     const bool whole = tile0 == 0 && tile1 == tl.n;
     // record of the item this CTA continues: slot 2c, of the one it starts: 2c + 1
     const size_t rec = ((size_t)blockIdx.x * 2 + (tile0 == 0 ? 1 : 0)) * p.rows;
@@ -681,7 +707,7 @@ __global__ void __launch_bounds__(Split4Cfg<D, NV, VG, FS>::THREADS, Split4Cfg<D
 static long long whole_keys4(int hd) { return hd == 256 ? 768 : 1024; }
 
 struct Split4Plan {
-  int rows, whole, grid;       // query vectors of a block (0: no sequence for this kernel)
+  int rows, vecs, whole, grid; // query vectors of a block (0: no sequence for this kernel), and those that sequences have at most
   size_t off_ml, off_desc, bytes;
 };
 
@@ -691,9 +717,9 @@ static int split4_occupancy() {
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return 1;
   if (!cache[dev]) {
-    auto k = paged4_split_kernel<D, NV, VG, FS>;
+    auto k = paged4_split_kernel<D, NV, VG, FS, 0>;   // (the other form has the same bounds)
     int n = 0;
-    if (allow_smem<paged4_split_kernel<D, NV, VG, FS>>(Split4Cfg<D, NV, VG, FS>::SMEM) != cudaSuccess ||
+    if (allow_smem<paged4_split_kernel<D, NV, VG, FS, 0>>(Split4Cfg<D, NV, VG, FS>::SMEM) != cudaSuccess ||
         cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, k, Split4Cfg<D, NV, VG, FS>::THREADS, Split4Cfg<D, NV, VG, FS>::SMEM) != cudaSuccess || n < 1) {
       (void)cudaGetLastError();
       n = 1;
@@ -703,11 +729,11 @@ static int split4_occupancy() {
   return cache[dev];
 }
 
-template <int D, int NV, int VG, int FS>
+template <int D, int NV, int VG, int FS, int REST>
 static int launch_split4(const Attend4Params& p, const Split4Plan& sp, cudaStream_t s) {
-  const cudaError_t e = allow_smem<paged4_split_kernel<D, NV, VG, FS>>(Split4Cfg<D, NV, VG, FS>::SMEM);
+  const cudaError_t e = allow_smem<paged4_split_kernel<D, NV, VG, FS, REST>>(Split4Cfg<D, NV, VG, FS>::SMEM);
   if (e != cudaSuccess) return cuda_status(e);
-  const int rc = finish_launch(launch_pdl(paged4_split_kernel<D, NV, VG, FS>, dim3(sp.grid), dim3(Split4Cfg<D, NV, VG, FS>::THREADS),
+  const int rc = finish_launch(launch_pdl(paged4_split_kernel<D, NV, VG, FS, REST>, dim3(sp.grid), dim3(Split4Cfg<D, NV, VG, FS>::THREADS),
                                           Split4Cfg<D, NV, VG, FS>::SMEM, s, p));
   if (rc != SWA_OK || p.a.whole) return rc;
   // a block a row up to 16, which then take rows in turn: most of sp.grid's columns are empty
@@ -735,6 +761,7 @@ static int split4_vecs(int hd) { return hd == 256 ? 16 : 32; }
 static void split4_plan(const swa_paged4_attend_args* a, long long vecs, Split4Plan* sp) {
   const swa_paged4_cache& c = a->cache;
   *sp = Split4Plan{};
+  sp->vecs = (int)vecs;
   sp->rows = vecs <= 8 ? 8 : vecs <= 16 ? 16 : 32;
   long long keys = (long long)c.max_pages * c.page;
   if (a->window) {
@@ -851,7 +878,14 @@ int swa_paged4_attend(const swa_paged4_attend_args* a, cudaStream_t stream) {
     pa.ws_ml = reinterpret_cast<float2*>(ws + pl.split.off_ml);
     pa.ws_desc = reinterpret_cast<int4*>(ws + pl.split.off_desc);
     rc = by_size4(c.hd, pl.split.rows, [&](auto d, auto n, auto g, auto f) {
-      return launch_split4<decltype(d)::value, decltype(n)::value, decltype(g)::value, decltype(f)::value>(p, pl.split, stream);
+      constexpr int D = decltype(d)::value, NV = decltype(n)::value, VG = decltype(g)::value, FS = decltype(f)::value;
+      if constexpr (NV * VG <= 2)
+        if (!p.bf || pa.out_f32) {
+          if constexpr (NV == 1)
+            if (pl.split.vecs <= 4) return launch_split4<D, NV, VG, FS, 2>(p, pl.split, stream);
+          return launch_split4<D, NV, VG, FS, 1>(p, pl.split, stream);
+        }
+      return launch_split4<D, NV, VG, FS, 0>(p, pl.split, stream);
     });
     if (rc != SWA_OK) return rc;
   }
