@@ -585,7 +585,7 @@ __global__ void __launch_bounds__(128) chunk_merge_kernel(const ChunkParams p) {
   for (int i = 0; i < p.splits; ++i) {
     const size_t rec = rec0 + (size_t)i * NT * 128;
     const float2 ml = p.rec_ml[rec];
-    if (ml.x == -INFINITY) continue;
+    if (ml.y == 0.f) continue;             // the row sees no key of it (with NaN keys alone m is -inf too, but l NaN)
     const float f = ex2(ml.x - m);
     float y[8];
     load8(p.rec_acc + rec * D + c * 8, y);
