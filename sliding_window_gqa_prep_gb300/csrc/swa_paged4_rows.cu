@@ -49,9 +49,11 @@ struct AppendCfg {
   static constexpr int LANES = HD / kE, ROWS_WARP = 32 / LANES;   // of a head; rows that a warp takes at once
   static constexpr int ROWS = HD == 64 ? 8 : 4;                   // most rows of a block
 };
-// sincospif is good to an ulp (2^-24), the step by what the angle's f32 leaves to 2^-25, mag to 2^-25, the two
-// products' roundings 2^-25 each: 1.8e-7 of |u| + |v|, times mag.
-constexpr float kTol = 0x1p-22f;
+// How far a rotated value, the quotients made of it and the ends of their interval may be off in f32, in all and at most, as
+// a part of |u| + |v| (times mag), in units of 2^-24: sincospif an ulp (1), the step that adds what the angle's f32 lacks 0.5,
+// mag 1, the product and the fused sum 1 each: 4.5. For codes the quotient and an end, which has to pass the border: 3. For scales
+// an end's sum, 1 / 6, the product with it, and passing the border: 5. (tests/test_paged4_encoding_cpu.py)
+constexpr float kTol = 0x1.4p-21f;       // 10 of these
 
 // The last b with row_start[b] <= row (0 if none), by a whole warp: 32 probes a step.
 __device__ __forceinline__ int find_seq4(const int32_t* row_start, int B, int row) {
