@@ -335,14 +335,13 @@ __global__ void __launch_bounds__(kRThreads, sizeof(TI) == 2 ? 4 : 3) paged4_app
     const long long at = at_of(i);
     float x[kE], b[kE], y[kE];
     rotate(r, raw, static_cast<const TI*>(p.k) + (row0 + r) * p.k_row + (long long)g * HD, x, b, y);
-    const Scale s = scale_of(y, p.k_div);
+    Scale s = scale_of(y, p.k_div);
     // how far y may be from the rotated value; at position 0 it is that
     const int pos = p.rot ? p.pos[row0 + r] : 0;
-    float tol = 0.f;
+    float t = 0.f;                                       // |u| + |v| is 2 t at most; NaN where one is
 #pragma unroll
-    for (int j = 0; j < kE; ++j)
-      if (PAIRS == 0 || pair_of(j) >= 0) tol = fmaxf(tol, fabsf(x[j]) + fabsf(b[j]));
-    tol = (pos == 0 && p.mag == 1.f) || f0 >= p.rot ? 0.f : tol * (kTol * fabsf(p.mag) * p.k_div);
+    for (int j = 0; j < kE; j += 1 + (PAIRS == 1)) t = nan_max(t, fabsf(x[j]), fabsf(PAIRS == 1 ? x[j + 1] : b[j]));
+    const float tol = (pos == 0 && p.mag == 1.f) || f0 >= p.rot ? 0.f : t * (2.f * kTol * fabsf(p.mag) * p.k_div);
     float tol_top = tol;
 #pragma unroll
     for (int o = 1; o < L; o <<= 1) tol_top = fmaxf(tol_top, __shfl_xor_sync(0xffffffffu, tol_top, o));
@@ -355,8 +354,18 @@ __global__ void __launch_bounds__(kRThreads, sizeof(TI) == 2 ? 4 : 3) paged4_app
       y[j] -= d;
     }
     uint32_t codes = codes_of(y), scale = s.bits;
+    const bool two = codes != codes_of(hi);
+    if (__any_sync(0xffffffffu, s.bad)) {                // an infinity or NaN, or finite features whose rotation passes f32's range: open
+#pragma unroll
+      for (int o = 1; o < L; o <<= 1) t = nan_max(t, __shfl_xor_sync(0xffffffffu, t, o), t);
+      if (s.bad && t < INFINITY) {
+        s.bad = false;
+        s.top = 0.f;
+        tol_top = INFINITY;
+      }
+    }
     const bool open = at >= 0 && !s.bad && tol_top > 0.f &&
-                      (codes != codes_of(hi) || f32_e4m3((s.top - tol_top) * (1.f / 6.f)) != f32_e4m3((s.top + tol_top) * (1.f / 6.f)));
+                      (two || f32_e4m3((s.top - tol_top) * (1.f / 6.f)) != f32_e4m3((s.top + tol_top) * (1.f / 6.f)));
     const unsigned any = __ballot_sync(0xffffffffu, open);
     if (any) {
       int e[kE];

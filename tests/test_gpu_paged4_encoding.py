@@ -136,3 +136,27 @@ def test_append_rotated_next_to_borders_of_scales_and_codes(inter, mag):
     k[..., first] = ((want[..., first] + k[..., second].double() * sn) / safe).float()
     bt = Cache([T], [T], 1, hd, 64, seed=29)
     append_and_check(bt, 0, FP, rot, inter, mag, BF, pos, (None, k, k))
+
+
+@pytest.mark.parametrize("src", [FP, BF])
+def test_append_of_finite_keys_near_the_largest(src):
+    """Finite keys and values near the type's largest: a rotation whose f32 result passes the range is no
+    infinity, it takes the largest scale. An infinity or NaN still makes its pair's blocks NaN."""
+    hd = rot = 64
+    T = 300
+    g = torch.Generator(device="cuda").manual_seed(30)
+    big = float(torch.finfo(src).max)
+    k = (torch.rand(T, 2, hd, generator=g, device="cuda") * 2 - 1) * big
+    k[:100] = big
+    k[100:200] = torch.where(torch.rand(100, 2, hd, generator=g, device="cuda") < 0.5, -big, big)
+    k[200:, :, :20] *= 1e-30
+    k = k.to(src).clamp(-big, big)
+    pos = torch.randint(0, 60000, (T,), generator=g, device="cuda", dtype=torch.int32)
+    pos[::7] = 0
+    for inter, mag in ((False, 1.0), (True, 1.0), (False, 1.5), (True, 2.0 ** 100)):
+        bt = Cache([T], [T + 3], 2, hd, 64, seed=31, exps=(20, 32))
+        append_and_check(bt, 0, src, rot, inter, mag, BF, pos, (None, k, k))
+        assert not (bt.pools[1].view(U8)[bt.table[0].long()[:4]] == 127).any()
+    k[5, 0, 3], k[6, 1, 40], k[250, 0, 63] = float("inf"), float("nan"), float("-inf")
+    bt = Cache([T], [T], 2, hd, 64, seed=31, exps=(20, 32))
+    append_and_check(bt, 0, src, rot, False, 1.0, BF, pos, (None, k, k))
