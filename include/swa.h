@@ -923,7 +923,8 @@ typedef struct swa_page_pools {
  *         max_pages * page are clamped, SWA_DERR_META)
  *   parent [R], room [R] or NULL i32: a parent outside -1 .. B - 1 is taken as -1,
  *         room below 0 as 0, room past the table's width as that (SWA_DERR_META)
- *   refs [num_pages] i32; refs_out may be refs itself. A count that falls below 0
+ *   refs [num_pages] i32; refs_out may be refs itself (with pools some microseconds
+ *         more). A count that falls below 0
  *         is no free page (SWA_DERR_META). An entry of the old table that should
  *         hold a key's page and names none is passed on as -1 (SWA_DERR_PAGE).
  *   table_out [R][max_pages], lens_out [R], refs_out [num_pages] i32

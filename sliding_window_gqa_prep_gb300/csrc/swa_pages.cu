@@ -4,7 +4,7 @@
 // Both are integer work over the tables and the counts, a few passes with sums in between,
 // and then copies of whole pages. The passes are bound by latency, not by what they read, the copies by
 // memory. Where the counts fit in shared memory and the tables are short, one launch does everything: every SM's CTA
-// makes the passes for itself, the first one writes the outputs, and each copies its share (waiting for
+// makes the passes for itself, the first one writes the outputs (counts in place: the last one), and each copies its share (waiting for
 // another launch, or for the other SMs, would take longer than the passes). Otherwise one cluster of 8 CTAs
 // makes them in global memory, with the cluster's barrier (which orders it among them) in place of the block's, and a
 // second launch copies from the list that it leaves in the workspace.
@@ -49,7 +49,7 @@ struct ForkParams {
   int* open_page;                      // [R]: the page that the sequence writes next, if it has begun, or -1
   int2* copies;                        // [R]
   int* count;
-  int apart;                           // refs and refs_out are two arrays
+  int in_place;                        // refs_out is refs, and more than one CTA reads it
   uint32_t* err;
   PageCopies pages;
 };
@@ -66,7 +66,7 @@ struct CompactParams {
   int* refs_moved;                     // [num_pages] counts of the pages that move
   int2* copies;                        // [num_pages]
   int* count;
-  int apart;                           // refs and refs_out are two arrays
+  int in_place;                        // refs_out is refs, and more than one CTA reads it
   uint32_t* err;
   PageCopies pages;
 };
@@ -162,9 +162,19 @@ __device__ __forceinline__ void copy_pages(const PageCopies& p, const int2* list
   }
 }
 
-// In one launch, counts that are written in place are not written before every CTA has read them.
-__device__ __forceinline__ void all_have_read(int apart) {
-  if (!apart) cg::this_grid().sync();
+// Whether this CTA writes the counts (all have the same): the first one, or with the counts in place the last that has
+// read them, by a ticket that was set to 0. No CTA waits for another.
+__device__ __forceinline__ bool writes_counts(int in_place, int32_t* ticket) {
+  if (!in_place) return blockIdx.x == 0;
+  __shared__ int s_last;
+  __syncthreads();
+  if (threadIdx.x == 0) {
+    __threadfence();
+    s_last = atomicAdd(ticket, 1) == (int)gridDim.x - 1;
+    __threadfence();
+  }
+  __syncthreads();
+  return s_last;
 }
 
 template <bool ONE>
@@ -344,16 +354,17 @@ __global__ void __launch_bounds__(Ctas<ONE>::THREADS) paged_fork_kernel(const __
       if (writes) row[first + i] = e;
     }
   }
-  if (me == 0 && writes) {
+  if (!ONE && me == 0) {
     *p.left = free_all.x - need_all.x;
-    if (!ONE) *p.count = need_all.y;
+    *p.count = need_all.y;
   }
   if (bits && writes) set_err(p.err, bits);
   if constexpr (ONE) {
-    all_have_read(p.apart);
     __syncthreads();
-    if (writes)
+    if (writes_counts(p.in_place, p.left)) {
       for (int i = tid; i < p.num_pages; i += C::THREADS) p.refs_out[i] = counts[i];
+      if (tid == 0) *p.left = free_all.x - need_all.x;
+    }
     constexpr int G = C::THREADS / kCopyThreads;
     copy_pages(p.pages, copies, need_all.y, blockIdx.x * G + tid / kCopyThreads, gridDim.x * G, tid % kCopyThreads);
   }
@@ -435,18 +446,16 @@ __global__ void __launch_bounds__(Ctas<ONE>::THREADS) paged_compact_kernel(const
     k.y += step.y;
   }
   C::sync();
-  if (ONE) {
-    all_have_read(p.apart);            // writes of the counts follow
-    if (writes)
-      for (int i = tid; i < p.num_pages; i += C::THREADS) {
-        const int c = refs[i];
-        if (!kind(i, c).x && !kind(i, c).y) p.refs_out[i] = c;
-      }
-  }
+  const bool writes_refs = !ONE || writes_counts(p.in_place, p.used);
+  if (ONE && writes_refs)
+    for (int i = tid; i < p.num_pages; i += C::THREADS) {
+      const int c = refs[i];
+      if (!kind(i, c).x && !kind(i, c).y) p.refs_out[i] = c;
+    }
   for (int x = me; x < lists_all.y; x += all) {
     const int2 c = copies[x];
     moved[c.x] = c.y;
-    if (writes) {
+    if (writes_refs) {
       p.refs_out[c.y] = refs_moved[x];
       p.refs_out[c.x] = 0;
     }
@@ -463,12 +472,10 @@ __global__ void __launch_bounds__(Ctas<ONE>::THREADS) paged_compact_kernel(const
     }
     if (ONE)
       for (int i = tid; i < p.num_pages; i += C::THREADS) p.moved[i] = moved[i];
-    if (me == 0) {
-      *p.used = n;
-      if (!ONE) *p.count = lists_all.y;
-    }
+    if (!ONE && me == 0) *p.count = lists_all.y;
     if (bits) set_err(p.err, bits);
   }
+  if (writes_refs && me == 0) *p.used = n;
   if constexpr (ONE) {
     constexpr int G = C::THREADS / kCopyThreads;
     copy_pages(p.pages, copies, lists_all.y, blockIdx.x * G + tid / kCopyThreads, gridDim.x * G, tid % kCopyThreads);
@@ -527,25 +534,18 @@ static PageCopies copies_of(const swa_page_pools& c) {
   return p;
 }
 
-// One launch of a CTA an SM with `smem` bytes of shared memory (`most` at most), cooperative where they have to wait
-// for each other
+// One launch of a CTA an SM with `smem` bytes of shared memory (`most` at most). With the counts in place `ticket`, an output, is
+// set to 0 before it. (A grid that waits for itself needs every SM at once: it starts when no other stream holds one, and
+// not at all where a process has fewer. Of 64 beams, and 32 prompts continued eight ways, on the GPU: apart 9.5 and 20.0 us, in place
+// 14.9 and 25.4, with a second launch for the counts 16.7 and 29.6, as a grid that waits 11.0 and 21.4.)
 template <auto One, typename P>
-static int launch_one(size_t smem, int most, const P& p, cudaStream_t s) {
+static int launch_one(size_t smem, int most, P& p, bool in_place, int32_t* ticket, cudaStream_t s) {
   cudaError_t e = allow_smem<One>(most);
   if (e != cudaSuccess) return cuda_status(e);
   const dim3 grid(p.pages.pools ? (num_sms() > 0 ? num_sms() : 148) : 1);
-  if (p.apart) return finish_launch(launch_pdl(One, grid, dim3(kOneThreads), smem, s, p));
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = grid;
-  cfg.blockDim = dim3(kOneThreads);
-  cfg.dynamicSmemBytes = smem;
-  cfg.stream = s;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeCooperative;
-  attr[0].val.cooperative = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  return finish_launch(cudaLaunchKernelEx(&cfg, One, p));
+  p.in_place = in_place && grid.x > 1;
+  if (p.in_place && (e = cudaMemsetAsync(ticket, 0, sizeof(int32_t), s)) != cudaSuccess) return cuda_status(e);
+  return finish_launch(launch_pdl(One, grid, dim3(kOneThreads), smem, s, p));
 }
 // The passes on a cluster, then the copies of at most `most` pages
 template <auto Many, typename P>
@@ -647,12 +647,11 @@ int swa_paged_fork(const swa_paged_fork_args* a, cudaStream_t stream) {
   p.width_inv = a->max_pages > 1 ? ~0ull / a->max_pages + 1 : 0;
   p.table = a->table; p.lens = a->lens; p.parent = a->parent; p.room = a->room; p.refs = a->refs;
   p.table_out = a->table_out; p.lens_out = a->lens_out; p.refs_out = a->refs_out; p.left = a->left;
-  p.apart = a->refs != a->refs_out;
   p.err = a->err;
   p.pages = copies_of(a->pools);
   if (w.one)
     return launch_one<paged_fork_kernel<true>>((size_t)p.num_pages * 16 + (size_t)p.R * 24 + (size_t)p.B * 8,
-                                               kOnePages * 16 + kOneSeqs * 32, p, stream);
+                                               kOnePages * 16 + kOneSeqs * 32, p, a->refs == a->refs_out, a->left, stream);
   char* ws = static_cast<char*>(a->workspace);
   p.children = reinterpret_cast<int*>(ws);
   p.opens = reinterpret_cast<int2*>(ws + w.opens);
@@ -692,11 +691,11 @@ int swa_paged_compact(const swa_paged_compact_args* a, cudaStream_t stream) {
   p.entries = (long long)entries;
   p.table = a->table; p.refs = a->refs;
   p.table_out = a->table_out; p.refs_out = a->refs_out; p.moved = a->moved; p.used = a->used;
-  p.apart = a->refs != a->refs_out;
   p.err = a->err;
   p.pages = copies_of(a->pools);
   if (w.one)
-    return launch_one<paged_compact_kernel<true>>((size_t)p.num_pages * 8 + (size_t)((p.num_pages + 1) / 2) * 12, kOnePages * 14, p, stream);
+    return launch_one<paged_compact_kernel<true>>((size_t)p.num_pages * 8 + (size_t)((p.num_pages + 1) / 2) * 12, kOnePages * 14, p,
+                                                  a->refs == a->refs_out, a->used, stream);
   char* ws = static_cast<char*>(a->workspace);
   p.refs_moved = reinterpret_cast<int*>(ws);
   p.copies = reinterpret_cast<int2*>(ws + w.copies);
