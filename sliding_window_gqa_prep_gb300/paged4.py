@@ -206,7 +206,7 @@ def _pools(pools, num_pages, dev):
         if p.get_device() != dev or not p.is_contiguous():
             _complain(p, f"pools[{len(base)}]", dev, p.dtype, None)
         base.append(p.data_ptr())
-        size.append(p.nbytes // num_pages)
+        size.append(p.nbytes // max(num_pages, 1))           # (the call refuses pools without pages)
     rest = [0] * (_abi.SWA_MAX_POOLS - n)
     return (num_pages, n, *base, *rest, *size, *rest)
 
