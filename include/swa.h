@@ -921,8 +921,9 @@ typedef struct swa_page_pools {
  * SWA_DERR_FULL is set; what is there is consistent.
  *   table [B][max_pages], lens [B] i32: the old batch (lengths outside 0 ..
  *         max_pages * page are clamped, SWA_DERR_META)
- *   parent [R], room [R] or NULL i32: a parent outside -1 .. B - 1 is taken as -1,
- *         room below 0 as 0, room past the table's width as that (SWA_DERR_META)
+ *   parent [R], room [R] or NULL i32: a parent outside -1 .. B - 1 is taken as -1
+ *         and room past the table's width as that (SWA_DERR_META both); room below 0
+ *         is 0
  *   refs [num_pages] i32; refs_out may be refs itself (with pools some microseconds
  *         more). A count that falls below 0
  *         is no free page (SWA_DERR_META). An entry of the old table that should

@@ -51,8 +51,9 @@ struct Split4Cfg {
   static constexpr int ROWS = 8 * NV * VG;                  // query vectors
   static constexpr int DW = D / FS;                         // features of a warp
   static constexpr bool QS = NV * DW > 128;                 // Q^T waits in shared memory, not in registers
-  // CTAs an SM: 96 registers a thread for four, 128 for three, 168 for two (NV = 2 with 128 features spills with 128:
-  // 16 vectors over 32 x 6144 keys, 8 KV heads, 93 us with three, 85 with two)
+  // CTAs an SM: 96 registers a thread for four, 128 for three, 168 for two. All forms spill a little within these (16 to 164 bytes a
+  // thread stored, 28 to 304 loaded); NV = 2 with 128 features spills more with 128: 16 vectors over 32 x 6144 keys, 8 KV
+  // heads, 93 us with three, 85 with two
   static constexpr int CTAS = DW == 64 ? 5 - NV : 4 - NV;
   static constexpr int G = 2;                               // groups of 16 keys that a warp takes at a time (one: 64 x 1024 .. 8192
                                                             // keys, 4 vectors, hd 128, 89 us; two: 85)

@@ -16,7 +16,8 @@
 //     out; a row's own limits are masks.
 // 4 chunks of up to 2048 rows over 2048 .. 16384 keys, 32 heads on 8, hd 128: 562 us, 1115 TFLOP/s (451 us without the
 // conversions). The tensor pipe is busy for 49 % of it (both operands of Q K^T come from shared memory), the issue slots for 50 %;
-// a tile's chain of scores, softmax and values has no second S buffer to hide in. (Two softmax warpgroups a query tile, half
+// a tile's chain of scores, softmax and values has no second S buffer to hide in, and at hd 64 and 128 the softmax threads spill (48
+// and 60 bytes stored, 232 and 344 loaded). (Two softmax warpgroups a query tile, half
 // a row each: 594. An eighth or a quarter of the exponentials as polynomials: 587, 617.)
 #pragma once
 #include "swa_paged4_attend.cuh"
@@ -622,9 +623,13 @@ ChunkPlan chunk4_plan(const swa_paged4_attend_args* a, int max_rows) {
   long long sp = sms / pl.items;
   if (sp > (tiles + 3) / 4) sp = (tiles + 3) / 4;
   // About as many items as SMs: the longest sequence's CTA, or a second round of a few, would decide. Shares of 2560 keys at
-  // least, so that two of them fall to each SM (38 sequences of 21 or 40 rows, 16 heads on 4, 152 items: hd 256 over
-  // 3729 .. 12025 keys, when the kernel was slower, 306 us whole, 246 in two; 8000 keys each 225, 245; 160 items of 8000 keys 424, 346; hd 128, 80 items
-  // 178 whole, 118 in three; but 192 items of 2000 .. 4000 keys 117, 133)
+  // least, so that two of them fall to each SM. The host knows no lengths, so that this gains where a second round would be
+  // a few items of full length, and loses where lengths differ and even that round out. 16 heads on 4, whole / cut, us:
+  //   152 items (38 sequences; 21 rows at hd 256, 40 below)  3729 .. 12025 keys  hd 256 238 / 209, 128 185 / 171, 64 152 / 134
+  //                                                          8000 keys each      hd 256 165 / 193, 128 132 / 156
+  //   160 and 200 items   8000 keys each      hd 256 319 / 269, 322 / 278   128 256 / 225, 258 / 230   64 209 / 175, 211 / 179
+  //                       3729 .. 12025 keys  hd 256 237 / 246, 253 / 292   128 190 / 206, 218 / 246   64 157 / 158, 180 / 194
+  //   80 items            3729 .. 12025 keys  128 181 / 119 (in three), 64 149 / 93
   // (One sequence's items are about equal: only where SMs would be left over. Where the keys are cut anyway twice as many shares
   // cost more: 64 rows over 131072 keys, 8 items in 19, 138 us, in 38 177.)
   if (sp < 2 && pl.items * 3 <= sms * 4 && (c.B > 1 || pl.items * 4 < sms * 3)) {
